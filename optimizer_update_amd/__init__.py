@@ -573,6 +573,14 @@ class Graph:
 
 __all__ += ["QBLOCK", "qmap", "state8_sizes", "optimizer_update_8bit_blockwise", "Plan8", "Graph"]
 
+from .mx4 import (MX4_BLOCK, MX4_PAD, Mx4, Mx4Weight, load_mx4, mx4_dequantize,  # noqa: E402
+                  mx4_grouped_linear, mx4_grouped_matmul, mx4_grouped_outer, mx4_linear, mx4_matmul,
+                  mx4_quantize, mx4_quantize_both, mx4_quantize_grouped)
+
+__all__ += ["MX4_BLOCK", "MX4_PAD", "Mx4", "Mx4Weight", "load_mx4", "mx4_dequantize", "mx4_grouped_linear",
+            "mx4_grouped_matmul", "mx4_grouped_outer", "mx4_linear", "mx4_matmul", "mx4_quantize",
+            "mx4_quantize_both", "mx4_quantize_grouped"]
+
 from .optim import AdamW32, AdEMAMix32, Adagrad32, Lion32, Momentum32, RMSprop32  # noqa: E402
 from .optim import AdamW8bit, AdEMAMix8bit  # noqa: E402
 

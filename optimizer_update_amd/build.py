@@ -26,6 +26,10 @@ HEADERS = [os.path.join(CSRC, "elem.hpp"), os.path.join(CSRC, "internal.h"),
            os.path.join(CSRC, "stream.hpp"),
            os.path.join(os.path.dirname(HERE), "include", "optimizer_update.h")]
 
+# The microscaled 4-bit operators: a library and a header of their own.
+MX4_LIBRARY = os.path.join(HERE, "liboptimizer_mx4.so")
+MX4_SOURCES = [os.path.join(CSRC, "mx4_kernels.hip"), os.path.join(CSRC, "mx4_host.hip")]
+
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
     "-ffp-contract=off", "-fno-fast-math",
@@ -36,11 +40,19 @@ HIPCC_FLAGS = [
 
 
 def build(out_path: str = LIBRARY, extra_flags: list[str] | None = None, quiet: bool = True) -> str:
-    """Compile the library (always; atomically replaces ``out_path``)."""
+    """Compile the library (always; atomically replaces ``out_path``), the
+    library of the 4-bit operators and the CPython module."""
+    _compile(SOURCES, out_path, extra_flags, quiet)
+    _compile(MX4_SOURCES, MX4_LIBRARY, extra_flags, quiet)
+    build_fast()
+    return out_path
+
+
+def _compile(sources: list[str], out_path: str, extra_flags: list[str] | None, quiet: bool) -> None:
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
     fd, tmp = tempfile.mkstemp(suffix=".so", dir=os.path.dirname(out_path))
     os.close(fd)
-    cmd = [hipcc, *HIPCC_FLAGS, *(extra_flags or []), "-o", tmp, *SOURCES]
+    cmd = [hipcc, *HIPCC_FLAGS, *(extra_flags or []), "-o", tmp, *sources]
     try:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
@@ -51,8 +63,6 @@ def build(out_path: str = LIBRARY, extra_flags: list[str] | None = None, quiet: 
     finally:
         if os.path.exists(tmp):
             os.unlink(tmp)
-    build_fast()
-    return out_path
 
 
 def build_fast(out_path: str = FAST) -> str:

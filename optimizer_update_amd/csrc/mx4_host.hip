@@ -1,0 +1,421 @@
+// mx4_host.hip -- C ABI of the microscaled 4-bit operators (host side):
+// argument checks, launch shapes and workspaces.  The arithmetic is in
+// mx4_kernels.hip.
+#include <atomic>
+#include <cstdarg>
+#include <cstdio>
+#include <cstring>
+
+#include "../../include/optimizer_mx4.h"
+#include "mx4.h"
+
+using namespace mx4;
+
+namespace {
+
+thread_local char g_error[512] = "";
+
+__attribute__((format(printf, 2, 3)))
+int fail(int status, const char* fmt, ...)
+{
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_error, sizeof(g_error), fmt, ap);
+    va_end(ap);
+    return status;
+}
+
+int hip_fail(hipError_t e, const char* what) { return fail(OU_EHIP, "%s: %s", what, hipGetErrorString(e)); }
+
+constexpr int kMaxDevices = 64;
+std::atomic<int> g_arch[kMaxDevices];   // 0 unknown, 1 gfx950, 2 another
+
+// OU_OK if the current device is a gfx950 (looked up once per device).
+int check_device()
+{
+    int dev = -1;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return fail(OU_EUNSUPPORTED, "no HIP device: %s", hipGetErrorString(e));
+    if (dev < 0 || dev >= kMaxDevices) return fail(OU_EUNSUPPORTED, "device %d", dev);
+    int a = g_arch[dev].load(std::memory_order_relaxed);
+    if (!a) {
+        hipDeviceProp_t p;
+        e = hipGetDeviceProperties(&p, dev);
+        if (e != hipSuccess) return hip_fail(e, "hipGetDeviceProperties");
+        a = std::strncmp(p.gcnArchName, "gfx950", 6) == 0 ? 1 : 2;
+        g_arch[dev].store(a, std::memory_order_relaxed);
+    }
+    return a == 1 ? OU_OK : fail(OU_EUNSUPPORTED, "device %d is not a gfx950", dev);
+}
+
+// Largest extent of any axis, and of any product of axes in bytes: every
+// address and count below stays far inside 64 bits.
+constexpr int64_t kMaxAxis = int64_t(1) << 31;
+constexpr int64_t kMaxBytes = int64_t(1) << 46;
+constexpr int32_t kMaxBatch = 65535;      // second axis of a grid
+
+int elem_bytes(int dtype) { return dtype == OU_F32 ? 4 : 2; }
+bool valid_dtype(int dtype) { return dtype == OU_F32 || dtype == OU_F16 || dtype == OU_BF16; }
+int64_t pad(int64_t k) { return (k + kPad - 1) / kPad * kPad; }
+int64_t cut(int64_t n, int64_t d) { return (n + d - 1) / d; }
+
+int check_axis(int64_t n, const char* what)
+{
+    if (n < 0 || n > kMaxAxis) return fail(OU_EINVAL, "%s = %lld is out of range", what, static_cast<long long>(n));
+    return OU_OK;
+}
+
+// A buffer of a call; check() tests all of them.
+struct Buffer {
+    const char* name;
+    const void* p;
+    double bytes;      // extent, as a double so that no product wraps
+    unsigned align;
+    bool written;
+};
+
+int check_buffers(const Buffer* b, int n)
+{
+    for (int i = 0; i < n; ++i) {
+        if (b[i].bytes <= 0) continue;
+        if (!b[i].p) return fail(OU_EINVAL, "%s is null", b[i].name);
+        if (b[i].bytes > static_cast<double>(kMaxBytes)) return fail(OU_EINVAL, "%s is too large", b[i].name);
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(b[i].p);
+        if (lo % b[i].align) return fail(OU_EALIGN, "%s is not %u-byte aligned", b[i].name, b[i].align);
+        if (lo + static_cast<uintptr_t>(b[i].bytes) < lo) return fail(OU_EINVAL, "%s wraps", b[i].name);
+    }
+    for (int i = 0; i < n; ++i) {
+        if (!b[i].written || b[i].bytes <= 0) continue;
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(b[i].p), hi = lo + static_cast<uintptr_t>(b[i].bytes);
+        for (int j = 0; j < n; ++j) {
+            if (j == i || b[j].bytes <= 0) continue;
+            const uintptr_t lj = reinterpret_cast<uintptr_t>(b[j].p), hj = lj + static_cast<uintptr_t>(b[j].bytes);
+            if (lo < hj && lj < hi) return fail(OU_EOVERLAP, "%s overlaps %s", b[i].name, b[j].name);
+        }
+    }
+    return OU_OK;
+}
+
+double held_codes(int64_t rows, int64_t pcols) { return static_cast<double>(rows) * static_cast<double>(pcols) / 2; }
+double held_scales(int64_t rows, int64_t pcols) { return static_cast<double>(rows) * static_cast<double>(pcols) / kBlock; }
+
+// Bytes of `rows` rows of `cols` elements, `stride` elements apart.
+double extent(int64_t rows, int64_t cols, int64_t stride, int bytes)
+{
+    if (rows == 0 || cols == 0) return 0;
+    return (static_cast<double>(rows - 1) * static_cast<double>(stride) + static_cast<double>(cols)) * bytes;
+}
+
+int launch(const void* fn, int64_t gx, int64_t gy, int threads, void** args, void* stream, const char* what)
+{
+    if (gx > INT32_MAX || gy > kMaxBatch) return fail(OU_EINVAL, "%s: too many tiles", what);
+    const hipError_t e = hipLaunchKernel(fn, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)),
+                                         dim3(static_cast<unsigned>(threads)), args, 0,
+                                         static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? OU_OK : hip_fail(e, what);
+}
+
+int64_t grouped_units(int64_t rows, int32_t groups, int64_t unit)
+{
+    return (rows + (unit - 1) * static_cast<int64_t>(groups)) / unit;
+}
+
+bool wide_rows(const void* p, int64_t stride, int64_t batch_stride, int bytes, int align)
+{
+    return reinterpret_cast<uintptr_t>(p) % align == 0 && (stride * bytes) % align == 0 &&
+           (batch_stride * bytes) % align == 0;
+}
+
+int launch_quantize(int dtype, QuantArgs& q, int64_t batch, int64_t units, void* stream)
+{
+    q.wide = wide_rows(q.x, q.row_stride, batch > 1 ? q.batch_stride : 0, elem_bytes(dtype), 16);
+    if (!q.codes_t) {
+        int64_t n = q.rows * (q.pcols / kPad);
+        void* args[] = {&q, &n};
+        return launch(quant_rows_kernel(dtype), cut(n, (kQuantThreads / 16) * kQuantUnits), batch, kQuantThreads, args,
+                      stream, "k_quant_rows");
+    }
+    void* args[] = {&q};
+    return launch(quant_tile_kernel(dtype), units * (q.pcols / kQuantTile), batch, kQuantThreads, args, stream,
+                  "k_quant_tile");
+}
+
+int launch_matmul(int out_dtype, int grouping, MatmulArgs& p, int64_t units, int64_t batch, void* stream)
+{
+    p.n_tiles = cut(p.n, kMatmulTile);
+    p.wide = wide_rows(p.out, p.out_stride, grouping == kByContraction ? p.m * p.out_stride : 0, elem_bytes(out_dtype),
+                       4 * elem_bytes(out_dtype));
+    void* args[] = {&p};
+    return launch(matmul_kernel(out_dtype, grouping), units * p.n_tiles, batch, kMatmulThreads, args, stream, "k_matmul");
+}
+
+int check_groups(const int32_t* offsets, int32_t groups)
+{
+    if (groups < 0 || groups > kMaxBatch) return fail(OU_EINVAL, "groups = %d is out of range", groups);
+    if (!offsets) return fail(OU_EINVAL, "offsets is null");
+    if (reinterpret_cast<uintptr_t>(offsets) % 4) return fail(OU_EALIGN, "offsets is not 4-byte aligned");
+    return OU_OK;
+}
+
+// x's 4-bit form at the start of a workspace.
+int64_t values_bytes(int64_t m, int64_t k) { return m * (pad(k) / 2) + (m * (pad(k) / kBlock) + 15) / 16 * 16; }
+
+}  // namespace
+
+extern "C" {
+
+#define OU_EXPORT __attribute__((visibility("default")))
+
+OU_EXPORT const char* ou_mx4_last_error(void) { return g_error; }
+
+OU_EXPORT int64_t ou_mx4_columns(int64_t k) { return k < 0 || k > kMaxAxis ? -1 : pad(k); }
+
+OU_EXPORT int64_t ou_mx4_grouped_columns(int64_t rows, int32_t groups)
+{
+    return rows < 0 || rows > kMaxAxis || groups < 0 ? -1 : grouped_units(rows, groups, kPad) * kPad;
+}
+
+OU_EXPORT int ou_mx4_quantize(int dtype, const void* x, int64_t batch, int64_t rows, int64_t cols, int64_t row_stride,
+                              int64_t batch_stride, uint8_t* codes, uint8_t* scales, uint8_t* codes_t,
+                              uint8_t* scales_t, void* stream)
+{
+    if (!valid_dtype(dtype)) return fail(OU_EINVAL, "unknown dtype %d", dtype);
+    if (int st = check_axis(rows, "rows")) return st;
+    if (int st = check_axis(cols, "cols")) return st;
+    if (batch < 0 || batch > kMaxBatch) return fail(OU_EINVAL, "batch = %lld is out of range", (long long)batch);
+    if (row_stride < cols || row_stride > kMaxAxis) return fail(OU_EINVAL, "row_stride is out of range");
+    if (batch_stride < 0 || (batch > 1 && rows > 0 && batch_stride < cols)) return fail(OU_EINVAL, "batch_stride is out of range");
+    if (batch == 0 || rows == 0 || cols == 0) return OU_OK;
+    if (!codes != !scales || !codes_t != !scales_t || (!codes && !codes_t))
+        return fail(OU_EINVAL, "codes and scales come in pairs, one pair at least");
+    const int eb = elem_bytes(dtype);
+    const double xb = extent(rows, cols, row_stride, eb) + static_cast<double>(batch - 1) * batch_stride * eb;
+    const Buffer bufs[] = {{"x", x, xb, static_cast<unsigned>(eb), false},
+                           {"codes", codes, codes ? held_codes(batch * rows, pad(cols)) : 0, 16, true},
+                           {"scales", scales, scales ? held_scales(batch * rows, pad(cols)) : 0, 4, true},
+                           {"codes_t", codes_t, codes_t ? held_codes(batch * cols, pad(rows)) : 0, 16, true},
+                           {"scales_t", scales_t, scales_t ? held_scales(batch * cols, pad(rows)) : 0, 4, true}};
+    if (int st = check_buffers(bufs, 5)) return st;
+    if (int st = check_device()) return st;
+    QuantArgs q{x, codes, scales, codes_t, scales_t, rows, cols, row_stride, batch_stride, pad(cols), pad(rows), nullptr,
+                0, 0};
+    return launch_quantize(dtype, q, batch, pad(rows) / kQuantTile, stream);
+}
+
+OU_EXPORT int ou_mx4_quantize_grouped(int dtype, const void* x, int64_t rows, int64_t cols, int64_t row_stride,
+                                      const int32_t* offsets, int32_t groups, uint8_t* codes, uint8_t* scales,
+                                      uint8_t* codes_t, uint8_t* scales_t, void* stream)
+{
+    if (!valid_dtype(dtype)) return fail(OU_EINVAL, "unknown dtype %d", dtype);
+    if (int st = check_axis(rows, "rows")) return st;
+    if (int st = check_axis(cols, "cols")) return st;
+    if (row_stride < cols || row_stride > kMaxAxis) return fail(OU_EINVAL, "row_stride is out of range");
+    if (int st = check_groups(offsets, groups)) return st;
+    if (rows == 0 || cols == 0 || groups == 0) return OU_OK;
+    if (!codes != !scales) return fail(OU_EINVAL, "codes and scales come in pairs");
+    if (!codes_t || !scales_t) return fail(OU_EINVAL, "codes_t or scales_t is null");
+    const int eb = elem_bytes(dtype);
+    const int64_t pr = ou_mx4_grouped_columns(rows, groups);
+    const Buffer bufs[] = {{"x", x, extent(rows, cols, row_stride, eb), static_cast<unsigned>(eb), false},
+                           {"offsets", offsets, 4.0 * (groups + 1.0), 4, false},
+                           {"codes", codes, codes ? held_codes(rows, pad(cols)) : 0, 16, true},
+                           {"scales", scales, scales ? held_scales(rows, pad(cols)) : 0, 4, true},
+                           {"codes_t", codes_t, held_codes(cols, pr), 16, true},
+                           {"scales_t", scales_t, held_scales(cols, pr), 4, true}};
+    if (int st = check_buffers(bufs, 6)) return st;
+    if (int st = check_device()) return st;
+    QuantArgs q{x, codes, scales, codes_t, scales_t, rows, cols, row_stride, 0, pad(cols), pr, offsets, groups, 0};
+    return launch_quantize(dtype, q, 1, pr / kQuantTile, stream);
+}
+
+OU_EXPORT int ou_mx4_dequantize(int dtype, const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                                void* out, int64_t row_stride, void* stream)
+{
+    if (!valid_dtype(dtype)) return fail(OU_EINVAL, "unknown dtype %d", dtype);
+    if (rows < 0 || rows > (int64_t(1) << 40)) return fail(OU_EINVAL, "rows is out of range");
+    if (int st = check_axis(cols, "cols")) return st;
+    if (row_stride < cols || row_stride > kMaxAxis) return fail(OU_EINVAL, "row_stride is out of range");
+    if (rows == 0 || cols == 0) return OU_OK;
+    const int eb = elem_bytes(dtype);
+    const Buffer bufs[] = {{"codes", codes, held_codes(rows, pad(cols)), 16, false},
+                           {"scales", scales, held_scales(rows, pad(cols)), 4, false},
+                           {"out", out, extent(rows, cols, row_stride, eb), static_cast<unsigned>(eb), true}};
+    if (int st = check_buffers(bufs, 3)) return st;
+    if (int st = check_device()) return st;
+    DequantArgs d{codes, scales, out, rows, cols, pad(cols), row_stride, wide_rows(out, row_stride, 0, eb, 4 * eb)};
+    int64_t octets = rows * (pad(cols) / 8);
+    void* args[] = {&d, &octets};
+    return launch(dequant_kernel(dtype), cut(octets, kQuantThreads), 1, kQuantThreads, args, stream, "k_dequant");
+}
+
+OU_EXPORT int64_t ou_mx4_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k, int from_values)
+{
+    if (check_axis(m, "m") || check_axis(n, "n") || check_axis(k, "k")) return -1;
+    return from_values ? values_bytes(m, k) : 0;
+}
+
+OU_EXPORT int64_t ou_mx4_grouped_workspace_bytes(int64_t rows, int64_t n, int64_t k, int32_t groups, int from_values)
+{
+    if (groups < 0 || groups > kMaxBatch) return -1;
+    return ou_mx4_matmul_workspace_bytes(rows, n, k, from_values);
+}
+
+}  // extern "C"
+
+namespace {
+
+// What the four products share.  x (or a): the left matrix as values (or held).
+struct Product {
+    int x_dtype;
+    const void* x;
+    int64_t x_stride;
+    const uint8_t *a, *as;
+    int64_t m;
+    int out_dtype;
+    const uint8_t *b, *bs;
+    int64_t n, k;
+    const int32_t* offsets;   // nullptr: not grouped
+    int32_t groups;
+    void* out;
+    int64_t out_stride;
+    int zero_rest;
+    void* workspace;
+    int64_t workspace_bytes;
+    void* stream;
+};
+
+int product(Product& q, bool values, bool grouped)
+{
+    if (!valid_dtype(q.out_dtype) || (values && !valid_dtype(q.x_dtype))) return fail(OU_EINVAL, "unknown dtype");
+    if (int st = check_axis(q.m, "m")) return st;
+    if (int st = check_axis(q.n, "n")) return st;
+    if (int st = check_axis(q.k, "k")) return st;
+    if (values && (q.x_stride < q.k || q.x_stride > kMaxAxis)) return fail(OU_EINVAL, "x_stride is out of range");
+    if (q.out_stride < q.n || q.out_stride > kMaxAxis) return fail(OU_EINVAL, "out_stride is out of range");
+    if (grouped)
+        if (int st = check_groups(q.offsets, q.groups)) return st;
+    if (q.m == 0 || q.n == 0) return OU_OK;
+    const int64_t need = grouped ? ou_mx4_grouped_workspace_bytes(q.m, q.n, q.k, q.groups, values)
+                                 : ou_mx4_matmul_workspace_bytes(q.m, q.n, q.k, values);
+    if (need > 0 && (!q.workspace || q.workspace_bytes < need))
+        return fail(OU_EINVAL, "workspace: %lld bytes are needed", static_cast<long long>(need));
+    const int64_t pk = pad(q.k);
+    const int eo = elem_bytes(q.out_dtype), ex = values ? elem_bytes(q.x_dtype) : 1;
+    const double bm = grouped ? q.groups : 1;
+    const Buffer bufs[] = {{"x", q.x, values ? extent(q.m, q.k, q.x_stride, ex) : 0, static_cast<unsigned>(ex), false},
+                           {"a_codes", q.a, values ? 0 : held_codes(q.m, pk), 16, false},
+                           {"a_scales", q.as, values ? 0 : held_scales(q.m, pk), 4, false},
+                           {"b_codes", q.b, bm * held_codes(q.n, pk), 16, false},
+                           {"b_scales", q.bs, bm * held_scales(q.n, pk), 4, false},
+                           {"offsets", q.offsets, grouped ? 4.0 * (q.groups + 1.0) : 0, 4, false},
+                           {"workspace", q.workspace, static_cast<double>(need), 16, true},
+                           {"out", q.out, extent(q.m, q.n, q.out_stride, eo), static_cast<unsigned>(eo), true}};
+    if (int st = check_buffers(bufs, 8)) return st;
+    if (int st = check_device()) return st;
+    const uint8_t *a = q.a, *as = q.as;
+    if (values && pk > 0) {
+        uint8_t* wc = static_cast<uint8_t*>(q.workspace);
+        uint8_t* wsc = wc + q.m * (pk / 2);
+        QuantArgs qa{q.x, wc, wsc, nullptr, nullptr, q.m, q.k, q.x_stride, 0, pk, 0, nullptr, 0, 0};
+        if (int st = launch_quantize(q.x_dtype, qa, 1, 0, q.stream)) return st;
+        a = wc;
+        as = wsc;
+    }
+    MatmulArgs p{};
+    p.a = a;
+    p.as = as;
+    p.b = q.b;
+    p.bs = q.bs;
+    p.out = q.out;
+    p.m = q.m;
+    p.n = q.n;
+    p.out_stride = q.out_stride;
+    p.steps = pk / kPad;
+    p.offsets = q.offsets;
+    p.rows = q.m;
+    p.groups = q.groups;
+    p.zero_rest = q.zero_rest != 0;
+    // two units more: the rows in front of the first group and behind the last
+    const int64_t units = grouped ? grouped_units(q.m, q.groups + 2, kMatmulTile) : cut(q.m, kMatmulTile);
+    return launch_matmul(q.out_dtype, grouped ? kByRows : kPlain, p, units, 1, q.stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+OU_EXPORT int ou_mx4_matmul(int out_dtype, const uint8_t* a_codes, const uint8_t* a_scales, int64_t m,
+                            const uint8_t* b_codes, const uint8_t* b_scales, int64_t n, int64_t k, void* out,
+                            int64_t out_stride, void* workspace, int64_t workspace_bytes, void* stream)
+{
+    Product q{0,         nullptr, 0, a_codes, a_scales, m,          out_dtype, b_codes,   b_scales,        n, k,
+              nullptr,   0,       out, out_stride, 0,   workspace,  workspace_bytes, stream};
+    return product(q, false, false);
+}
+
+OU_EXPORT int ou_mx4_matmul_values(int x_dtype, const void* x, int64_t m, int64_t x_stride, int out_dtype,
+                                   const uint8_t* b_codes, const uint8_t* b_scales, int64_t n, int64_t k, void* out,
+                                   int64_t out_stride, void* workspace, int64_t workspace_bytes, void* stream)
+{
+    Product q{x_dtype, x, x_stride, nullptr, nullptr, m, out_dtype, b_codes, b_scales, n, k,
+              nullptr, 0, out, out_stride, 0, workspace, workspace_bytes, stream};
+    return product(q, true, false);
+}
+
+OU_EXPORT int ou_mx4_grouped_matmul(int out_dtype, const uint8_t* a_codes, const uint8_t* a_scales, int64_t rows,
+                                    const uint8_t* b_codes, const uint8_t* b_scales, int64_t n, int64_t k,
+                                    const int32_t* offsets, int32_t groups, void* out, int64_t out_stride,
+                                    int zero_rest, void* workspace, int64_t workspace_bytes, void* stream)
+{
+    Product q{0, nullptr, 0, a_codes, a_scales, rows, out_dtype, b_codes, b_scales, n, k,
+              offsets, groups, out, out_stride, zero_rest, workspace, workspace_bytes, stream};
+    return product(q, false, true);
+}
+
+OU_EXPORT int ou_mx4_grouped_matmul_values(int x_dtype, const void* x, int64_t rows, int64_t x_stride, int out_dtype,
+                                           const uint8_t* b_codes, const uint8_t* b_scales, int64_t n, int64_t k,
+                                           const int32_t* offsets, int32_t groups, void* out, int64_t out_stride,
+                                           int zero_rest, void* workspace, int64_t workspace_bytes, void* stream)
+{
+    Product q{x_dtype, x, x_stride, nullptr, nullptr, rows, out_dtype, b_codes, b_scales, n, k,
+              offsets, groups, out, out_stride, zero_rest, workspace, workspace_bytes, stream};
+    return product(q, true, true);
+}
+
+OU_EXPORT int ou_mx4_grouped_outer(int out_dtype, const uint8_t* a_codes_t, const uint8_t* a_scales_t, int64_t m,
+                                   const uint8_t* b_codes_t, const uint8_t* b_scales_t, int64_t n, int64_t rows,
+                                   const int32_t* offsets, int32_t groups, void* out, void* stream)
+{
+    if (!valid_dtype(out_dtype)) return fail(OU_EINVAL, "unknown dtype %d", out_dtype);
+    if (int st = check_axis(m, "m")) return st;
+    if (int st = check_axis(n, "n")) return st;
+    if (int st = check_axis(rows, "rows")) return st;
+    if (int st = check_groups(offsets, groups)) return st;
+    if (m == 0 || n == 0 || groups == 0) return OU_OK;
+    const int64_t pr = ou_mx4_grouped_columns(rows, groups);
+    const int eo = elem_bytes(out_dtype);
+    const Buffer bufs[] = {{"a_codes_t", a_codes_t, held_codes(m, pr), 16, false},
+                           {"a_scales_t", a_scales_t, held_scales(m, pr), 4, false},
+                           {"b_codes_t", b_codes_t, held_codes(n, pr), 16, false},
+                           {"b_scales_t", b_scales_t, held_scales(n, pr), 4, false},
+                           {"offsets", offsets, 4.0 * (groups + 1.0), 4, false},
+                           {"out", out, static_cast<double>(groups) * m * n * eo, static_cast<unsigned>(eo), true}};
+    if (int st = check_buffers(bufs, 6)) return st;
+    if (int st = check_device()) return st;
+    MatmulArgs p{};
+    p.a = a_codes_t;
+    p.as = a_scales_t;
+    p.b = b_codes_t;
+    p.bs = b_scales_t;
+    p.out = out;
+    p.m = m;
+    p.n = n;
+    p.out_stride = n;
+    p.steps = pr / kPad;
+    p.offsets = offsets;
+    p.rows = rows;
+    p.groups = groups;
+    return launch_matmul(out_dtype, kByContraction, p, cut(m, kMatmulTile), groups, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,614 @@
+// mx4_kernels.hip -- microscaled 4-bit floats (device): quantisation,
+// dequantisation and products.
+//
+// Format.  A block of 32 neighbouring values along the contracted axis holds
+// one scale code s (the power of two 2^(s - 127); 255: the block has a NaN
+// or an infinity and stands for NaN) and 32 codes of 4 bits: sign, two bits
+// of exponent, one of mantissa, magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6.
+// s = max(0, e - 2) with e the biased binary32 exponent of the block's
+// largest magnitude, so the largest value lands in [4, 8) and what exceeds 6
+// gives 6; all others round to nearest, ties to the even code.
+//
+// Held matrices: codes [rows][P / 2], the even column in the low four bits,
+// and scales [rows][P / 32], P the columns padded to 128 with zeros.  A row
+// is a whole number of 64-byte pieces, one k-step of the 16x16x128 matrix
+// instruction.
+#include "mx4.h"
+
+#pragma clang fp contract(off)
+
+namespace mx4 {
+namespace {
+
+using i32x4 = int __attribute__((ext_vector_type(4)));
+using i32x8 = int __attribute__((ext_vector_type(8)));
+using u32x2 = uint32_t __attribute__((ext_vector_type(2)));
+using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
+using f32x2 = float __attribute__((ext_vector_type(2)));
+using f32x4 = float __attribute__((ext_vector_type(4)));
+using bf16x2 = __bf16 __attribute__((ext_vector_type(2)));
+using f16x2 = _Float16 __attribute__((ext_vector_type(2)));
+
+// ---- storage types ------------------------------------------------------
+// pack(): two neighbouring values as the converter takes them; the block's
+// largest magnitude is found on the bit patterns without their signs, whose
+// order as integers is that of the magnitudes with infinities and NaNs above.
+
+template <int DT>
+struct Type;
+
+template <>
+struct Type<kF32> {
+    using Elem = float;
+    static constexpr int kBytes = 4;
+};
+template <>
+struct Type<kF16> {
+    using Elem = uint16_t;
+    static constexpr int kBytes = 2;
+};
+template <>
+struct Type<kBF16> {
+    using Elem = uint16_t;
+    static constexpr int kBytes = 2;
+};
+
+// Biased binary32 exponent of a magnitude given by its storage bits.
+template <int DT>
+__device__ __forceinline__ uint32_t exponent_of(uint32_t mag)
+{
+    if constexpr (DT == kF32) return mag >> 23;
+    if constexpr (DT == kBF16) return mag >> 7;
+    const float f = static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(mag)));
+    return __builtin_bit_cast(uint32_t, f) >> 23;
+}
+
+__device__ __forceinline__ uint32_t scale_code(uint32_t e)
+{
+    return e == 255u ? 255u : (e < 2u ? 0u : e - 2u);
+}
+
+// The converter's scale operand: a binary32 whose exponent field is the scale
+// code.
+__device__ __forceinline__ float scale_operand(uint32_t s) { return __builtin_bit_cast(float, s << 23); }
+
+// Packed maximum of the magnitudes of two 16-bit values.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
+{
+    using u16x2 = uint16_t __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
+                                                                  __builtin_bit_cast(u16x2, b)));
+}
+
+// Byte SEL of `old` becomes the codes of the pair (lo first).
+template <int SEL>
+__device__ __forceinline__ uint32_t convert_f32(uint32_t old, uint32_t lo, uint32_t hi, float scale)
+{
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, __builtin_bit_cast(float, lo),
+                                                    __builtin_bit_cast(float, hi), scale, SEL);
+}
+template <int DT, int SEL>
+__device__ __forceinline__ uint32_t convert_16(uint32_t old, uint32_t pair, float scale)
+{
+    if constexpr (DT == kBF16)
+        return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(old, __builtin_bit_cast(bf16x2, pair), scale, SEL);
+    else
+        return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(old, __builtin_bit_cast(f16x2, pair), scale, SEL);
+}
+
+// Eight neighbouring values: storage bits, four dwords (16-bit types) or
+// eight (binary32).
+template <int DT>
+struct Octet {
+    static constexpr int kWords = Type<DT>::kBytes * 2;
+    uint32_t w[kWords];
+
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+    }
+
+    // n of the eight values starting at p (0 <= n <= 8), the rest 0.
+    __device__ __forceinline__ void load(const typename Type<DT>::Elem* p, int n, bool wide)
+    {
+        if (n >= 8 && wide) {
+            const u32x4* q = reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i) {
+                const u32x4 v = __builtin_nontemporal_load(q + i);
+                w[4 * i] = v[0];
+                w[4 * i + 1] = v[1];
+                w[4 * i + 2] = v[2];
+                w[4 * i + 3] = v[3];
+            }
+            return;
+        }
+        zero();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i >= n) continue;
+            if constexpr (DT == kF32)
+                w[i] = __builtin_bit_cast(uint32_t, p[i]);
+            else
+                w[i / 2] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
+        }
+    }
+
+    // Bits of the largest magnitude.
+    __device__ __forceinline__ uint32_t top() const
+    {
+        if constexpr (DT == kF32) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7fffffffu);
+            return m;
+        } else {
+            uint32_t m = w[0] & 0x7fff7fffu;
+#pragma unroll
+            for (int i = 1; i < 4; ++i) m = max_u16x2(m, w[i] & 0x7fff7fffu);
+            return max(m & 0xffffu, m >> 16);
+        }
+    }
+
+    __device__ __forceinline__ uint32_t codes(float scale) const
+    {
+        uint32_t r = 0;
+        if constexpr (DT == kF32) {
+            r = convert_f32<0>(r, w[0], w[1], scale);
+            r = convert_f32<1>(r, w[2], w[3], scale);
+            r = convert_f32<2>(r, w[4], w[5], scale);
+            r = convert_f32<3>(r, w[6], w[7], scale);
+        } else {
+            r = convert_16<DT, 0>(r, w[0], scale);
+            r = convert_16<DT, 1>(r, w[1], scale);
+            r = convert_16<DT, 2>(r, w[2], scale);
+            r = convert_16<DT, 3>(r, w[3], scale);
+        }
+        return r;
+    }
+};
+
+// Maximum over the four lanes of a quad.
+__device__ __forceinline__ uint32_t quad_max(uint32_t x)
+{
+    x = max(x, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0xB1, 0xf, 0xf, false)));
+    x = max(x, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x4E, 0xf, 0xf, false)));
+    return x;
+}
+
+// ---- groups ---------------------------------------------------------------
+
+struct Place {
+    int32_t group;   // -1: of no group (rows = 0: behind everything)
+    int64_t row;     // first row of the unit
+    int64_t rows;    // rows of the unit inside its group
+    int64_t first;   // unit index of the group's first unit
+    int64_t units;   // units of the group
+};
+
+__device__ __forceinline__ int64_t clamp_offset(int32_t o, int64_t rows)
+{
+    return o < 0 ? 0 : (o > rows ? rows : o);
+}
+
+// The group that unit `index` falls in when every group is cut into units of
+// `unit` rows, for offsets that may be anything (clamped to [0, rows], a
+// group that runs backwards is empty).  All lanes of the wave take part and
+// get the same answer.  Lane l looks at group base + l.
+__device__ __forceinline__ Place locate(const int32_t* offsets, int32_t groups, int64_t rows, int unit, int64_t index)
+{
+    const int lane = static_cast<int>(threadIdx.x) & (kWave - 1);
+    int64_t before = 0;
+    for (int32_t base = 0; base < groups; base += kWave) {
+        const int32_t e = base + lane;
+        int64_t lo = 0, n = 0;
+        if (e < groups) {
+            lo = clamp_offset(offsets[e], rows);
+            const int64_t hi = clamp_offset(offsets[e + 1], rows);
+            n = hi > lo ? hi - lo : 0;
+        }
+        const int64_t u = (n + unit - 1) / unit;
+        int64_t sum = u;   // inclusive prefix sum over the wave
+        for (int d = 1; d < kWave; d <<= 1) {
+            const int64_t o = __shfl_up(sum, d);
+            if (lane >= d) sum += o;
+        }
+        const uint64_t past = __ballot(before + sum > index);
+        if (past) {
+            const int hit = __builtin_ctzll(past);
+            Place p;
+            p.group = base + hit;
+            p.units = __shfl(u, hit);
+            p.first = before + __shfl(sum, hit) - p.units;
+            const int64_t start = __shfl(lo, hit), count = __shfl(n, hit);
+            const int64_t at = (index - p.first) * unit;
+            p.row = start + at;
+            p.rows = count - at < unit ? count - at : unit;
+            return p;
+        }
+        before += __shfl(sum, kWave - 1);
+    }
+    // units of the rows in front of the first group, then of those behind the last
+    const int64_t front = groups ? clamp_offset(offsets[0], rows) : 0;
+    const int64_t back = groups ? clamp_offset(offsets[groups], rows) : 0;
+    const int64_t nf = (front + unit - 1) / unit, nb = (rows - back + unit - 1) / unit;
+    const int64_t j = index - before;
+    Place p{-1, 0, 0, before, nf + nb};
+    if (j < nf) {
+        p.row = j * unit;
+        p.rows = front - p.row < unit ? front - p.row : unit;
+    } else if (j < nf + nb) {
+        p.row = back + (j - nf) * unit;
+        p.rows = rows - p.row < unit ? rows - p.row : unit;
+    }
+    return p;
+}
+
+// Units before group e and the units of e.
+__device__ __forceinline__ Place units_of(const int32_t* offsets, int64_t rows, int unit, int32_t group)
+{
+    const int lane = static_cast<int>(threadIdx.x) & (kWave - 1);
+    int64_t sum = 0;
+    for (int32_t e = lane; e < group; e += kWave) {
+        const int64_t lo = clamp_offset(offsets[e], rows), hi = clamp_offset(offsets[e + 1], rows);
+        if (hi > lo) sum += (hi - lo + unit - 1) / unit;
+    }
+    for (int d = 1; d < kWave; d <<= 1) sum += __shfl_xor(sum, d);
+    const int64_t lo = clamp_offset(offsets[group], rows), hi = clamp_offset(offsets[group + 1], rows);
+    Place p;
+    p.group = group;
+    p.row = lo;
+    p.rows = hi > lo ? hi - lo : 0;
+    p.first = sum;
+    p.units = (p.rows + unit - 1) / unit;
+    return p;
+}
+
+// ---- quantisation along the columns --------------------------------------
+
+// 16 lanes hold one unit of 128 columns of a row, eight values a lane, so a
+// block is a quad.  Lanes keep kQuantUnits units in flight.
+template <int DT>
+__global__ __launch_bounds__(kQuantThreads) void k_quant_rows(QuantArgs q, int64_t units)
+{
+    using Elem = typename Type<DT>::Elem;
+    const int64_t per_row = q.pcols / kPad;
+    const int sub = static_cast<int>(threadIdx.x) & 15;
+    const int64_t group = (static_cast<int64_t>(blockIdx.x) * kQuantThreads + threadIdx.x) >> 4;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * (kQuantThreads / 16);
+    const int64_t batch = blockIdx.y;
+    const Elem* x = static_cast<const Elem*>(q.x) + batch * q.batch_stride;
+    uint8_t* codes = q.codes + batch * q.rows * (q.pcols / 2);
+    uint8_t* scales = q.scales + batch * q.rows * (q.pcols / kBlock);
+    Octet<DT> v[kQuantUnits];
+#pragma unroll
+    for (int i = 0; i < kQuantUnits; ++i) {
+        const int64_t u = group + i * stride;
+        if (u >= units) {
+            v[i].zero();
+            continue;
+        }
+        const int64_t row = u / per_row, col = (u - row * per_row) * kPad + sub * 8;
+        const int64_t left = q.cols - col;
+        v[i].load(x + row * q.row_stride + col, left < 0 ? 0 : (left > 8 ? 8 : static_cast<int>(left)), q.wide);
+    }
+#pragma unroll
+    for (int i = 0; i < kQuantUnits; ++i) {
+        const int64_t u = group + i * stride;
+        const uint32_t s = scale_code(exponent_of<DT>(quad_max(v[i].top())));
+        const uint32_t c = s == kScaleNaN ? 0u : v[i].codes(scale_operand(s));
+        if (u >= units) continue;
+        *reinterpret_cast<uint32_t*>(codes + u * (kPad / 2) + sub * 4) = c;
+        if ((sub & 3) == 0) scales[u * (kPad / kBlock) + (sub >> 2)] = static_cast<uint8_t>(s);
+    }
+}
+
+// ---- quantisation along the rows, or along both axes ---------------------
+
+// One tile of 128 x 128 values.  It is read along the columns (eight values
+// a lane), quantised that way from registers if wanted, and left in LDS;
+// then each lane takes two neighbouring columns and a block of 32 rows.
+// The LDS row pitch of 130 16-bit values (130 of binary32) puts the lanes of
+// a wave, which read neighbouring dwords of one row, on different banks.
+template <int DT>
+__global__ __launch_bounds__(kQuantThreads) void k_quant_tile(QuantArgs q)
+{
+    using Elem = typename Type<DT>::Elem;
+    constexpr int T = kQuantTile;
+    constexpr int kRowWords = T * Type<DT>::kBytes / 4 + 4;
+    __shared__ __attribute__((aligned(16))) uint32_t tile[T * kRowWords];
+    const int t = static_cast<int>(threadIdx.x);
+    const int64_t batch = blockIdx.y;
+    const int64_t col_tiles = q.pcols / T;
+    const int64_t unit = blockIdx.x / col_tiles;        // block of 128 padded rows
+    int64_t row0 = unit * T, nrows = q.rows - row0;
+    if (q.offsets) {
+        const Place p = locate(q.offsets, q.groups, q.rows, T, unit);
+        if (p.group < 0) return;
+        row0 = p.row;
+        nrows = p.rows;
+    }
+    if (nrows > T) nrows = T;
+    const int64_t col0 = (blockIdx.x - unit * col_tiles) * T;
+    const Elem* x = static_cast<const Elem*>(q.x) + batch * q.batch_stride;
+    const int sub = t & 15;
+    const int64_t col = col0 + sub * 8, left = q.cols - col;
+    const int n = left < 0 ? 0 : (left > 8 ? 8 : static_cast<int>(left));
+    Octet<DT> v[T / 16];
+#pragma unroll
+    for (int i = 0; i < T / 16; ++i) {
+        const int r = i * 16 + (t >> 4);
+        v[i].load(x + (row0 + r) * q.row_stride + col, r < nrows ? n : 0, q.wide);
+    }
+#pragma unroll
+    for (int i = 0; i < T / 16; ++i) {
+        const int r = i * 16 + (t >> 4);
+#pragma unroll
+        for (int j = 0; j < Octet<DT>::kWords / 4; ++j)
+            *reinterpret_cast<u32x4*>(&tile[r * kRowWords + sub * Octet<DT>::kWords + 4 * j]) =
+                u32x4{v[i].w[4 * j], v[i].w[4 * j + 1], v[i].w[4 * j + 2], v[i].w[4 * j + 3]};
+        if (!q.codes) continue;
+        const uint32_t s = scale_code(exponent_of<DT>(quad_max(v[i].top())));
+        const uint32_t c = s == kScaleNaN ? 0u : v[i].codes(scale_operand(s));
+        if (r >= nrows || col >= q.pcols) continue;
+        const int64_t at = (batch * q.rows + row0 + r) * (q.pcols / kBlock) + (col0 >> 5);
+        *reinterpret_cast<uint32_t*>(q.codes + at * (kBlock / 2) + sub * 4) = c;
+        if ((sub & 3) == 0) q.scales[at + (sub >> 2)] = static_cast<uint8_t>(s);
+    }
+    __syncthreads();
+    const int pair = t & 63, rb = t >> 6;               // columns 2 pair, 2 pair + 1; rows 32 rb ..
+    uint32_t top[2] = {0, 0};
+    u32x4 out[2] = {};
+    float sc[2];
+    uint32_t s[2];
+    if constexpr (DT == kF32) {
+        u32x2 d[kBlock];
+#pragma unroll
+        for (int i = 0; i < kBlock; ++i) {
+            d[i] = *reinterpret_cast<const u32x2*>(&tile[(rb * kBlock + i) * kRowWords + 2 * pair]);
+            top[0] = max(top[0], d[i][0] & 0x7fffffffu);
+            top[1] = max(top[1], d[i][1] & 0x7fffffffu);
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            s[c] = scale_code(exponent_of<DT>(top[c]));
+            sc[c] = scale_operand(s[c]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t r = 0;
+                r = convert_f32<0>(r, d[8 * i][c], d[8 * i + 1][c], sc[c]);
+                r = convert_f32<1>(r, d[8 * i + 2][c], d[8 * i + 3][c], sc[c]);
+                r = convert_f32<2>(r, d[8 * i + 4][c], d[8 * i + 5][c], sc[c]);
+                r = convert_f32<3>(r, d[8 * i + 6][c], d[8 * i + 7][c], sc[c]);
+                out[c][i] = r;
+            }
+        }
+    } else {
+        uint32_t d[kBlock], m = 0;
+#pragma unroll
+        for (int i = 0; i < kBlock; ++i) {
+            d[i] = tile[(rb * kBlock + i) * kRowWords + pair];
+            m = max_u16x2(m, d[i] & 0x7fff7fffu);
+        }
+        top[0] = m & 0xffffu;
+        top[1] = m >> 16;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            s[c] = scale_code(exponent_of<DT>(top[c]));
+            sc[c] = scale_operand(s[c]);
+            // the same column of two neighbouring rows as one pair
+            constexpr uint32_t kLow = 0x05040100u, kHigh = 0x07060302u;
+            const uint32_t sel = c ? kHigh : kLow;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t r = 0;
+                r = convert_16<DT, 0>(r, __builtin_amdgcn_perm(d[8 * i + 1], d[8 * i], sel), sc[c]);
+                r = convert_16<DT, 1>(r, __builtin_amdgcn_perm(d[8 * i + 3], d[8 * i + 2], sel), sc[c]);
+                r = convert_16<DT, 2>(r, __builtin_amdgcn_perm(d[8 * i + 5], d[8 * i + 4], sel), sc[c]);
+                r = convert_16<DT, 3>(r, __builtin_amdgcn_perm(d[8 * i + 7], d[8 * i + 6], sel), sc[c]);
+                out[c][i] = r;
+            }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const int64_t cc = col0 + 2 * pair + c;
+        if (cc >= q.cols) continue;
+        if (s[c] == kScaleNaN) out[c] = u32x4{0, 0, 0, 0};
+        const int64_t at = (batch * q.cols + cc) * (q.prows / kBlock) + unit * (T / kBlock) + rb;
+        *reinterpret_cast<u32x4*>(q.codes_t + at * (kBlock / 2)) = out[c];
+        q.scales_t[at] = static_cast<uint8_t>(s[c]);
+    }
+}
+
+// ---- results in the storage types -----------------------------------------
+
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b)
+{
+    return __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(a), static_cast<__bf16>(b)});
+}
+__device__ __forceinline__ uint32_t f16_pair(float a, float b)
+{
+    return __builtin_bit_cast(uint32_t, f16x2{static_cast<_Float16>(a), static_cast<_Float16>(b)});
+}
+
+// Stores n (1..4) of four neighbouring results, rounded once to nearest even.
+template <int DT>
+__device__ __forceinline__ void store4(void* out, int64_t at, f32x4 v, int n, bool wide)
+{
+    if constexpr (DT == kF32) {
+        float* p = static_cast<float*>(out) + at;
+        if (n >= 4 && wide) {
+            *reinterpret_cast<f32x4*>(p) = v;
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) p[i] = v[i];
+    } else {
+        const u32x2 w = DT == kBF16 ? u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])}
+                                    : u32x2{f16_pair(v[0], v[1]), f16_pair(v[2], v[3])};
+        uint16_t* p = static_cast<uint16_t*>(out) + at;
+        if (n >= 4 && wide) {
+            *reinterpret_cast<u32x2*>(p) = w;
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) p[i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+    }
+}
+
+// ---- dequantisation ---------------------------------------------------------
+
+// Eight values a lane.
+template <int DT>
+__global__ __launch_bounds__(kQuantThreads) void k_dequant(DequantArgs d, int64_t octets)
+{
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * kQuantThreads + threadIdx.x;
+    if (i >= octets) return;
+    const int64_t per_row = d.pcols / 8, row = i / per_row, col = (i - row * per_row) * 8;
+    if (col >= d.cols) return;
+    const uint32_t c = reinterpret_cast<const uint32_t*>(d.codes)[i];
+    const uint32_t s = d.scales[i >> 2];
+    const float scale = s == kScaleNaN ? __builtin_nanf("") : __builtin_bit_cast(float, s ? s << 23 : 1u << 22);
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t k = (c >> (4 * j)) & 15u, e = (k >> 1) & 3u, m = k & 1u;
+        const float mag = e ? __builtin_bit_cast(float, ((e + 126u) << 23) | (m << 22)) : 0.5f * static_cast<float>(m);
+        v[j] = (k & 8u ? -mag : mag) * scale;
+    }
+    const int64_t left = d.cols - col;
+    const int n = left > 8 ? 8 : static_cast<int>(left);
+    store4<DT>(d.out, row * d.row_stride + col, f32x4{v[0], v[1], v[2], v[3]}, n, d.wide);
+    if (n > 4) store4<DT>(d.out, row * d.row_stride + col + 4, f32x4{v[4], v[5], v[6], v[7]}, n - 4, d.wide);
+}
+
+// ---- products -----------------------------------------------------------------
+
+// A wave's fragment of a matrix for the 16x16x128 instruction: lane l holds
+// the 32 columns 32 (l / 16) .. of row l mod 16, and the scale of that block.
+__device__ __forceinline__ i32x8 widen(i32x4 v) { return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
+
+// Four waves, 32 x 32 results each.  The fragment of b is the instruction's
+// first operand, so a lane's four results are neighbours in a row of out.
+template <int DT, int G>
+__global__ __launch_bounds__(kMatmulThreads) void k_matmul(MatmulArgs p)
+{
+    const int t = static_cast<int>(threadIdx.x), wave = t >> 6, lane = t & 63, r = lane & 15, g = lane >> 4;
+    const int64_t unit = blockIdx.x / p.n_tiles, ntile = blockIdx.x - unit * p.n_tiles;
+    int64_t row0 = unit * kMatmulTile, mrows = p.m - row0;
+    int64_t step0 = 0, steps = p.steps;
+    const uint8_t* b = p.b;
+    const uint8_t* bs = p.bs;
+    int64_t out0 = 0;
+    if constexpr (G == kByRows) {
+        const Place at = locate(p.offsets, p.groups, p.rows, kMatmulTile, unit);
+        row0 = at.row;
+        mrows = at.rows;
+        if (at.group < 0) {
+            if (!p.zero_rest || mrows <= 0) return;
+            steps = 0;   // rows of no group: the sum over nothing
+        } else {
+            b += at.group * p.n * p.steps * (kPad / 2);
+            bs += at.group * p.n * p.steps * (kPad / kBlock);
+        }
+    }
+    if constexpr (G == kByContraction) {
+        const Place at = units_of(p.offsets, p.rows, kPad, static_cast<int32_t>(blockIdx.y));
+        step0 = at.first;
+        steps = at.units;
+        if (step0 > p.steps) step0 = p.steps;
+        if (steps > p.steps - step0) steps = p.steps - step0;
+        out0 = static_cast<int64_t>(blockIdx.y) * p.m * p.out_stride;
+    }
+    const int64_t n0 = ntile * kMatmulTile + (wave & 1) * 32;
+    const int64_t m0 = (wave >> 1) * 32;
+    const uint8_t *ap[2], *asp[2], *bp[2], *bsp[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        int64_t m = m0 + 16 * i + r, n = n0 + 16 * i + r;   // rows behind the edge read the last one
+        m = row0 + (m < mrows ? m : mrows - 1);
+        n = n < p.n ? n : p.n - 1;
+        ap[i] = p.a + (m * p.steps + step0) * (kPad / 2) + g * 16;
+        asp[i] = p.as + (m * p.steps + step0) * (kPad / kBlock) + g;
+        bp[i] = b + (n * p.steps + step0) * (kPad / 2) + g * 16;
+        bsp[i] = bs + (n * p.steps + step0) * (kPad / kBlock) + g;
+    }
+    f32x4 acc[2][2] = {};
+    for (int64_t k = 0; k < steps; ++k) {
+        i32x8 av[2], bv[2];
+        int as[2], bsc[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            av[i] = widen(*reinterpret_cast<const i32x4*>(ap[i] + k * (kPad / 2)));
+            bv[i] = widen(*reinterpret_cast<const i32x4*>(bp[i] + k * (kPad / 2)));
+            as[i] = asp[i][k * (kPad / kBlock)];
+            bsc[i] = bsp[i][k * (kPad / kBlock)];
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bv[j], av[i], acc[i][j], 4, 4, 0, bsc[j],
+                                                                            0, as[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int64_t m = m0 + 16 * i + r;
+        if (m >= mrows) continue;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int64_t n = n0 + 16 * j + 4 * g, left = p.n - n;
+            if (left <= 0) continue;
+            store4<DT>(p.out, out0 + (row0 + m) * p.out_stride + n, acc[i][j], left > 4 ? 4 : static_cast<int>(left),
+                       p.wide);
+        }
+    }
+}
+
+}  // namespace
+
+const void* quant_rows_kernel(int dtype)
+{
+    const void* fns[3] = {reinterpret_cast<const void*>(&k_quant_rows<kF32>),
+                          reinterpret_cast<const void*>(&k_quant_rows<kF16>),
+                          reinterpret_cast<const void*>(&k_quant_rows<kBF16>)};
+    return fns[dtype];
+}
+
+const void* quant_tile_kernel(int dtype)
+{
+    const void* fns[3] = {reinterpret_cast<const void*>(&k_quant_tile<kF32>),
+                          reinterpret_cast<const void*>(&k_quant_tile<kF16>),
+                          reinterpret_cast<const void*>(&k_quant_tile<kBF16>)};
+    return fns[dtype];
+}
+
+const void* dequant_kernel(int dtype)
+{
+    const void* fns[3] = {reinterpret_cast<const void*>(&k_dequant<kF32>),
+                          reinterpret_cast<const void*>(&k_dequant<kF16>),
+                          reinterpret_cast<const void*>(&k_dequant<kBF16>)};
+    return fns[dtype];
+}
+
+template <int G>
+const void* matmul_of(int dtype)
+{
+    const void* fns[3] = {reinterpret_cast<const void*>(&k_matmul<kF32, G>),
+                          reinterpret_cast<const void*>(&k_matmul<kF16, G>),
+                          reinterpret_cast<const void*>(&k_matmul<kBF16, G>)};
+    return fns[dtype];
+}
+
+const void* matmul_kernel(int out_dtype, int grouping)
+{
+    return grouping == kPlain ? matmul_of<kPlain>(out_dtype)
+           : grouping == kByRows ? matmul_of<kByRows>(out_dtype)
+                                 : matmul_of<kByContraction>(out_dtype);
+}
+
+}  // namespace mx4

@@ -1,0 +1,531 @@
+"""Microscaled 4-bit floats: quantisation, products of quantised matrices and
+products grouped by expert (binding of ``liboptimizer_mx4.so``,
+``include/optimizer_mx4.h``).
+
+    q = mx4_quantize(w)                       Mx4: codes, scales, k
+    q, qt = mx4_quantize_both(w)              along the columns and along the rows, one read
+    w4 = mx4_dequantize(q, torch.bfloat16)    the values held
+    y = mx4_matmul(x, q)                      x q^T; x as values (quantised on the way) or Mx4
+    y = mx4_grouped_matmul(x, qe, offsets)    rows offsets[e]:offsets[e+1] of x against expert e
+    y = mx4_linear(x, w)                      the layer with its gradients (straight through
+    y = mx4_grouped_linear(x, w, offsets)     the roundings), all three products in 4 bits
+    Mx4Weight(w)                              both 4-bit forms of a weight, refreshed by its
+                                              optimizer's step (``mx4=`` of the collections)
+
+As in the rest of the package, functions check and marshal arguments; all
+arithmetic runs in the HIP kernels.  Every call goes to the current stream of
+the operands' device, or to ``stream``; results and workspaces are allocated
+on that stream.  The functions other than the two layers do not record
+gradients.
+"""
+from __future__ import annotations
+
+import ctypes
+import os
+
+import torch
+
+from . import _lib
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+LIBRARY = os.path.join(HERE, "liboptimizer_mx4.so")
+HEADER = os.path.join(os.path.dirname(HERE), "include", "optimizer_mx4.h")
+
+MX4_BLOCK = 32     # values that share a scale
+MX4_PAD = 128      # columns of a held matrix are padded to this
+_DTYPES = {torch.float32: _lib.OU_F32, torch.float16: _lib.OU_F16, torch.bfloat16: _lib.OU_BF16}
+_mx4 = None
+
+
+def load_mx4(path: str = LIBRARY) -> ctypes.CDLL:
+    """Load the library of the 4-bit operators (raises if it is missing)."""
+    global _mx4
+    if _mx4 is not None and path == LIBRARY:
+        return _mx4
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is not built; run __graft_entry__.build() "
+                          "(python -c 'import __graft_entry__ as g; g.build()')")
+    lib = ctypes.CDLL(path)
+    i32, i64, vp = ctypes.c_int, ctypes.c_int64, ctypes.c_void_p
+    for name, res, args in (
+            ("ou_mx4_columns", i64, [i64]),
+            ("ou_mx4_grouped_columns", i64, [i64, i32]),
+            ("ou_mx4_quantize", i32, [i32, vp, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp]),
+            ("ou_mx4_quantize_grouped", i32, [i32, vp, i64, i64, i64, vp, i32, vp, vp, vp, vp, vp]),
+            ("ou_mx4_dequantize", i32, [i32, vp, vp, i64, i64, vp, i64, vp]),
+            ("ou_mx4_matmul_workspace_bytes", i64, [i64, i64, i64, i32]),
+            ("ou_mx4_grouped_workspace_bytes", i64, [i64, i64, i64, i32, i32]),
+            ("ou_mx4_matmul", i32, [i32, vp, vp, i64, vp, vp, i64, i64, vp, i64, vp, i64, vp]),
+            ("ou_mx4_matmul_values", i32, [i32, vp, i64, i64, i32, vp, vp, i64, i64, vp, i64, vp, i64, vp]),
+            ("ou_mx4_grouped_matmul", i32, [i32, vp, vp, i64, vp, vp, i64, i64, vp, i32, vp, i64, i32, vp, i64, vp]),
+            ("ou_mx4_grouped_matmul_values", i32, [i32, vp, i64, i64, i32, vp, vp, i64, i64, vp, i32, vp, i64, i32,
+                                                   vp, i64, vp]),
+            ("ou_mx4_grouped_outer", i32, [i32, vp, vp, i64, vp, vp, i64, i64, vp, i32, vp, vp]),
+            ("ou_mx4_last_error", ctypes.c_char_p, [])):
+        f = getattr(lib, name)
+        f.restype, f.argtypes = res, args
+    if path == LIBRARY:
+        _mx4 = lib
+    return lib
+
+
+def _check(status: int, lib) -> None:
+    if status:
+        raise _lib.OptimizerUpdateError(status, lib.ou_mx4_last_error().decode(errors="replace"))
+
+
+def _columns(k: int) -> int:
+    return -(-k // MX4_PAD) * MX4_PAD
+
+
+class Mx4:
+    """A matrix, or a batch of them, held in 4 bits: ``codes`` uint8
+    [..., R, P / 2], ``scales`` uint8 [..., R, P / 32], ``k`` columns, P = k
+    rounded up to 128 (the layout of ``include/optimizer_mx4.h``)."""
+
+    __slots__ = ("codes", "scales", "k")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, k: int):
+        p = _columns(k)
+        if k < 0 or codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+            raise ValueError("codes and scales are uint8 tensors, k >= 0")
+        if codes.dim() < 2 or codes.shape[:-1] != scales.shape[:-1] or codes.shape[-1] * 2 != p \
+                or scales.shape[-1] * MX4_BLOCK != p:
+            raise ValueError(f"k = {k} wants codes [..., {p // 2}] and scales [..., {p // MX4_BLOCK}]: "
+                             f"got {list(codes.shape)} and {list(scales.shape)}")
+        if not codes.is_contiguous() or not scales.is_contiguous() or codes.device != scales.device:
+            raise ValueError("codes and scales must be contiguous and on one device")
+        self.codes, self.scales, self.k = codes, scales, k
+
+    @property
+    def shape(self) -> torch.Size:
+        return torch.Size((*self.codes.shape[:-1], self.k))
+
+    @property
+    def device(self) -> torch.device:
+        return self.codes.device
+
+    def __getitem__(self, i: int) -> "Mx4":
+        """Matrix i of a batch."""
+        if self.codes.dim() < 3:
+            raise ValueError("not a batch of matrices")
+        return _held(self.codes[i], self.scales[i], self.k)
+
+    def __repr__(self) -> str:
+        return f"Mx4(shape={list(self.shape)}, device={self.device})"
+
+
+def _held(codes, scales, k) -> Mx4:
+    """An Mx4 of tensors made here."""
+    q = Mx4.__new__(Mx4)
+    q.codes, q.scales, q.k = codes, scales, k
+    return q
+
+
+def _empty(lead, k, device) -> Mx4:
+    p = _columns(k)
+    return _held(torch.empty((*lead, p // 2), dtype=torch.uint8, device=device),
+                 torch.empty((*lead, p // MX4_BLOCK), dtype=torch.uint8, device=device), k)
+
+
+class _Call:
+    """The device and the stream of a call: makes both current (what is
+    allocated inside belongs to that stream) and holds the handle."""
+
+    __slots__ = ("index", "stream", "handle", "_ctx")
+
+    def __init__(self, t: torch.Tensor, stream):
+        index = t.get_device()
+        if index < 0:
+            raise ValueError("operands must be tensors on a HIP device")
+        self.index = index
+        self.stream = stream
+        self._ctx = None
+
+    def __enter__(self) -> "_Call":
+        s = self.stream
+        if s is not None:
+            if not isinstance(s, torch.cuda.Stream):
+                s = torch.cuda.ExternalStream(int(s), device=torch.device("cuda", self.index))
+            self._ctx = torch.cuda.stream(s)
+            self._ctx.__enter__()
+            self.handle = s.cuda_stream
+        else:
+            if torch.cuda.current_device() != self.index:
+                self._ctx = torch.cuda.device(self.index)
+                self._ctx.__enter__()
+            self.handle = torch._C._cuda_getCurrentRawStream(self.index)
+        return self
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+        return False
+
+
+def _values(x, name: str, dims: int | None = None) -> int:
+    """dtype code of a tensor of values."""
+    if not isinstance(x, torch.Tensor) or x.get_device() < 0:
+        raise ValueError(f"{name} must be a tensor on a HIP device")
+    dt = _DTYPES.get(x.dtype)
+    if dt is None:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16")
+    if dims is not None and x.dim() != dims:
+        raise ValueError(f"{name} must have {dims} axes, got {x.dim()}")
+    return dt
+
+
+def _same_device(first, **others) -> None:
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, the first operand on {first.device}")
+
+
+def _row_stride(x: torch.Tensor, name: str) -> int:
+    """Elements between the rows of x [R, C], its columns being neighbours."""
+    r, c = x.shape
+    if c > 1 and x.stride(1) != 1 or r > 1 and x.stride(0) < c:
+        raise ValueError(f"the last axis of {name} must be contiguous and its rows apart")
+    return x.stride(0) if r > 1 else c
+
+
+def _offsets(offsets, like) -> int:
+    """Groups of an offsets tensor."""
+    if not isinstance(offsets, torch.Tensor) or offsets.dtype != torch.int32 or offsets.dim() != 1 \
+            or offsets.shape[0] < 1 or not offsets.is_contiguous():
+        raise ValueError("offsets must be a contiguous int32 tensor of groups + 1 values")
+    _same_device(like, offsets=offsets)
+    return offsets.shape[0] - 1
+
+
+def _quantize(x: torch.Tensor, rows: bool, transposed: bool, stream) -> tuple[Mx4 | None, Mx4 | None]:
+    dt = _values(x, "x")
+    if x.dim() < 2:
+        raise ValueError("x must have two axes at least")
+    r, c = x.shape[-2], x.shape[-1]
+    lead = x.shape[:-2]
+    if c > 1 and x.stride(-1) != 1 and x.stride(-2) == 1 and x.dim() == 2:
+        # a transposed view: its rows are the columns of what lies in memory
+        qt, q = _quantize(x.t(), transposed, rows, stream)
+        return q, qt
+    batch = lead.numel() if len(lead) else 1
+    if len(lead) == 0:
+        rs, bs = _row_stride(x, "x"), 0
+    else:
+        if not x.is_contiguous():
+            raise ValueError("a batch of matrices must be contiguous")
+        rs, bs = c, r * c
+    lib = load_mx4()
+    with _Call(x, stream) as call:
+        q = _empty((*lead, r), c, x.device) if rows else None
+        qt = _empty((*lead, c), r, x.device) if transposed else None
+        _check(lib.ou_mx4_quantize(dt, x.data_ptr(), batch, r, c, rs, bs,
+                                   q.codes.data_ptr() if rows else None, q.scales.data_ptr() if rows else None,
+                                   qt.codes.data_ptr() if transposed else None,
+                                   qt.scales.data_ptr() if transposed else None, call.handle), lib)
+    return q, qt
+
+
+def mx4_quantize(x: torch.Tensor, stream=None) -> Mx4:
+    """x [..., R, C] (float32, float16 or bfloat16) in 4 bits along its last
+    axis.  A matrix may have any row stride, or be the transposed view of
+    one; a batch must be contiguous."""
+    return _quantize(x, True, False, stream)[0]
+
+
+def mx4_quantize_both(x: torch.Tensor, stream=None) -> tuple[Mx4, Mx4]:
+    """(x along its last axis, x transposed along its rows): [..., R, C] and
+    [..., C, R] in 4 bits, with one read of x."""
+    return _quantize(x, True, True, stream)
+
+
+def mx4_quantize_grouped(x: torch.Tensor, offsets: torch.Tensor, rows: bool = True,
+                         stream=None) -> tuple[Mx4 | None, Mx4]:
+    """x [T, C] along its columns (None with rows=False) and, group by group,
+    along its rows: group e is rows offsets[e]:offsets[e + 1] (int32, on the
+    device), a matrix of its own padded to 128 rows (``ou_mx4_quantize_grouped``).
+    The operands of ``mx4_grouped_outer``."""
+    dt = _values(x, "x", 2)
+    groups = _offsets(offsets, x)
+    t, c = x.shape
+    rs = _row_stride(x, "x")
+    lib = load_mx4()
+    p = int(lib.ou_mx4_grouped_columns(t, groups))
+    with _Call(x, stream) as call:
+        q = _empty((t,), c, x.device) if rows else None
+        qt = _empty((c,), p, x.device)
+        _check(lib.ou_mx4_quantize_grouped(dt, x.data_ptr(), t, c, rs, offsets.data_ptr(), groups,
+                                           q.codes.data_ptr() if rows else None,
+                                           q.scales.data_ptr() if rows else None,
+                                           qt.codes.data_ptr(), qt.scales.data_ptr(), call.handle), lib)
+    return q, qt
+
+
+def mx4_dequantize(q: Mx4, dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+    """The values that q holds, in ``dtype`` (or in ``out``, contiguous)."""
+    if not isinstance(q, Mx4):
+        raise ValueError("q must be an Mx4")
+    lib = load_mx4()
+    with _Call(q.codes, stream) as call:
+        if out is None:
+            if dtype not in _DTYPES:
+                raise ValueError("dtype must be float32, float16 or bfloat16")
+            out = torch.empty(q.shape, dtype=dtype, device=q.device)
+        else:
+            _values(out, "out")
+            _same_device(q, out=out)
+            if out.shape != q.shape or not out.is_contiguous():
+                raise ValueError(f"out must be contiguous, of shape {list(q.shape)}")
+        rows = out.numel() // q.k if q.k else 0
+        _check(lib.ou_mx4_dequantize(_DTYPES[out.dtype], q.codes.data_ptr(), q.scales.data_ptr(), rows, q.k,
+                                     out.data_ptr(), q.k, call.handle), lib)
+    return out
+
+
+def _output(out, rows: int, n: int, dtype, like) -> tuple[torch.Tensor, int]:
+    if out is None:
+        if dtype not in _DTYPES:
+            raise ValueError("dtype must be float32, float16 or bfloat16")
+        return torch.empty((rows, n), dtype=dtype, device=like.device), n
+    _values(out, "out", 2)
+    _same_device(like, out=out)
+    if tuple(out.shape) != (rows, n):
+        raise ValueError(f"out must have shape [{rows}, {n}], got {list(out.shape)}")
+    return out, _row_stride(out, "out")
+
+
+def _left(a, k: int) -> tuple[bool, int, torch.dtype, torch.Tensor]:
+    """(given as values, rows, default dtype of a result, a tensor of it)."""
+    if isinstance(a, Mx4):
+        if a.codes.dim() != 2:
+            raise ValueError("the left operand must be a matrix")
+        if a.k != k:
+            raise ValueError(f"the operands contract {a.k} and {k} columns")
+        return False, a.codes.shape[0], torch.bfloat16, a.codes
+    _values(a, "the left operand", 2)
+    if a.shape[1] != k:
+        raise ValueError(f"the operands contract {a.shape[1]} and {k} columns")
+    return True, a.shape[0], a.dtype, a
+
+
+def mx4_matmul(a, b: Mx4, dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+    """a b^T: a [M, K] as values (quantised along K on the way, in the same
+    call) or as Mx4, b an Mx4 [N, K].  The result is [M, N] of ``dtype``
+    (default: a's, bfloat16 for an Mx4), or ``out`` (any row stride)."""
+    if not isinstance(b, Mx4) or b.codes.dim() != 2:
+        raise ValueError("b must be an Mx4 matrix")
+    values, m, default, at = _left(a, b.k)
+    _same_device(at, b=b)
+    n, k = b.codes.shape[0], b.k
+    lib = load_mx4()
+    with _Call(at, stream) as call:
+        out, stride = _output(out, m, n, dtype or default, at)
+        need = lib.ou_mx4_matmul_workspace_bytes(m, n, k, int(values))
+        ws = torch.empty(need, dtype=torch.uint8, device=at.device) if need > 0 else None
+        wp = ws.data_ptr() if ws is not None else None
+        if values:
+            st = lib.ou_mx4_matmul_values(_DTYPES[a.dtype], a.data_ptr(), m, _row_stride(a, "a"), _DTYPES[out.dtype],
+                                          b.codes.data_ptr(), b.scales.data_ptr(), n, k, out.data_ptr(), stride, wp,
+                                          need, call.handle)
+        else:
+            st = lib.ou_mx4_matmul(_DTYPES[out.dtype], a.codes.data_ptr(), a.scales.data_ptr(), m,
+                                   b.codes.data_ptr(), b.scales.data_ptr(), n, k, out.data_ptr(), stride, wp, need,
+                                   call.handle)
+        _check(st, lib)
+    return out
+
+
+def mx4_grouped_matmul(a, b: Mx4, offsets: torch.Tensor, dtype: torch.dtype | None = None,
+                       out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Rows of a [T, K] (values or Mx4) by groups: rows offsets[e]:offsets[e + 1]
+    times matrix e of b [E, N, K], transposed.  ``offsets``: E + 1 rising int32
+    on the device, read there.  Rows of no group are 0 in a new result and left
+    as they were in ``out``."""
+    if not isinstance(b, Mx4) or b.codes.dim() != 3:
+        raise ValueError("b must be an Mx4 batch [groups, N, K]")
+    values, m, default, at = _left(a, b.k)
+    _same_device(at, b=b)
+    groups = _offsets(offsets, at)
+    e, n, k = *b.codes.shape[:2], b.k
+    if groups != e:
+        raise ValueError(f"offsets name {groups} groups, b holds {e}")
+    lib = load_mx4()
+    zero_rest = int(out is None)
+    with _Call(at, stream) as call:
+        out, stride = _output(out, m, n, dtype or default, at)
+        need = lib.ou_mx4_grouped_workspace_bytes(m, n, k, groups, int(values))
+        ws = torch.empty(need, dtype=torch.uint8, device=at.device) if need > 0 else None
+        wp = ws.data_ptr() if ws is not None else None
+        if values:
+            st = lib.ou_mx4_grouped_matmul_values(_DTYPES[a.dtype], a.data_ptr(), m, _row_stride(a, "a"),
+                                                  _DTYPES[out.dtype], b.codes.data_ptr(), b.scales.data_ptr(), n, k,
+                                                  offsets.data_ptr(), groups, out.data_ptr(), stride, zero_rest, wp,
+                                                  need, call.handle)
+        else:
+            st = lib.ou_mx4_grouped_matmul(_DTYPES[out.dtype], a.codes.data_ptr(), a.scales.data_ptr(), m,
+                                           b.codes.data_ptr(), b.scales.data_ptr(), n, k, offsets.data_ptr(), groups,
+                                           out.data_ptr(), stride, zero_rest, wp, need, call.handle)
+        _check(st, lib)
+    return out
+
+
+def mx4_grouped_outer(at: Mx4, bt: Mx4, offsets: torch.Tensor, rows: int, dtype: torch.dtype = torch.bfloat16,
+                      stream=None) -> torch.Tensor:
+    """[E, M, N]: for every group the sum over its rows of a's row times b's,
+    from the transposed forms [M, *] and [N, *] that ``mx4_quantize_grouped``
+    made of matrices of ``rows`` rows with the same offsets."""
+    for name, q in (("at", at), ("bt", bt)):
+        if not isinstance(q, Mx4) or q.codes.dim() != 2:
+            raise ValueError(f"{name} must be an Mx4 matrix")
+    if dtype not in _DTYPES:
+        raise ValueError("dtype must be float32, float16 or bfloat16")
+    _same_device(at, bt=bt)
+    groups = _offsets(offsets, at)
+    lib = load_mx4()
+    p = int(lib.ou_mx4_grouped_columns(rows, groups))
+    if at.k != p or bt.k != p:
+        raise ValueError(f"{rows} rows in {groups} groups are held in {p} columns: got {at.k} and {bt.k}")
+    m, n = at.codes.shape[0], bt.codes.shape[0]
+    with _Call(at.codes, stream) as call:
+        out = torch.empty((groups, m, n), dtype=dtype, device=at.device)
+        _check(lib.ou_mx4_grouped_outer(_DTYPES[dtype], at.codes.data_ptr(), at.scales.data_ptr(), m,
+                                        bt.codes.data_ptr(), bt.scales.data_ptr(), n, rows, offsets.data_ptr(),
+                                        groups, out.data_ptr(), call.handle), lib)
+    return out
+
+
+# ------------------------------------------------------------------ layers
+
+class Mx4Weight:
+    """The 4-bit forms of a weight [N, K] or [E, N, K] for the layers below:
+    ``q`` along K (forward) and ``qt`` along N (the input's gradient).
+    ``refresh()`` quantises the weight's present values into them; an optimizer
+    built with ``mx4=[...]`` does so after every step, so that the passes in
+    between (micro-batches) read the 4-bit forms alone."""
+
+    def __init__(self, weight: torch.Tensor):
+        if weight.dim() not in (2, 3):
+            raise ValueError("weight must be [N, K] or [E, N, K]")
+        if not weight.is_contiguous():
+            raise ValueError("weight must be contiguous")
+        self.weight = weight
+        self.q, self.qt = mx4_quantize_both(weight.detach())
+
+    def refresh(self, stream=None) -> None:
+        """Quantise the weight's present values into the same buffers."""
+        w, q, qt = self.weight.detach(), self.q, self.qt
+        dt = _values(w, "weight")
+        r, c = w.shape[-2:]
+        if w.shape != q.shape or not w.is_contiguous():
+            raise ValueError("the weight changed its shape or layout")
+        lib = load_mx4()
+        with _Call(w, stream) as call:
+            _check(lib.ou_mx4_quantize(dt, w.data_ptr(), w.shape[0] if w.dim() == 3 else 1, r, c, c, r * c,
+                                       q.codes.data_ptr(), q.scales.data_ptr(), qt.codes.data_ptr(),
+                                       qt.scales.data_ptr(), call.handle), lib)
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, held):
+        need_x, need_w = ctx.needs_input_grad[:2]
+        q, qt = (held.q, held.qt) if held is not None else _quantize(w, True, need_x, None)
+        ctx.x_dtype, ctx.w_dtype = x.dtype, w.dtype
+        if need_w:
+            xq, xt = mx4_quantize_both(x)
+            y = mx4_matmul(xq, q, x.dtype)
+        else:
+            xt = None
+            y = mx4_matmul(x, q)
+        ctx.held = (qt if need_x else None, xt)
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        need_x, need_w = ctx.needs_input_grad[:2]
+        qt, xt = ctx.held
+        dy = dy.contiguous()
+        dx = dw = None
+        if need_w:
+            dq, dt = _quantize(dy, need_x, True, None)
+            dw = mx4_matmul(dt, xt, ctx.w_dtype)
+            if need_x:
+                dx = mx4_matmul(dq, qt, ctx.x_dtype)
+        elif need_x:
+            dx = mx4_matmul(dy, qt, ctx.x_dtype)
+        return dx, dw, None
+
+
+class _GroupedLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, offsets, held):
+        need_x, need_w = ctx.needs_input_grad[:2]
+        q, qt = (held.q, held.qt) if held is not None else _quantize(w, True, need_x, None)
+        ctx.x_dtype, ctx.w_dtype, ctx.rows = x.dtype, w.dtype, x.shape[0]
+        if need_w:
+            xq, xt = mx4_quantize_grouped(x, offsets)
+            y = mx4_grouped_matmul(xq, q, offsets, x.dtype)
+        else:
+            xt = None
+            y = mx4_grouped_matmul(x, q, offsets)
+        ctx.held = (qt if need_x else None, xt)
+        ctx.save_for_backward(offsets)
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        need_x, need_w = ctx.needs_input_grad[:2]
+        qt, xt = ctx.held
+        offsets, = ctx.saved_tensors
+        dy = dy.contiguous()
+        dx = dw = None
+        if need_w:
+            dq, dt = mx4_quantize_grouped(dy, offsets, rows=need_x)
+            dw = mx4_grouped_outer(dt, xt, offsets, ctx.rows, ctx.w_dtype)
+            if need_x:
+                dx = mx4_grouped_matmul(dq, qt, offsets, ctx.x_dtype)
+        elif need_x:
+            dx = mx4_grouped_matmul(dy, qt, offsets, ctx.x_dtype)
+        return dx, dw, None, None
+
+
+def _layer_operands(x, w, dims: int):
+    held = w if isinstance(w, Mx4Weight) else None
+    weight = held.weight if held is not None else w
+    _values(x, "x")
+    _values(weight, "w", dims)
+    _same_device(x, w=weight)
+    if not weight.is_contiguous():
+        raise ValueError("w must be contiguous")
+    if x.dim() < 2 or x.shape[-1] != weight.shape[-1]:
+        raise ValueError(f"x must be [..., {weight.shape[-1]}], got {list(x.shape)}")
+    return held, weight
+
+
+def mx4_linear(x: torch.Tensor, w) -> torch.Tensor:
+    """x w^T with its gradients, the three products in 4 bits: with Q the
+    rounding along the contracted axis (in blocks of 32),
+        y = Q(x) Q(w)^T,  dx = Q(dy) Q(w^T)^T,  dw = Q(dy^T) Q(x^T)^T,
+    each summed in binary32 and rounded once to the dtype of x (y, dx) or w
+    (dw).  x is [..., K], w [N, K] or an ``Mx4Weight`` (its 4-bit forms are
+    used as they are, its ``weight`` gets the gradient).  For the backward
+    pass 4-bit forms are kept, not x."""
+    held, weight = _layer_operands(x, w, 2)
+    y = _Linear.apply(x.reshape(-1, x.shape[-1]), weight, held)
+    return y.view(*x.shape[:-1], weight.shape[0])
+
+
+def mx4_grouped_linear(x: torch.Tensor, w, offsets: torch.Tensor) -> torch.Tensor:
+    """``mx4_linear`` by groups: rows offsets[e]:offsets[e + 1] of x [T, K]
+    with expert e of w [E, N, K] (or an ``Mx4Weight``).  Rows of no group give
+    0 and get 0; an expert without rows gets a gradient of 0."""
+    held, weight = _layer_operands(x, w, 3)
+    if x.dim() != 2:
+        raise ValueError("x must be [T, K]")
+    if _offsets(offsets, x) != weight.shape[0]:
+        raise ValueError(f"offsets name {offsets.shape[0] - 1} groups, w holds {weight.shape[0]}")
+    return _GroupedLinear.apply(x, weight, offsets, held)

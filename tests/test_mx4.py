@@ -1,0 +1,214 @@
+"""CPU: the library of the 4-bit operators: its exports, its refusals (no
+device is touched before the arguments are checked) and the binding's."""
+import ctypes
+import os
+import re
+import subprocess
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+import optimizer_update_amd as ou
+from optimizer_update_amd import _lib, mx4
+from tests import mx4_reference as R
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+OK, EINVAL, EUNSUPPORTED, EALIGN, EOVERLAP = 0, -1, -2, -3, -4
+X, C, S, CT, ST, O, W = (0x100000000 * i for i in range(1, 8))
+
+
+@pytest.fixture(scope="module")
+def L():
+    return ou.load_mx4()
+
+
+@pytest.fixture
+def no_gpu():
+    if torch.cuda.is_available():
+        pytest.skip("calls that pass the checks would launch on these addresses")
+
+
+def test_exports_every_header_function(L):
+    names = _lib.header_functions(mx4.HEADER)
+    assert len(names) == 13 and len(set(names)) == 13
+    out = subprocess.run(["nm", "-D", "--defined-only", mx4.LIBRARY], capture_output=True, text=True, check=True).stdout
+    assert set(re.findall(r" T (\w+)$", out, flags=re.M)) == set(names)
+
+
+def test_header_is_plain_c(tmp_path):
+    c = tmp_path / "t.c"
+    c.write_text('#include "optimizer_mx4.h"\nint main(void) { return ou_mx4_columns(1) == 128 ? 0 : 1; }\n')
+    subprocess.run(["gcc", "-std=c11", "-Wall", "-Werror", "-I", os.path.join(ROOT, "include"), "-c", str(c), "-o",
+                    str(tmp_path / "t.o")], check=True)
+
+
+def test_missing_library_fails_loudly(tmp_path):
+    with pytest.raises(ImportError):
+        ou.load_mx4(str(tmp_path / "liboptimizer_mx4.so"))
+
+
+@pytest.mark.parametrize("k,p", [(0, 0), (1, 128), (127, 128), (128, 128), (129, 256), (1 << 31, 1 << 31), (-1, -1)])
+def test_columns(L, k, p):
+    assert L.ou_mx4_columns(k) == p
+
+
+@pytest.mark.parametrize("counts", [[], [0], [1], [128], [129, 0, 1], [127, 128, 129], [1] * 50])
+def test_grouped_columns_hold_any_split(L, counts):
+    rows = sum(counts)
+    have = L.ou_mx4_grouped_columns(rows, len(counts))
+    assert have % 128 == 0 and have >= sum(R.columns(c) for c in counts)
+    assert L.ou_mx4_grouped_columns(-1, 1) == -1 and L.ou_mx4_grouped_columns(1, -1) == -1
+
+
+def _quantize(L, dtype=0, x=X, batch=1, rows=64, cols=256, rs=256, bs=0, c=C, s=S, ct=None, st=None):
+    return L.ou_mx4_quantize(dtype, x, batch, rows, cols, rs, bs, c, s, ct, st, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dtype=3), EINVAL), (dict(dtype=-1), EINVAL), (dict(x=None), EINVAL), (dict(rows=-1), EINVAL),
+    (dict(cols=-1), EINVAL), (dict(rows=(1 << 31) + 1), EINVAL), (dict(rs=255), EINVAL), (dict(batch=-1), EINVAL),
+    (dict(batch=65536), EINVAL), (dict(batch=2, bs=255), EINVAL), (dict(bs=-1), EINVAL), (dict(c=None), EINVAL),
+    (dict(s=None), EINVAL), (dict(c=None, s=None), EINVAL), (dict(ct=CT), EINVAL), (dict(st=ST), EINVAL),
+    (dict(x=X + 2), EALIGN), (dict(dtype=1, x=X + 1), EALIGN), (dict(c=C + 8), EALIGN), (dict(s=S + 2), EALIGN),
+    (dict(ct=CT + 4, st=ST), EALIGN), (dict(c=X), EOVERLAP), (dict(c=X + 64 * 256 * 4 - 16), EOVERLAP),
+    (dict(s=C + 64), EOVERLAP), (dict(ct=CT, st=C), EOVERLAP), (dict(ct=C, st=ST), EOVERLAP),
+    (dict(rows=1 << 31, cols=1 << 31, rs=1 << 31), EINVAL),
+])
+def test_quantize_refusals(L, kw, code):
+    assert _quantize(L, **kw) == code
+    assert L.ou_mx4_last_error()
+
+
+def test_quantize_passes_its_checks(L, no_gpu):
+    assert _quantize(L) == EUNSUPPORTED
+    assert _quantize(L, c=X + 64 * 256 * 4) == EUNSUPPORTED      # right behind x
+    assert _quantize(L, c=None, s=None, ct=CT, st=ST) == EUNSUPPORTED
+    assert _quantize(L, batch=3, bs=64 * 256, ct=CT, st=ST) == EUNSUPPORTED
+
+
+def test_nothing_to_do_is_no_error(L):
+    assert _quantize(L, rows=0, x=None) == OK and _quantize(L, cols=0, x=None) == OK
+    assert _quantize(L, batch=0, x=None) == OK
+    assert L.ou_mx4_dequantize(0, None, None, 0, 5, None, 5, None) == OK
+    assert L.ou_mx4_matmul(0, None, None, 0, None, None, 4, 4, None, 4, None, 0, None) == OK
+    assert L.ou_mx4_matmul(0, None, None, 4, None, None, 0, 4, None, 4, None, 0, None) == OK
+    assert L.ou_mx4_grouped_outer(0, C, S, 8, CT, ST, 8, 0, X, 0, None, None) == OK
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dtype=7), EINVAL), (dict(rows=-1), EINVAL), (dict(cols=-2), EINVAL), (dict(rs=99), EINVAL),
+    (dict(off=None), EINVAL), (dict(off=O + 2), EALIGN), (dict(groups=-1), EINVAL), (dict(groups=65536), EINVAL),
+    (dict(c=None), EINVAL), (dict(ct=None), EINVAL), (dict(st=None), EINVAL), (dict(ct=CT + 1), EALIGN),
+    (dict(ct=X), EOVERLAP), (dict(st=O), EOVERLAP), (dict(x=None), EINVAL),
+])
+def test_quantize_grouped_refusals(L, kw, code):
+    a = dict(dtype=2, x=X, rows=200, cols=100, rs=100, off=O, groups=4, c=C, s=S, ct=CT, st=ST) | kw
+    assert L.ou_mx4_quantize_grouped(*a.values(), None) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dtype=5), EINVAL), (dict(rows=-1), EINVAL), (dict(cols=-1), EINVAL), (dict(rs=63), EINVAL),
+    (dict(c=None), EINVAL), (dict(out=None), EINVAL), (dict(out=O + 1), EALIGN), (dict(out=C), EOVERLAP),
+    (dict(c=C + 4), EALIGN), (dict(s=S + 1), EALIGN),
+])
+def test_dequantize_refusals(L, kw, code):
+    a = dict(dtype=0, c=C, s=S, rows=16, cols=64, out=O, rs=64) | kw
+    assert L.ou_mx4_dequantize(*a.values(), None) == code
+
+
+MATMUL = dict(dt=2, a=X, as_=X + (1 << 24), m=40, b=C, bs=S, n=72, k=300, out=O, os=72, ws=W, wb=1 << 24)
+BAD_PRODUCTS = [
+    (dict(dt=9), EINVAL), (dict(m=-1), EINVAL), (dict(n=-1), EINVAL), (dict(k=-1), EINVAL), (dict(b=None), EINVAL),
+    (dict(bs=None), EINVAL), (dict(os=71), EINVAL), (dict(out=None), EINVAL), (dict(out=O + 1), EALIGN),
+    (dict(b=C + 8), EALIGN), (dict(bs=S + 2), EALIGN), (dict(out=C), EOVERLAP), (dict(out=X), EOVERLAP),
+    (dict(m=1 << 31, n=1 << 31, os=1 << 31), EINVAL),
+]
+
+
+@pytest.mark.parametrize("kw,code", BAD_PRODUCTS + [
+    (dict(a=None), EINVAL), (dict(as_=None), EINVAL), (dict(a=X + 4), EALIGN)])
+def test_matmul_refusals(L, kw, code):
+    assert L.ou_mx4_matmul(*(MATMUL | kw).values(), None) == code
+
+
+def _matmul_values(L, xd=0, xs=300, **kw):
+    a = MATMUL | kw
+    return L.ou_mx4_matmul_values(xd, a["a"], a["m"], xs, a["dt"], a["b"], a["bs"], a["n"], a["k"], a["out"], a["os"],
+                                  a["ws"], a["wb"], None)
+
+
+@pytest.mark.parametrize("kw,code", BAD_PRODUCTS + [
+    (dict(xd=4), EINVAL), (dict(xs=299), EINVAL), (dict(a=None), EINVAL), (dict(a=X + 2), EALIGN),
+    (dict(ws=None), EINVAL), (dict(wb=10), EINVAL), (dict(ws=W + 8), EALIGN), (dict(ws=X), EOVERLAP),
+    (dict(ws=O), EOVERLAP)])
+def test_matmul_values_refusals(L, kw, code):
+    assert _matmul_values(L, **kw) == code
+
+
+def _grouped(L, values, off=0x900000000, groups=3, **kw):
+    a = MATMUL | kw
+    tail = (a["b"], a["bs"], a["n"], a["k"], off, groups, a["out"], a["os"], 1, a["ws"], a["wb"], None)
+    if values:
+        return L.ou_mx4_grouped_matmul_values(0, a["a"], a["m"], 300, a["dt"], *tail)
+    return L.ou_mx4_grouped_matmul(a["dt"], a["a"], a["as_"], a["m"], *tail)
+
+
+@pytest.mark.parametrize("values", [False, True])
+@pytest.mark.parametrize("kw,code", BAD_PRODUCTS + [
+    (dict(off=None), EINVAL), (dict(off=0x900000001), EALIGN), (dict(groups=-1), EINVAL),
+    (dict(groups=65536), EINVAL), (dict(out=0x900000000), EOVERLAP)])
+def test_grouped_matmul_refusals(L, values, kw, code):
+    assert _grouped(L, values, **kw) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dt=3), EINVAL), (dict(m=-1), EINVAL), (dict(n=-1), EINVAL), (dict(rows=-1), EINVAL), (dict(off=None), EINVAL),
+    (dict(groups=-2), EINVAL), (dict(a=None), EINVAL), (dict(bs=None), EINVAL), (dict(out=None), EINVAL),
+    (dict(out=O + 1), EALIGN), (dict(a=C + 8), EALIGN), (dict(out=C), EOVERLAP), (dict(out=X), EOVERLAP)])
+def test_grouped_outer_refusals(L, kw, code):
+    a = dict(dt=1, a=C, as_=S, m=48, b=CT, bs=ST, n=80, rows=500, off=X, groups=5, out=O) | kw
+    assert L.ou_mx4_grouped_outer(*a.values(), None) == code
+
+
+def test_products_pass_their_checks(L, no_gpu):
+    assert L.ou_mx4_matmul(*MATMUL.values(), None) == EUNSUPPORTED
+    assert _matmul_values(L) == EUNSUPPORTED
+    assert _grouped(L, False) == EUNSUPPORTED and _grouped(L, True) == EUNSUPPORTED
+
+
+def test_binding_refuses_host_tensors_and_bad_forms():
+    x = torch.zeros(4, 64)
+    q = ou.Mx4(torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(4, 4, dtype=torch.uint8), 64)
+    assert list(q.shape) == [4, 64]
+    off = torch.zeros(1, dtype=torch.int32)
+    for call in (lambda: ou.mx4_quantize(x), lambda: ou.mx4_quantize_both(x), lambda: ou.mx4_dequantize(q),
+                 lambda: ou.mx4_matmul(x, q), lambda: ou.mx4_matmul(q, q), lambda: ou.mx4_matmul(x, x),
+                 lambda: ou.mx4_quantize_grouped(x, off), lambda: ou.mx4_linear(x, x), lambda: ou.Mx4Weight(x),
+                 lambda: ou.mx4_grouped_linear(x, x[None], off), lambda: ou.mx4_grouped_matmul(x, q, off)):
+        with pytest.raises(ValueError):
+            call()
+    for codes, scales, k in (((4, 32), (4, 4), 64), ((4, 64), (4, 2), 64), ((4, 64), (3, 4), 64), ((64,), (4,), 64),
+                             ((4, 64), (4, 4), 129), ((4, 64), (4, 4), -1)):
+        with pytest.raises(ValueError):
+            ou.Mx4(torch.zeros(codes, dtype=torch.uint8), torch.zeros(scales, dtype=torch.uint8), k)
+    with pytest.raises(ValueError):
+        ou.Mx4(torch.zeros(4, 64), torch.zeros(4, 4, dtype=torch.uint8), 64)
+    with pytest.raises(ValueError):
+        ou.Mx4(torch.zeros(64, 4, dtype=torch.uint8).t(), torch.zeros(4, 4, dtype=torch.uint8), 64)
+
+
+def test_reference_rounds_to_the_nearest_level():
+    """The reference's codes are the nearest of the 15 values, ties to the
+    even code, by brute force over the distances."""
+    m = np.concatenate([np.arange(0, 8.001, 1 / 64), R.BORDERS])
+    x = np.zeros((m.size, 32))
+    x[:, 0], x[:, 1] = 4.0, m                       # 4 fixes the scale at 1 for what is below 8
+    x = x[m < 8]
+    code, s = R.quantize(x)
+    assert (s[:, 0] == 127).all()
+    for v, c in zip(x[:, 1], code[:, 1]):
+        d = np.abs(np.minimum(v, 6.0) - R.LEVELS)
+        near = np.flatnonzero(d == d.min())
+        assert c == (near[0] if near.size == 1 else near[near % 2 == 0][0]), v
