@@ -53,7 +53,7 @@ struct MatmulArgs {
     const uint8_t* bs;
     void* out;
     int64_t m, n, out_stride;
-    int64_t n_tiles;          // tiles along n
+    int64_t units, n_tiles;   // tiles along m (plain, by contraction) and n
     int64_t steps;            // k-steps of a row of a and b as stored
     const int32_t* offsets;
     int64_t rows;             // grouped: rows that offsets may point to
@@ -67,7 +67,8 @@ enum Grouping { kPlain = 0, kByRows = 1, kByContraction = 2 };
 const void* quant_rows_kernel(int dtype);
 const void* quant_tile_kernel(int dtype);
 const void* dequant_kernel(int dtype);
-const void* matmul_kernel(int out_dtype, int grouping);
+// tile: rows and columns of a block's tile, 64, 128 or 256.
+const void* matmul_kernel(int out_dtype, int grouping, int tile);
 
 constexpr int kQuantThreads = 256;
 constexpr int kQuantUnits = 4;      // units of 128 columns per 16 lanes of k_quant_rows

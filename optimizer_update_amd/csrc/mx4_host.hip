@@ -140,13 +140,30 @@ int launch_quantize(int dtype, QuantArgs& q, int64_t batch, int64_t units, void*
                   "k_quant_tile");
 }
 
-int launch_matmul(int out_dtype, int grouping, MatmulArgs& p, int64_t units, int64_t batch, void* stream)
+// Rows and columns of a block's tile.
+int select_tile(int64_t m, int64_t n, int64_t steps, int64_t batch)
 {
-    p.n_tiles = cut(p.n, kMatmulTile);
+#ifdef MX4_FORCE_TILE
+    return MX4_FORCE_TILE;
+#endif
+    if (steps >= (int64_t(1) << 17)) return 64;   // the larger tiles address a tile's rows by 32 bits
+    if (cut(m, 256) * cut(n, 256) * batch >= 256) return 256;
+    if (cut(m, 128) * cut(n, 128) * batch >= 128) return 128;
+    return 64;
+}
+
+// m: the rows that the tiles along m cover.  groups > 0: grouped by rows.
+int launch_matmul(int out_dtype, int grouping, MatmulArgs& p, int64_t batch, void* stream)
+{
+    const int tile = select_tile(p.m, p.n, p.steps, batch);
+    // by rows: two groups more, the rows in front of the first and behind the last
+    p.units = grouping == kByRows ? grouped_units(p.m, p.groups + 2, tile) : cut(p.m, tile);
+    p.n_tiles = cut(p.n, tile);
     p.wide = wide_rows(p.out, p.out_stride, grouping == kByContraction ? p.m * p.out_stride : 0, elem_bytes(out_dtype),
                        4 * elem_bytes(out_dtype));
     void* args[] = {&p};
-    return launch(matmul_kernel(out_dtype, grouping), units * p.n_tiles, batch, kMatmulThreads, args, stream, "k_matmul");
+    return launch(matmul_kernel(out_dtype, grouping, tile), p.units * p.n_tiles, batch, kMatmulThreads, args, stream,
+                  "k_matmul");
 }
 
 int check_groups(const int32_t* offsets, int32_t groups)
@@ -335,9 +352,7 @@ int product(Product& q, bool values, bool grouped)
     p.rows = q.m;
     p.groups = q.groups;
     p.zero_rest = q.zero_rest != 0;
-    // two units more: the rows in front of the first group and behind the last
-    const int64_t units = grouped ? grouped_units(q.m, q.groups + 2, kMatmulTile) : cut(q.m, kMatmulTile);
-    return launch_matmul(q.out_dtype, grouped ? kByRows : kPlain, p, units, 1, q.stream);
+    return launch_matmul(q.out_dtype, grouped ? kByRows : kPlain, p, 1, q.stream);
 }
 
 }  // namespace
@@ -415,7 +430,7 @@ OU_EXPORT int ou_mx4_grouped_outer(int out_dtype, const uint8_t* a_codes_t, cons
     p.offsets = offsets;
     p.rows = rows;
     p.groups = groups;
-    return launch_matmul(out_dtype, kByContraction, p, cut(m, kMatmulTile), groups, stream);
+    return launch_matmul(out_dtype, kByContraction, p, groups, stream);
 }
 
 }  // extern "C"

@@ -569,6 +569,236 @@ __global__ __launch_bounds__(kMatmulThreads) void k_matmul(MatmulArgs p)
     }
 }
 
+
+// ---- products, tiled through LDS ------------------------------------------
+
+using f32x16 = float __attribute__((ext_vector_type(16)));
+
+// 16 bytes a lane from `rsrc` + voff to LDS at lds + lane * 16; what lies
+// behind the resource's end arrives as 0.
+__device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t rsrc, uint32_t voff, uint32_t lds)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)lds, 16, voff, 0, 0, 0);
+}
+
+// All but the newest LEFT transfers of the wave have arrived.
+template <int LEFT>
+__device__ __forceinline__ void wait_transfers()
+{
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LEFT) : "memory");
+}
+
+// The block's barrier alone; no LDS access moves across it.
+__device__ __forceinline__ void block_barrier()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const uint8_t* p, uint32_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, static_cast<int>(bytes), 0x00020000);
+}
+
+// The tile of a block: XCDs (blocks b mod 8) take contiguous runs of the tile
+// order, which walks bands of 8 units down, then along n, so that the blocks
+// that run together on one XCD share rows of a and of b in its L2.
+__device__ __forceinline__ void tile_of(int64_t b, int64_t units, int64_t n_tiles, int64_t* unit, int64_t* ntile)
+{
+    const int64_t total = units * n_tiles, x = b & 7, per = total >> 3, extra = total & 7;
+    const int64_t t = x * per + (x < extra ? x : extra) + (b >> 3);
+    constexpr int64_t kBand = 8;
+    const int64_t band = t / (kBand * n_tiles), in = t - band * kBand * n_tiles;
+    const int64_t left = units - band * kBand, h = left < kBand ? left : kBand;
+    *ntile = in / h;
+    *unit = band * kBand + (in - *ntile * h);
+}
+
+// Four waves in a square, 32 WM x 32 WN results each, by the 32x32x64
+// instruction.  A k-tile is 256 columns: 128 bytes of codes of every row,
+// moved to LDS in two alternating buffers while the other is multiplied; the
+// scales of two k-tiles (16 bytes a row) move together.  In LDS the eight
+// 16-byte pieces of a row are exchanged by (row / 2) mod 8, so that the
+// lanes of a read, which take one piece of 32 rows, meet all banks.
+template <int DT, int G, int WM, int WN>
+__global__ __launch_bounds__(256, 1) void k_matmul_tile(MatmulArgs p)
+{
+    constexpr int BM = 64 * WM, BN = 64 * WN;
+    constexpr int kCodes = (BM + BN) * 128, kScales = (BM + BN) * 16;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kCodes + 2 * kScales];
+    const int t = static_cast<int>(threadIdx.x), lane = t & 63, r = lane & 31, g = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const uint32_t lds0 = static_cast<uint32_t>(
+        reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
+
+    int64_t unit, ntile, row0, mrows, step0 = 0, steps = p.steps, out0 = 0;
+    const uint8_t *b = p.b, *bs = p.bs;
+    if constexpr (G == kByRows) {
+        const Place end = locate(p.offsets, p.groups, p.rows, BM, INT64_MAX);
+        const int64_t units = end.first + (p.zero_rest ? end.units : 0);
+        if (static_cast<int64_t>(blockIdx.x) >= units * p.n_tiles) return;
+        tile_of(blockIdx.x, units, p.n_tiles, &unit, &ntile);
+        const Place at = locate(p.offsets, p.groups, p.rows, BM, unit);
+        row0 = at.row;
+        mrows = at.rows;
+        if (mrows <= 0) return;
+        if (at.group < 0) {
+            steps = 0;   // rows of no group: the sum over nothing
+        } else {
+            b += at.group * p.n * p.steps * (kPad / 2);
+            bs += at.group * p.n * p.steps * (kPad / kBlock);
+        }
+    } else {
+        tile_of(blockIdx.x, p.units, p.n_tiles, &unit, &ntile);
+        row0 = unit * BM;
+        mrows = p.m - row0;
+        if constexpr (G == kByContraction) {
+            const Place at = units_of(p.offsets, p.rows, kPad, static_cast<int32_t>(blockIdx.y));
+            step0 = at.first;
+            steps = at.units;
+            if (step0 > p.steps) step0 = p.steps;
+            if (steps > p.steps - step0) steps = p.steps - step0;
+            out0 = static_cast<int64_t>(blockIdx.y) * p.m * p.out_stride;
+        }
+    }
+    if (mrows > BM) mrows = BM;
+    const int64_t n0 = ntile * BN;
+    const int64_t ncols = p.n - n0 < BN ? p.n - n0 : BN;
+
+    // sources: the tile's rows from the first step on, up to the last row's end
+    const uint32_t crow = static_cast<uint32_t>(p.steps) * (kPad / 2), srow = static_cast<uint32_t>(p.steps) * 4;
+    const uint32_t c0 = static_cast<uint32_t>(step0) * (kPad / 2), s0 = static_cast<uint32_t>(step0) * 4;
+    const uint8_t* ac = p.a + row0 * crow + c0;
+    const uint8_t* asc = p.as + row0 * srow + s0;
+    const uint8_t* bc = b + n0 * crow + c0;
+    const uint8_t* bsc = bs + n0 * srow + s0;
+    const uint32_t ace = static_cast<uint32_t>(mrows) * crow - c0, ase = static_cast<uint32_t>(mrows) * srow - s0;
+    const uint32_t bce = static_cast<uint32_t>(ncols) * crow - c0, bse = static_cast<uint32_t>(ncols) * srow - s0;
+
+    // transfer i of an operand's codes covers rows 8 i .. 8 i + 7; wave w
+    // makes i = w, w + 4, ..  (row / 2) mod 8 = (4 w + lane / 16) mod 8
+    const uint32_t cvoff = static_cast<uint32_t>(wave * 8 + (lane >> 3)) * crow +
+                           static_cast<uint32_t>(((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7)) * 16);
+    const uint32_t svoff = static_cast<uint32_t>(wave * 64 + lane) * srow;
+    auto move_codes = [&](int64_t kt) {
+        const uint32_t at = static_cast<uint32_t>(kt) * 128;
+        const uint32_t dst = lds0 + (kt & 1) * kCodes + wave * 1024;
+        const auto ra = resource(ac + at, ace - at), rb = resource(bc + at, bce - at);
+#pragma unroll
+        for (int i = 0; i < BM / 32; ++i) to_lds(ra, cvoff + i * 32 * crow, dst + i * 4096);
+#pragma unroll
+        for (int i = 0; i < BN / 32; ++i) to_lds(rb, cvoff + i * 32 * crow, dst + BM * 128 + i * 4096);
+    };
+    auto move_scales = [&](int64_t pair) {
+        const uint32_t at = static_cast<uint32_t>(pair) * 16;
+        const uint32_t dst = lds0 + 2 * kCodes + (pair & 1) * kScales + wave * 1024;
+        if (wave * 64 < BM) to_lds(resource(asc + at, ase - at), svoff, dst);
+        if (wave * 64 < BN) to_lds(resource(bsc + at, bse - at), svoff, dst + BM * 16);
+    };
+
+    // a lane's place in LDS: row r of a 32-row fragment, piece 2 s + g
+    const int wm = wave >> 1, wn = wave & 1;
+    uint32_t piece[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) piece[s] = r * 128 + (((2 * s + g) ^ ((r >> 1) & 7)) * 16);
+    const uint32_t sel = g ? 0x07050301u : 0x06040200u;
+    f32x16 acc[WM][WN] = {};
+    i32x4 fa[2][WM], fb[2][WN];
+    int sa[2][WM], sb[2][WN];
+    auto read_codes = [&](int buf, int s, int to) {
+        const uint8_t* base = lds + buf * kCodes + piece[s];
+#pragma unroll
+        for (int i = 0; i < WM; ++i) fa[to][i] = *reinterpret_cast<const i32x4*>(base + (wm * WM + i) * 4096);
+#pragma unroll
+        for (int j = 0; j < WN; ++j) fb[to][j] = *reinterpret_cast<const i32x4*>(base + BM * 128 + (wn * WN + j) * 4096);
+    };
+    auto read_scales = [&](int64_t kt, int to) {
+        const uint8_t* base = lds + 2 * kCodes + ((kt >> 1) & 1) * kScales + (kt & 1) * 8 + r * 16;
+#pragma unroll
+        for (int i = 0; i < WM; ++i) {
+            const u32x2 v = *reinterpret_cast<const u32x2*>(base + (wm * WM + i) * 512);
+            sa[to][i] = static_cast<int>(__builtin_amdgcn_perm(v[1], v[0], sel));
+        }
+#pragma unroll
+        for (int j = 0; j < WN; ++j) {
+            const u32x2 v = *reinterpret_cast<const u32x2*>(base + BM * 16 + (wn * WN + j) * 512);
+            sb[to][j] = static_cast<int>(__builtin_amdgcn_perm(v[1], v[0], sel));
+        }
+    };
+#define MX4_STEP(S, F, Q)                                                                                            \
+    _Pragma("unroll") for (int i = 0; i < WM; ++i) _Pragma("unroll") for (int j = 0; j < WN; ++j)                    \
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(fb[F][j]), widen(fa[F][i]), acc[i][j], 4, 4, \
+                                                                    S, sb[Q][j], S, sa[Q][i])
+
+    const int64_t kts = (steps + 1) >> 1;
+    if (kts > 0) {
+        move_scales(0);
+        move_codes(0);
+        if (kts > 1) {
+            move_codes(1);
+            wait_transfers<(BM + BN) / 32>();
+        } else {
+            wait_transfers<0>();
+        }
+        block_barrier();
+        read_scales(0, 0);
+        read_codes(0, 0, 0);
+        for (int64_t kt = 0; kt < kts - 1; ++kt) {
+            const int buf = static_cast<int>(kt & 1);
+            read_codes(buf, 1, 1);
+            MX4_STEP(0, 0, 0);
+            read_codes(buf, 2, 0);
+            MX4_STEP(1, 1, 0);
+            read_codes(buf, 3, 1);
+            MX4_STEP(2, 0, 0);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            wait_transfers<0>();
+            block_barrier();
+            if (kt + 2 < kts) {
+                if (!(kt & 1)) move_scales((kt >> 1) + 1);
+                move_codes(kt + 2);
+            }
+            read_codes(buf ^ 1, 0, 0);
+            read_scales(kt + 1, 1);
+            MX4_STEP(3, 1, 0);
+#pragma unroll
+            for (int i = 0; i < WM; ++i) sa[0][i] = sa[1][i];
+#pragma unroll
+            for (int j = 0; j < WN; ++j) sb[0][j] = sb[1][j];
+        }
+        const int buf = static_cast<int>((kts - 1) & 1);
+        read_codes(buf, 1, 1);
+        MX4_STEP(0, 0, 0);
+        MX4_STEP(1, 1, 0);
+        if (!(steps & 1)) {   // the last k-tile is whole
+            read_codes(buf, 2, 0);
+            read_codes(buf, 3, 1);
+            MX4_STEP(2, 0, 0);
+            MX4_STEP(3, 1, 0);
+        }
+    }
+#undef MX4_STEP
+
+    // result (i, j, q, e) of a lane: row 32 i + r, column 32 j + 8 q + 4 g + e
+#pragma unroll
+    for (int i = 0; i < WM; ++i) {
+        const int64_t m = (wm * WM + i) * 32 + r;
+        if (m >= mrows) continue;
+        const int64_t row = out0 + (row0 + m) * p.out_stride + n0;
+#pragma unroll
+        for (int j = 0; j < WN; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int64_t n = (wn * WN + j) * 32 + 8 * q + 4 * g, left = ncols - n;
+                if (left <= 0) continue;
+                store4<DT>(p.out, row + n,
+                           f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]},
+                           left > 4 ? 4 : static_cast<int>(left), p.wide);
+            }
+    }
+}
+
 }  // namespace
 
 const void* quant_rows_kernel(int dtype)
@@ -604,11 +834,26 @@ const void* matmul_of(int dtype)
     return fns[dtype];
 }
 
-const void* matmul_kernel(int out_dtype, int grouping)
+template <int G, int W>
+const void* matmul_tile_of(int dtype)
 {
-    return grouping == kPlain ? matmul_of<kPlain>(out_dtype)
-           : grouping == kByRows ? matmul_of<kByRows>(out_dtype)
-                                 : matmul_of<kByContraction>(out_dtype);
+    const void* fns[3] = {reinterpret_cast<const void*>(&k_matmul_tile<kF32, G, W, W>),
+                          reinterpret_cast<const void*>(&k_matmul_tile<kF16, G, W, W>),
+                          reinterpret_cast<const void*>(&k_matmul_tile<kBF16, G, W, W>)};
+    return fns[dtype];
+}
+
+template <int G>
+const void* matmul_any(int dtype, int tile)
+{
+    return tile == 256 ? matmul_tile_of<G, 4>(dtype) : tile == 128 ? matmul_tile_of<G, 2>(dtype) : matmul_of<G>(dtype);
+}
+
+const void* matmul_kernel(int out_dtype, int grouping, int tile)
+{
+    return grouping == kPlain ? matmul_any<kPlain>(out_dtype, tile)
+           : grouping == kByRows ? matmul_any<kByRows>(out_dtype, tile)
+                                 : matmul_any<kByContraction>(out_dtype, tile);
 }
 
 }  // namespace mx4
