@@ -160,7 +160,7 @@ int launch_matmul(int out_dtype, int grouping, MatmulArgs& p, int64_t batch, voi
     p.units = grouping == kByRows ? grouped_units(p.m, p.groups + 2, tile) : cut(p.m, tile);
     p.n_tiles = cut(p.n, tile);
     p.wide = wide_rows(p.out, p.out_stride, grouping == kByContraction ? p.m * p.out_stride : 0, elem_bytes(out_dtype),
-                       4 * elem_bytes(out_dtype));
+                       tile == 64 ? 4 * elem_bytes(out_dtype) : 16);
     void* args[] = {&p};
     return launch(matmul_kernel(out_dtype, grouping, tile), p.units * p.n_tiles, batch, kMatmulThreads, args, stream,
                   "k_matmul");

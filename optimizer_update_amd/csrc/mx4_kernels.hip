@@ -13,6 +13,8 @@
 // and scales [rows][P / 32], P the columns padded to 128 with zeros.  A row
 // is a whole number of 64-byte pieces, one k-step of the 16x16x128 matrix
 // instruction.
+#include <type_traits>
+
 #include "mx4.h"
 
 #pragma clang fp contract(off)
@@ -572,8 +574,6 @@ __global__ __launch_bounds__(kMatmulThreads) void k_matmul(MatmulArgs p)
 
 // ---- products, tiled through LDS ------------------------------------------
 
-using f32x16 = float __attribute__((ext_vector_type(16)));
-
 // 16 bytes a lane from `rsrc` + voff to LDS at lds + lane * 16; what lies
 // behind the resource's end arrives as 0.
 __device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t rsrc, uint32_t voff, uint32_t lds)
@@ -587,6 +587,19 @@ __device__ __forceinline__ void wait_transfers()
 {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LEFT) : "memory");
 }
+
+// acc += the product of two fragments, in place.  Written as assembly because
+// the builtin's result may be another register than its addend, and with the
+// whole accumulator file in use the compiler then moves and spills
+// accumulators.  settle_products() stands before the first other use of acc:
+// the compiler does not know that this is a matrix instruction.
+__device__ __forceinline__ void multiply_add(f32x4& acc, i32x4 b, i32x4 a, int sb, int sa)
+{
+    asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[0,0,0] op_sel_hi:[0,0,0] cbsz:4 blgp:4"
+                 : "+a"(acc)
+                 : "v"(b), "v"(a), "v"(sb), "v"(sa));
+}
+__device__ __forceinline__ void settle_products() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
 // The block's barrier alone; no LDS access moves across it.
 __device__ __forceinline__ void block_barrier()
@@ -615,19 +628,21 @@ __device__ __forceinline__ void tile_of(int64_t b, int64_t units, int64_t n_tile
     *unit = band * kBand + (in - *ntile * h);
 }
 
-// Four waves in a square, 32 WM x 32 WN results each, by the 32x32x64
-// instruction.  A k-tile is 256 columns: 128 bytes of codes of every row,
-// moved to LDS in two alternating buffers while the other is multiplied; the
-// scales of two k-tiles (16 bytes a row) move together.  In LDS the eight
-// 16-byte pieces of a row are exchanged by (row / 2) mod 8, so that the
-// lanes of a read, which take one piece of 32 rows, meet all banks.
+// Four waves in a square, 16 WM x 16 WN results each.  A stage is one k-step
+// of 128 columns: 64 bytes of codes of every row, moved to LDS by a ring of
+// four buffers; the scales of four stages (16 bytes a row) move together, in
+// two buffers.  At stage s a wave multiplies the fragments of s from
+// registers, reads those of s + 1 from LDS and starts the transfers of s + 4
+// into the buffer of s, all laid between the matrix instructions.  In LDS the
+// four 16-byte pieces of a row are exchanged by (row / 4) mod 4, so that the
+// lanes of a read, which take one piece of 16 rows, meet all banks.
 template <int DT, int G, int WM, int WN>
 __global__ __launch_bounds__(256, 1) void k_matmul_tile(MatmulArgs p)
 {
-    constexpr int BM = 64 * WM, BN = 64 * WN;
-    constexpr int kCodes = (BM + BN) * 128, kScales = (BM + BN) * 16;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kCodes + 2 * kScales];
-    const int t = static_cast<int>(threadIdx.x), lane = t & 63, r = lane & 31, g = lane >> 5;
+    constexpr int BM = 32 * WM, BN = 32 * WN;
+    constexpr int kCodes = (BM + BN) * 64, kScales = (BM + BN) * 16;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[4 * kCodes + 2 * kScales];
+    const int t = static_cast<int>(threadIdx.x), lane = t & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const uint32_t lds0 = static_cast<uint32_t>(
         reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
@@ -676,126 +691,151 @@ __global__ __launch_bounds__(256, 1) void k_matmul_tile(MatmulArgs p)
     const uint32_t ace = static_cast<uint32_t>(mrows) * crow - c0, ase = static_cast<uint32_t>(mrows) * srow - s0;
     const uint32_t bce = static_cast<uint32_t>(ncols) * crow - c0, bse = static_cast<uint32_t>(ncols) * srow - s0;
 
-    // transfer i of an operand's codes covers rows 8 i .. 8 i + 7; wave w
-    // makes i = w, w + 4, ..  (row / 2) mod 8 = (4 w + lane / 16) mod 8
-    const uint32_t cvoff = static_cast<uint32_t>(wave * 8 + (lane >> 3)) * crow +
-                           static_cast<uint32_t>(((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7)) * 16);
+    // a transfer covers 16 rows of codes, or 64 rows of scales
+    constexpr int kMoves = (BM + BN) / 64;       // code transfers of a wave and stage
+    const uint32_t cvoff = static_cast<uint32_t>(wave * 16 + (lane >> 2)) * crow +
+                           static_cast<uint32_t>(((lane & 3) ^ ((lane >> 4) & 3)) * 16);
     const uint32_t svoff = static_cast<uint32_t>(wave * 64 + lane) * srow;
-    auto move_codes = [&](int64_t kt) {
-        const uint32_t at = static_cast<uint32_t>(kt) * 128;
-        const uint32_t dst = lds0 + (kt & 1) * kCodes + wave * 1024;
-        const auto ra = resource(ac + at, ace - at), rb = resource(bc + at, bce - at);
-#pragma unroll
-        for (int i = 0; i < BM / 32; ++i) to_lds(ra, cvoff + i * 32 * crow, dst + i * 4096);
-#pragma unroll
-        for (int i = 0; i < BN / 32; ++i) to_lds(rb, cvoff + i * 32 * crow, dst + BM * 128 + i * 4096);
+    // transfer i of stage s, nothing behind the last stage
+    auto move_codes = [&](int64_t s, int i) {
+        const uint32_t at = static_cast<uint32_t>(s) * 64;
+        const uint32_t dst = lds0 + (s & 3) * kCodes + wave * 1024 + i * 4096;
+        if (i < BM / 64)
+            to_lds(resource(ac + at, s < steps ? ace - at : 0), cvoff + i * 64 * crow, dst);
+        else
+            to_lds(resource(bc + at, s < steps ? bce - at : 0), cvoff + (i - BM / 64) * 64 * crow, dst);
     };
-    auto move_scales = [&](int64_t pair) {
-        const uint32_t at = static_cast<uint32_t>(pair) * 16;
-        const uint32_t dst = lds0 + 2 * kCodes + (pair & 1) * kScales + wave * 1024;
-        if (wave * 64 < BM) to_lds(resource(asc + at, ase - at), svoff, dst);
-        if (wave * 64 < BN) to_lds(resource(bsc + at, bse - at), svoff, dst + BM * 16);
+    // the scales of stages 4 q ..: every wave moves 64 rows of each operand
+    constexpr int kScaleMoves = 2;
+    auto move_scales = [&](int64_t q) {
+        const uint32_t at = static_cast<uint32_t>(q) * 16;
+        const uint32_t dst = lds0 + 4 * kCodes + (q & 1) * kScales;
+        // where a wave has no rows of its own left it repeats the first ones
+        const uint32_t wa = wave * 64 < BM ? 0 : BM, wb = wave * 64 < BN ? 0 : BN;
+        to_lds(resource(asc + at, 4 * q < steps ? ase - at : 0), svoff - wa * srow, dst + (wave * 64 - wa) * 16);
+        to_lds(resource(bsc + at, 4 * q < steps ? bse - at : 0), svoff - wb * srow, dst + BM * 16 + (wave * 64 - wb) * 16);
     };
 
-    // a lane's place in LDS: row r of a 32-row fragment, piece 2 s + g
+    // a lane's place in LDS: row r of a 16-row fragment, piece (and scale) g
     const int wm = wave >> 1, wn = wave & 1;
-    uint32_t piece[4];
-#pragma unroll
-    for (int s = 0; s < 4; ++s) piece[s] = r * 128 + (((2 * s + g) ^ ((r >> 1) & 7)) * 16);
-    const uint32_t sel = g ? 0x07050301u : 0x06040200u;
-    f32x16 acc[WM][WN] = {};
+    const uint8_t* const cbase = lds + r * 64 + ((g ^ (r >> 2)) * 16);
+    const uint8_t* const sbase = lds + 4 * kCodes + r * 16 + g;
+    f32x4 acc[WM][WN] = {};
     i32x4 fa[2][WM], fb[2][WN];
     int sa[2][WM], sb[2][WN];
-    auto read_codes = [&](int buf, int s, int to) {
-        const uint8_t* base = lds + buf * kCodes + piece[s];
-#pragma unroll
-        for (int i = 0; i < WM; ++i) fa[to][i] = *reinterpret_cast<const i32x4*>(base + (wm * WM + i) * 4096);
-#pragma unroll
-        for (int j = 0; j < WN; ++j) fb[to][j] = *reinterpret_cast<const i32x4*>(base + BM * 128 + (wn * WN + j) * 4096);
-    };
-    auto read_scales = [&](int64_t kt, int to) {
-        const uint8_t* base = lds + 2 * kCodes + ((kt >> 1) & 1) * kScales + (kt & 1) * 8 + r * 16;
-#pragma unroll
-        for (int i = 0; i < WM; ++i) {
-            const u32x2 v = *reinterpret_cast<const u32x2*>(base + (wm * WM + i) * 512);
-            sa[to][i] = static_cast<int>(__builtin_amdgcn_perm(v[1], v[0], sel));
-        }
-#pragma unroll
-        for (int j = 0; j < WN; ++j) {
-            const u32x2 v = *reinterpret_cast<const u32x2*>(base + BM * 16 + (wn * WN + j) * 512);
-            sb[to][j] = static_cast<int>(__builtin_amdgcn_perm(v[1], v[0], sel));
-        }
-    };
-#define MX4_STEP(S, F, Q)                                                                                            \
-    _Pragma("unroll") for (int i = 0; i < WM; ++i) _Pragma("unroll") for (int j = 0; j < WN; ++j)                    \
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(fb[F][j]), widen(fa[F][i]), acc[i][j], 4, 4, \
-                                                                    S, sb[Q][j], S, sa[Q][i])
-
-    const int64_t kts = (steps + 1) >> 1;
-    if (kts > 0) {
-        move_scales(0);
-        move_codes(0);
-        if (kts > 1) {
-            move_codes(1);
-            wait_transfers<(BM + BN) / 32>();
+    // fragment x of stage s to register set `to`: a's and b's in turn
+    auto read = [&](int64_t s, int x, int to) {
+        const uint8_t* c = cbase + (s & 3) * kCodes;
+        const uint8_t* q = sbase + ((s >> 2) & 1) * kScales + (s & 3) * 4;
+        const int i = x >> 1;
+        if (x & 1) {
+            if (i >= WN) return;
+            fb[to][i] = *reinterpret_cast<const i32x4*>(c + BM * 64 + (wn * WN + i) * 1024);
+            sb[to][i] = q[BM * 16 + (wn * WN + i) * 256];
         } else {
-            wait_transfers<0>();
+            if (i >= WM) return;
+            fa[to][i] = *reinterpret_cast<const i32x4*>(c + (wm * WM + i) * 1024);
+            sa[to][i] = q[(wm * WM + i) * 256];
         }
+    };
+    constexpr int kReads = 2 * (WM > WN ? WM : WN);
+    // One stage, PHASE = s mod 4.  Behind its barrier all waves hold stage s
+    // in registers and the transfers of s + 1 have arrived: those of s + 2
+    // and s + 3, and scales started with them, may be on their way.
+    auto stage = [&](int64_t s, auto phase) {
+        constexpr int PHASE = decltype(phase)::value, set = PHASE & 1;
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        wait_transfers<2 * kMoves + (PHASE == 1 || PHASE == 2 ? kScaleMoves : 0)>();
         block_barrier();
-        read_scales(0, 0);
-        read_codes(0, 0, 0);
-        for (int64_t kt = 0; kt < kts - 1; ++kt) {
-            const int buf = static_cast<int>(kt & 1);
-            read_codes(buf, 1, 1);
-            MX4_STEP(0, 0, 0);
-            read_codes(buf, 2, 0);
-            MX4_STEP(1, 1, 0);
-            read_codes(buf, 3, 1);
-            MX4_STEP(2, 0, 0);
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            wait_transfers<0>();
-            block_barrier();
-            if (kt + 2 < kts) {
-                if (!(kt & 1)) move_scales((kt >> 1) + 1);
-                move_codes(kt + 2);
-            }
-            read_codes(buf ^ 1, 0, 0);
-            read_scales(kt + 1, 1);
-            MX4_STEP(3, 1, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (PHASE == 0) move_scales((s >> 2) + 1);
 #pragma unroll
-            for (int i = 0; i < WM; ++i) sa[0][i] = sa[1][i];
-#pragma unroll
-            for (int j = 0; j < WN; ++j) sb[0][j] = sb[1][j];
+        for (int x = 0; x < WM * WN; ++x) {
+            const int i = x / WN, j = x % WN;
+            multiply_add(acc[i][j], fb[set][j], fa[set][i], sb[set][j], sa[set][i]);
+            constexpr int kReadEvery = WM * WN / kReads / 2 ? WM * WN / kReads / 2 : 1;
+            if (x % kReadEvery == 0 && x / kReadEvery < kReads) read(s + 1, x / kReadEvery, set ^ 1);
+            constexpr int kMoveEvery = WM * WN / kMoves;
+            if (x % kMoveEvery == kMoveEvery - 1) move_codes(s + 4, x / kMoveEvery);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        const int buf = static_cast<int>((kts - 1) & 1);
-        read_codes(buf, 1, 1);
-        MX4_STEP(0, 0, 0);
-        MX4_STEP(1, 1, 0);
-        if (!(steps & 1)) {   // the last k-tile is whole
-            read_codes(buf, 2, 0);
-            read_codes(buf, 3, 1);
-            MX4_STEP(2, 0, 0);
-            MX4_STEP(3, 1, 0);
-        }
-    }
-#undef MX4_STEP
+    };
 
-    // result (i, j, q, e) of a lane: row 32 i + r, column 32 j + 8 q + 4 g + e
+    if (steps > 0) {
+        move_scales(0);
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 0; i < kMoves; ++i) move_codes(s, i);
+        wait_transfers<3 * kMoves>();
+        block_barrier();
+#pragma unroll
+        for (int x = 0; x < kReads; ++x) read(0, x, 0);
+        settle_products();   // and behind acc's first values
+        int64_t s = 0;
+        for (; s + 4 <= steps; s += 4) {
+            stage(s, std::integral_constant<int, 0>{});
+            stage(s + 1, std::integral_constant<int, 1>{});
+            stage(s + 2, std::integral_constant<int, 2>{});
+            stage(s + 3, std::integral_constant<int, 3>{});
+        }
+        if (s < steps) {
+            stage(s, std::integral_constant<int, 0>{});
+            if (s + 1 < steps) {
+                stage(s + 1, std::integral_constant<int, 1>{});
+                if (s + 2 < steps) stage(s + 2, std::integral_constant<int, 2>{});
+            }
+        }
+        wait_transfers<0>();   // none may arrive in another block's LDS
+        settle_products();
+#pragma unroll
+        for (int i = 0; i < WM; ++i)
+#pragma unroll
+            for (int j = 0; j < WN; ++j) asm volatile("" : "+a"(acc[i][j]));   // read behind that
+    }
+
+    // Result (i, j, e) of a lane is row 16 i + r, column 16 j + 4 g + e.  16
+    // rows at a time pass through the wave's part of LDS (the codes are done
+    // with), so that whole pieces of rows go out together.
+    block_barrier();
+    constexpr int kSize = DT == kF32 ? 4 : 2, kRow = 16 * WN * kSize, kPitch = kRow + 16, kPieces = kRow / 16;
+    uint8_t* const mine = lds + wave * 16 * kPitch;
+    const int64_t col0 = n0 + wn * (16 * WN), left = ncols - wn * (16 * WN);
 #pragma unroll
     for (int i = 0; i < WM; ++i) {
-        const int64_t m = (wm * WM + i) * 32 + r;
-        if (m >= mrows) continue;
-        const int64_t row = out0 + (row0 + m) * p.out_stride + n0;
 #pragma unroll
-        for (int j = 0; j < WN; ++j)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int64_t n = (wn * WN + j) * 32 + 8 * q + 4 * g, left = ncols - n;
-                if (left <= 0) continue;
-                store4<DT>(p.out, row + n,
-                           f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]},
-                           left > 4 ? 4 : static_cast<int>(left), p.wide);
+        for (int j = 0; j < WN; ++j) {
+            const f32x4 v = acc[i][j];
+            uint8_t* to = mine + r * kPitch + (16 * j + 4 * g) * kSize;
+            if constexpr (DT == kF32)
+                *reinterpret_cast<f32x4*>(to) = v;
+            else
+                *reinterpret_cast<u32x2*>(to) = DT == kBF16 ? u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])}
+                                                            : u32x2{f16_pair(v[0], v[1]), f16_pair(v[2], v[3])};
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        const int64_t m0 = (wm * WM + i) * 16;
+#pragma unroll 1
+        for (int x = lane; x < 16 * kPieces; x += kWave) {
+            const int row = x / kPieces, piece = x % kPieces;
+            const int64_t m = m0 + row, n = piece * (16 / kSize);
+            if (m >= mrows || n >= left) continue;
+            const uint8_t* from = mine + row * kPitch + piece * 16;
+            uint8_t* out = static_cast<uint8_t*>(p.out) + (out0 + (row0 + m) * p.out_stride + col0 + n) * kSize;
+            if (p.wide && n + 16 / kSize <= left) {
+                *reinterpret_cast<u32x4*>(out) = *reinterpret_cast<const u32x4*>(from);
+            } else {
+                const int have = left - n < 16 / kSize ? static_cast<int>(left - n) : 16 / kSize;
+#pragma unroll 1
+                for (int e = 0; e < have; ++e) {
+                    if constexpr (DT == kF32)
+                        reinterpret_cast<uint32_t*>(out)[e] = reinterpret_cast<const uint32_t*>(from)[e];
+                    else
+                        reinterpret_cast<uint16_t*>(out)[e] = reinterpret_cast<const uint16_t*>(from)[e];
+                }
             }
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
 }
 
@@ -846,7 +886,7 @@ const void* matmul_tile_of(int dtype)
 template <int G>
 const void* matmul_any(int dtype, int tile)
 {
-    return tile == 256 ? matmul_tile_of<G, 4>(dtype) : tile == 128 ? matmul_tile_of<G, 2>(dtype) : matmul_of<G>(dtype);
+    return tile == 256 ? matmul_tile_of<G, 8>(dtype) : tile == 128 ? matmul_tile_of<G, 4>(dtype) : matmul_of<G>(dtype);
 }
 
 const void* matmul_kernel(int out_dtype, int grouping, int tile)
