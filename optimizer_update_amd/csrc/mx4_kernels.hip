@@ -628,20 +628,23 @@ __device__ __forceinline__ void tile_of(int64_t b, int64_t units, int64_t n_tile
     *unit = band * kBand + (in - *ntile * h);
 }
 
-// Four waves in a square, 16 WM x 16 WN results each.  A stage is one k-step
-// of 128 columns: 64 bytes of codes of every row, moved to LDS by a ring of
-// four buffers; the scales of four stages (16 bytes a row) move together, in
-// two buffers.  At stage s a wave multiplies the fragments of s from
-// registers, reads those of s + 1 from LDS and starts the transfers of s + 4
-// into the buffer of s, all laid between the matrix instructions.  In LDS the
-// four 16-byte pieces of a row are exchanged by (row / 4) mod 4, so that the
-// lanes of a read, which take one piece of 16 rows, meet all banks.
+// Four waves in a square, 16 WM x 16 WN results each.  A pair is two k-steps,
+// 256 columns: 128 bytes of codes of every row, moved to LDS in two
+// alternating buffers (pieces of 128 bytes: the memory pipeline takes about
+// 0.42 requests a cycle and CU whether they are of 64 or of 128 bytes); the
+// scales of four pairs (32 bytes a row) move together, a quarter with each
+// pair.  A wave multiplies the fragments of one k-step from registers while
+// it reads those of the next from LDS; transfers start as soon as a buffer is
+// free and are laid between the matrix instructions.  In LDS the eight
+// 16-byte pieces of a row are exchanged by (row / 2) mod 8: a read of one
+// piece of 16 rows by 64 lanes then meets no bank twice (lanes 0-3, 12-15,
+// 20-27 of it go together, and so on).
 template <int DT, int G, int WM, int WN>
 __global__ __launch_bounds__(256, 1) void k_matmul_tile(MatmulArgs p)
 {
     constexpr int BM = 32 * WM, BN = 32 * WN;
-    constexpr int kCodes = (BM + BN) * 64, kScales = (BM + BN) * 16;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[4 * kCodes + 2 * kScales];
+    constexpr int kCodes = (BM + BN) * 128, kScales = (BM + BN) * 32;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kCodes + 2 * kScales];
     const int t = static_cast<int>(threadIdx.x), lane = t & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const uint32_t lds0 = static_cast<uint32_t>(
@@ -691,102 +694,129 @@ __global__ __launch_bounds__(256, 1) void k_matmul_tile(MatmulArgs p)
     const uint32_t ace = static_cast<uint32_t>(mrows) * crow - c0, ase = static_cast<uint32_t>(mrows) * srow - s0;
     const uint32_t bce = static_cast<uint32_t>(ncols) * crow - c0, bse = static_cast<uint32_t>(ncols) * srow - s0;
 
-    // a transfer covers 16 rows of codes, or 64 rows of scales
-    constexpr int kMoves = (BM + BN) / 64;       // code transfers of a wave and stage
-    const uint32_t cvoff = static_cast<uint32_t>(wave * 16 + (lane >> 2)) * crow +
-                           static_cast<uint32_t>(((lane & 3) ^ ((lane >> 4) & 3)) * 16);
-    const uint32_t svoff = static_cast<uint32_t>(wave * 64 + lane) * srow;
-    // transfer i of stage s, nothing behind the last stage
-    auto move_codes = [&](int64_t s, int i) {
-        const uint32_t at = static_cast<uint32_t>(s) * 64;
-        const uint32_t dst = lds0 + (s & 3) * kCodes + wave * 1024 + i * 4096;
-        if (i < BM / 64)
-            to_lds(resource(ac + at, s < steps ? ace - at : 0), cvoff + i * 64 * crow, dst);
-        else
-            to_lds(resource(bc + at, s < steps ? bce - at : 0), cvoff + (i - BM / 64) * 64 * crow, dst);
+    // a transfer covers 8 rows of codes, or 32 rows of scales
+    constexpr int kMoves = (BM + BN) / 32 + 1;   // transfers of a wave for a pair
+    const uint32_t cvoff = static_cast<uint32_t>(wave * 8 + (lane >> 3)) * crow +
+                           static_cast<uint32_t>(((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7)) * 16);
+    const uint32_t svoff = static_cast<uint32_t>(lane >> 1) * srow +
+                           static_cast<uint32_t>(((lane & 1) ^ ((lane >> 4) & 1)) * 16);
+    const uint32_t pairs = static_cast<uint32_t>((steps + 1) >> 1);
+    // an odd last step has a pair of its own, whose second half is nobody's:
+    // its lanes read behind the resource's end (a tile's rows end below 2^31)
+    // and bring zeros
+    const uint32_t odd = steps & 1 ? pairs - 1 : ~0u;
+    const uint32_t cvoff_odd = cvoff | (((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7)) & 4 ? 0x80000000u : 0);
+    auto move_scales = [&](uint32_t quad, int part) {
+        const int i = (part * 4 + wave) & ((BM + BN) / 32 - 1);
+        const uint32_t at = quad * 32, dst = lds0 + 2 * kCodes + (quad & 1) * kScales + i * 1024;
+        const bool left = i < BM / 32;
+        const uint8_t* src = left ? asc : bsc;
+        const uint32_t end = left ? ase : bse, row = static_cast<uint32_t>(left ? i : i - BM / 32) * 32;
+        to_lds(resource(src + at, quad * 4 < pairs ? end - at : 0), svoff + row * srow, dst);
     };
-    // the scales of stages 4 q ..: every wave moves 64 rows of each operand
-    constexpr int kScaleMoves = 2;
-    auto move_scales = [&](int64_t q) {
-        const uint32_t at = static_cast<uint32_t>(q) * 16;
-        const uint32_t dst = lds0 + 4 * kCodes + (q & 1) * kScales;
-        // where a wave has no rows of its own left it repeats the first ones
-        const uint32_t wa = wave * 64 < BM ? 0 : BM, wb = wave * 64 < BN ? 0 : BN;
-        to_lds(resource(asc + at, 4 * q < steps ? ase - at : 0), svoff - wa * srow, dst + (wave * 64 - wa) * 16);
-        to_lds(resource(bsc + at, 4 * q < steps ? bse - at : 0), svoff - wb * srow, dst + BM * 16 + (wave * 64 - wb) * 16);
+    // transfer i of pair q, nothing behind the last pair: the codes, and the
+    // quarter of the scales that is due (those of pairs 4 u .. come with the
+    // pairs 4 u - 3 .. 4 u)
+    auto move = [&](uint32_t q, int i) {
+        if (i == kMoves - 1) {
+            move_scales((q + 3) >> 2, (q + 3) & 3);
+            return;
+        }
+        const uint32_t at = q * 128, dst = lds0 + (q & 1) * kCodes + wave * 1024 + i * 4096;
+        const uint32_t from = q == odd ? cvoff_odd : cvoff;
+        if (i < BM / 32)
+            to_lds(resource(ac + at, q < pairs ? ace - at : 0), from + i * 32 * crow, dst);
+        else
+            to_lds(resource(bc + at, q < pairs ? bce - at : 0), from + (i - BM / 32) * 32 * crow, dst);
     };
 
-    // a lane's place in LDS: row r of a 16-row fragment, piece (and scale) g
-    const int wm = wave >> 1, wn = wave & 1;
-    const uint8_t* const cbase = lds + r * 64 + ((g ^ (r >> 2)) * 16);
-    const uint8_t* const sbase = lds + 4 * kCodes + r * 16 + g;
+    // a lane's place in LDS: row r of a 16-row fragment, piece 4 (k-step) + g
+    const int wm = wave >> 1, wn = wave & 1, shift = 8 * g;
+    const uint8_t* cbase[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) cbase[k] = lds + r * 128 + (((4 * k + g) ^ (r >> 1)) * 16);
+    const uint8_t* const sbase = lds + 2 * kCodes + r * 32;
     f32x4 acc[WM][WN] = {};
-    i32x4 fa[2][WM], fb[2][WN];
-    int sa[2][WM], sb[2][WN];
-    // fragment x of stage s to register set `to`: a's and b's in turn
-    auto read = [&](int64_t s, int x, int to) {
-        const uint8_t* c = cbase + (s & 3) * kCodes;
-        const uint8_t* q = sbase + ((s >> 2) & 1) * kScales + (s & 3) * 4;
+    i32x4 fa[2][WM], fb[2][WN];   // fragments by k-step of the pair
+    u32x2 qa[WM], qb[WN];         // scale codes of a pair, four blocks a word
+    int sa[2][WM], sb[2][WN];     // scale codes by k-step, the lane's own
+    constexpr int kReads = WM + WN;
+    // fragment x of k-step k of pair q (a's and b's in turn), and with the
+    // first k-step its scales
+    auto read = [&](uint32_t q, int k, int x) {
+        const uint8_t* c = cbase[k] + (q & 1) * kCodes;
+        const uint8_t* w = sbase + ((q >> 2) & 1) * kScales + ((((q >> 1) & 1) ^ ((r >> 3) & 1)) * 16) + (q & 1) * 8;
         const int i = x >> 1;
         if (x & 1) {
-            if (i >= WN) return;
-            fb[to][i] = *reinterpret_cast<const i32x4*>(c + BM * 64 + (wn * WN + i) * 1024);
-            sb[to][i] = q[BM * 16 + (wn * WN + i) * 256];
+            fb[k][i] = *reinterpret_cast<const i32x4*>(c + BM * 128 + (wn * WN + i) * 2048);
+            if (k == 0) qb[i] = *reinterpret_cast<const u32x2*>(w + BM * 32 + (wn * WN + i) * 512);
         } else {
-            if (i >= WM) return;
-            fa[to][i] = *reinterpret_cast<const i32x4*>(c + (wm * WM + i) * 1024);
-            sa[to][i] = q[(wm * WM + i) * 256];
+            fa[k][i] = *reinterpret_cast<const i32x4*>(c + (wm * WM + i) * 2048);
+            if (k == 0) qa[i] = *reinterpret_cast<const u32x2*>(w + (wm * WM + i) * 512);
         }
     };
-    constexpr int kReads = 2 * (WM > WN ? WM : WN);
-    // One stage, PHASE = s mod 4.  Behind its barrier all waves hold stage s
-    // in registers and the transfers of s + 1 have arrived: those of s + 2
-    // and s + 3, and scales started with them, may be on their way.
-    auto stage = [&](int64_t s, auto phase) {
-        constexpr int PHASE = decltype(phase)::value, set = PHASE & 1;
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        wait_transfers<2 * kMoves + (PHASE == 1 || PHASE == 2 ? kScaleMoves : 0)>();
-        block_barrier();
-        __builtin_amdgcn_sched_barrier(0);
-        if constexpr (PHASE == 0) move_scales((s >> 2) + 1);
+    // The lane's scale code x (a's, then b's) of k-step k; width: 8, or 0 for
+    // the step behind the last one (scales 2^-127, codes zero).
+    auto take_scale = [&](int k, int x, uint32_t width) {
+        if (x < WM)
+            sa[k][x] = static_cast<int>(__builtin_amdgcn_ubfe(qa[x][k], shift, width));
+        else
+            sb[k][x - WM] = static_cast<int>(__builtin_amdgcn_ubfe(qb[x - WM][k], shift, width));
+    };
+    // The products of k-step K; between them what next(x) starts.
+    auto multiply = [&](auto kstep, auto next) {
+        constexpr int K = decltype(kstep)::value;
 #pragma unroll
         for (int x = 0; x < WM * WN; ++x) {
             const int i = x / WN, j = x % WN;
-            multiply_add(acc[i][j], fb[set][j], fa[set][i], sb[set][j], sa[set][i]);
-            constexpr int kReadEvery = WM * WN / kReads / 2 ? WM * WN / kReads / 2 : 1;
-            if (x % kReadEvery == 0 && x / kReadEvery < kReads) read(s + 1, x / kReadEvery, set ^ 1);
-            constexpr int kMoveEvery = WM * WN / kMoves;
-            if (x % kMoveEvery == kMoveEvery - 1) move_codes(s + 4, x / kMoveEvery);
+            if (K == 0 && j == 0) take_scale(0, i, 8);
+            if (K == 0 && i == 0) take_scale(0, WM + j, 8);
+            multiply_add(acc[i][j], fb[K][j], fa[K][i], sb[K][j], sa[K][i]);
+            next(x);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
+    using First = std::integral_constant<int, 0>;
+    using Second = std::integral_constant<int, 1>;
+    constexpr int kProducts = WM * WN;
+    static_assert(WM == WN, "reads take a's and b's fragments in turn");
+    constexpr int kReadEvery = kProducts / kReads / 2 ? kProducts / kReads / 2 : 1;
+    constexpr int kMoveEvery = 3 * kProducts / 2 / kMoves;   // over three quarters of a pair
+    constexpr int kEarly = kProducts / kMoveEvery < kMoves ? kProducts / kMoveEvery : kMoves;   // with the second k-step
+    static_assert(kReadEvery * kReads <= kProducts && kMoveEvery >= 1, "spacing");
 
-    if (steps > 0) {
-        move_scales(0);
+    if (pairs > 0) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
+        for (int part = 0; part < 3; ++part) move_scales(0, part);
 #pragma unroll
-            for (int i = 0; i < kMoves; ++i) move_codes(s, i);
-        wait_transfers<3 * kMoves>();
+        for (int i = 0; i < kMoves; ++i) move(0, i);
+#pragma unroll
+        for (int i = 0; i < kEarly; ++i) move(1, i);
+        wait_transfers<kEarly>();
         block_barrier();
 #pragma unroll
-        for (int x = 0; x < kReads; ++x) read(0, x, 0);
+        for (int x = 0; x < kReads; ++x) read(0, 0, x);
         settle_products();   // and behind acc's first values
-        int64_t s = 0;
-        for (; s + 4 <= steps; s += 4) {
-            stage(s, std::integral_constant<int, 0>{});
-            stage(s + 1, std::integral_constant<int, 1>{});
-            stage(s + 2, std::integral_constant<int, 2>{});
-            stage(s + 3, std::integral_constant<int, 3>{});
+        for (uint32_t q = 0; q < pairs; ++q) {
+            // the first k-step; the last transfers of pair q + 1 start here
+            multiply(First{}, [&](int x) {
+                if (x % kReadEvery == 0 && x / kReadEvery < kReads) read(q, 1, x / kReadEvery);
+                // the second k-step's scales, before the next pair's replace them
+                if (x >= kProducts - kReads) take_scale(1, x - (kProducts - kReads), q == odd ? 0 : 8);
+                const int y = kProducts + x;
+                if (y % kMoveEvery == kMoveEvery - 1 && y / kMoveEvery < kMoves) move(q + 1, y / kMoveEvery);
+            });
+            // all waves hold the second k-step in registers, pair q + 1 is here
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            wait_transfers<0>();
+            block_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(Second{}, [&](int x) {
+                if (x % kReadEvery == 0 && x / kReadEvery < kReads) read(q + 1, 0, x / kReadEvery);
+                if (x % kMoveEvery == kMoveEvery - 1 && x / kMoveEvery < kMoves) move(q + 2, x / kMoveEvery);
+            });
         }
-        if (s < steps) {
-            stage(s, std::integral_constant<int, 0>{});
-            if (s + 1 < steps) {
-                stage(s + 1, std::integral_constant<int, 1>{});
-                if (s + 2 < steps) stage(s + 2, std::integral_constant<int, 2>{});
-            }
-        }
-        wait_transfers<0>();   // none may arrive in another block's LDS
+        wait_transfers<0>();   // none may arrive in what LDS holds next
         settle_products();
 #pragma unroll
         for (int i = 0; i < WM; ++i)
