@@ -617,13 +617,13 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const uint8_t* p, uin
 // The tile of a block: XCDs (blocks b mod 8) take contiguous runs of the tile
 // order, which walks bands of 8 units down, then along n, so that the blocks
 // that run together on one XCD share rows of a and of b in its L2.
-__device__ __forceinline__ void tile_of(int64_t b, int64_t units, int64_t n_tiles, int64_t* unit, int64_t* ntile)
+__device__ __forceinline__ void tile_of(uint32_t b, uint32_t units, uint32_t n_tiles, uint32_t* unit, uint32_t* ntile)
 {
-    const int64_t total = units * n_tiles, x = b & 7, per = total >> 3, extra = total & 7;
-    const int64_t t = x * per + (x < extra ? x : extra) + (b >> 3);
-    constexpr int64_t kBand = 8;
-    const int64_t band = t / (kBand * n_tiles), in = t - band * kBand * n_tiles;
-    const int64_t left = units - band * kBand, h = left < kBand ? left : kBand;
+    const uint32_t total = units * n_tiles, x = b & 7, per = total >> 3, extra = total & 7;
+    const uint32_t t = x * per + (x < extra ? x : extra) + (b >> 3);
+    constexpr uint32_t kBand = 8;
+    const uint32_t band = t / (kBand * n_tiles), in = t - band * kBand * n_tiles;
+    const uint32_t left = units - band * kBand, h = left < kBand ? left : kBand;
     *ntile = in / h;
     *unit = band * kBand + (in - *ntile * h);
 }
@@ -650,13 +650,15 @@ __global__ __launch_bounds__(256, 1) void k_matmul_tile(MatmulArgs p)
     const uint32_t lds0 = static_cast<uint32_t>(
         reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
 
-    int64_t unit, ntile, row0, mrows, step0 = 0, steps = p.steps, out0 = 0;
+    uint32_t unit, ntile;   // a grid holds fewer than 2^31 tiles
+    int64_t row0, mrows, step0 = 0, steps = p.steps, out0 = 0;
     const uint8_t *b = p.b, *bs = p.bs;
     if constexpr (G == kByRows) {
         const Place end = locate(p.offsets, p.groups, p.rows, BM, INT64_MAX);
-        const int64_t units = end.first + (p.zero_rest ? end.units : 0);
+        int64_t units = end.first + (p.zero_rest ? end.units : 0);
+        if (units > p.units) units = p.units;   // offsets that overlap
         if (static_cast<int64_t>(blockIdx.x) >= units * p.n_tiles) return;
-        tile_of(blockIdx.x, units, p.n_tiles, &unit, &ntile);
+        tile_of(blockIdx.x, static_cast<uint32_t>(units), static_cast<uint32_t>(p.n_tiles), &unit, &ntile);
         const Place at = locate(p.offsets, p.groups, p.rows, BM, unit);
         row0 = at.row;
         mrows = at.rows;
@@ -668,8 +670,8 @@ __global__ __launch_bounds__(256, 1) void k_matmul_tile(MatmulArgs p)
             bs += at.group * p.n * p.steps * (kPad / kBlock);
         }
     } else {
-        tile_of(blockIdx.x, p.units, p.n_tiles, &unit, &ntile);
-        row0 = unit * BM;
+        tile_of(blockIdx.x, static_cast<uint32_t>(p.units), static_cast<uint32_t>(p.n_tiles), &unit, &ntile);
+        row0 = static_cast<int64_t>(unit) * BM;
         mrows = p.m - row0;
         if constexpr (G == kByContraction) {
             const Place at = units_of(p.offsets, p.rows, kPad, static_cast<int32_t>(blockIdx.y));
@@ -681,7 +683,7 @@ __global__ __launch_bounds__(256, 1) void k_matmul_tile(MatmulArgs p)
         }
     }
     if (mrows > BM) mrows = BM;
-    const int64_t n0 = ntile * BN;
+    const int64_t n0 = static_cast<int64_t>(ntile) * BN;
     const int64_t ncols = p.n - n0 < BN ? p.n - n0 : BN;
 
     // sources: the tile's rows from the first step on, up to the last row's end
@@ -736,7 +738,7 @@ __global__ __launch_bounds__(256, 1) void k_matmul_tile(MatmulArgs p)
 #pragma unroll
     for (int k = 0; k < 2; ++k) cbase[k] = lds + r * 128 + (((4 * k + g) ^ (r >> 1)) * 16);
     const uint8_t* const sbase = lds + 2 * kCodes + r * 32;
-    f32x4 acc[WM][WN] = {};
+    f32x4 acc[WM][WN];
     i32x4 fa[2][WM], fb[2][WN];   // fragments by k-step of the pair
     u32x2 qa[WM], qb[WN];         // scale codes of a pair, four blocks a word
     int sa[2][WM], sb[2][WN];     // scale codes by k-step, the lane's own
@@ -785,6 +787,16 @@ __global__ __launch_bounds__(256, 1) void k_matmul_tile(MatmulArgs p)
     constexpr int kEarly = kProducts / kMoveEvery < kMoves ? kProducts / kMoveEvery : kMoves;   // with the second k-step
     static_assert(kReadEvery * kReads <= kProducts && kMoveEvery >= 1, "spacing");
 
+    auto zero = [&]() {
+#pragma unroll
+        for (int i = 0; i < WM; ++i)
+#pragma unroll
+            for (int j = 0; j < WN; ++j) {
+                acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                asm volatile("" : "+a"(acc[i][j]));
+            }
+    };
+    if (pairs == 0) zero();
     if (pairs > 0) {
 #pragma unroll
         for (int part = 0; part < 3; ++part) move_scales(0, part);
@@ -792,6 +804,7 @@ __global__ __launch_bounds__(256, 1) void k_matmul_tile(MatmulArgs p)
         for (int i = 0; i < kMoves; ++i) move(0, i);
 #pragma unroll
         for (int i = 0; i < kEarly; ++i) move(1, i);
+        zero();   // while they are on their way
         wait_transfers<kEarly>();
         block_barrier();
 #pragma unroll
@@ -824,48 +837,57 @@ __global__ __launch_bounds__(256, 1) void k_matmul_tile(MatmulArgs p)
             for (int j = 0; j < WN; ++j) asm volatile("" : "+a"(acc[i][j]));   // read behind that
     }
 
-    // Result (i, j, e) of a lane is row 16 i + r, column 16 j + 4 g + e.  16
-    // rows at a time pass through the wave's part of LDS (the codes are done
-    // with), so that whole pieces of rows go out together.
+    // Result (i, j, e) of a lane is row 16 i + r, column 16 j + 4 g + e.  They
+    // pass through the wave's part of LDS (the codes are done with), so that
+    // whole pieces of rows go out together.
     block_barrier();
     constexpr int kSize = DT == kF32 ? 4 : 2, kRow = 16 * WN * kSize, kPitch = kRow + 16, kPieces = kRow / 16;
-    uint8_t* const mine = lds + wave * 16 * kPitch;
-    const int64_t col0 = n0 + wn * (16 * WN), left = ncols - wn * (16 * WN);
+    constexpr int kPart = static_cast<int>(sizeof(lds)) / 4;
+    constexpr int kFrags = kPart / (16 * kPitch) < WM ? (kPart / (16 * kPitch) < WM / 2 ? WM / 4 : WM / 2) : WM;
+    static_assert(kFrags * 16 * kPitch <= kPart && WM % kFrags == 0, "room in LDS");
+    uint8_t* const mine = lds + wave * kPart;
+    const int64_t left = ncols - wn * (16 * WN);
+    constexpr int kTurn = kWave / kPieces;   // rows that a wave stores at once
+    const int row = lane / kPieces, n = (lane % kPieces) * (16 / kSize);
 #pragma unroll
-    for (int i = 0; i < WM; ++i) {
+    for (int f = 0; f < WM; f += kFrags) {
 #pragma unroll
-        for (int j = 0; j < WN; ++j) {
-            const f32x4 v = acc[i][j];
-            uint8_t* to = mine + r * kPitch + (16 * j + 4 * g) * kSize;
-            if constexpr (DT == kF32)
-                *reinterpret_cast<f32x4*>(to) = v;
-            else
-                *reinterpret_cast<u32x2*>(to) = DT == kBF16 ? u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])}
-                                                            : u32x2{f16_pair(v[0], v[1]), f16_pair(v[2], v[3])};
-        }
+        for (int i = 0; i < kFrags; ++i)
+#pragma unroll
+            for (int j = 0; j < WN; ++j) {
+                const f32x4 v = acc[f + i][j];
+                uint8_t* to = mine + (16 * i + r) * kPitch + (16 * j + 4 * g) * kSize;
+                if constexpr (DT == kF32)
+                    *reinterpret_cast<f32x4*>(to) = v;
+                else
+                    *reinterpret_cast<u32x2*>(to) = DT == kBF16
+                                                        ? u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])}
+                                                        : u32x2{f16_pair(v[0], v[1]), f16_pair(v[2], v[3])};
+            }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        const int64_t m0 = (wm * WM + i) * 16;
-#pragma unroll 1
-        for (int x = lane; x < 16 * kPieces; x += kWave) {
-            const int row = x / kPieces, piece = x % kPieces;
-            const int64_t m = m0 + row, n = piece * (16 / kSize);
-            if (m >= mrows || n >= left) continue;
-            const uint8_t* from = mine + row * kPitch + piece * 16;
-            uint8_t* out = static_cast<uint8_t*>(p.out) + (out0 + (row0 + m) * p.out_stride + col0 + n) * kSize;
-            if (p.wide && n + 16 / kSize <= left) {
+        const int m0 = (wm * WM + f) * 16;
+        const int have = mrows - m0 < 16 * kFrags ? static_cast<int>(mrows - m0) : 16 * kFrags;
+        const uint8_t* from = mine + row * kPitch + n * kSize;
+        uint8_t* out = static_cast<uint8_t*>(p.out) +
+                       (out0 + (row0 + m0 + row) * p.out_stride + n0 + wn * (16 * WN) + n) * kSize;
+        const int64_t step = kTurn * p.out_stride * kSize;
+        if (p.wide && n + 16 / kSize <= left) {
+#pragma unroll 8
+            for (int y = row; y < have; y += kTurn, from += kTurn * kPitch, out += step)
                 *reinterpret_cast<u32x4*>(out) = *reinterpret_cast<const u32x4*>(from);
-            } else {
-                const int have = left - n < 16 / kSize ? static_cast<int>(left - n) : 16 / kSize;
+        } else if (n < left) {
+            const int some = left - n < 16 / kSize ? static_cast<int>(left - n) : 16 / kSize;
 #pragma unroll 1
-                for (int e = 0; e < have; ++e) {
+            for (int y = row; y < have; y += kTurn, from += kTurn * kPitch, out += step)
+#pragma unroll 1
+                for (int e = 0; e < some; ++e) {
                     if constexpr (DT == kF32)
                         reinterpret_cast<uint32_t*>(out)[e] = reinterpret_cast<const uint32_t*>(from)[e];
                     else
                         reinterpret_cast<uint16_t*>(out)[e] = reinterpret_cast<const uint16_t*>(from)[e];
                 }
-            }
         }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (f + kFrags < WM) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
 }
 
