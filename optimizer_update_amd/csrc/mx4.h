@@ -12,7 +12,7 @@ constexpr int kBlock = 32;   // values that share one scale
 constexpr int kPad = 128;    // columns of a held matrix are padded to this
 constexpr int kScaleNaN = 255;
 
-enum Dtype { kF32 = 0, kF16 = 1, kBF16 = 2 };
+enum Dtype { kF32 = 0, kF16 = 1, kBF16 = 2, kHeld = 3 };   // kHeld: 4-bit codes and scales
 
 // Quantisation of x [batch][rows][cols] (element strides given) along its
 // columns (codes/scales, nullptr: not wanted) and along its rows
@@ -60,6 +60,12 @@ struct MatmulArgs {
     int32_t groups;
     int32_t zero_rest;        // grouped by rows: rows of no group become 0
     int32_t wide;             // stores of 4 neighbouring results (tiles 128, 256: of 16 bytes) are aligned
+    int32_t out_dtype;        // k_matmul_split
+    // the left matrix as values (k_matmul_split)
+    const void* x;
+    int64_t x_stride, k;
+    int32_t x_dtype;
+    int32_t x_wide;           // 16-byte loads of whole octets of x are allowed
 };
 
 enum Grouping { kPlain = 0, kByRows = 1, kByContraction = 2 };
@@ -67,13 +73,20 @@ enum Grouping { kPlain = 0, kByRows = 1, kByContraction = 2 };
 const void* quant_rows_kernel(int dtype);
 const void* quant_tile_kernel(int dtype);
 const void* dequant_kernel(int dtype);
-// tile: rows and columns of a block's tile, 64, 128 or 256.
-const void* matmul_kernel(int out_dtype, int grouping, int tile);
+// tile: rows and columns of a block's tile, 128 or 256.
+const void* matmul_tile_kernel(int out_dtype, int grouping, int tile);
+
+// Products of few rows or few tiles: rows x cols results a block of `waves`
+// waves; 16 x 16, 16 x 64, 32 x 32 or 64 x 64.
+struct SplitKernel {
+    const void* fn;
+    int rows, cols, waves;
+};
+SplitKernel matmul_split_kernel(int x_dtype, int grouping, int rows, int cols);
 
 constexpr int kQuantThreads = 256;
 constexpr int kQuantUnits = 4;      // units of 128 columns per 16 lanes of k_quant_rows
 constexpr int kQuantTile = 128;     // rows and columns of a tile of k_quant_tile
 constexpr int kMatmulThreads = 256;
-constexpr int kMatmulTile = 64;     // rows and columns of a tile of k_matmul
 
 }  // namespace mx4

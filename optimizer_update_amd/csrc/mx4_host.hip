@@ -140,30 +140,46 @@ int launch_quantize(int dtype, QuantArgs& q, int64_t batch, int64_t units, void*
                   "k_quant_tile");
 }
 
-// Rows and columns of a block's tile.
-int select_tile(int64_t m, int64_t n, int64_t steps, int64_t batch)
+// Which kernel makes a product: tile 128 or 256 (k_matmul_tile), or 0 and the
+// block of k_matmul_split.  `rows`: those of the left matrix, by groups their
+// mean.
+struct Choice {
+    int tile, rows, cols;
+};
+
+Choice choose(int64_t rows, int64_t n, int64_t steps, int64_t batch)
 {
-#ifdef MX4_FORCE_TILE
-    return MX4_FORCE_TILE;
-#endif
-    if (steps >= (int64_t(1) << 17)) return 64;   // the larger tiles address a tile's rows by 32 bits
-    if (cut(m, 256) * cut(n, 256) * batch >= 256) return 256;
-    if (cut(m, 128) * cut(n, 128) * batch >= 128) return 128;
-    return 64;
+    if (rows <= 16) return {0, 16, cut(n, 16) * batch <= 1024 ? 16 : 64};
+    if (rows <= 32) return {0, 32, 32};
+    // the tiles address their rows by 31 bits
+    if (steps < (int64_t(1) << 17)) {
+        if (cut(rows, 256) * cut(n, 256) * batch >= 256) return {256, 0, 0};
+        if (cut(rows, 128) * cut(n, 128) * batch >= 128) return {128, 0, 0};
+    }
+    return {0, 64, 64};
 }
 
-// m: the rows that the tiles along m cover.  groups > 0: grouped by rows.
-int launch_matmul(int out_dtype, int grouping, MatmulArgs& p, int64_t batch, void* stream)
+// By groups: the mean of the groups' rows decides, as the rows themselves are
+// known on the device only.
+Choice choose_grouped(int64_t rows, int64_t n, int64_t steps, int32_t groups)
 {
-    const int tile = select_tile(p.m, p.n, p.steps, batch);
+    const int64_t g = groups > 0 ? groups : 1;
+    return choose(cut(rows, g), n, steps, g < rows ? g : (rows > 0 ? rows : 1));
+}
+
+int launch_matmul(int out_dtype, int grouping, const Choice& c, MatmulArgs& p, int64_t batch, void* stream)
+{
+    const SplitKernel s = c.tile ? SplitKernel{} : matmul_split_kernel(p.x ? p.x_dtype : kHeld, grouping, c.rows, c.cols);
+    const int rows = c.tile ? c.tile : s.rows, cols = c.tile ? c.tile : s.cols;
     // by rows: two groups more, the rows in front of the first and behind the last
-    p.units = grouping == kByRows ? grouped_units(p.m, p.groups + 2, tile) : cut(p.m, tile);
-    p.n_tiles = cut(p.n, tile);
+    p.units = grouping == kByRows ? grouped_units(p.m, p.groups + 2, rows) : cut(p.m, rows);
+    p.n_tiles = cut(p.n, cols);
+    p.out_dtype = out_dtype;
     p.wide = wide_rows(p.out, p.out_stride, grouping == kByContraction ? p.m * p.out_stride : 0, elem_bytes(out_dtype),
-                       tile == 64 ? 4 * elem_bytes(out_dtype) : 16);
+                       c.tile ? 16 : 4 * elem_bytes(out_dtype));
     void* args[] = {&p};
-    return launch(matmul_kernel(out_dtype, grouping, tile), p.units * p.n_tiles, batch, kMatmulThreads, args, stream,
-                  "k_matmul");
+    return launch(c.tile ? matmul_tile_kernel(out_dtype, grouping, c.tile) : s.fn, p.units * p.n_tiles, batch,
+                  c.tile ? kMatmulThreads : kWave * s.waves, args, stream, "the product's kernel");
 }
 
 int check_groups(const int32_t* offsets, int32_t groups)
@@ -268,13 +284,14 @@ OU_EXPORT int ou_mx4_dequantize(int dtype, const uint8_t* codes, const uint8_t* 
 OU_EXPORT int64_t ou_mx4_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k, int from_values)
 {
     if (check_axis(m, "m") || check_axis(n, "n") || check_axis(k, "k")) return -1;
-    return from_values ? values_bytes(m, k) : 0;
+    return from_values && choose(m, n, pad(k) / kPad, 1).rows != 16 ? values_bytes(m, k) : 0;
 }
 
 OU_EXPORT int64_t ou_mx4_grouped_workspace_bytes(int64_t rows, int64_t n, int64_t k, int32_t groups, int from_values)
 {
     if (groups < 0 || groups > kMaxBatch) return -1;
-    return ou_mx4_matmul_workspace_bytes(rows, n, k, from_values);
+    if (check_axis(rows, "rows") || check_axis(n, "n") || check_axis(k, "k")) return -1;
+    return from_values && choose_grouped(rows, n, pad(k) / kPad, groups).rows != 16 ? values_bytes(rows, k) : 0;
 }
 
 }  // extern "C"
@@ -330,7 +347,15 @@ int product(Product& q, bool values, bool grouped)
     if (int st = check_buffers(bufs, 8)) return st;
     if (int st = check_device()) return st;
     const uint8_t *a = q.a, *as = q.as;
-    if (values && pk > 0) {
+    const Choice c = grouped ? choose_grouped(q.m, q.n, pk / kPad, q.groups) : choose(q.m, q.n, pk / kPad, 1);
+    MatmulArgs p{};
+    if (values && c.rows == 16) {   // quantised where it is multiplied
+        p.x = q.x;
+        p.x_dtype = q.x_dtype;
+        p.x_stride = q.x_stride;
+        p.k = q.k;
+        p.x_wide = wide_rows(q.x, q.x_stride, 0, ex, 16);
+    } else if (values && pk > 0) {
         uint8_t* wc = static_cast<uint8_t*>(q.workspace);
         uint8_t* wsc = wc + q.m * (pk / 2);
         QuantArgs qa{q.x, wc, wsc, nullptr, nullptr, q.m, q.k, q.x_stride, 0, pk, 0, nullptr, 0, 0};
@@ -338,7 +363,6 @@ int product(Product& q, bool values, bool grouped)
         a = wc;
         as = wsc;
     }
-    MatmulArgs p{};
     p.a = a;
     p.as = as;
     p.b = q.b;
@@ -352,7 +376,7 @@ int product(Product& q, bool values, bool grouped)
     p.rows = q.m;
     p.groups = q.groups;
     p.zero_rest = q.zero_rest != 0;
-    return launch_matmul(q.out_dtype, grouped ? kByRows : kPlain, p, 1, q.stream);
+    return launch_matmul(q.out_dtype, grouped ? kByRows : kPlain, c, p, 1, q.stream);
 }
 
 }  // namespace
@@ -430,7 +454,10 @@ OU_EXPORT int ou_mx4_grouped_outer(int out_dtype, const uint8_t* a_codes_t, cons
     p.offsets = offsets;
     p.rows = rows;
     p.groups = groups;
-    return launch_matmul(out_dtype, kByContraction, p, groups, stream);
+    // the mean depth does not matter for the choice, the tiles do
+    Choice c = choose(m, n, p.steps, groups);
+    if (!c.tile) c = {0, 64, 64};
+    return launch_matmul(out_dtype, kByContraction, c, p, groups, stream);
 }
 
 }  // extern "C"

@@ -494,24 +494,34 @@ __global__ __launch_bounds__(kQuantThreads) void k_dequant(DequantArgs d, int64_
 // the 32 columns 32 (l / 16) .. of row l mod 16, and the scale of that block.
 __device__ __forceinline__ i32x8 widen(i32x4 v) { return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
 
-// Four waves, 32 x 32 results each.  The fragment of b is the instruction's
-// first operand, so a lane's four results are neighbours in a row of out.
-template <int DT, int G>
-__global__ __launch_bounds__(kMatmulThreads) void k_matmul(MatmulArgs p)
+// Few rows, or few tiles: 16 MT x 16 NT results a block, the k-steps dealt to
+// its W waves in contiguous runs, fragments loaded straight to registers U
+// steps ahead, the waves' sums joined in LDS in the order of the waves.  Such
+// a product waits for memory: what counts is that all of a block's rows of b
+// are under way at once.  With XT (one row of fragments) the left matrix is
+// given as values of that type: a lane's fragment is one block of 32 values,
+// quantised in its registers.  The fragment of b is the instruction's first
+// operand, so that a lane's four results are neighbours in a row of out.
+template <int XT, int G, int MT, int NT, int W, int U>
+__global__ __launch_bounds__(kWave * W) void k_matmul_split(MatmulArgs p)
 {
-    const int t = static_cast<int>(threadIdx.x), wave = t >> 6, lane = t & 63, r = lane & 15, g = lane >> 4;
-    const int64_t unit = blockIdx.x / p.n_tiles, ntile = blockIdx.x - unit * p.n_tiles;
-    int64_t row0 = unit * kMatmulTile, mrows = p.m - row0;
-    int64_t step0 = 0, steps = p.steps;
-    const uint8_t* b = p.b;
-    const uint8_t* bs = p.bs;
-    int64_t out0 = 0;
+    constexpr bool kValues = XT != kHeld;
+    static_assert(!kValues || MT == 1, "values are quantised for one row of fragments");
+    __shared__ f32x4 part[W][MT * NT][kWave];
+    const int t = static_cast<int>(threadIdx.x), lane = t & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const uint32_t unit = blockIdx.x / static_cast<uint32_t>(p.n_tiles);
+    const uint32_t ntile = blockIdx.x - unit * static_cast<uint32_t>(p.n_tiles);
+    int64_t row0 = static_cast<int64_t>(unit) * (16 * MT), mrows = p.m - row0;
+    int64_t step0 = 0, steps = p.steps, out0 = 0;
+    const uint8_t *b = p.b, *bs = p.bs;
     if constexpr (G == kByRows) {
-        const Place at = locate(p.offsets, p.groups, p.rows, kMatmulTile, unit);
+        const Place at = locate(p.offsets, p.groups, p.rows, 16 * MT, unit);
         row0 = at.row;
         mrows = at.rows;
+        if (mrows <= 0) return;
         if (at.group < 0) {
-            if (!p.zero_rest || mrows <= 0) return;
+            if (!p.zero_rest) return;
             steps = 0;   // rows of no group: the sum over nothing
         } else {
             b += at.group * p.n * p.steps * (kPad / 2);
@@ -526,51 +536,99 @@ __global__ __launch_bounds__(kMatmulThreads) void k_matmul(MatmulArgs p)
         if (steps > p.steps - step0) steps = p.steps - step0;
         out0 = static_cast<int64_t>(blockIdx.y) * p.m * p.out_stride;
     }
-    const int64_t n0 = ntile * kMatmulTile + (wave & 1) * 32;
-    const int64_t m0 = (wave >> 1) * 32;
-    const uint8_t *ap[2], *asp[2], *bp[2], *bsp[2];
+    const int64_t n0 = static_cast<int64_t>(ntile) * (16 * NT);
+    const uint8_t *ap[MT], *asp[MT], *bp[NT], *bsp[NT];
+    using Elem = typename Type<kValues ? XT : kF32>::Elem;
+    const Elem* xp = nullptr;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        int64_t m = m0 + 16 * i + r, n = n0 + 16 * i + r;   // rows behind the edge read the last one
+    for (int i = 0; i < MT; ++i) {
+        int64_t m = 16 * i + r;              // rows behind the edge read the last one
         m = row0 + (m < mrows ? m : mrows - 1);
+        if constexpr (kValues) {
+            xp = static_cast<const Elem*>(p.x) + m * p.x_stride;
+        } else {
+            ap[i] = p.a + (m * p.steps + step0) * (kPad / 2) + g * 16;
+            asp[i] = p.as + (m * p.steps + step0) * (kPad / kBlock);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        int64_t n = n0 + 16 * j + r;
         n = n < p.n ? n : p.n - 1;
-        ap[i] = p.a + (m * p.steps + step0) * (kPad / 2) + g * 16;
-        asp[i] = p.as + (m * p.steps + step0) * (kPad / kBlock) + g;
-        bp[i] = b + (n * p.steps + step0) * (kPad / 2) + g * 16;
-        bsp[i] = bs + (n * p.steps + step0) * (kPad / kBlock) + g;
+        bp[j] = b + (n * p.steps + step0) * (kPad / 2) + g * 16;
+        bsp[j] = bs + (n * p.steps + step0) * (kPad / kBlock);
     }
-    f32x4 acc[2][2] = {};
-    for (int64_t k = 0; k < steps; ++k) {
-        i32x8 av[2], bv[2];
-        int as[2], bsc[2];
+    f32x4 acc[MT][NT] = {};
+    const int64_t run = (steps + W - 1) / W, first = wave * run;
+    const int64_t last = first + run < steps ? first + run : steps;
+    for (int64_t k0 = first; k0 < last; k0 += U) {
+        i32x4 av[U][MT], bv[U][NT];
+        int as[U][MT], bsc[U][NT];
+        Octet<kValues ? XT : kF32> v[kValues ? U : 1][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            av[i] = widen(*reinterpret_cast<const i32x4*>(ap[i] + k * (kPad / 2)));
-            bv[i] = widen(*reinterpret_cast<const i32x4*>(bp[i] + k * (kPad / 2)));
-            as[i] = asp[i][k * (kPad / kBlock)];
-            bsc[i] = bsp[i][k * (kPad / kBlock)];
+        for (int u = 0; u < U; ++u) {
+            const int64_t k = k0 + u < last ? k0 + u : last - 1;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                bv[u][j] = *reinterpret_cast<const i32x4*>(bp[j] + k * (kPad / 2));
+                bsc[u][j] = *reinterpret_cast<const int*>(bsp[j] + k * (kPad / kBlock));
+            }
+            if constexpr (kValues) {
+                const int64_t at = k * kPad + g * kBlock;
+#pragma unroll
+                for (int o = 0; o < 4; ++o) {
+                    const int64_t have = r < mrows ? p.k - at - 8 * o : 0;
+                    v[u][o].load(xp + at + 8 * o, have < 0 ? 0 : (have > 8 ? 8 : static_cast<int>(have)), p.x_wide);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    av[u][i] = *reinterpret_cast<const i32x4*>(ap[i] + k * (kPad / 2));
+                    as[u][i] = *reinterpret_cast<const int*>(asp[i] + k * (kPad / kBlock));
+                }
+            }
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int u = 0; u < U; ++u) {
+            if (k0 + u >= last) break;
+            if constexpr (kValues) {
+                const uint32_t top = max(max(v[u][0].top(), v[u][1].top()), max(v[u][2].top(), v[u][3].top()));
+                const uint32_t s = scale_code(exponent_of<XT>(top));
+                const float scale = scale_operand(s);
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bv[j], av[i], acc[i][j], 4, 4, 0, bsc[j],
-                                                                            0, as[i]);
+                for (int o = 0; o < 4; ++o) av[u][0][o] = s == kScaleNaN ? 0 : static_cast<int>(v[u][o].codes(scale));
+                as[u][0] = static_cast<int>(s << (8 * g));
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        widen(bv[u][j]), widen(av[u][i]), acc[i][j], 4, 4, 0, bsc[u][j] >> (8 * g), 0, as[u][i] >> (8 * g));
+        }
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int64_t m = m0 + 16 * i + r;
-        if (m >= mrows) continue;
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int64_t n = n0 + 16 * j + 4 * g, left = p.n - n;
-            if (left <= 0) continue;
-            store4<DT>(p.out, out0 + (row0 + m) * p.out_stride + n, acc[i][j], left > 4 ? 4 : static_cast<int>(left),
-                       p.wide);
-        }
+        for (int j = 0; j < NT; ++j) part[wave][i * NT + j][lane] = acc[i][j];
+    __syncthreads();
+    for (int x = t; x < MT * NT * kWave; x += kWave * W) {
+        const int f = x >> 6, i = f / NT, j = f - i * NT;   // lane x mod 64 is this one
+        f32x4 sum = part[0][f][lane];
+#pragma unroll
+        for (int w = 1; w < W; ++w) sum += part[w][f][lane];
+        const int64_t m = 16 * i + r, n = n0 + 16 * j + 4 * g, left = p.n - n;
+        if (m >= mrows || left <= 0) continue;
+        const int64_t at = out0 + (row0 + m) * p.out_stride + n;
+        const int have = left > 4 ? 4 : static_cast<int>(left);
+        if (p.out_dtype == kF32)
+            store4<kF32>(p.out, at, sum, have, p.wide);
+        else if (p.out_dtype == kF16)
+            store4<kF16>(p.out, at, sum, have, p.wide);
+        else
+            store4<kBF16>(p.out, at, sum, have, p.wide);
     }
 }
-
 
 // ---- products, tiled through LDS ------------------------------------------
 
@@ -917,15 +975,6 @@ const void* dequant_kernel(int dtype)
     return fns[dtype];
 }
 
-template <int G>
-const void* matmul_of(int dtype)
-{
-    const void* fns[3] = {reinterpret_cast<const void*>(&k_matmul<kF32, G>),
-                          reinterpret_cast<const void*>(&k_matmul<kF16, G>),
-                          reinterpret_cast<const void*>(&k_matmul<kBF16, G>)};
-    return fns[dtype];
-}
-
 template <int G, int W>
 const void* matmul_tile_of(int dtype)
 {
@@ -935,17 +984,47 @@ const void* matmul_tile_of(int dtype)
     return fns[dtype];
 }
 
-template <int G>
-const void* matmul_any(int dtype, int tile)
+const void* matmul_tile_kernel(int out_dtype, int grouping, int tile)
 {
-    return tile == 256 ? matmul_tile_of<G, 8>(dtype) : tile == 128 ? matmul_tile_of<G, 4>(dtype) : matmul_of<G>(dtype);
+    const bool large = tile == 256;
+    return grouping == kPlain    ? (large ? matmul_tile_of<kPlain, 8>(out_dtype) : matmul_tile_of<kPlain, 4>(out_dtype))
+           : grouping == kByRows ? (large ? matmul_tile_of<kByRows, 8>(out_dtype) : matmul_tile_of<kByRows, 4>(out_dtype))
+                                 : (large ? matmul_tile_of<kByContraction, 8>(out_dtype)
+                                          : matmul_tile_of<kByContraction, 4>(out_dtype));
 }
 
-const void* matmul_kernel(int out_dtype, int grouping, int tile)
+template <int XT, int G>
+SplitKernel split_of(int rows, int cols)
 {
-    return grouping == kPlain ? matmul_any<kPlain>(out_dtype, tile)
-           : grouping == kByRows ? matmul_any<kByRows>(out_dtype, tile)
-                                 : matmul_any<kByContraction>(out_dtype, tile);
+#define MX4_SPLIT(MT, NT, W, U) \
+    SplitKernel{reinterpret_cast<const void*>(&k_matmul_split<XT, G, MT, NT, W, U>), 16 * MT, 16 * NT, W}
+    if constexpr (G != kByContraction) {
+        if (rows == 16) return cols == 16 ? MX4_SPLIT(1, 1, 8, 4) : MX4_SPLIT(1, 4, 8, 2);
+    }
+    if constexpr (XT == kHeld) {
+        if (rows == 32) return MX4_SPLIT(2, 2, 8, 2);
+        return MX4_SPLIT(4, 4, 8, 1);
+    }
+#undef MX4_SPLIT
+    return SplitKernel{nullptr, 0, 0, 0};
+}
+
+template <int G>
+SplitKernel split_any(int x_dtype, int rows, int cols)
+{
+    if constexpr (G != kByContraction) {
+        if (x_dtype == kF32) return split_of<kF32, G>(rows, cols);
+        if (x_dtype == kF16) return split_of<kF16, G>(rows, cols);
+        if (x_dtype == kBF16) return split_of<kBF16, G>(rows, cols);
+    }
+    return split_of<kHeld, G>(rows, cols);
+}
+
+SplitKernel matmul_split_kernel(int x_dtype, int grouping, int rows, int cols)
+{
+    return grouping == kPlain    ? split_any<kPlain>(x_dtype, rows, cols)
+           : grouping == kByRows ? split_any<kByRows>(x_dtype, rows, cols)
+                                 : split_any<kByContraction>(x_dtype, rows, cols);
 }
 
 }  // namespace mx4

@@ -205,6 +205,45 @@ def test_matmul(m, n, k, dtype):
     assert torch.equal(got, ou.mx4_matmul(xq, b, dtype))
 
 
+# many tiles of 128 and of 256, ragged edges, odd and even numbers of k-steps
+@pytest.mark.parametrize("m,n,k,dtype", [(1500, 1490, 129, F32), (1411, 1537, 1200, BF16), (2500, 700, 2200, F16),
+                                         (4099, 4100, 100, BF16), (4200, 4001, 257, F32), (4097, 3905, 640, F16),
+                                         (3841, 4100, 1300, F32), (200, 70000, 500, BF16)])
+def test_matmul_many_tiles(m, n, k, dtype):
+    print("many tiles", m, n, k, dtype, flush=True)
+    a, b = _random_held(m, k, 28), _random_held(n, k, 29)
+    a.scales[m // 2, 0] = 255                      # one NaN block: its row alone
+    got = ou.mx4_matmul(a, b, dtype)
+    want, mag = R.product(R.held(a), R.held(b))
+    R.check_product(got, want, mag, k)
+    buf = torch.full((m, n + 5), 3.0, dtype=dtype, device="cuda")
+    ou.mx4_matmul(a, b, out=buf[:, 1:n + 1])       # no 16 bytes aligned
+    assert torch.equal(buf[:, 1:n + 1].nan_to_num(7.0), got.nan_to_num(7.0))
+    assert (buf[:, 0] == 3).all() and (buf[:, n + 1:] == 3).all()
+
+
+@pytest.mark.parametrize("counts,front,back,n,k", [([700, 0, 1300, 129, 1], 0, 0, 1100, 300),
+                                                   ([2100, 900, 0, 2000, 300], 3, 5, 4100, 200)])
+def test_grouped_products_of_many_tiles(counts, front, back, n, k):
+    t, e = front + sum(counts) + back, len(counts)
+    off = _offsets(counts, front).cuda()
+    x, b = _values((t, k), BF16, 34).cuda(), _random_held(n, k, 35, lead=(e,))
+    dy = _values((t, n), BF16, 36).cuda()
+    got = ou.mx4_grouped_matmul(x, b, off)
+    xq, xt = ou.mx4_quantize_grouped(x, off)
+    _, dt = ou.mx4_quantize_grouped(dy, off, rows=False)
+    dw = ou.mx4_grouped_outer(dt, xt, off, t, F32)
+    x64, d64 = R.host(x), R.host(dy)
+    out = torch.full((t, n), 5.0, dtype=BF16, device="cuda")
+    ou.mx4_grouped_matmul(x, b, off, out=out)
+    for i, (lo, hi) in enumerate(zip(off[:-1].tolist(), off[1:].tolist())):
+        R.check_product(got[lo:hi], *R.product(R.rounded(x64[lo:hi]), R.held(b[i])), k)
+        R.check_product(dw[i], *R.product(R.rounded(d64[lo:hi].T), R.rounded(x64[lo:hi].T)), max(1, hi - lo))
+        assert torch.equal(out[lo:hi], got[lo:hi])
+    for rest in (slice(0, front), slice(t - back, t)):
+        assert (got[rest] == 0).all() and (out[rest] == 5).all()
+
+
 @pytest.mark.parametrize("m", [1, 16, 40, 200])
 def test_matmul_scales_of_every_size(m):
     """Scales over the whole range of binary32, results up to infinity."""
