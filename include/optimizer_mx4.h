@@ -60,7 +60,8 @@ int ou_mx4_quantize(int dtype, const void* x, int64_t batch, int64_t rows, int64
 int64_t ou_mx4_grouped_columns(int64_t rows, int32_t groups);
 
 /* The same for one matrix whose rows fall into groups: group e is rows
- * [offsets[e], offsets[e + 1]), offsets being groups + 1 int32 in device
+ * [offsets[e], offsets[e + 1]) (rows at most 2^28 in the calls by groups),
+ * offsets being groups + 1 int32 in device
  * memory, rising, within [0, rows] (others are clamped to that; a group that
  * runs backwards is empty).  Along the rows every group is a matrix of its
  * own: its columns of codes_t start at the sum of the earlier groups' rows,

@@ -65,6 +65,7 @@ struct MatmulArgs {
     const void* x;
     int64_t x_stride, k;
     int32_t x_dtype;
+    int32_t few_rows;         // rows that k_matmul_few has room for
     int32_t x_wide;           // 16-byte loads of whole octets of x are allowed
 };
 
@@ -77,11 +78,16 @@ const void* dequant_kernel(int dtype);
 const void* matmul_tile_kernel(int out_dtype, int grouping, int tile);
 
 // Products of few rows or few tiles: rows x cols results a block of `waves`
-// waves; 16 x 16, 16 x 64, 32 x 32 or 64 x 64.
+// waves; 16 x 16 and 16 x 64 (k_matmul_few, with few_lds() bytes of dynamic
+// LDS), 32 x 32 and 64 x 64 (k_matmul_split).
 struct SplitKernel {
     const void* fn;
     int rows, cols, waves;
 };
+inline int64_t few_lds(int64_t rows, int64_t steps, int cols, int waves)   // rows: 0 for a held left matrix
+{
+    return rows * (steps * 64 + 16) + (rows * (steps * 4 + 4) + 15) / 16 * 16 + static_cast<int64_t>(waves) * cols * 64;
+}
 SplitKernel matmul_split_kernel(int x_dtype, int grouping, int rows, int cols);
 
 constexpr int kQuantThreads = 256;

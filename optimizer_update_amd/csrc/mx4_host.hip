@@ -106,11 +106,12 @@ double extent(int64_t rows, int64_t cols, int64_t stride, int bytes)
     return (static_cast<double>(rows - 1) * static_cast<double>(stride) + static_cast<double>(cols)) * bytes;
 }
 
-int launch(const void* fn, int64_t gx, int64_t gy, int threads, void** args, void* stream, const char* what)
+int launch(const void* fn, int64_t gx, int64_t gy, int threads, void** args, void* stream, const char* what,
+           int64_t lds = 0)
 {
     if (gx > INT32_MAX || gy > kMaxBatch) return fail(OU_EINVAL, "%s: too many tiles", what);
     const hipError_t e = hipLaunchKernel(fn, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)),
-                                         dim3(static_cast<unsigned>(threads)), args, 0,
+                                         dim3(static_cast<unsigned>(threads)), args, static_cast<size_t>(lds),
                                          static_cast<hipStream_t>(stream));
     return e == hipSuccess ? OU_OK : hip_fail(e, what);
 }
@@ -145,18 +146,24 @@ int launch_quantize(int dtype, QuantArgs& q, int64_t batch, int64_t units, void*
 // mean.
 struct Choice {
     int tile, rows, cols;
+    bool values;   // the left matrix may come as values
 };
 
-Choice choose(int64_t rows, int64_t n, int64_t steps, int64_t batch)
+// The rows in LDS (k_matmul_few) are quantised by every block again: that
+// pays while they are few and short (and 36 KiB hold them).
+constexpr int64_t kValuesSteps = 512;
+
+// room: the rows of a block, at most (by groups not known here: 16).
+Choice choose(int64_t rows, int64_t n, int64_t steps, int64_t batch, int64_t room)
 {
-    if (rows <= 16) return {0, 16, cut(n, 16) * batch <= 1024 ? 16 : 64};
-    if (rows <= 32) return {0, 32, 32};
+    if (rows <= 16) return {0, 16, cut(n, 16) * batch <= 1024 ? 16 : 64, room * steps <= kValuesSteps};
+    if (rows <= 32) return {0, 32, 32, false};
     // the tiles address their rows by 31 bits
     if (steps < (int64_t(1) << 17)) {
-        if (cut(rows, 256) * cut(n, 256) * batch >= 256) return {256, 0, 0};
-        if (cut(rows, 128) * cut(n, 128) * batch >= 128) return {128, 0, 0};
+        if (cut(rows, 256) * cut(n, 256) * batch >= 256) return {256, 0, 0, false};
+        if (cut(rows, 128) * cut(n, 128) * batch >= 128) return {128, 0, 0, false};
     }
-    return {0, 64, 64};
+    return {0, 64, 64, false};
 }
 
 // By groups: the mean of the groups' rows decides, as the rows themselves are
@@ -164,7 +171,7 @@ Choice choose(int64_t rows, int64_t n, int64_t steps, int64_t batch)
 Choice choose_grouped(int64_t rows, int64_t n, int64_t steps, int32_t groups)
 {
     const int64_t g = groups > 0 ? groups : 1;
-    return choose(cut(rows, g), n, steps, g < rows ? g : (rows > 0 ? rows : 1));
+    return choose(cut(rows, g), n, steps, g < rows ? g : (rows > 0 ? rows : 1), rows < 16 ? rows : 16);
 }
 
 int launch_matmul(int out_dtype, int grouping, const Choice& c, MatmulArgs& p, int64_t batch, void* stream)
@@ -179,11 +186,13 @@ int launch_matmul(int out_dtype, int grouping, const Choice& c, MatmulArgs& p, i
                        c.tile ? 16 : 4 * elem_bytes(out_dtype));
     void* args[] = {&p};
     return launch(c.tile ? matmul_tile_kernel(out_dtype, grouping, c.tile) : s.fn, p.units * p.n_tiles, batch,
-                  c.tile ? kMatmulThreads : kWave * s.waves, args, stream, "the product's kernel");
+                  c.tile ? kMatmulThreads : kWave * s.waves, args, stream, "the product's kernel",
+                  rows == 16 ? few_lds(p.few_rows, p.steps, cols, s.waves) : 0);
 }
 
-int check_groups(const int32_t* offsets, int32_t groups)
+int check_groups(const int32_t* offsets, int32_t groups, int64_t rows)
 {
+    if (rows > (int64_t(1) << 28)) return fail(OU_EINVAL, "%lld rows by groups: 2^28 at most", (long long)rows);
     if (groups < 0 || groups > kMaxBatch) return fail(OU_EINVAL, "groups = %d is out of range", groups);
     if (!offsets) return fail(OU_EINVAL, "offsets is null");
     if (reinterpret_cast<uintptr_t>(offsets) % 4) return fail(OU_EALIGN, "offsets is not 4-byte aligned");
@@ -243,7 +252,7 @@ OU_EXPORT int ou_mx4_quantize_grouped(int dtype, const void* x, int64_t rows, in
     if (int st = check_axis(rows, "rows")) return st;
     if (int st = check_axis(cols, "cols")) return st;
     if (row_stride < cols || row_stride > kMaxAxis) return fail(OU_EINVAL, "row_stride is out of range");
-    if (int st = check_groups(offsets, groups)) return st;
+    if (int st = check_groups(offsets, groups, rows)) return st;
     if (rows == 0 || cols == 0 || groups == 0) return OU_OK;
     if (!codes != !scales) return fail(OU_EINVAL, "codes and scales come in pairs");
     if (!codes_t || !scales_t) return fail(OU_EINVAL, "codes_t or scales_t is null");
@@ -284,14 +293,14 @@ OU_EXPORT int ou_mx4_dequantize(int dtype, const uint8_t* codes, const uint8_t* 
 OU_EXPORT int64_t ou_mx4_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k, int from_values)
 {
     if (check_axis(m, "m") || check_axis(n, "n") || check_axis(k, "k")) return -1;
-    return from_values && choose(m, n, pad(k) / kPad, 1).rows != 16 ? values_bytes(m, k) : 0;
+    return from_values && !choose(m, n, pad(k) / kPad, 1, m).values ? values_bytes(m, k) : 0;
 }
 
 OU_EXPORT int64_t ou_mx4_grouped_workspace_bytes(int64_t rows, int64_t n, int64_t k, int32_t groups, int from_values)
 {
     if (groups < 0 || groups > kMaxBatch) return -1;
     if (check_axis(rows, "rows") || check_axis(n, "n") || check_axis(k, "k")) return -1;
-    return from_values && choose_grouped(rows, n, pad(k) / kPad, groups).rows != 16 ? values_bytes(rows, k) : 0;
+    return from_values && !choose_grouped(rows, n, pad(k) / kPad, groups).values ? values_bytes(rows, k) : 0;
 }
 
 }  // extern "C"
@@ -327,7 +336,7 @@ int product(Product& q, bool values, bool grouped)
     if (values && (q.x_stride < q.k || q.x_stride > kMaxAxis)) return fail(OU_EINVAL, "x_stride is out of range");
     if (q.out_stride < q.n || q.out_stride > kMaxAxis) return fail(OU_EINVAL, "out_stride is out of range");
     if (grouped)
-        if (int st = check_groups(q.offsets, q.groups)) return st;
+        if (int st = check_groups(q.offsets, q.groups, q.m)) return st;
     if (q.m == 0 || q.n == 0) return OU_OK;
     const int64_t need = grouped ? ou_mx4_grouped_workspace_bytes(q.m, q.n, q.k, q.groups, values)
                                  : ou_mx4_matmul_workspace_bytes(q.m, q.n, q.k, values);
@@ -347,13 +356,14 @@ int product(Product& q, bool values, bool grouped)
     if (int st = check_buffers(bufs, 8)) return st;
     if (int st = check_device()) return st;
     const uint8_t *a = q.a, *as = q.as;
-    const Choice c = grouped ? choose_grouped(q.m, q.n, pk / kPad, q.groups) : choose(q.m, q.n, pk / kPad, 1);
+    const Choice c = grouped ? choose_grouped(q.m, q.n, pk / kPad, q.groups) : choose(q.m, q.n, pk / kPad, 1, q.m);
     MatmulArgs p{};
-    if (values && c.rows == 16) {   // quantised where it is multiplied
+    if (values && c.values) {   // quantised where it is multiplied
         p.x = q.x;
         p.x_dtype = q.x_dtype;
         p.x_stride = q.x_stride;
         p.k = q.k;
+        p.few_rows = static_cast<int32_t>(q.m < 16 ? q.m : 16);
         p.x_wide = wide_rows(q.x, q.x_stride, 0, ex, 16);
     } else if (values && pk > 0) {
         uint8_t* wc = static_cast<uint8_t*>(q.workspace);
@@ -429,7 +439,7 @@ OU_EXPORT int ou_mx4_grouped_outer(int out_dtype, const uint8_t* a_codes_t, cons
     if (int st = check_axis(m, "m")) return st;
     if (int st = check_axis(n, "n")) return st;
     if (int st = check_axis(rows, "rows")) return st;
-    if (int st = check_groups(offsets, groups)) return st;
+    if (int st = check_groups(offsets, groups, rows)) return st;
     if (m == 0 || n == 0 || groups == 0) return OU_OK;
     const int64_t pr = ou_mx4_grouped_columns(rows, groups);
     const int eo = elem_bytes(out_dtype);
@@ -455,8 +465,8 @@ OU_EXPORT int ou_mx4_grouped_outer(int out_dtype, const uint8_t* a_codes_t, cons
     p.rows = rows;
     p.groups = groups;
     // the mean depth does not matter for the choice, the tiles do
-    Choice c = choose(m, n, p.steps, groups);
-    if (!c.tile) c = {0, 64, 64};
+    Choice c = choose(m, n, p.steps, groups, 16);
+    if (!c.tile) c = {0, 64, 64, false};
     return launch_matmul(out_dtype, kByContraction, c, p, groups, stream);
 }
 

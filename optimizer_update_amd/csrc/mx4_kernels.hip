@@ -182,90 +182,121 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t x)
 // ---- groups ---------------------------------------------------------------
 
 struct Place {
-    int32_t group;   // -1: of no group (rows = 0: behind everything)
-    int64_t row;     // first row of the unit
-    int64_t rows;    // rows of the unit inside its group
-    int64_t first;   // unit index of the group's first unit
-    int64_t units;   // units of the group
+    int32_t group;    // -1: of no group (rows = 0: behind everything)
+    int32_t row;      // first row of the unit
+    int32_t rows;     // rows of the unit inside its group
 };
 
-__device__ __forceinline__ int64_t clamp_offset(int32_t o, int64_t rows)
+// Sum over the lanes up to this one.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t x)
 {
-    return o < 0 ? 0 : (o > rows ? rows : o);
+    // within rows of 16 lanes, then the rows' ends to the lanes behind them
+    x += static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x111, 0xf, 0xf, false));
+    x += static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x112, 0xf, 0xf, false));
+    x += static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x114, 0xf, 0xf, false));
+    x += static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x118, 0xf, 0xf, false));
+    x += static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x142, 0xa, 0xf, false));
+    x += static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x143, 0xc, 0xf, false));
+    return x;
 }
 
-// The group that unit `index` falls in when every group is cut into units of
-// `unit` rows, for offsets that may be anything (clamped to [0, rows], a
-// group that runs backwards is empty).  All lanes of the wave take part and
-// get the same answer.  Lane l looks at group base + l.
-__device__ __forceinline__ Place locate(const int32_t* offsets, int32_t groups, int64_t rows, int unit, int64_t index)
+__device__ __forceinline__ uint32_t lane_value(uint32_t x, int lane)
 {
-    const int lane = static_cast<int>(threadIdx.x) & (kWave - 1);
-    int64_t before = 0;
-    for (int32_t base = 0; base < groups; base += kWave) {
-        const int32_t e = base + lane;
-        int64_t lo = 0, n = 0;
+    return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(x), lane));
+}
+
+// The groups of a call, cut into units of `unit` rows each.  Offsets may be
+// anything: they are clamped to [0, rows], and a group that runs backwards is
+// empty.  rows is at most 2^28 and unit at least 16, so the units of 64 groups
+// stay below 2^31 even where groups overlap; sums over more groups saturate.
+// All lanes of a wave take part and get the same answers; lane l looks at
+// group base + l.
+struct Groups {
+    const int32_t* offsets;
+    int32_t groups, rows, unit;
+    // the chunk of 64 groups at hand
+    int32_t base = -1;
+    uint32_t lo, n, scan;
+
+    __device__ __forceinline__ Groups(const int32_t* o, int32_t g, int64_t r, int u)
+        : offsets(o), groups(g), rows(static_cast<int32_t>(r)), unit(u)
+    {
+    }
+    __device__ __forceinline__ uint32_t offset(int32_t i) const
+    {
+        const int32_t o = offsets[i];
+        return static_cast<uint32_t>(o < 0 ? 0 : (o > rows ? rows : o));
+    }
+    __device__ __forceinline__ uint32_t units(uint32_t count) const { return (count + unit - 1) / unit; }
+    __device__ __forceinline__ void chunk(int32_t at)
+    {
+        if (base == at) return;
+        base = at;
+        const int32_t e = at + (static_cast<int>(threadIdx.x) & (kWave - 1));
+        lo = n = 0;
         if (e < groups) {
-            lo = clamp_offset(offsets[e], rows);
-            const int64_t hi = clamp_offset(offsets[e + 1], rows);
+            lo = offset(e);
+            const uint32_t hi = offset(e + 1);
             n = hi > lo ? hi - lo : 0;
         }
-        const int64_t u = (n + unit - 1) / unit;
-        int64_t sum = u;   // inclusive prefix sum over the wave
-        for (int d = 1; d < kWave; d <<= 1) {
-            const int64_t o = __shfl_up(sum, d);
-            if (lane >= d) sum += o;
+        scan = wave_scan(units(n));
+    }
+    static __device__ __forceinline__ uint32_t add(uint32_t before, uint32_t more)
+    {
+        const uint32_t s = before + more;   // both below 2^31
+        return s > 0x7fffffffu ? 0x7fffffffu : s;
+    }
+    // units of all groups
+    __device__ __forceinline__ uint32_t total()
+    {
+        uint32_t before = 0;
+        for (int32_t at = 0; at < groups; at += kWave) {
+            chunk(at);
+            before = add(before, lane_value(scan, kWave - 1));
         }
-        const uint64_t past = __ballot(before + sum > index);
-        if (past) {
-            const int hit = __builtin_ctzll(past);
-            Place p;
-            p.group = base + hit;
-            p.units = __shfl(u, hit);
-            p.first = before + __shfl(sum, hit) - p.units;
-            const int64_t start = __shfl(lo, hit), count = __shfl(n, hit);
-            const int64_t at = (index - p.first) * unit;
-            p.row = start + at;
-            p.rows = count - at < unit ? count - at : unit;
-            return p;
+        return before;
+    }
+    // units of the rows in front of the first group, and behind the last
+    __device__ __forceinline__ uint32_t front() const { return groups ? offset(0) : 0; }
+    __device__ __forceinline__ uint32_t back() const { return groups ? offset(groups) : 0; }
+    __device__ __forceinline__ uint32_t rest() const { return units(front()) + units(rows - back()); }
+    // unit `index` of all, those of no group last
+    __device__ __forceinline__ Place locate(uint32_t index)
+    {
+        uint32_t before = 0;
+        for (int32_t at = 0; at < groups; at += kWave) {
+            chunk(at);
+            const uint64_t past = __ballot(before + scan > index);
+            if (past) {
+                const int hit = __builtin_ctzll(past);
+                const uint32_t count = lane_value(n, hit);
+                const uint32_t first = before + lane_value(scan, hit) - units(count);
+                const uint32_t from = (index - first) * unit;
+                return Place{at + hit, static_cast<int32_t>(lane_value(lo, hit) + from),
+                             static_cast<int32_t>(count - from < static_cast<uint32_t>(unit) ? count - from : unit)};
+            }
+            before = add(before, lane_value(scan, kWave - 1));
         }
-        before += __shfl(sum, kWave - 1);
+        const uint32_t f = front(), b = back(), nf = units(f), j = index - before;
+        if (j >= nf + units(rows - b)) return Place{-1, 0, 0};
+        const uint32_t row = j < nf ? j * unit : b + (j - nf) * unit, end = j < nf ? f : rows;
+        return Place{-1, static_cast<int32_t>(row),
+                     static_cast<int32_t>(end - row < static_cast<uint32_t>(unit) ? end - row : unit)};
     }
-    // units of the rows in front of the first group, then of those behind the last
-    const int64_t front = groups ? clamp_offset(offsets[0], rows) : 0;
-    const int64_t back = groups ? clamp_offset(offsets[groups], rows) : 0;
-    const int64_t nf = (front + unit - 1) / unit, nb = (rows - back + unit - 1) / unit;
-    const int64_t j = index - before;
-    Place p{-1, 0, 0, before, nf + nb};
-    if (j < nf) {
-        p.row = j * unit;
-        p.rows = front - p.row < unit ? front - p.row : unit;
-    } else if (j < nf + nb) {
-        p.row = back + (j - nf) * unit;
-        p.rows = rows - p.row < unit ? rows - p.row : unit;
+    // units of the groups before `group`, and its own
+    __device__ __forceinline__ void span(int32_t group, uint32_t* first, uint32_t* count)
+    {
+        uint32_t before = 0;
+        for (int32_t at = 0;; at += kWave) {
+            chunk(at);
+            if (group < at + kWave) break;
+            before = add(before, lane_value(scan, kWave - 1));
+        }
+        const uint32_t own = units(lane_value(n, group - base));
+        *first = add(before, lane_value(scan, group - base) - own);
+        *count = own;
     }
-    return p;
-}
-
-// Units before group e and the units of e.
-__device__ __forceinline__ Place units_of(const int32_t* offsets, int64_t rows, int unit, int32_t group)
-{
-    const int lane = static_cast<int>(threadIdx.x) & (kWave - 1);
-    int64_t sum = 0;
-    for (int32_t e = lane; e < group; e += kWave) {
-        const int64_t lo = clamp_offset(offsets[e], rows), hi = clamp_offset(offsets[e + 1], rows);
-        if (hi > lo) sum += (hi - lo + unit - 1) / unit;
-    }
-    for (int d = 1; d < kWave; d <<= 1) sum += __shfl_xor(sum, d);
-    const int64_t lo = clamp_offset(offsets[group], rows), hi = clamp_offset(offsets[group + 1], rows);
-    Place p;
-    p.group = group;
-    p.row = lo;
-    p.rows = hi > lo ? hi - lo : 0;
-    p.first = sum;
-    p.units = (p.rows + unit - 1) / unit;
-    return p;
-}
+};
 
 // ---- quantisation along the columns --------------------------------------
 
@@ -326,7 +357,7 @@ __global__ __launch_bounds__(kQuantThreads) void k_quant_tile(QuantArgs q)
     const int64_t unit = blockIdx.x / col_tiles;        // block of 128 padded rows
     int64_t row0 = unit * T, nrows = q.rows - row0;
     if (q.offsets) {
-        const Place p = locate(q.offsets, q.groups, q.rows, T, unit);
+        const Place p = Groups(q.offsets, q.groups, q.rows, T).locate(static_cast<uint32_t>(unit));
         if (p.group < 0) return;
         row0 = p.row;
         nrows = p.rows;
@@ -494,119 +525,22 @@ __global__ __launch_bounds__(kQuantThreads) void k_dequant(DequantArgs d, int64_
 // the 32 columns 32 (l / 16) .. of row l mod 16, and the scale of that block.
 __device__ __forceinline__ i32x8 widen(i32x4 v) { return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
 
-// Few rows, or few tiles: 16 MT x 16 NT results a block, the k-steps dealt to
-// its W waves in contiguous runs, fragments loaded straight to registers U
-// steps ahead, the waves' sums joined in LDS in the order of the waves.  Such
-// a product waits for memory: what counts is that all of a block's rows of b
-// are under way at once.  With XT (one row of fragments) the left matrix is
-// given as values of that type: a lane's fragment is one block of 32 values,
-// quantised in its registers.  The fragment of b is the instruction's first
-// operand, so that a lane's four results are neighbours in a row of out.
-template <int XT, int G, int MT, int NT, int W, int U>
-__global__ __launch_bounds__(kWave * W) void k_matmul_split(MatmulArgs p)
+// The block's barrier alone; no LDS access moves across it.
+__device__ __forceinline__ void block_barrier()
 {
-    constexpr bool kValues = XT != kHeld;
-    static_assert(!kValues || MT == 1, "values are quantised for one row of fragments");
-    __shared__ f32x4 part[W][MT * NT][kWave];
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// What k_matmul_few and k_matmul_split do with the waves' sums: joined in LDS
+// in the order of the waves, rounded once, stored.
+template <int MT, int NT, int W>
+__device__ __forceinline__ void join_and_store(const MatmulArgs& p, f32x4 (*part)[MT * NT][kWave],
+                                               const f32x4 (&acc)[MT][NT], int wave, int64_t out0, int64_t row0,
+                                               int64_t mrows, int64_t n0)
+{
     const int t = static_cast<int>(threadIdx.x), lane = t & 63, r = lane & 15, g = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-    const uint32_t unit = blockIdx.x / static_cast<uint32_t>(p.n_tiles);
-    const uint32_t ntile = blockIdx.x - unit * static_cast<uint32_t>(p.n_tiles);
-    int64_t row0 = static_cast<int64_t>(unit) * (16 * MT), mrows = p.m - row0;
-    int64_t step0 = 0, steps = p.steps, out0 = 0;
-    const uint8_t *b = p.b, *bs = p.bs;
-    if constexpr (G == kByRows) {
-        const Place at = locate(p.offsets, p.groups, p.rows, 16 * MT, unit);
-        row0 = at.row;
-        mrows = at.rows;
-        if (mrows <= 0) return;
-        if (at.group < 0) {
-            if (!p.zero_rest) return;
-            steps = 0;   // rows of no group: the sum over nothing
-        } else {
-            b += at.group * p.n * p.steps * (kPad / 2);
-            bs += at.group * p.n * p.steps * (kPad / kBlock);
-        }
-    }
-    if constexpr (G == kByContraction) {
-        const Place at = units_of(p.offsets, p.rows, kPad, static_cast<int32_t>(blockIdx.y));
-        step0 = at.first;
-        steps = at.units;
-        if (step0 > p.steps) step0 = p.steps;
-        if (steps > p.steps - step0) steps = p.steps - step0;
-        out0 = static_cast<int64_t>(blockIdx.y) * p.m * p.out_stride;
-    }
-    const int64_t n0 = static_cast<int64_t>(ntile) * (16 * NT);
-    const uint8_t *ap[MT], *asp[MT], *bp[NT], *bsp[NT];
-    using Elem = typename Type<kValues ? XT : kF32>::Elem;
-    const Elem* xp = nullptr;
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        int64_t m = 16 * i + r;              // rows behind the edge read the last one
-        m = row0 + (m < mrows ? m : mrows - 1);
-        if constexpr (kValues) {
-            xp = static_cast<const Elem*>(p.x) + m * p.x_stride;
-        } else {
-            ap[i] = p.a + (m * p.steps + step0) * (kPad / 2) + g * 16;
-            asp[i] = p.as + (m * p.steps + step0) * (kPad / kBlock);
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        int64_t n = n0 + 16 * j + r;
-        n = n < p.n ? n : p.n - 1;
-        bp[j] = b + (n * p.steps + step0) * (kPad / 2) + g * 16;
-        bsp[j] = bs + (n * p.steps + step0) * (kPad / kBlock);
-    }
-    f32x4 acc[MT][NT] = {};
-    const int64_t run = (steps + W - 1) / W, first = wave * run;
-    const int64_t last = first + run < steps ? first + run : steps;
-    for (int64_t k0 = first; k0 < last; k0 += U) {
-        i32x4 av[U][MT], bv[U][NT];
-        int as[U][MT], bsc[U][NT];
-        Octet<kValues ? XT : kF32> v[kValues ? U : 1][4];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t k = k0 + u < last ? k0 + u : last - 1;
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                bv[u][j] = *reinterpret_cast<const i32x4*>(bp[j] + k * (kPad / 2));
-                bsc[u][j] = *reinterpret_cast<const int*>(bsp[j] + k * (kPad / kBlock));
-            }
-            if constexpr (kValues) {
-                const int64_t at = k * kPad + g * kBlock;
-#pragma unroll
-                for (int o = 0; o < 4; ++o) {
-                    const int64_t have = r < mrows ? p.k - at - 8 * o : 0;
-                    v[u][o].load(xp + at + 8 * o, have < 0 ? 0 : (have > 8 ? 8 : static_cast<int>(have)), p.x_wide);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    av[u][i] = *reinterpret_cast<const i32x4*>(ap[i] + k * (kPad / 2));
-                    as[u][i] = *reinterpret_cast<const int*>(asp[i] + k * (kPad / kBlock));
-                }
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (k0 + u >= last) break;
-            if constexpr (kValues) {
-                const uint32_t top = max(max(v[u][0].top(), v[u][1].top()), max(v[u][2].top(), v[u][3].top()));
-                const uint32_t s = scale_code(exponent_of<XT>(top));
-                const float scale = scale_operand(s);
-#pragma unroll
-                for (int o = 0; o < 4; ++o) av[u][0][o] = s == kScaleNaN ? 0 : static_cast<int>(v[u][o].codes(scale));
-                as[u][0] = static_cast<int>(s << (8 * g));
-            }
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        widen(bv[u][j]), widen(av[u][i]), acc[i][j], 4, 4, 0, bsc[u][j] >> (8 * g), 0, as[u][i] >> (8 * g));
-        }
-    }
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -628,6 +562,198 @@ __global__ __launch_bounds__(kWave * W) void k_matmul_split(MatmulArgs p)
         else
             store4<kBF16>(p.out, at, sum, have, p.wide);
     }
+}
+
+// Up to 16 rows (of a group): 16 x 16 NT results a block, the k-steps dealt to
+// its W waves in contiguous runs, b's fragments loaded straight to registers.
+// Such a product waits for b from memory: its first U steps are under way
+// before anything else.  With XT the left matrix is given as values of that
+// type: the block meanwhile quantises its rows into LDS.  The fragment of b is
+// the instruction's first operand, so that a lane's four results are
+// neighbours in a row of out.
+template <int XT, int G, int NT, int W, int U>
+__global__ __launch_bounds__(kWave * W) void k_matmul_few(MatmulArgs p)
+{
+    constexpr bool kValues = XT != kHeld;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    const int t = static_cast<int>(threadIdx.x), lane = t & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const uint32_t unit = blockIdx.x / static_cast<uint32_t>(p.n_tiles);
+    const uint32_t ntile = blockIdx.x - unit * static_cast<uint32_t>(p.n_tiles);
+    int64_t row0 = static_cast<int64_t>(unit) * 16, mrows = p.m - row0;
+    const int64_t row_steps = p.steps;
+    int64_t steps = p.steps;
+    const uint8_t *b = p.b, *bs = p.bs;
+    if constexpr (G == kByRows) {
+        const Place at = Groups(p.offsets, p.groups, p.rows, 16).locate(unit);
+        row0 = at.row;
+        mrows = at.rows;
+        if (mrows <= 0) return;
+        if (at.group < 0) {
+            if (!p.zero_rest) return;
+            steps = 0;   // rows of no group: the sum over nothing
+        } else {
+            b += static_cast<int64_t>(at.group) * p.n * row_steps * (kPad / 2);
+            bs += static_cast<int64_t>(at.group) * p.n * row_steps * (kPad / kBlock);
+        }
+    }
+    const int rows = mrows < 16 ? static_cast<int>(mrows) : 16;
+    const int64_t n0 = static_cast<int64_t>(ntile) * (16 * NT);
+    const uint8_t *bp[NT], *bsp[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        int64_t n = n0 + 16 * j + r;
+        n = n < p.n ? n : p.n - 1;           // rows behind the edge read the last one
+        bp[j] = b + n * row_steps * (kPad / 2) + g * 16;
+        bsp[j] = bs + n * row_steps * (kPad / kBlock);
+    }
+    const int64_t run = (steps + W - 1) / W, first = wave * run;
+    const int64_t last = first + run < steps ? first + run : steps;
+    i32x4 bv[U][NT];
+    int bsc[U][NT];
+    auto load_b = [&](int64_t k0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t k = k0 + u < last ? k0 + u : last - 1;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                bv[u][j] = *reinterpret_cast<const i32x4*>(bp[j] + k * (kPad / 2));
+                bsc[u][j] = *reinterpret_cast<const int*>(bsp[j] + k * (kPad / kBlock));
+            }
+        }
+    };
+    if (first < last) load_b(first);
+    // the left fragments' source: row, or the last one
+    const int ar = r < rows ? r : rows - 1;
+    const uint8_t *ap, *asp;
+    uint8_t* tail = lds;
+    if constexpr (kValues) {
+        // codes of the rows, 16 bytes more apart than they are long, then scales
+        const int pitch = static_cast<int>(row_steps) * (kPad / 2) + 16, spitch = static_cast<int>(row_steps) * 4 + 4;
+        using Elem = typename Type<XT>::Elem;
+        const Elem* x = static_cast<const Elem*>(p.x) + row0 * p.x_stride;
+        const int units = steps ? rows * static_cast<int>(row_steps) : 0, sub = t & 15;
+        uint8_t* const sc = lds + p.few_rows * pitch;
+        for (int u = t >> 4; u < units; u += 4 * W) {
+            const int row = u / static_cast<int>(row_steps), step = u - row * static_cast<int>(row_steps);
+            const int64_t col = static_cast<int64_t>(step) * kPad + sub * 8, left = p.k - col;
+            Octet<XT> v;
+            v.load(x + row * p.x_stride + col, left < 0 ? 0 : (left > 8 ? 8 : static_cast<int>(left)), p.x_wide);
+            const uint32_t s = scale_code(exponent_of<XT>(quad_max(v.top())));
+            *reinterpret_cast<uint32_t*>(lds + row * pitch + step * (kPad / 2) + sub * 4) =
+                s == kScaleNaN ? 0u : v.codes(scale_operand(s));
+            if ((sub & 3) == 0) sc[row * spitch + step * 4 + (sub >> 2)] = static_cast<uint8_t>(s);
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        block_barrier();
+        ap = lds + ar * pitch + g * 16;
+        asp = sc + ar * spitch + g;
+        tail = sc + (p.few_rows * spitch + 15) / 16 * 16;
+    } else {
+        ap = p.a + (row0 + ar) * row_steps * (kPad / 2) + g * 16;
+        asp = p.as + (row0 + ar) * row_steps * (kPad / kBlock) + g;
+    }
+    f32x4 acc[1][NT] = {};
+    for (int64_t k0 = first; k0 < last; k0 += U) {
+        if (k0 > first) load_b(k0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (k0 + u >= last) break;
+            const int64_t k = k0 + u;
+            const i32x4 av = *reinterpret_cast<const i32x4*>(ap + k * (kPad / 2));
+            const int as = asp[k * (kPad / kBlock)];
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                acc[0][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(bv[u][j]), widen(av), acc[0][j], 4, 4,
+                                                                            0, bsc[u][j] >> (8 * g), 0, as);
+        }
+    }
+    join_and_store<1, NT, W>(p, reinterpret_cast<f32x4(*)[NT][kWave]>(tail), acc, wave, 0, row0, rows, n0);
+}
+
+// Few tiles: 16 MT x 16 NT results a block, k-steps dealt to its W waves in
+// contiguous runs, fragments loaded straight to registers, U steps at a time.
+template <int G, int MT, int NT, int W, int U>
+__global__ __launch_bounds__(kWave * W) void k_matmul_split(MatmulArgs p)
+{
+    __shared__ f32x4 part[W][MT * NT][kWave];
+    const int t = static_cast<int>(threadIdx.x), lane = t & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const uint32_t unit = blockIdx.x / static_cast<uint32_t>(p.n_tiles);
+    const uint32_t ntile = blockIdx.x - unit * static_cast<uint32_t>(p.n_tiles);
+    int64_t row0 = static_cast<int64_t>(unit) * (16 * MT), mrows = p.m - row0;
+    int64_t step0 = 0, steps = p.steps, out0 = 0;
+    const uint8_t *b = p.b, *bs = p.bs;
+    if constexpr (G == kByRows) {
+        const Place at = Groups(p.offsets, p.groups, p.rows, 16 * MT).locate(unit);
+        row0 = at.row;
+        mrows = at.rows;
+        if (mrows <= 0) return;
+        if (at.group < 0) {
+            if (!p.zero_rest) return;
+            steps = 0;   // rows of no group: the sum over nothing
+        } else {
+            b += static_cast<int64_t>(at.group) * p.n * p.steps * (kPad / 2);
+            bs += static_cast<int64_t>(at.group) * p.n * p.steps * (kPad / kBlock);
+        }
+    }
+    if constexpr (G == kByContraction) {
+        uint32_t before, own;
+        Groups(p.offsets, p.groups, p.rows, kPad).span(static_cast<int32_t>(blockIdx.y), &before, &own);
+        step0 = before;
+        steps = own;
+        if (step0 > p.steps) step0 = p.steps;
+        if (steps > p.steps - step0) steps = p.steps - step0;
+        out0 = static_cast<int64_t>(blockIdx.y) * p.m * p.out_stride;
+    }
+    const int64_t n0 = static_cast<int64_t>(ntile) * (16 * NT);
+    const uint8_t *ap[MT], *asp[MT], *bp[NT], *bsp[NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        int64_t m = 16 * i + r;              // rows behind the edge read the last one
+        m = row0 + (m < mrows ? m : mrows - 1);
+        ap[i] = p.a + (m * p.steps + step0) * (kPad / 2) + g * 16;
+        asp[i] = p.as + (m * p.steps + step0) * (kPad / kBlock);
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        int64_t n = n0 + 16 * j + r;
+        n = n < p.n ? n : p.n - 1;
+        bp[j] = b + (n * p.steps + step0) * (kPad / 2) + g * 16;
+        bsp[j] = bs + (n * p.steps + step0) * (kPad / kBlock);
+    }
+    f32x4 acc[MT][NT] = {};
+    const int64_t run = (steps + W - 1) / W, first = wave * run;
+    const int64_t last = first + run < steps ? first + run : steps;
+    for (int64_t k0 = first; k0 < last; k0 += U) {
+        i32x4 av[U][MT], bv[U][NT];
+        int as[U][MT], bsc[U][NT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t k = k0 + u < last ? k0 + u : last - 1;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                bv[u][j] = *reinterpret_cast<const i32x4*>(bp[j] + k * (kPad / 2));
+                bsc[u][j] = *reinterpret_cast<const int*>(bsp[j] + k * (kPad / kBlock));
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                av[u][i] = *reinterpret_cast<const i32x4*>(ap[i] + k * (kPad / 2));
+                as[u][i] = *reinterpret_cast<const int*>(asp[i] + k * (kPad / kBlock));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (k0 + u >= last) break;
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        widen(bv[u][j]), widen(av[u][i]), acc[i][j], 4, 4, 0, bsc[u][j] >> (8 * g), 0, as[u][i] >> (8 * g));
+        }
+    }
+    join_and_store<MT, NT, W>(p, part, acc, wave, out0, row0, mrows, n0);
 }
 
 // ---- products, tiled through LDS ------------------------------------------
@@ -658,14 +784,6 @@ __device__ __forceinline__ void multiply_add(f32x4& acc, i32x4 b, i32x4 a, int s
                  : "v"(b), "v"(a), "v"(sb), "v"(sa));
 }
 __device__ __forceinline__ void settle_products() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
-
-// The block's barrier alone; no LDS access moves across it.
-__device__ __forceinline__ void block_barrier()
-{
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const uint8_t* p, uint32_t bytes)
 {
@@ -712,29 +830,31 @@ __global__ __launch_bounds__(256, 1) void k_matmul_tile(MatmulArgs p)
     int64_t row0, mrows, step0 = 0, steps = p.steps, out0 = 0;
     const uint8_t *b = p.b, *bs = p.bs;
     if constexpr (G == kByRows) {
-        const Place end = locate(p.offsets, p.groups, p.rows, BM, INT64_MAX);
-        int64_t units = end.first + (p.zero_rest ? end.units : 0);
-        if (units > p.units) units = p.units;   // offsets that overlap
-        if (static_cast<int64_t>(blockIdx.x) >= units * p.n_tiles) return;
-        tile_of(blockIdx.x, static_cast<uint32_t>(units), static_cast<uint32_t>(p.n_tiles), &unit, &ntile);
-        const Place at = locate(p.offsets, p.groups, p.rows, BM, unit);
+        Groups groups(p.offsets, p.groups, p.rows, BM);
+        uint32_t units = groups.total();
+        if (p.zero_rest) units = Groups::add(units, groups.rest());
+        if (units > p.units) units = static_cast<uint32_t>(p.units);   // offsets that overlap
+        if (static_cast<int64_t>(blockIdx.x) >= static_cast<int64_t>(units) * p.n_tiles) return;
+        tile_of(blockIdx.x, units, static_cast<uint32_t>(p.n_tiles), &unit, &ntile);
+        const Place at = groups.locate(unit);
         row0 = at.row;
         mrows = at.rows;
         if (mrows <= 0) return;
         if (at.group < 0) {
             steps = 0;   // rows of no group: the sum over nothing
         } else {
-            b += at.group * p.n * p.steps * (kPad / 2);
-            bs += at.group * p.n * p.steps * (kPad / kBlock);
+            b += static_cast<int64_t>(at.group) * p.n * p.steps * (kPad / 2);
+            bs += static_cast<int64_t>(at.group) * p.n * p.steps * (kPad / kBlock);
         }
     } else {
         tile_of(blockIdx.x, static_cast<uint32_t>(p.units), static_cast<uint32_t>(p.n_tiles), &unit, &ntile);
         row0 = static_cast<int64_t>(unit) * BM;
         mrows = p.m - row0;
         if constexpr (G == kByContraction) {
-            const Place at = units_of(p.offsets, p.rows, kPad, static_cast<int32_t>(blockIdx.y));
-            step0 = at.first;
-            steps = at.units;
+            uint32_t before, own;
+            Groups(p.offsets, p.groups, p.rows, kPad).span(static_cast<int32_t>(blockIdx.y), &before, &own);
+            step0 = before;
+            steps = own;
             if (step0 > p.steps) step0 = p.steps;
             if (steps > p.steps - step0) steps = p.steps - step0;
             out0 = static_cast<int64_t>(blockIdx.y) * p.m * p.out_stride;
@@ -994,37 +1114,31 @@ const void* matmul_tile_kernel(int out_dtype, int grouping, int tile)
 }
 
 template <int XT, int G>
-SplitKernel split_of(int rows, int cols)
+SplitKernel few_of(int cols)
 {
-#define MX4_SPLIT(MT, NT, W, U) \
-    SplitKernel{reinterpret_cast<const void*>(&k_matmul_split<XT, G, MT, NT, W, U>), 16 * MT, 16 * NT, W}
-    if constexpr (G != kByContraction) {
-        if (rows == 16) return cols == 16 ? MX4_SPLIT(1, 1, 8, 4) : MX4_SPLIT(1, 4, 8, 2);
-    }
-    if constexpr (XT == kHeld) {
-        if (rows == 32) return MX4_SPLIT(2, 2, 8, 2);
-        return MX4_SPLIT(4, 4, 8, 1);
-    }
-#undef MX4_SPLIT
-    return SplitKernel{nullptr, 0, 0, 0};
+    if (cols == 16) return {reinterpret_cast<const void*>(&k_matmul_few<XT, G, 1, 8, 4>), 16, 16, 8};
+    return {reinterpret_cast<const void*>(&k_matmul_few<XT, G, 4, 4, 2>), 16, 64, 4};
 }
 
 template <int G>
-SplitKernel split_any(int x_dtype, int rows, int cols)
+SplitKernel split_of(int x_dtype, int rows, int cols)
 {
     if constexpr (G != kByContraction) {
-        if (x_dtype == kF32) return split_of<kF32, G>(rows, cols);
-        if (x_dtype == kF16) return split_of<kF16, G>(rows, cols);
-        if (x_dtype == kBF16) return split_of<kBF16, G>(rows, cols);
+        if (rows == 16)
+            return x_dtype == kF32    ? few_of<kF32, G>(cols)
+                   : x_dtype == kF16  ? few_of<kF16, G>(cols)
+                   : x_dtype == kBF16 ? few_of<kBF16, G>(cols)
+                                      : few_of<kHeld, G>(cols);
     }
-    return split_of<kHeld, G>(rows, cols);
+    if (rows == 32) return {reinterpret_cast<const void*>(&k_matmul_split<G, 2, 2, 8, 2>), 32, 32, 8};
+    return {reinterpret_cast<const void*>(&k_matmul_split<G, 4, 4, 8, 1>), 64, 64, 8};
 }
 
 SplitKernel matmul_split_kernel(int x_dtype, int grouping, int rows, int cols)
 {
-    return grouping == kPlain    ? split_any<kPlain>(x_dtype, rows, cols)
-           : grouping == kByRows ? split_any<kByRows>(x_dtype, rows, cols)
-                                 : split_any<kByContraction>(x_dtype, rows, cols);
+    return grouping == kPlain    ? split_of<kPlain>(x_dtype, rows, cols)
+           : grouping == kByRows ? split_of<kByRows>(x_dtype, rows, cols)
+                                 : split_of<kByContraction>(x_dtype, rows, cols);
 }
 
 }  // namespace mx4
