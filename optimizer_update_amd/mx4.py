@@ -21,11 +21,13 @@ gradients.
 from __future__ import annotations
 
 import ctypes
+import functools
+import math
 import os
 
 import torch
 
-from . import _lib
+from . import DTYPES, _GET_DEVICE, _lib, _raw_stream
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIBRARY = os.path.join(HERE, "liboptimizer_mx4.so")
@@ -33,7 +35,6 @@ HEADER = os.path.join(os.path.dirname(HERE), "include", "optimizer_mx4.h")
 
 MX4_BLOCK = 32     # values that share a scale
 MX4_PAD = 128      # columns of a held matrix are padded to this
-_DTYPES = {torch.float32: _lib.OU_F32, torch.float16: _lib.OU_F16, torch.bfloat16: _lib.OU_BF16}
 _mx4 = None
 
 
@@ -69,9 +70,8 @@ def load_mx4(path: str = LIBRARY) -> ctypes.CDLL:
     return lib
 
 
-def _check(status: int, lib) -> None:
-    if status:
-        raise _lib.OptimizerUpdateError(status, lib.ou_mx4_last_error().decode(errors="replace"))
+def _fail(status: int) -> None:
+    raise _lib.OptimizerUpdateError(status, load_mx4().ou_mx4_last_error().decode(errors="replace"))
 
 
 def _columns(k: int) -> int:
@@ -129,45 +129,44 @@ def _empty(lead, k, device) -> Mx4:
 
 
 class _Call:
-    """The device and the stream of a call: makes both current (what is
-    allocated inside belongs to that stream) and holds the handle."""
+    """Makes a device, or a given stream of it, current for a call: what is
+    allocated inside belongs to that stream; ``handle`` is the stream's."""
 
-    __slots__ = ("index", "stream", "handle", "_ctx")
+    __slots__ = ("handle", "_ctx")
 
-    def __init__(self, t: torch.Tensor, stream):
-        index = t.get_device()
-        if index < 0:
-            raise ValueError("operands must be tensors on a HIP device")
-        self.index = index
-        self.stream = stream
-        self._ctx = None
-
-    def __enter__(self) -> "_Call":
-        s = self.stream
-        if s is not None:
-            if not isinstance(s, torch.cuda.Stream):
-                s = torch.cuda.ExternalStream(int(s), device=torch.device("cuda", self.index))
-            self._ctx = torch.cuda.stream(s)
-            self._ctx.__enter__()
-            self.handle = s.cuda_stream
+    def __init__(self, index: int, stream):
+        if stream is None:
+            self._ctx = torch.cuda.device(index)
         else:
-            if torch.cuda.current_device() != self.index:
-                self._ctx = torch.cuda.device(self.index)
-                self._ctx.__enter__()
-            self.handle = torch._C._cuda_getCurrentRawStream(self.index)
-        return self
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=torch.device("cuda", index))
+            self._ctx = torch.cuda.stream(stream)
+            self.handle = stream.cuda_stream
+        if stream is None:
+            self.handle = _raw_stream(index)
+
+    def __enter__(self) -> int:
+        self._ctx.__enter__()
+        return self.handle
 
     def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
-        return False
+        return self._ctx.__exit__(*exc)
+
+
+def _run(index: int, stream, fn, *args):
+    """fn(*args, stream handle) on device `index`, switching to it (or to the
+    stream) only when it is not the current one."""
+    if stream is None and _GET_DEVICE() == index:
+        return fn(*args, _raw_stream(index))
+    with _Call(index, stream) as handle:
+        return fn(*args, handle)
 
 
 def _values(x, name: str, dims: int | None = None) -> int:
     """dtype code of a tensor of values."""
     if not isinstance(x, torch.Tensor) or x.get_device() < 0:
         raise ValueError(f"{name} must be a tensor on a HIP device")
-    dt = _DTYPES.get(x.dtype)
+    dt = DTYPES.get(x.dtype)
     if dt is None:
         raise ValueError(f"{name} must be float32, float16 or bfloat16")
     if dims is not None and x.dim() != dims:
@@ -175,55 +174,92 @@ def _values(x, name: str, dims: int | None = None) -> int:
     return dt
 
 
-def _same_device(first, **others) -> None:
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, the first operand on {first.device}")
+def _result_type(dtype) -> int:
+    dt = DTYPES.get(dtype)
+    if dt is None:
+        raise ValueError("dtype must be float32, float16 or bfloat16")
+    return dt
+
+
+def _held_on(q, name: str, dims: int | None = None) -> int:
+    """Device index of an Mx4."""
+    if not isinstance(q, Mx4) or dims is not None and q.codes.dim() != dims:
+        raise ValueError(f"{name} must be an Mx4" + ("" if dims is None else
+                                                     " matrix" if dims == 2 else " batch of matrices"))
+    index = q.codes.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be on a HIP device")
+    return index
+
+
+def _same(index: int, other: int, name: str) -> None:
+    if index != other:
+        raise ValueError(f"{name} is on another device than the first operand")
 
 
 def _row_stride(x: torch.Tensor, name: str) -> int:
     """Elements between the rows of x [R, C], its columns being neighbours."""
     r, c = x.shape
-    if c > 1 and x.stride(1) != 1 or r > 1 and x.stride(0) < c:
+    if x.is_contiguous():
+        return c
+    rs, cs = x.stride()
+    if c > 1 and cs != 1 or r > 1 and rs < c:
         raise ValueError(f"the last axis of {name} must be contiguous and its rows apart")
-    return x.stride(0) if r > 1 else c
+    return rs if r > 1 else c
 
 
-def _offsets(offsets, like) -> int:
+def _offsets(offsets, index: int) -> int:
     """Groups of an offsets tensor."""
     if not isinstance(offsets, torch.Tensor) or offsets.dtype != torch.int32 or offsets.dim() != 1 \
             or offsets.shape[0] < 1 or not offsets.is_contiguous():
         raise ValueError("offsets must be a contiguous int32 tensor of groups + 1 values")
-    _same_device(like, offsets=offsets)
+    _same(index, offsets.get_device(), "offsets")
     return offsets.shape[0] - 1
+
+
+# The workspaces' sizes are the library's to say, and go by sizes alone.
+@functools.lru_cache(maxsize=4096)
+def _matmul_workspace(m: int, n: int, k: int, values: bool) -> int:
+    return int(load_mx4().ou_mx4_matmul_workspace_bytes(m, n, k, values))
+
+
+@functools.lru_cache(maxsize=4096)
+def _grouped_workspace(m: int, n: int, k: int, groups: int, values: bool) -> int:
+    return int(load_mx4().ou_mx4_grouped_workspace_bytes(m, n, k, groups, values))
+
+
+@functools.lru_cache(maxsize=4096)
+def _grouped_columns(rows: int, groups: int) -> int:
+    return int(load_mx4().ou_mx4_grouped_columns(rows, groups))
+
+
+def _ptrs(q: Mx4 | None) -> tuple:
+    return (None, None) if q is None else (q.codes.data_ptr(), q.scales.data_ptr())
+
+
+def _do_quantize(x, dt, lead, batch, r, c, rs, bs, rows, transposed, handle):
+    q = _empty((*lead, r), c, x.device) if rows else None
+    qt = _empty((*lead, c), r, x.device) if transposed else None
+    st = load_mx4().ou_mx4_quantize(dt, x.data_ptr(), batch, r, c, rs, bs, *_ptrs(q), *_ptrs(qt), handle)
+    if st:
+        _fail(st)
+    return q, qt
 
 
 def _quantize(x: torch.Tensor, rows: bool, transposed: bool, stream) -> tuple[Mx4 | None, Mx4 | None]:
     dt = _values(x, "x")
     if x.dim() < 2:
         raise ValueError("x must have two axes at least")
-    r, c = x.shape[-2], x.shape[-1]
-    lead = x.shape[:-2]
-    if c > 1 and x.stride(-1) != 1 and x.stride(-2) == 1 and x.dim() == 2:
+    *lead, r, c = x.shape
+    if lead:
+        if not x.is_contiguous():
+            raise ValueError("a batch of matrices must be contiguous")
+        return _run(x.get_device(), stream, _do_quantize, x, dt, lead, math.prod(lead), r, c, c, r * c, rows, transposed)
+    if c > 1 and x.stride(1) != 1 and x.stride(0) == 1:
         # a transposed view: its rows are the columns of what lies in memory
         qt, q = _quantize(x.t(), transposed, rows, stream)
         return q, qt
-    batch = lead.numel() if len(lead) else 1
-    if len(lead) == 0:
-        rs, bs = _row_stride(x, "x"), 0
-    else:
-        if not x.is_contiguous():
-            raise ValueError("a batch of matrices must be contiguous")
-        rs, bs = c, r * c
-    lib = load_mx4()
-    with _Call(x, stream) as call:
-        q = _empty((*lead, r), c, x.device) if rows else None
-        qt = _empty((*lead, c), r, x.device) if transposed else None
-        _check(lib.ou_mx4_quantize(dt, x.data_ptr(), batch, r, c, rs, bs,
-                                   q.codes.data_ptr() if rows else None, q.scales.data_ptr() if rows else None,
-                                   qt.codes.data_ptr() if transposed else None,
-                                   qt.scales.data_ptr() if transposed else None, call.handle), lib)
-    return q, qt
+    return _run(x.get_device(), stream, _do_quantize, x, dt, lead, 1, r, c, _row_stride(x, "x"), 0, rows, transposed)
 
 
 def mx4_quantize(x: torch.Tensor, stream=None) -> Mx4:
@@ -239,74 +275,105 @@ def mx4_quantize_both(x: torch.Tensor, stream=None) -> tuple[Mx4, Mx4]:
     return _quantize(x, True, True, stream)
 
 
+def _do_quantize_grouped(x, dt, t, c, rs, offsets, groups, rows, handle):
+    q = _empty((t,), c, x.device) if rows else None
+    qt = _empty((c,), _grouped_columns(t, groups), x.device)
+    st = load_mx4().ou_mx4_quantize_grouped(dt, x.data_ptr(), t, c, rs, offsets.data_ptr(), groups, *_ptrs(q),
+                                            *_ptrs(qt), handle)
+    if st:
+        _fail(st)
+    return q, qt
+
+
 def mx4_quantize_grouped(x: torch.Tensor, offsets: torch.Tensor, rows: bool = True,
                          stream=None) -> tuple[Mx4 | None, Mx4]:
     """x [T, C] along its columns (None with rows=False) and, group by group,
     along its rows: group e is rows offsets[e]:offsets[e + 1] (int32, on the
     device), a matrix of its own padded to 128 rows (``ou_mx4_quantize_grouped``).
-    The operands of ``mx4_grouped_outer``."""
+    Rows of no group are not quantised.  The operands of ``mx4_grouped_outer``."""
     dt = _values(x, "x", 2)
-    groups = _offsets(offsets, x)
+    index = x.get_device()
+    groups = _offsets(offsets, index)
     t, c = x.shape
-    rs = _row_stride(x, "x")
-    lib = load_mx4()
-    p = int(lib.ou_mx4_grouped_columns(t, groups))
-    with _Call(x, stream) as call:
-        q = _empty((t,), c, x.device) if rows else None
-        qt = _empty((c,), p, x.device)
-        _check(lib.ou_mx4_quantize_grouped(dt, x.data_ptr(), t, c, rs, offsets.data_ptr(), groups,
-                                           q.codes.data_ptr() if rows else None,
-                                           q.scales.data_ptr() if rows else None,
-                                           qt.codes.data_ptr(), qt.scales.data_ptr(), call.handle), lib)
-    return q, qt
+    return _run(index, stream, _do_quantize_grouped, x, dt, t, c, _row_stride(x, "x"), offsets, groups, rows)
+
+
+def _do_dequantize(q, dtype, dt, out, handle):
+    if out is None:
+        out = torch.empty(q.shape, dtype=dtype, device=q.codes.device)
+    rows = out.numel() // q.k if q.k else 0
+    st = load_mx4().ou_mx4_dequantize(dt, q.codes.data_ptr(), q.scales.data_ptr(), rows, q.k, out.data_ptr(), q.k,
+                                      handle)
+    if st:
+        _fail(st)
+    return out
 
 
 def mx4_dequantize(q: Mx4, dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None,
                    stream=None) -> torch.Tensor:
     """The values that q holds, in ``dtype`` (or in ``out``, contiguous)."""
-    if not isinstance(q, Mx4):
-        raise ValueError("q must be an Mx4")
-    lib = load_mx4()
-    with _Call(q.codes, stream) as call:
-        if out is None:
-            if dtype not in _DTYPES:
-                raise ValueError("dtype must be float32, float16 or bfloat16")
-            out = torch.empty(q.shape, dtype=dtype, device=q.device)
-        else:
-            _values(out, "out")
-            _same_device(q, out=out)
-            if out.shape != q.shape or not out.is_contiguous():
-                raise ValueError(f"out must be contiguous, of shape {list(q.shape)}")
-        rows = out.numel() // q.k if q.k else 0
-        _check(lib.ou_mx4_dequantize(_DTYPES[out.dtype], q.codes.data_ptr(), q.scales.data_ptr(), rows, q.k,
-                                     out.data_ptr(), q.k, call.handle), lib)
-    return out
-
-
-def _output(out, rows: int, n: int, dtype, like) -> tuple[torch.Tensor, int]:
+    index = _held_on(q, "q")
     if out is None:
-        if dtype not in _DTYPES:
-            raise ValueError("dtype must be float32, float16 or bfloat16")
-        return torch.empty((rows, n), dtype=dtype, device=like.device), n
-    _values(out, "out", 2)
-    _same_device(like, out=out)
+        dt = _result_type(dtype)
+    else:
+        dt = _values(out, "out")
+        _same(index, out.get_device(), "out")
+        if out.shape != q.shape or not out.is_contiguous():
+            raise ValueError(f"out must be contiguous, of shape {list(q.shape)}")
+    return _run(index, stream, _do_dequantize, q, dtype, dt, out)
+
+
+def _output(out, rows: int, n: int, dtype, index: int) -> tuple[int, int]:
+    """dtype code and row stride of a result, given or to be made."""
+    if out is None:
+        return _result_type(dtype), n
+    dt = _values(out, "out", 2)
+    _same(index, out.get_device(), "out")
     if tuple(out.shape) != (rows, n):
         raise ValueError(f"out must have shape [{rows}, {n}], got {list(out.shape)}")
-    return out, _row_stride(out, "out")
+    return dt, _row_stride(out, "out")
 
 
-def _left(a, k: int) -> tuple[bool, int, torch.dtype, torch.Tensor]:
-    """(given as values, rows, default dtype of a result, a tensor of it)."""
+def _left(a, k: int) -> tuple[bool, int, torch.dtype, int, int, int]:
+    """(given as values, device index, default dtype of a result, rows, dtype
+    code, row stride) of a left operand."""
     if isinstance(a, Mx4):
-        if a.codes.dim() != 2:
-            raise ValueError("the left operand must be a matrix")
-        if a.k != k:
-            raise ValueError(f"the operands contract {a.k} and {k} columns")
-        return False, a.codes.shape[0], torch.bfloat16, a.codes
-    _values(a, "the left operand", 2)
-    if a.shape[1] != k:
-        raise ValueError(f"the operands contract {a.shape[1]} and {k} columns")
-    return True, a.shape[0], a.dtype, a
+        index = _held_on(a, "the left operand", 2)
+        m, have, values, dtype, dt, rs = a.codes.shape[0], a.k, False, torch.bfloat16, 0, 0
+    else:
+        dt = _values(a, "the left operand", 2)
+        m, have = a.shape
+        index, values, dtype, rs = a.get_device(), True, a.dtype, _row_stride(a, "the left operand")
+    if have != k:
+        raise ValueError(f"the operands contract {have} and {k} columns")
+    return values, index, dtype, m, dt, rs
+
+
+def _do_matmul(a, values, dt, rs, m, b, n, k, dtype, od, out, stride, offsets, groups, handle):
+    """Both products: grouped with offsets."""
+    lib = load_mx4()
+    device = b.codes.device
+    zero_rest = out is None
+    if out is None:
+        out = torch.empty((m, n), dtype=dtype, device=device)
+    need = (_matmul_workspace(m, n, k, values) if offsets is None else _grouped_workspace(m, n, k, groups, values))
+    ws = torch.empty(need, dtype=torch.uint8, device=device) if need > 0 else None
+    tail = (ws.data_ptr() if ws is not None else None, need, handle)
+    right = (b.codes.data_ptr(), b.scales.data_ptr(), n, k)
+    if offsets is None:
+        if values:
+            st = lib.ou_mx4_matmul_values(dt, a.data_ptr(), m, rs, od, *right, out.data_ptr(), stride, *tail)
+        else:
+            st = lib.ou_mx4_matmul(od, a.codes.data_ptr(), a.scales.data_ptr(), m, *right, out.data_ptr(), stride, *tail)
+    else:
+        by = (offsets.data_ptr(), groups, out.data_ptr(), stride, zero_rest)
+        if values:
+            st = lib.ou_mx4_grouped_matmul_values(dt, a.data_ptr(), m, rs, od, *right, *by, *tail)
+        else:
+            st = lib.ou_mx4_grouped_matmul(od, a.codes.data_ptr(), a.scales.data_ptr(), m, *right, *by, *tail)
+    if st:
+        _fail(st)
+    return out
 
 
 def mx4_matmul(a, b: Mx4, dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
@@ -314,27 +381,13 @@ def mx4_matmul(a, b: Mx4, dtype: torch.dtype | None = None, out: torch.Tensor | 
     """a b^T: a [M, K] as values (quantised along K on the way, in the same
     call) or as Mx4, b an Mx4 [N, K].  The result is [M, N] of ``dtype``
     (default: a's, bfloat16 for an Mx4), or ``out`` (any row stride)."""
-    if not isinstance(b, Mx4) or b.codes.dim() != 2:
-        raise ValueError("b must be an Mx4 matrix")
-    values, m, default, at = _left(a, b.k)
-    _same_device(at, b=b)
+    on = _held_on(b, "b", 2)
     n, k = b.codes.shape[0], b.k
-    lib = load_mx4()
-    with _Call(at, stream) as call:
-        out, stride = _output(out, m, n, dtype or default, at)
-        need = lib.ou_mx4_matmul_workspace_bytes(m, n, k, int(values))
-        ws = torch.empty(need, dtype=torch.uint8, device=at.device) if need > 0 else None
-        wp = ws.data_ptr() if ws is not None else None
-        if values:
-            st = lib.ou_mx4_matmul_values(_DTYPES[a.dtype], a.data_ptr(), m, _row_stride(a, "a"), _DTYPES[out.dtype],
-                                          b.codes.data_ptr(), b.scales.data_ptr(), n, k, out.data_ptr(), stride, wp,
-                                          need, call.handle)
-        else:
-            st = lib.ou_mx4_matmul(_DTYPES[out.dtype], a.codes.data_ptr(), a.scales.data_ptr(), m,
-                                   b.codes.data_ptr(), b.scales.data_ptr(), n, k, out.data_ptr(), stride, wp, need,
-                                   call.handle)
-        _check(st, lib)
-    return out
+    values, index, default, m, dt, rs = _left(a, k)
+    _same(index, on, "b")
+    dtype = dtype or default
+    od, stride = _output(out, m, n, dtype, index)
+    return _run(index, stream, _do_matmul, a, values, dt, rs, m, b, n, k, dtype, od, out, stride, None, 0)
 
 
 def mx4_grouped_matmul(a, b: Mx4, offsets: torch.Tensor, dtype: torch.dtype | None = None,
@@ -343,31 +396,25 @@ def mx4_grouped_matmul(a, b: Mx4, offsets: torch.Tensor, dtype: torch.dtype | No
     times matrix e of b [E, N, K], transposed.  ``offsets``: E + 1 rising int32
     on the device, read there.  Rows of no group are 0 in a new result and left
     as they were in ``out``."""
-    if not isinstance(b, Mx4) or b.codes.dim() != 3:
-        raise ValueError("b must be an Mx4 batch [groups, N, K]")
-    values, m, default, at = _left(a, b.k)
-    _same_device(at, b=b)
-    groups = _offsets(offsets, at)
-    e, n, k = *b.codes.shape[:2], b.k
+    on = _held_on(b, "b", 3)
+    (e, n), k = b.codes.shape[:2], b.k
+    values, index, default, m, dt, rs = _left(a, k)
+    _same(index, on, "b")
+    groups = _offsets(offsets, index)
     if groups != e:
         raise ValueError(f"offsets name {groups} groups, b holds {e}")
-    lib = load_mx4()
-    zero_rest = int(out is None)
-    with _Call(at, stream) as call:
-        out, stride = _output(out, m, n, dtype or default, at)
-        need = lib.ou_mx4_grouped_workspace_bytes(m, n, k, groups, int(values))
-        ws = torch.empty(need, dtype=torch.uint8, device=at.device) if need > 0 else None
-        wp = ws.data_ptr() if ws is not None else None
-        if values:
-            st = lib.ou_mx4_grouped_matmul_values(_DTYPES[a.dtype], a.data_ptr(), m, _row_stride(a, "a"),
-                                                  _DTYPES[out.dtype], b.codes.data_ptr(), b.scales.data_ptr(), n, k,
-                                                  offsets.data_ptr(), groups, out.data_ptr(), stride, zero_rest, wp,
-                                                  need, call.handle)
-        else:
-            st = lib.ou_mx4_grouped_matmul(_DTYPES[out.dtype], a.codes.data_ptr(), a.scales.data_ptr(), m,
-                                           b.codes.data_ptr(), b.scales.data_ptr(), n, k, offsets.data_ptr(), groups,
-                                           out.data_ptr(), stride, zero_rest, wp, need, call.handle)
-        _check(st, lib)
+    dtype = dtype or default
+    od, stride = _output(out, m, n, dtype, index)
+    return _run(index, stream, _do_matmul, a, values, dt, rs, m, b, n, k, dtype, od, out, stride, offsets, groups)
+
+
+def _do_outer(at, bt, offsets, groups, rows, dtype, dt, handle):
+    m, n = at.codes.shape[0], bt.codes.shape[0]
+    out = torch.empty((groups, m, n), dtype=dtype, device=at.codes.device)
+    st = load_mx4().ou_mx4_grouped_outer(dt, *_ptrs(at), m, *_ptrs(bt), n, rows, offsets.data_ptr(), groups,
+                                         out.data_ptr(), handle)
+    if st:
+        _fail(st)
     return out
 
 
@@ -376,24 +423,14 @@ def mx4_grouped_outer(at: Mx4, bt: Mx4, offsets: torch.Tensor, rows: int, dtype:
     """[E, M, N]: for every group the sum over its rows of a's row times b's,
     from the transposed forms [M, *] and [N, *] that ``mx4_quantize_grouped``
     made of matrices of ``rows`` rows with the same offsets."""
-    for name, q in (("at", at), ("bt", bt)):
-        if not isinstance(q, Mx4) or q.codes.dim() != 2:
-            raise ValueError(f"{name} must be an Mx4 matrix")
-    if dtype not in _DTYPES:
-        raise ValueError("dtype must be float32, float16 or bfloat16")
-    _same_device(at, bt=bt)
-    groups = _offsets(offsets, at)
-    lib = load_mx4()
-    p = int(lib.ou_mx4_grouped_columns(rows, groups))
+    index = _held_on(at, "at", 2)
+    _same(index, _held_on(bt, "bt", 2), "bt")
+    dt = _result_type(dtype)
+    groups = _offsets(offsets, index)
+    p = _grouped_columns(rows, groups)
     if at.k != p or bt.k != p:
         raise ValueError(f"{rows} rows in {groups} groups are held in {p} columns: got {at.k} and {bt.k}")
-    m, n = at.codes.shape[0], bt.codes.shape[0]
-    with _Call(at.codes, stream) as call:
-        out = torch.empty((groups, m, n), dtype=dtype, device=at.device)
-        _check(lib.ou_mx4_grouped_outer(_DTYPES[dtype], at.codes.data_ptr(), at.scales.data_ptr(), m,
-                                        bt.codes.data_ptr(), bt.scales.data_ptr(), n, rows, offsets.data_ptr(),
-                                        groups, out.data_ptr(), call.handle), lib)
-    return out
+    return _run(index, stream, _do_outer, at, bt, offsets, groups, rows, dtype, dt)
 
 
 # ------------------------------------------------------------------ layers
@@ -415,16 +452,18 @@ class Mx4Weight:
 
     def refresh(self, stream=None) -> None:
         """Quantise the weight's present values into the same buffers."""
-        w, q, qt = self.weight.detach(), self.q, self.qt
+        w = self.weight.detach()
         dt = _values(w, "weight")
-        r, c = w.shape[-2:]
-        if w.shape != q.shape or not w.is_contiguous():
+        if w.shape != self.q.shape or not w.is_contiguous():
             raise ValueError("the weight changed its shape or layout")
-        lib = load_mx4()
-        with _Call(w, stream) as call:
-            _check(lib.ou_mx4_quantize(dt, w.data_ptr(), w.shape[0] if w.dim() == 3 else 1, r, c, c, r * c,
-                                       q.codes.data_ptr(), q.scales.data_ptr(), qt.codes.data_ptr(),
-                                       qt.scales.data_ptr(), call.handle), lib)
+        _run(w.get_device(), stream, self._refresh, w, dt)
+
+    def _refresh(self, w, dt, handle):
+        *lead, r, c = w.shape
+        st = load_mx4().ou_mx4_quantize(dt, w.data_ptr(), math.prod(lead), r, c, c, r * c, *_ptrs(self.q),
+                                        *_ptrs(self.qt), handle)
+        if st:
+            _fail(st)
 
 
 class _Linear(torch.autograd.Function):
@@ -498,7 +537,7 @@ def _layer_operands(x, w, dims: int):
     weight = held.weight if held is not None else w
     _values(x, "x")
     _values(weight, "w", dims)
-    _same_device(x, w=weight)
+    _same(x.get_device(), weight.get_device(), "w")
     if not weight.is_contiguous():
         raise ValueError("w must be contiguous")
     if x.dim() < 2 or x.shape[-1] != weight.shape[-1]:
@@ -526,6 +565,6 @@ def mx4_grouped_linear(x: torch.Tensor, w, offsets: torch.Tensor) -> torch.Tenso
     held, weight = _layer_operands(x, w, 3)
     if x.dim() != 2:
         raise ValueError("x must be [T, K]")
-    if _offsets(offsets, x) != weight.shape[0]:
+    if _offsets(offsets, x.get_device()) != weight.shape[0]:
         raise ValueError(f"offsets name {offsets.shape[0] - 1} groups, w holds {weight.shape[0]}")
     return _GroupedLinear.apply(x, weight, offsets, held)
