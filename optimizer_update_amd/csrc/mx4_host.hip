@@ -131,7 +131,8 @@ int launch_quantize(int dtype, QuantArgs& q, int64_t batch, int64_t units, void*
 {
     q.wide = wide_rows(q.x, q.row_stride, batch > 1 ? q.batch_stride : 0, elem_bytes(dtype), 16);
     if (!q.codes_t) {
-        int64_t n = q.rows * (q.pcols / kPad);
+        if (q.rows * (q.pcols / kPad) > UINT32_MAX / 2) return fail(OU_EINVAL, "x is too large");
+        uint32_t n = static_cast<uint32_t>(q.rows * (q.pcols / kPad));
         void* args[] = {&q, &n};
         return launch(quant_rows_kernel(dtype), cut(n, (kQuantThreads / 16) * kQuantUnits), batch, kQuantThreads, args,
                       stream, "k_quant_rows");
@@ -284,10 +285,12 @@ OU_EXPORT int ou_mx4_dequantize(int dtype, const uint8_t* codes, const uint8_t* 
                            {"out", out, extent(rows, cols, row_stride, eb), static_cast<unsigned>(eb), true}};
     if (int st = check_buffers(bufs, 3)) return st;
     if (int st = check_device()) return st;
-    DequantArgs d{codes, scales, out, rows, cols, pad(cols), row_stride, wide_rows(out, row_stride, 0, eb, 4 * eb)};
-    int64_t octets = rows * (pad(cols) / 8);
-    void* args[] = {&d, &octets};
-    return launch(dequant_kernel(dtype), cut(octets, kQuantThreads), 1, kQuantThreads, args, stream, "k_dequant");
+    DequantArgs d{codes, scales, out, rows, cols, pad(cols), row_stride, wide_rows(out, row_stride, 0, eb, 16)};
+    if (rows * (pad(cols) / kPad) > UINT32_MAX / 2) return fail(OU_EINVAL, "the matrix is too large");
+    uint32_t units = static_cast<uint32_t>(rows * (pad(cols) / kPad));
+    void* args[] = {&d, &units};
+    return launch(dequant_kernel(dtype), cut(units, (kQuantThreads / 16) * kQuantUnits), 1, kQuantThreads, args, stream,
+                  "k_dequant");
 }
 
 OU_EXPORT int64_t ou_mx4_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k, int from_values)

@@ -303,13 +303,12 @@ struct Groups {
 // 16 lanes hold one unit of 128 columns of a row, eight values a lane, so a
 // block is a quad.  Lanes keep kQuantUnits units in flight.
 template <int DT>
-__global__ __launch_bounds__(kQuantThreads) void k_quant_rows(QuantArgs q, int64_t units)
+__global__ __launch_bounds__(kQuantThreads) void k_quant_rows(QuantArgs q, uint32_t units)
 {
     using Elem = typename Type<DT>::Elem;
-    const int64_t per_row = q.pcols / kPad;
+    const uint32_t per_row = static_cast<uint32_t>(q.pcols / kPad);
     const int sub = static_cast<int>(threadIdx.x) & 15;
-    const int64_t group = (static_cast<int64_t>(blockIdx.x) * kQuantThreads + threadIdx.x) >> 4;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * (kQuantThreads / 16);
+    const uint32_t first = blockIdx.x * (kQuantThreads / 16 * kQuantUnits) + (threadIdx.x >> 4);
     const int64_t batch = blockIdx.y;
     const Elem* x = static_cast<const Elem*>(q.x) + batch * q.batch_stride;
     uint8_t* codes = q.codes + batch * q.rows * (q.pcols / 2);
@@ -317,23 +316,23 @@ __global__ __launch_bounds__(kQuantThreads) void k_quant_rows(QuantArgs q, int64
     Octet<DT> v[kQuantUnits];
 #pragma unroll
     for (int i = 0; i < kQuantUnits; ++i) {
-        const int64_t u = group + i * stride;
+        const uint32_t u = first + i * (kQuantThreads / 16);
         if (u >= units) {
             v[i].zero();
             continue;
         }
-        const int64_t row = u / per_row, col = (u - row * per_row) * kPad + sub * 8;
-        const int64_t left = q.cols - col;
+        const uint32_t row = u / per_row;
+        const int64_t col = static_cast<int64_t>(u - row * per_row) * kPad + sub * 8, left = q.cols - col;
         v[i].load(x + row * q.row_stride + col, left < 0 ? 0 : (left > 8 ? 8 : static_cast<int>(left)), q.wide);
     }
 #pragma unroll
     for (int i = 0; i < kQuantUnits; ++i) {
-        const int64_t u = group + i * stride;
+        const uint32_t u = first + i * (kQuantThreads / 16);
         const uint32_t s = scale_code(exponent_of<DT>(quad_max(v[i].top())));
         const uint32_t c = s == kScaleNaN ? 0u : v[i].codes(scale_operand(s));
         if (u >= units) continue;
-        *reinterpret_cast<uint32_t*>(codes + u * (kPad / 2) + sub * 4) = c;
-        if ((sub & 3) == 0) scales[u * (kPad / kBlock) + (sub >> 2)] = static_cast<uint8_t>(s);
+        reinterpret_cast<uint32_t*>(codes)[static_cast<int64_t>(u) * 16 + sub] = c;
+        if ((sub & 3) == 0) scales[static_cast<int64_t>(u) * (kPad / kBlock) + (sub >> 2)] = static_cast<uint8_t>(s);
     }
 }
 
@@ -353,17 +352,17 @@ __global__ __launch_bounds__(kQuantThreads) void k_quant_tile(QuantArgs q)
     __shared__ __attribute__((aligned(16))) uint32_t tile[T * kRowWords];
     const int t = static_cast<int>(threadIdx.x);
     const int64_t batch = blockIdx.y;
-    const int64_t col_tiles = q.pcols / T;
-    const int64_t unit = blockIdx.x / col_tiles;        // block of 128 padded rows
-    int64_t row0 = unit * T, nrows = q.rows - row0;
+    const uint32_t col_tiles = static_cast<uint32_t>(q.pcols / T);
+    const uint32_t unit = blockIdx.x / col_tiles;       // block of 128 padded rows
+    int64_t row0 = static_cast<int64_t>(unit) * T, nrows = q.rows - row0;
     if (q.offsets) {
-        const Place p = Groups(q.offsets, q.groups, q.rows, T).locate(static_cast<uint32_t>(unit));
+        const Place p = Groups(q.offsets, q.groups, q.rows, T).locate(unit);
         if (p.group < 0) return;
         row0 = p.row;
         nrows = p.rows;
     }
     if (nrows > T) nrows = T;
-    const int64_t col0 = (blockIdx.x - unit * col_tiles) * T;
+    const int64_t col0 = static_cast<int64_t>(blockIdx.x - unit * col_tiles) * T;
     const Elem* x = static_cast<const Elem*>(q.x) + batch * q.batch_stride;
     const int sub = t & 15;
     const int64_t col = col0 + sub * 8, left = q.cols - col;
@@ -444,15 +443,29 @@ __global__ __launch_bounds__(kQuantThreads) void k_quant_tile(QuantArgs q)
             }
         }
     }
+    // Through LDS, so that a column's 64 bytes of codes and 4 of scales go out
+    // as one piece each (80 bytes a column: no bank is met twice by a quad).
+    __syncthreads();
+    constexpr int kOut = 20;   // words a column
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-        const int64_t cc = col0 + 2 * pair + c;
-        if (cc >= q.cols) continue;
         if (s[c] == kScaleNaN) out[c] = u32x4{0, 0, 0, 0};
-        const int64_t at = (batch * q.cols + cc) * (q.prows / kBlock) + unit * (T / kBlock) + rb;
-        *reinterpret_cast<u32x4*>(q.codes_t + at * (kBlock / 2)) = out[c];
-        q.scales_t[at] = static_cast<uint8_t>(s[c]);
+        uint32_t* to = &tile[(2 * pair + c) * kOut];
+        *reinterpret_cast<u32x4*>(to + 4 * rb) = out[c];
+        reinterpret_cast<uint8_t*>(to + 16)[rb] = static_cast<uint8_t>(s[c]);
     }
+    __syncthreads();
+    const int64_t cols = q.cols - col0 < T ? q.cols - col0 : T;
+    const int64_t at = (batch * q.cols + col0) * (q.prows / kBlock) + static_cast<int64_t>(unit) * (T / kBlock);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int c = i * 64 + (t >> 2);
+        if (c >= cols) continue;
+        *reinterpret_cast<u32x4*>(q.codes_t + (at + c * (q.prows / kBlock)) * (kBlock / 2) + (t & 3) * 16) =
+            *reinterpret_cast<const u32x4*>(&tile[c * kOut + 4 * (t & 3)]);
+    }
+    if (t < cols)
+        *reinterpret_cast<uint32_t*>(q.scales_t + at + t * (q.prows / kBlock)) = tile[t * kOut + 16];
 }
 
 // ---- results in the storage types -----------------------------------------
@@ -495,28 +508,98 @@ __device__ __forceinline__ void store4(void* out, int64_t at, f32x4 v, int n, bo
 
 // ---- dequantisation ---------------------------------------------------------
 
-// Eight values a lane.
+// Two neighbouring codes (byte SEL of c) as values of the type, for scale
+// codes whose values are all normal numbers of it (the converter flushes
+// subnormal results): from 2^-126 and 2^-14 = 0.5 * 2^(s - 127) on, up to
+// 6 * 2^(s - 127) within the type.
 template <int DT>
-__global__ __launch_bounds__(kQuantThreads) void k_dequant(DequantArgs d, int64_t octets)
+struct Normal {
+    static constexpr uint32_t kFirst = DT == kF16 ? 114 : 2, kLast = DT == kF16 ? 140 : 252;
+};
+template <int DT, int SEL>
+__device__ __forceinline__ void values_of(uint32_t c, float scale, uint32_t* out)
 {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kQuantThreads + threadIdx.x;
-    if (i >= octets) return;
-    const int64_t per_row = d.pcols / 8, row = i / per_row, col = (i - row * per_row) * 8;
-    if (col >= d.cols) return;
-    const uint32_t c = reinterpret_cast<const uint32_t*>(d.codes)[i];
-    const uint32_t s = d.scales[i >> 2];
-    const float scale = s == kScaleNaN ? __builtin_nanf("") : __builtin_bit_cast(float, s ? s << 23 : 1u << 22);
-    float v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t k = (c >> (4 * j)) & 15u, e = (k >> 1) & 3u, m = k & 1u;
-        const float mag = e ? __builtin_bit_cast(float, ((e + 126u) << 23) | (m << 22)) : 0.5f * static_cast<float>(m);
-        v[j] = (k & 8u ? -mag : mag) * scale;
+    if constexpr (DT == kF32) {
+        // by way of bfloat16, which holds these values exactly
+        const uint32_t v = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, SEL));
+        out[0] = v << 16;
+        out[1] = v & 0xffff0000u;
+    } else if constexpr (DT == kBF16) {
+        out[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, SEL));
+    } else {
+        out[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, scale, SEL));
     }
-    const int64_t left = d.cols - col;
-    const int n = left > 8 ? 8 : static_cast<int>(left);
-    store4<DT>(d.out, row * d.row_stride + col, f32x4{v[0], v[1], v[2], v[3]}, n, d.wide);
-    if (n > 4) store4<DT>(d.out, row * d.row_stride + col + 4, f32x4{v[4], v[5], v[6], v[7]}, n - 4, d.wide);
+}
+
+// The value of one code under any scale code, in binary32.
+__device__ __forceinline__ float value_of(uint32_t code, uint32_t s)
+{
+    const uint32_t e = (code >> 1) & 3u, m = code & 1u;
+    const float scale = s == kScaleNaN ? __builtin_nanf("") : __builtin_bit_cast(float, s ? s << 23 : 1u << 22);
+    const float mag = e ? __builtin_bit_cast(float, ((e + 126u) << 23) | (m << 22)) : 0.5f * static_cast<float>(m);
+    return (code & 8u ? -mag : mag) * scale;
+}
+
+// As k_quant_rows: 16 lanes a unit of 128 columns, eight values a lane,
+// kQuantUnits units of a lane in flight.
+template <int DT>
+__global__ __launch_bounds__(kQuantThreads) void k_dequant(DequantArgs d, uint32_t units)
+{
+    using Elem = typename Type<DT>::Elem;
+    constexpr int kWords = Type<DT>::kBytes * 2;
+    const uint32_t per_row = static_cast<uint32_t>(d.pcols / kPad);
+    const int sub = static_cast<int>(threadIdx.x) & 15;
+    const uint32_t first = blockIdx.x * (kQuantThreads / 16 * kQuantUnits) + (threadIdx.x >> 4);
+    uint32_t c[kQuantUnits], s[kQuantUnits];
+#pragma unroll
+    for (int i = 0; i < kQuantUnits; ++i) {
+        const uint32_t u = first + i * (kQuantThreads / 16), v = u < units ? u : units - 1;
+        c[i] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(d.codes) + static_cast<int64_t>(v) * 16 + sub);
+        s[i] = d.scales[static_cast<int64_t>(v) * (kPad / kBlock) + (sub >> 2)];
+    }
+#pragma unroll
+    for (int i = 0; i < kQuantUnits; ++i) {
+        const uint32_t u = first + i * (kQuantThreads / 16);
+        if (u >= units) continue;
+        const uint32_t row = u / per_row;
+        const int64_t col = static_cast<int64_t>(u - row * per_row) * kPad + sub * 8, left = d.cols - col;
+        if (left <= 0) continue;
+        uint32_t w[kWords];
+        if (s[i] >= Normal<DT>::kFirst && s[i] <= Normal<DT>::kLast) {
+            const float scale = scale_operand(s[i]);
+            values_of<DT, 0>(c[i], scale, w);
+            values_of<DT, 1>(c[i], scale, w + kWords / 4);
+            values_of<DT, 2>(c[i], scale, w + kWords / 2);
+            values_of<DT, 3>(c[i], scale, w + 3 * kWords / 4);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float a = value_of((c[i] >> (8 * j)) & 15u, s[i]), b = value_of((c[i] >> (8 * j + 4)) & 15u, s[i]);
+                if constexpr (DT == kF32) {
+                    w[2 * j] = __builtin_bit_cast(uint32_t, a);
+                    w[2 * j + 1] = __builtin_bit_cast(uint32_t, b);
+                } else {
+                    w[j] = DT == kBF16 ? bf16_pair(a, b) : f16_pair(a, b);
+                }
+            }
+        }
+        Elem* out = static_cast<Elem*>(d.out) + row * d.row_stride + col;
+        if (left >= 8 && d.wide) {
+#pragma unroll
+            for (int j = 0; j < kWords / 4; ++j)
+                *reinterpret_cast<u32x4*>(reinterpret_cast<uint32_t*>(out) + 4 * j) =
+                    u32x4{w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]};
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (j >= left) continue;
+                if constexpr (DT == kF32)
+                    out[j] = __builtin_bit_cast(float, w[j]);
+                else
+                    out[j] = static_cast<uint16_t>(w[j / 2] >> (16 * (j & 1)));
+            }
+        }
+    }
 }
 
 // ---- products -----------------------------------------------------------------
