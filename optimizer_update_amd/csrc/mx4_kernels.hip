@@ -587,8 +587,8 @@ __global__ __launch_bounds__(kQuantThreads) void k_dequant(DequantArgs d, uint32
         if (left >= 8 && d.wide) {
 #pragma unroll
             for (int j = 0; j < kWords / 4; ++j)
-                *reinterpret_cast<u32x4*>(reinterpret_cast<uint32_t*>(out) + 4 * j) =
-                    u32x4{w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]};
+                __builtin_nontemporal_store(u32x4{w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]},
+                                            reinterpret_cast<u32x4*>(reinterpret_cast<uint32_t*>(out) + 4 * j));
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
