@@ -79,7 +79,7 @@ int ou_mx4_dequantize(int dtype, const uint8_t* codes, const uint8_t* scales, in
                       int64_t cols, void* out, int64_t row_stride, void* stream);
 
 /* out[i][j] = sum over k of a[i][k] * b[j][k]: a holds m rows, b n rows, of k
- * columns.  Sums in binary32 (where the terms'
+ * columns (k at most 2^25).  Sums in binary32 (where the terms'
  * magnitudes sum to more than it holds, a result may be infinite or NaN),
  * rounded once to out_dtype (nearest even).
  * `workspace` is caller-owned device memory of at least
@@ -120,7 +120,8 @@ int ou_mx4_grouped_matmul_values(int x_dtype, const void* x, int64_t rows, int64
  * of a[r][i] * b[r][j], from the transposed forms that
  * ou_mx4_quantize_grouped made with the same rows, offsets and groups: a_t
  * holds m rows, b_t n rows.  out is groups matrices of m x n, one after the
- * other; an empty group's is 0. */
+ * other; an empty group's is 0.  At
+ * most 2^25 columns are held. */
 int ou_mx4_grouped_outer(int out_dtype, const uint8_t* a_codes_t, const uint8_t* a_scales_t, int64_t m,
                          const uint8_t* b_codes_t, const uint8_t* b_scales_t, int64_t n, int64_t rows,
                          const int32_t* offsets, int32_t groups, void* out, void* stream);

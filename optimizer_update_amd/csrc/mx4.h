@@ -60,8 +60,8 @@ struct MatmulArgs {
     int32_t groups;
     int32_t zero_rest;        // grouped by rows: rows of no group become 0
     int32_t wide;             // stores of 4 neighbouring results (tiles 128, 256: of 16 bytes) are aligned
-    int32_t out_dtype;        // k_matmul_split
-    // the left matrix as values (k_matmul_split)
+    int32_t out_dtype;        // k_matmul_few
+    // the left matrix as values (k_matmul_few)
     const void* x;
     int64_t x_stride, k;
     int32_t x_dtype;
@@ -74,25 +74,28 @@ enum Grouping { kPlain = 0, kByRows = 1, kByContraction = 2 };
 const void* quant_rows_kernel(int dtype);
 const void* quant_tile_kernel(int dtype);
 const void* dequant_kernel(int dtype);
-// tile: rows and columns of a block's tile, 128 or 256.
-const void* matmul_tile_kernel(int out_dtype, int grouping, int tile);
-
-// Products of few rows or few tiles: rows x cols results a block of `waves`
-// waves; 16 x 16 and 16 x 64 (k_matmul_few, with few_lds() bytes of dynamic
-// LDS), 32 x 32 and 64 x 64 (k_matmul_split).
-struct SplitKernel {
+// tile: rows and columns of a block's tile, 256, 128 or 64 (its k-steps shared
+// by four groups of waves).
+struct TileKernel {
     const void* fn;
-    int rows, cols, waves;
+    int tile, threads;
+};
+TileKernel matmul_tile_kernel(int out_dtype, int grouping, int tile);
+
+// Products of up to 16 rows (by groups: in units of 16): 16 or 64 columns a
+// block of `waves` waves, with few_lds() bytes of dynamic LDS.
+struct FewKernel {
+    const void* fn;
+    int cols, waves;
 };
 inline int64_t few_lds(int64_t rows, int64_t steps, int cols, int waves)   // rows: 0 for a held left matrix
 {
     return rows * (steps * 64 + 16) + (rows * (steps * 4 + 4) + 15) / 16 * 16 + static_cast<int64_t>(waves) * cols * 64;
 }
-SplitKernel matmul_split_kernel(int x_dtype, int grouping, int rows, int cols);
+FewKernel matmul_few_kernel(int x_dtype, int grouping, int cols);
 
 constexpr int kQuantThreads = 256;
 constexpr int kQuantUnits = 4;      // units of 128 columns per 16 lanes of k_quant_rows
 constexpr int kQuantTile = 128;     // rows and columns of a tile of k_quant_tile
-constexpr int kMatmulThreads = 256;
 
 }  // namespace mx4

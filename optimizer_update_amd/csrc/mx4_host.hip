@@ -51,6 +51,7 @@ int check_device()
 // Largest extent of any axis, and of any product of axes in bytes: every
 // address and count below stays far inside 64 bits.
 constexpr int64_t kMaxAxis = int64_t(1) << 31;
+constexpr int64_t kMaxDepth = int64_t(1) << 25;   // contracted columns of a product
 constexpr int64_t kMaxBytes = int64_t(1) << 46;
 constexpr int32_t kMaxBatch = 65535;      // second axis of a grid
 
@@ -142,11 +143,10 @@ int launch_quantize(int dtype, QuantArgs& q, int64_t batch, int64_t units, void*
                   "k_quant_tile");
 }
 
-// Which kernel makes a product: tile 128 or 256 (k_matmul_tile), or 0 and the
-// block of k_matmul_split.  `rows`: those of the left matrix, by groups their
-// mean.
+// Which kernel makes a product: a tile of k_matmul_tile, or 0 and the columns of
+// a block of k_matmul_few.
 struct Choice {
-    int tile, rows, cols;
+    int tile, cols;
     bool values;   // the left matrix may come as values
 };
 
@@ -154,17 +154,29 @@ struct Choice {
 // pays while they are few and short (and 36 KiB hold them).
 constexpr int64_t kValuesSteps = 512;
 
-// room: the rows of a block, at most (by groups not known here: 16).
+// rows: those of the left matrix, by groups their mean; room: the rows of a
+// block, at most (by groups not known here: 16).
 Choice choose(int64_t rows, int64_t n, int64_t steps, int64_t batch, int64_t room)
 {
-    if (rows <= 16) return {0, 16, cut(n, 16) * batch <= 1024 ? 16 : 64, room * steps <= kValuesSteps};
-    if (rows <= 32) return {0, 32, 32, false};
-    // the tiles address their rows by 31 bits
-    if (steps < (int64_t(1) << 17)) {
-        if (cut(rows, 256) * cut(n, 256) * batch >= 256) return {256, 0, 0, false};
-        if (cut(rows, 128) * cut(n, 128) * batch >= 128) return {128, 0, 0, false};
-    }
-    return {0, 64, 64, false};
+    if (rows <= 16) return {0, cut(n, 16) * batch <= 1024 ? 16 : 64, room * steps <= kValuesSteps};
+    // a tile addresses its rows of a and b by 31 bits (kMaxDepth: 64 of them)
+    if (steps >= (int64_t(1) << 17)) return {64, 0, false};
+    const int64_t t64 = cut(rows, 64) * cut(n, 64) * batch;
+    const int64_t t128 = cut(rows, 128) * cut(n, 128) * batch, t256 = cut(rows, 256) * cut(n, 256) * batch;
+    // At most one 64-tile a CU, its k-steps shared by four groups of waves:
+    // 256 x 4096 x 4096 8.5 us, by 128-tiles 11.9; 777 x 2063 x 4104 (429
+    // tiles) 21.5 us against 15.8.
+    if (t64 <= 256) return {64, 0, false};
+    // Rounds of the device, in tenths of a microsecond per pair of k-steps as
+    // measured with 4096 columns: 256-tiles one a CU, 12 + 7 by how full the
+    // round is (3000 x 3000 29.7 us, 4096 x 4096 37.3); 128-tiles two a CU,
+    // 11.5, or 7.3 while they are one (35.0 and 44.1 us; 2048 x 4096 24.4 us,
+    // by 256-tiles 29.9).
+    const int64_t r256 = t256 % 256, r128 = t128 % 512;
+    const int64_t by256 = t256 / 256 * 190 + (r256 ? 120 + 70 * r256 / 256 : 0);
+    const int64_t by128 = t128 / 512 * 115 + (r128 > 256 ? 115 : r128 ? 73 : 0);
+    if (by256 <= by128) return {256, 0, false};
+    return {128, 0, false};
 }
 
 // By groups: the mean of the groups' rows decides, as the rows themselves are
@@ -177,8 +189,9 @@ Choice choose_grouped(int64_t rows, int64_t n, int64_t steps, int32_t groups)
 
 int launch_matmul(int out_dtype, int grouping, const Choice& c, MatmulArgs& p, int64_t batch, void* stream)
 {
-    const SplitKernel s = c.tile ? SplitKernel{} : matmul_split_kernel(p.x ? p.x_dtype : kHeld, grouping, c.rows, c.cols);
-    const int rows = c.tile ? c.tile : s.rows, cols = c.tile ? c.tile : s.cols;
+    const TileKernel t = c.tile ? matmul_tile_kernel(out_dtype, grouping, c.tile) : TileKernel{};
+    const FewKernel f = c.tile ? FewKernel{} : matmul_few_kernel(p.x ? p.x_dtype : kHeld, grouping, c.cols);
+    const int rows = c.tile ? t.tile : 16, cols = c.tile ? t.tile : f.cols;
     // by rows: two groups more, the rows in front of the first and behind the last
     p.units = grouping == kByRows ? grouped_units(p.m, p.groups + 2, rows) : cut(p.m, rows);
     p.n_tiles = cut(p.n, cols);
@@ -186,9 +199,8 @@ int launch_matmul(int out_dtype, int grouping, const Choice& c, MatmulArgs& p, i
     p.wide = wide_rows(p.out, p.out_stride, grouping == kByContraction ? p.m * p.out_stride : 0, elem_bytes(out_dtype),
                        c.tile ? 16 : 4 * elem_bytes(out_dtype));
     void* args[] = {&p};
-    return launch(c.tile ? matmul_tile_kernel(out_dtype, grouping, c.tile) : s.fn, p.units * p.n_tiles, batch,
-                  c.tile ? kMatmulThreads : kWave * s.waves, args, stream, "the product's kernel",
-                  rows == 16 ? few_lds(p.few_rows, p.steps, cols, s.waves) : 0);
+    return launch(c.tile ? t.fn : f.fn, p.units * p.n_tiles, batch, c.tile ? t.threads : kWave * f.waves, args, stream,
+                  "the product's kernel", c.tile ? 0 : few_lds(p.few_rows, p.steps, cols, f.waves));
 }
 
 int check_groups(const int32_t* offsets, int32_t groups, int64_t rows)
@@ -336,6 +348,7 @@ int product(Product& q, bool values, bool grouped)
     if (int st = check_axis(q.m, "m")) return st;
     if (int st = check_axis(q.n, "n")) return st;
     if (int st = check_axis(q.k, "k")) return st;
+    if (q.k > kMaxDepth) return fail(OU_EINVAL, "k = %lld: 2^25 at most", static_cast<long long>(q.k));
     if (values && (q.x_stride < q.k || q.x_stride > kMaxAxis)) return fail(OU_EINVAL, "x_stride is out of range");
     if (q.out_stride < q.n || q.out_stride > kMaxAxis) return fail(OU_EINVAL, "out_stride is out of range");
     if (grouped)
@@ -445,6 +458,7 @@ OU_EXPORT int ou_mx4_grouped_outer(int out_dtype, const uint8_t* a_codes_t, cons
     if (int st = check_groups(offsets, groups, rows)) return st;
     if (m == 0 || n == 0 || groups == 0) return OU_OK;
     const int64_t pr = ou_mx4_grouped_columns(rows, groups);
+    if (pr > kMaxDepth) return fail(OU_EINVAL, "%lld columns are held: 2^25 at most", static_cast<long long>(pr));
     const int eo = elem_bytes(out_dtype);
     const Buffer bufs[] = {{"a_codes_t", a_codes_t, held_codes(m, pr), 16, false},
                            {"a_scales_t", a_scales_t, held_scales(m, pr), 4, false},
@@ -467,9 +481,7 @@ OU_EXPORT int ou_mx4_grouped_outer(int out_dtype, const uint8_t* a_codes_t, cons
     p.offsets = offsets;
     p.rows = rows;
     p.groups = groups;
-    // the mean depth does not matter for the choice, the tiles do
-    Choice c = choose(m, n, p.steps, groups, 16);
-    if (!c.tile) c = {0, 64, 64, false};
+    const Choice c = choose(m > 16 ? m : 17, n, p.steps, groups, 16);   // few rows have no kernel of their own here
     return launch_matmul(out_dtype, kByContraction, c, p, groups, stream);
 }
 

@@ -298,6 +298,20 @@ struct Groups {
     }
 };
 
+// The tile of a block: XCDs (blocks b mod 8) take contiguous runs of the tile
+// order, which walks bands of 8 units down, then along n, so that the blocks
+// that run together on one XCD share rows of a and of b in its L2.
+__device__ __forceinline__ void tile_of(uint32_t b, uint32_t units, uint32_t n_tiles, uint32_t* unit, uint32_t* ntile)
+{
+    const uint32_t total = units * n_tiles, x = b & 7, per = total >> 3, extra = total & 7;
+    const uint32_t t = x * per + (x < extra ? x : extra) + (b >> 3);
+    constexpr uint32_t kBand = 8;
+    const uint32_t band = t / (kBand * n_tiles), in = t - band * kBand * n_tiles;
+    const uint32_t left = units - band * kBand, h = left < kBand ? left : kBand;
+    *ntile = in / h;
+    *unit = band * kBand + (in - *ntile * h);
+}
+
 // ---- quantisation along the columns --------------------------------------
 
 // 16 lanes hold one unit of 128 columns of a row, eight values a lane, so a
@@ -353,7 +367,8 @@ __global__ __launch_bounds__(kQuantThreads) void k_quant_tile(QuantArgs q)
     const int t = static_cast<int>(threadIdx.x);
     const int64_t batch = blockIdx.y;
     const uint32_t col_tiles = static_cast<uint32_t>(q.pcols / T);
-    const uint32_t unit = blockIdx.x / col_tiles;       // block of 128 padded rows
+    uint32_t unit, col_tile;                            // block of 128 padded rows, of columns
+    tile_of(blockIdx.x, gridDim.x / col_tiles, col_tiles, &unit, &col_tile);
     int64_t row0 = static_cast<int64_t>(unit) * T, nrows = q.rows - row0;
     if (q.offsets) {
         const Place p = Groups(q.offsets, q.groups, q.rows, T).locate(unit);
@@ -362,7 +377,7 @@ __global__ __launch_bounds__(kQuantThreads) void k_quant_tile(QuantArgs q)
         nrows = p.rows;
     }
     if (nrows > T) nrows = T;
-    const int64_t col0 = static_cast<int64_t>(blockIdx.x - unit * col_tiles) * T;
+    const int64_t col0 = static_cast<int64_t>(col_tile) * T;
     const Elem* x = static_cast<const Elem*>(q.x) + batch * q.batch_stride;
     const int sub = t & 15;
     const int64_t col = col0 + sub * 8, left = q.cols - col;
@@ -616,37 +631,6 @@ __device__ __forceinline__ void block_barrier()
     asm volatile("" ::: "memory");
 }
 
-// What k_matmul_few and k_matmul_split do with the waves' sums: joined in LDS
-// in the order of the waves, rounded once, stored.
-template <int MT, int NT, int W>
-__device__ __forceinline__ void join_and_store(const MatmulArgs& p, f32x4 (*part)[MT * NT][kWave],
-                                               const f32x4 (&acc)[MT][NT], int wave, int64_t out0, int64_t row0,
-                                               int64_t mrows, int64_t n0)
-{
-    const int t = static_cast<int>(threadIdx.x), lane = t & 63, r = lane & 15, g = lane >> 4;
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) part[wave][i * NT + j][lane] = acc[i][j];
-    __syncthreads();
-    for (int x = t; x < MT * NT * kWave; x += kWave * W) {
-        const int f = x >> 6, i = f / NT, j = f - i * NT;   // lane x mod 64 is this one
-        f32x4 sum = part[0][f][lane];
-#pragma unroll
-        for (int w = 1; w < W; ++w) sum += part[w][f][lane];
-        const int64_t m = 16 * i + r, n = n0 + 16 * j + 4 * g, left = p.n - n;
-        if (m >= mrows || left <= 0) continue;
-        const int64_t at = out0 + (row0 + m) * p.out_stride + n;
-        const int have = left > 4 ? 4 : static_cast<int>(left);
-        if (p.out_dtype == kF32)
-            store4<kF32>(p.out, at, sum, have, p.wide);
-        else if (p.out_dtype == kF16)
-            store4<kF16>(p.out, at, sum, have, p.wide);
-        else
-            store4<kBF16>(p.out, at, sum, have, p.wide);
-    }
-}
-
 // Up to 16 rows (of a group): 16 x 16 NT results a block, the k-steps dealt to
 // its W waves in contiguous runs, b's fragments loaded straight to registers.
 // Such a product waits for b from memory: its first U steps are under way
@@ -736,7 +720,7 @@ __global__ __launch_bounds__(kWave * W) void k_matmul_few(MatmulArgs p)
         ap = p.a + (row0 + ar) * row_steps * (kPad / 2) + g * 16;
         asp = p.as + (row0 + ar) * row_steps * (kPad / kBlock) + g;
     }
-    f32x4 acc[1][NT] = {};
+    f32x4 acc[NT] = {};
     for (int64_t k0 = first; k0 < last; k0 += U) {
         if (k0 > first) load_b(k0);
 #pragma unroll
@@ -747,96 +731,30 @@ __global__ __launch_bounds__(kWave * W) void k_matmul_few(MatmulArgs p)
             const int as = asp[k * (kPad / kBlock)];
 #pragma unroll
             for (int j = 0; j < NT; ++j)
-                acc[0][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(bv[u][j]), widen(av), acc[0][j], 4, 4,
+                acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(bv[u][j]), widen(av), acc[j], 4, 4,
                                                                             0, bsc[u][j] >> (8 * g), 0, as);
         }
     }
-    join_and_store<1, NT, W>(p, reinterpret_cast<f32x4(*)[NT][kWave]>(tail), acc, wave, 0, row0, rows, n0);
-}
-
-// Few tiles: 16 MT x 16 NT results a block, k-steps dealt to its W waves in
-// contiguous runs, fragments loaded straight to registers, U steps at a time.
-template <int G, int MT, int NT, int W, int U>
-__global__ __launch_bounds__(kWave * W) void k_matmul_split(MatmulArgs p)
-{
-    __shared__ f32x4 part[W][MT * NT][kWave];
-    const int t = static_cast<int>(threadIdx.x), lane = t & 63, r = lane & 15, g = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-    const uint32_t unit = blockIdx.x / static_cast<uint32_t>(p.n_tiles);
-    const uint32_t ntile = blockIdx.x - unit * static_cast<uint32_t>(p.n_tiles);
-    int64_t row0 = static_cast<int64_t>(unit) * (16 * MT), mrows = p.m - row0;
-    int64_t step0 = 0, steps = p.steps, out0 = 0;
-    const uint8_t *b = p.b, *bs = p.bs;
-    if constexpr (G == kByRows) {
-        const Place at = Groups(p.offsets, p.groups, p.rows, 16 * MT).locate(unit);
-        row0 = at.row;
-        mrows = at.rows;
-        if (mrows <= 0) return;
-        if (at.group < 0) {
-            if (!p.zero_rest) return;
-            steps = 0;   // rows of no group: the sum over nothing
-        } else {
-            b += static_cast<int64_t>(at.group) * p.n * p.steps * (kPad / 2);
-            bs += static_cast<int64_t>(at.group) * p.n * p.steps * (kPad / kBlock);
-        }
+    // the waves' sums, joined in LDS in the order of the waves, rounded once
+    f32x4 (*part)[NT][kWave] = reinterpret_cast<f32x4(*)[NT][kWave]>(tail);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) part[wave][j][lane] = acc[j];
+    __syncthreads();
+    for (int j = wave; j < NT; j += W) {
+        f32x4 sum = part[0][j][lane];
+#pragma unroll
+        for (int w = 1; w < W; ++w) sum += part[w][j][lane];
+        const int64_t n = n0 + 16 * j + 4 * g, left = p.n - n;
+        if (r >= rows || left <= 0) continue;
+        const int64_t at = (row0 + r) * p.out_stride + n;
+        const int have = left > 4 ? 4 : static_cast<int>(left);
+        if (p.out_dtype == kF32)
+            store4<kF32>(p.out, at, sum, have, p.wide);
+        else if (p.out_dtype == kF16)
+            store4<kF16>(p.out, at, sum, have, p.wide);
+        else
+            store4<kBF16>(p.out, at, sum, have, p.wide);
     }
-    if constexpr (G == kByContraction) {
-        uint32_t before, own;
-        Groups(p.offsets, p.groups, p.rows, kPad).span(static_cast<int32_t>(blockIdx.y), &before, &own);
-        step0 = before;
-        steps = own;
-        if (step0 > p.steps) step0 = p.steps;
-        if (steps > p.steps - step0) steps = p.steps - step0;
-        out0 = static_cast<int64_t>(blockIdx.y) * p.m * p.out_stride;
-    }
-    const int64_t n0 = static_cast<int64_t>(ntile) * (16 * NT);
-    const uint8_t *ap[MT], *asp[MT], *bp[NT], *bsp[NT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        int64_t m = 16 * i + r;              // rows behind the edge read the last one
-        m = row0 + (m < mrows ? m : mrows - 1);
-        ap[i] = p.a + (m * p.steps + step0) * (kPad / 2) + g * 16;
-        asp[i] = p.as + (m * p.steps + step0) * (kPad / kBlock);
-    }
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        int64_t n = n0 + 16 * j + r;
-        n = n < p.n ? n : p.n - 1;
-        bp[j] = b + (n * p.steps + step0) * (kPad / 2) + g * 16;
-        bsp[j] = bs + (n * p.steps + step0) * (kPad / kBlock);
-    }
-    f32x4 acc[MT][NT] = {};
-    const int64_t run = (steps + W - 1) / W, first = wave * run;
-    const int64_t last = first + run < steps ? first + run : steps;
-    for (int64_t k0 = first; k0 < last; k0 += U) {
-        i32x4 av[U][MT], bv[U][NT];
-        int as[U][MT], bsc[U][NT];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t k = k0 + u < last ? k0 + u : last - 1;
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                bv[u][j] = *reinterpret_cast<const i32x4*>(bp[j] + k * (kPad / 2));
-                bsc[u][j] = *reinterpret_cast<const int*>(bsp[j] + k * (kPad / kBlock));
-            }
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                av[u][i] = *reinterpret_cast<const i32x4*>(ap[i] + k * (kPad / 2));
-                as[u][i] = *reinterpret_cast<const int*>(asp[i] + k * (kPad / kBlock));
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (k0 + u >= last) break;
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        widen(bv[u][j]), widen(av[u][i]), acc[i][j], 4, 4, 0, bsc[u][j] >> (8 * g), 0, as[u][i] >> (8 * g));
-        }
-    }
-    join_and_store<MT, NT, W>(p, part, acc, wave, out0, row0, mrows, n0);
 }
 
 // ---- products, tiled through LDS ------------------------------------------
@@ -873,20 +791,6 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const uint8_t* p, uin
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, static_cast<int>(bytes), 0x00020000);
 }
 
-// The tile of a block: XCDs (blocks b mod 8) take contiguous runs of the tile
-// order, which walks bands of 8 units down, then along n, so that the blocks
-// that run together on one XCD share rows of a and of b in its L2.
-__device__ __forceinline__ void tile_of(uint32_t b, uint32_t units, uint32_t n_tiles, uint32_t* unit, uint32_t* ntile)
-{
-    const uint32_t total = units * n_tiles, x = b & 7, per = total >> 3, extra = total & 7;
-    const uint32_t t = x * per + (x < extra ? x : extra) + (b >> 3);
-    constexpr uint32_t kBand = 8;
-    const uint32_t band = t / (kBand * n_tiles), in = t - band * kBand * n_tiles;
-    const uint32_t left = units - band * kBand, h = left < kBand ? left : kBand;
-    *ntile = in / h;
-    *unit = band * kBand + (in - *ntile * h);
-}
-
 // Four waves in a square, 16 WM x 16 WN results each.  A pair is two k-steps,
 // 256 columns: 128 bytes of codes of every row, moved to LDS in two
 // alternating buffers (pieces of 128 bytes: the memory pipeline takes about
@@ -898,14 +802,18 @@ __device__ __forceinline__ void tile_of(uint32_t b, uint32_t units, uint32_t n_t
 // 16-byte pieces of a row are exchanged by (row / 2) mod 8: a read of one
 // piece of 16 rows by 64 lanes then meets no bank twice (lanes 0-3, 12-15,
 // 20-27 of it go together, and so on).
-template <int DT, int G, int WM, int WN>
-__global__ __launch_bounds__(256, 1) void k_matmul_tile(MatmulArgs p)
+// With few tiles KG such groups of waves share a block, each with its part of
+// LDS and a contiguous part of the pairs; their sums are added in order.
+template <int DT, int G, int WM, int WN, int KG>
+__global__ __launch_bounds__(256 * KG, 1) void k_matmul_tile(MatmulArgs p)
 {
     constexpr int BM = 32 * WM, BN = 32 * WN;
-    constexpr int kCodes = (BM + BN) * 128, kScales = (BM + BN) * 32;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kCodes + 2 * kScales];
-    const int t = static_cast<int>(threadIdx.x), lane = t & 63, r = lane & 15, g = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    constexpr int kCodes = (BM + BN) * 128, kScales = (BM + BN) * 32, kGroup = 2 * kCodes + 2 * kScales;
+    __shared__ __attribute__((aligned(16))) uint8_t all_lds[KG * kGroup];
+    const int lane = static_cast<int>(threadIdx.x) & 63, r = lane & 15, g = lane >> 4;
+    const int block_wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+    const int wave = block_wave & 3, kg = block_wave >> 2;   // of the group; the group
+    uint8_t* const lds = all_lds + kg * kGroup;
     const uint32_t lds0 = static_cast<uint32_t>(
         reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
 
@@ -944,6 +852,13 @@ __global__ __launch_bounds__(256, 1) void k_matmul_tile(MatmulArgs p)
         }
     }
     if (mrows > BM) mrows = BM;
+    // the group's pairs; all groups turn as often, over nothing at the end
+    const uint32_t turns = static_cast<uint32_t>(((steps + 1) / 2 + KG - 1) / KG);
+    if constexpr (KG > 1) {
+        const int64_t skip = 2 * static_cast<int64_t>(turns) * kg;
+        step0 += skip < steps ? skip : steps;
+        steps = skip < steps ? (steps - skip < 2 * turns ? steps - skip : 2 * turns) : 0;
+    }
     const int64_t n0 = static_cast<int64_t>(ntile) * BN;
     const int64_t ncols = p.n - n0 < BN ? p.n - n0 : BN;
 
@@ -1026,14 +941,15 @@ __global__ __launch_bounds__(256, 1) void k_matmul_tile(MatmulArgs p)
         else
             sb[k][x - WM] = static_cast<int>(__builtin_amdgcn_ubfe(qb[x - WM][k], shift, width));
     };
-    // The products of k-step K; between them what next(x) starts.
-    auto multiply = [&](auto kstep, auto next) {
+    // The products of k-step K; between them what next(x) starts.  width: of
+    // the first k-step's scales.
+    auto multiply = [&](auto kstep, uint32_t width, auto next) {
         constexpr int K = decltype(kstep)::value;
 #pragma unroll
         for (int x = 0; x < WM * WN; ++x) {
             const int i = x / WN, j = x % WN;
-            if (K == 0 && j == 0) take_scale(0, i, 8);
-            if (K == 0 && i == 0) take_scale(0, WM + j, 8);
+            if (K == 0 && j == 0) take_scale(0, i, width);
+            if (K == 0 && i == 0) take_scale(0, WM + j, width);
             multiply_add(acc[i][j], fb[K][j], fa[K][i], sb[K][j], sa[K][i]);
             next(x);
             __builtin_amdgcn_sched_barrier(0);
@@ -1057,8 +973,8 @@ __global__ __launch_bounds__(256, 1) void k_matmul_tile(MatmulArgs p)
                 asm volatile("" : "+a"(acc[i][j]));
             }
     };
-    if (pairs == 0) zero();
-    if (pairs > 0) {
+    if (turns == 0) zero();
+    if (turns > 0) {
 #pragma unroll
         for (int part = 0; part < 3; ++part) move_scales(0, part);
 #pragma unroll
@@ -1071,12 +987,12 @@ __global__ __launch_bounds__(256, 1) void k_matmul_tile(MatmulArgs p)
 #pragma unroll
         for (int x = 0; x < kReads; ++x) read(0, 0, x);
         settle_products();   // and behind acc's first values
-        for (uint32_t q = 0; q < pairs; ++q) {
+        for (uint32_t q = 0; q < turns; ++q) {
             // the first k-step; the last transfers of pair q + 1 start here
-            multiply(First{}, [&](int x) {
+            multiply(First{}, KG == 1 || q < pairs ? 8 : 0, [&](int x) {
                 if (x % kReadEvery == 0 && x / kReadEvery < kReads) read(q, 1, x / kReadEvery);
                 // the second k-step's scales, before the next pair's replace them
-                if (x >= kProducts - kReads) take_scale(1, x - (kProducts - kReads), q == odd ? 0 : 8);
+                if (x >= kProducts - kReads) take_scale(1, x - (kProducts - kReads), q == odd || (KG > 1 && q >= pairs) ? 0 : 8);
                 const int y = kProducts + x;
                 if (y % kMoveEvery == kMoveEvery - 1 && y / kMoveEvery < kMoves) move(q + 1, y / kMoveEvery);
             });
@@ -1085,7 +1001,7 @@ __global__ __launch_bounds__(256, 1) void k_matmul_tile(MatmulArgs p)
             wait_transfers<0>();
             block_barrier();
             __builtin_amdgcn_sched_barrier(0);
-            multiply(Second{}, [&](int x) {
+            multiply(Second{}, 8, [&](int x) {
                 if (x % kReadEvery == 0 && x / kReadEvery < kReads) read(q + 1, 0, x / kReadEvery);
                 if (x % kMoveEvery == kMoveEvery - 1 && x / kMoveEvery < kMoves) move(q + 2, x / kMoveEvery);
             });
@@ -1098,12 +1014,31 @@ __global__ __launch_bounds__(256, 1) void k_matmul_tile(MatmulArgs p)
             for (int j = 0; j < WN; ++j) asm volatile("" : "+a"(acc[i][j]));   // read behind that
     }
 
+    block_barrier();
+    if constexpr (KG > 1) {
+        if (kg > 0) {
+#pragma unroll
+            for (int i = 0; i < WM; ++i)
+#pragma unroll
+                for (int j = 0; j < WN; ++j)
+                    reinterpret_cast<f32x4*>(lds)[((wave * WM + i) * WN + j) * kWave + lane] = acc[i][j];
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        }
+        block_barrier();
+        if (kg > 0) return;
+#pragma unroll
+        for (int k = 1; k < KG; ++k)
+#pragma unroll
+            for (int i = 0; i < WM; ++i)
+#pragma unroll
+                for (int j = 0; j < WN; ++j)
+                    acc[i][j] += reinterpret_cast<const f32x4*>(lds + k * kGroup)[((wave * WM + i) * WN + j) * kWave + lane];
+    }
     // Result (i, j, e) of a lane is row 16 i + r, column 16 j + 4 g + e.  They
     // pass through the wave's part of LDS (the codes are done with), so that
     // whole pieces of rows go out together.
-    block_barrier();
     constexpr int kSize = DT == kF32 ? 4 : 2, kRow = 16 * WN * kSize, kPitch = kRow + 16, kPieces = kRow / 16;
-    constexpr int kPart = static_cast<int>(sizeof(lds)) / 4;
+    constexpr int kPart = kGroup / 4;
     constexpr int kFrags = kPart / (16 * kPitch) < WM ? (kPart / (16 * kPitch) < WM / 2 ? WM / 4 : WM / 2) : WM;
     static_assert(kFrags * 16 * kPitch <= kPart && WM % kFrags == 0, "room in LDS");
     uint8_t* const mine = lds + wave * kPart;
@@ -1178,50 +1113,49 @@ const void* dequant_kernel(int dtype)
     return fns[dtype];
 }
 
-template <int G, int W>
-const void* matmul_tile_of(int dtype)
+template <int G, int W, int KG>
+TileKernel tile_of_type(int dtype)
 {
-    const void* fns[3] = {reinterpret_cast<const void*>(&k_matmul_tile<kF32, G, W, W>),
-                          reinterpret_cast<const void*>(&k_matmul_tile<kF16, G, W, W>),
-                          reinterpret_cast<const void*>(&k_matmul_tile<kBF16, G, W, W>)};
-    return fns[dtype];
-}
-
-const void* matmul_tile_kernel(int out_dtype, int grouping, int tile)
-{
-    const bool large = tile == 256;
-    return grouping == kPlain    ? (large ? matmul_tile_of<kPlain, 8>(out_dtype) : matmul_tile_of<kPlain, 4>(out_dtype))
-           : grouping == kByRows ? (large ? matmul_tile_of<kByRows, 8>(out_dtype) : matmul_tile_of<kByRows, 4>(out_dtype))
-                                 : (large ? matmul_tile_of<kByContraction, 8>(out_dtype)
-                                          : matmul_tile_of<kByContraction, 4>(out_dtype));
-}
-
-template <int XT, int G>
-SplitKernel few_of(int cols)
-{
-    if (cols == 16) return {reinterpret_cast<const void*>(&k_matmul_few<XT, G, 1, 8, 4>), 16, 16, 8};
-    return {reinterpret_cast<const void*>(&k_matmul_few<XT, G, 4, 4, 2>), 16, 64, 4};
+    const void* fns[3] = {reinterpret_cast<const void*>(&k_matmul_tile<kF32, G, W, W, KG>),
+                          reinterpret_cast<const void*>(&k_matmul_tile<kF16, G, W, W, KG>),
+                          reinterpret_cast<const void*>(&k_matmul_tile<kBF16, G, W, W, KG>)};
+    return {fns[dtype], 32 * W, 256 * KG};
 }
 
 template <int G>
-SplitKernel split_of(int x_dtype, int rows, int cols)
+TileKernel tile_of_shape(int dtype, int tile)
 {
-    if constexpr (G != kByContraction) {
-        if (rows == 16)
-            return x_dtype == kF32    ? few_of<kF32, G>(cols)
-                   : x_dtype == kF16  ? few_of<kF16, G>(cols)
-                   : x_dtype == kBF16 ? few_of<kBF16, G>(cols)
-                                      : few_of<kHeld, G>(cols);
-    }
-    if (rows == 32) return {reinterpret_cast<const void*>(&k_matmul_split<G, 2, 2, 8, 2>), 32, 32, 8};
-    return {reinterpret_cast<const void*>(&k_matmul_split<G, 4, 4, 8, 1>), 64, 64, 8};
+    return tile == 256   ? tile_of_type<G, 8, 1>(dtype)
+           : tile == 128 ? tile_of_type<G, 4, 1>(dtype)
+                         : tile_of_type<G, 2, 4>(dtype);
 }
 
-SplitKernel matmul_split_kernel(int x_dtype, int grouping, int rows, int cols)
+TileKernel matmul_tile_kernel(int out_dtype, int grouping, int tile)
 {
-    return grouping == kPlain    ? split_of<kPlain>(x_dtype, rows, cols)
-           : grouping == kByRows ? split_of<kByRows>(x_dtype, rows, cols)
-                                 : split_of<kByContraction>(x_dtype, rows, cols);
+    return grouping == kPlain    ? tile_of_shape<kPlain>(out_dtype, tile)
+           : grouping == kByRows ? tile_of_shape<kByRows>(out_dtype, tile)
+                                 : tile_of_shape<kByContraction>(out_dtype, tile);
+}
+
+template <int XT, int G>
+FewKernel few_of(int cols)
+{
+    if (cols == 16) return {reinterpret_cast<const void*>(&k_matmul_few<XT, G, 1, 8, 4>), 16, 8};
+    return {reinterpret_cast<const void*>(&k_matmul_few<XT, G, 4, 4, 2>), 64, 4};
+}
+
+template <int G>
+FewKernel few_of_type(int x_dtype, int cols)
+{
+    return x_dtype == kF32    ? few_of<kF32, G>(cols)
+           : x_dtype == kF16  ? few_of<kF16, G>(cols)
+           : x_dtype == kBF16 ? few_of<kBF16, G>(cols)
+                              : few_of<kHeld, G>(cols);
+}
+
+FewKernel matmul_few_kernel(int x_dtype, int grouping, int cols)
+{
+    return grouping == kPlain ? few_of_type<kPlain>(x_dtype, cols) : few_of_type<kByRows>(x_dtype, cols);
 }
 
 }  // namespace mx4

@@ -123,7 +123,7 @@ BAD_PRODUCTS = [
     (dict(dt=9), EINVAL), (dict(m=-1), EINVAL), (dict(n=-1), EINVAL), (dict(k=-1), EINVAL), (dict(b=None), EINVAL),
     (dict(bs=None), EINVAL), (dict(os=71), EINVAL), (dict(out=None), EINVAL), (dict(out=O + 1), EALIGN),
     (dict(b=C + 8), EALIGN), (dict(bs=S + 2), EALIGN), (dict(out=C), EOVERLAP), (dict(out=X), EOVERLAP),
-    (dict(m=1 << 31, n=1 << 31, os=1 << 31), EINVAL),
+    (dict(m=1 << 31, n=1 << 31, os=1 << 31), EINVAL), (dict(k=(1 << 25) + 1), EINVAL),
 ]
 
 
@@ -157,6 +157,7 @@ def _grouped(L, values, off=0x900000000, groups=3, **kw):
 
 @pytest.mark.parametrize("values", [False, True])
 @pytest.mark.parametrize("kw,code", BAD_PRODUCTS + [
+    (dict(m=(1 << 28) + 1), EINVAL),
     (dict(off=None), EINVAL), (dict(off=0x900000001), EALIGN), (dict(groups=-1), EINVAL),
     (dict(groups=65536), EINVAL), (dict(out=0x900000000), EOVERLAP)])
 def test_grouped_matmul_refusals(L, values, kw, code):
@@ -165,7 +166,7 @@ def test_grouped_matmul_refusals(L, values, kw, code):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(dt=3), EINVAL), (dict(m=-1), EINVAL), (dict(n=-1), EINVAL), (dict(rows=-1), EINVAL), (dict(off=None), EINVAL),
-    (dict(groups=-2), EINVAL), (dict(a=None), EINVAL), (dict(bs=None), EINVAL), (dict(out=None), EINVAL),
+    (dict(groups=-2), EINVAL), (dict(rows=(1 << 25) + 1), EINVAL), (dict(rows=(1 << 28) + 1), EINVAL), (dict(a=None), EINVAL), (dict(bs=None), EINVAL), (dict(out=None), EINVAL),
     (dict(out=O + 1), EALIGN), (dict(a=C + 8), EALIGN), (dict(out=C), EOVERLAP), (dict(out=X), EOVERLAP)])
 def test_grouped_outer_refusals(L, kw, code):
     a = dict(dt=1, a=C, as_=S, m=48, b=CT, bs=ST, n=80, rows=500, off=X, groups=5, out=O) | kw
