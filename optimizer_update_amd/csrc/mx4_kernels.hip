@@ -632,12 +632,15 @@ __device__ __forceinline__ void block_barrier()
 }
 
 // Up to 16 rows (of a group): 16 x 16 NT results a block, the k-steps dealt to
-// its W waves in contiguous runs, b's fragments loaded straight to registers.
-// Such a product waits for b from memory: its first U steps are under way
-// before anything else.  With XT the left matrix is given as values of that
-// type: the block meanwhile quantises its rows into LDS.  The fragment of b is
-// the instruction's first operand, so that a lane's four results are
-// neighbours in a row of out.
+// its W waves in contiguous runs of pairs, b's fragments loaded straight to
+// registers.  Such a product waits for b from memory: its first U pairs are
+// under way before anything else.  Which block of 32 columns a lane holds is
+// free as long as a and b agree: here lane group g holds blocks 2 g (for the
+// first product of a pair) and 2 g + 1 (for the second) of the pair's eight,
+// so that the four lanes of a row ask for 128 bytes together.  With XT the
+// left matrix is given as values of that type: the block meanwhile quantises
+// its rows into LDS.  The fragment of b is the instruction's first operand, so
+// that a lane's four results are neighbours in a row of out.
 template <int XT, int G, int NT, int W, int U>
 __global__ __launch_bounds__(kWave * W) void k_matmul_few(MatmulArgs p)
 {
@@ -648,8 +651,8 @@ __global__ __launch_bounds__(kWave * W) void k_matmul_few(MatmulArgs p)
     const uint32_t unit = blockIdx.x / static_cast<uint32_t>(p.n_tiles);
     const uint32_t ntile = blockIdx.x - unit * static_cast<uint32_t>(p.n_tiles);
     int64_t row0 = static_cast<int64_t>(unit) * 16, mrows = p.m - row0;
-    const int64_t row_steps = p.steps;
-    int64_t steps = p.steps;
+    const int row_steps = static_cast<int>(p.steps);   // below 2^18
+    int steps = row_steps;
     const uint8_t *b = p.b, *bs = p.bs;
     if constexpr (G == kByRows) {
         const Place at = Groups(p.offsets, p.groups, p.rows, 16).locate(unit);
@@ -660,8 +663,8 @@ __global__ __launch_bounds__(kWave * W) void k_matmul_few(MatmulArgs p)
             if (!p.zero_rest) return;
             steps = 0;   // rows of no group: the sum over nothing
         } else {
-            b += static_cast<int64_t>(at.group) * p.n * row_steps * (kPad / 2);
-            bs += static_cast<int64_t>(at.group) * p.n * row_steps * (kPad / kBlock);
+            b += at.group * p.n * p.steps * (kPad / 2);
+            bs += at.group * p.n * p.steps * (kPad / kBlock);
         }
     }
     const int rows = mrows < 16 ? static_cast<int>(mrows) : 16;
@@ -671,21 +674,38 @@ __global__ __launch_bounds__(kWave * W) void k_matmul_few(MatmulArgs p)
     for (int j = 0; j < NT; ++j) {
         int64_t n = n0 + 16 * j + r;
         n = n < p.n ? n : p.n - 1;           // rows behind the edge read the last one
-        bp[j] = b + n * row_steps * (kPad / 2) + g * 16;
-        bsp[j] = bs + n * row_steps * (kPad / kBlock);
+        bp[j] = b + n * p.steps * (kPad / 2) + g * 32;
+        bsp[j] = bs + n * p.steps * (kPad / kBlock);
     }
-    const int64_t run = (steps + W - 1) / W, first = wave * run;
-    const int64_t last = first + run < steps ? first + run : steps;
-    i32x4 bv[U][NT];
-    int bsc[U][NT];
-    auto load_b = [&](int64_t k0) {
+    const int pairs = (steps + 1) / 2, run = (pairs + W - 1) / W, first = wave * run;
+    const int last = first + run < pairs ? first + run : pairs;
+    i32x4 bv[U][NT][2];
+    uint32_t bsc[U][NT];   // the lane's two scale codes, in the low bytes
+    // An odd last step is half a pair: lanes of groups 2 and 3 hold nothing of it.
+    auto whole = [&](int q) { return 2 * q + 1 < steps; };
+    auto load_b = [&](int q0) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t k = k0 + u < last ? k0 + u : last - 1;
+        for (int j = 0; j < NT; ++j) {
+            if (U == 2 && q0 + 1 < last && whole(q0 + 1)) {   // four steps' scales of a row by one request
+                const u32x4 w = *reinterpret_cast<const u32x4*>(bsp[j] + q0 * 8);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                bv[u][j] = *reinterpret_cast<const i32x4*>(bp[j] + k * (kPad / 2));
-                bsc[u][j] = *reinterpret_cast<const int*>(bsp[j] + k * (kPad / kBlock));
+                for (int u = 0; u < U; ++u) bsc[u][j] = (g & 2 ? w[2 * u + 1] : w[2 * u]) >> (16 * (g & 1));
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int q = q0 + u < last ? q0 + u : last - 1;
+                const i32x4* c = reinterpret_cast<const i32x4*>(bp[j] + static_cast<int64_t>(q) * 128);
+                const uint16_t* w = reinterpret_cast<const uint16_t*>(bsp[j] + q * 8 + 2 * g);
+                const bool scales = !(U == 2 && q0 + 1 < last && whole(q0 + 1));
+                if (whole(q)) {
+                    bv[u][j][0] = c[0];
+                    bv[u][j][1] = c[1];
+                    if (scales) bsc[u][j] = *w;
+                } else {
+                    bv[u][j][0] = g < 2 ? c[0] : i32x4{0, 0, 0, 0};
+                    bv[u][j][1] = g < 2 ? c[1] : i32x4{0, 0, 0, 0};
+                    bsc[u][j] = g < 2 ? *w : 0;
+                }
             }
         }
     };
@@ -696,43 +716,64 @@ __global__ __launch_bounds__(kWave * W) void k_matmul_few(MatmulArgs p)
     uint8_t* tail = lds;
     if constexpr (kValues) {
         // codes of the rows, 16 bytes more apart than they are long, then scales
-        const int pitch = static_cast<int>(row_steps) * (kPad / 2) + 16, spitch = static_cast<int>(row_steps) * 4 + 4;
+        const int pitch = row_steps * (kPad / 2) + 16, spitch = row_steps * 4 + 4;
         using Elem = typename Type<XT>::Elem;
         const Elem* x = static_cast<const Elem*>(p.x) + row0 * p.x_stride;
-        const int units = steps ? rows * static_cast<int>(row_steps) : 0, sub = t & 15;
+        const int units = steps ? rows * row_steps : 0, sub = t & 15;
         uint8_t* const sc = lds + p.few_rows * pitch;
-        for (int u = t >> 4; u < units; u += 4 * W) {
-            const int row = u / static_cast<int>(row_steps), step = u - row * static_cast<int>(row_steps);
-            const int64_t col = static_cast<int64_t>(step) * kPad + sub * 8, left = p.k - col;
-            Octet<XT> v;
-            v.load(x + row * p.x_stride + col, left < 0 ? 0 : (left > 8 ? 8 : static_cast<int>(left)), p.x_wide);
-            const uint32_t s = scale_code(exponent_of<XT>(quad_max(v.top())));
-            *reinterpret_cast<uint32_t*>(lds + row * pitch + step * (kPad / 2) + sub * 4) =
-                s == kScaleNaN ? 0u : v.codes(scale_operand(s));
-            if ((sub & 3) == 0) sc[row * spitch + step * 4 + (sub >> 2)] = static_cast<uint8_t>(s);
+        constexpr int kAhead = 4;
+        for (int u0 = t >> 4; u0 < units; u0 += 4 * W * kAhead) {
+            Octet<XT> v[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int u = u0 + i * 4 * W;
+                v[i].zero();
+                if (u >= units) continue;
+                const int row = u / row_steps, step = u - row * row_steps;
+                const int64_t col = static_cast<int64_t>(step) * kPad + sub * 8, left = p.k - col;
+                v[i].load(x + row * p.x_stride + col, left < 0 ? 0 : (left > 8 ? 8 : static_cast<int>(left)), p.x_wide);
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int u = u0 + i * 4 * W;
+                const uint32_t s = scale_code(exponent_of<XT>(quad_max(v[i].top())));
+                if (u >= units) continue;
+                const int row = u / row_steps, step = u - row * row_steps;
+                *reinterpret_cast<uint32_t*>(lds + row * pitch + step * (kPad / 2) + sub * 4) =
+                    s == kScaleNaN ? 0u : v[i].codes(scale_operand(s));
+                if ((sub & 3) == 0) sc[row * spitch + step * 4 + (sub >> 2)] = static_cast<uint8_t>(s);
+            }
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         block_barrier();
-        ap = lds + ar * pitch + g * 16;
-        asp = sc + ar * spitch + g;
+        ap = lds + ar * pitch + g * 32;
+        asp = sc + ar * spitch + 2 * g;
         tail = sc + (p.few_rows * spitch + 15) / 16 * 16;
     } else {
-        ap = p.a + (row0 + ar) * row_steps * (kPad / 2) + g * 16;
-        asp = p.as + (row0 + ar) * row_steps * (kPad / kBlock) + g;
+        ap = p.a + (row0 + ar) * p.steps * (kPad / 2) + g * 32;
+        asp = p.as + (row0 + ar) * p.steps * (kPad / kBlock) + 2 * g;
     }
     f32x4 acc[NT] = {};
-    for (int64_t k0 = first; k0 < last; k0 += U) {
-        if (k0 > first) load_b(k0);
+    for (int q0 = first; q0 < last; q0 += U) {
+        if (q0 > first) load_b(q0);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (k0 + u >= last) break;
-            const int64_t k = k0 + u;
-            const i32x4 av = *reinterpret_cast<const i32x4*>(ap + k * (kPad / 2));
-            const int as = asp[k * (kPad / kBlock)];
+            const int q = q0 + u;
+            if (q >= last) break;
+            i32x4 av[2] = {};
+            uint32_t as = 0;
+            if (whole(q) || g < 2) {
+                av[0] = *reinterpret_cast<const i32x4*>(ap + static_cast<int64_t>(q) * 128);
+                av[1] = *reinterpret_cast<const i32x4*>(ap + static_cast<int64_t>(q) * 128 + 16);
+                as = *reinterpret_cast<const uint16_t*>(asp + q * 8);
+            }
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-                acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(bv[u][j]), widen(av), acc[j], 4, 4,
-                                                                            0, bsc[u][j] >> (8 * g), 0, as);
+            for (int j = 0; j < NT; ++j) {
+                acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    widen(bv[u][j][0]), widen(av[0]), acc[j], 4, 4, 0, static_cast<int>(bsc[u][j]), 0, static_cast<int>(as));
+                acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    widen(bv[u][j][1]), widen(av[1]), acc[j], 4, 4, 1, static_cast<int>(bsc[u][j]), 1, static_cast<int>(as));
+            }
         }
     }
     // the waves' sums, joined in LDS in the order of the waves, rounded once
@@ -1140,8 +1181,8 @@ TileKernel matmul_tile_kernel(int out_dtype, int grouping, int tile)
 template <int XT, int G>
 FewKernel few_of(int cols)
 {
-    if (cols == 16) return {reinterpret_cast<const void*>(&k_matmul_few<XT, G, 1, 8, 4>), 16, 8};
-    return {reinterpret_cast<const void*>(&k_matmul_few<XT, G, 4, 4, 2>), 64, 4};
+    if (cols == 16) return {reinterpret_cast<const void*>(&k_matmul_few<XT, G, 1, 8, 2>), 16, 8};
+    return {reinterpret_cast<const void*>(&k_matmul_few<XT, G, 4, 4, 1>), 64, 4};
 }
 
 template <int G>
