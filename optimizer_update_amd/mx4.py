@@ -10,7 +10,7 @@ products grouped by expert (binding of ``liboptimizer_mx4.so``,
     y = mx4_linear(x, w)                      the layer with its gradients (straight through
     y = mx4_grouped_linear(x, w, offsets)     the roundings), all three products in 4 bits
     Mx4Weight(w)                              both 4-bit forms of a weight, refreshed by its
-                                              optimizer's step (``mx4=`` of the collections)
+                                              optimizer's steps (``attach_mx4``)
 
 As in the rest of the package, functions check and marshal arguments; all
 arithmetic runs in the HIP kernels.  Every call goes to the current stream of
@@ -439,8 +439,8 @@ class Mx4Weight:
     """The 4-bit forms of a weight [N, K] or [E, N, K] for the layers below:
     ``q`` along K (forward) and ``qt`` along N (the input's gradient).
     ``refresh()`` quantises the weight's present values into them; an optimizer
-    built with ``mx4=[...]`` does so after every step, so that the passes in
-    between (micro-batches) read the 4-bit forms alone."""
+    that it is given to (``attach_mx4``) does so after every step, so that the
+    passes in between (micro-batches) read the 4-bit forms alone."""
 
     def __init__(self, weight: torch.Tensor):
         if weight.dim() not in (2, 3):

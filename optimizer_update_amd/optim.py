@@ -22,6 +22,9 @@ elsewhere (torch's default) makes the next backward allocate new gradient
 tensors, and the plan is then rebuilt on them (a step with a parameter whose
 ``.grad`` is None raises).  The optimizers' own ``zero_grad()`` zeroes the
 captured gradients in place, which keeps the plan.
+
+``attach_mx4`` gives an optimizer the 4-bit forms of weights (``Mx4Weight``)
+that its steps keep up to date.
 """
 from __future__ import annotations
 
@@ -30,9 +33,32 @@ import torch
 from . import (DTYPES, TWO_STATE, Graph, HParams, Plan, Plan8, _kind, _on_device, _ptr, _raw_stream,
                _tensor_args, check, clip_workspace, load, optimizer_update_8bit_blockwise,
                optimizer_update_32bit, optimizer_update_32bit_clip, state8_sizes, state_sizes)
+from .mx4 import Mx4Weight
 
 
-class _Collection:
+class _Mx4Copies:
+    """The 4-bit copies of weights that an optimizer keeps up to date."""
+    _mx4 = ()
+
+    def attach_mx4(self, weights) -> None:
+        """Refresh these ``Mx4Weight``s (of parameters of this optimizer) after
+        every step, on the step's stream: the products in between read the
+        4-bit forms alone.  Replaces what was attached before."""
+        weights = list(weights)
+        mine = {p.data_ptr() for p in self.params}
+        for w in weights:
+            if not isinstance(w, Mx4Weight):
+                raise ValueError("attach_mx4 takes Mx4Weight objects")
+            if w.weight.data_ptr() not in mine:
+                raise ValueError("the weight is not a parameter of this optimizer")
+        self._mx4 = weights
+
+    def _refresh_mx4(self, stream) -> None:
+        for w in self._mx4:
+            w.refresh(stream)
+
+
+class _Collection(_Mx4Copies):
     kind = "adam"
 
     def __init__(self, params, hp: HParams, grads=None, max_unorm: float = 0.0,
@@ -89,6 +115,7 @@ class _Collection:
             self.plan.graph_step(self.hp, self.step_count, stream)
         else:
             self.plan.step(self.hp, self.step_count, stream)
+        self._refresh_mx4(stream)
 
     @torch.no_grad()
     def step_per_tensor(self, stream=None) -> None:
@@ -109,6 +136,7 @@ class _Collection:
                                             eps=h.eps, weight_decay=h.weight_decay,
                                             skip_zeros=h.skip_zeros,
                                             decay_after=self.decay_after, stream=stream)
+            self._refresh_mx4(stream)
             return
         if self._direct is None:
             for p, g, s1, s2 in self.segments():   # full checks once
@@ -127,6 +155,7 @@ class _Collection:
                 st = fn(*args, *tail)
                 if st:
                     check(st, lib)
+        self._refresh_mx4(stream)
 
     def state_dict(self) -> dict:
         return {"step": self.step_count,
@@ -267,7 +296,7 @@ def _zero_in_place(followed, grads) -> None:
     torch._foreach_zero_(list(grads))
 
 
-class _Collection8:
+class _Collection8(_Mx4Copies):
     """Tensors of at least ``min_8bit_size`` elements keep 8-bit block-wise
     states (uint8 codes, fp32 absmax per 256 elements) and step through one
     8-bit plan; smaller tensors keep fp32 states and step through one 32-bit
@@ -328,11 +357,13 @@ class _Collection8:
             if self._graph is None:
                 self._graph = Graph([self.plan32], [self.plan8])
             self._graph.step(self.hp, self.step_count, stream)
+            self._refresh_mx4(stream)
             return
         if self.plan8 is not None:
             self.plan8.step(self.hp, self.step_count, stream)
         if self.plan32 is not None:
             self.plan32.step(self.hp, self.step_count, stream)
+        self._refresh_mx4(stream)
 
     @torch.no_grad()
     def step_per_tensor(self, stream=None) -> None:
@@ -348,6 +379,7 @@ class _Collection8:
                 optimizer_update_8bit_blockwise(self.kind, p, g, *st[1:], **kw)
             else:
                 optimizer_update_32bit(self.kind, p, g, *st[1:], **kw)
+        self._refresh_mx4(stream)
 
     def state_dict(self) -> dict:
         return {"step": self.step_count,

@@ -181,7 +181,7 @@ def _random_held(rows, k, seed, lo=119, hi=135, lead=()):
 
 
 # rows, columns and depths around every border of the kernels' tiles
-PRODUCTS = [(1, 1, 1), (1, 64, 128), (1, 4096, 1024), (2, 33, 33), (3, 300, 4000), (15, 17, 500), (16, 16, 129),
+PRODUCTS = [(13, 70, 4100), (16, 33, 3000), (5, 16500, 300), (2, 20000, 140), (1, 1, 1), (1, 64, 128), (1, 4096, 1024), (2, 33, 33), (3, 300, 4000), (15, 17, 500), (16, 16, 129),
             (16, 512, 384), (17, 65, 256), (31, 127, 640), (32, 128, 100), (33, 129, 1100), (63, 40, 2048), (64, 64, 64),
             (65, 200, 900), (100, 1000, 257), (128, 256, 512), (129, 255, 511), (130, 2000, 700), (255, 129, 383),
             (256, 256, 256), (257, 257, 1025), (300, 70, 5000), (512, 512, 4096), (700, 900, 1300), (1030, 1100, 640)]
@@ -451,6 +451,54 @@ def test_grouped_linear_forward_and_gradients(counts, front, back, dtype):
     y2 = ou.mx4_grouped_linear(x2, held, off.cuda())
     y2.backward(dy.cuda())
     assert torch.equal(y2, y) and torch.equal(x2.grad, xd.grad) and torch.equal(held.weight.grad, wd.grad)
+
+
+@pytest.mark.parametrize("make", [lambda p: ou.AdamW32(p, lr=1e-2), lambda p: ou.AdamW8bit(p, lr=1e-2),
+                                  lambda p: ou.Lion32(p, lr=1e-3), lambda p: ou.AdamW32(p, lr=1e-2, max_unorm=1.0)])
+@pytest.mark.parametrize("how", ["step", "graph", "per tensor"])
+def test_training_with_kept_forms(make, how):
+    """Two layers and an expert layer trained through kept 4-bit forms, two
+    micro-batches a step: every step's products are those of the weights that
+    the optimizer has just updated, bit for bit."""
+    m, k, h, n = 60, 96, 128, 64
+    off = _offsets([20, 0, 40]).cuda()
+    w1, w2 = (torch.nn.Parameter(_values(s, BF16, i, special=False).cuda() * 0.1) for i, s in ((80, (h, k)), (81, (n, h))))
+    we = torch.nn.Parameter(_values((3, n, n), BF16, 82, special=False).cuda() * 0.1)
+    params = [w1, w2, we]
+    for p in params:
+        p.grad = torch.zeros_like(p)
+    opt = make(params)
+    held = [ou.Mx4Weight(p) for p in params]
+    opt.attach_mx4(held)
+    for step in range(3):
+        opt.zero_grad()
+        want = [torch.zeros_like(p) for p in params]
+        for micro in range(2):
+            x = _values((m, k), BF16, 90 + 2 * step + micro, special=False).cuda()
+            outs = []
+            for a, b, c in (held, params):
+                y = ou.mx4_grouped_linear(ou.mx4_linear(ou.mx4_linear(x, a).relu(), b), c, off)
+                outs.append(y)
+            assert torch.equal(outs[0], outs[1])
+            dy = _values((m, n), BF16, 70 + micro, special=False).cuda()
+            grads = torch.autograd.grad(outs[1], params, dy)
+            outs[0].backward(dy)                      # adds to .grad in place
+            for t, g in zip(want, grads):
+                t += g
+        for p, t in zip(params, want):
+            assert torch.equal(p.grad, t)
+        before = [p.detach().clone() for p in params]
+        opt.step_per_tensor() if how == "per tensor" else opt.step(graph=how == "graph")
+        for p, b, q in zip(params, before, held):
+            assert not torch.equal(p, b)
+            fresh = ou.mx4_quantize_both(p.detach())
+            for got, new in zip((q.q, q.qt), fresh):
+                assert torch.equal(got.codes, new.codes) and torch.equal(got.scales, new.scales)
+    with pytest.raises(ValueError):
+        opt.attach_mx4([ou.Mx4Weight(torch.ones(4, 4, device="cuda"))])
+    with pytest.raises(ValueError):
+        opt.attach_mx4([w1])
+    opt.close()
 
 
 def test_results_do_not_change_from_call_to_call():
