@@ -448,6 +448,7 @@ class Mx4Weight:
         if not weight.is_contiguous():
             raise ValueError("weight must be contiguous")
         self.weight = weight
+        self.version = 0   # of the forms: a backward pass refuses later ones than its forward pass read
         self.q, self.qt = mx4_quantize_both(weight.detach())
 
     def refresh(self, stream=None) -> None:
@@ -457,6 +458,7 @@ class Mx4Weight:
         if w.shape != self.q.shape or not w.is_contiguous():
             raise ValueError("the weight changed its shape or layout")
         _run(w.get_device(), stream, self._refresh, w, dt)
+        self.version += 1
 
     def _refresh(self, w, dt, handle):
         *lead, r, c = w.shape
@@ -466,70 +468,163 @@ class Mx4Weight:
             _fail(st)
 
 
-class _Linear(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, x, w, held):
-        need_x, need_w = ctx.needs_input_grad[:2]
-        q, qt = (held.q, held.qt) if held is not None else _quantize(w, True, need_x, None)
-        ctx.x_dtype, ctx.w_dtype = x.dtype, w.dtype
-        if need_w:
-            xq, xt = mx4_quantize_both(x)
-            y = mx4_matmul(xq, q, x.dtype)
-        else:
-            xt = None
-            y = mx4_matmul(x, q)
-        ctx.held = (qt if need_x else None, xt)
-        return y
+class _Room:
+    """Places of held matrices in one buffer: the layers' own forms, which
+    nobody else sees, are spared a tensor for each of their parts."""
 
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, dy):
-        need_x, need_w = ctx.needs_input_grad[:2]
-        qt, xt = ctx.held
-        dy = dy.contiguous()
-        dx = dw = None
-        if need_w:
-            dq, dt = _quantize(dy, need_x, True, None)
-            dw = mx4_matmul(dt, xt, ctx.w_dtype)
-            if need_x:
-                dx = mx4_matmul(dq, qt, ctx.x_dtype)
-        elif need_x:
-            dx = mx4_matmul(dy, qt, ctx.x_dtype)
-        return dx, dw, None
+    __slots__ = ("bytes",)
+
+    def __init__(self):
+        self.bytes = 0
+
+    def form(self, rows: int, columns: int) -> tuple[int, int]:
+        """Offsets of codes and scales of `rows` rows of padded `columns`."""
+        codes = self.bytes
+        scales = codes + rows * columns // 2
+        self.bytes = scales + -(-rows * columns // MX4_BLOCK // 16) * 16
+        return codes, scales
+
+    def make(self, device) -> tuple[torch.Tensor, int]:
+        buf = torch.empty(self.bytes, dtype=torch.uint8, device=device)
+        return buf, buf.data_ptr()
 
 
-class _GroupedLinear(torch.autograd.Function):
+def _rows_apart(x: torch.Tensor) -> torch.Tensor:
+    """x, or a copy whose columns are neighbours and whose rows do not overlap."""
+    r, c = x.shape
+    return x if x.is_contiguous() or (c <= 1 or x.stride(1) == 1) and (r <= 1 or x.stride(0) >= c) else x.contiguous()
+
+
+def _place(base, offsets):
+    return (None, None) if offsets is None else (base + offsets[0], base + offsets[1])
+
+
+class _Layer(torch.autograd.Function):
+    """Both layers; offsets: None for the plain one."""
+
     @staticmethod
     def forward(ctx, x, w, offsets, held):
+        return _run(x.get_device(), None, _Layer._forward, ctx, _rows_apart(x), w, offsets, held)
+
+    @staticmethod
+    def _forward(ctx, x, w, offsets, held, handle):
+        lib, device = load_mx4(), x.device
         need_x, need_w = ctx.needs_input_grad[:2]
-        q, qt = (held.q, held.qt) if held is not None else _quantize(w, True, need_x, None)
-        ctx.x_dtype, ctx.w_dtype, ctx.rows = x.dtype, w.dtype, x.shape[0]
-        if need_w:
-            xq, xt = mx4_quantize_grouped(x, offsets)
-            y = mx4_grouped_matmul(xq, q, offsets, x.dtype)
+        m, k = x.shape
+        n, groups = w.shape[-2], w.shape[0] if offsets is not None else 1
+        pk, rs = _columns(k), _row_stride(x, "x")
+        xd, off = DTYPES[x.dtype], None if offsets is None else offsets.data_ptr()
+        held_m = _columns(m) if offsets is None else _grouped_columns(m, groups)
+        temp, kept = _Room(), _Room()
+        wq = temp.form(groups * n, pk) if held is None else None
+        wt = kept.form(groups * k, _columns(n)) if held is None and need_x else None
+        xq = temp.form(m, pk) if need_w else None
+        xt = kept.form(k, held_m) if need_w else None
+        grow = 0
+        if not need_w:   # x goes in as values
+            grow = _matmul_workspace(m, n, k, True) if off is None else _grouped_workspace(m, n, k, groups, True)
+        ws = temp.bytes
+        temp.bytes += grow
+        buf, at = temp.make(device)
+        keep, kp = kept.make(device)
+        st = 0
+        if held is None:
+            st = lib.ou_mx4_quantize(DTYPES[w.dtype], w.data_ptr(), groups, n, k, k, n * k, *_place(at, wq), *_place(kp, wt),
+                                     handle)
+            right = _place(at, wq)
         else:
-            xt = None
-            y = mx4_grouped_matmul(x, q, offsets)
-        ctx.held = (qt if need_x else None, xt)
-        ctx.save_for_backward(offsets)
+            right = _ptrs(held.q)
+        if st:
+            _fail(st)
+        y = torch.empty((m, n), dtype=x.dtype, device=device)
+        if need_w:
+            if off is None:
+                st = lib.ou_mx4_quantize(xd, x.data_ptr(), 1, m, k, rs, 0, *_place(at, xq), *_place(kp, xt), handle)
+            else:
+                st = lib.ou_mx4_quantize_grouped(xd, x.data_ptr(), m, k, rs, off, groups, *_place(at, xq),
+                                                 *_place(kp, xt), handle)
+            if st:
+                _fail(st)
+        _multiply(lib, xd, None if need_w else x, rs, _place(at, xq), m, xd, right, n, k, off, groups, y, at + ws, grow,
+                  handle)
+        ctx.shape = (m, n, k, groups, held_m)
+        ctx.types = (x.dtype, w.dtype)
+        ctx.keep, ctx.wt, ctx.xt = keep, wt, xt
+        ctx.held = held if need_x else None
+        ctx.version = None if held is None else held.version
+        if offsets is not None:
+            ctx.save_for_backward(offsets)
         return y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
+        if ctx.held is not None and ctx.held.version != ctx.version:
+            raise RuntimeError("the Mx4Weight was refreshed between the forward and the backward pass")
+        return _run(dy.get_device(), None, _Layer._backward, ctx, _rows_apart(dy))
+
+    @staticmethod
+    def _backward(ctx, dy, handle):
+        lib, device = load_mx4(), dy.device
         need_x, need_w = ctx.needs_input_grad[:2]
-        qt, xt = ctx.held
-        offsets, = ctx.saved_tensors
-        dy = dy.contiguous()
+        m, n, k, groups, held_m = ctx.shape
+        x_dtype, w_dtype = ctx.types
+        offsets, = ctx.saved_tensors or (None,)
+        off = None if offsets is None else offsets.data_ptr()
+        pn, rs, yd = _columns(n), _row_stride(dy, "the gradient"), DTYPES[dy.dtype]
+        kp = ctx.keep.data_ptr()
+        temp = _Room()
+        dq = temp.form(m, pn) if need_x and need_w else None
+        dt = temp.form(n, held_m) if need_w else None
+        ws = temp.bytes
+        grow = 0
+        if not need_w:
+            grow = _matmul_workspace(m, k, n, True) if off is None else _grouped_workspace(m, k, n, groups, True)
+            temp.bytes += grow
+        buf, at = temp.make(device)
         dx = dw = None
         if need_w:
-            dq, dt = mx4_quantize_grouped(dy, offsets, rows=need_x)
-            dw = mx4_grouped_outer(dt, xt, offsets, ctx.rows, ctx.w_dtype)
-            if need_x:
-                dx = mx4_grouped_matmul(dq, qt, offsets, ctx.x_dtype)
-        elif need_x:
-            dx = mx4_grouped_matmul(dy, qt, offsets, ctx.x_dtype)
+            if off is None:
+                st = lib.ou_mx4_quantize(yd, dy.data_ptr(), 1, m, n, rs, 0, *_place(at, dq), *_place(at, dt), handle)
+            else:
+                st = lib.ou_mx4_quantize_grouped(yd, dy.data_ptr(), m, n, rs, off, groups, *_place(at, dq),
+                                                 *_place(at, dt), handle)
+            if st:
+                _fail(st)
+            if off is None:
+                dw = torch.empty((n, k), dtype=w_dtype, device=device)
+                _multiply(lib, 0, None, 0, _place(at, dt), n, DTYPES[w_dtype], _place(kp, ctx.xt), k, m, None, 0, dw, None,
+                          0, handle)
+            else:
+                dw = torch.empty((groups, n, k), dtype=w_dtype, device=device)
+                st = lib.ou_mx4_grouped_outer(DTYPES[w_dtype], *_place(at, dt), n, *_place(kp, ctx.xt), k, m, off, groups,
+                                              dw.data_ptr(), handle)
+                if st:
+                    _fail(st)
+        if need_x:
+            dx = torch.empty((m, k), dtype=x_dtype, device=device)
+            right = _ptrs(ctx.held.qt) if ctx.held is not None else _place(kp, ctx.wt)
+            _multiply(lib, yd, None if need_w else dy, rs, _place(at, dq), m, DTYPES[x_dtype], right, k, n, off, groups, dx,
+                      at + ws, grow, handle)
         return dx, dw, None, None
+
+
+def _multiply(lib, xd, x, rs, left, m, od, right, n, k, off, groups, out, ws, need, handle):
+    """A product of a layer: x as values, or the held matrix `left`."""
+    ws = ws if need else None
+    tail = (out.data_ptr(), n)
+    if off is None:
+        if x is None:
+            st = lib.ou_mx4_matmul(od, *left, m, *right, n, k, *tail, None, 0, handle)
+        else:
+            st = lib.ou_mx4_matmul_values(xd, x.data_ptr(), m, rs, od, *right, n, k, *tail, ws, need, handle)
+    elif x is None:
+        st = lib.ou_mx4_grouped_matmul(od, *left, m, *right, n, k, off, groups, *tail, 1, None, 0, handle)
+    else:
+        st = lib.ou_mx4_grouped_matmul_values(xd, x.data_ptr(), m, rs, od, *right, n, k, off, groups, *tail, 1, ws, need,
+                                              handle)
+    if st:
+        _fail(st)
 
 
 def _layer_operands(x, w, dims: int):
@@ -551,10 +646,13 @@ def mx4_linear(x: torch.Tensor, w) -> torch.Tensor:
         y = Q(x) Q(w)^T,  dx = Q(dy) Q(w^T)^T,  dw = Q(dy^T) Q(x^T)^T,
     each summed in binary32 and rounded once to the dtype of x (y, dx) or w
     (dw).  x is [..., K], w [N, K] or an ``Mx4Weight`` (its 4-bit forms are
-    used as they are, its ``weight`` gets the gradient).  For the backward
-    pass 4-bit forms are kept, not x."""
+    used as they are, its ``weight`` gets the gradient; it must not be
+    refreshed before the backward pass).  For the backward pass 4-bit forms
+    are kept, not x."""
     held, weight = _layer_operands(x, w, 2)
-    y = _Linear.apply(x.reshape(-1, x.shape[-1]), weight, held)
+    if x.dim() == 2:
+        return _Layer.apply(x, weight, None, held)
+    y = _Layer.apply(x.reshape(math.prod(x.shape[:-1]), x.shape[-1]), weight, None, held)
     return y.view(*x.shape[:-1], weight.shape[0])
 
 
@@ -567,4 +665,4 @@ def mx4_grouped_linear(x: torch.Tensor, w, offsets: torch.Tensor) -> torch.Tenso
         raise ValueError("x must be [T, K]")
     if _offsets(offsets, x.get_device()) != weight.shape[0]:
         raise ValueError(f"offsets name {offsets.shape[0] - 1} groups, w holds {weight.shape[0]}")
-    return _GroupedLinear.apply(x, weight, offsets, held)
+    return _Layer.apply(x, weight, offsets, held)

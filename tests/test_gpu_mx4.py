@@ -580,6 +580,25 @@ def test_rows_far_behind_4_gib():
     assert np.array_equal(R.held(again), R.held(tail))
 
 
+def test_layers_take_any_strides():
+    """An input and a gradient whose rows overlap or whose columns are apart
+    are copied; the 4-bit forms must stay until the backward pass."""
+    x, w = _values((40, 96), BF16, 83).cuda(), _values((64, 96), BF16, 84).cuda()
+    for view in (x.t().contiguous().t(), x[:1].expand(40, 96), torch.cat((x, x), 1)[:, 3:99], x[::2]):
+        v = view.detach().requires_grad_()
+        d = v.detach().contiguous().requires_grad_()
+        for dy in (torch.ones(view.shape[0], 64, device="cuda", dtype=BF16).t().contiguous().t(),
+                   torch.ones((), device="cuda", dtype=BF16).expand(view.shape[0], 64)):
+            got = torch.autograd.grad(ou.mx4_linear(v, w), v, dy)[0]
+            want = torch.autograd.grad(ou.mx4_linear(d, w), d, dy.contiguous())[0]
+            assert torch.equal(got, want)
+    held = ou.Mx4Weight(w.clone().requires_grad_())
+    y = ou.mx4_linear(x.clone().requires_grad_(), held)
+    held.refresh()
+    with pytest.raises(RuntimeError):
+        y.sum().backward()
+
+
 def test_refusals_on_the_device():
     x = torch.ones(4, 64, device="cuda")
     q = ou.mx4_quantize(x)
