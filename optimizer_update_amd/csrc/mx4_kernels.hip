@@ -827,9 +827,19 @@ __device__ __forceinline__ void multiply_add(f32x4& acc, i32x4 b, i32x4 a, int s
 }
 __device__ __forceinline__ void settle_products() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const uint8_t* p, uint32_t bytes)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(uint64_t address, uint32_t bytes)
 {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, static_cast<int>(bytes), 0x00020000);
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(address), 0, static_cast<int>(bytes), 0x00020000);
+}
+
+// f(0), f(1), .. f(N - 1), each with its index as a constant.
+template <int N, int X = 0, class F>
+__device__ __forceinline__ void each(F&& f)
+{
+    if constexpr (X < N) {
+        f(std::integral_constant<int, X>{});
+        each<N, X + 1>(f);
+    }
 }
 
 // Four waves in a square, 16 WM x 16 WN results each.  A pair is two k-steps,
@@ -925,46 +935,94 @@ __global__ __launch_bounds__(256 * KG, 1) void k_matmul_tile(MatmulArgs p)
     // and bring zeros
     const uint32_t odd = steps & 1 ? pairs - 1 : ~0u;
     const uint32_t cvoff_odd = cvoff | (((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7)) & 4 ? 0x80000000u : 0);
-    auto move_scales = [&](uint32_t quad, int part) {
-        const int i = (part * 4 + wave) & ((BM + BN) / 32 - 1);
-        const uint32_t at = quad * 32, dst = lds0 + 2 * kCodes + (quad & 1) * kScales + i * 1024;
-        const bool left = i < BM / 32;
-        const uint8_t* src = left ? asc : bsc;
-        const uint32_t end = left ? ase : bse, row = static_cast<uint32_t>(left ? i : i - BM / 32) * 32;
-        to_lds(resource(src + at, quad * 4 < pairs ? end - at : 0), svoff + row * srow, dst);
-    };
-    // transfer i of pair q, nothing behind the last pair: the codes, and the
-    // quarter of the scales that is due (those of pairs 4 u .. come with the
-    // pairs 4 u - 3 .. 4 u)
-    auto move = [&](uint32_t q, int i) {
-        if (i == kMoves - 1) {
-            move_scales((q + 3) >> 2, (q + 3) & 3);
-            return;
+    // The transfers of the pair whose turn it is: where from (a resource each,
+    // of no bytes behind the last pair), and where to.  The quarter of the
+    // scales that is due comes with them (those of pairs 4 u .. with the pairs
+    // 4 u - 3 .. 4 u).
+    uint64_t pa = reinterpret_cast<uint64_t>(ac), pb = reinterpret_cast<uint64_t>(bc), ps;
+    uint32_t ea = pairs > 0 ? ace : 0, eb = pairs > 0 ? bce : 0, es;
+    uint32_t from = odd == 0 ? cvoff_odd : cvoff, to = lds0 + wave * 1024, sfrom, sto;
+    // scale transfers of four pairs: BM / 32 of a's, then as many of b's
+    static_assert(BM == BN, "a's and b's scales are told apart by a bit");
+    const uint64_t asc0 = reinterpret_cast<uint64_t>(asc), bsc0 = reinterpret_cast<uint64_t>(bsc);
+    auto scale_index = [&](uint32_t part) { return (part * 4 + wave) & ((BM + BN) / 32 - 1); };
+    auto of_b = [&](uint32_t i) { return (i / (BM / 32)) & 1; };   // 0 or 1
+    auto aim_scales = [&](uint32_t quad, uint32_t part, int step) {
+        const uint32_t i = scale_index(part);
+        if (step == 0) {
+            sfrom = svoff + (i & (BM / 32 - 1)) * 32 * srow;
+            asm volatile("" : "+v"(sfrom));
+        } else if (step == 1) {
+            sto = lds0 + 2 * kCodes + (quad & 1) * kScales + i * 1024;
+            asm volatile("" : "+s"(sto));
+        } else if (step == 2) {
+            ps = (asc0 ^ ((asc0 ^ bsc0) & (uint64_t(0) - of_b(i)))) + quad * 32;
+            asm volatile("" : "+s"(ps));
+        } else {
+            const uint32_t on = 0u - static_cast<uint32_t>(quad * 4 < pairs);
+            es = ((ase ^ ((ase ^ bse) & (0u - of_b(i)))) - quad * 32) & on;
+            asm volatile("" : "+s"(es));
         }
-        const uint32_t at = q * 128, dst = lds0 + (q & 1) * kCodes + wave * 1024 + i * 4096;
-        const uint32_t from = q == odd ? cvoff_odd : cvoff;
-        if (i < BM / 32)
-            to_lds(resource(ac + at, q < pairs ? ace - at : 0), from + i * 32 * crow, dst);
+    };
+    auto move_scales = [&]() { to_lds(resource(ps, es), sfrom, sto); };
+    auto move = [&](int i) {
+        if (i == kMoves - 1)
+            move_scales();
+        else if (i < BM / 32)
+            to_lds(resource(pa, ea), from + i * 32 * crow, to + i * 4096);
         else
-            to_lds(resource(bc + at, q < pairs ? bce - at : 0), from + (i - BM / 32) * 32 * crow, dst);
+            to_lds(resource(pb, eb), from + (i - BM / 32) * 32 * crow, to + i * 4096);
+    };
+    // Turns to pair q in kAims steps of a few scalar instructions, which are
+    // laid apart: a wave is alone on its SIMD, and more of them between two
+    // matrix instructions than their 16 cycles hold would stop those.
+    constexpr int kAims = 7;
+    auto aim = [&](uint32_t q, int step) {
+        asm volatile("" : "+s"(q));   // not to be computed earlier
+        if (step == 0) {
+            pa += 128;
+            pb += 128;
+            asm volatile("" : "+s"(pa));
+            asm volatile("" : "+s"(pb));
+        } else if (step == 1) {
+            ea = q < pairs ? ea - 128 : 0;
+            eb = q < pairs ? eb - 128 : 0;
+            asm volatile("" : "+s"(ea));
+            asm volatile("" : "+s"(eb));
+        } else if (step == 2) {
+            from = q == odd ? cvoff_odd : cvoff;
+            asm volatile("" : "+v"(from));
+            to = lds0 + (q & 1) * kCodes + wave * 1024;
+            asm volatile("" : "+s"(to));
+        } else {
+            aim_scales((q + 3) >> 2, (q + 3) & 3, step - 3);
+        }
     };
 
     // a lane's place in LDS: row r of a 16-row fragment, piece 4 (k-step) + g
     const int wm = wave >> 1, wn = wave & 1, shift = 8 * g;
-    const uint8_t* cbase[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) cbase[k] = lds + r * 128 + (((4 * k + g) ^ (r >> 1)) * 16);
-    const uint8_t* const sbase = lds + 2 * kCodes + r * 32;
+    const uint32_t place[2] = {static_cast<uint32_t>(r * 128 + ((g ^ (r >> 1)) * 16)),
+                               static_cast<uint32_t>(r * 128 + (((4 + g) ^ (r >> 1)) * 16))};
+    uint32_t codes_at[2] = {place[0], place[1]};   // of the pair to be read
+    uint32_t scales_at = 0;
+    auto find_codes = [&](uint32_t q, int k) {
+        codes_at[k] = place[k] + (q & 1) * kCodes;
+        asm volatile("" : "+v"(codes_at[k]));
+    };
+    auto find_scales = [&](uint32_t q) {
+        asm volatile("" : "+s"(q));
+        scales_at = 2 * kCodes + ((q >> 2) & 1) * kScales + (q & 1) * 8 + r * 32 + ((((q >> 1) & 1) ^ ((r >> 3) & 1)) * 16);
+        asm volatile("" : "+v"(scales_at));
+    };
     f32x4 acc[WM][WN];
     i32x4 fa[2][WM], fb[2][WN];   // fragments by k-step of the pair
     u32x2 qa[WM], qb[WN];         // scale codes of a pair, four blocks a word
     int sa[2][WM], sb[2][WN];     // scale codes by k-step, the lane's own
     constexpr int kReads = WM + WN;
-    // fragment x of k-step k of pair q (a's and b's in turn), and with the
-    // first k-step its scales
-    auto read = [&](uint32_t q, int k, int x) {
-        const uint8_t* c = cbase[k] + (q & 1) * kCodes;
-        const uint8_t* w = sbase + ((q >> 2) & 1) * kScales + ((((q >> 1) & 1) ^ ((r >> 3) & 1)) * 16) + (q & 1) * 8;
+    // fragment x of k-step k of the pair that codes_at and scales_at name (a's
+    // and b's in turn), and with the first k-step its scales
+    auto read = [&](int k, int x) {
+        const uint8_t *c = lds + codes_at[k], *w = lds + scales_at;
         const int i = x >> 1;
         if (x & 1) {
             fb[k][i] = *reinterpret_cast<const i32x4*>(c + BM * 128 + (wn * WN + i) * 2048);
@@ -986,15 +1044,14 @@ __global__ __launch_bounds__(256 * KG, 1) void k_matmul_tile(MatmulArgs p)
     // the first k-step's scales.
     auto multiply = [&](auto kstep, uint32_t width, auto next) {
         constexpr int K = decltype(kstep)::value;
-#pragma unroll
-        for (int x = 0; x < WM * WN; ++x) {
-            const int i = x / WN, j = x % WN;
-            if (K == 0 && j == 0) take_scale(0, i, width);
-            if (K == 0 && i == 0) take_scale(0, WM + j, width);
+        each<WM * WN>([&](auto index) {
+            constexpr int x = decltype(index)::value, i = x / WN, j = x % WN;
+            if constexpr (K == 0 && j == 0) take_scale(0, i, width);
+            if constexpr (K == 0 && i == 0) take_scale(0, WM + j, width);
             multiply_add(acc[i][j], fb[K][j], fa[K][i], sb[K][j], sa[K][i]);
-            next(x);
+            next(index);
             __builtin_amdgcn_sched_barrier(0);
-        }
+        });
     };
     using First = std::integral_constant<int, 0>;
     using Second = std::integral_constant<int, 1>;
@@ -1003,6 +1060,11 @@ __global__ __launch_bounds__(256 * KG, 1) void k_matmul_tile(MatmulArgs p)
     constexpr int kReadEvery = kProducts / kReads / 2 ? kProducts / kReads / 2 : 1;
     constexpr int kMoveEvery = 3 * kProducts / 2 / kMoves;   // over three quarters of a pair
     constexpr int kEarly = kProducts / kMoveEvery < kMoves ? kProducts / kMoveEvery : kMoves;   // with the second k-step
+    // behind the last transfer of the pair before (move kMoves - 1)
+    constexpr int kFirstAim = kMoves * kMoveEvery - kProducts > 0 ? kMoves * kMoveEvery - kProducts : 0;
+    constexpr int kAimEvery = (kProducts - kFirstAim) / (kAims + 2);   // 0: all behind the last product
+    constexpr int kFindScales = kAimEvery ? kFirstAim + kAims * kAimEvery : kProducts - 1;
+    constexpr int kFindCodes = kAimEvery ? kFindScales + kAimEvery : kProducts - 1;
     static_assert(kReadEvery * kReads <= kProducts && kMoveEvery >= 1, "spacing");
 
     auto zero = [&]() {
@@ -1017,34 +1079,55 @@ __global__ __launch_bounds__(256 * KG, 1) void k_matmul_tile(MatmulArgs p)
     if (turns == 0) zero();
     if (turns > 0) {
 #pragma unroll
-        for (int part = 0; part < 3; ++part) move_scales(0, part);
+        for (int part = 0; part < 4; ++part) {
 #pragma unroll
-        for (int i = 0; i < kMoves; ++i) move(0, i);
+            for (int step = 0; step < 4; ++step) aim_scales(0, part, step);
+            if (part < 3) move_scales();
+        }
 #pragma unroll
-        for (int i = 0; i < kEarly; ++i) move(1, i);
+        for (int i = 0; i < kMoves; ++i) move(i);
+#pragma unroll
+        for (int i = 0; i < kAims; ++i) aim(1, i);
+#pragma unroll
+        for (int i = 0; i < kEarly; ++i) move(i);
+        find_scales(0);
         zero();   // while they are on their way
         wait_transfers<kEarly>();
         block_barrier();
 #pragma unroll
-        for (int x = 0; x < kReads; ++x) read(0, 0, x);
+        for (int x = 0; x < kReads; ++x) read(0, x);
         settle_products();   // and behind acc's first values
         for (uint32_t q = 0; q < turns; ++q) {
-            // the first k-step; the last transfers of pair q + 1 start here
-            multiply(First{}, KG == 1 || q < pairs ? 8 : 0, [&](int x) {
-                if (x % kReadEvery == 0 && x / kReadEvery < kReads) read(q, 1, x / kReadEvery);
+            // The first k-step of pair q.  The last transfers of pair q + 1
+            // start; then the aim turns to pair q + 2.
+            multiply(First{}, KG == 1 || q < pairs ? 8 : 0, [&](auto index) {
+                constexpr int x = decltype(index)::value, y = kProducts + x, z = x - kFirstAim;
+                if constexpr (x % kReadEvery == 0 && x / kReadEvery < kReads) read(1, x / kReadEvery);
                 // the second k-step's scales, before the next pair's replace them
-                if (x >= kProducts - kReads) take_scale(1, x - (kProducts - kReads), q == odd || (KG > 1 && q >= pairs) ? 0 : 8);
-                const int y = kProducts + x;
-                if (y % kMoveEvery == kMoveEvery - 1 && y / kMoveEvery < kMoves) move(q + 1, y / kMoveEvery);
+                if constexpr (x >= kProducts - kReads)
+                    take_scale(1, x - (kProducts - kReads), q == odd || (KG > 1 && q >= pairs) ? 0 : 8);
+                if constexpr (y % kMoveEvery == kMoveEvery - 1 && y / kMoveEvery < kMoves) move(y / kMoveEvery);
+                if constexpr (kAimEvery > 0) {
+                    if constexpr (z >= 0 && z % kAimEvery == 0 && z / kAimEvery < kAims) aim(q + 2, z / kAimEvery);
+                } else if constexpr (x == kProducts - 1) {
+                    each<kAims>([&](auto step) { aim(q + 2, decltype(step)::value); });
+                }
+                // and the reads to pair q + 1
+                if constexpr (x == kFindCodes) find_codes(q + 1, 0);
+                if constexpr (x == kFindScales) find_scales(q + 1);
             });
             // all waves hold the second k-step in registers, pair q + 1 is here
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
             wait_transfers<0>();
             block_barrier();
             __builtin_amdgcn_sched_barrier(0);
-            multiply(Second{}, 8, [&](int x) {
-                if (x % kReadEvery == 0 && x / kReadEvery < kReads) read(q + 1, 0, x / kReadEvery);
-                if (x % kMoveEvery == kMoveEvery - 1 && x / kMoveEvery < kMoves) move(q + 2, x / kMoveEvery);
+            multiply(Second{}, 8, [&](auto index) {
+                constexpr int x = decltype(index)::value;
+                if constexpr (x % kReadEvery == 0 && x / kReadEvery < kReads) read(0, x / kReadEvery);
+                if constexpr (x % kMoveEvery == kMoveEvery - 1 && x / kMoveEvery < kMoves) move(x / kMoveEvery);
+                if constexpr (x == kProducts - 1) {
+                    find_codes(q + 1, 1);
+                }
             });
         }
         wait_transfers<0>();   // none may arrive in what LDS holds next
