@@ -189,6 +189,13 @@ Choice choose_grouped(int64_t rows, int64_t n, int64_t steps, int32_t groups)
     return choose(cut(rows, g), n, steps, g < rows ? g : (rows > 0 ? rows : 1), rows < 16 ? rows : 16);
 }
 
+// Results beyond this leave by non-temporal stores: they would only push
+// others out of the 256 MiB last cache.  256 MiB of them (16 x 4096 x 2048,
+// 512 rows each) 112 us against 125, and the product behind it 67 against 81;
+// 128 MiB (8192 x 8192, k = 4096) 148 against 135 us, where the next reader
+// finds them in the cache otherwise.
+constexpr int64_t kKeptBytes = int64_t(192) << 20;
+
 int launch_matmul(int out_dtype, int grouping, const Choice& c, MatmulArgs& p, int64_t batch, void* stream)
 {
     const TileKernel t = c.tile ? matmul_tile_kernel(out_dtype, grouping, c.tile) : TileKernel{};
@@ -200,6 +207,7 @@ int launch_matmul(int out_dtype, int grouping, const Choice& c, MatmulArgs& p, i
     p.out_dtype = out_dtype;
     p.wide = wide_rows(p.out, p.out_stride, grouping == kByContraction ? p.m * p.out_stride : 0, elem_bytes(out_dtype),
                        c.tile ? 16 : 4 * elem_bytes(out_dtype));
+    p.past_caches = p.m * (grouping == kByContraction ? p.groups : 1) * p.n * elem_bytes(out_dtype) > kKeptBytes;
     void* args[] = {&p};
     return launch(c.tile ? t.fn : f.fn, p.units * p.n_tiles, batch, c.tile ? t.threads : kWave * f.waves, args, stream,
                   "the product's kernel", c.tile ? 0 : few_lds(p.few_rows, p.steps, cols, f.waves));

@@ -1058,7 +1058,9 @@ __global__ __launch_bounds__(256 * KG, 1) void k_matmul_tile(MatmulArgs p)
     constexpr int kProducts = WM * WN;
     static_assert(WM == WN, "reads take a's and b's fragments in turn");
     constexpr int kReadEvery = kProducts / kReads / 2 ? kProducts / kReads / 2 : 1;
-    constexpr int kMoveEvery = 3 * kProducts / 2 / kMoves;   // over three quarters of a pair
+    // transfers start within the first four fifths of a k-step (16384^3: 4.94
+    // PFLOP/s, spread over three quarters of a pair 4.76)
+    constexpr int kMoveEvery = 4 * kProducts / 5 / kMoves ? 4 * kProducts / 5 / kMoves : 1;
     constexpr int kEarly = kProducts / kMoveEvery < kMoves ? kProducts / kMoveEvery : kMoves;   // with the second k-step
     // behind the last transfer of the pair before (move kMoves - 1)
     constexpr int kFirstAim = kMoves * kMoveEvery - kProducts > 0 ? kMoves * kMoveEvery - kProducts : 0;
@@ -1192,9 +1194,15 @@ __global__ __launch_bounds__(256 * KG, 1) void k_matmul_tile(MatmulArgs p)
                        (out0 + (row0 + m0 + row) * p.out_stride + n0 + wn * (16 * WN) + n) * kSize;
         const int64_t step = kTurn * p.out_stride * kSize;
         if (p.wide && n + 16 / kSize <= left) {
+            if (p.past_caches) {
 #pragma unroll 8
-            for (int y = row; y < have; y += kTurn, from += kTurn * kPitch, out += step)
-                *reinterpret_cast<u32x4*>(out) = *reinterpret_cast<const u32x4*>(from);
+                for (int y = row; y < have; y += kTurn, from += kTurn * kPitch, out += step)
+                    __builtin_nontemporal_store(*reinterpret_cast<const u32x4*>(from), reinterpret_cast<u32x4*>(out));
+            } else {
+#pragma unroll 8
+                for (int y = row; y < have; y += kTurn, from += kTurn * kPitch, out += step)
+                    *reinterpret_cast<u32x4*>(out) = *reinterpret_cast<const u32x4*>(from);
+            }
         } else if (n < left) {
             const int some = left - n < 16 / kSize ? static_cast<int>(left - n) : 16 / kSize;
 #pragma unroll 1
