@@ -26,7 +26,7 @@ using i32x4 = int __attribute__((ext_vector_type(4)));
 using i32x8 = int __attribute__((ext_vector_type(8)));
 using u32x2 = uint32_t __attribute__((ext_vector_type(2)));
 using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
-using f32x2 = float __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(4)));   // scales: 4-byte aligned
 using f32x4 = float __attribute__((ext_vector_type(4)));
 using bf16x2 = __bf16 __attribute__((ext_vector_type(2)));
 using f16x2 = _Float16 __attribute__((ext_vector_type(2)));
@@ -687,7 +687,7 @@ __global__ __launch_bounds__(kWave * W) void k_matmul_few(MatmulArgs p)
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             if (U == 2 && q0 + 1 < last && whole(q0 + 1)) {   // four steps' scales of a row by one request
-                const u32x4 w = *reinterpret_cast<const u32x4*>(bsp[j] + q0 * 8);
+                const u32x4_any w = *reinterpret_cast<const u32x4_any*>(bsp[j] + q0 * 8);
 #pragma unroll
                 for (int u = 0; u < U; ++u) bsc[u][j] = (g & 2 ? w[2 * u + 1] : w[2 * u]) >> (16 * (g & 1));
             }
@@ -1040,14 +1040,16 @@ __global__ __launch_bounds__(256 * KG, 1) void k_matmul_tile(MatmulArgs p)
         else
             sb[k][x - WM] = static_cast<int>(__builtin_amdgcn_ubfe(qb[x - WM][k], shift, width));
     };
-    // The products of k-step K; between them what next(x) starts.  width: of
-    // the first k-step's scales.
-    auto multiply = [&](auto kstep, uint32_t width, auto next) {
+    auto take_first = [&](uint32_t q, int x) { take_scale(0, x, KG == 1 || q < pairs ? 8 : 0); };
+    // The products of k-step K; between them what next(x) starts.  The scale
+    // codes are taken in the k-step before: a matrix instruction may not follow
+    // within two of the one that makes its operand, and the compiler does not
+    // see to that where the instruction is written as assembly.
+    auto multiply = [&](auto kstep, auto next) {
         constexpr int K = decltype(kstep)::value;
+        asm volatile("s_nop 1" ::: "memory");
         each<WM * WN>([&](auto index) {
             constexpr int x = decltype(index)::value, i = x / WN, j = x % WN;
-            if constexpr (K == 0 && j == 0) take_scale(0, i, width);
-            if constexpr (K == 0 && i == 0) take_scale(0, WM + j, width);
             multiply_add(acc[i][j], fb[K][j], fa[K][i], sb[K][j], sa[K][i]);
             next(index);
             __builtin_amdgcn_sched_barrier(0);
@@ -1098,11 +1100,13 @@ __global__ __launch_bounds__(256 * KG, 1) void k_matmul_tile(MatmulArgs p)
         block_barrier();
 #pragma unroll
         for (int x = 0; x < kReads; ++x) read(0, x);
+#pragma unroll
+        for (int x = 0; x < kReads; ++x) take_first(0, x);
         settle_products();   // and behind acc's first values
         for (uint32_t q = 0; q < turns; ++q) {
             // The first k-step of pair q.  The last transfers of pair q + 1
             // start; then the aim turns to pair q + 2.
-            multiply(First{}, KG == 1 || q < pairs ? 8 : 0, [&](auto index) {
+            multiply(First{}, [&](auto index) {
                 constexpr int x = decltype(index)::value, y = kProducts + x, z = x - kFirstAim;
                 if constexpr (x % kReadEvery == 0 && x / kReadEvery < kReads) read(1, x / kReadEvery);
                 // the second k-step's scales, before the next pair's replace them
@@ -1123,13 +1127,17 @@ __global__ __launch_bounds__(256 * KG, 1) void k_matmul_tile(MatmulArgs p)
             wait_transfers<0>();
             block_barrier();
             __builtin_amdgcn_sched_barrier(0);
-            multiply(Second{}, 8, [&](auto index) {
+            multiply(Second{}, [&](auto index) {
                 constexpr int x = decltype(index)::value;
                 if constexpr (x % kReadEvery == 0 && x / kReadEvery < kReads) read(0, x / kReadEvery);
                 if constexpr (x % kMoveEvery == kMoveEvery - 1 && x / kMoveEvery < kMoves) move(x / kMoveEvery);
-                if constexpr (x == kProducts - 1) {
-                    find_codes(q + 1, 1);
+                // the next pair's first scales, read in this k-step
+                if constexpr (kProducts >= 2 * kReads) {
+                    if constexpr (x >= kProducts - kReads) take_first(q + 1, x - (kProducts - kReads));
+                } else if constexpr (x == kProducts - 1) {
+                    each<kReads>([&](auto y) { take_first(q + 1, decltype(y)::value); });
                 }
+                if constexpr (x == kProducts - 1) find_codes(q + 1, 1);
             });
         }
         wait_transfers<0>();   // none may arrive in what LDS holds next

@@ -580,6 +580,23 @@ def test_rows_far_behind_4_gib():
     assert np.array_equal(R.held(again), R.held(tail))
 
 
+def test_no_rows_no_groups():
+    """No rows at all, or no groups: empty results, zero gradients."""
+    w = _values((64, 96), BF16, 85).cuda().requires_grad_()
+    x = torch.empty(0, 96, device="cuda", dtype=BF16, requires_grad=True)
+    ou.mx4_linear(x, w).backward(torch.empty(0, 64, device="cuda", dtype=BF16))
+    assert x.grad.shape == (0, 96) and (w.grad == 0).all()
+    we = _values((3, 64, 96), BF16, 86).cuda().requires_grad_()
+    off = torch.zeros(4, dtype=torch.int32, device="cuda")
+    x = torch.empty(0, 96, device="cuda", dtype=BF16, requires_grad=True)
+    ou.mx4_grouped_linear(x, we, off).backward(torch.empty(0, 64, device="cuda", dtype=BF16))
+    assert (we.grad == 0).all()
+    none = ou.mx4_quantize(torch.empty(0, 64, 96, device="cuda"))
+    for t in (1, 5, 300):
+        y = ou.mx4_grouped_matmul(torch.ones(t, 96, device="cuda"), none, off[:1])
+        assert torch.equal(y, torch.zeros(t, 64, device="cuda"))
+
+
 def test_layers_take_any_strides():
     """An input and a gradient whose rows overlap or whose columns are apart
     are copied; the 4-bit forms must stay until the backward pass."""

@@ -44,6 +44,60 @@ def test_header_is_plain_c(tmp_path):
                     str(tmp_path / "t.o")], check=True)
 
 
+def _registers(operand):
+    m = re.match(r"([va])\[(\d+):(\d+)\]$", operand)
+    if m:
+        return {(m[1], i) for i in range(int(m[2]), int(m[3]) + 1)}
+    m = re.match(r"([va])(\d+)$", operand)
+    return {(m[1], int(m[2]))} if m else set()
+
+
+def _wait_state_faults(instructions):
+    """Places where a matrix instruction stands within two wait states of the
+    vector instruction that makes one of its operands, or where a vector
+    instruction touches an accumulator within 18 of the matrix instruction
+    that makes it."""
+    faults, made, summed, now = [], {}, {}, 0
+    for op, operands in instructions:
+        now += 1 + (int(operands[0]) if op == "s_nop" else 0)
+        if op.startswith("v_mfma"):
+            for r in set().union(*map(_registers, operands[1:6])):
+                if now - made.get(r, -9) <= 2:
+                    faults.append((now, op, r))
+            summed |= dict.fromkeys(_registers(operands[0]), now)
+        elif op.startswith("v_"):
+            for r in set().union(*map(_registers, operands)) if operands else ():
+                if now - summed.get(r, -99) <= 18:
+                    faults.append((now, op, r))
+            made |= dict.fromkeys(_registers(operands[0]) if operands else (), now)
+    return faults
+
+
+def test_matrix_instructions_keep_their_wait_states(tmp_path):
+    """The tiled products write their matrix instruction as assembly, for which
+    the compiler inserts no wait states: in what it makes of the kernels here,
+    none is missing (checked in the order of the text, in which a loop's end is
+    followed by more than that, and its barrier by an s_nop)."""
+    made = [("v_bfe_u32", ["v1", "v2", "s0", "8"]), ("v_mfma_x", ["a[0:3]", "v[4:7]", "v[8:11]", "a[0:3]", "v1", "v3"])]
+    assert _wait_state_faults(made) and not _wait_state_faults([made[0], ("s_nop", ["1"]), made[1]])
+    assert _wait_state_faults([made[1], ("v_accvgpr_read_b32", ["v9", "a2"])])
+    from optimizer_update_amd import build
+    out = tmp_path / "k.s"
+    flags = [f for f in build.HIPCC_FLAGS if f not in ("-shared", "-fPIC", "-Wall")]
+    subprocess.run(["/opt/rocm/bin/hipcc", *flags, "-S", "--cuda-device-only", build.MX4_SOURCES[0], "-o", str(out)],
+                   check=True, capture_output=True)
+    kernels = re.findall(r"^(_ZN3mx4\S*k_matmul_tile\S*):[^\n]*\n(.*?)^\.Lfunc_end", out.read_text(), flags=re.M | re.S)
+    assert len(kernels) == 27
+    for name, body in kernels:
+        instructions = []
+        for line in body.split("\n"):
+            words = line.split(";")[0].replace(",", " ").split()
+            if words and not words[0].startswith(".") and not words[0].endswith(":"):
+                instructions.append((words[0], words[1:]))
+        assert sum(op.startswith("v_mfma") for op, _ in instructions) in (8, 32, 128), name
+        assert not _wait_state_faults(instructions), name
+
+
 def test_missing_library_fails_loudly(tmp_path):
     with pytest.raises(ImportError):
         ou.load_mx4(str(tmp_path / "liboptimizer_mx4.so"))
