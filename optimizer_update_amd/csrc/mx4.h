@@ -75,13 +75,13 @@ enum Grouping { kPlain = 0, kByRows = 1, kByContraction = 2 };
 const void* quant_rows_kernel(int dtype);
 const void* quant_tile_kernel(int dtype);
 const void* dequant_kernel(int dtype);
-// tile: rows and columns of a block's tile, 256, 128 or 64 (its k-steps shared
-// by four groups of waves).
+// tile: rows and columns of a block's tile, 256, 128 or 64; shared: the k-steps
+// of a 64-tile by two groups of waves.
 struct TileKernel {
     const void* fn;
     int tile, threads;
 };
-TileKernel matmul_tile_kernel(int out_dtype, int grouping, int tile);
+TileKernel matmul_tile_kernel(int out_dtype, int grouping, int tile, bool shared);
 
 // Products of up to 16 rows (by groups: in units of 16): 16 or 64 columns a
 // block of `waves` waves, with few_lds() bytes of dynamic LDS.

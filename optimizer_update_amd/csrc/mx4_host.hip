@@ -148,6 +148,7 @@ int launch_quantize(int dtype, QuantArgs& q, int64_t batch, int64_t units, void*
 struct Choice {
     int tile, cols;
     bool values;   // the left matrix may come as values
+    bool shared;   // the 64-tile's k-steps
 };
 
 // The rows in LDS (k_matmul_few) are quantised by every block again: that pays
@@ -160,15 +161,18 @@ constexpr int64_t kValuesSteps = 320;
 // block, at most (by groups not known here: 16).
 Choice choose(int64_t rows, int64_t n, int64_t steps, int64_t batch, int64_t room)
 {
-    if (rows <= 16) return {0, cut(n, 16) * batch <= 1024 ? 16 : 64, room * steps <= kValuesSteps};
+    if (rows <= 16) return {0, cut(n, 16) * batch <= 1024 ? 16 : 64, room * steps <= kValuesSteps, false};
     // a tile addresses its rows of a and b by 31 bits (kMaxDepth: 64 of them)
-    if (steps >= (int64_t(1) << 17)) return {64, 0, false};
+    if (steps >= (int64_t(1) << 17)) return {64, 0, false, true};
     const int64_t t64 = cut(rows, 64) * cut(n, 64) * batch;
     const int64_t t128 = cut(rows, 128) * cut(n, 128) * batch, t256 = cut(rows, 256) * cut(n, 256) * batch;
-    // At most one 64-tile a CU, its k-steps shared by four groups of waves:
-    // 256 x 4096 x 4096 8.5 us, by 128-tiles 11.9; 777 x 2063 x 4104 (429
-    // tiles) 21.5 us against 15.8.
-    if (t64 <= 256) return {64, 0, false};
+    // While they are at most two a CU, 64-tiles: 512 x 4096 x 1024 6.3 us, by
+    // 128-tiles 6.7; 1024 x 2048 x 4096 13.7 against 15.0; but 1500 x 1500 x
+    // 1500 (576 tiles) 10.9 against 10.3.  Two groups of waves share a long
+    // chain of k-steps: k = 4096 10.1 us against 11.3 with one tile a CU and
+    // 13.7 against 14.1 with two, k = 1024 5.3 against 5.1 and 7.4 against 6.3
+    // (four groups: 10.4 and 18.3 us with k = 4096).
+    if (t64 <= 512) return {64, 0, false, steps >= (t64 <= 256 ? 16 : 32)};
     // Rounds of the device, in tenths of a microsecond per pair of k-steps as
     // measured with 4096 columns: 256-tiles one a CU, 12 + 7 by how full the
     // round is (3000 x 3000 29.7 us, 4096 x 4096 37.3); 128-tiles two a CU,
@@ -177,8 +181,8 @@ Choice choose(int64_t rows, int64_t n, int64_t steps, int64_t batch, int64_t roo
     const int64_t r256 = t256 % 256, r128 = t128 % 512;
     const int64_t by256 = t256 / 256 * 190 + (r256 ? 120 + 70 * r256 / 256 : 0);
     const int64_t by128 = t128 / 512 * 115 + (r128 > 256 ? 115 : r128 ? 73 : 0);
-    if (by256 <= by128) return {256, 0, false};
-    return {128, 0, false};
+    if (by256 <= by128) return {256, 0, false, false};
+    return {128, 0, false, false};
 }
 
 // By groups: the mean of the groups' rows decides, as the rows themselves are
@@ -198,7 +202,7 @@ constexpr int64_t kKeptBytes = int64_t(192) << 20;
 
 int launch_matmul(int out_dtype, int grouping, const Choice& c, MatmulArgs& p, int64_t batch, void* stream)
 {
-    const TileKernel t = c.tile ? matmul_tile_kernel(out_dtype, grouping, c.tile) : TileKernel{};
+    const TileKernel t = c.tile ? matmul_tile_kernel(out_dtype, grouping, c.tile, c.shared) : TileKernel{};
     const FewKernel f = c.tile ? FewKernel{} : matmul_few_kernel(p.x ? p.x_dtype : kHeld, grouping, c.cols);
     const int rows = c.tile ? t.tile : 16, cols = c.tile ? t.tile : f.cols;
     // by rows: two groups more, the rows in front of the first and behind the last

@@ -1274,18 +1274,19 @@ TileKernel tile_of_type(int dtype)
 }
 
 template <int G>
-TileKernel tile_of_shape(int dtype, int tile)
+TileKernel tile_of_shape(int dtype, int tile, bool shared)
 {
     return tile == 256   ? tile_of_type<G, 8, 1>(dtype)
            : tile == 128 ? tile_of_type<G, 4, 1>(dtype)
-                         : tile_of_type<G, 2, 4>(dtype);
+           : shared      ? tile_of_type<G, 2, 2>(dtype)
+                         : tile_of_type<G, 2, 1>(dtype);
 }
 
-TileKernel matmul_tile_kernel(int out_dtype, int grouping, int tile)
+TileKernel matmul_tile_kernel(int out_dtype, int grouping, int tile, bool shared)
 {
-    return grouping == kPlain    ? tile_of_shape<kPlain>(out_dtype, tile)
-           : grouping == kByRows ? tile_of_shape<kByRows>(out_dtype, tile)
-                                 : tile_of_shape<kByContraction>(out_dtype, tile);
+    return grouping == kPlain    ? tile_of_shape<kPlain>(out_dtype, tile, shared)
+           : grouping == kByRows ? tile_of_shape<kByRows>(out_dtype, tile, shared)
+                                 : tile_of_shape<kByContraction>(out_dtype, tile, shared);
 }
 
 template <int XT, int G>

@@ -184,7 +184,8 @@ def _random_held(rows, k, seed, lo=119, hi=135, lead=()):
 PRODUCTS = [(13, 70, 4100), (16, 33, 3000), (5, 16500, 300), (2, 20000, 140), (1, 1, 1), (1, 64, 128), (1, 4096, 1024), (2, 33, 33), (3, 300, 4000), (15, 17, 500), (16, 16, 129),
             (16, 512, 384), (17, 65, 256), (31, 127, 640), (32, 128, 100), (33, 129, 1100), (63, 40, 2048), (64, 64, 64),
             (65, 200, 900), (100, 1000, 257), (128, 256, 512), (129, 255, 511), (130, 2000, 700), (255, 129, 383),
-            (256, 256, 256), (257, 257, 1025), (300, 70, 5000), (512, 512, 4096), (700, 900, 1300), (1030, 1100, 640)]
+            (256, 256, 256), (257, 257, 1025), (300, 70, 5000), (512, 512, 4096), (700, 900, 1300), (1030, 1100, 640), (40, 90, 1930), (40, 90, 2060),
+            (500, 2100, 600), (500, 2100, 4100)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)

@@ -87,7 +87,7 @@ def test_matrix_instructions_keep_their_wait_states(tmp_path):
     subprocess.run(["/opt/rocm/bin/hipcc", *flags, "-S", "--cuda-device-only", build.MX4_SOURCES[0], "-o", str(out)],
                    check=True, capture_output=True)
     kernels = re.findall(r"^(_ZN3mx4\S*k_matmul_tile\S*):[^\n]*\n(.*?)^\.Lfunc_end", out.read_text(), flags=re.M | re.S)
-    assert len(kernels) == 27
+    assert len(kernels) == 36
     for name, body in kernels:
         instructions = []
         for line in body.split("\n"):
