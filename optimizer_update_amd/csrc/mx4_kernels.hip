@@ -646,6 +646,8 @@ __device__ __forceinline__ void block_barrier()
 // left matrix is given as values of that type: the block meanwhile quantises
 // its rows into LDS.  The fragment of b is the instruction's first operand, so
 // that a lane's four results are neighbours in a row of out.
+// 16 x 4096 x 4096, held: 10.0 us; 17.0 where a row's lanes ask for 64 bytes
+// and each step for its scales by itself.
 template <int XT, int G, int NT, int W, int U>
 __global__ __launch_bounds__(kWave * W) void k_matmul_few(MatmulArgs p)
 {

@@ -640,6 +640,14 @@ def _layer_operands(x, w, dims: int):
     return held, weight
 
 
+def _apply(x, weight, offsets, held):
+    if not torch.is_grad_enabled():
+        # the forward pass sees what requires gradients, not whether any are
+        # recorded: without, x goes in as values and no transposed form is made
+        x, weight = x.detach(), weight.detach()
+    return _Layer.apply(x, weight, offsets, held)
+
+
 def mx4_linear(x: torch.Tensor, w) -> torch.Tensor:
     """x w^T with its gradients, the three products in 4 bits: with Q the
     rounding along the contracted axis (in blocks of 32),
@@ -651,8 +659,8 @@ def mx4_linear(x: torch.Tensor, w) -> torch.Tensor:
     are kept, not x."""
     held, weight = _layer_operands(x, w, 2)
     if x.dim() == 2:
-        return _Layer.apply(x, weight, None, held)
-    y = _Layer.apply(x.reshape(math.prod(x.shape[:-1]), x.shape[-1]), weight, None, held)
+        return _apply(x, weight, None, held)
+    y = _apply(x.reshape(math.prod(x.shape[:-1]), x.shape[-1]), weight, None, held)
     return y.view(*x.shape[:-1], weight.shape[0])
 
 
@@ -665,4 +673,4 @@ def mx4_grouped_linear(x: torch.Tensor, w, offsets: torch.Tensor) -> torch.Tenso
         raise ValueError("x must be [T, K]")
     if _offsets(offsets, x.get_device()) != weight.shape[0]:
         raise ValueError(f"offsets name {offsets.shape[0] - 1} groups, w holds {weight.shape[0]}")
-    return _Layer.apply(x, weight, offsets, held)
+    return _apply(x, weight, offsets, held)

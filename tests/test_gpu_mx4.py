@@ -581,6 +581,37 @@ def test_rows_far_behind_4_gib():
     assert np.array_equal(R.held(again), R.held(tail))
 
 
+@pytest.mark.parametrize("grouped", [False, True])
+def test_layers_without_gradients(grouped):
+    """Where no gradients are recorded the layers are the products alone, also
+    of leaves that require gradients: no form of x that outlives the call and
+    none along the rows (x [4096, 1024]: 2.1 MiB each, of it the values' form
+    passes through the workspace)."""
+    m, n, k = 4096, 64, 1024
+    x = _values((m, k), BF16, 87).cuda().requires_grad_()
+    w = _values((2, n, k) if grouped else (n, k), BF16, 88).cuda().requires_grad_()
+    off = torch.tensor([0, 1000, m], dtype=torch.int32, device="cuda")
+    held = ou.Mx4Weight(w)
+
+    def layer():
+        return ou.mx4_grouped_linear(x, held, off) if grouped else ou.mx4_linear(x, held)
+
+    xs = x.detach()
+    want = ou.mx4_grouped_matmul(xs, held.q, off) if grouped else ou.mx4_matmul(xs, held.q)
+    assert torch.equal(layer(), want)
+    form = m * k // 2 + m * k // 32
+    for mode in (torch.no_grad, torch.inference_mode):
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_allocated()
+        torch.cuda.reset_peak_memory_stats()
+        with mode():
+            y = layer()
+        assert torch.equal(y, want) and not y.requires_grad
+        del y
+        # the result, the form, the comparison's flags and roundings of sizes
+        assert torch.cuda.max_memory_allocated() - before < 1.5 * form + m * n * 3
+
+
 def test_no_rows_no_groups():
     """No rows at all, or no groups: empty results, zero gradients."""
     w = _values((64, 96), BF16, 85).cuda().requires_grad_()
