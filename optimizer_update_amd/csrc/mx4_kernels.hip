@@ -358,8 +358,9 @@ __global__ __launch_bounds__(kQuantThreads) void k_quant_rows(QuantArgs q, uint3
 // axes: 411 MB in 86 us, the rate of a copy).  It is read along the columns (eight values
 // a lane), quantised that way from registers if wanted, and left in LDS;
 // then each lane takes two neighbouring columns and a block of 32 rows.
-// The LDS row pitch of 130 16-bit values (130 of binary32) puts the lanes of
-// a wave, which read neighbouring dwords of one row, on different banks.
+// The lanes of a wave read neighbouring dwords of one row of LDS, so they meet
+// on no bank; the row pitch of four dwords more than a row keeps the writes,
+// four rows a wave, apart.
 template <int DT>
 __global__ __launch_bounds__(kQuantThreads) void k_quant_tile(QuantArgs q)
 {
