@@ -245,6 +245,27 @@ def test_grouped_products_of_many_tiles(counts, front, back, n, k):
         assert (got[rest] == 0).all() and (out[rest] == 5).all()
 
 
+@pytest.mark.parametrize("m,n", [(3, 40), (70, 65)])
+@pytest.mark.parametrize("k", [(1 << 24) - 200, (1 << 25) - 5])
+def test_matmul_of_the_greatest_depths(m, n, k):
+    """Operands that are zero but for a few k-steps at the start, between and
+    at the end: the product of those steps alone."""
+    p = R.columns(k)
+    steps = [0, 1, p // 256 - 1, p // 256, p // 128 - 3, p // 128 - 2, p // 128 - 1]
+    forms = []
+    for rows, seed in ((m, 90), (n, 91)):
+        part = _random_held(rows, 128 * len(steps), seed)
+        part.codes.view(rows, len(steps), 64)[:, -1, (k - p + 128) // 2:] = 0
+        codes = torch.zeros(rows, p // 128, 64, dtype=torch.uint8, device="cuda")
+        scales = torch.full((rows, p // 128, 4), 127, dtype=torch.uint8, device="cuda")
+        codes[:, steps] = part.codes.view(rows, len(steps), 64)
+        scales[:, steps] = part.scales.view(rows, len(steps), 4)
+        forms.append((part, ou.Mx4(codes.view(rows, p // 2), scales.view(rows, p // 32), k)))
+    (a, far_a), (b, far_b) = forms
+    want, mag = R.product(R.held(a), R.held(b))
+    R.check_product(ou.mx4_matmul(far_a, far_b, F32), want, mag, 128 * len(steps))
+
+
 @pytest.mark.parametrize("m", [1, 16, 40, 200])
 def test_matmul_scales_of_every_size(m):
     """Scales over the whole range of binary32, results up to infinity."""
