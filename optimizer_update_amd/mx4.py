@@ -451,12 +451,25 @@ class Mx4Weight:
         self.version = 0   # of the forms: a backward pass refuses later ones than its forward pass read
         self.q, self.qt = mx4_quantize_both(weight.detach())
 
+    def _check_forms(self) -> None:
+        """Raises if the weight has taken another shape or device than its
+        forms (a new ``weight`` or ``weight.data``): the kernels take sizes
+        from the one and addresses from the others."""
+        *lead, r, c = shape = self.weight.shape
+        q, qt, index = self.q, self.qt, self.weight.get_device()
+        if q.k != c or q.codes.shape[:-1] != shape[:-1] or qt.k != r or qt.codes.shape[:-1] != (*lead, c):
+            raise ValueError(f"the 4-bit forms are of a weight of shape {list(q.shape)}, the weight is now "
+                             f"{list(shape)}: make a new Mx4Weight")
+        if q.codes.get_device() != index or qt.codes.get_device() != index:
+            raise ValueError("the 4-bit forms are on another device than the weight: make a new Mx4Weight")
+
     def refresh(self, stream=None) -> None:
         """Quantise the weight's present values into the same buffers."""
+        self._check_forms()
         w = self.weight.detach()
         dt = _values(w, "weight")
-        if w.shape != self.q.shape or not w.is_contiguous():
-            raise ValueError("the weight changed its shape or layout")
+        if not w.is_contiguous():
+            raise ValueError("the weight changed its layout")
         _run(w.get_device(), stream, self._refresh, w, dt)
         self.version += 1
 
@@ -551,7 +564,8 @@ class _Layer(torch.autograd.Function):
         ctx.types = (x.dtype, w.dtype)
         ctx.keep, ctx.wt, ctx.xt = keep, wt, xt
         ctx.held = held if need_x else None
-        ctx.version = None if held is None else held.version
+        if ctx.held is not None:
+            ctx.version, ctx.qt = held.version, held.qt   # the form that the shapes were checked against
         if offsets is not None:
             ctx.save_for_backward(offsets)
         return y
@@ -603,7 +617,7 @@ class _Layer(torch.autograd.Function):
                     _fail(st)
         if need_x:
             dx = torch.empty((m, k), dtype=x_dtype, device=device)
-            right = _ptrs(ctx.held.qt) if ctx.held is not None else _place(kp, ctx.wt)
+            right = _ptrs(ctx.qt) if ctx.held is not None else _place(kp, ctx.wt)
             _multiply(lib, yd, None if need_w else dy, rs, _place(at, dq), m, DTYPES[x_dtype], right, k, n, off, groups, dx,
                       at + ws, grow, handle)
         return dx, dw, None, None
@@ -630,6 +644,8 @@ def _multiply(lib, xd, x, rs, left, m, od, right, n, k, off, groups, out, ws, ne
 def _layer_operands(x, w, dims: int):
     held = w if isinstance(w, Mx4Weight) else None
     weight = held.weight if held is not None else w
+    if held is not None:
+        held._check_forms()
     _values(x, "x")
     _values(weight, "w", dims)
     _same(x.get_device(), weight.get_device(), "w")

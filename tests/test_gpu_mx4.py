@@ -690,3 +690,25 @@ def test_refusals_on_the_device():
     with pytest.raises(_lib.OptimizerUpdateError) as err:       # the result over the operand
         ou.mx4_matmul(x, q, out=x[:, :4])
     assert err.value.status == -4
+
+
+def test_replaced_weights_are_refused():
+    """Kept forms whose weight was replaced by one of another shape, or that
+    are on another device than it: refused before anything is launched."""
+    x = torch.ones(5, 96, device="cuda")
+    for now in ((65, 96), (640, 96), (32, 96)):
+        held = ou.Mx4Weight(torch.ones(64, 96, device="cuda"))
+        assert ou.mx4_linear(x, held).shape == (5, 64)
+        held.weight.data = torch.ones(now, device="cuda")
+        for call in (lambda: ou.mx4_linear(x, held), held.refresh):
+            with pytest.raises(ValueError, match="forms are of a weight of shape"):
+                call()
+    off = torch.tensor([0, 2, 5, 5], dtype=torch.int32, device="cuda")
+    held = ou.Mx4Weight(torch.ones(2, 64, 96, device="cuda"))
+    held.weight = torch.ones(3, 64, 96, device="cuda")
+    with pytest.raises(ValueError, match="forms are of a weight of shape"):
+        ou.mx4_grouped_linear(x, held, off)
+    held = ou.Mx4Weight(torch.ones(64, 96, device="cuda"))
+    held.q = ou.Mx4(held.q.codes.cpu(), held.q.scales.cpu(), 96)
+    with pytest.raises(ValueError, match="forms are on another device"):
+        ou.mx4_linear(x, held)

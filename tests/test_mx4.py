@@ -267,3 +267,41 @@ def test_reference_rounds_to_the_nearest_level():
         d = np.abs(np.minimum(v, 6.0) - R.LEVELS)
         near = np.flatnonzero(d == d.min())
         assert c == (near[0] if near.size == 1 else near[near % 2 == 0][0]), v
+
+
+def _kept(weight, of=None):
+    """An Mx4Weight whose forms are those of a matrix of shape `of`, without a device."""
+    def form(*shape):
+        p = R.columns(shape[-1])
+        return ou.Mx4(torch.zeros(*shape[:-1], p // 2, dtype=torch.uint8),
+                      torch.zeros(*shape[:-1], p // 32, dtype=torch.uint8), shape[-1])
+
+    *lead, r, c = of or weight.shape
+    held = object.__new__(ou.Mx4Weight)
+    held.weight, held.version, held.q, held.qt = weight, 0, form(*lead, r, c), form(*lead, c, r)
+    return held
+
+
+@pytest.mark.parametrize("now", [(65, 96), (63, 96), (64, 97), (64, 224), (96, 64)])
+def test_kept_forms_of_another_shape_are_refused(now):
+    """A weight that grew or shrank since its forms were made: the layers and
+    the refresh refuse it before they touch an address of the forms."""
+    held = _kept(torch.zeros(64, 96))
+    held._check_forms()
+    held.weight.data = torch.zeros(now)
+    off = torch.zeros(3, dtype=torch.int32)
+    for call in (held._check_forms, held.refresh, lambda: ou.mx4_linear(torch.zeros(5, now[1]), held)):
+        with pytest.raises(ValueError, match="forms are of a weight of shape"):
+            call()
+    for of in ((1, *now), (3, *now)):
+        held = _kept(torch.zeros(2, *now), of)
+        with pytest.raises(ValueError, match="forms are of a weight of shape"):
+            ou.mx4_grouped_linear(torch.zeros(5, now[1]), held, off)
+
+
+def test_kept_forms_on_another_device_are_refused():
+    held = _kept(torch.zeros(64, 96))
+    held.weight = type("Elsewhere", (), {"shape": torch.Size((64, 96)), "get_device": lambda self: 1})()
+    for call in (held._check_forms, held.refresh, lambda: ou.mx4_linear(torch.zeros(5, 96), held)):
+        with pytest.raises(ValueError, match="forms are on another device"):
+            call()
