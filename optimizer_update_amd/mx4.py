@@ -562,12 +562,12 @@ class _Layer(torch.autograd.Function):
                   handle)
         ctx.shape = (m, n, k, groups, held_m)
         ctx.types = (x.dtype, w.dtype)
-        ctx.keep, ctx.wt, ctx.xt = keep, wt, xt
+        ctx.wt, ctx.xt = wt, xt
         ctx.held = held if need_x else None
         if ctx.held is not None:
             ctx.version, ctx.qt = held.version, held.qt   # the form that the shapes were checked against
-        if offsets is not None:
-            ctx.save_for_backward(offsets)
+        # as saved tensors: freed by the backward pass, seen by hooks and checkpoints
+        ctx.save_for_backward(keep if kept.bytes else None, offsets)
         return y
 
     @staticmethod
@@ -583,10 +583,10 @@ class _Layer(torch.autograd.Function):
         need_x, need_w = ctx.needs_input_grad[:2]
         m, n, k, groups, held_m = ctx.shape
         x_dtype, w_dtype = ctx.types
-        offsets, = ctx.saved_tensors or (None,)
+        keep, offsets = ctx.saved_tensors
         off = None if offsets is None else offsets.data_ptr()
         pn, rs, yd = _columns(n), _row_stride(dy, "the gradient"), DTYPES[dy.dtype]
-        kp = ctx.keep.data_ptr()
+        kp = 0 if keep is None else keep.data_ptr()
         temp = _Room()
         dq = temp.form(m, pn) if need_x and need_w else None
         dt = temp.form(n, held_m) if need_w else None

@@ -712,3 +712,40 @@ def test_replaced_weights_are_refused():
     held.q = ou.Mx4(held.q.codes.cpu(), held.q.scales.cpu(), 96)
     with pytest.raises(ValueError, match="forms are on another device"):
         ou.mx4_linear(x, held)
+
+
+@pytest.mark.parametrize("grouped", [False, True])
+def test_forms_for_the_backward_pass_are_saved_tensors(grouped):
+    """What a layer keeps is freed by the backward pass although the result
+    lives, passes through hooks on saved tensors, and is dropped and made again
+    under a checkpoint."""
+    from torch.utils.checkpoint import checkpoint
+    m, n, k = 2048, 128, 1024
+    x = _values((m, k), BF16, 93).cuda().requires_grad_()
+    w = _values((2, n, k) if grouped else (n, k), BF16, 94).cuda().requires_grad_()
+    dy = _values((m, n), BF16, 95).cuda()
+    off = torch.tensor([0, 900, m], dtype=torch.int32, device="cuda")
+
+    def layer(x, w):
+        return ou.mx4_grouped_linear(x, w, off) if grouped else ou.mx4_linear(x, w)
+
+    form = m * k // 2 + m * k // 32                    # x along its rows, without padding
+    y = layer(x, w)
+    before = torch.cuda.memory_allocated()
+    want = torch.autograd.grad(y, (x, w), dy)
+    made = sum(t.numel() * 2 for t in want)
+    assert torch.cuda.memory_allocated() <= before + made - form
+    with pytest.raises(RuntimeError):                  # once, like torch's own layers
+        torch.autograd.grad(y, (x, w), dy)
+    packed = []
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: packed.append(t) or t.cpu(), lambda t: t.cuda()):
+        y2 = layer(x, w)
+    assert sum(t.numel() * t.element_size() for t in packed) >= form
+    del packed
+    for got, ref in zip(torch.autograd.grad(y2, (x, w), dy), want):
+        assert torch.equal(got, ref)
+    before = torch.cuda.memory_allocated()
+    y3 = checkpoint(layer, x, w, use_reentrant=False)
+    assert torch.cuda.memory_allocated() < before + m * n * 2 + form // 2
+    for got, ref in zip(torch.autograd.grad(y3, (x, w), dy), want):
+        assert torch.equal(got, ref)
