@@ -61,14 +61,14 @@ int64_t ou_mx4_grouped_columns(int64_t rows, int32_t groups);
 
 /* The same for one matrix whose rows fall into groups: group e is rows
  * [offsets[e], offsets[e + 1]) (rows at most 2^28 in the calls by groups),
- * offsets being groups + 1 int32 in device
- * memory, rising, within [0, rows] (others are clamped to that; a group that
- * runs backwards is empty).  Along the rows every group is a matrix of its
- * own: its columns of codes_t start at the sum of the earlier groups' rows,
- * each rounded up to 128, and its blocks at its first row.  A row of codes_t
- * holds ou_mx4_grouped_columns(rows, groups) columns; those behind the last
- * group are not written.  codes/scales (or NULL) get the rows of the groups;
- * rows of no group are not written. */
+ * offsets being groups + 1 int32 in device memory, rising, within [0, rows]
+ * (others are clamped to that, and one below an earlier one counts as that
+ * one: no row is of two groups).  Along the rows every group is a matrix of
+ * its own: its columns of codes_t start at the sum of the earlier groups'
+ * rows, each rounded up to 128, and its blocks at its first row.  A row of
+ * codes_t holds ou_mx4_grouped_columns(rows, groups) columns; those behind the
+ * last group are not written.  codes/scales (or NULL) get the rows of the
+ * groups; rows of no group are not written. */
 int ou_mx4_quantize_grouped(int dtype, const void* x, int64_t rows, int64_t cols, int64_t row_stride,
                             const int32_t* offsets, int32_t groups, uint8_t* codes, uint8_t* scales,
                             uint8_t* codes_t, uint8_t* scales_t, void* stream);

@@ -200,17 +200,29 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t x)
     return x;
 }
 
+// Largest value over the lanes up to this one.
+__device__ __forceinline__ uint32_t wave_max(uint32_t x)
+{
+    x = max(x, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x111, 0xf, 0xf, false)));
+    x = max(x, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x112, 0xf, 0xf, false)));
+    x = max(x, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x114, 0xf, 0xf, false)));
+    x = max(x, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x118, 0xf, 0xf, false)));
+    x = max(x, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x142, 0xa, 0xf, false)));
+    x = max(x, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x143, 0xc, 0xf, false)));
+    return x;
+}
+
 __device__ __forceinline__ uint32_t lane_value(uint32_t x, int lane)
 {
     return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(x), lane));
 }
 
 // The groups of a call, cut into units of `unit` rows each.  Offsets may be
-// anything: they are clamped to [0, rows], and a group that runs backwards is
-// empty.  rows is at most 2^28 and unit at least 16, so the units of 64 groups
-// stay below 2^31 even where groups overlap; sums over more groups saturate.
-// All lanes of a wave take part and get the same answers; lane l looks at
-// group base + l.
+// anything: they are clamped to [0, rows], and one below an earlier one counts
+// as that one.  So every row is of one group at most, in front of the first or
+// behind the last, and the units are no more than a grid that is sized for any
+// rising offsets.  All lanes of a wave take part and get the same answers;
+// lane l looks at group base + l.  The chunks of 64 groups are taken in order.
 struct Groups {
     const int32_t* offsets;
     int32_t groups, rows, unit;
@@ -224,27 +236,24 @@ struct Groups {
     }
     __device__ __forceinline__ uint32_t offset(int32_t i) const
     {
-        const int32_t o = offsets[i];
+        const int32_t o = offsets[i < groups ? i : groups];
         return static_cast<uint32_t>(o < 0 ? 0 : (o > rows ? rows : o));
     }
     __device__ __forceinline__ uint32_t units(uint32_t count) const { return (count + unit - 1) / unit; }
     __device__ __forceinline__ void chunk(int32_t at)
     {
         if (base == at) return;
+        const uint32_t reached = at ? lane_value(lo + n, kWave - 1) : 0;   // by the chunk before
         base = at;
         const int32_t e = at + (static_cast<int>(threadIdx.x) & (kWave - 1));
-        lo = n = 0;
-        if (e < groups) {
-            lo = offset(e);
-            const uint32_t hi = offset(e + 1);
-            n = hi > lo ? hi - lo : 0;
+        lo = offset(e);
+        uint32_t hi = offset(e + 1);
+        if (__ballot(hi < lo || lo < reached)) {
+            lo = max(wave_max(lo), reached);
+            hi = max(lo, hi);
         }
+        n = hi - lo;
         scan = wave_scan(units(n));
-    }
-    static __device__ __forceinline__ uint32_t add(uint32_t before, uint32_t more)
-    {
-        const uint32_t s = before + more;   // both below 2^31
-        return s > 0x7fffffffu ? 0x7fffffffu : s;
     }
     // units of all groups
     __device__ __forceinline__ uint32_t total()
@@ -252,13 +261,14 @@ struct Groups {
         uint32_t before = 0;
         for (int32_t at = 0; at < groups; at += kWave) {
             chunk(at);
-            before = add(before, lane_value(scan, kWave - 1));
+            before += lane_value(scan, kWave - 1);
         }
         return before;
     }
-    // units of the rows in front of the first group, and behind the last
+    // end of the rows in front of the first group; start of those behind the
+    // last one, whose chunk is at hand; units of both
     __device__ __forceinline__ uint32_t front() const { return groups ? offset(0) : 0; }
-    __device__ __forceinline__ uint32_t back() const { return groups ? offset(groups) : 0; }
+    __device__ __forceinline__ uint32_t back() const { return groups ? lane_value(lo + n, kWave - 1) : 0; }
     __device__ __forceinline__ uint32_t rest() const { return units(front()) + units(rows - back()); }
     // unit `index` of all, those of no group last
     __device__ __forceinline__ Place locate(uint32_t index)
@@ -275,7 +285,7 @@ struct Groups {
                 return Place{at + hit, static_cast<int32_t>(lane_value(lo, hit) + from),
                              static_cast<int32_t>(count - from < static_cast<uint32_t>(unit) ? count - from : unit)};
             }
-            before = add(before, lane_value(scan, kWave - 1));
+            before += lane_value(scan, kWave - 1);
         }
         const uint32_t f = front(), b = back(), nf = units(f), j = index - before;
         if (j >= nf + units(rows - b)) return Place{-1, 0, 0};
@@ -290,10 +300,10 @@ struct Groups {
         for (int32_t at = 0;; at += kWave) {
             chunk(at);
             if (group < at + kWave) break;
-            before = add(before, lane_value(scan, kWave - 1));
+            before += lane_value(scan, kWave - 1);
         }
         const uint32_t own = units(lane_value(n, group - base));
-        *first = add(before, lane_value(scan, group - base) - own);
+        *first = before + lane_value(scan, group - base) - own;
         *count = own;
     }
 };
@@ -888,8 +898,7 @@ __global__ __launch_bounds__(256 * KG, 1) void k_matmul_tile(MatmulArgs p)
     if constexpr (G == kByRows) {
         Groups groups(p.offsets, p.groups, p.rows, BM);
         uint32_t units = groups.total();
-        if (p.zero_rest) units = Groups::add(units, groups.rest());
-        if (units > p.units) units = static_cast<uint32_t>(p.units);   // offsets that overlap
+        if (p.zero_rest) units += groups.rest();
         if (static_cast<int64_t>(blockIdx.x) >= static_cast<int64_t>(units) * p.n_tiles) return;
         tile_of(blockIdx.x, units, static_cast<uint32_t>(p.n_tiles), &unit, &ntile);
         const Place at = groups.locate(unit);
@@ -911,8 +920,6 @@ __global__ __launch_bounds__(256 * KG, 1) void k_matmul_tile(MatmulArgs p)
             Groups(p.offsets, p.groups, p.rows, kPad).span(static_cast<int32_t>(blockIdx.y), &before, &own);
             step0 = before;
             steps = own;
-            if (step0 > p.steps) step0 = p.steps;
-            if (steps > p.steps - step0) steps = p.steps - step0;
             out0 = static_cast<int64_t>(blockIdx.y) * p.m * p.out_stride;
         }
     }

@@ -749,3 +749,64 @@ def test_forms_for_the_backward_pass_are_saved_tensors(grouped):
     assert torch.cuda.memory_allocated() < before + m * n * 2 + form // 2
     for got, ref in zip(torch.autograd.grad(y3, (x, w), dy), want):
         assert torch.equal(got, ref)
+
+
+def _falling(t):
+    return [[0, t, t // 2, 4 * t // 5], [3, t // 2, t // 4, t - 2], [t + 5, -3, t // 2, 2], [-7, 2**31 - 1, 0, 5],
+            [t // 3, t // 5, t // 2, t // 2 - 1]]
+
+
+# few rows; tiles of 64, with the k-steps shared, of 128, of 256
+@pytest.mark.parametrize("t,n,k", [(10, 40, 130), (100, 70, 300), (100, 70, 4100), (2500, 1200, 130), (4100, 2100, 130)])
+def test_offsets_that_fall_make_no_row_of_two_groups(t, n, k):
+    """An offset below an earlier one counts as that one: every row of a new
+    result is of one group, or 0; each group's part of the contraction is of
+    its own rows."""
+    x, b = _values((t, k), BF16, 97).cuda(), _random_held(n, k, 98, lead=(3,))
+    x64 = R.host(x)
+    for bad in _falling(t):
+        print("falling", t, n, k, bad, flush=True)
+        off = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        rising = np.maximum.accumulate(np.clip(bad, 0, t))
+        rest = torch.full((t, n), float("nan"), dtype=BF16, device="cuda")
+        del rest                                       # what a new result is made of
+        got = ou.mx4_grouped_matmul(x, b, off)
+        into = torch.full((t, n), 5.0, dtype=BF16, device="cuda")
+        ou.mx4_grouped_matmul(x, b, off, out=into)
+        q, xt = ou.mx4_quantize_grouped(x, off)
+        assert torch.equal(got, ou.mx4_grouped_matmul(q, b, off))
+        dw = ou.mx4_grouped_outer(xt, xt, off, t, F32) if k < 1000 else None
+        inside = np.zeros(t, bool)
+        for e, (lo, hi) in enumerate(zip(rising[:-1], rising[1:])):
+            inside[lo:hi] = True
+            R.check_product(got[lo:hi], *R.product(R.rounded(x64[lo:hi]), R.held(b[e])), k)
+            if dw is not None:
+                R.check_product(dw[e], *R.product(R.rounded(x64[lo:hi].T), R.rounded(x64[lo:hi].T)), max(1, hi - lo))
+        inside = torch.from_numpy(inside).cuda()
+        assert (got[~inside] == 0).all() and (into[~inside] == 5).all() and torch.equal(into[inside], got[inside])
+
+
+@pytest.mark.parametrize("groups", [63, 64, 65, 150, 200])
+def test_offsets_of_many_groups_that_fall(groups):
+    """More groups than lanes: what an earlier chunk of groups has reached
+    counts for the later ones."""
+    t, n, k = 1000, 40, 130
+    g = _gen(groups)
+    bad = torch.sort(torch.randint(-20, t + 20, (groups + 1,), generator=g)).values
+    bad += torch.randint(-60, 60, (groups + 1,), generator=g)
+    bad[groups // 2] = t - 300                          # behind it most fall
+    rising = np.maximum.accumulate(np.clip(bad.numpy(), 0, t))
+    off = bad.to(torch.int32).cuda()
+    x, b = _values((t, k), BF16, 99).cuda(), _random_held(n, k, 100, lead=(groups,))
+    x64 = R.host(x)
+    for rows in (t, 37):                                # few rows a group, and hardly any
+        ends = np.minimum(rising, rows)
+        got = ou.mx4_grouped_matmul(x[:rows], b, off)
+        _, xt = ou.mx4_quantize_grouped(x[:rows], off)
+        dw = ou.mx4_grouped_outer(xt, xt, off, rows, F32)
+        inside = torch.zeros(rows, dtype=torch.bool, device="cuda")
+        for e, (lo, hi) in enumerate(zip(ends[:-1], ends[1:])):
+            inside[lo:hi] = True
+            R.check_product(got[lo:hi], *R.product(R.rounded(x64[lo:hi]), R.held(b[e])), k)
+            R.check_product(dw[e], *R.product(R.rounded(x64[lo:hi].T), R.rounded(x64[lo:hi].T)), max(1, hi - lo))
+        assert (got[~inside] == 0).all()
