@@ -24,6 +24,8 @@ import ctypes
 import functools
 import math
 import os
+import warnings
+import weakref
 
 import torch
 
@@ -440,7 +442,14 @@ class Mx4Weight:
     ``q`` along K (forward) and ``qt`` along N (the input's gradient).
     ``refresh()`` quantises the weight's present values into them; an optimizer
     that it is given to (``attach_mx4``) does so after every step, so that the
-    passes in between (micro-batches) read the 4-bit forms alone."""
+    passes in between (micro-batches) read the 4-bit forms alone.  The layers
+    use the forms as they are and warn where the weight was written since:
+    by torch, by assigning another one, or by a step of a collection optimizer
+    that the forms are not attached to.  (Single updates and plans, and writes
+    through ``weight.data``, are not seen.)"""
+
+    live = weakref.WeakSet()
+    _made_of = None   # address and version of the weight that the forms are of
 
     def __init__(self, weight: torch.Tensor):
         if weight.dim() not in (2, 3):
@@ -450,6 +459,17 @@ class Mx4Weight:
         self.weight = weight
         self.version = 0   # of the forms: a backward pass refuses later ones than its forward pass read
         self.q, self.qt = mx4_quantize_both(weight.detach())
+        self._made_of = self._weight_state()
+        Mx4Weight.live.add(self)
+
+    def _weight_state(self) -> tuple[int, int]:
+        w = self.weight
+        return w.data_ptr(), 0 if w.is_inference() else w._version
+
+    def _warn_if_stale(self) -> None:
+        if self._made_of != self._weight_state():
+            warnings.warn("the weight was written after its 4-bit forms were made, and the layer uses the forms: "
+                          "refresh() brings them up to date", stacklevel=4)
 
     def _check_forms(self) -> None:
         """Raises if the weight has taken another shape or device than its
@@ -472,6 +492,7 @@ class Mx4Weight:
             raise ValueError("the weight changed its layout")
         _run(w.get_device(), stream, self._refresh, w, dt)
         self.version += 1
+        self._made_of = self._weight_state()
 
     def _refresh(self, w, dt, handle):
         *lead, r, c = w.shape
@@ -653,6 +674,8 @@ def _layer_operands(x, w, dims: int):
         raise ValueError("w must be contiguous")
     if x.dim() < 2 or x.shape[-1] != weight.shape[-1]:
         raise ValueError(f"x must be [..., {weight.shape[-1]}], got {list(x.shape)}")
+    if held is not None:
+        held._warn_if_stale()
     return held, weight
 
 
@@ -670,8 +693,9 @@ def mx4_linear(x: torch.Tensor, w) -> torch.Tensor:
         y = Q(x) Q(w)^T,  dx = Q(dy) Q(w^T)^T,  dw = Q(dy^T) Q(x^T)^T,
     each summed in binary32 and rounded once to the dtype of x (y, dx) or w
     (dw).  x is [..., K], w [N, K] or an ``Mx4Weight`` (its 4-bit forms are
-    used as they are, its ``weight`` gets the gradient; it must not be
-    refreshed before the backward pass).  For the backward pass 4-bit forms
+    used as they are, with a warning if the weight was written since; its
+    ``weight`` gets the gradient; it must not be refreshed before the backward
+    pass).  For the backward pass 4-bit forms
     are kept, not x."""
     held, weight = _layer_operands(x, w, 2)
     if x.dim() == 2:

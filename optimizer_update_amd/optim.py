@@ -39,6 +39,7 @@ from .mx4 import Mx4Weight
 class _Mx4Copies:
     """The 4-bit copies of weights that an optimizer keeps up to date."""
     _mx4 = ()
+    _mine = None
 
     def attach_mx4(self, weights) -> None:
         """Refresh these ``Mx4Weight``s (of parameters of this optimizer) after
@@ -54,8 +55,16 @@ class _Mx4Copies:
         self._mx4 = weights
 
     def _refresh_mx4(self, stream) -> None:
+        """After a step: refresh what is attached; forms of these parameters
+        that are not are out of date now."""
         for w in self._mx4:
             w.refresh(stream)
+        if len(Mx4Weight.live) > len(self._mx4):
+            if self._mine is None:   # parameters stay in place
+                self._mine = {p.data_ptr() for p in self.params if p.numel()}
+            for w in Mx4Weight.live.difference(self._mx4):
+                if w.weight.data_ptr() in self._mine:
+                    w._made_of = None
 
 
 class _Collection(_Mx4Copies):

@@ -2,6 +2,8 @@
 (tests/mx4_reference.py).  Quantisation and dequantisation are exact: codes,
 scales and values are compared for equality.  Products are held to the
 tolerance derived there."""
+import warnings
+
 import numpy as np
 import pytest
 import torch
@@ -810,3 +812,43 @@ def test_offsets_of_many_groups_that_fall(groups):
             R.check_product(got[lo:hi], *R.product(R.rounded(x64[lo:hi]), R.held(b[e])), k)
             R.check_product(dw[e], *R.product(R.rounded(x64[lo:hi].T), R.rounded(x64[lo:hi].T)), max(1, hi - lo))
         assert (got[~inside] == 0).all()
+
+
+def test_forms_older_than_their_weight_are_used_with_a_warning():
+    """The layers use kept forms as they are; a weight that torch, a new
+    tensor or an optimizer without these forms has written since is warned of,
+    until the forms are refreshed."""
+    x = _values((9, 96), BF16, 101).cuda()
+    w = torch.nn.Parameter(_values((64, 96), BF16, 102, special=False).cuda())
+    w.grad = torch.ones_like(w)
+    held, other = ou.Mx4Weight(w), ou.Mx4Weight(torch.ones(64, 96, device="cuda", dtype=BF16))
+    opt = ou.AdamW32([w], lr=1e-2)
+
+    def quiet(form=held):
+        with warnings.catch_warnings():
+            warnings.simplefilter("error")
+            return ou.mx4_linear(x, form)
+
+    def stepped(attached):
+        opt.attach_mx4(attached)
+        opt.step()
+
+    def assigned():
+        held.weight = torch.nn.Parameter(w.detach() + 1)
+
+    quiet()
+    for write in (lambda: w.detach().copy_(_values((64, 96), BF16, 103)), lambda: stepped([]), assigned):
+        old = quiet()
+        write()
+        with pytest.warns(UserWarning, match="refresh"):
+            assert torch.equal(ou.mx4_linear(x, held), old)
+        held.refresh()
+        assert torch.equal(quiet(), ou.mx4_linear(x, held.weight))
+    held.weight = w
+    stepped([held])
+    assert torch.equal(quiet(), ou.mx4_linear(x, w))
+    quiet(other)
+    with torch.inference_mode():
+        form = ou.Mx4Weight(torch.ones(64, 96, device="cuda", dtype=BF16))
+        quiet(form)
+    opt.close()
