@@ -11,6 +11,8 @@
  * anything is launched, on an error nothing is launched or written, calls
  * enqueue on `stream` (hipStream_t, NULL = the default stream) and return
  * without synchronising, and all of them may be captured into a graph.
+ * Sizes that pass what one launch can hold (some 2^30 rows or columns) are
+ * OU_EINVAL.
  * The library is liboptimizer_mx4.so.
  *
  * Format.  A block is 32 neighbouring values along the contracted axis,

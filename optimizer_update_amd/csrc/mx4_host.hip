@@ -107,14 +107,30 @@ double extent(int64_t rows, int64_t cols, int64_t stride, int bytes)
     return (static_cast<double>(rows - 1) * static_cast<double>(stride) + static_cast<double>(cols)) * bytes;
 }
 
-int launch(const void* fn, int64_t gx, int64_t gy, int threads, void** args, void* stream, const char* what,
-           int64_t lds = 0)
+struct Launch {
+    const void* fn;
+    int64_t gx, gy;
+    int threads;
+    const char* what;
+    int64_t lds;
+};
+
+// A grid's threads along an axis are counted in 32 bits.
+int check_grid(const Launch& l)
 {
-    if (gx > INT32_MAX || gy > kMaxBatch) return fail(OU_EINVAL, "%s: too many tiles", what);
-    const hipError_t e = hipLaunchKernel(fn, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)),
-                                         dim3(static_cast<unsigned>(threads)), args, static_cast<size_t>(lds),
+    if (l.gx > INT32_MAX || l.gx * l.threads > UINT32_MAX || l.gy > kMaxBatch)
+        return fail(OU_EINVAL, "%s: too many tiles", l.what);
+    return OU_OK;
+}
+
+int launch(const Launch& l, void** args, void* stream)
+{
+    if (int st = check_grid(l)) return st;
+    if (int st = check_device()) return st;
+    const hipError_t e = hipLaunchKernel(l.fn, dim3(static_cast<unsigned>(l.gx), static_cast<unsigned>(l.gy)),
+                                         dim3(static_cast<unsigned>(l.threads)), args, static_cast<size_t>(l.lds),
                                          static_cast<hipStream_t>(stream));
-    return e == hipSuccess ? OU_OK : hip_fail(e, what);
+    return e == hipSuccess ? OU_OK : hip_fail(e, l.what);
 }
 
 int64_t grouped_units(int64_t rows, int32_t groups, int64_t unit)
@@ -135,12 +151,12 @@ int launch_quantize(int dtype, QuantArgs& q, int64_t batch, int64_t units, void*
         if (q.rows * (q.pcols / kPad) > UINT32_MAX / 2) return fail(OU_EINVAL, "x is too large");
         uint32_t n = static_cast<uint32_t>(q.rows * (q.pcols / kPad));
         void* args[] = {&q, &n};
-        return launch(quant_rows_kernel(dtype), cut(n, (kQuantThreads / 16) * kQuantUnits), batch, kQuantThreads, args,
-                      stream, "k_quant_rows");
+        return launch({quant_rows_kernel(dtype), cut(n, (kQuantThreads / 16) * kQuantUnits), batch, kQuantThreads,
+                       "k_quant_rows", 0}, args, stream);
     }
     void* args[] = {&q};
-    return launch(quant_tile_kernel(dtype), units * (q.pcols / kQuantTile), batch, kQuantThreads, args, stream,
-                  "k_quant_tile");
+    return launch({quant_tile_kernel(dtype), units * (q.pcols / kQuantTile), batch, kQuantThreads, "k_quant_tile", 0},
+                  args, stream);
 }
 
 // Which kernel makes a product: a tile of k_matmul_tile, or 0 and the columns of
@@ -200,7 +216,8 @@ Choice choose_grouped(int64_t rows, int64_t n, int64_t steps, int32_t groups)
 // finds them in the cache otherwise.
 constexpr int64_t kKeptBytes = int64_t(192) << 20;
 
-int launch_matmul(int out_dtype, int grouping, const Choice& c, MatmulArgs& p, int64_t batch, void* stream)
+// The launch of a product, and what goes by it in p.
+Launch matmul_launch(int out_dtype, int grouping, const Choice& c, MatmulArgs& p, int64_t batch)
 {
     const TileKernel t = c.tile ? matmul_tile_kernel(out_dtype, grouping, c.tile, c.shared) : TileKernel{};
     const FewKernel f = c.tile ? FewKernel{} : matmul_few_kernel(p.x ? p.x_dtype : kHeld, grouping, c.cols);
@@ -212,9 +229,8 @@ int launch_matmul(int out_dtype, int grouping, const Choice& c, MatmulArgs& p, i
     p.wide = wide_rows(p.out, p.out_stride, grouping == kByContraction ? p.m * p.out_stride : 0, elem_bytes(out_dtype),
                        c.tile ? 16 : 4 * elem_bytes(out_dtype));
     p.past_caches = p.m * (grouping == kByContraction ? p.groups : 1) * p.n * elem_bytes(out_dtype) > kKeptBytes;
-    void* args[] = {&p};
-    return launch(c.tile ? t.fn : f.fn, p.units * p.n_tiles, batch, c.tile ? t.threads : kWave * f.waves, args, stream,
-                  "the product's kernel", c.tile ? 0 : few_lds(p.few_rows, p.steps, cols, f.waves));
+    return {c.tile ? t.fn : f.fn, p.units * p.n_tiles, batch, c.tile ? t.threads : kWave * f.waves,
+            "the product's kernel", c.tile ? 0 : few_lds(p.few_rows, p.steps, cols, f.waves)};
 }
 
 int check_groups(const int32_t* offsets, int32_t groups, int64_t rows)
@@ -265,7 +281,6 @@ OU_EXPORT int ou_mx4_quantize(int dtype, const void* x, int64_t batch, int64_t r
                            {"codes_t", codes_t, codes_t ? held_codes(batch * cols, pad(rows)) : 0, 16, true},
                            {"scales_t", scales_t, scales_t ? held_scales(batch * cols, pad(rows)) : 0, 4, true}};
     if (int st = check_buffers(bufs, 5)) return st;
-    if (int st = check_device()) return st;
     QuantArgs q{x, codes, scales, codes_t, scales_t, rows, cols, row_stride, batch_stride, pad(cols), pad(rows), nullptr,
                 0, 0};
     return launch_quantize(dtype, q, batch, pad(rows) / kQuantTile, stream);
@@ -292,7 +307,6 @@ OU_EXPORT int ou_mx4_quantize_grouped(int dtype, const void* x, int64_t rows, in
                            {"codes_t", codes_t, held_codes(cols, pr), 16, true},
                            {"scales_t", scales_t, held_scales(cols, pr), 4, true}};
     if (int st = check_buffers(bufs, 6)) return st;
-    if (int st = check_device()) return st;
     QuantArgs q{x, codes, scales, codes_t, scales_t, rows, cols, row_stride, 0, pad(cols), pr, offsets, groups, 0};
     return launch_quantize(dtype, q, 1, pr / kQuantTile, stream);
 }
@@ -310,13 +324,12 @@ OU_EXPORT int ou_mx4_dequantize(int dtype, const uint8_t* codes, const uint8_t* 
                            {"scales", scales, held_scales(rows, pad(cols)), 4, false},
                            {"out", out, extent(rows, cols, row_stride, eb), static_cast<unsigned>(eb), true}};
     if (int st = check_buffers(bufs, 3)) return st;
-    if (int st = check_device()) return st;
     DequantArgs d{codes, scales, out, rows, cols, pad(cols), row_stride, wide_rows(out, row_stride, 0, eb, 16)};
     if (rows * (pad(cols) / kPad) > UINT32_MAX / 2) return fail(OU_EINVAL, "the matrix is too large");
     uint32_t units = static_cast<uint32_t>(rows * (pad(cols) / kPad));
     void* args[] = {&d, &units};
-    return launch(dequant_kernel(dtype), cut(units, (kQuantThreads / 16) * kQuantUnits), 1, kQuantThreads, args, stream,
-                  "k_dequant");
+    return launch({dequant_kernel(dtype), cut(units, (kQuantThreads / 16) * kQuantUnits), 1, kQuantThreads, "k_dequant",
+                   0}, args, stream);
 }
 
 OU_EXPORT int64_t ou_mx4_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k, int from_values)
@@ -384,8 +397,6 @@ int product(Product& q, bool values, bool grouped)
                            {"workspace", q.workspace, static_cast<double>(need), 16, true},
                            {"out", q.out, extent(q.m, q.n, q.out_stride, eo), static_cast<unsigned>(eo), true}};
     if (int st = check_buffers(bufs, 8)) return st;
-    if (int st = check_device()) return st;
-    const uint8_t *a = q.a, *as = q.as;
     const Choice c = grouped ? choose_grouped(q.m, q.n, pk / kPad, q.groups) : choose(q.m, q.n, pk / kPad, 1, q.m);
     MatmulArgs p{};
     if (values && c.values) {   // quantised where it is multiplied
@@ -395,16 +406,11 @@ int product(Product& q, bool values, bool grouped)
         p.k = q.k;
         p.few_rows = static_cast<int32_t>(q.m < 16 ? q.m : 16);
         p.x_wide = wide_rows(q.x, q.x_stride, 0, ex, 16);
-    } else if (values && pk > 0) {
-        uint8_t* wc = static_cast<uint8_t*>(q.workspace);
-        uint8_t* wsc = wc + q.m * (pk / 2);
-        QuantArgs qa{q.x, wc, wsc, nullptr, nullptr, q.m, q.k, q.x_stride, 0, pk, 0, nullptr, 0, 0};
-        if (int st = launch_quantize(q.x_dtype, qa, 1, 0, q.stream)) return st;
-        a = wc;
-        as = wsc;
     }
-    p.a = a;
-    p.as = as;
+    uint8_t* const wc = static_cast<uint8_t*>(q.workspace);
+    const bool first = values && !c.values && pk > 0;   // quantised by a kernel of its own
+    p.a = first ? wc : q.a;
+    p.as = first ? wc + q.m * (pk / 2) : q.as;
     p.b = q.b;
     p.bs = q.bs;
     p.out = q.out;
@@ -416,7 +422,14 @@ int product(Product& q, bool values, bool grouped)
     p.rows = q.m;
     p.groups = q.groups;
     p.zero_rest = q.zero_rest != 0;
-    return launch_matmul(q.out_dtype, grouped ? kByRows : kPlain, c, p, 1, q.stream);
+    const Launch l = matmul_launch(q.out_dtype, grouped ? kByRows : kPlain, c, p, 1);
+    if (int st = check_grid(l)) return st;
+    if (first) {
+        QuantArgs qa{q.x, wc, wc + q.m * (pk / 2), nullptr, nullptr, q.m, q.k, q.x_stride, 0, pk, 0, nullptr, 0, 0};
+        if (int st = launch_quantize(q.x_dtype, qa, 1, 0, q.stream)) return st;
+    }
+    void* args[] = {&p};
+    return launch(l, args, q.stream);
 }
 
 }  // namespace
@@ -481,7 +494,6 @@ OU_EXPORT int ou_mx4_grouped_outer(int out_dtype, const uint8_t* a_codes_t, cons
                            {"offsets", offsets, 4.0 * (groups + 1.0), 4, false},
                            {"out", out, static_cast<double>(groups) * m * n * eo, static_cast<unsigned>(eo), true}};
     if (int st = check_buffers(bufs, 6)) return st;
-    if (int st = check_device()) return st;
     MatmulArgs p{};
     p.a = a_codes_t;
     p.as = a_scales_t;
@@ -496,7 +508,8 @@ OU_EXPORT int ou_mx4_grouped_outer(int out_dtype, const uint8_t* a_codes_t, cons
     p.rows = rows;
     p.groups = groups;
     const Choice c = choose(m > 16 ? m : 17, n, p.steps, groups, 16);   // few rows have no kernel of their own here
-    return launch_matmul(out_dtype, kByContraction, c, p, groups, stream);
+    void* args[] = {&p};
+    return launch(matmul_launch(out_dtype, kByContraction, c, p, groups), args, stream);
 }
 
 }  // extern "C"

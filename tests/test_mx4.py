@@ -305,3 +305,32 @@ def test_kept_forms_on_another_device_are_refused():
     for call in (held._check_forms, held.refresh, lambda: ou.mx4_linear(torch.zeros(5, 96), held)):
         with pytest.raises(ValueError, match="forms are on another device"):
             call()
+
+
+FAR = [1 << 43, 2 << 43, 3 << 43, 4 << 43, 5 << 43, 6 << 43, 7 << 43]
+
+
+def test_more_tiles_than_a_launch_holds_are_refused(L):
+    """Grids of 2^32 threads and more: refused with the other checks, before
+    a device is looked for or anything (a left matrix's 4-bit form) is made."""
+    x, c, s, ct, st, w, o = FAR
+    big = 1 << 30
+    quantize = lambda rows, *to: L.ou_mx4_quantize(2, x, 1, rows, 1, 1, 0, *to, None)  # noqa: E731
+    need = L.ou_mx4_matmul_workspace_bytes(4096, 1 << 31, 1, 1)
+    calls = [lambda: quantize(big, c, s, None, None), lambda: quantize(1 << 31, None, None, ct, st),
+             lambda: L.ou_mx4_dequantize(0, c, s, big, 1, o, 1, None),
+             lambda: L.ou_mx4_matmul(2, x, s, 1, c, st, big, 1, o, big, None, 0, None),
+             lambda: L.ou_mx4_matmul_values(2, x, 4096, 1, 2, c, s, 1 << 31, 1, o, 1 << 31, w, need, None),
+             lambda: L.ou_mx4_grouped_matmul(2, x, s, 65535, c, st, 1 << 20, 1, ct, 65535, o, 1 << 20, 0, None, 0, None),
+             lambda: L.ou_mx4_grouped_outer(2, x, s, 1 << 20, c, st, 1 << 20, 1, ct, 2, o, None)]
+    for i, call in enumerate(calls):
+        assert call() == EINVAL, i
+        assert "too many tiles" in L.ou_mx4_last_error().decode() or "too large" in L.ou_mx4_last_error().decode(), i
+
+
+def test_the_largest_grids_pass_the_checks(L, no_gpu):
+    x, c, s, ct, st, w, o = FAR
+    n = (1 << 30) - 64
+    assert L.ou_mx4_quantize(2, x, 1, n, 1, 1, 0, c, s, None, None, None) == EUNSUPPORTED
+    assert L.ou_mx4_quantize(2, x, 1, (1 << 31) - 128, 1, 1, 0, None, None, ct, st, None) == EUNSUPPORTED
+    assert L.ou_mx4_matmul(2, x, s, 1, c, st, n, 1, o, n, None, 0, None) == EUNSUPPORTED
