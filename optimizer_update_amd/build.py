@@ -40,10 +40,11 @@ HIPCC_FLAGS = [
 
 
 def build(out_path: str = LIBRARY, extra_flags: list[str] | None = None, quiet: bool = True) -> str:
-    """Compile the library (always; atomically replaces ``out_path``), the
-    library of the 4-bit operators and the CPython module."""
+    """Compile the library (always; atomically replaces ``out_path``) and the
+    CPython module, and with the in-tree library that of the 4-bit operators."""
     _compile(SOURCES, out_path, extra_flags, quiet)
-    _compile(MX4_SOURCES, MX4_LIBRARY, extra_flags, quiet)
+    if out_path == LIBRARY:
+        _compile(MX4_SOURCES, MX4_LIBRARY, extra_flags, quiet)
     build_fast()
     return out_path
 

@@ -334,3 +334,17 @@ def test_the_largest_grids_pass_the_checks(L, no_gpu):
     assert L.ou_mx4_quantize(2, x, 1, n, 1, 1, 0, c, s, None, None, None) == EUNSUPPORTED
     assert L.ou_mx4_quantize(2, x, 1, (1 << 31) - 128, 1, 1, 0, None, None, ct, st, None) == EUNSUPPORTED
     assert L.ou_mx4_matmul(2, x, s, 1, c, st, n, 1, o, n, None, 0, None) == EUNSUPPORTED
+
+
+def test_a_build_elsewhere_leaves_the_library_alone(monkeypatch, tmp_path):
+    """A build of the update library to another path, with other flags,
+    compiles nothing over this library."""
+    from optimizer_update_amd import build
+    made = []
+    monkeypatch.setattr(build, "_compile", lambda sources, out, flags, quiet: made.append((out, flags)))
+    monkeypatch.setattr(build, "build_fast", lambda: None)
+    other = str(tmp_path / "variant.so")
+    assert build.build(other, ["-g"]) == other and made == [(other, ["-g"])]
+    made.clear()
+    build.build()
+    assert made == [(build.LIBRARY, None), (mx4.LIBRARY, None)] and build.MX4_LIBRARY == mx4.LIBRARY
