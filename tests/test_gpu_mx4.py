@@ -852,3 +852,51 @@ def test_forms_older_than_their_weight_are_used_with_a_warning():
         form = ou.Mx4Weight(torch.ones(64, 96, device="cuda", dtype=BF16))
         quiet(form)
     opt.close()
+
+
+def _check_by_rows(counts, front, back, n, k, dtype, seed):
+    t, e = front + sum(counts) + back, len(counts)
+    off = _offsets(counts, front).cuda()
+    x, b = _values((t, k), dtype, seed).cuda(), _random_held(n, k, seed + 1, lead=(e,))
+    q = ou.mx4_quantize(x)
+    got = ou.mx4_grouped_matmul(q, b, off, dtype)
+    assert torch.equal(got, ou.mx4_grouped_matmul(x, b, off))
+    buf = torch.full((t, n + 3), 5.0, dtype=dtype, device="cuda")
+    ou.mx4_grouped_matmul(q, b, off, out=buf[:, :n])
+    held = R.held(q)
+    for i, (lo, hi) in enumerate(zip(off[:-1].tolist(), off[1:].tolist())):
+        R.check_product(got[lo:hi], *R.product(held[lo:hi], R.held(b[i])), k)
+    for rest in (slice(0, front), slice(t - back, t)):
+        assert (got[rest] == 0).all() and (buf[rest] == 5).all()
+    assert torch.equal(buf[front:t - back, :n], got[front:t - back]) and (buf[:, n:] == 5).all()
+
+
+# By rows, 64-tiles whose k-steps two groups of waves share (17, 33 and 16
+# steps, the last two groups' parts of even and odd numbers); then 256-tiles of
+# 3 and 8 steps with ragged edges and rows of no group.
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("counts,front,back,n,k", [([33, 0, 64, 200], 2, 5, 150, 2060), ([70, 1, 129], 0, 1, 65, 4100),
+                                                   ([20, 31, 17], 1, 0, 257, 2048), ([2400, 0, 1500, 1893], 3, 4, 2100, 300),
+                                                   ([1900, 1301, 1107], 3, 4, 2101, 900)])
+def test_grouped_matmul_of_every_tile(counts, front, back, n, k, dtype):
+    print("by rows", counts, n, k, dtype, flush=True)
+    _check_by_rows(counts, front, back, n, k, dtype, 110)
+
+
+# By contraction: 64-tiles with shared k-steps, groups of 11, 0, 2, 6, 3 and 1
+# steps (a group's steps start anywhere, its second half is odd, or nothing);
+# of 21, 1 and 12; then tiles of 128 and of 256 with odd numbers of steps.
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("counts,m,n", [([1400, 0, 129, 700, 300, 1], 140, 270), ([2600, 100, 1500], 20, 33),
+                                        ([300, 0, 700], 1200, 1100), ([300, 650, 130], 2100, 2101)])
+def test_grouped_outer_of_every_tile(counts, m, n, dtype):
+    print("by contraction", counts, m, n, dtype, flush=True)
+    front, back = 1, 2
+    t = front + sum(counts) + back
+    off = _offsets(counts, front)
+    a, b = _values((t, m), dtype, 112), _values((t, n), dtype, 113)
+    at, bt = (ou.mx4_quantize_grouped(v.cuda(), off.cuda(), rows=False)[1] for v in (a, b))
+    got = ou.mx4_grouped_outer(at, bt, off.cuda(), t, dtype)
+    a64, b64 = R.host(a), R.host(b)
+    for i, (lo, hi) in enumerate(zip(off[:-1].tolist(), off[1:].tolist())):
+        R.check_product(got[i], *R.product(R.rounded(a64[lo:hi].T), R.rounded(b64[lo:hi].T)), max(1, hi - lo))
