@@ -142,6 +142,8 @@ class _Call:
         else:
             if not isinstance(stream, torch.cuda.Stream):
                 stream = torch.cuda.ExternalStream(int(stream), device=torch.device("cuda", index))
+            if stream.device_index != index:
+                raise ValueError(f"the stream is on device {stream.device_index}, the operands on {index}")
             self._ctx = torch.cuda.stream(stream)
             self.handle = stream.cuda_stream
         if stream is None:

@@ -1,5 +1,6 @@
 """CPU: the library of the 4-bit operators: its exports, its refusals (no
 device is touched before the arguments are checked) and the binding's."""
+import contextlib
 import ctypes
 import os
 import re
@@ -348,3 +349,17 @@ def test_a_build_elsewhere_leaves_the_library_alone(monkeypatch, tmp_path):
     made.clear()
     build.build()
     assert made == [(build.LIBRARY, None), (mx4.LIBRARY, None)] and build.MX4_LIBRARY == mx4.LIBRARY
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    """A stream object names its device: the kernels would run there on
+    addresses of the operands' device."""
+    class Stream:
+        def __init__(self, index):
+            self.device_index, self.cuda_stream = index, 7
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    assert mx4._run(1, Stream(1), lambda a, handle: (a, handle), 5) == (5, 7)
+    with pytest.raises(ValueError, match="device 0"):
+        mx4._run(1, Stream(0), lambda a, handle: pytest.fail("called"), 5)
