@@ -86,7 +86,9 @@ int ou_mx4_dequantize(int dtype, const uint8_t* codes, const uint8_t* scales, in
  * rounded once to out_dtype (nearest even).
  * `workspace` is caller-owned device memory of at least
  * ou_mx4_matmul_workspace_bytes(m, n, k, 0) bytes, 16-byte aligned (NULL if
- * that is 0); calls that may overlap in time need workspaces of their own. */
+ * that is 0, as it is where both matrices are held: what a workspace takes is
+ * the 4-bit form of a left matrix given as values); calls that may overlap in
+ * time need workspaces of their own. */
 int64_t ou_mx4_matmul_workspace_bytes(int64_t m, int64_t n, int64_t k, int from_values);
 int ou_mx4_matmul(int out_dtype, const uint8_t* a_codes, const uint8_t* a_scales, int64_t m,
                   const uint8_t* b_codes, const uint8_t* b_scales, int64_t n, int64_t k, void* out,

@@ -59,7 +59,7 @@ struct MatmulArgs {
     int64_t rows;             // grouped: rows that offsets may point to
     int32_t groups;
     int32_t zero_rest;        // grouped by rows: rows of no group become 0
-    int32_t wide;             // stores of 4 neighbouring results (tiles 128, 256: of 16 bytes) are aligned
+    int32_t wide;             // stores of 4 neighbouring results (tiles: of 16 bytes) are aligned
     int32_t past_caches;      // tiles: out is too large to stay in the last cache
     int32_t out_dtype;        // k_matmul_few
     // the left matrix as values (k_matmul_few)

@@ -187,7 +187,10 @@ Choice choose(int64_t rows, int64_t n, int64_t steps, int64_t batch, int64_t roo
     // 1500 (576 tiles) 10.9 against 10.3.  Two groups of waves share a long
     // chain of k-steps: k = 4096 10.1 us against 11.3 with one tile a CU and
     // 13.7 against 14.1 with two, k = 1024 5.3 against 5.1 and 7.4 against 6.3
-    // (four groups: 10.4 and 18.3 us with k = 4096).
+    // (four groups: 10.4 and 18.3 us with k = 4096).  Rows of results that
+    // are not 16-byte aligned and an odd number of k-steps cost every tile
+    // about as much: 777 x 2063 x 4104 17.6 us, by 128-tiles 17.2; x 2064 x
+    // 4096 13.0 against 14.1.
     if (t64 <= 512) return {64, 0, false, steps >= (t64 <= 256 ? 16 : 32)};
     // Rounds of the device, in tenths of a microsecond per pair of k-steps as
     // measured with 4096 columns: 256-tiles one a CU, 12 + 7 by how full the
@@ -507,7 +510,9 @@ OU_EXPORT int ou_mx4_grouped_outer(int out_dtype, const uint8_t* a_codes_t, cons
     p.offsets = offsets;
     p.rows = rows;
     p.groups = groups;
-    const Choice c = choose(m > 16 ? m : 17, n, p.steps, groups, 16);   // few rows have no kernel of their own here
+    // Few rows have no kernel of their own here.  The steps are those of all
+    // groups: how they are dealt is known on the device only.
+    const Choice c = choose(m > 16 ? m : 17, n, p.steps, groups, 16);
     void* args[] = {&p};
     return launch(matmul_launch(out_dtype, kByContraction, c, p, groups), args, stream);
 }

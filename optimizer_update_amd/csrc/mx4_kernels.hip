@@ -669,7 +669,7 @@ __global__ __launch_bounds__(kWave * W) void k_matmul_few(MatmulArgs p)
     const uint32_t unit = blockIdx.x / static_cast<uint32_t>(p.n_tiles);
     const uint32_t ntile = blockIdx.x - unit * static_cast<uint32_t>(p.n_tiles);
     int64_t row0 = static_cast<int64_t>(unit) * 16, mrows = p.m - row0;
-    const int row_steps = static_cast<int>(p.steps);   // below 2^18
+    const int row_steps = static_cast<int>(p.steps);   // at most 2^18
     int steps = row_steps;
     const uint8_t *b = p.b, *bs = p.bs;
     if constexpr (G == kByRows) {
