@@ -111,7 +111,7 @@ class Mx4:
         """Matrix i of a batch."""
         if self.codes.dim() < 3:
             raise ValueError("not a batch of matrices")
-        return _held(self.codes[i], self.scales[i], self.k)
+        return Mx4(self.codes[i], self.scales[i], self.k)
 
     def __repr__(self) -> str:
         return f"Mx4(shape={list(self.shape)}, device={self.device})"

@@ -363,3 +363,14 @@ def test_a_stream_of_another_device_is_refused(monkeypatch):
     assert mx4._run(1, Stream(1), lambda a, handle: (a, handle), 5) == (5, 7)
     with pytest.raises(ValueError, match="device 0"):
         mx4._run(1, Stream(0), lambda a, handle: pytest.fail("called"), 5)
+
+
+def test_parts_of_a_batch_are_held_matrices_or_refused():
+    """The kernels read codes and scales without strides: what an index leaves
+    apart in memory is refused."""
+    q = ou.Mx4(torch.arange(4 * 6 * 64).view(4, 6, 64).to(torch.uint8), torch.arange(4 * 6 * 4).view(4, 6, 4).to(torch.uint8), 100)
+    assert list(q[2].shape) == [6, 100] and torch.equal(q[-1].codes, q.codes[3]) and list(q[1:3].shape) == [2, 6, 100]
+    assert len(list(q)) == 4
+    for index in (slice(None, None, 2), (slice(None), slice(0, 3)), (0, 0), (0, slice(None), slice(0, 64))):
+        with pytest.raises(ValueError):
+            q[index]
