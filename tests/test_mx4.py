@@ -371,6 +371,7 @@ def test_parts_of_a_batch_are_held_matrices_or_refused():
     q = ou.Mx4(torch.arange(4 * 6 * 64).view(4, 6, 64).to(torch.uint8), torch.arange(4 * 6 * 4).view(4, 6, 4).to(torch.uint8), 100)
     assert list(q[2].shape) == [6, 100] and torch.equal(q[-1].codes, q.codes[3]) and list(q[1:3].shape) == [2, 6, 100]
     assert len(list(q)) == 4
-    for index in (slice(None, None, 2), (slice(None), slice(0, 3)), (0, 0), (0, slice(None), slice(0, 64))):
+    assert torch.equal(q[0, :, 0:64].codes, q.codes[0])          # all of a row's bytes
+    for index in (slice(None, None, 2), (slice(None), slice(0, 3)), (0, 0), (0, slice(None), slice(0, 32))):
         with pytest.raises(ValueError):
             q[index]
