@@ -55,16 +55,16 @@ class _Mx4Copies:
         self._mx4 = weights
 
     def _refresh_mx4(self, stream) -> None:
-        """After a step: refresh what is attached; forms of these parameters
-        that are not are out of date now."""
-        for w in self._mx4:
-            w.refresh(stream)
-        if len(Mx4Weight.live) > len(self._mx4):
+        """After a step: all forms of these parameters are out of date, and
+        those that are attached are refreshed."""
+        if Mx4Weight.live:
             if self._mine is None:   # parameters stay in place
                 self._mine = {p.data_ptr() for p in self.params if p.numel()}
-            for w in Mx4Weight.live.difference(self._mx4):
+            for w in Mx4Weight.live:
                 if w.weight.data_ptr() in self._mine:
                     w._made_of = None
+        for w in self._mx4:
+            w.refresh(stream)
 
 
 class _Collection(_Mx4Copies):

@@ -900,3 +900,19 @@ def test_grouped_outer_of_every_tile(counts, m, n, dtype):
     a64, b64 = R.host(a), R.host(b)
     for i, (lo, hi) in enumerate(zip(off[:-1].tolist(), off[1:].tolist())):
         R.check_product(got[i], *R.product(R.rounded(a64[lo:hi].T), R.rounded(b64[lo:hi].T)), max(1, hi - lo))
+
+
+def test_every_unattached_form_of_a_stepped_weight_is_stale():
+    """Also where one form is attached twice, or a copy of a form is."""
+    import copy
+    x = torch.ones(3, 64, device="cuda", dtype=BF16)
+    for attach in (lambda a: [a, a], lambda a: [copy.copy(a)]):
+        w = torch.nn.Parameter(_values((32, 64), BF16, 104, special=False).cuda())
+        w.grad = torch.ones_like(w)
+        held, other = ou.Mx4Weight(w), ou.Mx4Weight(w)
+        opt = ou.AdamW32([w], lr=1e-2)
+        opt.attach_mx4(attach(held))
+        opt.step()
+        with pytest.warns(UserWarning, match="refresh"):
+            ou.mx4_linear(x, other)
+        opt.close()
