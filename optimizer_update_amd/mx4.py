@@ -14,8 +14,9 @@ products grouped by expert (binding of ``liboptimizer_mx4.so``,
 
 As in the rest of the package, functions check and marshal arguments; all
 arithmetic runs in the HIP kernels.  Every call goes to the current stream of
-the operands' device, or to ``stream``; results and workspaces are allocated
-on that stream.  The functions other than the two layers do not record
+the operands' device, or to ``stream`` (a stream of that device or its handle,
+0 being the default stream); results and workspaces are allocated on that
+stream.  The functions other than the two layers do not record
 gradients.
 """
 from __future__ import annotations
@@ -141,7 +142,9 @@ class _Call:
             self._ctx = torch.cuda.device(index)
         else:
             if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=torch.device("cuda", index))
+                handle = int(stream)   # 0: the default stream, for which ExternalStream makes another
+                stream = (torch.cuda.ExternalStream(handle, device=torch.device("cuda", index)) if handle
+                          else torch.cuda.default_stream(index))
             if stream.device_index != index:
                 raise ValueError(f"the stream is on device {stream.device_index}, the operands on {index}")
             self._ctx = torch.cuda.stream(stream)

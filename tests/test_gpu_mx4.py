@@ -916,3 +916,22 @@ def test_every_unattached_form_of_a_stepped_weight_is_stale():
         with pytest.warns(UserWarning, match="refresh"):
             ou.mx4_linear(x, other)
         opt.close()
+
+
+def test_handle_of_the_default_stream():
+    """A call on the handle of the default stream is ordered with that stream's
+    work, also while another one is current."""
+    from optimizer_update_amd import mx4
+    handle = torch.cuda.default_stream().cuda_stream
+    with mx4._Call(torch.cuda.current_device(), handle) as got:
+        assert got == handle and torch.cuda.current_stream() == torch.cuda.default_stream()
+    w = torch.nn.Parameter(_values((512, 1024), BF16, 105, special=False).cuda())
+    w.grad = torch.ones_like(w)
+    x, held = _values((64, 1024), BF16, 106).cuda(), ou.Mx4Weight(w)
+    opt = ou.AdamW32([w], lr=1e-2)
+    opt.attach_mx4([held])
+    for _ in range(4):
+        opt.step(stream=handle)
+        got = ou.mx4_matmul(x, held.q, stream=handle)
+        assert torch.equal(got, ou.mx4_matmul(x, ou.mx4_quantize(w.detach())))
+    opt.close()

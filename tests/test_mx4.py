@@ -375,3 +375,18 @@ def test_parts_of_a_batch_are_held_matrices_or_refused():
     for index in (slice(None, None, 2), (slice(None), slice(0, 3)), (0, 0), (0, slice(None), slice(0, 32))):
         with pytest.raises(ValueError):
             q[index]
+
+
+def test_handle_0_is_the_default_stream(monkeypatch):
+    """As in the update's calls.  A stream made of the handle 0 is another one,
+    which nothing orders behind the default stream's work."""
+    class Stream:
+        def __init__(self, handle, device):
+            self.device_index, self.cuda_stream = device.index, handle or 99
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda i: type("Default", (), dict(device_index=i, cuda_stream=0))())
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    assert mx4._run(2, 0, lambda handle: handle) == 0
+    assert mx4._run(2, 55, lambda handle: handle) == 55
