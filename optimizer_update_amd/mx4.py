@@ -16,8 +16,9 @@ As in the rest of the package, functions check and marshal arguments; all
 arithmetic runs in the HIP kernels.  Every call goes to the current stream of
 the operands' device, or to ``stream`` (a stream of that device or its handle,
 0 being the default stream); results and workspaces are allocated on that
-stream.  The functions other than the two layers do not record
-gradients.
+stream.  As elsewhere in torch, an operand of another stream must stay until
+the call's work is done (``record_stream``).  The functions other than the two
+layers do not record gradients.
 """
 from __future__ import annotations
 
