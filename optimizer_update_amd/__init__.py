@@ -586,3 +586,10 @@ from .optim import AdamW8bit, AdEMAMix8bit  # noqa: E402
 
 __all__ += ["AdamW32", "AdEMAMix32", "Momentum32", "RMSprop32", "Adagrad32", "Lion32",
             "TWO_STATE", "AdamW8bit", "AdEMAMix8bit"]
+
+from .route import (RouteOrder, load_experts, route_balance, route_combine, route_dispatch, route_order,  # noqa: E402
+                    route_topk)
+from .int4 import Int4, int4_dequantize, int4_grouped_matmul, int4_matmul, int4_quantize  # noqa: E402
+
+__all__ += ["RouteOrder", "load_experts", "route_balance", "route_combine", "route_dispatch", "route_order", "route_topk",
+            "Int4", "int4_dequantize", "int4_grouped_matmul", "int4_matmul", "int4_quantize"]

@@ -30,6 +30,11 @@ HEADERS = [os.path.join(CSRC, "elem.hpp"), os.path.join(CSRC, "internal.h"),
 MX4_LIBRARY = os.path.join(HERE, "liboptimizer_mx4.so")
 MX4_SOURCES = [os.path.join(CSRC, "mx4_kernels.hip"), os.path.join(CSRC, "mx4_host.hip")]
 
+# The operators around experts (routing, 4-bit weights with group scales): likewise.
+EXPERTS_LIBRARY = os.path.join(HERE, "liboptimizer_experts.so")
+EXPERTS_SOURCES = [os.path.join(CSRC, "route_kernels.hip"), os.path.join(CSRC, "int4_kernels.hip"),
+                   os.path.join(CSRC, "experts_host.hip")]
+
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
     "-ffp-contract=off", "-fno-fast-math",
@@ -41,10 +46,12 @@ HIPCC_FLAGS = [
 
 def build(out_path: str = LIBRARY, extra_flags: list[str] | None = None, quiet: bool = True) -> str:
     """Compile the library (always; atomically replaces ``out_path``) and the
-    CPython module, and with the in-tree library that of the 4-bit operators."""
+    CPython module, and with the in-tree library those of the 4-bit operators
+    and of the operators around experts."""
     _compile(SOURCES, out_path, extra_flags, quiet)
     if out_path == LIBRARY:
         _compile(MX4_SOURCES, MX4_LIBRARY, extra_flags, quiet)
+        _compile(EXPERTS_SOURCES, EXPERTS_LIBRARY, extra_flags, quiet)
     build_fast()
     return out_path
 

@@ -1,0 +1,101 @@
+// experts.h -- declarations shared by the kernels and the host code of the
+// operators around experts.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace experts {
+
+constexpr int kWave = 64;
+
+enum Dtype { kF32 = 0, kF16 = 1, kBF16 = 2 };
+enum Scores { kSoftmax = 0, kSigmoid = 1 };
+
+struct TopkArgs {
+    const void* logits;
+    const float* bias;      // nullptr: none
+    const uint8_t* mask;    // nullptr: every token chooses
+    float* weights;
+    int32_t* ids;
+    int64_t tokens, row_stride;
+    int32_t experts, k, groups, top_groups;
+    int32_t scores, best_two, renormalize;
+    float scale;
+};
+
+struct TopkBackwardArgs {
+    const void* logits;
+    const int32_t* ids;
+    const float* dweights;
+    void* dlogits;
+    int64_t tokens, row_stride;
+    int32_t experts, k, scores, renormalize;
+    float scale;
+};
+
+struct OrderArgs {
+    const int32_t* ids;
+    int32_t* offsets;
+    int32_t* slot_of_row;
+    int32_t* row_of_slot;
+    int32_t* counts;        // [blocks][experts + 1]
+    int64_t slots, chunk;   // slots of a block
+    int32_t experts, blocks;
+};
+
+// Rows of x or y: `units` pieces of a vector load (wide) or single elements.
+struct RowsArgs {
+    const void* x;          // dispatch: x; combine: y; its gradient: dout
+    const void* y;          // gradient: y
+    const void* add;
+    const float* weights;
+    const int32_t* slot_of_row;
+    const int32_t* row_of_slot;
+    void* out;              // gradient: dy
+    float* dweights;
+    int64_t tokens, cols, x_stride, y_stride, add_stride, out_stride;
+    int32_t k, zero_rest;
+};
+
+// 4-bit weights; experts 0: one matrix, no groups of rows.
+struct Int4Args {
+    const void* x;
+    const uint8_t* codes;
+    const void* scales;
+    const void* zeros;      // nullptr: 8
+    void* out;
+    const int32_t* offsets;
+    int64_t m, n, k, x_stride, out_stride;
+    int32_t group, experts, zero_rest, x_dtype, out_dtype, scale_dtype;
+};
+
+struct Int4QuantArgs {
+    const void* x;
+    uint8_t* codes;
+    void* scales;
+    void* zeros;
+    int64_t rows, k, row_stride;
+    int32_t group, scale_dtype;
+};
+
+const void* topk_kernel(int dtype);
+const void* topk_backward_kernel(int dtype);
+const void* order_count_kernel();
+const void* order_place_kernel();
+const void* dispatch_kernel(int bytes, bool wide);
+const void* combine_kernel(int dtype, bool wide);
+const void* combine_backward_kernel(int dtype, bool wide);
+const void* balance_kernel();
+const void* int4_quantize_kernel(int dtype);
+const void* int4_dequantize_kernel(int dtype);
+const void* int4_matmul_kernel(bool grouped);
+
+constexpr int kTopkWaves = 4;          // tokens of a block
+constexpr int kOrderThreads = 512;
+constexpr int kOrderChunk = 4096;      // slots of a block, at least
+constexpr int kOrderBlocks = 256;      // at most
+constexpr int kRowThreads = 256;
+constexpr int kInt4Threads = 256;
+
+}  // namespace experts

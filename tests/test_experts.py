@@ -1,0 +1,289 @@
+"""CPU: the library of the operators around experts: its exports, its
+refusals (no device is touched before the arguments are checked) and the
+binding's; and the 64-bit definitions that the GPU tests compare with."""
+import os
+import re
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+import optimizer_update_amd as ou
+from optimizer_update_amd import _lib, route
+from tests import experts_reference as R
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+OK, EINVAL, EUNSUPPORTED, EALIGN, EOVERLAP = 0, -1, -2, -3, -4
+A, B, C, D, E, F, G = (0x100000000 * i for i in range(1, 8))
+
+
+@pytest.fixture(scope="module")
+def L():
+    return ou.load_experts()
+
+
+@pytest.fixture
+def no_gpu():
+    if torch.cuda.is_available():
+        pytest.skip("calls that pass the checks would launch on these addresses")
+
+
+def test_exports_every_header_function(L):
+    names = _lib.header_functions(route.HEADER)
+    assert len(names) == 13 and len(set(names)) == 13
+    out = subprocess.run(["nm", "-D", "--defined-only", route.LIBRARY], capture_output=True, text=True, check=True).stdout
+    assert set(re.findall(r" T (\w+)$", out, flags=re.M)) == set(names)
+
+
+def test_header_is_plain_c(tmp_path):
+    c = tmp_path / "t.c"
+    c.write_text('#include "optimizer_experts.h"\nint main(void) { return ou_route_order_workspace_bytes(1, 1) ? 1 : 0; }\n')
+    subprocess.run(["gcc", "-std=c11", "-Wall", "-Werror", "-I", os.path.join(ROOT, "include"), "-c", str(c), "-o",
+                    str(tmp_path / "t.o")], check=True)
+
+
+def test_missing_library_fails_loudly(tmp_path):
+    with pytest.raises(ImportError):
+        ou.load_experts(str(tmp_path / "liboptimizer_experts.so"))
+
+
+def test_public_names():
+    for name in ("RouteOrder", "load_experts", "route_balance", "route_combine", "route_dispatch", "route_order", "route_topk",
+                 "Int4", "int4_dequantize", "int4_grouped_matmul", "int4_matmul", "int4_quantize"):
+        assert name in ou.__all__ and hasattr(ou, name)
+
+
+TOPK = dict(dt=0, x=A, t=10, e=64, rs=64, scores=0, bias=None, groups=8, top=2, best2=1, renorm=1, scale=1.0, mask=None, k=4, w=B,
+            ids=C)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dt=3), EINVAL), (dict(x=None), EINVAL), (dict(t=-1), EINVAL), (dict(t=(1 << 26) + 1), EINVAL), (dict(e=0), EINVAL),
+    (dict(e=1025, rs=1025), EINVAL), (dict(rs=63), EINVAL), (dict(scores=2), EINVAL), (dict(groups=0), EINVAL),
+    (dict(groups=7), EINVAL), (dict(groups=65), EINVAL), (dict(top=0), EINVAL), (dict(top=9), EINVAL), (dict(best2=2), EINVAL),
+    (dict(scale=float("nan")), EINVAL), (dict(scale=float("inf")), EINVAL), (dict(k=0), EINVAL), (dict(k=65), EINVAL),
+    (dict(k=17), EINVAL), (dict(e=8, rs=8, groups=1, top=1, k=9), EINVAL), (dict(w=None), EINVAL), (dict(ids=None), EINVAL),
+    (dict(x=A + 2), EALIGN), (dict(w=B + 1), EALIGN), (dict(ids=C + 2), EALIGN), (dict(bias=D + 1), EALIGN), (dict(w=A), EOVERLAP),
+    (dict(ids=B + 156), EOVERLAP), (dict(bias=C, ids=C), EOVERLAP), (dict(mask=B), EOVERLAP), (dict(rs=(1 << 31) + 1), EINVAL),
+])
+def test_topk_refusals(L, kw, code):
+    assert L.ou_route_topk(*(TOPK | kw).values(), None) == code
+    assert L.ou_experts_last_error()
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dt=9), EINVAL), (dict(k=65), EINVAL), (dict(e=2000), EINVAL), (dict(ids=None), EINVAL), (dict(dw=None), EINVAL),
+    (dict(dx=None), EINVAL), (dict(dx=A), EOVERLAP), (dict(dx=C + 4), EOVERLAP), (dict(dx=D + 1), EALIGN), (dict(rs=3), EINVAL),
+    (dict(scores=-1), EINVAL),
+])
+def test_topk_backward_refusals(L, kw, code):
+    a = dict(dt=2, x=A, t=10, e=64, rs=64, scores=1, renorm=0, scale=1.0, ids=B, dw=C, k=4, dx=D) | kw
+    assert L.ou_route_topk_backward(*a.values(), None) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(n=-1), EINVAL), (dict(n=(1 << 28) + 1), EINVAL), (dict(e=0), EINVAL), (dict(e=1025), EINVAL), (dict(ids=None), EINVAL),
+    (dict(off=None), EINVAL), (dict(s=None), EINVAL), (dict(p=None), EINVAL), (dict(ids=A + 2), EALIGN), (dict(off=B + 1), EALIGN),
+    (dict(s=A), EOVERLAP), (dict(p=C + 4), EOVERLAP), (dict(off=D), EOVERLAP), (dict(n=20000), EINVAL),
+    (dict(n=20000, ws=E, wb=100), EINVAL), (dict(n=20000, ws=E + 1, wb=1 << 20), EALIGN),
+    (dict(n=20000, ws=D, wb=1 << 20), EOVERLAP),
+])
+def test_order_refusals(L, kw, code):
+    a = dict(ids=A, n=100, e=16, off=B, s=C, p=D, ws=None, wb=0) | kw
+    assert L.ou_route_order(*a.values(), None) == code
+
+
+def test_order_workspace(L):
+    f = L.ou_route_order_workspace_bytes
+    assert f(0, 1) == 0 and f(1, 1024) == 0 and f(-1, 4) == -1 and f(5, 0) == -1 and f(5, 1025) == -1 and f((1 << 28) + 1, 4) == -1
+    # bounded for any number of slots
+    assert 0 < f(1 << 28, 1024) <= 1024 * 1025 * 4
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dt=4), EINVAL), (dict(t=-1), EINVAL), (dict(h=-1), EINVAL), (dict(xs=63), EINVAL), (dict(os=10), EINVAL), (dict(k=0), EINVAL),
+    (dict(k=65), EINVAL), (dict(x=None), EINVAL), (dict(s=None), EINVAL), (dict(p=None), EINVAL), (dict(out=None), EINVAL),
+    (dict(x=A + 1), EALIGN), (dict(out=A), EOVERLAP), (dict(out=B), EOVERLAP), (dict(s=B + 2), EALIGN), (dict(t=1 << 28), EINVAL),
+    (dict(t=1 << 25, h=1 << 22, xs=1 << 22, os=1 << 22), EINVAL),
+])
+def test_dispatch_refusals(L, kw, code):
+    a = dict(dt=1, x=A, t=10, h=64, xs=64, k=2, s=B, p=C, out=D, os=64, z=1) | kw
+    assert L.ou_route_dispatch(*a.values(), None) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dt=4), EINVAL), (dict(ys=63), EINVAL), (dict(os=10), EINVAL), (dict(k=65), EINVAL), (dict(y=None), EINVAL),
+    (dict(p=None), EINVAL), (dict(out=None), EINVAL), (dict(as_=63), EINVAL), (dict(out=E), EOVERLAP), (dict(out=A), EOVERLAP),
+    (dict(w=B + 2), EALIGN), (dict(out=F + 1), EALIGN),
+])
+def test_combine_refusals(L, kw, code):
+    a = dict(dt=1, y=A, t=10, h=64, ys=64, k=2, w=B, p=C, add=E, as_=64, out=F, os=64) | kw
+    assert L.ou_route_combine(*a.values(), None) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dt=4), EINVAL), (dict(gs=63), EINVAL), (dict(ys=63), EINVAL), (dict(dy=None, dw=None), EINVAL), (dict(y=None), EINVAL),
+    (dict(w=None), EINVAL), (dict(s=None), EINVAL), (dict(p=None), EINVAL), (dict(dy=A), EOVERLAP), (dict(dw=C), EOVERLAP),
+    (dict(g=None), EINVAL), (dict(dy=F + 1), EALIGN), (dict(dw=G + 2), EALIGN),
+])
+def test_combine_backward_refusals(L, kw, code):
+    a = dict(dt=1, g=A, t=10, h=64, gs=64, k=2, y=B, ys=64, w=C, s=D, p=E, dy=F, dw=G) | kw
+    assert L.ou_route_combine_backward(*a.values(), None) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(e=0), EINVAL), (dict(bias=None), EINVAL), (dict(off=None), EINVAL), (dict(out=None), EINVAL), (dict(out=A + 4), EOVERLAP),
+    (dict(out=B), EOVERLAP), (dict(rate=float("inf")), EINVAL), (dict(out=C + 2), EALIGN),
+])
+def test_balance_refusals(L, kw, code):
+    a = dict(bias=A, off=B, e=8, rate=0.1, out=C) | kw
+    assert L.ou_route_balance(*a.values(), None) == code
+
+
+PRODUCT = dict(dt=2, x=A, m=3, xs=256, od=2, c=B, sd=2, s=C, z=D, n=40, k=256, group=64, out=E, os=40)
+BAD_PRODUCTS = [
+    (dict(dt=5), EINVAL), (dict(od=-1), EINVAL), (dict(sd=3), EINVAL), (dict(m=-1), EINVAL), (dict(n=-1), EINVAL), (dict(k=-32), EINVAL),
+    (dict(xs=255), EINVAL), (dict(os=39), EINVAL), (dict(group=0), EINVAL), (dict(group=16), EINVAL), (dict(group=48), EINVAL),
+    (dict(group=96), EINVAL), (dict(x=None), EINVAL), (dict(c=None), EINVAL), (dict(s=None), EINVAL), (dict(out=None), EINVAL),
+    (dict(c=B + 8), EALIGN), (dict(s=C + 1), EALIGN), (dict(z=D + 1), EALIGN), (dict(x=A + 1), EALIGN), (dict(out=B), EOVERLAP),
+    (dict(out=C), EOVERLAP), (dict(out=D), EOVERLAP), (dict(out=A), EOVERLAP), (dict(k=1 << 26, xs=1 << 26), EINVAL),
+    (dict(m=1 << 31, n=1 << 31, os=1 << 31), EINVAL),
+]
+
+
+@pytest.mark.parametrize("kw,code", BAD_PRODUCTS)
+def test_product_refusals(L, kw, code):
+    a = PRODUCT | kw
+    assert L.ou_int4_matmul(*a.values(), None) == code
+    tail = (a.pop("out"), a.pop("os"))
+    assert L.ou_int4_grouped_matmul(*a.values(), F, 4, *tail, 1, None) == code
+
+
+@pytest.mark.parametrize("off,experts,code", [(None, 4, EINVAL), (F + 2, 4, EALIGN), (F, -1, EINVAL), (F, 65536, EINVAL), (E, 4, EOVERLAP)])
+def test_grouped_product_refusals(L, off, experts, code):
+    a = dict(PRODUCT)
+    tail = (a.pop("out"), a.pop("os"))
+    assert L.ou_int4_grouped_matmul(*a.values(), off, experts, *tail, 1, None) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dt=3), EINVAL), (dict(rows=-1), EINVAL), (dict(rs=255), EINVAL), (dict(group=33), EINVAL), (dict(sd=7), EINVAL),
+    (dict(c=None), EINVAL), (dict(s=None), EINVAL), (dict(c=A), EOVERLAP), (dict(z=C), EOVERLAP), (dict(c=B + 4), EALIGN),
+])
+def test_quantize_refusals(L, kw, code):
+    a = dict(dt=0, x=A, rows=8, k=256, rs=256, group=128, sd=0, c=B, s=C, z=D) | kw
+    assert L.ou_int4_quantize(*a.values(), None) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dt=3), EINVAL), (dict(n=-1), EINVAL), (dict(os=255), EINVAL), (dict(group=512), EINVAL), (dict(c=None), EINVAL),
+    (dict(s=None), EINVAL), (dict(out=None), EINVAL), (dict(out=B), EOVERLAP), (dict(c=B + 4), EALIGN), (dict(out=E + 2), EALIGN),
+])
+def test_dequantize_refusals(L, kw, code):
+    a = dict(dt=0, c=B, sd=2, s=C, z=D, n=8, k=256, group=128, out=E, os=256) | kw
+    assert L.ou_int4_dequantize(*a.values(), None) == code
+
+
+def test_calls_pass_their_checks(L, no_gpu):
+    assert L.ou_route_topk(*TOPK.values(), None) == EUNSUPPORTED
+    assert L.ou_int4_matmul(*PRODUCT.values(), None) == EUNSUPPORTED
+    assert L.ou_route_balance(A, B, 8, 0.1, A, None) == EUNSUPPORTED
+    assert L.ou_route_combine(1, A, 10, 64, 64, 2, None, C, None, 0, F, 64, None) == EUNSUPPORTED
+    assert L.ou_route_order(A, 0, 4, B, None, None, None, 0, None) == EUNSUPPORTED   # offsets are written all the same
+
+
+def test_nothing_to_do_is_no_error(L):
+    assert L.ou_route_topk(*(TOPK | dict(t=0, x=None, w=None, ids=None)).values(), None) == OK
+    assert L.ou_route_dispatch(1, None, 0, 64, 64, 2, None, None, None, 64, 1, None) == OK
+    assert L.ou_route_dispatch(1, None, 5, 0, 0, 2, None, None, None, 0, 1, None) == OK
+    assert L.ou_route_combine(1, None, 0, 64, 64, 2, None, None, None, 0, None, 64, None) == OK
+    assert L.ou_int4_matmul(*(PRODUCT | dict(m=0)).values(), None) == OK
+    assert L.ou_int4_quantize(0, None, 0, 256, 256, 128, 0, None, None, None, None) == OK
+
+
+# ------------------------------------------------------------------ the binding
+
+def test_binding_refuses():
+    x = torch.zeros((4, 64))
+    ids = torch.zeros((4, 2), dtype=torch.int32)
+    for call in (lambda: ou.route_topk(x, 2), lambda: ou.route_topk(None, 2), lambda: ou.route_order(ids, 4),
+                 lambda: ou.route_order(ids.long(), 4), lambda: ou.route_order(ids.t(), 4), lambda: ou.route_order(ids[0], 4),
+                 lambda: ou.int4_matmul(x, None), lambda: ou.int4_quantize(x), lambda: ou.int4_dequantize(None),
+                 lambda: ou.int4_grouped_matmul(x, None, None)):
+        with pytest.raises(ValueError):
+            call()
+
+
+def test_route_order_checks():
+    off, slots, places = torch.zeros(5).int(), torch.zeros(8).int(), torch.zeros((4, 2)).int()
+    o = ou.RouteOrder(off, slots, places)
+    assert (o.experts, o.tokens, o.choices, o.device.type) == (4, 4, 2, "cpu")
+    for bad in ((off.long(), slots, places), (off, slots.float(), places), (off, slots, places.flatten()), (off[:1], slots, places),
+                (off, slots[:7], places), (off, slots, torch.zeros((2, 4)).int().t()), (None, slots, places)):
+        with pytest.raises(ValueError):
+            ou.RouteOrder(*bad)
+    for call in (lambda: ou.route_dispatch(torch.zeros((4, 8)), o), lambda: ou.route_combine(torch.zeros((8, 8)), torch.zeros((4, 2)), o),
+                 lambda: ou.route_balance(torch.zeros(4), o, 0.1)):
+        with pytest.raises(ValueError):   # not on a HIP device
+            call()
+
+
+def test_int4_checks():
+    codes, scales = torch.zeros((3, 64), dtype=torch.uint8), torch.zeros((3, 4))
+    q = ou.Int4(codes, scales, None, 32)
+    assert q.k == 128 and q.shape == (3, 128) and "group=32" in repr(q)
+    batch = ou.Int4(codes.expand(2, 3, 64).contiguous(), scales.expand(2, 3, 4).contiguous(), torch.zeros((2, 3, 4)), 32)
+    assert batch[1].shape == (3, 128) and batch[1].zeros.shape == (3, 4)
+    for bad in ((codes.int(), scales, None, 32), (codes, scales, None, 64), (codes, scales, None, 48), (codes, scales, None, 16),
+                (codes, scales.double(), None, 32), (codes, scales, scales.half(), 32), (codes, scales, scales[:2], 32),
+                (codes.t(), scales, None, 32), (codes[0], scales, None, 32), (codes, torch.zeros((4, 3)).t(), None, 32)):
+        with pytest.raises(ValueError):
+            ou.Int4(*bad)
+    with pytest.raises(ValueError):
+        q[0]
+
+
+# ------------------------------------------------------------------ the definitions
+
+def test_reference_topk_is_the_formula():
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn((30, 24), generator=g).double().numpy()
+    s = torch.softmax(torch.tensor(x), -1)
+    top = torch.topk(s, 4, dim=-1)
+    w, ids, _, _ = R.topk(x, 4, renormalize=False, scale=3.0)
+    assert np.array_equal(ids, top.indices.numpy())
+    np.testing.assert_allclose(w, 3 * top.values.numpy(), rtol=1e-12)
+    w, ids, _, _ = R.topk(x, 4, scores="sigmoid")
+    v = torch.sigmoid(torch.tensor(x)).topk(4, dim=-1).values
+    np.testing.assert_allclose(w, (v / v.sum(-1, keepdim=True)).numpy(), rtol=1e-12)
+    # two groups of the three best, by hand
+    x = np.log(np.array([[.05, .20, .24, .01, .25, .25]]))
+    assert R.topk(x, 3, groups=3, top_groups=2)[1].tolist() == [[4, 5, 1]]
+    assert R.topk(x, 3, groups=3, top_groups=2, group_score="best")[1].tolist() == [[4, 5, 2]]
+    assert R.topk(x, 2, bias=np.array([.3, 0, 0, 0, 0, 0]))[1].tolist() == [[0, 4]]
+
+
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_reference_gradient_is_autograds(scores, renormalize):
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn((9, 12), generator=g).double().requires_grad_(True)
+    d = torch.randn((9, 3), generator=g).double()
+    w, ids, _, _ = R.topk(x.detach().numpy(), 3, scores=scores, renormalize=renormalize, scale=1.5)
+    s = torch.softmax(x, -1) if scores == "softmax" else torch.sigmoid(x)
+    c = s.gather(1, torch.tensor(ids))
+    ref = 1.5 * (c / c.sum(-1, keepdim=True) if renormalize else c)
+    np.testing.assert_allclose(w, ref.detach().numpy(), rtol=1e-12)
+    ref.backward(d)
+    dx, size = R.topk_backward(x.detach().numpy(), ids, d.numpy(), scores, renormalize, 1.5)
+    np.testing.assert_allclose(dx, x.grad.numpy(), rtol=1e-9, atol=1e-14)
+    assert (size >= np.abs(dx) - 1e-15).all()
+
+
+def test_reference_order_and_weights():
+    offsets, slots, places = R.order(np.array([[2, 0], [-1, 2], [0, 9]]), 3)
+    assert offsets.tolist() == [0, 2, 2, 4] and slots.tolist() == [1, 4, 0, 3, -1, -1]
+    assert places.tolist() == [[2, 0], [-1, 3], [1, -1]]
+    values, codes = R.int4_values(np.array([[0x1F] + [0x88] * 15], np.uint8), torch.tensor([[2.0]]), None, 32)
+    assert codes[0, :2].tolist() == [15, 1] and values[0, :3].tolist() == [14, -14, 0]
