@@ -67,7 +67,8 @@ struct Int4Args {
     void* out;
     const int32_t* offsets;
     int64_t m, n, k, x_stride, out_stride;
-    int32_t group, experts, zero_rest, x_dtype, out_dtype, scale_dtype;
+    int32_t group, experts, zero_rest, out_dtype, scale_dtype;
+    int32_t x_wide;         // 16-byte loads of x are allowed
 };
 
 struct Int4QuantArgs {
@@ -89,7 +90,14 @@ const void* combine_backward_kernel(int dtype, bool wide);
 const void* balance_kernel();
 const void* int4_quantize_kernel(int dtype);
 const void* int4_dequantize_kernel(int dtype);
-const void* int4_matmul_kernel(bool grouped);
+
+// `rows` x `cols` results a block of `waves` waves; scales: groups of columns
+// in 128 (1, 2 or 4); tiles: 16 columns of results a block, or more.
+struct Int4Kernel {
+    const void* fn;
+    int rows, cols, waves;
+};
+Int4Kernel int4_matmul_kernel(int dtype, int scales, bool grouped, int tiles);
 
 constexpr int kTopkWaves = 4;          // tokens of a block
 constexpr int kOrderThreads = 512;

@@ -315,16 +315,16 @@ int check_weights(int64_t n, int64_t k, int32_t group, int scale_dtype)
 double code_bytes(double n, int64_t k) { return n * static_cast<double>(k) / 2; }
 double scale_bytes(double n, int64_t k, int32_t group, int bytes) { return n * static_cast<double>(k / group) * bytes; }
 
-int int4_product(Int4Args& p, void* stream)
+int int4_product(int dtype, Int4Args& p, void* stream)
 {
     const bool grouped = p.offsets || p.experts;
-    if (!valid_dtype(p.x_dtype) || !valid_dtype(p.out_dtype)) return fail(OU_EINVAL, "unknown dtype");
+    if (!valid_dtype(dtype) || !valid_dtype(p.out_dtype)) return fail(OU_EINVAL, "unknown dtype");
     if (int st = check_weights(p.n, p.k, p.group, p.scale_dtype)) return st;
     if (int st = check_axis(p.m, "m")) return st;
     if (int st = check_stride(p.x_stride, p.k, "x_stride")) return st;
     if (int st = check_stride(p.out_stride, p.n, "out_stride")) return st;
     if (p.m == 0 || p.n == 0) return OU_OK;
-    const int ex = elem_bytes(p.x_dtype), eo = elem_bytes(p.out_dtype), es = elem_bytes(p.scale_dtype);
+    const int ex = elem_bytes(dtype), eo = elem_bytes(p.out_dtype), es = elem_bytes(p.scale_dtype);
     const double all = static_cast<double>(p.n) * (grouped ? p.experts : 1);
     const Buffer bufs[] = {{"x", p.x, extent(p.m, p.k, p.x_stride, ex), static_cast<unsigned>(ex), false},
                            {"codes", p.codes, code_bytes(all, p.k), 16, false},
@@ -333,10 +333,13 @@ int int4_product(Int4Args& p, void* stream)
                            {"offsets", p.offsets, grouped ? 4.0 * (p.experts + 1.0) : 0, 4, false},
                            {"out", p.out, extent(p.m, p.n, p.out_stride, eo), static_cast<unsigned>(eo), true}};
     if (int st = check_buffers(bufs, 6)) return st;
-    const int64_t units = grouped ? cut(p.m + 15 * (p.experts + 2), 16) : cut(p.m, 16);
+    const int scales = p.group % 128 == 0 ? 1 : p.group % 64 == 0 ? 2 : 4;
+    const Int4Kernel f = int4_matmul_kernel(dtype, scales, grouped, 1);
+    p.x_wide = wide_rows(p.x, p.x_stride, 0, ex, 16);
+    // by groups: two more, the rows in front of the first and behind the last
+    const int64_t units = grouped ? cut(p.m + (f.rows - 1) * static_cast<int64_t>(p.experts + 2), f.rows) : cut(p.m, f.rows);
     void* args[] = {&p};
-    return launch({int4_matmul_kernel(grouped), units * cut(p.n, kInt4Threads / 64), 1, kInt4Threads, "k_int4_matmul", 0}, args,
-                  stream);
+    return launch({f.fn, units * cut(p.n, f.cols), 1, kWave * f.waves, "k_int4_matmul", 0}, args, stream);
 }
 
 }  // namespace
@@ -396,8 +399,8 @@ OU_EXPORT int ou_int4_matmul(int dtype, const void* x, int64_t m, int64_t x_stri
                              int scale_dtype, const void* scales, const void* zeros, int64_t n, int64_t k, int32_t group,
                              void* out, int64_t out_stride, void* stream)
 {
-    Int4Args p{x, codes, scales, zeros, out, nullptr, m, n, k, x_stride, out_stride, group, 0, 0, dtype, out_dtype, scale_dtype};
-    return int4_product(p, stream);
+    Int4Args p{x, codes, scales, zeros, out, nullptr, m, n, k, x_stride, out_stride, group, 0, 0, out_dtype, scale_dtype, 0};
+    return int4_product(dtype, p, stream);
 }
 
 OU_EXPORT int ou_int4_grouped_matmul(int dtype, const void* x, int64_t m, int64_t x_stride, int out_dtype,
@@ -406,9 +409,9 @@ OU_EXPORT int ou_int4_grouped_matmul(int dtype, const void* x, int64_t m, int64_
                                      int64_t out_stride, int zero_rest, void* stream)
 {
     if (int st = check_groups(offsets, experts, m)) return st;
-    Int4Args p{x, codes, scales, zeros, out, offsets, m, n, k, x_stride, out_stride, group, experts, zero_rest != 0, dtype,
-               out_dtype, scale_dtype};
-    return int4_product(p, stream);
+    Int4Args p{x, codes, scales, zeros, out, offsets, m, n, k, x_stride, out_stride, group, experts, zero_rest != 0, out_dtype,
+               scale_dtype, 0};
+    return int4_product(dtype, p, stream);
 }
 
 }  // extern "C"

@@ -11,13 +11,6 @@
 namespace experts {
 namespace {
 
-__device__ __forceinline__ float wave_sum(float x)
-{
-#pragma unroll
-    for (int s = 32; s; s >>= 1) x += __shfl_xor(x, s);
-    return x;
-}
-
 // `x` as the type holds it, at most its largest finite number.
 __device__ __forceinline__ float rounded(float x, int dtype)
 {
@@ -86,52 +79,280 @@ __global__ __launch_bounds__(kInt4Threads) void k_int4_dequantize(Int4Args p)
         Value<DT>::store(out, i, (static_cast<float>(c >> (4 * i) & 15u) - zero) * scale);
 }
 
-// A wave per row of weights and 16 rows of x.
-template <bool GROUPED>
-__global__ __launch_bounds__(kInt4Threads) void k_int4_matmul(Int4Args p)
+// ---- products --------------------------------------------------------------------
+//
+// out[i][j] = sum over the groups g of scale[j][g] * (sum_k x[i][k] code[j][k]
+// - zero[j][g] * sum_k x[i][k]), both inner sums over the group's columns by
+// the 16x16x32 matrix instruction: codes are whole numbers up to 15, which
+// bfloat16 and binary16 hold exactly, and x goes in as it is (binary32 in three
+// bfloat16 parts that add up to it), so that every product is exact.  The sum
+// of x is a product with ones.  Weights are the instruction's second operand:
+// lane l holds columns of row l mod 16, and its four results are of that row,
+// so that a lane needs one scale a group.
+
+using bf16x8 = __bf16 __attribute__((ext_vector_type(8)));
+using f16x8 = _Float16 __attribute__((ext_vector_type(8)));
+using f16x2 = _Float16 __attribute__((ext_vector_type(2)));
+using f32x4 = float __attribute__((ext_vector_type(4)));
+
+constexpr int kChunk = 128;   // columns of a step: 16 bytes of codes a lane
+
+// Eight codes (low four bits first) as values of the matrix instruction's type.
+template <int DT>
+__device__ __forceinline__ u32x4 code_values(uint32_t c)
 {
-    constexpr int kRows = 16, W = kInt4Threads / 64;
-    const int lane = static_cast<int>(threadIdx.x) & 63, wave = static_cast<int>(threadIdx.x) >> 6;
-    const uint32_t n_tiles = static_cast<uint32_t>((p.n + W - 1) / W);
-    const uint32_t unit = blockIdx.x / n_tiles;
-    const int64_t n = static_cast<int64_t>(blockIdx.x - unit * n_tiles) * W + wave;
-    int64_t row0 = static_cast<int64_t>(unit) * kRows, rows = p.m - row0, matrix = 0;
-    if constexpr (GROUPED) {
-        const groups::Place at = groups::Groups(p.offsets, p.experts, p.m, kRows).locate(unit);
-        row0 = at.row;
-        rows = at.rows;
-        matrix = at.group;
-        if (rows <= 0) return;
-    }
-    if (n >= p.n) return;
-    if (rows > kRows) rows = kRows;
-    if (GROUPED && matrix < 0) {
-        if (p.zero_rest && lane < rows) store_value(p.out, (row0 + lane) * p.out_stride + n, 0.0f, p.out_dtype);
-        return;
-    }
-    const int64_t row = matrix * p.n + n, groups = p.k / p.group;
-    const uint32_t* codes = reinterpret_cast<const uint32_t*>(p.codes) + row * (p.k / 8);
-    float acc[kRows] = {};
-    for (int64_t o = lane; o < p.k / 8; o += 64) {
-        const uint32_t c = codes[o];
-        const int64_t g = row * groups + o * 8 / p.group;
-        const float scale = load_value(p.scales, g, p.scale_dtype);
-        const float zero = p.zeros ? load_value(p.zeros, g, p.scale_dtype) : 8.0f;
+    u32x4 r;
+    if constexpr (DT == kF16) {
+        // 1024 + code by its bits, two values at a time: codes 0, 4, 1, 5, ..
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            if (r >= rows) break;
-            float part = 0.0f;
-            for (int i = 0; i < 8; ++i) {
-                const float v = load_value(p.x, (row0 + r) * p.x_stride + o * 8 + i, p.x_dtype);
-                part = __builtin_fmaf(v, static_cast<float>(c >> (4 * i) & 15u) - zero, part);
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t b = (c >> (4 * i) & 0x000f000fu) | 0x64006400u;
+            const f16x2 v = __builtin_bit_cast(f16x2, b) - f16x2{1024, 1024};
+            r[i] = __builtin_bit_cast(uint32_t, v);
+        }
+    } else {
+        const uint32_t lo = c & 0x0f0f0f0fu, hi = c >> 4 & 0x0f0f0f0fu;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = static_cast<float>(lo >> (8 * i) & 0xffu), b = static_cast<float>(hi >> (8 * i) & 0xffu);
+            r[i] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, a), 0x07060302u);
+        }
+    }
+    return r;
+}
+
+// x's eight neighbouring values as operands: one, or three parts of binary32.
+template <int DT>
+struct Rows8 {
+    static constexpr int kParts = DT == kF32 ? 3 : 1;
+    static constexpr int kWords = DT == kF32 ? 8 : 4;
+    u32x4 w[kWords / 4];
+
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < kWords / 4; ++i) w[i] = u32x4{0, 0, 0, 0};
+    }
+    __device__ __forceinline__ void load(const typename Value<DT>::Elem* p, bool wide)
+    {
+        if (wide) {
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i) w[i] = reinterpret_cast<const u32x4*>(p)[i];
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            if constexpr (DT == kF32)
+                w[i / 4][i % 4] = __builtin_bit_cast(uint32_t, p[i]);
+            else
+                w[0][i] = static_cast<uint32_t>(p[2 * i]) | static_cast<uint32_t>(p[2 * i + 1]) << 16;
+        }
+    }
+    __device__ __forceinline__ void operands(u32x4* out) const
+    {
+        if constexpr (DT == kBF16) {
+            out[0] = w[0];
+        } else if constexpr (DT == kF16) {   // in the order of code_values()
+            out[0] = u32x4{__builtin_amdgcn_perm(w[0][2], w[0][0], 0x05040100u), __builtin_amdgcn_perm(w[0][2], w[0][0], 0x07060302u),
+                           __builtin_amdgcn_perm(w[0][3], w[0][1], 0x05040100u), __builtin_amdgcn_perm(w[0][3], w[0][1], 0x07060302u)};
+        } else {
+            // eight bits of the fraction each, cut off: the rests are exact
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t a0 = w[i / 2][2 * i % 4], b0 = w[i / 2][2 * i % 4 + 1];
+                const float a1 = __builtin_bit_cast(float, a0) - __builtin_bit_cast(float, a0 & 0xffff0000u);
+                const float b1 = __builtin_bit_cast(float, b0) - __builtin_bit_cast(float, b0 & 0xffff0000u);
+                const uint32_t am = __builtin_bit_cast(uint32_t, a1), bm = __builtin_bit_cast(uint32_t, b1);
+                const float a2 = a1 - __builtin_bit_cast(float, am & 0xffff0000u);
+                const float b2 = b1 - __builtin_bit_cast(float, bm & 0xffff0000u);
+                out[0][i] = __builtin_amdgcn_perm(b0, a0, 0x07060302u);
+                out[1][i] = __builtin_amdgcn_perm(bm, am, 0x07060302u);
+                out[2][i] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, b2), __builtin_bit_cast(uint32_t, a2), 0x07060302u);
             }
-            acc[r] = __builtin_fmaf(part, scale, acc[r]);
+        }
+    }
+};
+
+template <int DT>
+__device__ __forceinline__ f32x4 multiply(u32x4 a, u32x4 b, f32x4 c)
+{
+    if constexpr (DT == kF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b)
+{
+    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+
+// 16 NT rows of weights and 16 MT rows of x a block, the steps of 128 columns
+// dealt to its W waves in runs; U steps of a wave are in flight.  Lane group g
+// (of 16 lanes) loads columns 32 g .. of a step, one request of 64 bytes a row.
+// An instruction's 32 columns have to be of one group of columns: where a step
+// has S = 2 or 4 of them, lane groups exchange registers first (halves, then
+// quarters), and take x from where that leads.
+template <int DT, int S, int NT, int MT, int W, int U, bool GROUPED>
+__global__ __launch_bounds__(kWave * W) void k_int4_matmul(Int4Args p)
+{
+    constexpr int P = Rows8<DT>::kParts;
+    using Elem = typename Value<DT>::Elem;
+    __shared__ f32x4 sums[W][NT * MT][kWave];
+    const int t = static_cast<int>(threadIdx.x), lane = t & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const uint32_t n_tiles = static_cast<uint32_t>((p.n + 16 * NT - 1) / (16 * NT));
+    const uint32_t unit = blockIdx.x / n_tiles, ntile = blockIdx.x - unit * n_tiles;
+    int64_t row0 = static_cast<int64_t>(unit) * (16 * MT), mrows = p.m - row0, matrix = 0;
+    if constexpr (GROUPED) {
+        const groups::Place at = groups::Groups(p.offsets, p.experts, p.m, 16 * MT).locate(unit);
+        row0 = at.row;
+        mrows = at.rows;
+        matrix = at.group;
+        if (mrows <= 0) return;
+        if (matrix < 0 && !p.zero_rest) return;
+    }
+    const int rows = mrows < 16 * MT ? static_cast<int>(mrows) : 16 * MT;
+    const int64_t n0 = static_cast<int64_t>(ntile) * (16 * NT), columns = p.k / p.group;
+    const int chunks = GROUPED && matrix < 0 ? 0 : static_cast<int>((p.k + kChunk - 1) / kChunk);
+    const int run = (chunks + W - 1) / W, first = wave * run, last = first + run < chunks ? first + run : chunks;
+    const uint8_t* codes[NT];
+    int64_t scale_row[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        int64_t n = n0 + 16 * j + r;
+        n = (n < p.n ? n : p.n - 1) + (GROUPED && matrix > 0 ? matrix * p.n : 0);   // rows behind the edge read the last one
+        codes[j] = p.codes + n * (p.k / 2) + g * 16;
+        scale_row[j] = n * columns;
+    }
+    const Elem* x[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int xr = 16 * i + r < rows ? 16 * i + r : rows - 1;
+        x[i] = static_cast<const Elem*>(p.x) + (row0 + xr) * p.x_stride;
+    }
+    // the column of a step that register i of a lane holds, from where the exchanges bring it
+    auto column = [&](int i) {
+        return S == 1 ? g * 32 + i * 8 : S == 2 ? (i >> 1) * 64 + (g & 1) * 32 + (g >> 1) * 16 + (i & 1) * 8 : i * 32 + g * 8;
+    };
+    struct Step {
+        u32x4 c[NT];
+        Rows8<DT> x[MT][4];
+        float scale[NT][S], zero[NT][S];
+    } step[U];
+    auto load = [&](Step& s, int at) {
+        const int64_t k0 = static_cast<int64_t>(at) * kChunk;
+        const bool whole = k0 + kChunk <= p.k;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            s.c[j] = whole || k0 + g * 32 < p.k ? __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(codes[j] + k0 / 2))
+                                                : u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int64_t k = k0 + column(q);
+                if (whole || k < p.k)
+                    s.x[i][q].load(x[i] + k, p.x_wide);
+                else
+                    s.x[i][q].zero();
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < S; ++q) {
+            const int64_t k = k0 + q * (kChunk / S), last_k = p.k - 1;
+            const int64_t at_group = static_cast<int64_t>(static_cast<uint32_t>(k < last_k ? k : last_k) / static_cast<uint32_t>(p.group));
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                s.scale[j][q] = load_value(p.scales, scale_row[j] + at_group, p.scale_dtype);
+                s.zero[j][q] = p.zeros ? load_value(p.zeros, scale_row[j] + at_group, p.scale_dtype) : 8.0f;
+            }
+        }
+    };
+    f32x4 y[NT][MT] = {};
+    constexpr uint32_t kOne = DT == kF16 ? 0x3c003c00u : 0x3f803f80u;
+    const u32x4 ones{kOne, kOne, kOne, kOne};
+    auto compute = [&](Step& s) {
+        f32x4 sum[S][NT][MT] = {}, plain[S][MT] = {};
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            uint32_t c0 = s.c[j][0], c1 = s.c[j][1], c2 = s.c[j][2], c3 = s.c[j][3];
+            if constexpr (S >= 2) {
+                swap32(c0, c2);
+                swap32(c1, c3);
+            }
+            if constexpr (S == 4) {
+                swap16(c0, c1);
+                swap16(c2, c3);
+            }
+            s.c[j] = u32x4{c0, c1, c2, c3};
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            constexpr int kPer = 4 / S;
+            u32x4 a[MT][P];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                s.x[i][q].operands(a[i]);
+#pragma unroll
+                for (int h = 0; h < P; ++h) plain[q / kPer][i] = multiply<DT>(a[i][h], ones, plain[q / kPer][i]);
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const u32x4 b = code_values<DT>(s.c[j][q]);
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int h = 0; h < P; ++h) sum[q / kPer][j][i] = multiply<DT>(a[i][h], b, sum[q / kPer][j][i]);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < S; ++q)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        y[j][i][e] = __builtin_fmaf(s.scale[j][q], __builtin_fmaf(-s.zero[j][q], plain[q][i][e], sum[q][j][i][e]),
+                                                    y[j][i][e]);
+    };
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (first + u < last) load(step[u], first + u);
+    for (int at = first; at < last; at += U) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (at + u >= last) break;
+            compute(step[u]);
+            if (at + u + U < last) load(step[u], at + u + U);
         }
     }
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-        const float sum = wave_sum(acc[r]);
-        if (lane == 0 && r < rows) store_value(p.out, (row0 + r) * p.out_stride + n, sum, p.out_dtype);
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) sums[wave][j * MT + i][lane] = y[j][i];
+    __syncthreads();
+    for (int u = t; u < NT * MT * kWave; u += kWave * W) {
+        const int l = u & 63, tile = u >> 6, j = tile / MT, i = tile % MT;
+        f32x4 v = sums[0][tile][l];
+#pragma unroll
+        for (int w = 1; w < W; ++w) v += sums[w][tile][l];
+        const int64_t n = n0 + 16 * j + (l & 15);
+        if (n >= p.n) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int row = 16 * i + (l >> 4) * 4 + e;
+            if (row < rows) store_value(p.out, (row0 + row) * p.out_stride + n, v[e], p.out_dtype);
+        }
     }
 }
 
@@ -149,9 +370,36 @@ const void* int4_dequantize_kernel(int dtype)
            : dtype == kF16 ? reinterpret_cast<const void*>(k_int4_dequantize<kF16>)
                            : reinterpret_cast<const void*>(k_int4_dequantize<kBF16>);
 }
-const void* int4_matmul_kernel(bool grouped)
+
+namespace {
+
+template <int DT, int S, bool GROUPED>
+Int4Kernel choose_tile(int tiles)
 {
-    return grouped ? reinterpret_cast<const void*>(k_int4_matmul<true>) : reinterpret_cast<const void*>(k_int4_matmul<false>);
+    constexpr int U = DT == kF32 ? 2 : 4;
+    if (tiles == 1) return {reinterpret_cast<const void*>(k_int4_matmul<DT, S, 1, 1, 8, U, GROUPED>), 16, 16, 8};
+    return {reinterpret_cast<const void*>(k_int4_matmul<DT, S, 4, 1, 4, 2, GROUPED>), 16, 64, 4};
+}
+template <int DT, int S>
+Int4Kernel choose_grouped(bool grouped, int tiles)
+{
+    return grouped ? choose_tile<DT, S, true>(tiles) : choose_tile<DT, S, false>(tiles);
+}
+template <int DT>
+Int4Kernel choose_scales(int scales, bool grouped, int tiles)
+{
+    return scales == 1   ? choose_grouped<DT, 1>(grouped, tiles)
+           : scales == 2 ? choose_grouped<DT, 2>(grouped, tiles)
+                         : choose_grouped<DT, 4>(grouped, tiles);
+}
+
+}  // namespace
+
+Int4Kernel int4_matmul_kernel(int dtype, int scales, bool grouped, int tiles)
+{
+    return dtype == kF32   ? choose_scales<kF32>(scales, grouped, tiles)
+           : dtype == kF16 ? choose_scales<kF16>(scales, grouped, tiles)
+                           : choose_scales<kBF16>(scales, grouped, tiles);
 }
 
 }  // namespace experts
