@@ -22,6 +22,8 @@ struct TopkArgs {
     int32_t experts, k, groups, top_groups;
     int32_t scores, best_two, renormalize;
     float scale;
+    int32_t wide, bias_wide;   // loads of four neighbours are aligned
+    int32_t exact;             // every token's choice in 64 bits
 };
 
 struct TopkBackwardArgs {
@@ -80,7 +82,12 @@ struct Int4QuantArgs {
     int32_t group, scale_dtype;
 };
 
-const void* topk_kernel(int dtype);
+// `tokens` a wave
+struct TopkKernel {
+    const void* fn;
+    int tokens;
+};
+TopkKernel topk_kernel(int dtype, int32_t experts, int32_t k, int32_t groups);
 const void* topk_backward_kernel(int dtype);
 const void* order_count_kernel();
 const void* order_place_kernel();
@@ -99,7 +106,7 @@ struct Int4Kernel {
 };
 Int4Kernel int4_matmul_kernel(int dtype, int scales, bool grouped, int tiles);
 
-constexpr int kTopkWaves = 4;          // tokens of a block
+constexpr int kTopkWaves = 4;          // of a block
 constexpr int kOrderThreads = 512;
 constexpr int kOrderChunk = 4096;      // slots of a block, at least
 constexpr int kOrderBlocks = 256;      // at most

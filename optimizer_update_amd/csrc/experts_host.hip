@@ -97,9 +97,13 @@ OU_EXPORT int ou_route_topk(int dtype, const void* logits, int64_t tokens, int32
                            {"ids", ids, dense(tokens, k, 4), 4, true}};
     if (int st = check_buffers(bufs, 5)) return st;
     TopkArgs p{logits, bias, mask, weights, ids, tokens, row_stride, experts, k, groups, top_groups, scores,
-               group_score == OU_ROUTE_BEST_TWO, renormalize != 0, scale};
+               group_score == OU_ROUTE_BEST_TWO, renormalize != 0, scale, 0, 0, 0};
+    p.wide = experts % 4 == 0 && wide_rows(logits, row_stride, 0, eb, 4 * eb);
+    p.bias_wide = experts % 4 == 0 && wide_rows(bias, 0, 0, 4, 16);
+    const TopkKernel f = topk_kernel(dtype, experts, k, groups);
+    p.exact = f.tokens == 1 && k == kWave;   // no lane for the first one left out
     void* args[] = {&p};
-    return launch({topk_kernel(dtype), cut(tokens, kTopkWaves), 1, kTopkWaves * kWave, "k_topk", 0}, args, stream);
+    return launch({f.fn, cut(tokens, kTopkWaves * f.tokens), 1, kTopkWaves * kWave, "k_topk", 0}, args, stream);
 }
 
 OU_EXPORT int ou_route_topk_backward(int dtype, const void* logits, int64_t tokens, int32_t experts, int64_t row_stride,

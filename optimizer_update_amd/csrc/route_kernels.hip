@@ -52,72 +52,84 @@ __device__ __forceinline__ double key_value(uint64_t k)
     return __builtin_bit_cast(double, k >> 63 ? k ^ (uint64_t(1) << 63) : ~k);
 }
 
-// One wave per token, expert v * 64 + lane in register v: scores in 64 bits,
-// one round of the wave for each choice.
-template <int DT>
-__global__ __launch_bounds__(kTopkWaves * kWave) void k_topk(TopkArgs p)
+// Reductions over L neighbouring lanes (16, 32 or 64), the same answer in all
+// of them.
+template <int L, class F>
+__device__ __forceinline__ uint32_t reduce_lanes(uint32_t x, F f)
 {
-    constexpr int V = kMaxExperts / kWave;
-    __shared__ uint64_t lds[kTopkWaves][kMaxExperts];
-    const int lane = static_cast<int>(threadIdx.x) & 63, wave = static_cast<int>(threadIdx.x) >> 6;
-    const int64_t token = static_cast<int64_t>(blockIdx.x) * kTopkWaves + wave;
-    if (token >= p.tokens) return;   // waves do not meet
-    const int k = p.k;
-    float* const weights = p.weights + token * k;
-    int32_t* const ids = p.ids + token * k;
-    if (p.mask && !p.mask[token]) {
-        if (lane < k) {
-            weights[lane] = 0.0f;
-            ids[lane] = -1;
-        }
-        return;
+    x = f(x, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0xB1, 0xf, 0xf, true)));    // lane ^ 1
+    x = f(x, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x4E, 0xf, 0xf, true)));    // lane ^ 2
+    x = f(x, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x141, 0xf, 0xf, true)));   // mirrored 8
+    x = f(x, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), 0x140, 0xf, 0xf, true)));   // mirrored 16
+    if constexpr (L >= 32) {
+        const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+        const uint32_t u = r[0], v = r[1];
+        x = f(u, v);
     }
-    const typename Value<DT>::Elem* x = static_cast<const typename Value<DT>::Elem*>(p.logits) + token * p.row_stride;
+    if constexpr (L >= 64) {
+        const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+        const uint32_t u = r[0], v = r[1];
+        x = f(u, v);
+    }
+    return x;
+}
+template <int L>
+__device__ __forceinline__ uint32_t lanes_min_u32(uint32_t x)
+{
+    return reduce_lanes<L>(x, [](uint32_t u, uint32_t v) { return u < v ? u : v; });
+}
+template <int L>
+__device__ __forceinline__ float lanes_max(float x)
+{
+    return __builtin_bit_cast(float, reduce_lanes<L>(__builtin_bit_cast(uint32_t, x), [](uint32_t u, uint32_t v) {
+        return __builtin_bit_cast(uint32_t, fmaxf(__builtin_bit_cast(float, u), __builtin_bit_cast(float, v)));
+    }));
+}
+template <int L>
+__device__ __forceinline__ float lanes_sum(float x)
+{
+    return __builtin_bit_cast(float, reduce_lanes<L>(__builtin_bit_cast(uint32_t, x), [](uint32_t u, uint32_t v) {
+        return __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, u) + __builtin_bit_cast(float, v));
+    }));
+}
+
+// The choice of one token in 64 bits, by a whole wave: the choice `lane` in
+// each lane (-1: none).  keys: LDS for one of every expert.
+template <int DT>
+__device__ int choose_exact(const TopkArgs& p, int64_t token, int lane, uint64_t* keys)
+{
     constexpr float kInf = __builtin_inff();
-    const bool by_logit = !p.bias && (p.groups == 1 || !p.best_two);   // scores rise with the logits
-    float v[V], top = -kInf;
-    bool bad = false;                                                  // a NaN or +inf among the logits
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = i * kWave + lane;
-        v[i] = e < p.experts ? Value<DT>::load(x, e) : -kInf;
-        top = fmaxf(top, v[i]);
-        bad |= !(v[i] < kInf);
-    }
-    top = wave_max(top);
-    bad = __any(bad);
+    const typename Value<DT>::Elem* x = static_cast<const typename Value<DT>::Elem*>(p.logits) + token * p.row_stride;
+    const bool by_logit = !p.bias && (p.groups == 1 || !p.best_two);
+    float top = -kInf;
     double total = 0;
     if (p.scores == kSoftmax && !by_logit) {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (v[i] != -kInf) total += exp(static_cast<double>(v[i]) - top);
+        for (int e = lane; e < p.experts; e += kWave) top = fmaxf(top, Value<DT>::load(x, e));
+        top = wave_max(top);
+        for (int e = lane; e < p.experts; e += kWave) {
+            const float v = Value<DT>::load(x, e);
+            if (v != -kInf) total += exp(static_cast<double>(v) - top);
+        }
 #pragma unroll
         for (int s = 32; s; s >>= 1) total += __shfl_xor(total, s);
     }
-    uint64_t key[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = i * kWave + lane;
-        key[i] = 0;
-        if (e >= p.experts || v[i] == -kInf) continue;
-        double c = v[i];
+    for (int e = lane; e < p.experts; e += kWave) {
+        const float v = Value<DT>::load(x, e);
+        double c = v;
         if (!by_logit) {
             c = p.scores == kSoftmax ? exp(c - top) / total : 1 / (1 + exp(-c));
             if (p.bias) c += p.bias[e];
         }
-        key[i] = order_key(c);
+        keys[e] = v == -kInf ? 0 : order_key(c);
     }
+    wave_sync();
     if (p.groups > 1) {
         const int size = p.experts / p.groups;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (i * kWave + lane < p.experts) lds[wave][i * kWave + lane] = key[i];
-        wave_sync();
         uint64_t mine = 0;
         if (lane < p.groups) {
             uint64_t a = 0, b = 0;
             for (int i = 0; i < size; ++i) {
-                const uint64_t c = lds[wave][lane * size + i];
+                const uint64_t c = keys[lane * size + i];
                 if (c > a) {
                     b = a;
                     a = c;
@@ -132,22 +144,19 @@ __global__ __launch_bounds__(kTopkWaves * kWave) void k_topk(TopkArgs p)
             const uint64_t other = __shfl(mine, g);
             ahead += other > mine || (other == mine && g < lane);
         }
-        const uint64_t stays = __ballot(lane < p.groups && ahead < p.top_groups);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = i * kWave + lane;
-            if (e < p.experts && !(stays >> (e / size) & 1)) key[i] = 0;
-        }
+        if (lane < p.groups && ahead >= p.top_groups)
+            for (int i = 0; i < size; ++i) keys[lane * size + i] = 0;
+        wave_sync();
     }
-    int chosen = -1;   // of choice `lane`
-    for (int j = 0; j < k; ++j) {
-        uint64_t best = key[0];
-        int at = lane;
-#pragma unroll
-        for (int i = 1; i < V; ++i) {
-            if (key[i] > best) {
-                best = key[i];
-                at = i * kWave + lane;
+    int chosen = -1;
+    for (int j = 0; j < p.k; ++j) {
+        uint64_t best = 0;
+        int at = 0;
+        for (int e = lane; e < p.experts; e += kWave) {
+            const uint64_t c = keys[e];
+            if (c > best) {
+                best = c;
+                at = e;
             }
         }
 #pragma unroll
@@ -161,34 +170,244 @@ __global__ __launch_bounds__(kTopkWaves * kWave) void k_topk(TopkArgs p)
         }
         if (!best) break;
         if (lane == j) chosen = at;
+        if ((at & (kWave - 1)) == lane) keys[at] = 0;
+        wave_sync();
+    }
+    wave_sync();   // the next token's keys come behind this one's last reads
+    return chosen;
+}
+
+// L lanes a token, V of its experts a lane.  A choice of k out of E by k rounds
+// over values and indexes in 64 bits costs 500 us for 32768 x 256; so the
+// rounds go over 32-bit keys: the choice's value in 2^22 steps between the
+// row's extremes (or the 64 below the largest), then the expert from above, so
+// that all keys differ and the next one below `m` is m - 1 less the minimum of
+// m - 1 - key in unsigned arithmetic: one subtraction and half a three-way
+// minimum a key, nothing to mark as taken.  What this finds is right wherever
+// neighbours in the order differ by more than the binary32 scores and the steps
+// may be off (`margin`), or are of the same logit and bias; other tokens go
+// through choose_exact().  The scores' errors: 2^-22 for the logistic function
+// (an argument to half a step of itself, exponential and reciprocal to one
+// step), 45 half steps of the largest for the softmax (arguments, a sum of 16 +
+// 6 terms, the quotient), half a step of c for the bias.  Both are taken twice.
+template <int DT, int L, int V>
+__global__ __launch_bounds__(kTopkWaves * kWave) void k_topk(TopkArgs p)
+{
+    using Elem = typename Value<DT>::Elem;
+    constexpr int kTokens = kWave / L, kExperts = L * V;
+    constexpr int kIndex = kExperts <= 64 ? 6 : kExperts <= 128 ? 7 : kExperts <= 256 ? 8 : kExperts <= 512 ? 9 : 10;
+    constexpr float kSteps = 4194300.0f, kInf = __builtin_inff();
+    constexpr int kWords = kTokens * kExperts / 2 > kExperts ? kTokens * kExperts / 2 : kExperts;
+    __shared__ uint64_t lds[kTopkWaves][kWords];
+    const int lane = static_cast<int>(threadIdx.x) & 63, wave = static_cast<int>(threadIdx.x) >> 6;
+    const int sub = lane & (L - 1), row = lane / L;
+    const int64_t token0 = (static_cast<int64_t>(blockIdx.x) * kTopkWaves + wave) * kTokens, token = token0 + row;
+    if (token0 >= p.tokens) return;   // waves do not meet
+    const int k = p.k;
+    const bool inside = token < p.tokens, live = inside && !(p.mask && !p.mask[token]);
+    const Elem* const x = static_cast<const Elem*>(p.logits) + (inside ? token : p.tokens - 1) * p.row_stride;
+    const bool by_logit = !p.bias && (p.groups == 1 || !p.best_two);   // scores rise with the logits
+    auto expert = [&](int v) { return (v >> 2) * (4 * L) + sub * 4 + (v & 3); };
+
+    float v[V], c[V];
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+        const int e = expert(i);
+        if (p.wide) {
+            if (e < p.experts) {
+                Value<DT>::load4(x + e, &v[i]);
+            } else {
+#pragma unroll
+                for (int h = 0; h < 4; ++h) v[i + h] = -kInf;
+            }
+        } else {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) v[i + h] = e + h < p.experts ? Value<DT>::load(x, e + h) : -kInf;
+        }
+    }
+    float top = -kInf, sum = 1.0f, worst = 0.0f;   // worst: a NaN if any is NaN or +inf
+    if (p.scores == kSoftmax) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            top = fmaxf(top, v[i]);
+            worst += v[i] == -kInf ? 0.0f : v[i] - v[i];
+        }
+        top = lanes_max<L>(top);
+        worst = lanes_sum<L>(worst);
+    }
+    float error = 0.0f;
+    if (by_logit) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) c[i] = v[i];
+    } else if (p.scores == kSigmoid) {
+        constexpr float kLog2e = 1.44269504f;
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (i * kWave + lane == at) key[i] = 0;
+            c[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * v[i]));
+        error = 0x1p-21f;
+    } else {
+        constexpr float kLog2e = 1.44269504f;
+        float all = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            c[i] = v[i] == -kInf ? 0.0f : __builtin_amdgcn_exp2f(kLog2e * (v[i] - top));
+            all += c[i];
+        }
+        const float r = __builtin_amdgcn_rcpf(lanes_sum<L>(all));
+#pragma unroll
+        for (int i = 0; i < V; ++i) c[i] *= r;
+        error = r * (90.0f * 0x1p-24f);
+    }
+    if (p.bias) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            const int e = expert(i);
+            float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (p.bias_wide) {
+                if (e < p.experts) Value<kF32>::load4(p.bias + e, b);
+            } else {
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+                    if (e + h < p.experts) b[h] = p.bias[e + h];
+            }
+#pragma unroll
+            for (int h = 0; h < 4; ++h) c[i + h] += b[h];
+        }
+    }
+    float hi = -kInf, lo = kInf, odd = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const bool has = v[i] != -kInf;
+        hi = fmaxf(hi, has ? c[i] : -kInf);
+        lo = fminf(lo, has ? c[i] : kInf);
+        odd += has ? c[i] - c[i] : 0.0f;
+    }
+    hi = lanes_max<L>(hi);
+    lo = -lanes_max<L>(-lo);
+    odd = lanes_sum<L>(odd);
+    if (!by_logit) error += fmaxf(fabsf(hi), fabsf(lo)) * 0x1p-23f;
+    bool sure = odd == odd || hi == -kInf;   // of nothing: sure
+    const bool none = hi == -kInf;
+    const float base = none ? 0.0f : fmaxf(lo, hi - 64.0f), range = fmaxf(none ? 1.0f : hi - base, 0x1p-100f);
+    const float scale = kSteps / range;
+    const float off = 3.0f + 2.0f * error * scale;
+    const uint32_t margin = off < kSteps ? static_cast<uint32_t>(off) + 1 : 1u << 22;
+
+    uint64_t stays = ~uint64_t(0);
+    uint32_t part = 0;   // an expert's part is expert * part >> 20
+    if (p.groups > 1) {
+        const int size = p.experts / p.groups;
+        part = ((1u << 20) + size - 1) / size;
+        float* const room = reinterpret_cast<float*>(lds[wave]) + row * kExperts;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (expert(i) < p.experts) room[expert(i)] = v[i] == -kInf ? -kInf : c[i];
+        wave_sync();
+        float a = -kInf, b = -kInf;
+        if (sub < p.groups) {
+            for (int i = 0; i < size; ++i) {
+                const float u = room[sub * size + i];
+                b = fmaxf(b, fminf(a, u));
+                a = fmaxf(a, u);
+            }
+        }
+        const float mine = p.best_two && b != -kInf ? a + b : a;
+        int ahead = 0;
+        for (int g = 0; g < p.groups; ++g) {
+            const float other = __shfl(mine, g, L);
+            ahead += other > mine || (other == mine && g < sub);
+        }
+        const bool stay = sub < p.groups && ahead < p.top_groups;
+        stays = __ballot(stay) >> (row * L);
+        // the smallest that stays and the largest that does not
+        const float least = -lanes_max<L>(stay ? -mine : -kInf);
+        const float most = lanes_max<L>(sub < p.groups && !stay ? mine : -kInf);
+        // two sums of two, and their own rounding
+        if (most != -kInf && !(least - most > 4.0f * error + (fabsf(least) + fabsf(most)) * 0x1p-23f)) sure = false;
+        wave_sync();
+    }
+    uint32_t key[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const uint32_t e = static_cast<uint32_t>(expert(i));
+        const uint32_t q = 1u + static_cast<uint32_t>(fmaxf(c[i] - base, 0.0f) * scale);
+        bool has = v[i] != -kInf;
+        if (p.groups > 1) has = has && (stays >> (e * part >> 20 & 63u) & 1);
+        key[i] = has ? q << kIndex | (kExperts - 1 - e) : 0;
+    }
+    uint32_t m = ~0u, own = 0;   // own: the key of choice `sub`; choice k is the first one left out
+    for (int j = 0; j <= k; ++j) {
+        const uint32_t t = m - 1;
+        uint32_t r = ~0u;
+#pragma unroll
+        for (int i = 0; i < V; ++i) r = min(r, t - key[i]);
+        r = lanes_min_u32<L>(r);
+        m = m && r <= t ? t - r : 0;
+        if (sub == j) own = m;
+    }
+    int chosen = own >> kIndex && sub < k ? static_cast<int>(kExperts - 1 - (own & (kExperts - 1))) : -1;
+    const int at = own >> kIndex ? static_cast<int>(kExperts - 1 - (own & (kExperts - 1))) : 0;
+    float cx = Value<DT>::load(x, at);
+    const float cb = p.bias ? p.bias[at] : 0.0f;
+    {
+        const uint32_t next = __shfl_down(own, 1, L);
+        const float nx = __shfl_down(cx, 1, L), nb = __shfl_down(cb, 1, L);
+        const bool near = sub < k && (next >> kIndex) && (own >> kIndex) - (next >> kIndex) < margin;
+        const bool same = cx == nx && cb == nb;
+        const uint64_t rows = L == 64 ? ~uint64_t(0) : ((uint64_t(1) << (L & 63)) - 1) << (row * L);
+        if (__ballot(near && !same) & rows) sure = false;
+        // the last choice and the first one left out are alike: so must be all that are as near
+        if (__any(near && same && sub == k - 1)) {
+            const uint32_t edge = __shfl(own, k - 1, L) >> kIndex;
+            const float ex = __shfl(cx, k - 1, L), eb = __shfl(cb, k - 1, L);
+            bool other = false;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const uint32_t q = key[i] >> kIndex;
+                if (q && q <= edge && q + margin > edge)
+                    other |= !(v[i] == ex && (!p.bias || p.bias[expert(i)] == eb));
+            }
+            if (__ballot(other) & rows) sure = false;
+        }
+    }
+    if (p.exact) sure = false;
+    // rows that are not sure, one at a time
+    uint64_t open = __ballot(live && !sure);
+    while (open) {
+        const int which = __builtin_ctzll(open) / L;
+        const int found = choose_exact<DT>(p, token0 + which, lane, lds[wave]);
+        const int to = __shfl(found, sub);
+        if (row == which) {
+            chosen = sub < k ? to : -1;
+            if (chosen >= 0) cx = Value<DT>::load(x, chosen);
+        }
+        open &= L == 64 ? 0 : ~(((uint64_t(1) << (L & 63)) - 1) << (which * L));
     }
     // Weights.  Logistic scores are exp(min(x, 0)) / (1 + exp(-|x|)), so that a
     // common factor can leave both sides of a division of them.
-    const bool has = lane < k && chosen >= 0;
-    const float c = has ? Value<DT>::load(x, chosen) : -kInf;
+    const bool has = live && chosen >= 0;
+    if (!has) cx = -kInf;
     float s;
     if (p.scores == kSigmoid) {
-        const float low = fminf(c, 0.0f), most = p.renormalize ? wave_max(has ? low : -kInf) : 0.0f;
-        s = has ? expf(low - most) / (1.0f + expf(-fabsf(c))) : 0.0f;
-        if (has && c != c) s = c;
+        const float low = fminf(cx, 0.0f), most = lanes_max<L>(has ? low : -kInf);
+        s = has ? expf(p.renormalize ? low - most : low) / (1.0f + expf(-fabsf(cx))) : 0.0f;
+        if (has && cx != cx) s = cx;
     } else {
-        const float most = p.renormalize ? wave_max(c) : top;
-        s = has ? expf(c - most) : 0.0f;
+        const float most = lanes_max<L>(cx);
+        s = has ? expf(cx - (p.renormalize ? most : top)) : 0.0f;
         if (!p.renormalize) {
-            float sum = 0;
+            float all = 0.0f;
 #pragma unroll
-            for (int i = 0; i < V; ++i) sum += v[i] == -kInf ? 0.0f : expf(v[i] - top);
-            s /= wave_sum(sum);
+            for (int i = 0; i < V; ++i) all += v[i] == -kInf ? 0.0f : expf(v[i] - top);
+            s /= lanes_sum<L>(all);
         }
-        if (bad && has) s = __builtin_nanf("");
+        if (worst != worst && has) s = __builtin_nanf("");
     }
-    if (p.renormalize) s /= wave_sum(s);
-    if (lane < k) {
-        weights[lane] = has ? p.scale * s : 0.0f;
-        ids[lane] = chosen;
+    const float whole = lanes_sum<L>(s);
+    if (p.renormalize) s /= whole;
+    if (inside && sub < k) {
+        p.weights[token * k + sub] = has ? p.scale * s : 0.0f;
+        p.ids[token * k + sub] = has ? chosen : -1;
     }
 }
 
@@ -474,11 +693,28 @@ __global__ __launch_bounds__(kRowThreads) void k_combine_backward(RowsArgs p)
 
 }  // namespace
 
-const void* topk_kernel(int dtype)
+namespace {
+
+template <int DT>
+TopkKernel choose_topk(int32_t experts, int32_t k, int32_t groups)
 {
-    return dtype == kF32   ? reinterpret_cast<const void*>(k_topk<kF32>)
-           : dtype == kF16 ? reinterpret_cast<const void*>(k_topk<kF16>)
-                           : reinterpret_cast<const void*>(k_topk<kBF16>);
+    // choices and the first one left out are a lane each, and parts
+    if (experts <= 256 && k < 16 && groups <= 16) {
+        if (experts <= 64) return {reinterpret_cast<const void*>(k_topk<DT, 16, 4>), 4};
+        if (experts <= 128) return {reinterpret_cast<const void*>(k_topk<DT, 16, 8>), 4};
+        return {reinterpret_cast<const void*>(k_topk<DT, 16, 16>), 4};
+    }
+    if (experts <= 512 && k < 32 && groups <= 32) return {reinterpret_cast<const void*>(k_topk<DT, 32, 16>), 2};
+    return {reinterpret_cast<const void*>(k_topk<DT, 64, 16>), 1};
+}
+
+}  // namespace
+
+TopkKernel topk_kernel(int dtype, int32_t experts, int32_t k, int32_t groups)
+{
+    return dtype == kF32   ? choose_topk<kF32>(experts, k, groups)
+           : dtype == kF16 ? choose_topk<kF16>(experts, k, groups)
+                           : choose_topk<kBF16>(experts, k, groups);
 }
 const void* topk_backward_kernel(int dtype)
 {

@@ -10,6 +10,7 @@
 namespace experts {
 namespace {
 
+using u32x2 = uint32_t __attribute__((ext_vector_type(2)));
 using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
 
 template <int DT>
@@ -23,6 +24,16 @@ struct Value<kF32> {
     static __device__ __forceinline__ float from_float(float x) { return x; }
     static __device__ __forceinline__ float load(const float* p, int64_t i) { return p[i]; }
     static __device__ __forceinline__ void store(float* p, int64_t i, float x) { p[i] = x; }
+    // four neighbours, aligned
+    static __device__ __forceinline__ void load4(const float* p, float* out)
+    {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t d = w[j];   // a bit cast of the vector's element itself takes its first one
+            out[j] = __builtin_bit_cast(float, d);
+        }
+    }
 };
 template <>
 struct Value<kF16> {
@@ -32,6 +43,16 @@ struct Value<kF16> {
     static __device__ __forceinline__ uint16_t from_float(float x) { return __builtin_bit_cast(uint16_t, static_cast<_Float16>(x)); }
     static __device__ __forceinline__ float load(const uint16_t* p, int64_t i) { return to_float(p[i]); }
     static __device__ __forceinline__ void store(uint16_t* p, int64_t i, float x) { p[i] = from_float(x); }
+    static __device__ __forceinline__ void load4(const uint16_t* p, float* out)
+    {
+        const u32x2 w = *reinterpret_cast<const u32x2*>(p);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t d = w[j];
+            out[2 * j] = to_float(static_cast<uint16_t>(d));
+            out[2 * j + 1] = to_float(static_cast<uint16_t>(d >> 16));
+        }
+    }
 };
 template <>
 struct Value<kBF16> {
@@ -41,6 +62,16 @@ struct Value<kBF16> {
     static __device__ __forceinline__ uint16_t from_float(float x) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x)); }
     static __device__ __forceinline__ float load(const uint16_t* p, int64_t i) { return to_float(p[i]); }
     static __device__ __forceinline__ void store(uint16_t* p, int64_t i, float x) { p[i] = from_float(x); }
+    static __device__ __forceinline__ void load4(const uint16_t* p, float* out)
+    {
+        const u32x2 w = *reinterpret_cast<const u32x2*>(p);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t d = w[j];
+            out[2 * j] = to_float(static_cast<uint16_t>(d));
+            out[2 * j + 1] = to_float(static_cast<uint16_t>(d >> 16));
+        }
+    }
 };
 
 // The value at `i` of an array whose type is known at run time.
