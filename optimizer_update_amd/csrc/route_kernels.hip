@@ -52,6 +52,21 @@ __device__ __forceinline__ double key_value(uint64_t k)
     return __builtin_bit_cast(double, k >> 63 ? k ^ (uint64_t(1) << 63) : ~k);
 }
 
+// Larger and smaller of three without the quieting of signalling NaNs that
+// fmaxf() adds for every operand (rows with a NaN are seen by their sum).
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c)
+{
+    float r;
+    asm("v_min3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+
 // Reductions over L neighbouring lanes (16, 32 or 64), the same answer in all
 // of them.
 template <int L, class F>
@@ -185,7 +200,9 @@ __device__ int choose_exact(const TopkArgs& p, int64_t token, int lane, uint64_t
 // m - 1 - key in unsigned arithmetic: one subtraction and half a three-way
 // minimum a key, nothing to mark as taken.  What this finds is right wherever
 // neighbours in the order differ by more than the binary32 scores and the steps
-// may be off (`margin`), or are of the same logit and bias; other tokens go
+// may be off (`margin`), or are of the same logit and bias.  Otherwise the first
+// L in this order are put in the order of 64 bits, a lane each; and where that
+// does not settle it (many as near, a NaN, two parts alike) the token goes
 // through choose_exact().  The scores' errors: 2^-22 for the logistic function
 // (an argument to half a step of itself, exponential and reciprocal to one
 // step), 45 half steps of the largest for the softmax (arguments, a sum of 16 +
@@ -196,8 +213,8 @@ __global__ __launch_bounds__(kTopkWaves * kWave) void k_topk(TopkArgs p)
     using Elem = typename Value<DT>::Elem;
     constexpr int kTokens = kWave / L, kExperts = L * V;
     constexpr int kIndex = kExperts <= 64 ? 6 : kExperts <= 128 ? 7 : kExperts <= 256 ? 8 : kExperts <= 512 ? 9 : 10;
-    constexpr float kSteps = 4194300.0f, kInf = __builtin_inff();
-    constexpr int kWords = kTokens * kExperts / 2 > kExperts ? kTokens * kExperts / 2 : kExperts;
+    constexpr float kSteps = 4194000.0f, kInf = __builtin_inff();
+    constexpr int kRoom = kTokens * (kExperts + L) / 2, kWords = kRoom > kExperts ? kRoom : kExperts;
     __shared__ uint64_t lds[kTopkWaves][kWords];
     const int lane = static_cast<int>(threadIdx.x) & 63, wave = static_cast<int>(threadIdx.x) >> 6;
     const int sub = lane & (L - 1), row = lane / L;
@@ -238,7 +255,7 @@ __global__ __launch_bounds__(kTopkWaves * kWave) void k_topk(TopkArgs p)
     float error = 0.0f;
     if (by_logit) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) c[i] = v[i];
+        for (int i = 0; i < V; ++i) c[i] = v[i] == -kInf ? 0.0f : v[i];
     } else if (p.scores == kSigmoid) {
         constexpr float kLog2e = 1.44269504f;
 #pragma unroll
@@ -276,39 +293,45 @@ __global__ __launch_bounds__(kTopkWaves * kWave) void k_topk(TopkArgs p)
     }
     float hi = -kInf, lo = kInf, odd = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const bool has = v[i] != -kInf;
-        hi = fmaxf(hi, has ? c[i] : -kInf);
-        lo = fminf(lo, has ? c[i] : kInf);
-        odd += has ? c[i] - c[i] : 0.0f;
+    for (int i = 0; i < V; i += 2) {
+        hi = max3(hi, v[i] == -kInf ? -kInf : c[i], v[i + 1] == -kInf ? -kInf : c[i + 1]);
+        lo = min3(lo, v[i] == -kInf ? kInf : c[i], v[i + 1] == -kInf ? kInf : c[i + 1]);
+        odd += c[i] + c[i + 1];
     }
     hi = lanes_max<L>(hi);
     lo = -lanes_max<L>(-lo);
     odd = lanes_sum<L>(odd);
     if (!by_logit) error += fmaxf(fabsf(hi), fabsf(lo)) * 0x1p-23f;
-    bool sure = odd == odd || hi == -kInf;   // of nothing: sure
     const bool none = hi == -kInf;
-    const float base = none ? 0.0f : fmaxf(lo, hi - 64.0f), range = fmaxf(none ? 1.0f : hi - base, 0x1p-100f);
-    const float scale = kSteps / range;
+    bool sure = fabsf(odd) < kInf || none;
+    // steps of c from `base` on; a base that is far from 0 is rounded for all
+    // alike, by 64 steps at most
+    const float base = none ? 0.0f : fmaxf(lo, hi - 64.0f);
+    const float range = fmaxf(fmaxf(none ? 1.0f : hi - base, 0x1p-100f), fabsf(base) * 0x1p-8f);
+    const float scale = kSteps / range, shift = 65.0f - base * scale;
     const float off = 3.0f + 2.0f * error * scale;
     const uint32_t margin = off < kSteps ? static_cast<uint32_t>(off) + 1 : 1u << 22;
 
     uint64_t stays = ~uint64_t(0);
     uint32_t part = 0;   // an expert's part is expert * part >> 20
     if (p.groups > 1) {
+        // a lane reads a part: parts one word apart from where they would be, rows L words, for other banks
         const int size = p.experts / p.groups;
         part = ((1u << 20) + size - 1) / size;
-        float* const room = reinterpret_cast<float*>(lds[wave]) + row * kExperts;
+        float* const room = reinterpret_cast<float*>(lds[wave]) + row * (kExperts + L);
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (expert(i) < p.experts) room[expert(i)] = v[i] == -kInf ? -kInf : c[i];
+        for (int i = 0; i < V; ++i) {
+            const uint32_t e = static_cast<uint32_t>(expert(i));
+            if (e < static_cast<uint32_t>(p.experts)) room[e + (e * part >> 20)] = v[i] == -kInf ? -kInf : c[i];
+        }
         wave_sync();
         float a = -kInf, b = -kInf;
         if (sub < p.groups) {
+            const float* const mine = room + sub * (size + 1);
             for (int i = 0; i < size; ++i) {
-                const float u = room[sub * size + i];
-                b = fmaxf(b, fminf(a, u));
-                a = fmaxf(a, u);
+                const float u = mine[i];
+                b = __builtin_amdgcn_fmed3f(a, b, u);   // of a >= b and u the one between
+                a = max3(a, u, u);
             }
         }
         const float mine = p.best_two && b != -kInf ? a + b : a;
@@ -327,13 +350,14 @@ __global__ __launch_bounds__(kTopkWaves * kWave) void k_topk(TopkArgs p)
         wave_sync();
     }
     uint32_t key[V];
+    const uint32_t from = kExperts - 1 - sub * 4;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
+        const uint32_t q = max(static_cast<uint32_t>(__builtin_amdgcn_fmed3f(__builtin_fmaf(c[i], scale, shift), 1.0f, 4194303.0f)), 1u);
         const uint32_t e = static_cast<uint32_t>(expert(i));
-        const uint32_t q = 1u + static_cast<uint32_t>(fmaxf(c[i] - base, 0.0f) * scale);
-        bool has = v[i] != -kInf;
-        if (p.groups > 1) has = has && (stays >> (e * part >> 20 & 63u) & 1);
-        key[i] = has ? q << kIndex | (kExperts - 1 - e) : 0;
+        // without parts `part` is 0 and every bit of `stays` set
+        const bool in_part = L < 64 ? static_cast<uint32_t>(stays) >> (e * part >> 20 & 31u) & 1u : stays >> (e * part >> 20 & 63u) & 1u;
+        key[i] = (v[i] != -kInf) & in_part ? (q << kIndex) + (from - (i >> 2) * (4 * L) - (i & 3)) : 0;
     }
     uint32_t m = ~0u, own = 0;   // own: the key of choice `sub`; choice k is the first one left out
     for (int j = 0; j <= k; ++j) {
@@ -345,17 +369,19 @@ __global__ __launch_bounds__(kTopkWaves * kWave) void k_topk(TopkArgs p)
         m = m && r <= t ? t - r : 0;
         if (sub == j) own = m;
     }
-    int chosen = own >> kIndex && sub < k ? static_cast<int>(kExperts - 1 - (own & (kExperts - 1))) : -1;
-    const int at = own >> kIndex ? static_cast<int>(kExperts - 1 - (own & (kExperts - 1))) : 0;
-    float cx = Value<DT>::load(x, at);
-    const float cb = p.bias ? p.bias[at] : 0.0f;
+    // Candidates: choice `sub` and, behind the choices, those left out.
+    auto index_of = [](uint32_t key) { return static_cast<int>(kExperts - 1 - (key & (kExperts - 1))); };
+    const uint64_t rows = L == 64 ? ~uint64_t(0) : ((uint64_t(1) << (L & 63)) - 1) << (row * L);
+    bool has = own >> kIndex;
+    int chosen = has && sub < k ? index_of(own) : -1;
+    float cx = Value<DT>::load(x, has ? index_of(own) : 0);
     {
+        const float cb = p.bias ? p.bias[has ? index_of(own) : 0] : 0.0f;
         const uint32_t next = __shfl_down(own, 1, L);
         const float nx = __shfl_down(cx, 1, L), nb = __shfl_down(cb, 1, L);
         const bool near = sub < k && (next >> kIndex) && (own >> kIndex) - (next >> kIndex) < margin;
         const bool same = cx == nx && cb == nb;
-        const uint64_t rows = L == 64 ? ~uint64_t(0) : ((uint64_t(1) << (L & 63)) - 1) << (row * L);
-        if (__ballot(near && !same) & rows) sure = false;
+        bool open = __ballot(near && !same) & rows;
         // the last choice and the first one left out are alike: so must be all that are as near
         if (__any(near && same && sub == k - 1)) {
             const uint32_t edge = __shfl(own, k - 1, L) >> kIndex;
@@ -367,7 +393,54 @@ __global__ __launch_bounds__(kTopkWaves * kWave) void k_topk(TopkArgs p)
                 if (q && q <= edge && q + margin > edge)
                     other |= !(v[i] == ex && (!p.bias || p.bias[expert(i)] == eb));
             }
-            if (__ballot(other) & rows) sure = false;
+            open |= static_cast<bool>(__ballot(other) & rows);
+        }
+        open = open && live && sure && !p.exact;
+        if (__any(open)) {
+            // the first L candidates in the order of 64 bits; those behind them are
+            // out if the last one is far enough from the last choice
+            for (int j = k + 1; j < L; ++j) {
+                const uint32_t t = m - 1;
+                uint32_t r = ~0u;
+#pragma unroll
+                for (int i = 0; i < V; ++i) r = min(r, t - key[i]);
+                r = lanes_min_u32<L>(r);
+                m = m && r <= t ? t - r : 0;
+                if (sub == j) own = m;
+            }
+            has = own >> kIndex;
+            const int at = has ? index_of(own) : 0;
+            const float ox = Value<DT>::load(x, at);
+            double value = ox;
+            if (!by_logit && p.scores == kSigmoid) value = 1 / (1 + exp(-value));
+            if (!by_logit && p.scores == kSoftmax) {
+                double all = 0;
+                for (int e = sub; e < p.experts; e += L) {
+                    const float u = Value<DT>::load(x, e);
+                    all += u == -kInf ? 0 : exp(static_cast<double>(u) - top);
+                }
+#pragma unroll
+                for (int w = 1; w < L; w <<= 1) all += __shfl_xor(all, w);
+                value = exp(value - top) / all;
+            }
+            if (p.bias) value += p.bias[at];
+            int ahead = 0;
+            for (int j = 0; j < L; ++j) {
+                const double other = __shfl(value, j, L);
+                const int oat = __shfl(at, j, L), ohas = __shfl(static_cast<int>(has), j, L);
+                ahead += ohas && (other > value || (other == value && oat < at));
+            }
+            if (!has) ahead = sub;   // behind all others
+            // to the lane of its rank
+            const int to = (row * L + ahead) * 4;
+            const int moved = __builtin_amdgcn_ds_permute(to, at);
+            const uint32_t there = static_cast<uint32_t>(__builtin_amdgcn_ds_permute(to, static_cast<int>(own)));
+            const uint32_t edge = __shfl(there, k - 1, L) >> kIndex, last = __shfl(own, L - 1, L) >> kIndex;
+            if (open) {
+                chosen = there >> kIndex && sub < k ? moved : -1;
+                cx = Value<DT>::load(x, moved);
+                if (last && (edge < last || edge - last < margin)) sure = false;
+            }
         }
     }
     if (p.exact) sure = false;
@@ -385,7 +458,7 @@ __global__ __launch_bounds__(kTopkWaves * kWave) void k_topk(TopkArgs p)
     }
     // Weights.  Logistic scores are exp(min(x, 0)) / (1 + exp(-|x|)), so that a
     // common factor can leave both sides of a division of them.
-    const bool has = live && chosen >= 0;
+    has = live && chosen >= 0;
     if (!has) cx = -kInf;
     float s;
     if (p.scores == kSigmoid) {
