@@ -81,7 +81,7 @@ int ou_route_topk_backward(int dtype, const void* logits, int64_t tokens, int32_
  *   slot_of_row (slots): the slot of each row, -1 from offsets[experts] on
  *   row_of_slot (slots): the row of each slot, -1 for those of no expert
  * `workspace`: device memory of ou_route_order_workspace_bytes(slots,
- * experts) bytes, 4-byte aligned (NULL if that is 0); calls that may overlap
+ * experts) bytes, 16-byte aligned (NULL if that is 0); calls that may overlap
  * in time need workspaces of their own. */
 int64_t ou_route_order_workspace_bytes(int64_t slots, int32_t experts);
 int ou_route_order(const int32_t* ids, int64_t slots, int32_t experts, int32_t* offsets,

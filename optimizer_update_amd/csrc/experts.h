@@ -34,6 +34,7 @@ struct TopkBackwardArgs {
     int64_t tokens, row_stride;
     int32_t experts, k, scores, renormalize;
     float scale;
+    int32_t wide, dense_wide;   // four neighbours of a row of logits, of dlogits are aligned
 };
 
 struct OrderArgs {
@@ -41,9 +42,10 @@ struct OrderArgs {
     int32_t* offsets;
     int32_t* slot_of_row;
     int32_t* row_of_slot;
-    int32_t* counts;        // [blocks][experts + 1]
+    int32_t* counts;        // [blocks][bins]
     int64_t slots, chunk;   // slots of a block
     int32_t experts, blocks;
+    int32_t bins;           // experts and those of none, rounded up to 4
 };
 
 // Rows of x or y: `units` pieces of a vector load (wide) or single elements.
@@ -88,7 +90,7 @@ struct TopkKernel {
     int tokens;
 };
 TopkKernel topk_kernel(int dtype, int32_t experts, int32_t k, int32_t groups);
-const void* topk_backward_kernel(int dtype);
+TopkKernel topk_backward_kernel(int dtype, int32_t experts, int32_t k);
 const void* order_count_kernel();
 const void* order_place_kernel();
 const void* dispatch_kernel(int bytes, bool wide);
@@ -108,7 +110,8 @@ Int4Kernel int4_matmul_kernel(int dtype, int scales, bool grouped, int tiles);
 
 constexpr int kTopkWaves = 4;          // of a block
 constexpr int kOrderThreads = 512;
-constexpr int kOrderChunk = 4096;      // slots of a block, at least
+constexpr int kOrderAlone = 4096;      // slots that one block takes by itself
+constexpr int kOrderChunk = 2048;      // slots of a block, at least
 constexpr int kOrderBlocks = 256;      // at most
 constexpr int kRowThreads = 256;
 constexpr int kInt4Threads = 256;

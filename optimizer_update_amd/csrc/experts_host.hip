@@ -118,10 +118,12 @@ OU_EXPORT int ou_route_topk_backward(int dtype, const void* logits, int64_t toke
                            {"dweights", dweights, dense(tokens, k, 4), 4, false},
                            {"dlogits", dlogits, dense(tokens, experts, eb), static_cast<unsigned>(eb), true}};
     if (int st = check_buffers(bufs, 4)) return st;
-    TopkBackwardArgs p{logits, ids, dweights, dlogits, tokens, row_stride, experts, k, scores, renormalize != 0, scale};
+    TopkBackwardArgs p{logits, ids, dweights, dlogits, tokens, row_stride, experts, k, scores, renormalize != 0, scale, 0, 0};
+    p.wide = experts % 4 == 0 && wide_rows(logits, row_stride, 0, eb, 4 * eb);
+    p.dense_wide = experts % 4 == 0 && wide_rows(dlogits, experts, 0, eb, 4 * eb);
+    const TopkKernel f = topk_backward_kernel(dtype, experts, k);
     void* args[] = {&p};
-    return launch({topk_backward_kernel(dtype), cut(tokens, kTopkWaves), 1, kTopkWaves * kWave, "k_topk_backward", 0}, args,
-                  stream);
+    return launch({f.fn, cut(tokens, kTopkWaves * f.tokens), 1, kTopkWaves * kWave, "k_topk_backward", 0}, args, stream);
 }
 
 }  // extern "C"
@@ -131,11 +133,14 @@ namespace {
 // Slots of a block of the order, and blocks.
 int64_t order_chunk(int64_t slots)
 {
+    if (slots <= kOrderAlone) return kOrderAlone;
     const int64_t most = cut(cut(slots, kOrderBlocks), kOrderThreads) * kOrderThreads;
     return most > kOrderChunk ? most : kOrderChunk;
 }
 
 int64_t order_blocks(int64_t slots) { return slots ? cut(slots, order_chunk(slots)) : 1; }
+
+int32_t order_bins(int32_t experts) { return (experts + 4) / 4 * 4; }
 
 }  // namespace
 
@@ -145,7 +150,7 @@ OU_EXPORT int64_t ou_route_order_workspace_bytes(int64_t slots, int32_t experts)
 {
     if (slots < 0 || slots > OU_ROUTE_MAX_SLOTS || check_experts(experts)) return -1;
     const int64_t blocks = order_blocks(slots);
-    return blocks > 1 ? blocks * (experts + 1) * 4 : 0;
+    return blocks > 1 ? blocks * order_bins(experts) * 4 : 0;
 }
 
 OU_EXPORT int ou_route_order(const int32_t* ids, int64_t slots, int32_t experts, int32_t* offsets, int32_t* slot_of_row,
@@ -161,10 +166,10 @@ OU_EXPORT int ou_route_order(const int32_t* ids, int64_t slots, int32_t experts,
                            {"offsets", offsets, 4.0 * (experts + 1.0), 4, true},
                            {"slot_of_row", slot_of_row, sb, 4, true},
                            {"row_of_slot", row_of_slot, sb, 4, true},
-                           {"workspace", workspace, static_cast<double>(need), 4, true}};
+                           {"workspace", workspace, static_cast<double>(need), 16, true}};
     if (int st = check_buffers(bufs, 5)) return st;
     OrderArgs p{ids, offsets, slot_of_row, row_of_slot, static_cast<int32_t*>(workspace), slots, order_chunk(slots), experts,
-                static_cast<int32_t>(order_blocks(slots))};
+                static_cast<int32_t>(order_blocks(slots)), order_bins(experts)};
     void* args[] = {&p};
     if (p.blocks > 1)
         if (int st = launch({order_count_kernel(), p.blocks, 1, kOrderThreads, "k_order_count", 0}, args, stream)) return st;

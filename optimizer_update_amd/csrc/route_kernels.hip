@@ -14,6 +14,8 @@ namespace {
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxChoices = 64;
 
+using i32x4 = int32_t __attribute__((ext_vector_type(4)));
+
 // What lanes of a wave wrote to LDS is seen by the others behind this.
 __device__ __forceinline__ void wave_sync()
 {
@@ -242,7 +244,13 @@ __global__ __launch_bounds__(kTopkWaves * kWave) void k_topk(TopkArgs p)
             for (int h = 0; h < 4; ++h) v[i + h] = e + h < p.experts ? Value<DT>::load(x, e + h) : -kInf;
         }
     }
-    float top = -kInf, sum = 1.0f, worst = 0.0f;   // worst: a NaN if any is NaN or +inf
+    // Whether every register of the wave holds an expert: absent ones cost two
+    // instructions at each step of what follows.
+    float lowest = kInf;
+#pragma unroll
+    for (int i = 0; i < V; i += 2) lowest = min3(lowest, v[i], v[i + 1]);
+    const bool full = !__any(lowest == -kInf);
+    float top = -kInf, worst = 0.0f;   // worst: a NaN if any is NaN or +inf
     if (p.scores == kSoftmax) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -292,11 +300,20 @@ __global__ __launch_bounds__(kTopkWaves * kWave) void k_topk(TopkArgs p)
         }
     }
     float hi = -kInf, lo = kInf, odd = 0.0f;
+    if (full) {
 #pragma unroll
-    for (int i = 0; i < V; i += 2) {
-        hi = max3(hi, v[i] == -kInf ? -kInf : c[i], v[i + 1] == -kInf ? -kInf : c[i + 1]);
-        lo = min3(lo, v[i] == -kInf ? kInf : c[i], v[i + 1] == -kInf ? kInf : c[i + 1]);
-        odd += c[i] + c[i + 1];
+        for (int i = 0; i < V; i += 2) {
+            hi = max3(hi, c[i], c[i + 1]);
+            lo = min3(lo, c[i], c[i + 1]);
+            odd += c[i] + c[i + 1];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+            hi = max3(hi, v[i] == -kInf ? -kInf : c[i], v[i + 1] == -kInf ? -kInf : c[i + 1]);
+            lo = min3(lo, v[i] == -kInf ? kInf : c[i], v[i + 1] == -kInf ? kInf : c[i + 1]);
+            odd += c[i] + c[i + 1];
+        }
     }
     hi = lanes_max<L>(hi);
     lo = -lanes_max<L>(-lo);
@@ -312,39 +329,49 @@ __global__ __launch_bounds__(kTopkWaves * kWave) void k_topk(TopkArgs p)
     const float off = 3.0f + 2.0f * error * scale;
     const uint32_t margin = off < kSteps ? static_cast<uint32_t>(off) + 1 : 1u << 22;
 
-    uint64_t stays = ~uint64_t(0);
-    uint32_t part = 0;   // an expert's part is expert * part >> 20
+    uint64_t stays = 0;
+    uint32_t part = 0;     // an expert's part is expert * part >> 20
+    int helpers = 0;       // 2^helpers lanes look at a part
     if (p.groups > 1) {
-        // a lane reads a part: parts one word apart from where they would be, rows L words, for other banks
+        // parts one word apart from where they would be, rows L words, for other banks
         const int size = p.experts / p.groups;
         part = ((1u << 20) + size - 1) / size;
+        while ((p.groups << helpers) <= L / 2) ++helpers;
+        const int team = 1 << helpers;
         float* const room = reinterpret_cast<float*>(lds[wave]) + row * (kExperts + L);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const uint32_t e = static_cast<uint32_t>(expert(i));
-            if (e < static_cast<uint32_t>(p.experts)) room[e + (e * part >> 20)] = v[i] == -kInf ? -kInf : c[i];
+            if (full || e < static_cast<uint32_t>(p.experts)) room[e + (e * part >> 20)] = v[i] == -kInf ? -kInf : c[i];
         }
         wave_sync();
-        float a = -kInf, b = -kInf;
-        if (sub < p.groups) {
-            const float* const mine = room + sub * (size + 1);
-            for (int i = 0; i < size; ++i) {
+        float a = -kInf, b = -kInf;   // the two largest
+        const int g0 = sub >> helpers;
+        if (g0 < p.groups) {
+            const float* const mine = room + g0 * (size + 1);
+#pragma unroll 4
+            for (int i = sub & (team - 1); i < size; i += team) {
                 const float u = mine[i];
                 b = __builtin_amdgcn_fmed3f(a, b, u);   // of a >= b and u the one between
                 a = max3(a, u, u);
             }
         }
+        for (int w = 1; w < team; w <<= 1) {
+            const float oa = __shfl_xor(a, w), ob = __shfl_xor(b, w);
+            b = max3(__builtin_amdgcn_fmed3f(a, b, oa), ob, ob);
+            a = max3(a, oa, oa);
+        }
         const float mine = p.best_two && b != -kInf ? a + b : a;
         int ahead = 0;
         for (int g = 0; g < p.groups; ++g) {
-            const float other = __shfl(mine, g, L);
-            ahead += other > mine || (other == mine && g < sub);
+            const float other = __shfl(mine, g << helpers, L);
+            ahead += other > mine || (other == mine && g < g0);
         }
-        const bool stay = sub < p.groups && ahead < p.top_groups;
+        const bool stay = g0 < p.groups && ahead < p.top_groups;
         stays = __ballot(stay) >> (row * L);
         // the smallest that stays and the largest that does not
         const float least = -lanes_max<L>(stay ? -mine : -kInf);
-        const float most = lanes_max<L>(sub < p.groups && !stay ? mine : -kInf);
+        const float most = lanes_max<L>(g0 < p.groups && !stay ? mine : -kInf);
         // two sums of two, and their own rounding
         if (most != -kInf && !(least - most > 4.0f * error + (fabsf(least) + fabsf(most)) * 0x1p-23f)) sure = false;
         wave_sync();
@@ -353,11 +380,31 @@ __global__ __launch_bounds__(kTopkWaves * kWave) void k_topk(TopkArgs p)
     const uint32_t from = kExperts - 1 - sub * 4;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const uint32_t q = max(static_cast<uint32_t>(__builtin_amdgcn_fmed3f(__builtin_fmaf(c[i], scale, shift), 1.0f, 4194303.0f)), 1u);
-        const uint32_t e = static_cast<uint32_t>(expert(i));
-        // without parts `part` is 0 and every bit of `stays` set
-        const bool in_part = L < 64 ? static_cast<uint32_t>(stays) >> (e * part >> 20 & 31u) & 1u : stays >> (e * part >> 20 & 63u) & 1u;
-        key[i] = (v[i] != -kInf) & in_part ? (q << kIndex) + (from - (i >> 2) * (4 * L) - (i & 3)) : 0;
+        const uint32_t q = static_cast<uint32_t>(fmaxf(__builtin_fmaf(c[i], scale, shift), 1.0f));
+        key[i] = (q << kIndex) + from - ((i >> 2) * (4 * L) + (i & 3));
+    }
+    if (!full) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = v[i] == -kInf ? 0 : key[i];
+    }
+    if (p.groups > 1) {
+        // all ones where bit `at` is set
+        auto in_part = [&](uint32_t e) {
+            const uint32_t at = (e * part >> 20) << helpers;
+            return static_cast<uint32_t>(static_cast<int32_t>((L < 64 ? static_cast<uint32_t>(stays) >> (at & 31u)
+                                                                      : static_cast<uint32_t>(stays >> (at & 63u))) << 31) >> 31);
+        };
+        if (p.experts / p.groups % 4 == 0) {   // four neighbours are of one part
+#pragma unroll
+            for (int i = 0; i < V; i += 4) {
+                const uint32_t bits = in_part(static_cast<uint32_t>(expert(i)));
+#pragma unroll
+                for (int h = 0; h < 4; ++h) key[i + h] &= bits;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) key[i] &= in_part(static_cast<uint32_t>(expert(i)));
+        }
     }
     uint32_t m = ~0u, own = 0;   // own: the key of choice `sub`; choice k is the first one left out
     for (int j = 0; j <= k; ++j) {
@@ -484,128 +531,207 @@ __global__ __launch_bounds__(kTopkWaves * kWave) void k_topk(TopkArgs p)
     }
 }
 
-// One wave per token.
-template <int DT>
+// L lanes a token, V of its experts a lane, a choice a lane.  Where only the
+// chosen have a gradient, a token's logits are read at those alone.
+template <int DT, int L, int V>
 __global__ __launch_bounds__(kTopkWaves * kWave) void k_topk_backward(TopkBackwardArgs p)
 {
-    constexpr int V = kMaxExperts / kWave;
-    __shared__ float lds[kTopkWaves][kMaxExperts];
+    using Elem = typename Value<DT>::Elem;
+    constexpr int kTokens = kWave / L, kExperts = L * V;
+    __shared__ __attribute__((aligned(16))) float lds[kTopkWaves][kTokens * kExperts];
     const int lane = static_cast<int>(threadIdx.x) & 63, wave = static_cast<int>(threadIdx.x) >> 6;
-    const int64_t token = static_cast<int64_t>(blockIdx.x) * kTopkWaves + wave;
-    if (token >= p.tokens) return;
+    const int sub = lane & (L - 1), row = lane / L;
+    const int64_t token0 = (static_cast<int64_t>(blockIdx.x) * kTopkWaves + wave) * kTokens;
+    if (token0 >= p.tokens) return;
+    const bool inside = token0 + row < p.tokens;
+    const int64_t token = inside ? token0 + row : p.tokens - 1;
     const int k = p.k;
     constexpr float kInf = __builtin_inff();
-    const typename Value<DT>::Elem* x = static_cast<const typename Value<DT>::Elem*>(p.logits) + token * p.row_stride;
-    typename Value<DT>::Elem* dx = static_cast<typename Value<DT>::Elem*>(p.dlogits) + token * p.experts;
-    const int id = lane < k ? p.ids[token * k + lane] : -1;
+    const Elem* const x = static_cast<const Elem*>(p.logits) + token * p.row_stride;
+    Elem* const dx = static_cast<Elem*>(p.dlogits) + token * p.experts;
+    const int id = sub < k ? p.ids[token * k + sub] : -1;
     const bool has = id >= 0 && id < p.experts;
     const float c = has ? Value<DT>::load(x, id) : -kInf;
-    const float g = has ? p.dweights[token * k + lane] : 0.0f;
-    const bool dense = p.scores == kSoftmax && !p.renormalize && __any(has);
+    const float g = has ? p.dweights[token * k + sub] : 0.0f;
+    const bool dense = p.scores == kSoftmax && !p.renormalize;
+    auto expert = [&](int v) { return (v >> 2) * (4 * L) + sub * 4 + (v & 3); };
+    float* const room = lds[wave] + row * kExperts;
+    using f32x4 = float __attribute__((ext_vector_type(4)));
+#pragma unroll
+    for (int i = 0; i < V; i += 4) *reinterpret_cast<f32x4*>(room + expert(i)) = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     float v[V], top = -kInf, sum = 0.0f;
     if (dense) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = i * kWave + lane;
-            v[i] = e < p.experts ? Value<DT>::load(x, e) : -kInf;
-            top = fmaxf(top, v[i]);
-        }
-        top = wave_max(top);
+        for (int i = 0; i < V; i += 4) {
+            const int e = expert(i);
+            if (p.wide && e < p.experts) {
+                Value<DT>::load4(x + e, &v[i]);
+            } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) sum += v[i] == -kInf ? 0.0f : expf(v[i] - top);
-        sum = wave_sum(sum);
+                for (int h = 0; h < 4; ++h) v[i + h] = e + h < p.experts ? Value<DT>::load(x, e + h) : -kInf;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) top = fmaxf(top, v[i]);
+        top = lanes_max<L>(top);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            v[i] = v[i] == -kInf ? 0.0f : expf(v[i] - top);
+            sum += v[i];
+        }
+        sum = lanes_sum<L>(sum);
     }
     float s, d;
     if (p.scores == kSigmoid) {
-        const float low = fminf(c, 0.0f), most = p.renormalize ? wave_max(has ? low : -kInf) : 0.0f;
+        const float low = fminf(c, 0.0f), most = lanes_max<L>(has ? low : -kInf);
         const float t = expf(-fabsf(c));
-        s = has ? expf(low - most) / (1.0f + t) : 0.0f;
+        s = has ? expf(p.renormalize ? low - most : low) / (1.0f + t) : 0.0f;
         const float rest = (c > 0.0f ? t : 1.0f) / (1.0f + t);   // 1 - the score
-        if (p.renormalize) {
-            s /= wave_sum(s);
-            d = p.scale * s * rest * (g - wave_sum(g * s));
-        } else {
-            d = p.scale * s * rest * g;
-        }
-    } else if (p.renormalize) {
-        const float most = wave_max(c);   // by all lanes
-        s = has ? expf(c - most) : 0.0f;
-        s /= wave_sum(s);
-        d = p.scale * s * (g - wave_sum(g * s));
+        const float whole = lanes_sum<L>(s);
+        if (p.renormalize) s /= whole;
+        const float mean = lanes_sum<L>(g * s);
+        d = p.scale * s * rest * (p.renormalize ? g - mean : g);
     } else {
-        s = has ? expf(c - top) / sum : 0.0f;
-        d = wave_sum(g * s);   // of the row
+        const float most = lanes_max<L>(c);   // by all lanes
+        s = has ? expf(c - (dense ? top : most)) : 0.0f;
+        const float whole = lanes_sum<L>(s);
+        s /= dense ? sum : whole;
+        const float mean = lanes_sum<L>(g * s);
+        d = dense ? mean : p.scale * s * (g - mean);   // dense: of the row
     }
-    float* row = lds[wave];
-    for (int e = lane; e < p.experts; e += kWave) row[e] = 0.0f;
+    const bool any = __ballot(has) & (L == 64 ? ~uint64_t(0) : ((uint64_t(1) << (L & 63)) - 1) << (row * L));
     wave_sync();
-    if (has) row[id] = dense ? g : d;
+    if (has) room[id] = dense ? g : d;
     wave_sync();
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = i * kWave + lane;
-        if (e >= p.experts) continue;
-        float r = row[e];
-        if (dense) r = v[i] == -kInf ? 0.0f : p.scale * (expf(v[i] - top) / sum) * (r - d);
-        Value<DT>::store(dx, e, r);
+    for (int i = 0; i < V; i += 4) {
+        const int e = expert(i);
+        if (e >= p.experts || !inside) continue;
+        const f32x4 q = *reinterpret_cast<const f32x4*>(room + e);
+        float r[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            r[h] = q[h];
+            if (dense) r[h] = !any || v[i + h] == 0.0f ? 0.0f : p.scale * (v[i + h] / sum) * (r[h] - d);
+        }
+        if (p.dense_wide) {
+            Value<DT>::store4(dx + e, r);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+                if (e + h < p.experts) Value<DT>::store(dx, e + h, r[h]);
+        }
     }
 }
 
 // ---- the order of rows ----------------------------------------------------------
 
 // Sorting by counting: a block takes a run of slots, its waves parts of it.
-__device__ __forceinline__ int bin_of(const OrderArgs& p, int64_t slot)
+// With more than one block, the first kernel counts every block's slots by
+// expert, and each block of the second adds up the counts itself: 128 blocks of
+// 2048 slots with 257 bins are 17 MB from the L2, in 16-byte pieces of which a
+// thread has eight on their way.  262144 slots, 256 experts: ORDER_TIME.
+__device__ __forceinline__ int bin_of(const OrderArgs& p, int32_t id)
 {
-    const int32_t id = p.ids[slot];
-    return id >= 0 && id < p.experts ? id : p.experts;
+    return static_cast<uint32_t>(id) < static_cast<uint32_t>(p.experts) ? id : p.experts;
 }
 
 __global__ __launch_bounds__(kOrderThreads) void k_order_count(OrderArgs p)
 {
-    __shared__ int32_t count[kMaxExperts + 1];
-    const int t = static_cast<int>(threadIdx.x), bins = p.experts + 1;
-    for (int e = t; e < bins; e += kOrderThreads) count[e] = 0;
+    __shared__ int32_t count[kMaxExperts + 4];
+    const int t = static_cast<int>(threadIdx.x);
+    for (int e = t; e < p.bins; e += kOrderThreads) count[e] = 0;
     __syncthreads();
     const int64_t first = blockIdx.x * p.chunk, last = first + p.chunk < p.slots ? first + p.chunk : p.slots;
-    for (int64_t i = first + t; i < last; i += kOrderThreads) atomicAdd(&count[bin_of(p, i)], 1);
+    constexpr int U = 4;
+    for (int64_t i = first + t; i < last; i += U * kOrderThreads) {
+        int32_t id[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) id[u] = i + u * kOrderThreads < last ? p.ids[i + u * kOrderThreads] : 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i + u * kOrderThreads < last) atomicAdd(&count[bin_of(p, id[u])], 1);
+    }
     __syncthreads();
-    for (int e = t; e < bins; e += kOrderThreads) p.counts[static_cast<int64_t>(blockIdx.x) * bins + e] = count[e];
+    for (int e = t; e < p.bins; e += kOrderThreads) p.counts[static_cast<int64_t>(blockIdx.x) * p.bins + e] = count[e];
 }
 
 // A slot's row: rows of the experts before its own, rows of its own in earlier
 // blocks, in earlier waves of the block, in earlier lanes.
 __global__ __launch_bounds__(kOrderThreads) void k_order_place(OrderArgs p)
 {
-    constexpr int W = kOrderThreads / kWave;
-    __shared__ int32_t next[W][kMaxExperts + 1];   // the next row of each wave
-    __shared__ int32_t sums[W];
-    const int t = static_cast<int>(threadIdx.x), lane = t & 63, wave = t >> 6, bins = p.experts + 1;
-    for (int e = t; e < W * (kMaxExperts + 1); e += kOrderThreads) (&next[0][0])[e] = 0;
+    constexpr int W = kOrderThreads / kWave, U = 8;
+    __shared__ int32_t next[W][kMaxExperts + 4];   // slots of each wave, then its next row
+    __shared__ int32_t total[kMaxExperts + 4], before[kMaxExperts + 4], sums[W];
+    const int t = static_cast<int>(threadIdx.x), lane = t & 63, wave = t >> 6, bins = p.bins;
+    for (int e = t; e < bins; e += kOrderThreads) {
+        total[e] = before[e] = 0;
+#pragma unroll
+        for (int w = 0; w < W; ++w) next[w][e] = 0;
+    }
     __syncthreads();
     const int64_t part = p.chunk / W, begin = blockIdx.x * p.chunk + wave * part;
     const int64_t end = begin + part < p.slots ? begin + part : p.slots;
-    for (int64_t i = begin + lane; i < end; i += kWave) atomicAdd(&next[wave][bin_of(p, i)], 1);
+    int32_t id[U];
+    auto load = [&](int64_t i0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t i = i0 + u * kWave + lane;
+            id[u] = i < end ? p.ids[i] : -1;
+        }
+    };
+    for (int64_t i0 = begin; i0 < end; i0 += U * kWave) {
+        load(i0);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i0 + u * kWave + lane < end) atomicAdd(&next[wave][bin_of(p, id[u])], 1);
+    }
+    if (p.blocks > 1) {
+        const int quads = bins / 4, teams = kOrderThreads / quads, team = t / quads, quad = t - team * quads;
+        if (team < teams) {
+            int32_t all[4] = {}, mine[4] = {};
+            const int32_t* const c = p.counts + quad * 4;
+            for (int b = team; b < p.blocks; b += teams * U) {
+                i32x4 v[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    v[u] = b + u * teams < p.blocks ? *reinterpret_cast<const i32x4*>(c + static_cast<int64_t>(b + u * teams) * bins)
+                                                    : i32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const bool earlier = b + u * teams < static_cast<int>(blockIdx.x);
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        all[h] += v[u][h];
+                        mine[h] += earlier ? v[u][h] : 0;
+                    }
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                atomicAdd(&total[quad * 4 + h], all[h]);
+                atomicAdd(&before[quad * 4 + h], mine[h]);
+            }
+        }
+    }
     __syncthreads();
-    // two bins a thread at most: a thread's are neighbours
-    constexpr int B = (kMaxExperts + kOrderThreads) / kOrderThreads;
-    int32_t all[B], before[B], run = 0;
+    // neighbouring bins to a thread, and the sum over the threads before it
+    constexpr int B = (kMaxExperts + 4 + kOrderThreads - 1) / kOrderThreads;
+    const int per = bins > 2 * kOrderThreads ? 3 : bins > kOrderThreads ? 2 : 1;
+    int32_t all[B], run = 0;
 #pragma unroll
     for (int i = 0; i < B; ++i) {
-        const int e = t * B + i;
-        all[i] = before[i] = 0;
-        if (e >= bins) continue;
+        const int e = t * per + i;
+        all[i] = 0;
+        if (i >= per || e >= bins) continue;
         if (p.blocks == 1) {
+#pragma unroll
             for (int w = 0; w < W; ++w) all[i] += next[w][e];
         } else {
-            for (int b = 0; b < p.blocks; ++b) {
-                const int32_t c = p.counts[static_cast<int64_t>(b) * bins + e];
-                all[i] += c;
-                if (b < static_cast<int>(blockIdx.x)) before[i] += c;
-            }
+            all[i] = total[e];
         }
         run += all[i];
     }
-    // sum over the threads before this one
     int32_t scan = run;
     for (int s = 1; s < kWave; s <<= 1) {
         const int32_t up = __shfl_up(scan, s);
@@ -617,10 +743,11 @@ __global__ __launch_bounds__(kOrderThreads) void k_order_place(OrderArgs p)
     for (int w = 0; w < wave; ++w) row += sums[w];
 #pragma unroll
     for (int i = 0; i < B; ++i) {
-        const int e = t * B + i;
-        if (e >= bins) continue;
-        if (blockIdx.x == 0) p.offsets[e] = row;
-        int32_t at = row + before[i];
+        const int e = t * per + i;
+        if (i >= per || e >= bins) continue;
+        if (blockIdx.x == 0 && e <= p.experts) p.offsets[e] = row;
+        int32_t at = row + before[e];
+#pragma unroll
         for (int w = 0; w < W; ++w) {
             const int32_t c = next[w][e];
             next[w][e] = at;
@@ -630,24 +757,30 @@ __global__ __launch_bounds__(kOrderThreads) void k_order_place(OrderArgs p)
     }
     __syncthreads();
     int bits = 0;
-    while ((1 << bits) < bins) ++bits;
-    for (int64_t i0 = begin; i0 < end; i0 += kWave) {
-        const int64_t i = i0 + lane;
-        const bool in = i < end;
-        const int e = in ? bin_of(p, i) : 0;
-        uint64_t same = __ballot(in);   // lanes of the same bin
-        for (int b = 0; b < bits; ++b) {
-            const uint64_t set = __ballot(e >> b & 1);
-            same &= e >> b & 1 ? set : ~set;
-        }
-        const int rank = __popcll(same & ((uint64_t(1) << lane) - 1));
-        const int32_t at = in ? next[wave][e] + rank : 0;
-        wave_sync();
-        if (in && rank == 0) next[wave][e] = at + __popcll(same);
-        wave_sync();
-        if (in) {
-            p.slot_of_row[at] = e < p.experts ? static_cast<int32_t>(i) : -1;
-            p.row_of_slot[i] = e < p.experts ? at : -1;
+    while ((1 << bits) <= p.experts) ++bits;
+    const bool once = end - begin <= U * kWave;   // the ids are still there
+    for (int64_t i0 = begin; i0 < end; i0 += U * kWave) {
+        if (!once) load(i0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t i = i0 + u * kWave + lane;
+            if (i - lane >= end) break;
+            const bool in = i < end;
+            const int e = bin_of(p, id[u]);
+            uint64_t same = __ballot(in);   // lanes of the same bin
+            for (int b = 0; b < bits; ++b) {
+                const uint64_t set = __ballot(e >> b & 1);
+                same &= e >> b & 1 ? set : ~set;
+            }
+            const int rank = __popcll(same & ((uint64_t(1) << lane) - 1));
+            const int32_t at = in ? next[wave][e] + rank : 0;
+            wave_sync();
+            if (in && rank == 0) next[wave][e] = at + __popcll(same);
+            wave_sync();
+            if (in) {
+                p.slot_of_row[at] = e < p.experts ? static_cast<int32_t>(i) : -1;
+                p.row_of_slot[i] = e < p.experts ? at : -1;
+            }
         }
     }
 }
@@ -686,23 +819,36 @@ __global__ __launch_bounds__(kRowThreads) void k_dispatch(RowsArgs p)
     }
 }
 
+// A block per token; a lane has the pieces of eight of its rows on their way.
 template <int DT, bool WIDE>
 __global__ __launch_bounds__(kRowThreads) void k_combine(RowsArgs p)
 {
     using P = Piece<DT, WIDE>;
+    constexpr int U = 8;
     const int64_t t = blockIdx.x, rows = p.tokens * p.k;
-    const int32_t* from = p.row_of_slot + t * p.k;
+    const int32_t* const from = p.row_of_slot + t * p.k;
+    const float* const weights = p.weights ? p.weights + t * p.k : nullptr;
     for (int64_t c = static_cast<int64_t>(threadIdx.x) * P::kValues; c < p.cols;
          c += static_cast<int64_t>(kRowThreads) * P::kValues) {
         float acc[P::kValues] = {};
-        for (int j = 0; j < p.k; ++j) {
-            const int64_t r = from[j];
-            if (r < 0 || r >= rows) continue;
-            float v[P::kValues];
-            P::load(p.x, r * p.x_stride + c, v);
-            const float w = p.weights ? p.weights[t * p.k + j] : 1.0f;
+        for (int j0 = 0; j0 < p.k; j0 += U) {
+            typename P::Raw raw[U];
+            bool has[U];
 #pragma unroll
-            for (int i = 0; i < P::kValues; ++i) acc[i] = __builtin_fmaf(w, v[i], acc[i]);
+            for (int u = 0; u < U; ++u) {
+                const int64_t r = j0 + u < p.k ? from[j0 + u] : -1;
+                has[u] = r >= 0 && r < rows;
+                if (has[u]) raw[u] = P::fetch(p.x, r * p.x_stride + c);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (!has[u]) continue;
+                float v[P::kValues];
+                P::unpack(raw[u], v);
+                const float w = weights ? weights[j0 + u] : 1.0f;
+#pragma unroll
+                for (int i = 0; i < P::kValues; ++i) acc[i] = __builtin_fmaf(w, v[i], acc[i]);
+            }
         }
         if (p.add) {
             float v[P::kValues];
@@ -789,11 +935,27 @@ TopkKernel topk_kernel(int dtype, int32_t experts, int32_t k, int32_t groups)
            : dtype == kF16 ? choose_topk<kF16>(experts, k, groups)
                            : choose_topk<kBF16>(experts, k, groups);
 }
-const void* topk_backward_kernel(int dtype)
+namespace {
+
+template <int DT>
+TopkKernel choose_topk_backward(int32_t experts, int32_t k)
 {
-    return dtype == kF32   ? reinterpret_cast<const void*>(k_topk_backward<kF32>)
-           : dtype == kF16 ? reinterpret_cast<const void*>(k_topk_backward<kF16>)
-                           : reinterpret_cast<const void*>(k_topk_backward<kBF16>);
+    if (experts <= 256 && k <= 16) {
+        if (experts <= 64) return {reinterpret_cast<const void*>(k_topk_backward<DT, 16, 4>), 4};
+        if (experts <= 128) return {reinterpret_cast<const void*>(k_topk_backward<DT, 16, 8>), 4};
+        return {reinterpret_cast<const void*>(k_topk_backward<DT, 16, 16>), 4};
+    }
+    if (experts <= 512 && k <= 32) return {reinterpret_cast<const void*>(k_topk_backward<DT, 32, 16>), 2};
+    return {reinterpret_cast<const void*>(k_topk_backward<DT, 64, 16>), 1};
+}
+
+}  // namespace
+
+TopkKernel topk_backward_kernel(int dtype, int32_t experts, int32_t k)
+{
+    return dtype == kF32   ? choose_topk_backward<kF32>(experts, k)
+           : dtype == kF16 ? choose_topk_backward<kF16>(experts, k)
+                           : choose_topk_backward<kBF16>(experts, k);
 }
 const void* order_count_kernel() { return reinterpret_cast<const void*>(k_order_count); }
 const void* order_place_kernel() { return reinterpret_cast<const void*>(k_order_place); }

@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "experts.h"
 
 namespace experts {
@@ -34,6 +36,11 @@ struct Value<kF32> {
             out[j] = __builtin_bit_cast(float, d);
         }
     }
+    static __device__ __forceinline__ void store4(float* p, const float* v)
+    {
+        *reinterpret_cast<u32x4*>(p) = u32x4{__builtin_bit_cast(uint32_t, v[0]), __builtin_bit_cast(uint32_t, v[1]),
+                                             __builtin_bit_cast(uint32_t, v[2]), __builtin_bit_cast(uint32_t, v[3])};
+    }
 };
 template <>
 struct Value<kF16> {
@@ -53,6 +60,11 @@ struct Value<kF16> {
             out[2 * j + 1] = to_float(static_cast<uint16_t>(d >> 16));
         }
     }
+    static __device__ __forceinline__ void store4(uint16_t* p, const float* v)
+    {
+        *reinterpret_cast<u32x2*>(p) = u32x2{from_float(v[0]) | static_cast<uint32_t>(from_float(v[1])) << 16,
+                                             from_float(v[2]) | static_cast<uint32_t>(from_float(v[3])) << 16};
+    }
 };
 template <>
 struct Value<kBF16> {
@@ -71,6 +83,11 @@ struct Value<kBF16> {
             out[2 * j] = to_float(static_cast<uint16_t>(d));
             out[2 * j + 1] = to_float(static_cast<uint16_t>(d >> 16));
         }
+    }
+    static __device__ __forceinline__ void store4(uint16_t* p, const float* v)
+    {
+        *reinterpret_cast<u32x2*>(p) = u32x2{from_float(v[0]) | static_cast<uint32_t>(from_float(v[1])) << 16,
+                                             from_float(v[2]) | static_cast<uint32_t>(from_float(v[3])) << 16};
     }
 };
 
@@ -97,16 +114,20 @@ struct Piece {
     using Elem = typename V::Elem;
     static constexpr int kValues = WIDE ? 16 / V::kBytes : 1;
 
-    static __device__ __forceinline__ void load(const void* p, int64_t i, float* out)
+    using Raw = std::conditional_t<WIDE, u32x4, Elem>;
+
+    static __device__ __forceinline__ Raw fetch(const void* p, int64_t i)
     {
-        const Elem* q = static_cast<const Elem*>(p) + i;
-        if constexpr (!WIDE) {
-            out[0] = V::to_float(*q);
-        } else {
-            unpack(*reinterpret_cast<const u32x4*>(q), out);
-        }
+        return *reinterpret_cast<const Raw*>(static_cast<const Elem*>(p) + i);
     }
-    static __device__ __forceinline__ void unpack(u32x4 w, float* out)
+    static __device__ __forceinline__ void load(const void* p, int64_t i, float* out) { unpack(fetch(p, i), out); }
+    template <class R = Raw, std::enable_if_t<std::is_same_v<R, Elem>, int> = 0>
+    static __device__ __forceinline__ void unpack(R x, float* out)
+    {
+        out[0] = V::to_float(x);
+    }
+    template <class R = Raw, std::enable_if_t<std::is_same_v<R, u32x4>, int> = 0>
+    static __device__ __forceinline__ void unpack(R w, float* out)
     {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
