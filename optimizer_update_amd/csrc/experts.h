@@ -60,6 +60,7 @@ struct RowsArgs {
     float* dweights;
     int64_t tokens, cols, x_stride, y_stride, add_stride, out_stride;
     int32_t k, zero_rest;
+    int32_t past_caches;    // the rows are too many to stay in the last cache
 };
 
 // 4-bit weights; experts 0: one matrix, no groups of rows.
@@ -113,7 +114,7 @@ constexpr int kOrderThreads = 512;
 constexpr int kOrderAlone = 4096;      // slots that one block takes by itself
 constexpr int kOrderChunk = 2048;      // slots of a block, at least
 constexpr int kOrderBlocks = 256;      // at most
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 512;       // at most: a row's pieces, in whole waves
 constexpr int kInt4Threads = 256;
 
 }  // namespace experts

@@ -43,6 +43,17 @@ int check_topk(int dtype, int64_t tokens, int32_t experts, int64_t row_stride, i
     return OU_OK;
 }
 
+// Where the rows of all slots are more than this, what is written leaves by
+// non-temporal stores: it would only push others out of the 256 MiB last cache.
+constexpr int64_t kKeptBytes = int64_t(192) << 20;
+
+// Threads of a block that moves rows of `pieces`.
+int row_threads(int64_t pieces)
+{
+    const int64_t t = cut(pieces, kWave) * kWave;
+    return static_cast<int>(t < kWave ? kWave : t < kRowThreads ? t : kRowThreads);
+}
+
 double dense(int64_t rows, int64_t cols, int bytes) { return extent(rows, cols, cols, bytes); }
 
 // Rows of the three kernels that move them.
@@ -205,9 +216,10 @@ OU_EXPORT int ou_route_dispatch(int dtype, const void* x, int64_t tokens, int64_
     p.x_stride = x_stride / per;
     p.out_stride = out_stride / per;
     p.k = k;
+    p.past_caches = tokens * k * cols * eb > kKeptBytes;
     p.zero_rest = zero_rest != 0;
     void* args[] = {&p};
-    return launch({dispatch_kernel(eb, wide), tokens, 1, kRowThreads, "k_dispatch", 0}, args, stream);
+    return launch({dispatch_kernel(eb, wide), tokens, 1, row_threads(p.cols), "k_dispatch", 0}, args, stream);
 }
 
 OU_EXPORT int ou_route_combine(int dtype, const void* y, int64_t tokens, int64_t cols, int64_t y_stride, int32_t k,
@@ -241,10 +253,12 @@ OU_EXPORT int ou_route_combine(int dtype, const void* y, int64_t tokens, int64_t
     p.add_stride = add_stride;
     p.out_stride = out_stride;
     p.k = k;
+    p.past_caches = tokens * k * cols * eb > kKeptBytes;
     const void* const ptrs[] = {y, add, out};
     const int64_t strides[] = {y_stride, add_stride, out_stride};
     void* args[] = {&p};
-    return launch({combine_kernel(dtype, wide_cols(r, ptrs, strides, 3)), tokens, 1, kRowThreads, "k_combine", 0}, args,
+    const bool wide = wide_cols(r, ptrs, strides, 3);
+    return launch({combine_kernel(dtype, wide), tokens, 1, row_threads(wide ? cols * eb / 16 : cols), "k_combine", 0}, args,
                   stream);
 }
 
@@ -259,7 +273,7 @@ OU_EXPORT int ou_route_combine_backward(int dtype, const void* dout, int64_t tok
     if (!dy && !dweights) return fail(OU_EINVAL, "dy and dweights are null");
     if (dweights)
         if (int st = check_stride(y_stride, cols, "y_stride")) return st;
-    if (tokens == 0 || (cols == 0 && !dweights)) return OU_OK;
+    if (tokens == 0 || (cols == 0 && !dweights)) return OU_OK;   // without columns the weights' gradient is 0
     const int eb = elem_bytes(dtype);
     const unsigned ea = static_cast<unsigned>(eb);
     const Buffer bufs[] = {{"dout", dout, extent(tokens, cols, dout_stride, eb), ea, false},
@@ -284,10 +298,12 @@ OU_EXPORT int ou_route_combine_backward(int dtype, const void* dout, int64_t tok
     p.y_stride = y_stride;
     p.out_stride = cols;
     p.k = k;
+    p.past_caches = tokens * k * cols * eb > kKeptBytes;
     const void* const ptrs[] = {dout, dweights ? y : nullptr, dy};
     const int64_t strides[] = {dout_stride, y_stride, cols};
     void* args[] = {&p};
-    return launch({combine_backward_kernel(dtype, wide_cols(r, ptrs, strides, 3)), tokens, 1, kRowThreads,
+    const bool wide = wide_cols(r, ptrs, strides, 3);
+    return launch({combine_backward_kernel(dtype, wide), tokens, 1, row_threads(wide ? cols * eb / 16 : cols),
                    "k_combine_backward", 0}, args, stream);
 }
 

@@ -797,55 +797,79 @@ __global__ __launch_bounds__(256) void k_balance(const float* bias, const int32_
 
 // ---- rows -----------------------------------------------------------------------
 
-// A block per token: each piece of its row is read once and written to the rows
-// of its slots.  Block t also clears those of rows t * k .. that are of no slot.
+// A block per token.  Lane j of every wave holds the row (and the weight) of
+// choice j: taken from there by readlane they are uniform, and no load of them
+// stands between those of the rows.
+struct Choices {
+    int32_t row;      // of choice `lane`, -1: none
+    float weight;
+
+    __device__ __forceinline__ Choices(const int32_t* rows, const float* weights, int64_t t, int k, int64_t count)
+    {
+        const int lane = static_cast<int>(threadIdx.x) & 63;
+        row = lane < k ? rows[t * k + lane] : -1;
+        if (row >= count) row = -1;
+        weight = weights && lane < k ? weights[t * k + lane] : 1.0f;
+    }
+    __device__ __forceinline__ int64_t row_of(int j) const { return __builtin_amdgcn_readlane(row, j); }
+    __device__ __forceinline__ float weight_of(int j) const
+    {
+        return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int32_t, weight), j));
+    }
+};
+
+// Each piece of the token's row is read once and written to the rows of its
+// slots.  Block t also clears those of rows t * k .. that are of no slot.
 template <class U>
 __global__ __launch_bounds__(kRowThreads) void k_dispatch(RowsArgs p)
 {
-    const int64_t t = blockIdx.x, rows = p.tokens * p.k;
-    const U* x = reinterpret_cast<const U*>(p.x) + t * p.x_stride;
-    U* out = reinterpret_cast<U*>(p.out);
-    const int32_t* to = p.row_of_slot + t * p.k;
-    const int32_t* of = p.slot_of_row + t * p.k;
-    for (int64_t c = threadIdx.x; c < p.cols; c += kRowThreads) {
-        const U v = x[c];
-        for (int j = 0; j < p.k; ++j) {
-            const int64_t r = to[j];
-            if (r >= 0 && r < rows) out[r * p.out_stride + c] = v;
-        }
-        if (p.zero_rest)
-            for (int j = 0; j < p.k; ++j)
-                if (of[j] < 0) out[(t * p.k + j) * p.out_stride + c] = U{};
+    const int64_t t = blockIdx.x;
+    const U* const x = reinterpret_cast<const U*>(p.x) + t * p.x_stride;
+    U* const out = reinterpret_cast<U*>(p.out);
+    const Choices to(p.row_of_slot, nullptr, t, p.k, p.tokens * p.k);
+    const Choices of(p.slot_of_row, nullptr, t, p.k, p.tokens * p.k);
+    const uint64_t all = p.k == kWave ? ~uint64_t(0) : (uint64_t(1) << p.k) - 1;
+    const uint64_t has = __ballot(to.row >= 0) & all, rest = p.zero_rest ? __ballot(of.row < 0) & all : 0;
+    for (int64_t c = threadIdx.x; c < p.cols; c += blockDim.x) {
+        const U v = __builtin_nontemporal_load(x + c);
+        auto put = [&](U* q, U u) {
+            if (p.past_caches)
+                __builtin_nontemporal_store(u, q);
+            else
+                *q = u;
+        };
+        for (uint64_t m = has; m; m &= m - 1) put(out + to.row_of(__builtin_ctzll(m)) * p.out_stride + c, v);
+        for (uint64_t m = rest; m; m &= m - 1) put(out + (t * p.k + __builtin_ctzll(m)) * p.out_stride + c, U{});
     }
 }
 
-// A block per token; a lane has the pieces of eight of its rows on their way.
+// A lane has the pieces of eight of the token's rows on their way.
+// COMBINE_TIME
 template <int DT, bool WIDE>
 __global__ __launch_bounds__(kRowThreads) void k_combine(RowsArgs p)
 {
     using P = Piece<DT, WIDE>;
     constexpr int U = 8;
-    const int64_t t = blockIdx.x, rows = p.tokens * p.k;
-    const int32_t* const from = p.row_of_slot + t * p.k;
-    const float* const weights = p.weights ? p.weights + t * p.k : nullptr;
+    const int64_t t = blockIdx.x;
+    const Choices from(p.row_of_slot, p.weights, t, p.k, p.tokens * p.k);
+    const uint64_t has = __ballot(from.row >= 0);
     for (int64_t c = static_cast<int64_t>(threadIdx.x) * P::kValues; c < p.cols;
-         c += static_cast<int64_t>(kRowThreads) * P::kValues) {
+         c += static_cast<int64_t>(blockDim.x) * P::kValues) {
         float acc[P::kValues] = {};
         for (int j0 = 0; j0 < p.k; j0 += U) {
+            if (!(has >> j0 & 0xff)) continue;
             typename P::Raw raw[U];
-            bool has[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int64_t r = j0 + u < p.k ? from[j0 + u] : -1;
-                has[u] = r >= 0 && r < rows;
-                if (has[u]) raw[u] = P::fetch(p.x, r * p.x_stride + c);
+                const int64_t r = from.row_of(j0 + u);
+                raw[u] = P::fetch_once(p.x, (r < 0 ? 0 : r) * p.x_stride + c);   // row 0 for none: no branch between the loads
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (!has[u]) continue;
+                // for none 0 times 0: behind a branch the load would be put there too
                 float v[P::kValues];
-                P::unpack(raw[u], v);
-                const float w = weights ? weights[j0 + u] : 1.0f;
+                P::unpack(has >> (j0 + u) & 1 ? raw[u] : typename P::Raw{}, v);
+                const float w = has >> (j0 + u) & 1 ? from.weight_of(j0 + u) : 0.0f;
 #pragma unroll
                 for (int i = 0; i < P::kValues; ++i) acc[i] = __builtin_fmaf(w, v[i], acc[i]);
             }
@@ -856,57 +880,76 @@ __global__ __launch_bounds__(kRowThreads) void k_combine(RowsArgs p)
 #pragma unroll
             for (int i = 0; i < P::kValues; ++i) acc[i] += v[i];
         }
-        P::store(p.out, t * p.out_stride + c, acc);
+        P::store(p.out, t * p.out_stride + c, acc, p.past_caches);
     }
 }
 
+// Eight choices at a time: their rows of y are read and their rows of dy
+// written beside one another.  COMBINE_BACKWARD_TIME
 template <int DT, bool WIDE>
 __global__ __launch_bounds__(kRowThreads) void k_combine_backward(RowsArgs p)
 {
     using P = Piece<DT, WIDE>;
-    constexpr int W = kRowThreads / kWave;
+    constexpr int W = kRowThreads / kWave, U = 8;
     __shared__ float part[W][kMaxChoices];
-    const int64_t t = blockIdx.x, rows = p.tokens * p.k;
+    const int64_t t = blockIdx.x;
     const int tid = static_cast<int>(threadIdx.x);
-    const int32_t* from = p.row_of_slot + t * p.k;
-    const int32_t* of = p.slot_of_row + t * p.k;
-    for (int j = 0; j < p.k; ++j) {
-        const int64_t r = from[j];
-        const bool has = r >= 0 && r < rows, rest = p.out && of[j] < 0;
-        const float w = has && p.out ? p.weights[t * p.k + j] : 0.0f;
-        float dot = 0.0f;
+    const Choices from(p.row_of_slot, p.out ? p.weights : nullptr, t, p.k, p.tokens * p.k);
+    const Choices of(p.slot_of_row, nullptr, t, p.k, p.tokens * p.k);
+    const uint64_t has = __ballot(from.row >= 0);
+    const uint64_t all = p.k == kWave ? ~uint64_t(0) : (uint64_t(1) << p.k) - 1;
+    const uint64_t rest = p.out ? __ballot(of.row < 0) & all : 0;
+    for (int j0 = 0; j0 < p.k; j0 += U) {
+        float dot[U] = {};
         for (int64_t c = static_cast<int64_t>(tid) * P::kValues; c < p.cols;
-             c += static_cast<int64_t>(kRowThreads) * P::kValues) {
-            float g[P::kValues], v[P::kValues];
-            if (has) {
-                P::load(p.x, t * p.x_stride + c, g);
-                if (p.dweights) {
-                    P::load(p.y, r * p.y_stride + c, v);
+             c += static_cast<int64_t>(blockDim.x) * P::kValues) {
+            typename P::Raw raw[U];
+            if (p.dweights) {
 #pragma unroll
-                    for (int i = 0; i < P::kValues; ++i) dot = __builtin_fmaf(g[i], v[i], dot);
-                }
-                if (p.out) {
-#pragma unroll
-                    for (int i = 0; i < P::kValues; ++i) g[i] *= w;
-                    P::store(p.out, r * p.out_stride + c, g);
+                for (int u = 0; u < U; ++u) {
+                    const int64_t r = from.row_of(j0 + u);
+                    raw[u] = P::fetch_once(p.y, (r < 0 ? 0 : r) * p.y_stride + c);
                 }
             }
-            if (rest) {
+            float g[P::kValues];
+            P::load(p.x, t * p.x_stride + c, g);
 #pragma unroll
-                for (int i = 0; i < P::kValues; ++i) v[i] = 0.0f;
-                P::store(p.out, (t * p.k + j) * p.out_stride + c, v);
+            for (int u = 0; u < U; ++u) {
+                if (p.dweights) {
+                    float v[P::kValues];
+                    P::unpack(has >> (j0 + u) & 1 ? raw[u] : typename P::Raw{}, v);
+#pragma unroll
+                    for (int i = 0; i < P::kValues; ++i) dot[u] = __builtin_fmaf(g[i], v[i], dot[u]);
+                }
+                if (p.out && has >> (j0 + u) & 1) {
+                    const float w = from.weight_of(j0 + u);
+                    float v[P::kValues];
+#pragma unroll
+                    for (int i = 0; i < P::kValues; ++i) v[i] = w * g[i];
+                    P::store(p.out, from.row_of(j0 + u) * p.out_stride + c, v, p.past_caches);
+                }
             }
         }
-        dot = wave_sum(dot);
-        if ((tid & 63) == 0) part[tid >> 6][j] = dot;
+        if (p.dweights) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float sum = wave_sum(dot[u]);
+                if ((tid & 63) == 0 && j0 + u < p.k) part[tid >> 6][j0 + u] = sum;
+            }
+        }
+    }
+    for (uint64_t m = rest; m; m &= m - 1) {
+        const float zero[P::kValues] = {};
+        for (int64_t c = static_cast<int64_t>(tid) * P::kValues; c < p.cols;
+             c += static_cast<int64_t>(blockDim.x) * P::kValues)
+            P::store(p.out, (t * p.k + __builtin_ctzll(m)) * p.out_stride + c, zero, p.past_caches);
     }
     if (!p.dweights) return;
     __syncthreads();
     if (tid < p.k) {
         float sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < W; ++w) sum += part[w][tid];
-        p.dweights[t * p.k + tid] = sum;
+        for (int w = 0; w < static_cast<int>(blockDim.x) / kWave; ++w) sum += part[w][tid];
+        p.dweights[t * p.k + tid] = has >> tid & 1 ? sum : 0.0f;   // whatever dout holds
     }
 }
 

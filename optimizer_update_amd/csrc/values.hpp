@@ -120,6 +120,11 @@ struct Piece {
     {
         return *reinterpret_cast<const Raw*>(static_cast<const Elem*>(p) + i);
     }
+    // read once: past the caches
+    static __device__ __forceinline__ Raw fetch_once(const void* p, int64_t i)
+    {
+        return __builtin_nontemporal_load(reinterpret_cast<const Raw*>(static_cast<const Elem*>(p) + i));
+    }
     static __device__ __forceinline__ void load(const void* p, int64_t i, float* out) { unpack(fetch(p, i), out); }
     template <class R = Raw, std::enable_if_t<std::is_same_v<R, Elem>, int> = 0>
     static __device__ __forceinline__ void unpack(R x, float* out)
@@ -140,25 +145,29 @@ struct Piece {
             }
         }
     }
-    static __device__ __forceinline__ u32x4 pack(const float* v)
+    static __device__ __forceinline__ Raw pack(const float* v)
     {
-        u32x4 w;
+        if constexpr (!WIDE) {
+            return V::from_float(v[0]);
+        } else {
+            u32x4 w;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if constexpr (DT == kF32)
-                w[j] = __builtin_bit_cast(uint32_t, v[j]);
-            else
-                w[j] = static_cast<uint32_t>(V::from_float(v[2 * j])) | static_cast<uint32_t>(V::from_float(v[2 * j + 1])) << 16;
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (DT == kF32)
+                    w[j] = __builtin_bit_cast(uint32_t, v[j]);
+                else
+                    w[j] = static_cast<uint32_t>(V::from_float(v[2 * j])) | static_cast<uint32_t>(V::from_float(v[2 * j + 1])) << 16;
+            }
+            return w;
         }
-        return w;
     }
-    static __device__ __forceinline__ void store(void* p, int64_t i, const float* v)
+    static __device__ __forceinline__ void store(void* p, int64_t i, const float* v, bool past_caches)
     {
-        Elem* q = static_cast<Elem*>(p) + i;
-        if constexpr (!WIDE)
-            *q = V::from_float(v[0]);
+        Raw* const q = reinterpret_cast<Raw*>(static_cast<Elem*>(p) + i);
+        if (past_caches)
+            __builtin_nontemporal_store(pack(v), q);
         else
-            *reinterpret_cast<u32x4*>(q) = pack(v);
+            *q = pack(v);
     }
 };
 

@@ -321,6 +321,45 @@ def test_combine(t, k, e, h, dtype, added):
     assert torch.equal(room[:, 1:1 + h], out.detach()) and (room[:, 0] == 5).all() and (room[:, 1 + h:] == 5).all()
 
 
+def test_combine_keeps_what_it_should_not_read():
+    """An infinite gradient times a slot without a row is 0; and results of a
+    size that goes past the caches."""
+    places = torch.tensor([[0, -1]], dtype=torch.int32, device="cuda")
+    o = ou.RouteOrder(torch.tensor([0, 1], dtype=torch.int32, device="cuda"), torch.tensor([0, -1], dtype=torch.int32, device="cuda"), places)
+    y = torch.ones((2, 64), device="cuda").requires_grad_(True)
+    w = torch.ones((1, 2), device="cuda").requires_grad_(True)
+    out = ou.route_combine(y, w, o)
+    out.backward(torch.full((1, 64), INF, device="cuda"))
+    assert w.grad[0, 0] == INF and w.grad[0, 1] == 0 and (y.grad[1] == 0).all() and (y.grad[0] == INF).all()
+    t, k, h = 4096, 4, 8192   # 256 MiB in bfloat16
+    ids = _ids(t, k, 16, 5)
+    o = ou.route_order(ids.cuda(), 16)
+    x = torch.randn((t, h), device="cuda", dtype=BF16).requires_grad_(True)
+    w = torch.rand((t, k), device="cuda").requires_grad_(True)
+    rows = ou.route_dispatch(x, o)
+    out = ou.route_combine(rows, w, o)
+    g = torch.randn((t, h), device="cuda", dtype=BF16)
+    dx, dw = torch.autograd.grad(out, (x, w), g)
+    live = (o.places >= 0).float()
+    total = (w.detach() * live).sum(1, keepdim=True)
+    # each product and partial sum to half a step of the type at most, and the last rounding
+    torch.testing.assert_close(out.float(), x.detach().float() * total, rtol=2.0 ** -8, atol=1e-5)
+    torch.testing.assert_close(dx.float(), g.float() * total, rtol=3 * 2.0 ** -8, atol=2.0 ** -7)
+    ref = (x.detach().float() * g.float()).sum(1, keepdim=True) * live
+    torch.testing.assert_close(dw, ref, rtol=1e-4, atol=2e-2)
+
+
+def test_rows_without_columns():
+    o = ou.route_order(torch.zeros((3, 2), dtype=torch.int32, device="cuda"), 4)
+    x = torch.zeros((3, 0), device="cuda", requires_grad=True)
+    w = torch.ones((3, 2), device="cuda", requires_grad=True)
+    rows = ou.route_dispatch(x, o)
+    out = ou.route_combine(rows, w, o)
+    assert rows.shape == (6, 0) and out.shape == (3, 0)
+    dx, dw = torch.autograd.grad(out, (x, w), torch.zeros((3, 0), device="cuda"))
+    assert dx.shape == (3, 0) and torch.equal(dw, torch.zeros((3, 2), device="cuda"))
+
+
 def test_orders_with_bad_rows_stay_inside():
     """Places that a program made itself: what points nowhere is as -1."""
     places = torch.tensor([[5, -7], [1 << 30, 0]], dtype=torch.int32, device="cuda")
