@@ -197,10 +197,12 @@ __device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b)
 
 // 16 NT rows of weights and 16 MT rows of x a block, the steps of 128 columns
 // dealt to its W waves in runs; U steps of a wave are in flight.  Lane group g
-// (of 16 lanes) loads columns 32 g .. of a step, one request of 64 bytes a row.
-// An instruction's 32 columns have to be of one group of columns: where a step
-// has S = 2 or 4 of them, lane groups exchange registers first (halves, then
-// quarters), and take x from where that leads.
+// (of 16 lanes) loads columns 32 g .. of a step, one request of 64 bytes a row;
+// the groups then exchange registers so that register i of group g holds
+// columns 32 i + 8 g .., for two reasons: an instruction's 32 columns are of one
+// group of columns, and x is asked for by 64 bytes a row (as it would be by 16
+// where the codes were loaded).  S groups of columns are in a step: a lane group
+// loads the scale of one of four in a row, and a lane gets its row's from there.
 template <int DT, int S, int NT, int MT, int W, int U, bool GROUPED>
 __global__ __launch_bounds__(kWave * W) void k_int4_matmul(Int4Args p)
 {
@@ -234,19 +236,15 @@ __global__ __launch_bounds__(kWave * W) void k_int4_matmul(Int4Args p)
         scale_row[j] = n * columns;
     }
     const Elem* x[MT];
+    bool live[MT];   // rows behind the last one are 0 and not loaded
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-        const int xr = 16 * i + r < rows ? 16 * i + r : rows - 1;
-        x[i] = static_cast<const Elem*>(p.x) + (row0 + xr) * p.x_stride;
+        live[i] = 16 * i + r < rows;
+        x[i] = static_cast<const Elem*>(p.x) + (row0 + (live[i] ? 16 * i + r : 0)) * p.x_stride + g * 8;
     }
-    // the column of a step that register i of a lane holds, from where the exchanges bring it
-    auto column = [&](int i) {
-        return S == 1 ? g * 32 + i * 8 : S == 2 ? (i >> 1) * 64 + (g & 1) * 32 + (g >> 1) * 16 + (i & 1) * 8 : i * 32 + g * 8;
-    };
     struct Step {
         u32x4 c[NT];
         Rows8<DT> x[MT][4];
-        float scale[NT][S], zero[NT][S];
     } step[U];
     auto load = [&](Step& s, int at) {
         const int64_t k0 = static_cast<int64_t>(at) * kChunk;
@@ -259,40 +257,44 @@ __global__ __launch_bounds__(kWave * W) void k_int4_matmul(Int4Args p)
         for (int i = 0; i < MT; ++i) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int64_t k = k0 + column(q);
-                if (whole || k < p.k)
-                    s.x[i][q].load(x[i] + k, p.x_wide);
-                else
-                    s.x[i][q].zero();
+                s.x[i][q].zero();
+                if (live[i] && (whole || k0 + q * 32 < p.k)) s.x[i][q].load(x[i] + k0 + q * 32, p.x_wide);
             }
         }
+    };
+    // scale and zero of the group of columns `4 at + g` of the wave's run
+    float scale[NT], zero[NT], next_scale[NT], next_zero[NT];
+    auto load_scales = [&](int at) {
+        const uint32_t k = static_cast<uint32_t>(first) * kChunk + static_cast<uint32_t>(4 * at + g) * (kChunk / S);
+        const uint32_t of = k / static_cast<uint32_t>(p.group), most = static_cast<uint32_t>(columns) - 1;
+        const uint32_t column = of < most ? of : most;
 #pragma unroll
-        for (int q = 0; q < S; ++q) {
-            const int64_t k = k0 + q * (kChunk / S), last_k = p.k - 1;
-            const int64_t at_group = static_cast<int64_t>(static_cast<uint32_t>(k < last_k ? k : last_k) / static_cast<uint32_t>(p.group));
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                s.scale[j][q] = load_value(p.scales, scale_row[j] + at_group, p.scale_dtype);
-                s.zero[j][q] = p.zeros ? load_value(p.zeros, scale_row[j] + at_group, p.scale_dtype) : 8.0f;
-            }
+        for (int j = 0; j < NT; ++j) {
+            next_scale[j] = load_value(p.scales, scale_row[j] + column, p.scale_dtype);
+            next_zero[j] = p.zeros ? load_value(p.zeros, scale_row[j] + column, p.scale_dtype) : 8.0f;
         }
     };
     f32x4 y[NT][MT] = {};
     constexpr uint32_t kOne = DT == kF16 ? 0x3c003c00u : 0x3f803f80u;
     const u32x4 ones{kOne, kOne, kOne, kOne};
-    auto compute = [&](Step& s) {
+    auto compute = [&](Step& s, int at) {
+        const int of = (at - first) * S;   // the step's first group of columns in the run
+        if (of % 4 == 0) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                scale[j] = next_scale[j];
+                zero[j] = next_zero[j];
+            }
+            if (at + 4 / S < last) load_scales(of / 4 + 1);
+        }
         f32x4 sum[S][NT][MT] = {}, plain[S][MT] = {};
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             uint32_t c0 = s.c[j][0], c1 = s.c[j][1], c2 = s.c[j][2], c3 = s.c[j][3];
-            if constexpr (S >= 2) {
-                swap32(c0, c2);
-                swap32(c1, c3);
-            }
-            if constexpr (S == 4) {
-                swap16(c0, c1);
-                swap16(c2, c3);
-            }
+            swap32(c0, c2);
+            swap32(c1, c3);
+            swap16(c0, c1);
+            swap16(c2, c3);
             s.c[j] = u32x4{c0, c1, c2, c3};
         }
 #pragma unroll
@@ -315,16 +317,21 @@ __global__ __launch_bounds__(kWave * W) void k_int4_matmul(Int4Args p)
             }
         }
 #pragma unroll
-        for (int q = 0; q < S; ++q)
+        for (int q = 0; q < S; ++q) {
+            const int from = ((of + q) & 3) * 64 + r * 4;   // the lane that has them
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
+            for (int j = 0; j < NT; ++j) {
+                const float sc = __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(from, __builtin_bit_cast(int, scale[j])));
+                const float ze = __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(from, __builtin_bit_cast(int, zero[j])));
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        y[j][i][e] = __builtin_fmaf(s.scale[j][q], __builtin_fmaf(-s.zero[j][q], plain[q][i][e], sum[q][j][i][e]),
-                                                    y[j][i][e]);
+                        y[j][i][e] = __builtin_fmaf(sc, __builtin_fmaf(-ze, plain[q][i][e], sum[q][j][i][e]), y[j][i][e]);
+            }
+        }
     };
+    if (first < last) load_scales(0);
 #pragma unroll
     for (int u = 0; u < U; ++u)
         if (first + u < last) load(step[u], first + u);
@@ -332,7 +339,7 @@ __global__ __launch_bounds__(kWave * W) void k_int4_matmul(Int4Args p)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (at + u >= last) break;
-            compute(step[u]);
+            compute(step[u], at + u);
             if (at + u + U < last) load(step[u], at + u + U);
         }
     }
