@@ -74,6 +74,7 @@ struct Int4Args {
     int64_t m, n, k, x_stride, out_stride;
     int32_t group, experts, zero_rest, out_dtype, scale_dtype;
     int32_t x_wide;         // 16-byte loads of x are allowed
+    int32_t tiles;          // of 16 rows of weights a block, where x is held
 };
 
 struct Int4QuantArgs {
@@ -101,13 +102,14 @@ const void* balance_kernel();
 const void* int4_quantize_kernel(int dtype);
 const void* int4_dequantize_kernel(int dtype);
 
-// `rows` x `cols` results a block of `waves` waves; scales: groups of columns
-// in 128 (1, 2 or 4); tiles: 16 columns of results a block, or more.
+// scales: groups of columns in 128 (1, 2 or 4); steps: of 128 columns in k.
+// held: a block takes `tiles` tiles of 16 columns of results, else one.
 struct Int4Kernel {
     const void* fn;
-    int rows, cols, waves;
+    int waves;
+    bool held;
 };
-Int4Kernel int4_matmul_kernel(int dtype, int scales, bool grouped, int tiles);
+Int4Kernel int4_matmul_kernel(int dtype, int scales, bool grouped, int64_t steps);
 
 constexpr int kTopkWaves = 4;          // of a block
 constexpr int kOrderThreads = 512;

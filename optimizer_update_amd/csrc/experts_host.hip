@@ -340,6 +340,9 @@ int check_weights(int64_t n, int64_t k, int32_t group, int scale_dtype)
 double code_bytes(double n, int64_t k) { return n * static_cast<double>(k) / 2; }
 double scale_bytes(double n, int64_t k, int32_t group, int bytes) { return n * static_cast<double>(k / group) * bytes; }
 
+// Blocks that a product is cut into where it is large enough.
+constexpr int64_t kInt4Blocks = 2048;
+
 int int4_product(int dtype, Int4Args& p, void* stream)
 {
     const bool grouped = p.offsets || p.experts;
@@ -359,13 +362,15 @@ int int4_product(int dtype, Int4Args& p, void* stream)
                            {"out", p.out, extent(p.m, p.n, p.out_stride, eo), static_cast<unsigned>(eo), true}};
     if (int st = check_buffers(bufs, 6)) return st;
     const int scales = p.group % 128 == 0 ? 1 : p.group % 64 == 0 ? 2 : 4;
-    const int64_t few = grouped ? (p.m < p.experts ? p.m : p.experts) : 1;   // matrices that have rows, at most
-    const Int4Kernel f = int4_matmul_kernel(dtype, scales, grouped, cut(p.n, 16) * few <= 1024 ? 1 : 4);
+    const Int4Kernel f = int4_matmul_kernel(dtype, scales, grouped, cut(p.k, 128));
     p.x_wide = wide_rows(p.x, p.x_stride, 0, ex, 16);
     // by groups: two more, the rows in front of the first and behind the last
-    const int64_t units = grouped ? cut(p.m + (f.rows - 1) * static_cast<int64_t>(p.experts + 2), f.rows) : cut(p.m, f.rows);
+    const int64_t units = grouped ? cut(p.m + 15 * static_cast<int64_t>(p.experts + 2), 16) : cut(p.m, 16);
+    const int64_t few = grouped ? (p.m < p.experts ? p.m : p.experts) : units;   // units with rows, about
+    const int64_t tiles = cut(p.n, 16) * few / kInt4Blocks;
+    p.tiles = static_cast<int32_t>(!f.held || tiles < 1 ? 1 : tiles > 16 ? 16 : tiles);
     void* args[] = {&p};
-    return launch({f.fn, units * cut(p.n, f.cols), 1, kWave * f.waves, "k_int4_matmul", 0}, args, stream);
+    return launch({f.fn, units * cut(cut(p.n, 16), p.tiles), 1, kWave * f.waves, "k_int4_matmul", 0}, args, stream);
 }
 
 }  // namespace
@@ -425,7 +430,7 @@ OU_EXPORT int ou_int4_matmul(int dtype, const void* x, int64_t m, int64_t x_stri
                              int scale_dtype, const void* scales, const void* zeros, int64_t n, int64_t k, int32_t group,
                              void* out, int64_t out_stride, void* stream)
 {
-    Int4Args p{x, codes, scales, zeros, out, nullptr, m, n, k, x_stride, out_stride, group, 0, 0, out_dtype, scale_dtype, 0};
+    Int4Args p{x, codes, scales, zeros, out, nullptr, m, n, k, x_stride, out_stride, group, 0, 0, out_dtype, scale_dtype, 0, 1};
     return int4_product(dtype, p, stream);
 }
 
@@ -436,7 +441,7 @@ OU_EXPORT int ou_int4_grouped_matmul(int dtype, const void* x, int64_t m, int64_
 {
     if (int st = check_groups(offsets, experts, m)) return st;
     Int4Args p{x, codes, scales, zeros, out, offsets, m, n, k, x_stride, out_stride, group, experts, zero_rest != 0, out_dtype,
-               scale_dtype, 0};
+               scale_dtype, 0, 1};
     return int4_product(dtype, p, stream);
 }
 

@@ -97,28 +97,24 @@ using f32x4 = float __attribute__((ext_vector_type(4)));
 
 constexpr int kChunk = 128;   // columns of a step: 16 bytes of codes a lane
 
-// Eight codes (low four bits first) as values of the matrix instruction's type.
+// Eight codes as values of the matrix instruction's type, in the order 0, 2, 4,
+// 6, 1, 3, 5, 7.  A byte of 0 .. 15 is an 8-bit float (e4m3) of so many times
+// 2^-9, subnormal numbers and the first binade being in line, and the converter
+// multiplies by 2^9: seven instructions, fifteen by way of binary32.
 template <int DT>
 __device__ __forceinline__ u32x4 code_values(uint32_t c)
 {
-    u32x4 r;
-    if constexpr (DT == kF16) {
-        // 1024 + code by its bits, two values at a time: codes 0, 4, 1, 5, ..
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t b = (c >> (4 * i) & 0x000f000fu) | 0x64006400u;
-            const f16x2 v = __builtin_bit_cast(f16x2, b) - f16x2{1024, 1024};
-            r[i] = __builtin_bit_cast(uint32_t, v);
-        }
-    } else {
-        const uint32_t lo = c & 0x0f0f0f0fu, hi = c >> 4 & 0x0f0f0f0fu;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float a = static_cast<float>(lo >> (8 * i) & 0xffu), b = static_cast<float>(hi >> (8 * i) & 0xffu);
-            r[i] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, a), 0x07060302u);
-        }
-    }
-    return r;
+    const int lo = static_cast<int>(c & 0x0f0f0f0fu), hi = static_cast<int>(c >> 4 & 0x0f0f0f0fu);
+    if constexpr (DT == kF16)
+        return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 512.0f, false)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 512.0f, true)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.0f, false)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.0f, true))};
+    else
+        return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, false)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, true)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, false)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, true))};
 }
 
 // x's eight neighbouring values as operands: one, or three parts of binary32.
@@ -148,13 +144,17 @@ struct Rows8 {
                 w[0][i] = static_cast<uint32_t>(p[2 * i]) | static_cast<uint32_t>(p[2 * i + 1]) << 16;
         }
     }
+    // in the order of code_values()
+    static __device__ __forceinline__ u32x4 ordered(u32x4 w)
+    {
+        constexpr uint32_t kLow = 0x05040100u, kHigh = 0x07060302u;
+        return u32x4{__builtin_amdgcn_perm(w[1], w[0], kLow), __builtin_amdgcn_perm(w[3], w[2], kLow),
+                     __builtin_amdgcn_perm(w[1], w[0], kHigh), __builtin_amdgcn_perm(w[3], w[2], kHigh)};
+    }
     __device__ __forceinline__ void operands(u32x4* out) const
     {
-        if constexpr (DT == kBF16) {
-            out[0] = w[0];
-        } else if constexpr (DT == kF16) {   // in the order of code_values()
-            out[0] = u32x4{__builtin_amdgcn_perm(w[0][2], w[0][0], 0x05040100u), __builtin_amdgcn_perm(w[0][2], w[0][0], 0x07060302u),
-                           __builtin_amdgcn_perm(w[0][3], w[0][1], 0x05040100u), __builtin_amdgcn_perm(w[0][3], w[0][1], 0x07060302u)};
+        if constexpr (DT != kF32) {
+            out[0] = ordered(w[0]);
         } else {
             // eight bits of the fraction each, cut off: the rests are exact
 #pragma unroll
@@ -169,6 +169,8 @@ struct Rows8 {
                 out[1][i] = __builtin_amdgcn_perm(bm, am, 0x07060302u);
                 out[2][i] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, b2), __builtin_bit_cast(uint32_t, a2), 0x07060302u);
             }
+#pragma unroll
+            for (int h = 0; h < 3; ++h) out[h] = ordered(out[h]);
         }
     }
 };
@@ -263,15 +265,16 @@ __global__ __launch_bounds__(kWave * W) void k_int4_matmul(Int4Args p)
         }
     };
     // scale and zero of the group of columns `4 at + g` of the wave's run
-    float scale[NT], zero[NT], next_scale[NT], next_zero[NT];
+    float scale[NT], zero[NT];
+    uint32_t next_scale[NT], next_zero[NT];   // their bits
     auto load_scales = [&](int at) {
         const uint32_t k = static_cast<uint32_t>(first) * kChunk + static_cast<uint32_t>(4 * at + g) * (kChunk / S);
         const uint32_t of = k / static_cast<uint32_t>(p.group), most = static_cast<uint32_t>(columns) - 1;
         const uint32_t column = of < most ? of : most;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            next_scale[j] = load_value(p.scales, scale_row[j] + column, p.scale_dtype);
-            next_zero[j] = p.zeros ? load_value(p.zeros, scale_row[j] + column, p.scale_dtype) : 8.0f;
+            next_scale[j] = load_bits(p.scales, scale_row[j] + column, p.scale_dtype);
+            if (p.zeros) next_zero[j] = load_bits(p.zeros, scale_row[j] + column, p.scale_dtype);
         }
     };
     f32x4 y[NT][MT] = {};
@@ -282,8 +285,8 @@ __global__ __launch_bounds__(kWave * W) void k_int4_matmul(Int4Args p)
         if (of % 4 == 0) {
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                scale[j] = next_scale[j];
-                zero[j] = next_zero[j];
+                scale[j] = bits_value(next_scale[j], p.scale_dtype);
+                zero[j] = p.zeros ? bits_value(next_zero[j], p.scale_dtype) : 8.0f;
             }
             if (at + 4 / S < last) load_scales(of / 4 + 1);
         }
@@ -363,6 +366,164 @@ __global__ __launch_bounds__(kWave * W) void k_int4_matmul(Int4Args p)
     }
 }
 
+// The same with x held: a block takes 16 rows of x and `p.tiles` tiles of 16
+// rows of weights one after the other, its W waves RC steps each of the
+// columns, whose x they keep in registers; codes of the next two tiles are on
+// their way.  The waves' sums meet in LDS, and the waves take turns at adding
+// them up.
+template <int DT, int S, int W, int RC, bool GROUPED>
+__global__ __launch_bounds__(kWave * W) void k_int4_tiles(Int4Args p)
+{
+    constexpr int P = Rows8<DT>::kParts, D = 2, Q = RC * S / 4 > 0 ? RC * S / 4 : 1;   // Q: loads of scales a tile
+    using Elem = typename Value<DT>::Elem;
+    __shared__ f32x4 sums[2][W][kWave];
+    __shared__ f32x4 plain[W][RC * S][4];   // x's sums over a group of columns, four rows
+    const int t = static_cast<int>(threadIdx.x), lane = t & 63, r = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const uint32_t all_tiles = static_cast<uint32_t>((p.n + 15) / 16);
+    const uint32_t parts = (all_tiles + p.tiles - 1) / p.tiles, unit = blockIdx.x / parts, part = blockIdx.x - unit * parts;
+    int64_t row0 = static_cast<int64_t>(unit) * 16, mrows = p.m - row0, matrix = 0;
+    if constexpr (GROUPED) {
+        const groups::Place at = groups::Groups(p.offsets, p.experts, p.m, 16).locate(unit);
+        row0 = at.row;
+        mrows = at.rows;
+        matrix = at.group;
+        if (mrows <= 0) return;
+        if (matrix < 0 && !p.zero_rest) return;
+    }
+    const int rows = mrows < 16 ? static_cast<int>(mrows) : 16;
+    const int tile0 = static_cast<int>(part * p.tiles), left = static_cast<int>(all_tiles) - tile0;
+    const int tiles = left < p.tiles ? left : p.tiles;
+    const uint32_t columns = static_cast<uint32_t>(p.k / p.group);
+    const int chunks = GROUPED && matrix < 0 ? 0 : static_cast<int>((p.k + kChunk - 1) / kChunk);
+    const int run = (chunks + W - 1) / W, first = wave * run, count = first + run < chunks ? run : chunks - first;   // may be below 0
+    const uint8_t* const codes = p.codes + (GROUPED && matrix > 0 ? matrix : 0) * p.n * (p.k / 2) + static_cast<int64_t>(first) * (kChunk / 2);
+    const int scale_bytes = p.scale_dtype == kF32 ? 4 : 2;
+    const uint8_t *const scales = static_cast<const uint8_t*>(p.scales), *const zeros = static_cast<const uint8_t*>(p.zeros);
+    const int64_t scale0 = (GROUPED && matrix > 0 ? matrix : 0) * p.n * columns;
+    uint32_t column[Q];   // the group of columns whose scale the lane loads
+#pragma unroll
+    for (int i = 0; i < Q; ++i) {
+        const uint32_t of = (static_cast<uint32_t>(first < 0 ? 0 : first) * kChunk + static_cast<uint32_t>(4 * i + g) * (kChunk / S)) / static_cast<uint32_t>(p.group);
+        column[i] = of < columns ? of : columns - 1;
+    }
+    bool inside[RC];   // the lane's codes of a step
+#pragma unroll
+    for (int c = 0; c < RC; ++c) inside[c] = c < count && static_cast<int64_t>(first + c) * kChunk + g * 32 < p.k;
+
+    struct Tile {
+        u32x4 c[RC];
+        uint32_t scale[Q], zero[Q];   // their bits
+    } tile[D];
+    const uint32_t row_bytes = static_cast<uint32_t>(p.k / 2);
+    auto load = [&](Tile& s, int at) {
+        const int64_t n = static_cast<int64_t>(tile0 + at) * 16;
+        const int64_t behind = p.n - 1 - n;   // rows behind the edge read the last one
+        const uint32_t rr = r < behind ? r : static_cast<uint32_t>(behind);
+        const uint8_t* const from = codes + n * row_bytes;   // uniform: the lanes' offsets fit 32 bits
+        const uint32_t offset = rr * row_bytes + g * 16;
+#pragma unroll
+        for (int c = 0; c < RC; ++c)
+            s.c[c] = inside[c] ? __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(from + offset + c * (kChunk / 2))) : u32x4{0, 0, 0, 0};
+        if (count <= 0) return;
+        const int64_t base = scale0 + n * columns;
+        const uint32_t of = rr * columns;
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+            s.scale[i] = load_bits(scales + base * scale_bytes, of + column[i], p.scale_dtype);
+            if (p.zeros) s.zero[i] = load_bits(zeros + base * scale_bytes, of + column[i], p.scale_dtype);
+        }
+    };
+#pragma unroll
+    for (int u = 0; u < D; ++u)
+        if (u < tiles) load(tile[u], u);
+
+    u32x4 a[RC][4][P];
+    constexpr uint32_t kOne = DT == kF16 ? 0x3c003c00u : 0x3f803f80u;
+    const u32x4 ones{kOne, kOne, kOne, kOne};
+    const Elem* const x = static_cast<const Elem*>(p.x) + (row0 + (r < rows ? r : 0)) * p.x_stride + static_cast<int64_t>(first) * kChunk + g * 8;
+#pragma unroll
+    for (int c = 0; c < RC; ++c) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            Rows8<DT> v;
+            v.zero();
+            if (r < rows && c < count && static_cast<int64_t>(first + c) * kChunk + q * 32 < p.k) v.load(x + c * kChunk + q * 32, p.x_wide);
+            v.operands(a[c][q]);
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < RC; ++c) {
+        f32x4 sum[S] = {};
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int h = 0; h < P; ++h) sum[q * S / 4] = multiply<DT>(a[c][q][h], ones, sum[q * S / 4]);
+        if (r == 0) {
+#pragma unroll
+            for (int q = 0; q < S; ++q) plain[wave][c * S + q][g] = sum[q];
+        }
+    }
+    __syncthreads();
+
+    auto compute = [&](Tile& s, int at) {
+        f32x4 y{0, 0, 0, 0};
+        float scale[Q], zero[Q];
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+            scale[i] = bits_value(s.scale[i], p.scale_dtype);
+            zero[i] = p.zeros ? bits_value(s.zero[i], p.scale_dtype) : 8.0f;
+        }
+#pragma unroll
+        for (int c = 0; c < RC; ++c) {
+            if (c >= count) break;
+            uint32_t c0 = s.c[c][0], c1 = s.c[c][1], c2 = s.c[c][2], c3 = s.c[c][3];
+            swap32(c0, c2);
+            swap32(c1, c3);
+            swap16(c0, c1);
+            swap16(c2, c3);
+            const uint32_t word[4] = {c0, c1, c2, c3};
+            f32x4 sum[S] = {};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const u32x4 b = code_values<DT>(word[q]);
+#pragma unroll
+                for (int h = 0; h < P; ++h) sum[q * S / 4] = multiply<DT>(a[c][q][h], b, sum[q * S / 4]);
+            }
+#pragma unroll
+            for (int q = 0; q < S; ++q) {
+                const int i = c * S + q, from = (i & 3) * 64 + r * 4;   // the lane that has the scale
+                const float sc = __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(from, __builtin_bit_cast(int, scale[i / 4])));
+                const float ze = __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(from, __builtin_bit_cast(int, zero[i / 4])));
+                const f32x4 xs = plain[wave][i][g];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(sc, __builtin_fmaf(-ze, xs[e], sum[q][e]), y[e]);
+            }
+        }
+        sums[at & 1][wave][lane] = y;
+        __syncthreads();   // the tile before the last one was added up before its wave came here
+        if (at % W != wave) return;
+        f32x4 v = sums[at & 1][0][lane];
+#pragma unroll
+        for (int w = 1; w < W; ++w) v += sums[at & 1][w][lane];
+        const int64_t n = static_cast<int64_t>(tile0 + at) * 16 + r;
+        if (n >= p.n) return;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int row = g * 4 + e;
+            if (row < rows) store_value(p.out, (row0 + row) * p.out_stride + n, v[e], p.out_dtype);
+        }
+    };
+    for (int at = 0; at < tiles; at += D) {
+#pragma unroll
+        for (int u = 0; u < D; ++u) {
+            if (at + u >= tiles) break;
+            compute(tile[u], at + u);
+            if (at + u + D < tiles) load(tile[u], at + u + D);
+        }
+    }
+}
+
 }  // namespace
 
 const void* int4_quantize_kernel(int dtype)
@@ -380,33 +541,38 @@ const void* int4_dequantize_kernel(int dtype)
 
 namespace {
 
+// Steps of a wave whose x is held: 64 or 96 registers of it.
+template <int DT>
+constexpr int kHeldSteps = DT == kF32 ? 2 : 4;
+
 template <int DT, int S, bool GROUPED>
-Int4Kernel choose_tile(int tiles)
+Int4Kernel choose_waves(int64_t steps)
 {
-    constexpr int U = DT == kF32 ? 2 : 4;
-    if (tiles == 1) return {reinterpret_cast<const void*>(k_int4_matmul<DT, S, 1, 1, 8, U, GROUPED>), 16, 16, 8};
-    return {reinterpret_cast<const void*>(k_int4_matmul<DT, S, 4, 1, 4, 2, GROUPED>), 16, 64, 4};
+    constexpr int RC = kHeldSteps<DT>, U = DT == kF32 ? 2 : 4;
+    if (steps <= 4 * RC) return {reinterpret_cast<const void*>(k_int4_tiles<DT, S, 4, RC, GROUPED>), 4, true};
+    if (steps <= 8 * RC) return {reinterpret_cast<const void*>(k_int4_tiles<DT, S, 8, RC, GROUPED>), 8, true};
+    return {reinterpret_cast<const void*>(k_int4_matmul<DT, S, 1, 1, 8, U, GROUPED>), 8, false};
 }
 template <int DT, int S>
-Int4Kernel choose_grouped(bool grouped, int tiles)
+Int4Kernel choose_grouped(bool grouped, int64_t steps)
 {
-    return grouped ? choose_tile<DT, S, true>(tiles) : choose_tile<DT, S, false>(tiles);
+    return grouped ? choose_waves<DT, S, true>(steps) : choose_waves<DT, S, false>(steps);
 }
 template <int DT>
-Int4Kernel choose_scales(int scales, bool grouped, int tiles)
+Int4Kernel choose_scales(int scales, bool grouped, int64_t steps)
 {
-    return scales == 1   ? choose_grouped<DT, 1>(grouped, tiles)
-           : scales == 2 ? choose_grouped<DT, 2>(grouped, tiles)
-                         : choose_grouped<DT, 4>(grouped, tiles);
+    return scales == 1   ? choose_grouped<DT, 1>(grouped, steps)
+           : scales == 2 ? choose_grouped<DT, 2>(grouped, steps)
+                         : choose_grouped<DT, 4>(grouped, steps);
 }
 
 }  // namespace
 
-Int4Kernel int4_matmul_kernel(int dtype, int scales, bool grouped, int tiles)
+Int4Kernel int4_matmul_kernel(int dtype, int scales, bool grouped, int64_t steps)
 {
-    return dtype == kF32   ? choose_scales<kF32>(scales, grouped, tiles)
-           : dtype == kF16 ? choose_scales<kF16>(scales, grouped, tiles)
-                           : choose_scales<kBF16>(scales, grouped, tiles);
+    return dtype == kF32   ? choose_scales<kF32>(scales, grouped, steps)
+           : dtype == kF16 ? choose_scales<kF16>(scales, grouped, steps)
+                           : choose_scales<kBF16>(scales, grouped, steps);
 }
 
 }  // namespace experts
