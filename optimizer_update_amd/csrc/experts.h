@@ -109,7 +109,7 @@ struct Int4Kernel {
     int waves;
     bool held;
 };
-Int4Kernel int4_matmul_kernel(int dtype, int scales, bool grouped, int64_t steps);
+Int4Kernel int4_matmul_kernel(int dtype, int scales, bool grouped, int64_t steps, int scale_bytes);
 
 constexpr int kTopkWaves = 4;          // of a block
 constexpr int kOrderThreads = 512;

@@ -362,7 +362,7 @@ int int4_product(int dtype, Int4Args& p, void* stream)
                            {"out", p.out, extent(p.m, p.n, p.out_stride, eo), static_cast<unsigned>(eo), true}};
     if (int st = check_buffers(bufs, 6)) return st;
     const int scales = p.group % 128 == 0 ? 1 : p.group % 64 == 0 ? 2 : 4;
-    const Int4Kernel f = int4_matmul_kernel(dtype, scales, grouped, cut(p.k, 128));
+    const Int4Kernel f = int4_matmul_kernel(dtype, scales, grouped, cut(p.k, 128), es);
     p.x_wide = wide_rows(p.x, p.x_stride, 0, ex, 16);
     // by groups: two more, the rows in front of the first and behind the last
     const int64_t units = grouped ? cut(p.m + 15 * static_cast<int64_t>(p.experts + 2), 16) : cut(p.m, 16);

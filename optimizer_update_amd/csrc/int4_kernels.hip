@@ -184,6 +184,14 @@ __device__ __forceinline__ f32x4 multiply(u32x4 a, u32x4 b, f32x4 c)
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
+// The block's barrier for LDS alone: loads from memory stay on their way.
+__device__ __forceinline__ void lds_barrier()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 __device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b)
 {
     const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
@@ -370,8 +378,11 @@ __global__ __launch_bounds__(kWave * W) void k_int4_matmul(Int4Args p)
 // rows of weights one after the other, its W waves RC steps each of the
 // columns, whose x they keep in registers; codes of the next two tiles are on
 // their way.  The waves' sums meet in LDS, and the waves take turns at adding
-// them up.
-template <int DT, int S, int W, int RC, bool GROUPED>
+// them up.  No load of the steady loop stands behind a condition (the type of
+// the scales is a parameter, what is not there is loaded from elsewhere): the
+// compiler could not tell how many are younger than the one that it waits for,
+// and would wait for all.  SB: bytes of a scale.
+template <int DT, int SB, int S, int W, int RC, bool GROUPED>
 __global__ __launch_bounds__(kWave * W) void k_int4_tiles(Int4Args p)
 {
     constexpr int P = Rows8<DT>::kParts, D = 2, Q = RC * S / 4 > 0 ? RC * S / 4 : 1;   // Q: loads of scales a tile
@@ -397,9 +408,9 @@ __global__ __launch_bounds__(kWave * W) void k_int4_tiles(Int4Args p)
     const uint32_t columns = static_cast<uint32_t>(p.k / p.group);
     const int chunks = GROUPED && matrix < 0 ? 0 : static_cast<int>((p.k + kChunk - 1) / kChunk);
     const int run = (chunks + W - 1) / W, first = wave * run, count = first + run < chunks ? run : chunks - first;   // may be below 0
-    const uint8_t* const codes = p.codes + (GROUPED && matrix > 0 ? matrix : 0) * p.n * (p.k / 2) + static_cast<int64_t>(first) * (kChunk / 2);
-    const int scale_bytes = p.scale_dtype == kF32 ? 4 : 2;
-    const uint8_t *const scales = static_cast<const uint8_t*>(p.scales), *const zeros = static_cast<const uint8_t*>(p.zeros);
+    const uint8_t* const codes = p.codes + (GROUPED && matrix > 0 ? matrix : 0) * p.n * (p.k / 2);
+    using Bits = std::conditional_t<SB == 4, uint32_t, uint16_t>;
+    const Bits *const scales = static_cast<const Bits*>(p.scales), *const zeros = static_cast<const Bits*>(p.zeros ? p.zeros : p.scales);
     const int64_t scale0 = (GROUPED && matrix > 0 ? matrix : 0) * p.n * columns;
     uint32_t column[Q];   // the group of columns whose scale the lane loads
 #pragma unroll
@@ -407,9 +418,13 @@ __global__ __launch_bounds__(kWave * W) void k_int4_tiles(Int4Args p)
         const uint32_t of = (static_cast<uint32_t>(first < 0 ? 0 : first) * kChunk + static_cast<uint32_t>(4 * i + g) * (kChunk / S)) / static_cast<uint32_t>(p.group);
         column[i] = of < columns ? of : columns - 1;
     }
-    bool inside[RC];   // the lane's codes of a step
+    // where the lane's codes of a step are; the row's first where there are none (x is 0 there)
+    uint32_t place[RC];
 #pragma unroll
-    for (int c = 0; c < RC; ++c) inside[c] = c < count && static_cast<int64_t>(first + c) * kChunk + g * 32 < p.k;
+    for (int c = 0; c < RC; ++c) {
+        const bool inside = c < count && static_cast<int64_t>(first + c) * kChunk + g * 32 < p.k;
+        place[c] = inside ? (static_cast<uint32_t>(first + c) * kChunk + g * 32) / 2 : 0;
+    }
 
     struct Tile {
         u32x4 c[RC];
@@ -421,22 +436,20 @@ __global__ __launch_bounds__(kWave * W) void k_int4_tiles(Int4Args p)
         const int64_t behind = p.n - 1 - n;   // rows behind the edge read the last one
         const uint32_t rr = r < behind ? r : static_cast<uint32_t>(behind);
         const uint8_t* const from = codes + n * row_bytes;   // uniform: the lanes' offsets fit 32 bits
-        const uint32_t offset = rr * row_bytes + g * 16;
 #pragma unroll
         for (int c = 0; c < RC; ++c)
-            s.c[c] = inside[c] ? __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(from + offset + c * (kChunk / 2))) : u32x4{0, 0, 0, 0};
-        if (count <= 0) return;
+            s.c[c] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(from + (rr * row_bytes + place[c])));
         const int64_t base = scale0 + n * columns;
-        const uint32_t of = rr * columns;
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
-            s.scale[i] = load_bits(scales + base * scale_bytes, of + column[i], p.scale_dtype);
-            if (p.zeros) s.zero[i] = load_bits(zeros + base * scale_bytes, of + column[i], p.scale_dtype);
+            s.scale[i] = scales[base + (rr * columns + column[i])];
+            s.zero[i] = zeros[base + (rr * columns + column[i])];
         }
     };
+    const bool some = p.k > 0;
 #pragma unroll
     for (int u = 0; u < D; ++u)
-        if (u < tiles) load(tile[u], u);
+        if (some && u < tiles) load(tile[u], u);
 
     u32x4 a[RC][4][P];
     constexpr uint32_t kOne = DT == kF16 ? 0x3c003c00u : 0x3f803f80u;
@@ -464,7 +477,7 @@ __global__ __launch_bounds__(kWave * W) void k_int4_tiles(Int4Args p)
             for (int q = 0; q < S; ++q) plain[wave][c * S + q][g] = sum[q];
         }
     }
-    __syncthreads();
+    lds_barrier();
 
     auto compute = [&](Tile& s, int at) {
         f32x4 y{0, 0, 0, 0};
@@ -501,7 +514,7 @@ __global__ __launch_bounds__(kWave * W) void k_int4_tiles(Int4Args p)
             }
         }
         sums[at & 1][wave][lane] = y;
-        __syncthreads();   // the tile before the last one was added up before its wave came here
+        lds_barrier();   // the tile before the last one was added up before its wave came here
         if (at % W != wave) return;
         f32x4 v = sums[at & 1][0][lane];
 #pragma unroll
@@ -514,12 +527,20 @@ __global__ __launch_bounds__(kWave * W) void k_int4_tiles(Int4Args p)
             if (row < rows) store_value(p.out, (row0 + row) * p.out_stride + n, v[e], p.out_dtype);
         }
     };
-    for (int at = 0; at < tiles; at += D) {
+    int at = 0;
+    for (; at + 2 * D <= tiles && some; at += D) {
+#pragma unroll
+        for (int u = 0; u < D; ++u) {
+            compute(tile[u], at + u);
+            load(tile[u], at + u + D);
+        }
+    }
+    for (; at < tiles; at += D) {
 #pragma unroll
         for (int u = 0; u < D; ++u) {
             if (at + u >= tiles) break;
             compute(tile[u], at + u);
-            if (at + u + D < tiles) load(tile[u], at + u + D);
+            if (some && at + u + D < tiles) load(tile[u], at + u + D);
         }
     }
 }
@@ -545,34 +566,40 @@ namespace {
 template <int DT>
 constexpr int kHeldSteps = DT == kF32 ? 2 : 4;
 
-template <int DT, int S, bool GROUPED>
-Int4Kernel choose_waves(int64_t steps)
+template <int DT, int SB, int S, bool GROUPED>
+Int4Kernel choose_tiles(int64_t steps)
 {
-    constexpr int RC = kHeldSteps<DT>, U = DT == kF32 ? 2 : 4;
-    if (steps <= 4 * RC) return {reinterpret_cast<const void*>(k_int4_tiles<DT, S, 4, RC, GROUPED>), 4, true};
-    if (steps <= 8 * RC) return {reinterpret_cast<const void*>(k_int4_tiles<DT, S, 8, RC, GROUPED>), 8, true};
+    constexpr int RC = kHeldSteps<DT>;
+    if (steps <= 4 * RC) return {reinterpret_cast<const void*>(k_int4_tiles<DT, SB, S, 4, RC, GROUPED>), 4, true};
+    return {reinterpret_cast<const void*>(k_int4_tiles<DT, SB, S, 8, RC, GROUPED>), 8, true};
+}
+template <int DT, int S, bool GROUPED>
+Int4Kernel choose_waves(int64_t steps, int scale_bytes)
+{
+    constexpr int U = DT == kF32 ? 2 : 4;
+    if (steps <= 8 * kHeldSteps<DT>) return scale_bytes == 4 ? choose_tiles<DT, 4, S, GROUPED>(steps) : choose_tiles<DT, 2, S, GROUPED>(steps);
     return {reinterpret_cast<const void*>(k_int4_matmul<DT, S, 1, 1, 8, U, GROUPED>), 8, false};
 }
 template <int DT, int S>
-Int4Kernel choose_grouped(bool grouped, int64_t steps)
+Int4Kernel choose_grouped(bool grouped, int64_t steps, int scale_bytes)
 {
-    return grouped ? choose_waves<DT, S, true>(steps) : choose_waves<DT, S, false>(steps);
+    return grouped ? choose_waves<DT, S, true>(steps, scale_bytes) : choose_waves<DT, S, false>(steps, scale_bytes);
 }
 template <int DT>
-Int4Kernel choose_scales(int scales, bool grouped, int64_t steps)
+Int4Kernel choose_scales(int scales, bool grouped, int64_t steps, int scale_bytes)
 {
-    return scales == 1   ? choose_grouped<DT, 1>(grouped, steps)
-           : scales == 2 ? choose_grouped<DT, 2>(grouped, steps)
-                         : choose_grouped<DT, 4>(grouped, steps);
+    return scales == 1   ? choose_grouped<DT, 1>(grouped, steps, scale_bytes)
+           : scales == 2 ? choose_grouped<DT, 2>(grouped, steps, scale_bytes)
+                         : choose_grouped<DT, 4>(grouped, steps, scale_bytes);
 }
 
 }  // namespace
 
-Int4Kernel int4_matmul_kernel(int dtype, int scales, bool grouped, int64_t steps)
+Int4Kernel int4_matmul_kernel(int dtype, int scales, bool grouped, int64_t steps, int scale_bytes)
 {
-    return dtype == kF32   ? choose_scales<kF32>(scales, grouped, steps)
-           : dtype == kF16 ? choose_scales<kF16>(scales, grouped, steps)
-                           : choose_scales<kBF16>(scales, grouped, steps);
+    return dtype == kF32   ? choose_scales<kF32>(scales, grouped, steps, scale_bytes)
+           : dtype == kF16 ? choose_scales<kF16>(scales, grouped, steps, scale_bytes)
+                           : choose_scales<kBF16>(scales, grouped, steps, scale_bytes);
 }
 
 }  // namespace experts
