@@ -381,14 +381,19 @@ __global__ __launch_bounds__(kWave * W) void k_int4_matmul(Int4Args p)
 // them up.  No load of the steady loop stands behind a condition (the type of
 // the scales is a parameter, what is not there is loaded from elsewhere): the
 // compiler could not tell how many are younger than the one that it waits for,
-// and would wait for all.  SB: bytes of a scale.
+// and would wait for all.  The waves load the scales of 16 / W rows each, whole
+// rows of them, and share them through LDS: when each loaded what it multiplies,
+// they were 16 requests like the codes' own (21 us of 75 without any
+// arithmetic).  SB: bytes of a scale.
 template <int DT, int SB, int S, int W, int RC, bool GROUPED>
 __global__ __launch_bounds__(kWave * W) void k_int4_tiles(Int4Args p)
 {
-    constexpr int P = Rows8<DT>::kParts, D = 2, Q = RC * S / 4 > 0 ? RC * S / 4 : 1;   // Q: loads of scales a tile
+    constexpr int P = Rows8<DT>::kParts, D = 2, kUnits = W * RC * S;   // kUnits: groups of columns, at most
+    constexpr int Q = kUnits * 16 / W / kWave > 0 ? kUnits * 16 / W / kWave : 1;   // loads of scales a lane and tile
     using Elem = typename Value<DT>::Elem;
     __shared__ f32x4 sums[2][W][kWave];
     __shared__ f32x4 plain[W][RC * S][4];   // x's sums over a group of columns, four rows
+    __shared__ float2 scaling[2][16][kUnits + 1];   // scale and zero
     const int t = static_cast<int>(threadIdx.x), lane = t & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const uint32_t all_tiles = static_cast<uint32_t>((p.n + 15) / 16);
@@ -412,11 +417,15 @@ __global__ __launch_bounds__(kWave * W) void k_int4_tiles(Int4Args p)
     using Bits = std::conditional_t<SB == 4, uint32_t, uint16_t>;
     const Bits *const scales = static_cast<const Bits*>(p.scales), *const zeros = static_cast<const Bits*>(p.zeros ? p.zeros : p.scales);
     const int64_t scale0 = (GROUPED && matrix > 0 ? matrix : 0) * p.n * columns;
-    uint32_t column[Q];   // the group of columns whose scale the lane loads
+    // the scales that the lane loads: rows wave * 16 / W .., all groups of columns
+    uint32_t scale_at[Q], scale_row[Q], scale_unit[Q];
 #pragma unroll
     for (int i = 0; i < Q; ++i) {
-        const uint32_t of = (static_cast<uint32_t>(first < 0 ? 0 : first) * kChunk + static_cast<uint32_t>(4 * i + g) * (kChunk / S)) / static_cast<uint32_t>(p.group);
-        column[i] = of < columns ? of : columns - 1;
+        const uint32_t f = (i * kWave + lane) % (kUnits * 16 / W);
+        scale_row[i] = wave * (16 / W) + f / kUnits;
+        scale_unit[i] = f % kUnits;
+        const uint32_t of = scale_unit[i] * (kChunk / S) / static_cast<uint32_t>(p.group);
+        scale_at[i] = of < columns ? of : columns - 1;
     }
     // where the lane's codes of a step are; the row's first where there are none (x is 0 there)
     uint32_t place[RC];
@@ -442,9 +451,17 @@ __global__ __launch_bounds__(kWave * W) void k_int4_tiles(Int4Args p)
         const int64_t base = scale0 + n * columns;
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
-            s.scale[i] = scales[base + (rr * columns + column[i])];
-            s.zero[i] = zeros[base + (rr * columns + column[i])];
+            const uint32_t of = (scale_row[i] < behind ? scale_row[i] : static_cast<uint32_t>(behind)) * columns + scale_at[i];
+            s.scale[i] = scales[base + of];
+            s.zero[i] = zeros[base + of];
         }
+    };
+    // a tile's scales to LDS, ahead of a barrier
+    auto share = [&](const Tile& s, int at) {
+#pragma unroll
+        for (int i = 0; i < Q; ++i)
+            scaling[at & 1][scale_row[i]][scale_unit[i]] =
+                float2{bits_value(s.scale[i], p.scale_dtype), p.zeros ? bits_value(s.zero[i], p.scale_dtype) : 8.0f};
     };
     const bool some = p.k > 0;
 #pragma unroll
@@ -477,16 +494,11 @@ __global__ __launch_bounds__(kWave * W) void k_int4_tiles(Int4Args p)
             for (int q = 0; q < S; ++q) plain[wave][c * S + q][g] = sum[q];
         }
     }
+    if (some) share(tile[0], 0);
     lds_barrier();
 
-    auto compute = [&](Tile& s, int at) {
+    auto compute = [&](Tile& s, const Tile& then, int at) {
         f32x4 y{0, 0, 0, 0};
-        float scale[Q], zero[Q];
-#pragma unroll
-        for (int i = 0; i < Q; ++i) {
-            scale[i] = bits_value(s.scale[i], p.scale_dtype);
-            zero[i] = p.zeros ? bits_value(s.zero[i], p.scale_dtype) : 8.0f;
-        }
 #pragma unroll
         for (int c = 0; c < RC; ++c) {
             if (c >= count) break;
@@ -505,15 +517,15 @@ __global__ __launch_bounds__(kWave * W) void k_int4_tiles(Int4Args p)
             }
 #pragma unroll
             for (int q = 0; q < S; ++q) {
-                const int i = c * S + q, from = (i & 3) * 64 + r * 4;   // the lane that has the scale
-                const float sc = __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(from, __builtin_bit_cast(int, scale[i / 4])));
-                const float ze = __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(from, __builtin_bit_cast(int, zero[i / 4])));
+                const int i = c * S + q;
+                const float2 w = scaling[at & 1][r][first * S + i];
                 const f32x4 xs = plain[wave][i][g];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(sc, __builtin_fmaf(-ze, xs[e], sum[q][e]), y[e]);
+                for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(w.x, __builtin_fmaf(-w.y, xs[e], sum[q][e]), y[e]);
             }
         }
         sums[at & 1][wave][lane] = y;
+        if (some && at + 1 < tiles) share(then, at + 1);
         lds_barrier();   // the tile before the last one was added up before its wave came here
         if (at % W != wave) return;
         f32x4 v = sums[at & 1][0][lane];
@@ -531,7 +543,7 @@ __global__ __launch_bounds__(kWave * W) void k_int4_tiles(Int4Args p)
     for (; at + 2 * D <= tiles && some; at += D) {
 #pragma unroll
         for (int u = 0; u < D; ++u) {
-            compute(tile[u], at + u);
+            compute(tile[u], tile[(u + 1) % D], at + u);
             load(tile[u], at + u + D);
         }
     }
@@ -539,7 +551,7 @@ __global__ __launch_bounds__(kWave * W) void k_int4_tiles(Int4Args p)
 #pragma unroll
         for (int u = 0; u < D; ++u) {
             if (at + u >= tiles) break;
-            compute(tile[u], at + u);
+            compute(tile[u], tile[(u + 1) % D], at + u);
             if (some && at + u + D < tiles) load(tile[u], at + u + D);
         }
     }

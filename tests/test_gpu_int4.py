@@ -92,6 +92,35 @@ def test_grouped_matmul(counts, n, k, group, dtype, zeros):
         _check(y[at[i]:at[i + 1]], want, size, k, dtype)
 
 
+# many tiles: more than one slab of columns, an odd edge, experts without rows and with more than a unit's
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("zeros", [True, False])
+@pytest.mark.parametrize("counts,n,k,group", [([3, 0, 17, 1] * 20, 2100, 512, 128), ([1] * 65, 2063, 2560, 64), ([9, 8, 7, 2] * 16, 2085, 2432, 32),
+                                              ([1, 2] * 36, 2051, 4608, 128)])
+def test_grouped_matmul_of_many_tiles(counts, n, k, group, dtype, zeros):
+    print("int4 many tiles", len(counts), n, k, group, dtype, zeros, flush=True)
+    e, front, behind = len(counts), 2, 19
+    m = front + sum(counts) + behind
+    q = _weights((e, n), k, group, DTYPES[(n + k // 128) % 3], zeros)
+    x = (torch.randn((m, k), generator=_gen(1)) * torch.exp2(torch.randn(k, generator=_gen(2)))).to(dtype)
+    at = front + np.concatenate([[0], np.cumsum(counts)])
+    y = ou.int4_grouped_matmul(x.cuda(), q, torch.tensor(at, dtype=torch.int32).cuda())
+    assert (y[:front] == 0).all() and (y[at[-1]:] == 0).all()
+    for i in (*range(0, e, 7), e - 1):
+        want, size = R.int4_product(R.host(x[at[i]:at[i + 1]]), q[i])
+        _check(y[at[i]:at[i + 1]], want, size, k, dtype)
+        one = ou.int4_matmul(x[at[i]:at[i + 1]].cuda(), q[i])
+        _check(one, want, size, k, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_matmul_of_many_tiles(dtype):
+    q = _weights((131077,), 512, 64, F16, True)
+    x = torch.randn((5, 512), generator=_gen(1)).to(dtype)
+    want, size = R.int4_product(R.host(x), q)
+    _check(ou.int4_matmul(x.cuda(), q), want, size, 512, dtype)
+
+
 def test_grouped_matmul_with_offsets_that_fall_or_leave():
     q = _weights((4, 24), 64, 64, F32, True)
     x = torch.randn((40, 64), generator=_gen(1)).cuda()
@@ -214,10 +243,11 @@ def test_captured_and_streams():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, ou.int4_matmul(x * (i + 1), q))
-    assert torch.equal(ou.int4_matmul(x, q, stream=s), want)
-    s.synchronize()
-    assert torch.equal(ou.int4_matmul(x, q, stream=s.cuda_stream), want)
-    s.synchronize()
+    torch.cuda.synchronize()
+    for stream in (s, s.cuda_stream):
+        y = ou.int4_matmul(x, q, stream=stream)
+        s.synchronize()   # what is compared on the current stream is done on the other one
+        assert torch.equal(y, want)
 
 
 def test_many_experts_past_32_bits():
