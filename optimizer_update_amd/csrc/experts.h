@@ -103,13 +103,14 @@ const void* int4_quantize_kernel(int dtype);
 const void* int4_dequantize_kernel(int dtype);
 
 // scales: groups of columns in 128 (1, 2 or 4); steps: of 128 columns in k.
-// held: a block takes `tiles` tiles of 16 columns of results, else one.
+// may_hold: scales have 16 bits, and tiles are many.  held: a block takes
+// `tiles` tiles of 16 columns of results, else one.
 struct Int4Kernel {
     const void* fn;
     int waves;
     bool held;
 };
-Int4Kernel int4_matmul_kernel(int dtype, int scales, bool grouped, int64_t steps, int scale_bytes);
+Int4Kernel int4_matmul_kernel(int dtype, int scales, bool grouped, int64_t steps, bool may_hold);
 
 constexpr int kTopkWaves = 4;          // of a block
 constexpr int kOrderThreads = 512;

@@ -340,8 +340,12 @@ int check_weights(int64_t n, int64_t k, int32_t group, int scale_dtype)
 double code_bytes(double n, int64_t k) { return n * static_cast<double>(k) / 2; }
 double scale_bytes(double n, int64_t k, int32_t group, int bytes) { return n * static_cast<double>(k / group) * bytes; }
 
-// Blocks that a product is cut into where it is large enough.
-constexpr int64_t kInt4Blocks = 2048;
+// From so many tiles of 16 rows of weights on x is held over runs of them, in
+// about so many blocks and up to 16 a run.  2001 tiles, k = 1024: 12.4 us by runs
+// of 4, 14.1 by 2, 15.8 by 8, 16.5 to 21 with x not held; 256 tiles, k = 4096: 7.4
+// us against 5.5; 512 rows, 64 experts, k = 2048: 80 by 8 or 16, 88 by 4.
+constexpr int64_t kInt4Held = 1024;
+constexpr int64_t kInt4Blocks = 640;
 
 int int4_product(int dtype, Int4Args& p, void* stream)
 {
@@ -362,13 +366,14 @@ int int4_product(int dtype, Int4Args& p, void* stream)
                            {"out", p.out, extent(p.m, p.n, p.out_stride, eo), static_cast<unsigned>(eo), true}};
     if (int st = check_buffers(bufs, 6)) return st;
     const int scales = p.group % 128 == 0 ? 1 : p.group % 64 == 0 ? 2 : 4;
-    const Int4Kernel f = int4_matmul_kernel(dtype, scales, grouped, cut(p.k, 128), es);
     p.x_wide = wide_rows(p.x, p.x_stride, 0, ex, 16);
     // by groups: two more, the rows in front of the first and behind the last
     const int64_t units = grouped ? cut(p.m + 15 * static_cast<int64_t>(p.experts + 2), 16) : cut(p.m, 16);
     const int64_t few = grouped ? (p.m < p.experts ? p.m : p.experts) : units;   // units with rows, about
-    const int64_t tiles = cut(p.n, 16) * few / kInt4Blocks;
-    p.tiles = static_cast<int32_t>(!f.held || tiles < 1 ? 1 : tiles > 16 ? 16 : tiles);
+    const int64_t tiles = cut(p.n, 16) * few;
+    const Int4Kernel f = int4_matmul_kernel(dtype, scales, grouped, cut(p.k, 128), es == 2 && tiles >= kInt4Held);
+    const int64_t run = cut(tiles, kInt4Blocks);
+    p.tiles = static_cast<int32_t>(!f.held ? 1 : run > 16 ? 16 : run);
     void* args[] = {&p};
     return launch({f.fn, units * cut(cut(p.n, 16), p.tiles), 1, kWave * f.waves, "k_int4_matmul", 0}, args, stream);
 }

@@ -205,141 +205,105 @@ __device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b)
     b = r[1];
 }
 
-// 16 NT rows of weights and 16 MT rows of x a block, the steps of 128 columns
-// dealt to its W waves in runs; U steps of a wave are in flight.  Lane group g
-// (of 16 lanes) loads columns 32 g .. of a step, one request of 64 bytes a row;
-// the groups then exchange registers so that register i of group g holds
-// columns 32 i + 8 g .., for two reasons: an instruction's 32 columns are of one
-// group of columns, and x is asked for by 64 bytes a row (as it would be by 16
-// where the codes were loaded).  S groups of columns are in a step: a lane group
-// loads the scale of one of four in a row, and a lane gets its row's from there.
-template <int DT, int S, int NT, int MT, int W, int U, bool GROUPED>
+// 16 rows of weights and 16 rows of x a block, the steps of 128 columns dealt to
+// its W waves in runs; U steps of a wave are in flight.  Lane group g (of 16
+// lanes) loads columns 32 g .. of a step, one request of 64 bytes a row; the
+// groups then exchange registers so that register i of group g holds columns
+// 32 i + 8 g .., for two reasons: an instruction's 32 columns are of one group of
+// columns, and x is asked for by 64 bytes a row (by 16 where the codes were
+// loaded).  S groups of columns are in a step: a lane group loads the scale of
+// one of four in a row, and a lane gets its row's from there.  For few tiles,
+// long rows, and scales in binary32.  One token, 4096 x 4096 bf16: 5.5 us, with
+// four steps in flight 5.9, with x held 7.4.
+template <int DT, int S, int W, int U, bool GROUPED>
 __global__ __launch_bounds__(kWave * W) void k_int4_matmul(Int4Args p)
 {
     constexpr int P = Rows8<DT>::kParts;
     using Elem = typename Value<DT>::Elem;
-    __shared__ f32x4 sums[W][NT * MT][kWave];
+    __shared__ f32x4 sums[W][kWave];
     const int t = static_cast<int>(threadIdx.x), lane = t & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-    const uint32_t n_tiles = static_cast<uint32_t>((p.n + 16 * NT - 1) / (16 * NT));
+    const uint32_t n_tiles = static_cast<uint32_t>((p.n + 15) / 16);
     const uint32_t unit = blockIdx.x / n_tiles, ntile = blockIdx.x - unit * n_tiles;
-    int64_t row0 = static_cast<int64_t>(unit) * (16 * MT), mrows = p.m - row0, matrix = 0;
+    int64_t row0 = static_cast<int64_t>(unit) * 16, mrows = p.m - row0, matrix = 0;
     if constexpr (GROUPED) {
-        const groups::Place at = groups::Groups(p.offsets, p.experts, p.m, 16 * MT).locate(unit);
+        const groups::Place at = groups::Groups(p.offsets, p.experts, p.m, 16).locate(unit);
         row0 = at.row;
         mrows = at.rows;
         matrix = at.group;
         if (mrows <= 0) return;
         if (matrix < 0 && !p.zero_rest) return;
     }
-    const int rows = mrows < 16 * MT ? static_cast<int>(mrows) : 16 * MT;
-    const int64_t n0 = static_cast<int64_t>(ntile) * (16 * NT), columns = p.k / p.group;
+    const int rows = mrows < 16 ? static_cast<int>(mrows) : 16;
+    const int64_t n0 = static_cast<int64_t>(ntile) * 16, columns = p.k / p.group;
     const int chunks = GROUPED && matrix < 0 ? 0 : static_cast<int>((p.k + kChunk - 1) / kChunk);
     const int run = (chunks + W - 1) / W, first = wave * run, last = first + run < chunks ? first + run : chunks;
-    const uint8_t* codes[NT];
-    int64_t scale_row[NT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        int64_t n = n0 + 16 * j + r;
-        n = (n < p.n ? n : p.n - 1) + (GROUPED && matrix > 0 ? matrix * p.n : 0);   // rows behind the edge read the last one
-        codes[j] = p.codes + n * (p.k / 2) + g * 16;
-        scale_row[j] = n * columns;
-    }
-    const Elem* x[MT];
-    bool live[MT];   // rows behind the last one are 0 and not loaded
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        live[i] = 16 * i + r < rows;
-        x[i] = static_cast<const Elem*>(p.x) + (row0 + (live[i] ? 16 * i + r : 0)) * p.x_stride + g * 8;
-    }
+    // rows behind the edge read the last one
+    const int64_t n = (n0 + r < p.n ? n0 + r : p.n - 1) + (GROUPED && matrix > 0 ? matrix * p.n : 0);
+    const uint8_t* const codes = p.codes + n * (p.k / 2) + g * 16;
+    const int64_t scale_row = n * columns;
+    const bool live = r < rows;   // rows behind the last one are 0 and not loaded
+    const Elem* const x = static_cast<const Elem*>(p.x) + (row0 + (live ? r : 0)) * p.x_stride + g * 8;
     struct Step {
-        u32x4 c[NT];
-        Rows8<DT> x[MT][4];
+        u32x4 c;
+        Rows8<DT> x[4];
     } step[U];
     auto load = [&](Step& s, int at) {
         const int64_t k0 = static_cast<int64_t>(at) * kChunk;
         const bool whole = k0 + kChunk <= p.k;
+        s.c = whole || k0 + g * 32 < p.k ? __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(codes + k0 / 2)) : u32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-            s.c[j] = whole || k0 + g * 32 < p.k ? __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(codes[j] + k0 / 2))
-                                                : u32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                s.x[i][q].zero();
-                if (live[i] && (whole || k0 + q * 32 < p.k)) s.x[i][q].load(x[i] + k0 + q * 32, p.x_wide);
-            }
+        for (int q = 0; q < 4; ++q) {
+            s.x[q].zero();
+            if (live && (whole || k0 + q * 32 < p.k)) s.x[q].load(x + k0 + q * 32, p.x_wide);
         }
     };
     // scale and zero of the group of columns `4 at + g` of the wave's run
-    float scale[NT], zero[NT];
-    uint32_t next_scale[NT], next_zero[NT];   // their bits
+    float scale = 0.0f, zero = 8.0f;
+    uint32_t next_scale = 0, next_zero = 0;   // their bits
     auto load_scales = [&](int at) {
         const uint32_t k = static_cast<uint32_t>(first) * kChunk + static_cast<uint32_t>(4 * at + g) * (kChunk / S);
         const uint32_t of = k / static_cast<uint32_t>(p.group), most = static_cast<uint32_t>(columns) - 1;
         const uint32_t column = of < most ? of : most;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            next_scale[j] = load_bits(p.scales, scale_row[j] + column, p.scale_dtype);
-            if (p.zeros) next_zero[j] = load_bits(p.zeros, scale_row[j] + column, p.scale_dtype);
-        }
+        next_scale = load_bits(p.scales, scale_row + column, p.scale_dtype);
+        if (p.zeros) next_zero = load_bits(p.zeros, scale_row + column, p.scale_dtype);
     };
-    f32x4 y[NT][MT] = {};
+    f32x4 y{0, 0, 0, 0};
     constexpr uint32_t kOne = DT == kF16 ? 0x3c003c00u : 0x3f803f80u;
     const u32x4 ones{kOne, kOne, kOne, kOne};
     auto compute = [&](Step& s, int at) {
         const int of = (at - first) * S;   // the step's first group of columns in the run
         if (of % 4 == 0) {
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                scale[j] = bits_value(next_scale[j], p.scale_dtype);
-                zero[j] = p.zeros ? bits_value(next_zero[j], p.scale_dtype) : 8.0f;
-            }
+            scale = bits_value(next_scale, p.scale_dtype);
+            zero = p.zeros ? bits_value(next_zero, p.scale_dtype) : 8.0f;
             if (at + 4 / S < last) load_scales(of / 4 + 1);
         }
-        f32x4 sum[S][NT][MT] = {}, plain[S][MT] = {};
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            uint32_t c0 = s.c[j][0], c1 = s.c[j][1], c2 = s.c[j][2], c3 = s.c[j][3];
-            swap32(c0, c2);
-            swap32(c1, c3);
-            swap16(c0, c1);
-            swap16(c2, c3);
-            s.c[j] = u32x4{c0, c1, c2, c3};
-        }
+        f32x4 sum[S] = {}, plain[S] = {};
+        uint32_t c0 = s.c[0], c1 = s.c[1], c2 = s.c[2], c3 = s.c[3];
+        swap32(c0, c2);
+        swap32(c1, c3);
+        swap16(c0, c1);
+        swap16(c2, c3);
+        const uint32_t word[4] = {c0, c1, c2, c3};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             constexpr int kPer = 4 / S;
-            u32x4 a[MT][P];
+            u32x4 a[P];
+            s.x[q].operands(a);
+            const u32x4 b = code_values<DT>(word[q]);
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                s.x[i][q].operands(a[i]);
-#pragma unroll
-                for (int h = 0; h < P; ++h) plain[q / kPer][i] = multiply<DT>(a[i][h], ones, plain[q / kPer][i]);
-            }
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const u32x4 b = code_values<DT>(s.c[j][q]);
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int h = 0; h < P; ++h) sum[q / kPer][j][i] = multiply<DT>(a[i][h], b, sum[q / kPer][j][i]);
+            for (int h = 0; h < P; ++h) {
+                plain[q / kPer] = multiply<DT>(a[h], ones, plain[q / kPer]);
+                sum[q / kPer] = multiply<DT>(a[h], b, sum[q / kPer]);
             }
         }
 #pragma unroll
         for (int q = 0; q < S; ++q) {
             const int from = ((of + q) & 3) * 64 + r * 4;   // the lane that has them
+            const float sc = __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(from, __builtin_bit_cast(int, scale)));
+            const float ze = __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(from, __builtin_bit_cast(int, zero)));
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const float sc = __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(from, __builtin_bit_cast(int, scale[j])));
-                const float ze = __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(from, __builtin_bit_cast(int, zero[j])));
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        y[j][i][e] = __builtin_fmaf(sc, __builtin_fmaf(-ze, plain[q][i][e], sum[q][j][i][e]), y[j][i][e]);
-            }
+            for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(sc, __builtin_fmaf(-ze, plain[q][e], sum[q][e]), y[e]);
         }
     };
     if (first < last) load_scales(0);
@@ -354,23 +318,16 @@ __global__ __launch_bounds__(kWave * W) void k_int4_matmul(Int4Args p)
             if (at + u + U < last) load(step[u], at + u + U);
         }
     }
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int i = 0; i < MT; ++i) sums[wave][j * MT + i][lane] = y[j][i];
+    sums[wave][lane] = y;
     __syncthreads();
-    for (int u = t; u < NT * MT * kWave; u += kWave * W) {
-        const int l = u & 63, tile = u >> 6, j = tile / MT, i = tile % MT;
-        f32x4 v = sums[0][tile][l];
+    if (wave) return;
 #pragma unroll
-        for (int w = 1; w < W; ++w) v += sums[w][tile][l];
-        const int64_t n = n0 + 16 * j + (l & 15);
-        if (n >= p.n) continue;
+    for (int w = 1; w < W; ++w) y += sums[w][lane];
+    if (n0 + r >= p.n) return;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int row = 16 * i + (l >> 4) * 4 + e;
-            if (row < rows) store_value(p.out, (row0 + row) * p.out_stride + n, v[e], p.out_dtype);
-        }
+    for (int e = 0; e < 4; ++e) {
+        const int row = g * 4 + e;
+        if (row < rows) store_value(p.out, (row0 + row) * p.out_stride + n0 + r, y[e], p.out_dtype);
     }
 }
 
@@ -379,13 +336,13 @@ __global__ __launch_bounds__(kWave * W) void k_int4_matmul(Int4Args p)
 // columns, whose x they keep in registers; codes of the next two tiles are on
 // their way.  The waves' sums meet in LDS, and the waves take turns at adding
 // them up.  No load of the steady loop stands behind a condition (the type of
-// the scales is a parameter, what is not there is loaded from elsewhere): the
+// the scales has 16 bits, what is not there is loaded from elsewhere): the
 // compiler could not tell how many are younger than the one that it waits for,
 // and would wait for all.  The waves load the scales of 16 / W rows each, whole
 // rows of them, and share them through LDS: when each loaded what it multiplies,
 // they were 16 requests like the codes' own (21 us of 75 without any
-// arithmetic).  SB: bytes of a scale.
-template <int DT, int SB, int S, int W, int RC, bool GROUPED>
+// arithmetic); they are asked for a tile ahead of the codes.
+template <int DT, int S, int W, int RC, bool GROUPED>
 __global__ __launch_bounds__(kWave * W) void k_int4_tiles(Int4Args p)
 {
     constexpr int P = Rows8<DT>::kParts, D = 2, kUnits = W * RC * S;   // kUnits: groups of columns, at most
@@ -414,8 +371,7 @@ __global__ __launch_bounds__(kWave * W) void k_int4_tiles(Int4Args p)
     const int chunks = GROUPED && matrix < 0 ? 0 : static_cast<int>((p.k + kChunk - 1) / kChunk);
     const int run = (chunks + W - 1) / W, first = wave * run, count = first + run < chunks ? run : chunks - first;   // may be below 0
     const uint8_t* const codes = p.codes + (GROUPED && matrix > 0 ? matrix : 0) * p.n * (p.k / 2);
-    using Bits = std::conditional_t<SB == 4, uint32_t, uint16_t>;
-    const Bits *const scales = static_cast<const Bits*>(p.scales), *const zeros = static_cast<const Bits*>(p.zeros ? p.zeros : p.scales);
+    const uint16_t *const scales = static_cast<const uint16_t*>(p.scales), *const zeros = static_cast<const uint16_t*>(p.zeros ? p.zeros : p.scales);
     const int64_t scale0 = (GROUPED && matrix > 0 ? matrix : 0) * p.n * columns;
     // the scales that the lane loads: rows wave * 16 / W .., all groups of columns
     uint32_t scale_at[Q], scale_row[Q], scale_unit[Q];
@@ -435,38 +391,46 @@ __global__ __launch_bounds__(kWave * W) void k_int4_tiles(Int4Args p)
         place[c] = inside ? (static_cast<uint32_t>(first + c) * kChunk + g * 32) / 2 : 0;
     }
 
-    struct Tile {
+    struct Codes {
         u32x4 c[RC];
-        uint32_t scale[Q], zero[Q];   // their bits
     } tile[D];
+    struct Scales {
+        uint32_t scale[Q], zero[Q];   // their bits
+    } scaled[D];
     const uint32_t row_bytes = static_cast<uint32_t>(p.k / 2);
-    auto load = [&](Tile& s, int at) {
-        const int64_t n = static_cast<int64_t>(tile0 + at) * 16;
-        const int64_t behind = p.n - 1 - n;   // rows behind the edge read the last one
-        const uint32_t rr = r < behind ? r : static_cast<uint32_t>(behind);
-        const uint8_t* const from = codes + n * row_bytes;   // uniform: the lanes' offsets fit 32 bits
+    // rows behind the edge read the last one; the lanes' offsets from a tile fit 32 bits
+    auto behind = [&](int at) { return p.n - 1 - static_cast<int64_t>(tile0 + at) * 16; };
+    auto load = [&](Codes& s, int at) {
+        const int64_t last = behind(at);
+        const uint32_t row = r < last ? r : static_cast<uint32_t>(last);
+        const uint8_t* const from = codes + static_cast<int64_t>(tile0 + at) * 16 * row_bytes;
 #pragma unroll
         for (int c = 0; c < RC; ++c)
-            s.c[c] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(from + (rr * row_bytes + place[c])));
-        const int64_t base = scale0 + n * columns;
+            s.c[c] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(from + (row * row_bytes + place[c])));
+    };
+    auto load_scales = [&](Scales& s, int at) {
+        const int64_t last = behind(at), base = scale0 + static_cast<int64_t>(tile0 + at) * 16 * columns;
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
-            const uint32_t of = (scale_row[i] < behind ? scale_row[i] : static_cast<uint32_t>(behind)) * columns + scale_at[i];
+            const uint32_t of = (scale_row[i] < last ? scale_row[i] : static_cast<uint32_t>(last)) * columns + scale_at[i];
             s.scale[i] = scales[base + of];
             s.zero[i] = zeros[base + of];
         }
     };
     // a tile's scales to LDS, ahead of a barrier
-    auto share = [&](const Tile& s, int at) {
+    auto share = [&](const Scales& s, int at) {
 #pragma unroll
         for (int i = 0; i < Q; ++i)
             scaling[at & 1][scale_row[i]][scale_unit[i]] =
                 float2{bits_value(s.scale[i], p.scale_dtype), p.zeros ? bits_value(s.zero[i], p.scale_dtype) : 8.0f};
     };
-    const bool some = p.k > 0;
+    const bool some = chunks > 0;
+    const int most = tiles - 1;
+    if (some) {   // those behind the last tile are that one's again
+        load_scales(scaled[0], 0);
 #pragma unroll
-    for (int u = 0; u < D; ++u)
-        if (some && u < tiles) load(tile[u], u);
+        for (int u = 0; u < D; ++u) load(tile[u], u < most ? u : most);
+    }
 
     u32x4 a[RC][4][P];
     constexpr uint32_t kOne = DT == kF16 ? 0x3c003c00u : 0x3f803f80u;
@@ -494,43 +458,14 @@ __global__ __launch_bounds__(kWave * W) void k_int4_tiles(Int4Args p)
             for (int q = 0; q < S; ++q) plain[wave][c * S + q][g] = sum[q];
         }
     }
-    if (some) share(tile[0], 0);
+    if (some) {
+        share(scaled[0], 0);
+        load_scales(scaled[1], 1 < most ? 1 : most);
+        load_scales(scaled[0], 2 < most ? 2 : most);
+    }
     lds_barrier();
 
-    auto compute = [&](Tile& s, const Tile& then, int at) {
-        f32x4 y{0, 0, 0, 0};
-#pragma unroll
-        for (int c = 0; c < RC; ++c) {
-            if (c >= count) break;
-            uint32_t c0 = s.c[c][0], c1 = s.c[c][1], c2 = s.c[c][2], c3 = s.c[c][3];
-            swap32(c0, c2);
-            swap32(c1, c3);
-            swap16(c0, c1);
-            swap16(c2, c3);
-            const uint32_t word[4] = {c0, c1, c2, c3};
-            f32x4 sum[S] = {};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const u32x4 b = code_values<DT>(word[q]);
-#pragma unroll
-                for (int h = 0; h < P; ++h) sum[q * S / 4] = multiply<DT>(a[c][q][h], b, sum[q * S / 4]);
-            }
-#pragma unroll
-            for (int q = 0; q < S; ++q) {
-                const int i = c * S + q;
-                const float2 w = scaling[at & 1][r][first * S + i];
-                const f32x4 xs = plain[wave][i][g];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(w.x, __builtin_fmaf(-w.y, xs[e], sum[q][e]), y[e]);
-            }
-        }
-        sums[at & 1][wave][lane] = y;
-        if (some && at + 1 < tiles) share(then, at + 1);
-        lds_barrier();   // the tile before the last one was added up before its wave came here
-        if (at % W != wave) return;
-        f32x4 v = sums[at & 1][0][lane];
-#pragma unroll
-        for (int w = 1; w < W; ++w) v += sums[at & 1][w][lane];
+    auto store = [&](int at, f32x4 v) {
         const int64_t n = static_cast<int64_t>(tile0 + at) * 16 + r;
         if (n >= p.n) return;
 #pragma unroll
@@ -539,20 +474,67 @@ __global__ __launch_bounds__(kWave * W) void k_int4_tiles(Int4Args p)
             if (row < rows) store_value(p.out, (row0 + row) * p.out_stride + n, v[e], p.out_dtype);
         }
     };
+    auto compute = [&](const Codes& s, const Scales& then, int at) {
+        f32x4 y{0, 0, 0, 0};
+        // the steps' chains of instructions beside one another
+        uint32_t word[RC][4];
+        f32x4 sum[RC][S] = {};
+#pragma unroll
+        for (int c = 0; c < RC; ++c) {   // x and its sums are 0 in the steps that are not there
+            uint32_t c0 = s.c[c][0], c1 = s.c[c][1], c2 = s.c[c][2], c3 = s.c[c][3];
+            swap32(c0, c2);
+            swap32(c1, c3);
+            swap16(c0, c1);
+            swap16(c2, c3);
+            word[c][0] = c0;
+            word[c][1] = c1;
+            word[c][2] = c2;
+            word[c][3] = c3;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int c = 0; c < RC; ++c) {
+                const u32x4 b = code_values<DT>(word[c][q]);
+#pragma unroll
+                for (int h = 0; h < P; ++h) sum[c][q * S / 4] = multiply<DT>(a[c][q][h], b, sum[c][q * S / 4]);
+            }
+#pragma unroll
+        for (int i = 0; i < RC * S; ++i) {
+            const float2 w = scaling[at & 1][r][first * S + i];
+            const f32x4 xs = plain[wave][i][g];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(w.x, __builtin_fmaf(-w.y, xs[e], sum[i / S][i % S][e]), y[e]);
+        }
+        sums[at & 1][wave][lane] = y;
+        share(then, at + 1);
+        lds_barrier();   // the tile before the last one was added up before its wave came here
+        if (at % W != wave) return;
+        f32x4 v = sums[at & 1][0][lane];
+#pragma unroll
+        for (int w = 1; w < W; ++w) v += sums[at & 1][w][lane];
+        store(at, v);
+    };
+    if (!some) {   // rows of no group, or no columns
+        for (int at = wave; at < tiles; at += W) store(at, f32x4{0, 0, 0, 0});
+        return;
+    }
+    static_assert(D == 2, "a tile's scales stand in the place of the one after the next");
     int at = 0;
-    for (; at + 2 * D <= tiles && some; at += D) {
+    for (; at + D + 1 < tiles; at += D) {   // three tiles behind this one are there
 #pragma unroll
         for (int u = 0; u < D; ++u) {
-            compute(tile[u], tile[(u + 1) % D], at + u);
-            load(tile[u], at + u + D);
+            compute(tile[u], scaled[1 - u], at + u);
+            load_scales(scaled[1 - u], at + u + 3 < most ? at + u + 3 : most);
+            load(tile[u], at + u + 2);
         }
     }
-    for (; at < tiles; at += D) {
+    for (; at < tiles; at += D) {   // three at most
 #pragma unroll
         for (int u = 0; u < D; ++u) {
             if (at + u >= tiles) break;
-            compute(tile[u], tile[(u + 1) % D], at + u);
-            if (some && at + u + D < tiles) load(tile[u], at + u + D);
+            compute(tile[u], scaled[1 - u], at + u);
+            if (at + u + 2 < tiles) load(tile[u], at + u + 2);
         }
     }
 }
@@ -574,44 +556,35 @@ const void* int4_dequantize_kernel(int dtype)
 
 namespace {
 
-// Steps of a wave whose x is held: 64 or 96 registers of it.
-template <int DT>
-constexpr int kHeldSteps = DT == kF32 ? 2 : 4;
-
-template <int DT, int SB, int S, bool GROUPED>
-Int4Kernel choose_tiles(int64_t steps)
-{
-    constexpr int RC = kHeldSteps<DT>;
-    if (steps <= 4 * RC) return {reinterpret_cast<const void*>(k_int4_tiles<DT, SB, S, 4, RC, GROUPED>), 4, true};
-    return {reinterpret_cast<const void*>(k_int4_tiles<DT, SB, S, 8, RC, GROUPED>), 8, true};
-}
 template <int DT, int S, bool GROUPED>
-Int4Kernel choose_waves(int64_t steps, int scale_bytes)
+Int4Kernel choose_waves(int64_t steps, bool held)
 {
-    constexpr int U = DT == kF32 ? 2 : 4;
-    if (steps <= 8 * kHeldSteps<DT>) return scale_bytes == 4 ? choose_tiles<DT, 4, S, GROUPED>(steps) : choose_tiles<DT, 2, S, GROUPED>(steps);
-    return {reinterpret_cast<const void*>(k_int4_matmul<DT, S, 1, 1, 8, U, GROUPED>), 8, false};
+    constexpr int RC = DT == kF32 ? 2 : 4;   // steps whose x is held, 64 or 48 registers of it
+    if (held && steps <= 8) return {reinterpret_cast<const void*>(k_int4_tiles<DT, S, 4, 2, GROUPED>), 4, true};
+    if (held && steps <= 4 * RC) return {reinterpret_cast<const void*>(k_int4_tiles<DT, S, 4, RC, GROUPED>), 4, true};
+    if (held && steps <= 8 * RC) return {reinterpret_cast<const void*>(k_int4_tiles<DT, S, 8, RC, GROUPED>), 8, true};
+    return {reinterpret_cast<const void*>(k_int4_matmul<DT, S, 8, 2, GROUPED>), 8, false};
 }
 template <int DT, int S>
-Int4Kernel choose_grouped(bool grouped, int64_t steps, int scale_bytes)
+Int4Kernel choose_grouped(bool grouped, int64_t steps, bool held)
 {
-    return grouped ? choose_waves<DT, S, true>(steps, scale_bytes) : choose_waves<DT, S, false>(steps, scale_bytes);
+    return grouped ? choose_waves<DT, S, true>(steps, held) : choose_waves<DT, S, false>(steps, held);
 }
 template <int DT>
-Int4Kernel choose_scales(int scales, bool grouped, int64_t steps, int scale_bytes)
+Int4Kernel choose_scales(int scales, bool grouped, int64_t steps, bool held)
 {
-    return scales == 1   ? choose_grouped<DT, 1>(grouped, steps, scale_bytes)
-           : scales == 2 ? choose_grouped<DT, 2>(grouped, steps, scale_bytes)
-                         : choose_grouped<DT, 4>(grouped, steps, scale_bytes);
+    return scales == 1   ? choose_grouped<DT, 1>(grouped, steps, held)
+           : scales == 2 ? choose_grouped<DT, 2>(grouped, steps, held)
+                         : choose_grouped<DT, 4>(grouped, steps, held);
 }
 
 }  // namespace
 
-Int4Kernel int4_matmul_kernel(int dtype, int scales, bool grouped, int64_t steps, int scale_bytes)
+Int4Kernel int4_matmul_kernel(int dtype, int scales, bool grouped, int64_t steps, bool held)
 {
-    return dtype == kF32   ? choose_scales<kF32>(scales, grouped, steps, scale_bytes)
-           : dtype == kF16 ? choose_scales<kF16>(scales, grouped, steps, scale_bytes)
-                           : choose_scales<kBF16>(scales, grouped, steps, scale_bytes);
+    return dtype == kF32   ? choose_scales<kF32>(scales, grouped, steps, held)
+           : dtype == kF16 ? choose_scales<kF16>(scales, grouped, steps, held)
+                           : choose_scales<kBF16>(scales, grouped, steps, held);
 }
 
 }  // namespace experts
