@@ -44,7 +44,7 @@ class Int4:
                 raise ValueError("scales and zeros must be float32, float16 or bfloat16, of one type")
             if tuple(t.shape) != (*codes.shape[:-1], k // group):
                 raise ValueError(f"{name} must be {[*codes.shape[:-1], k // group]}: got {list(t.shape)}")
-            if t.device != codes.device or not t.is_contiguous():
+            if t.get_device() != codes.get_device() or not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous and on the codes' device")
         if not codes.is_contiguous():
             raise ValueError("codes must be contiguous")
@@ -148,7 +148,7 @@ def _do_matmul(x, rs, q, n, k, dtype, od, out, stride, offsets, groups, handle):
     fresh = out is None
     m = x.shape[0]
     if fresh:
-        out = torch.empty((m, n), dtype=dtype, device=x.device)
+        out = x.new_empty((m, n), dtype=dtype)
     lib = load_experts()
     left = (DTYPES[x.dtype], x.data_ptr(), m, rs, od, *_ptrs(q), n, k, q.group)
     if offsets is None:

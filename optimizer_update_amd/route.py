@@ -39,6 +39,7 @@ HEADER = os.path.join(os.path.dirname(HERE), "include", "optimizer_experts.h")
 SCORES = {"softmax": 0, "sigmoid": 1}
 GROUP_SCORES = {"best": 0, "best two": 1}
 _experts = None
+_F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
 
 
 def load_experts(path: str = LIBRARY) -> ctypes.CDLL:
@@ -98,8 +99,8 @@ class _Topk(torch.autograd.Function):
     def _forward(logits, bias, mask, k, call, handle):
         t, e = logits.shape
         scores, groups, top_groups, group_score, renorm, scale = call
-        w = torch.empty((t, k), dtype=torch.float32, device=logits.device)
-        ids = torch.empty((t, k), dtype=torch.int32, device=logits.device)
+        w = logits.new_empty((t, k), dtype=_F32)
+        ids = logits.new_empty((t, k), dtype=_I32)
         st = load_experts().ou_route_topk(
             DTYPES[logits.dtype], logits.data_ptr(), t, e, _row_stride(logits, "logits"), scores,
             None if bias is None else bias.data_ptr(), groups, top_groups, group_score, renorm, scale,
@@ -120,7 +121,7 @@ class _Topk(torch.autograd.Function):
     def _backward(ctx, logits, ids, dw, handle):
         t, e = logits.shape
         scores, _, _, _, renorm, scale = ctx.call
-        dx = torch.empty((t, e), dtype=logits.dtype, device=logits.device)
+        dx = logits.new_empty((t, e))
         st = load_experts().ou_route_topk_backward(
             DTYPES[logits.dtype], logits.data_ptr(), t, e, _row_stride(logits, "logits"), scores, renorm, scale,
             ids.data_ptr(), dw.data_ptr(), ctx.k, dx.data_ptr(), handle)
@@ -154,16 +155,17 @@ def route_topk(logits: torch.Tensor, k: int, *, scores: str = "softmax", bias: t
         if not isinstance(bias, torch.Tensor) or bias.dtype != torch.float32 or tuple(bias.shape) != (e,) or not bias.is_contiguous():
             raise ValueError(f"bias must be a contiguous float32 tensor of {e} values")
         _same(index, bias.get_device(), "bias")
-        bias = bias.detach()
+        if bias.requires_grad:
+            bias = bias.detach()
     if mask is not None:
         if not isinstance(mask, torch.Tensor) or mask.dtype != torch.bool or tuple(mask.shape) != (t,) or not mask.is_contiguous():
             raise ValueError(f"mask must be a contiguous bool tensor of {t} values")
         _same(index, mask.get_device(), "mask")
     call = (SCORES[scores], int(groups), int(top_groups), GROUP_SCORES[group_score], int(bool(renormalize)), float(scale))
     logits = _rows_apart(logits)
-    if not (torch.is_grad_enabled() and logits.requires_grad):
-        return _run(index, None, _Topk._forward, logits, bias, mask, int(k), call)
-    return _Topk.apply(logits, bias, mask, int(k), call)
+    if logits.requires_grad and torch.is_grad_enabled():
+        return _Topk.apply(logits, bias, mask, int(k), call)
+    return _run(index, None, _Topk._forward, logits, bias, mask, int(k), call)
 
 
 # ------------------------------------------------------------------ the order
@@ -184,7 +186,7 @@ class RouteOrder:
         if offsets.shape[0] < 2 or slots.shape[0] != places.numel():
             raise ValueError(f"offsets hold experts + 1 values, slots as many as places: got {list(offsets.shape)}, "
                              f"{list(slots.shape)} and {list(places.shape)}")
-        if not offsets.device == slots.device == places.device:
+        if not offsets.get_device() == slots.get_device() == places.get_device():
             raise ValueError("offsets, slots and places must be on one device")
         self.offsets, self.slots, self.places = offsets, slots, places
 
@@ -208,25 +210,29 @@ class RouteOrder:
         return f"RouteOrder(tokens={self.tokens}, choices={self.choices}, experts={self.experts}, device={self.device})"
 
 
+def _held_order(offsets, slots, places) -> RouteOrder:
+    """A RouteOrder of tensors made here."""
+    order = RouteOrder.__new__(RouteOrder)
+    order.offsets, order.slots, order.places = offsets, slots, places
+    return order
+
+
 @functools.lru_cache(maxsize=4096)
 def _order_workspace(slots: int, experts: int) -> int:
     return int(load_experts().ou_route_order_workspace_bytes(slots, experts))
 
 
 def _do_order(ids, experts, handle):
-    n, device = ids.numel(), ids.device
+    n = ids.numel()
     need = _order_workspace(n, experts)
-    offsets = torch.empty(experts + 1, dtype=torch.int32, device=device)
-    slots = torch.empty(n, dtype=torch.int32, device=device)
-    places = torch.empty(ids.shape, dtype=torch.int32, device=device)
-    ws = torch.empty(need, dtype=torch.uint8, device=device) if need > 0 else None
+    new = ids.new_empty
+    offsets, slots, places = new(experts + 1), new(n), new(ids.shape)
+    ws = new(need, dtype=_U8) if need > 0 else None
     st = load_experts().ou_route_order(ids.data_ptr(), n, experts, offsets.data_ptr(), slots.data_ptr(), places.data_ptr(),
                                        None if ws is None else ws.data_ptr(), need, handle)
     if st:
         _fail(st)
-    order = RouteOrder.__new__(RouteOrder)
-    order.offsets, order.slots, order.places = offsets, slots, places
-    return order
+    return _held_order(offsets, slots, places)
 
 
 def route_order(ids: torch.Tensor, experts: int, stream=None) -> RouteOrder:
@@ -276,26 +282,29 @@ def route_balance(bias: torch.Tensor, order: RouteOrder, rate: float, out: torch
 # ------------------------------------------------------------------ rows
 
 def _do_dispatch(x, order, out, handle):
-    t, h = x.shape
-    fresh = out is None
-    if fresh:
-        out = torch.empty((t * order.choices, h), dtype=x.dtype, device=x.device)
-    st = load_experts().ou_route_dispatch(DTYPES[x.dtype], x.data_ptr(), t, h, _row_stride(x, "x"), order.choices,
-                                          order.slots.data_ptr(), order.places.data_ptr(), out.data_ptr(),
-                                          _row_stride(out, "out"), fresh, handle)
+    (t, h), k = x.shape, order.places.shape[1]
+    if out is None:
+        out, stride, rest = x.new_empty((t * k, h)), h, 1
+    else:
+        stride, rest = _row_stride(out, "out"), 0
+    st = load_experts().ou_route_dispatch(DTYPES[x.dtype], x.data_ptr(), t, h, _row_stride(x, "x"), k,
+                                          order.slots.data_ptr(), order.places.data_ptr(), out.data_ptr(), stride, rest,
+                                          handle)
     if st:
         _fail(st)
     return out
 
 
 def _do_combine(y, w, order, add, out, handle):
-    t, h = order.tokens, y.shape[1]
+    (t, k), h = order.places.shape, y.shape[1]
     if out is None:
-        out = torch.empty((t, h), dtype=y.dtype, device=y.device)
+        out, stride = y.new_empty((t, h)), h
+    else:
+        stride = _row_stride(out, "out")
     st = load_experts().ou_route_combine(
-        DTYPES[y.dtype], y.data_ptr(), t, h, _row_stride(y, "y"), order.choices, None if w is None else w.data_ptr(),
+        DTYPES[y.dtype], y.data_ptr(), t, h, _row_stride(y, "y"), k, None if w is None else w.data_ptr(),
         order.places.data_ptr(), None if add is None else add.data_ptr(), 0 if add is None else _row_stride(add, "add"),
-        out.data_ptr(), _row_stride(out, "out"), handle)
+        out.data_ptr(), stride, handle)
     if st:
         _fail(st)
     return out
@@ -303,9 +312,9 @@ def _do_combine(y, w, order, add, out, handle):
 
 def _do_combine_backward(dout, y, w, order, need_y, need_w, handle):
     t, h = dout.shape
-    k = order.choices
-    dy = torch.empty((t * k, h), dtype=dout.dtype, device=dout.device) if need_y else None
-    dw = torch.empty((t, k), dtype=torch.float32, device=dout.device) if need_w else None
+    k = order.places.shape[1]
+    dy = dout.new_empty((t * k, h)) if need_y else None
+    dw = dout.new_empty((t, k), dtype=_F32) if need_w else None
     st = load_experts().ou_route_combine_backward(
         DTYPES[dout.dtype], dout.data_ptr(), t, h, _row_stride(dout, "the gradient"), k,
         y.data_ptr() if need_w else None, _row_stride(y, "y") if need_w else 0, w.data_ptr() if need_y else None,
@@ -314,12 +323,6 @@ def _do_combine_backward(dout, y, w, order, need_y, need_w, handle):
     if st:
         _fail(st)
     return dy, dw
-
-
-def _saved_order(offsets, slots, places) -> RouteOrder:
-    order = RouteOrder.__new__(RouteOrder)
-    order.offsets, order.slots, order.places = offsets, slots, places
-    return order
 
 
 class _Dispatch(torch.autograd.Function):
@@ -331,7 +334,7 @@ class _Dispatch(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        order = _saved_order(*ctx.saved_tensors)
+        order = _held_order(*ctx.saved_tensors)
         return _run(dy.get_device(), None, _do_combine, _rows_apart(dy), None, order, None, None), None
 
 
@@ -349,7 +352,7 @@ class _Combine(torch.autograd.Function):
         need_y, need_w, need_add = ctx.needs_input_grad[:3]
         dy = dw = None
         if need_y or need_w:
-            dy, dw = _run(dout.get_device(), None, _do_combine_backward, _rows_apart(dout), y, w, _saved_order(*order),
+            dy, dw = _run(dout.get_device(), None, _do_combine_backward, _rows_apart(dout), y, w, _held_order(*order),
                           need_y, need_w)
         return dy, dw, dout if need_add else None, None
 
@@ -368,14 +371,16 @@ def route_dispatch(x: torch.Tensor, order: RouteOrder, out: torch.Tensor | None 
     ``order.slots[p] // k``.  Rows of no slot are 0 in a new result and left as
     they were in ``out`` (any row stride; no gradients are recorded then)."""
     _values(x, "x", 2)
-    _ordered(order, x.get_device())
-    if x.shape[0] != order.tokens:
+    index = x.get_device()
+    _ordered(order, index)
+    if x.shape[0] != order.places.shape[0]:
         raise ValueError(f"x has {x.shape[0]} rows, the order {order.tokens} tokens")
     if out is not None:
         _output_like(out, order.slots.shape[0], x, (x,))
-    elif torch.is_grad_enabled() and x.requires_grad:
-        return _Dispatch.apply(_rows_apart(x), order)
-    return _run(x.get_device(), None, _do_dispatch, _rows_apart(x).detach(), order, out)
+    x = _rows_apart(x)
+    if x.requires_grad and torch.is_grad_enabled():
+        return _Dispatch.apply(x, order)
+    return _run(index, None, _do_dispatch, x, order, out)
 
 
 def route_combine(y: torch.Tensor, weights: torch.Tensor, order: RouteOrder, add: torch.Tensor | None = None,
@@ -399,7 +404,9 @@ def route_combine(y: torch.Tensor, weights: torch.Tensor, order: RouteOrder, add
         _same(index, add.get_device(), "add")
     if out is not None:
         _output_like(out, t, y, (y, weights, add))
-    y, weights, add = _rows_apart(y), weights.contiguous(), None if add is None else _rows_apart(add)
-    if torch.is_grad_enabled() and (y.requires_grad or weights.requires_grad or add is not None and add.requires_grad):
+    y, weights = _rows_apart(y), weights.contiguous()
+    if add is not None:
+        add = _rows_apart(add)
+    if (y.requires_grad or weights.requires_grad or add is not None and add.requires_grad) and torch.is_grad_enabled():
         return _Combine.apply(y, weights, add, order)
     return _run(index, None, _do_combine, y, weights, order, add, out)
