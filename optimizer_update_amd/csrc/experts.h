@@ -74,7 +74,7 @@ struct Int4Args {
     int64_t m, n, k, x_stride, out_stride;
     int32_t group, experts, zero_rest, out_dtype, scale_dtype;
     int32_t x_wide;         // 16-byte loads of x are allowed
-    int32_t tiles;          // of 16 rows of weights a block, where x is held
+    int32_t tiles;          // of rows of weights a block, where x is held
 };
 
 struct Int4QuantArgs {
@@ -104,11 +104,11 @@ const void* int4_dequantize_kernel(int dtype);
 
 // scales: groups of columns in 128 (1, 2 or 4); steps: of 128 columns in k.
 // may_hold: scales have 16 bits, and tiles are many.  held: a block takes
-// `tiles` tiles of 16 columns of results, else one.
+// `tiles` tiles of 16 `held` columns of results; 0: 16 columns.
 struct Int4Kernel {
     const void* fn;
     int waves;
-    bool held;
+    int held;
 };
 Int4Kernel int4_matmul_kernel(int dtype, int scales, bool grouped, int64_t steps, bool may_hold);
 

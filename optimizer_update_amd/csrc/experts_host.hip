@@ -341,8 +341,8 @@ double code_bytes(double n, int64_t k) { return n * static_cast<double>(k) / 2; 
 double scale_bytes(double n, int64_t k, int32_t group, int bytes) { return n * static_cast<double>(k / group) * bytes; }
 
 // From so many tiles of 16 rows of weights on x is held over runs of them, in
-// about so many blocks and up to 16 a run.  2001 tiles, k = 1024: 12.4 us by runs
-// of 4, 14.1 by 2, 15.8 by 8, 16.5 to 21 with x not held; 256 tiles, k = 4096: 7.4
+// about so many blocks and up to 16 a run.  2001 tiles, k = 1024: 10.5 us by runs
+// of 4, 11.9 by 6, 16.6 by 2, 16.5 to 21 with x not held; 256 tiles, k = 4096: 7.4
 // us against 5.5; 512 rows, 64 experts, k = 2048: 80 by 8 or 16, 88 by 4.
 constexpr int64_t kInt4Held = 1024;
 constexpr int64_t kInt4Blocks = 640;
@@ -372,10 +372,10 @@ int int4_product(int dtype, Int4Args& p, void* stream)
     const int64_t few = grouped ? (p.m < p.experts ? p.m : p.experts) : units;   // units with rows, about
     const int64_t tiles = cut(p.n, 16) * few;
     const Int4Kernel f = int4_matmul_kernel(dtype, scales, grouped, cut(p.k, 128), es == 2 && tiles >= kInt4Held);
-    const int64_t run = cut(tiles, kInt4Blocks);
-    p.tiles = static_cast<int32_t>(!f.held ? 1 : run > 16 ? 16 : run);
+    const int64_t run = cut(tiles, kInt4Blocks), held = f.held ? f.held : 1;
+    p.tiles = static_cast<int32_t>(!f.held ? 1 : cut(run > 16 ? 16 : run, held));
     void* args[] = {&p};
-    return launch({f.fn, units * cut(cut(p.n, 16), p.tiles), 1, kWave * f.waves, "k_int4_matmul", 0}, args, stream);
+    return launch({f.fn, units * cut(cut(p.n, 16 * held), p.tiles), 1, kWave * f.waves, "k_int4_matmul", 0}, args, stream);
 }
 
 }  // namespace

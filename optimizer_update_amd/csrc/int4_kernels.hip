@@ -331,29 +331,29 @@ __global__ __launch_bounds__(kWave * W) void k_int4_matmul(Int4Args p)
     }
 }
 
-// The same with x held: a block takes 16 rows of x and `p.tiles` tiles of 16
+// The same with x held: a block takes 16 rows of x and `p.tiles` tiles of 16 NT
 // rows of weights one after the other, its W waves RC steps each of the
 // columns, whose x they keep in registers; codes of the next two tiles are on
 // their way.  The waves' sums meet in LDS, and the waves take turns at adding
 // them up.  No load of the steady loop stands behind a condition (the type of
 // the scales has 16 bits, what is not there is loaded from elsewhere): the
 // compiler could not tell how many are younger than the one that it waits for,
-// and would wait for all.  The waves load the scales of 16 / W rows each, whole
+// and would wait for all.  The waves load the scales of 16 NT / W rows each, whole
 // rows of them, and share them through LDS: when each loaded what it multiplies,
 // they were 16 requests like the codes' own (21 us of 75 without any
 // arithmetic); they are asked for a tile ahead of the codes.
-template <int DT, int S, int W, int RC, bool GROUPED>
+template <int DT, int S, int NT, int W, int RC, bool GROUPED>
 __global__ __launch_bounds__(kWave * W) void k_int4_tiles(Int4Args p)
 {
     constexpr int P = Rows8<DT>::kParts, D = 2, kUnits = W * RC * S;   // kUnits: groups of columns, at most
-    constexpr int Q = kUnits * 16 / W / kWave > 0 ? kUnits * 16 / W / kWave : 1;   // loads of scales a lane and tile
+    constexpr int kRows = 16 * NT, kPart = kUnits * kRows / W, Q = kPart > kWave ? kPart / kWave : 1;   // loads of scales a lane and tile
     using Elem = typename Value<DT>::Elem;
-    __shared__ f32x4 sums[2][W][kWave];
+    __shared__ f32x4 sums[2][W][NT][kWave];
     __shared__ f32x4 plain[W][RC * S][4];   // x's sums over a group of columns, four rows
-    __shared__ float2 scaling[2][16][kUnits + 1];   // scale and zero
+    __shared__ float2 scaling[2][kRows][kUnits + 1];   // scale and zero
     const int t = static_cast<int>(threadIdx.x), lane = t & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-    const uint32_t all_tiles = static_cast<uint32_t>((p.n + 15) / 16);
+    const uint32_t all_tiles = static_cast<uint32_t>((p.n + kRows - 1) / kRows);
     const uint32_t parts = (all_tiles + p.tiles - 1) / p.tiles, unit = blockIdx.x / parts, part = blockIdx.x - unit * parts;
     int64_t row0 = static_cast<int64_t>(unit) * 16, mrows = p.m - row0, matrix = 0;
     if constexpr (GROUPED) {
@@ -377,8 +377,8 @@ __global__ __launch_bounds__(kWave * W) void k_int4_tiles(Int4Args p)
     uint32_t scale_at[Q], scale_row[Q], scale_unit[Q];
 #pragma unroll
     for (int i = 0; i < Q; ++i) {
-        const uint32_t f = (i * kWave + lane) % (kUnits * 16 / W);
-        scale_row[i] = wave * (16 / W) + f / kUnits;
+        const uint32_t f = (i * kWave + lane) % kPart;
+        scale_row[i] = wave * (kRows / W) + f / kUnits;
         scale_unit[i] = f % kUnits;
         const uint32_t of = scale_unit[i] * (kChunk / S) / static_cast<uint32_t>(p.group);
         scale_at[i] = of < columns ? of : columns - 1;
@@ -392,24 +392,27 @@ __global__ __launch_bounds__(kWave * W) void k_int4_tiles(Int4Args p)
     }
 
     struct Codes {
-        u32x4 c[RC];
+        u32x4 c[NT][RC];
     } tile[D];
     struct Scales {
         uint32_t scale[Q], zero[Q];   // their bits
     } scaled[D];
     const uint32_t row_bytes = static_cast<uint32_t>(p.k / 2);
     // rows behind the edge read the last one; the lanes' offsets from a tile fit 32 bits
-    auto behind = [&](int at) { return p.n - 1 - static_cast<int64_t>(tile0 + at) * 16; };
+    auto behind = [&](int at) { return p.n - 1 - static_cast<int64_t>(tile0 + at) * kRows; };
     auto load = [&](Codes& s, int at) {
         const int64_t last = behind(at);
-        const uint32_t row = r < last ? r : static_cast<uint32_t>(last);
-        const uint8_t* const from = codes + static_cast<int64_t>(tile0 + at) * 16 * row_bytes;
+        const uint8_t* const from = codes + static_cast<int64_t>(tile0 + at) * kRows * row_bytes;
 #pragma unroll
-        for (int c = 0; c < RC; ++c)
-            s.c[c] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(from + (row * row_bytes + place[c])));
+        for (int j = 0; j < NT; ++j) {
+            const uint32_t row = 16 * j + r < last ? 16 * j + r : static_cast<uint32_t>(last);
+#pragma unroll
+            for (int c = 0; c < RC; ++c)
+                s.c[j][c] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(from + (row * row_bytes + place[c])));
+        }
     };
     auto load_scales = [&](Scales& s, int at) {
-        const int64_t last = behind(at), base = scale0 + static_cast<int64_t>(tile0 + at) * 16 * columns;
+        const int64_t last = behind(at), base = scale0 + static_cast<int64_t>(tile0 + at) * kRows * columns;
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
             const uint32_t of = (scale_row[i] < last ? scale_row[i] : static_cast<uint32_t>(last)) * columns + scale_at[i];
@@ -465,8 +468,8 @@ __global__ __launch_bounds__(kWave * W) void k_int4_tiles(Int4Args p)
     }
     lds_barrier();
 
-    auto store = [&](int at, f32x4 v) {
-        const int64_t n = static_cast<int64_t>(tile0 + at) * 16 + r;
+    auto store = [&](int at, int j, f32x4 v) {
+        const int64_t n = static_cast<int64_t>(tile0 + at) * kRows + 16 * j + r;
         if (n >= p.n) return;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -475,48 +478,56 @@ __global__ __launch_bounds__(kWave * W) void k_int4_tiles(Int4Args p)
         }
     };
     auto compute = [&](const Codes& s, const Scales& then, int at) {
-        f32x4 y{0, 0, 0, 0};
         // the steps' chains of instructions beside one another
-        uint32_t word[RC][4];
-        f32x4 sum[RC][S] = {};
+        uint32_t word[NT][RC][4];
+        f32x4 sum[NT][RC][S] = {}, y[NT] = {};
 #pragma unroll
-        for (int c = 0; c < RC; ++c) {   // x and its sums are 0 in the steps that are not there
-            uint32_t c0 = s.c[c][0], c1 = s.c[c][1], c2 = s.c[c][2], c3 = s.c[c][3];
-            swap32(c0, c2);
-            swap32(c1, c3);
-            swap16(c0, c1);
-            swap16(c2, c3);
-            word[c][0] = c0;
-            word[c][1] = c1;
-            word[c][2] = c2;
-            word[c][3] = c3;
-        }
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int c = 0; c < RC; ++c) {   // x and its sums are 0 in the steps that are not there
+                uint32_t c0 = s.c[j][c][0], c1 = s.c[j][c][1], c2 = s.c[j][c][2], c3 = s.c[j][c][3];
+                swap32(c0, c2);
+                swap32(c1, c3);
+                swap16(c0, c1);
+                swap16(c2, c3);
+                word[j][c][0] = c0;
+                word[j][c][1] = c1;
+                word[j][c][2] = c2;
+                word[j][c][3] = c3;
+            }
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int c = 0; c < RC; ++c) {
-                const u32x4 b = code_values<DT>(word[c][q]);
+            for (int c = 0; c < RC; ++c)
 #pragma unroll
-                for (int h = 0; h < P; ++h) sum[c][q * S / 4] = multiply<DT>(a[c][q][h], b, sum[c][q * S / 4]);
-            }
+                for (int j = 0; j < NT; ++j) {
+                    const u32x4 b = code_values<DT>(word[j][c][q]);
+#pragma unroll
+                    for (int h = 0; h < P; ++h) sum[j][c][q * S / 4] = multiply<DT>(a[c][q][h], b, sum[j][c][q * S / 4]);
+                }
 #pragma unroll
         for (int i = 0; i < RC * S; ++i) {
-            const float2 w = scaling[at & 1][r][first * S + i];
             const f32x4 xs = plain[wave][i][g];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(w.x, __builtin_fmaf(-w.y, xs[e], sum[i / S][i % S][e]), y[e]);
+            for (int j = 0; j < NT; ++j) {
+                const float2 w = scaling[at & 1][16 * j + r][first * S + i];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[j][e] = __builtin_fmaf(w.x, __builtin_fmaf(-w.y, xs[e], sum[j][i / S][i % S][e]), y[j][e]);
+            }
         }
-        sums[at & 1][wave][lane] = y;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) sums[at & 1][wave][j][lane] = y[j];
         share(then, at + 1);
         lds_barrier();   // the tile before the last one was added up before its wave came here
-        if (at % W != wave) return;
-        f32x4 v = sums[at & 1][0][lane];
+        const int j = wave - at * NT % W;
+        if (j < 0 || j >= NT) return;
+        f32x4 v = sums[at & 1][0][j][lane];
 #pragma unroll
-        for (int w = 1; w < W; ++w) v += sums[at & 1][w][lane];
-        store(at, v);
+        for (int w = 1; w < W; ++w) v += sums[at & 1][w][j][lane];
+        store(at, j, v);
     };
     if (!some) {   // rows of no group, or no columns
-        for (int at = wave; at < tiles; at += W) store(at, f32x4{0, 0, 0, 0});
+        for (int at = wave; at < tiles * NT; at += W) store(at / NT, at % NT, f32x4{0, 0, 0, 0});
         return;
     }
     static_assert(D == 2, "a tile's scales stand in the place of the one after the next");
@@ -560,10 +571,14 @@ template <int DT, int S, bool GROUPED>
 Int4Kernel choose_waves(int64_t steps, bool held)
 {
     constexpr int RC = DT == kF32 ? 2 : 4;   // steps whose x is held, 64 or 48 registers of it
-    if (held && steps <= 8) return {reinterpret_cast<const void*>(k_int4_tiles<DT, S, 4, 2, GROUPED>), 4, true};
-    if (held && steps <= 4 * RC) return {reinterpret_cast<const void*>(k_int4_tiles<DT, S, 4, RC, GROUPED>), 4, true};
-    if (held && steps <= 8 * RC) return {reinterpret_cast<const void*>(k_int4_tiles<DT, S, 8, RC, GROUPED>), 8, true};
-    return {reinterpret_cast<const void*>(k_int4_matmul<DT, S, 8, 2, GROUPED>), 8, false};
+    // 2001 tiles of 8 steps: eight waves of one 10.5 us by pairs of tiles, 11.2 by
+    // single ones, four waves of two 11.6 and 12.8.  16 steps, 64 experts: four
+    // waves of four 80 us, by pairs 95, eight of two 96, by pairs 82.
+    if (held && steps <= 8) return {reinterpret_cast<const void*>(k_int4_tiles<DT, S, 2, 8, 1, GROUPED>), 8, 2};
+    if constexpr (RC == 4)
+        if (held && steps <= 16) return {reinterpret_cast<const void*>(k_int4_tiles<DT, S, 1, 4, 4, GROUPED>), 4, 1};
+    if (held && steps <= 8 * RC) return {reinterpret_cast<const void*>(k_int4_tiles<DT, S, 1, 8, RC, GROUPED>), 8, 1};
+    return {reinterpret_cast<const void*>(k_int4_matmul<DT, S, 8, 2, GROUPED>), 8, 0};
 }
 template <int DT, int S>
 Int4Kernel choose_grouped(bool grouped, int64_t steps, bool held)

@@ -151,6 +151,21 @@ def test_rows_do_not_mix():
         assert torch.equal(y[keep], z[keep])
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_rows_do_not_mix_where_tiles_are_many(dtype):
+    e, n, k = 70, 600, 512
+    q = _weights((e, n), k, 128, BF16, True)
+    off = torch.arange(0, 3 * e + 1, 3, dtype=torch.int32, device="cuda")
+    x = torch.randn((3 * e, k), generator=_gen(3)).to(dtype).cuda()
+    y = ou.int4_grouped_matmul(x, q, off)
+    bad = [4, 17, 100, 3 * e - 1]
+    for i, r in enumerate(bad):
+        x[r, 100 * i + 9] = float("nan") if i % 2 else float("inf")
+    z = ou.int4_grouped_matmul(x, q, off)
+    keep = [i for i in range(3 * e) if i not in bad]
+    assert not torch.isfinite(z[bad]).any() and torch.equal(y[keep], z[keep])
+
+
 def test_small_and_large_values():
     """x over the range of its type, with scales that bring the sums back."""
     for dtype, top, low in ((F32, 1e30, 1e-30), (BF16, 1e30, 1e-30), (F16, 6e4, 1e-6)):
