@@ -74,6 +74,7 @@ struct Int4Args {
     int64_t m, n, k, x_stride, out_stride;
     int32_t group, experts, zero_rest, out_dtype, scale_dtype;
     int32_t x_wide;         // 16-byte loads of x are allowed
+    int32_t out_wide;       // dequantisation: 16-byte stores are
     int32_t tiles;          // of rows of weights a block, where x is held
 };
 
@@ -84,6 +85,8 @@ struct Int4QuantArgs {
     void* zeros;
     int64_t rows, k, row_stride;
     int32_t group, scale_dtype;
+    int32_t wide;           // 16-byte loads of x are allowed
+    int32_t lanes_log2;     // of a group
 };
 
 // `tokens` a wave

@@ -396,10 +396,12 @@ OU_EXPORT int ou_int4_quantize(int dtype, const void* x, int64_t rows, int64_t k
                            {"scales", scales, scale_bytes(n, k, group, es), static_cast<unsigned>(es), true},
                            {"zeros", zeros, zeros ? scale_bytes(n, k, group, es) : 0, static_cast<unsigned>(es), true}};
     if (int st = check_buffers(bufs, 4)) return st;
-    Int4QuantArgs q{x, codes, scales, zeros, rows, k, row_stride, group, scale_dtype};
+    Int4QuantArgs q{x, codes, scales, zeros, rows, k, row_stride, group, scale_dtype, 0, 0};
+    q.wide = wide_rows(x, row_stride, 0, eb, 16);
+    q.lanes_log2 = group / 8 % 16 == 0 ? 4 : group / 8 % 8 == 0 ? 3 : 2;
     void* args[] = {&q};
-    return launch({int4_quantize_kernel(dtype), cut(rows * (k / group), kInt4Threads / 16), 1, kInt4Threads, "k_int4_quantize",
-                   0}, args, stream);
+    return launch({int4_quantize_kernel(dtype), cut(rows * (k / group), kInt4Threads >> q.lanes_log2), 1, kInt4Threads,
+                   "k_int4_quantize", 0}, args, stream);
 }
 
 OU_EXPORT int ou_int4_dequantize(int dtype, const uint8_t* codes, int scale_dtype, const void* scales, const void* zeros,
@@ -426,6 +428,7 @@ OU_EXPORT int ou_int4_dequantize(int dtype, const uint8_t* codes, int scale_dtyp
     p.out_stride = out_stride;
     p.group = group;
     p.scale_dtype = scale_dtype;
+    p.out_wide = wide_rows(out, out_stride, 0, eb, 16);
     void* args[] = {&p};
     return launch({int4_dequantize_kernel(dtype), cut(n * (k / 8), kInt4Threads), 1, kInt4Threads, "k_int4_dequantize", 0}, args,
                   stream);
@@ -435,7 +438,7 @@ OU_EXPORT int ou_int4_matmul(int dtype, const void* x, int64_t m, int64_t x_stri
                              int scale_dtype, const void* scales, const void* zeros, int64_t n, int64_t k, int32_t group,
                              void* out, int64_t out_stride, void* stream)
 {
-    Int4Args p{x, codes, scales, zeros, out, nullptr, m, n, k, x_stride, out_stride, group, 0, 0, out_dtype, scale_dtype, 0, 1};
+    Int4Args p{x, codes, scales, zeros, out, nullptr, m, n, k, x_stride, out_stride, group, 0, 0, out_dtype, scale_dtype, 0, 0, 1};
     return int4_product(dtype, p, stream);
 }
 
@@ -446,7 +449,7 @@ OU_EXPORT int ou_int4_grouped_matmul(int dtype, const void* x, int64_t m, int64_
 {
     if (int st = check_groups(offsets, experts, m)) return st;
     Int4Args p{x, codes, scales, zeros, out, offsets, m, n, k, x_stride, out_stride, group, experts, zero_rest != 0, out_dtype,
-               scale_dtype, 0, 1};
+               scale_dtype, 0, 0, 1};
     return int4_product(dtype, p, stream);
 }
 

@@ -20,25 +20,52 @@ __device__ __forceinline__ float rounded(float x, int dtype)
     return r > 3.3895313892515355e38f ? 3.3895313892515355e38f : r;
 }
 
-// 16 lanes a group of columns: its extremes, then its codes, two a byte.
+// Quotient and rest; 64-bit division only where it is needed.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b, int64_t* rest)
+{
+    if (a >> 32 || b >> 32) {
+        *rest = a % b;
+        return a / b;
+    }
+    const uint32_t q = static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    *rest = static_cast<uint32_t>(a) - q * static_cast<uint32_t>(b);
+    return q;
+}
+
+// 4, 8 or 16 lanes a group of columns, eight columns a lane and turn: its
+// extremes, then its codes.  QUANT_TIME
 template <int DT>
 __global__ __launch_bounds__(kInt4Threads) void k_int4_quantize(Int4QuantArgs q)
 {
-    const int64_t groups = q.k / q.group, unit = static_cast<int64_t>(blockIdx.x) * (kInt4Threads / 16) + (threadIdx.x >> 4);
-    const bool in = unit < q.rows * groups;
-    const int lane = static_cast<int>(threadIdx.x) & 15;
-    const int64_t row = in ? unit / groups : 0, g = in ? unit - row * groups : 0;
-    const typename Value<DT>::Elem* x = static_cast<const typename Value<DT>::Elem*>(q.x) + row * q.row_stride + g * q.group;
+    using P = Piece<DT, true>;
+    using Elem = typename Value<DT>::Elem;
+    const int lanes = 1 << q.lanes_log2, octets = q.group / 8;
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kInt4Threads >> q.lanes_log2) + (threadIdx.x >> q.lanes_log2);
+    const bool in = unit < q.rows * (q.k / q.group);
+    const int lane = static_cast<int>(threadIdx.x) & (lanes - 1);
+    int64_t g;
+    const int64_t row = divide(in ? unit : 0, q.k / q.group, &g);
+    const Elem* const x = static_cast<const Elem*>(q.x) + row * q.row_stride + g * q.group;
+    float v[8];
+    auto load = [&](int o) {
+        if (q.wide) {
+#pragma unroll
+            for (int i = 0; i < 8; i += P::kValues) P::unpack(P::fetch(x, o * 8 + i), v + i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = Value<DT>::load(x, o * 8 + i);
+        }
+    };
     float lo = 0.0f, hi = 0.0f;
-    if (in) {
-        for (int i = lane; i < q.group; i += 16) {
-            const float v = Value<DT>::load(x, i);
-            lo = fminf(lo, v);
-            hi = fmaxf(hi, v);
+    for (int o = lane; o < octets; o += lanes) {
+        load(o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            lo = fminf(lo, v[i]);
+            hi = fmaxf(hi, v[i]);
         }
     }
-#pragma unroll
-    for (int s = 8; s; s >>= 1) {
+    for (int s = lanes / 2; s; s >>= 1) {
         lo = fminf(lo, __shfl_xor(lo, s));
         hi = fmaxf(hi, __shfl_xor(hi, s));
     }
@@ -50,33 +77,44 @@ __global__ __launch_bounds__(kInt4Threads) void k_int4_quantize(Int4QuantArgs q)
         store_value(q.scales, unit, scale, q.scale_dtype);
         if (q.zeros) store_value(q.zeros, unit, zero, q.scale_dtype);
     }
-    uint8_t* codes = q.codes + row * (q.k / 2) + g * (q.group / 2);
-    for (int i = lane; i < q.group / 2; i += 16) {
-        uint32_t c[2];
+    uint32_t* const codes = reinterpret_cast<uint32_t*>(q.codes) + (row * q.k + g * q.group) / 8;
+    for (int o = lane; o < octets; o += lanes) {
+        if (octets > lanes) load(o);   // else still there
+        uint32_t c = 0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float v = scale > 0.0f ? rintf(Value<DT>::load(x, 2 * i + h) / scale) + zero : zero;
-            c[h] = static_cast<uint32_t>(fminf(fmaxf(v, 0.0f), 15.0f));
+        for (int i = 0; i < 8; ++i) {
+            const float u = scale > 0.0f ? rintf(v[i] / scale) + zero : zero;
+            c |= static_cast<uint32_t>(fminf(fmaxf(u, 0.0f), 15.0f)) << (4 * i);
         }
-        codes[i] = static_cast<uint8_t>(c[0] | c[1] << 4);
+        codes[o] = c;
     }
 }
 
-// Eight columns a thread.
+// Eight columns a thread, written as one or two pieces where rows allow it.
+// DEQUANT_TIME
 template <int DT>
 __global__ __launch_bounds__(kInt4Threads) void k_int4_dequantize(Int4Args p)
 {
+    using P = Piece<DT, true>;
     const int64_t octets = p.k / 8, u = static_cast<int64_t>(blockIdx.x) * kInt4Threads + threadIdx.x;
     if (u >= p.n * octets) return;
-    const int64_t row = u / octets, o = u - row * octets;
-    const int64_t g = row * (p.k / p.group) + o * 8 / p.group;
-    const uint32_t c = reinterpret_cast<const uint32_t*>(p.codes)[u];
+    int64_t o;
+    const int64_t row = divide(u, octets, &o);
+    const int64_t g = row * (p.k / p.group) + static_cast<uint32_t>(o * 8) / static_cast<uint32_t>(p.group);
+    const uint32_t c = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p.codes) + u);
     const float scale = load_value(p.scales, g, p.scale_dtype);
     const float zero = p.zeros ? load_value(p.zeros, g, p.scale_dtype) : 8.0f;
-    typename Value<DT>::Elem* out = static_cast<typename Value<DT>::Elem*>(p.out) + row * p.out_stride + o * 8;
+    float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        Value<DT>::store(out, i, (static_cast<float>(c >> (4 * i) & 15u) - zero) * scale);
+    for (int i = 0; i < 8; ++i) v[i] = (static_cast<float>(c >> (4 * i) & 15u) - zero) * scale;
+    const int64_t at = row * p.out_stride + o * 8;
+    if (p.out_wide) {
+#pragma unroll
+        for (int i = 0; i < 8; i += P::kValues) P::store(p.out, at + i, v + i, true);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) Value<DT>::store(static_cast<typename Value<DT>::Elem*>(p.out), at + i, v[i]);
+    }
 }
 
 // ---- products --------------------------------------------------------------------
