@@ -139,10 +139,13 @@ int ou_int4_dequantize(int dtype, const uint8_t* codes, int scale_dtype, const v
                        int64_t out_stride, void* stream);
 
 /* out[i][j] = sum_k x[i][k] * value[j][k]: x m x k of `dtype`, out m x n of
- * out_dtype.  The products of codes and x are exact; sums in binary32,
- * rounded once.  A row of x that holds an infinity or a NaN gives NaN or
- * infinities.  Made for few rows (tokens in serving): from some hundred on,
- * dequantised weights and a library product are faster. */
+ * out_dtype.  The products of codes and x are exact (of a binary32 x what lies
+ * below 2^-133 is cut off); sums in binary32, of x code and of x apart, so that
+ * a result may be infinite or NaN where 15 times the terms' magnitudes pass
+ * what it holds; rounded once.  A row of x that holds an infinity or a NaN gives
+ * NaN or infinities, and no other row does by it.  Made for few rows (tokens in
+ * serving): from some hundred on, dequantised weights and a library product
+ * are faster. */
 int ou_int4_matmul(int dtype, const void* x, int64_t m, int64_t x_stride, int out_dtype,
                    const uint8_t* codes, int scale_dtype, const void* scales, const void* zeros,
                    int64_t n, int64_t k, int32_t group, void* out, int64_t out_stride,

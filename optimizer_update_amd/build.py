@@ -1,5 +1,7 @@
 """Build liboptimizer_update.so (HIP, gfx950) in-tree with hipcc, and the
-CPython module _fast that calls its per-step entry points without ctypes.
+CPython module _fast that calls its per-step entry points without ctypes; the
+libraries of the 4-bit operators and of the operators around experts, and for
+the latter _fast_experts.
 
 The flags fix the arithmetic: no contraction into fused multiply-adds,
 correctly rounded binary32 division and square root, denormals kept, and no
@@ -32,6 +34,7 @@ MX4_SOURCES = [os.path.join(CSRC, "mx4_kernels.hip"), os.path.join(CSRC, "mx4_ho
 
 # The operators around experts (routing, 4-bit weights with group scales): likewise.
 EXPERTS_LIBRARY = os.path.join(HERE, "liboptimizer_experts.so")
+FAST_EXPERTS = os.path.join(HERE, "_fast_experts" + sysconfig.get_config_var("EXT_SUFFIX"))
 EXPERTS_SOURCES = [os.path.join(CSRC, "route_kernels.hip"), os.path.join(CSRC, "int4_kernels.hip"),
                    os.path.join(CSRC, "experts_host.hip")]
 
@@ -52,6 +55,7 @@ def build(out_path: str = LIBRARY, extra_flags: list[str] | None = None, quiet: 
     if out_path == LIBRARY:
         _compile(MX4_SOURCES, MX4_LIBRARY, extra_flags, quiet)
         _compile(EXPERTS_SOURCES, EXPERTS_LIBRARY, extra_flags, quiet)
+        build_fast(FAST_EXPERTS, "pyexperts.c", "optimizer_experts")
     build_fast()
     return out_path
 
@@ -73,18 +77,18 @@ def _compile(sources: list[str], out_path: str, extra_flags: list[str] | None, q
             os.unlink(tmp)
 
 
-def build_fast(out_path: str = FAST) -> str:
-    """Compile the CPython module (gcc, linked to the library next to it)."""
+def build_fast(out_path: str = FAST, source: str = "pyfast.c", library: str = "optimizer_update") -> str:
+    """Compile a CPython module (gcc, linked to the library next to it)."""
     cc = os.environ.get("CC", "gcc")
     fd, tmp = tempfile.mkstemp(suffix=".so", dir=os.path.dirname(out_path))
     os.close(fd)
     cmd = [cc, "-O2", "-std=c11", "-shared", "-fPIC", "-Wall", "-Werror",
-           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "pyfast.c"),
-           "-L", HERE, "-loptimizer_update", "-Wl,-rpath,$ORIGIN", "-o", tmp]
+           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, source),
+           "-L", HERE, "-l" + library, "-Wl,-rpath,$ORIGIN", "-o", tmp]
     try:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError("building _fast failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
+            raise RuntimeError(f"building {os.path.basename(out_path)} failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
         os.chmod(tmp, 0o755)
         os.replace(tmp, out_path)
     finally:

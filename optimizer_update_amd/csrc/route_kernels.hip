@@ -208,7 +208,9 @@ __device__ int choose_exact(const TopkArgs& p, int64_t token, int lane, uint64_t
 // through choose_exact().  The scores' errors: 2^-22 for the logistic function
 // (an argument to half a step of itself, exponential and reciprocal to one
 // step), 45 half steps of the largest for the softmax (arguments, a sum of 16 +
-// 6 terms, the quotient), half a step of c for the bias.  Both are taken twice.
+// 6 terms, the quotient), half a step of c for the bias.  All are taken twice.
+// 32768 x 256 fp32 in 8 parts: 29 us, bound by instructions (some 1230 for a
+// wave's four tokens, 300 of them the rounds); its 34 MB would take 7.
 template <int DT, int L, int V>
 __global__ __launch_bounds__(kTopkWaves * kWave) void k_topk(TopkArgs p)
 {
@@ -532,7 +534,9 @@ __global__ __launch_bounds__(kTopkWaves * kWave) void k_topk(TopkArgs p)
 }
 
 // L lanes a token, V of its experts a lane, a choice a lane.  Where only the
-// chosen have a gradient, a token's logits are read at those alone.
+// chosen have a gradient, a token's logits are read at those alone.  32768 x 256
+// fp32: 8.6 us, 3.9 TB/s of stores (18.5 with a wave a token, by its
+// instructions).
 template <int DT, int L, int V>
 __global__ __launch_bounds__(kTopkWaves * kWave) void k_topk_backward(TopkBackwardArgs p)
 {
@@ -630,7 +634,10 @@ __global__ __launch_bounds__(kTopkWaves * kWave) void k_topk_backward(TopkBackwa
 // With more than one block, the first kernel counts every block's slots by
 // expert, and each block of the second adds up the counts itself: 128 blocks of
 // 2048 slots with 257 bins are 17 MB from the L2, in 16-byte pieces of which a
-// thread has eight on their way.  262144 slots, 256 experts: ORDER_TIME.
+// thread has eight on their way.  262144 slots, 256 experts: 3.6 us of counting
+// and 9.2 (41 where a thread read the counts of its bins one by one); up to 4096
+// slots 3.0 in one launch.  Bound by latency: counting, the counts' way through
+// the L2, then the waves' steps of 64 slots one behind the other.
 __device__ __forceinline__ int bin_of(const OrderArgs& p, int32_t id)
 {
     return static_cast<uint32_t>(id) < static_cast<uint32_t>(p.experts) ? id : p.experts;
@@ -819,7 +826,9 @@ struct Choices {
 };
 
 // Each piece of the token's row is read once and written to the rows of its
-// slots.  Block t also clears those of rows t * k .. that are of no slot.
+// slots.  Block t also clears those of rows t * k .. that are of no slot.  Bound
+// by memory: 8190 x 8 rows of 2048 bf16 302 MB in 46 us, 6.6 TB/s, nearly all of
+// it stores.
 template <class U>
 __global__ __launch_bounds__(kRowThreads) void k_dispatch(RowsArgs p)
 {
@@ -843,8 +852,10 @@ __global__ __launch_bounds__(kRowThreads) void k_dispatch(RowsArgs p)
     }
 }
 
-// A lane has the pieces of eight of the token's rows on their way.
-// COMBINE_TIME
+// A lane has the pieces of eight of the token's rows on their way.  They are read
+// once, so past the caches: 8190 x 8 rows of 2048 bf16 302 MB in 57 us, 5.3 TB/s
+// (88 by cached loads, whatever their number); 16384 x 8 of 4096 with what is
+// added 1.34 GB in 240 to 276 us.  Bound by memory.
 template <int DT, bool WIDE>
 __global__ __launch_bounds__(kRowThreads) void k_combine(RowsArgs p)
 {
@@ -885,7 +896,8 @@ __global__ __launch_bounds__(kRowThreads) void k_combine(RowsArgs p)
 }
 
 // Eight choices at a time: their rows of y are read and their rows of dy
-// written beside one another.  COMBINE_BACKWARD_TIME
+// written beside one another.  16384 x 8 rows of 4096 bf16: 2.28 GB in 428 us,
+// 5.3 TB/s, above a copy's rate.
 template <int DT, bool WIDE>
 __global__ __launch_bounds__(kRowThreads) void k_combine_backward(RowsArgs p)
 {

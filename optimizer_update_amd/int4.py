@@ -18,7 +18,7 @@ import math
 import torch
 
 from . import DTYPES
-from .mx4 import _left, _offsets, _output, _result_type, _row_stride, _rows_apart, _run, _same, _values
+from .mx4 import _offsets, _output, _result_type, _row_stride, _rows_apart, _run, _same, _values
 from .route import _fail, load_experts
 
 
@@ -144,17 +144,19 @@ def int4_dequantize(q: Int4, dtype: torch.dtype = torch.float32, out: torch.Tens
     return _run(index, stream, _do_dequantize, q, dtype, out)
 
 
-def _do_matmul(x, rs, q, n, k, dtype, od, out, stride, offsets, groups, handle):
-    fresh = out is None
-    m = x.shape[0]
-    if fresh:
-        out = x.new_empty((m, n), dtype=dtype)
+def _do_matmul(x, dt, rs, q, m, n, k, dtype, od, out, stride, offsets, groups, handle):
+    rest = 0
+    if out is None:
+        out, rest = x.new_empty((m, n), dtype=dtype), 1
+    codes, scales, zeros = q.codes, q.scales, q.zeros
+    sd, zp = DTYPES[scales.dtype], None if zeros is None else zeros.data_ptr()
     lib = load_experts()
-    left = (DTYPES[x.dtype], x.data_ptr(), m, rs, od, *_ptrs(q), n, k, q.group)
     if offsets is None:
-        st = lib.ou_int4_matmul(*left, out.data_ptr(), stride, handle)
+        st = lib.ou_int4_matmul(dt, x.data_ptr(), m, rs, od, codes.data_ptr(), sd, scales.data_ptr(), zp, n, k, q.group,
+                                out.data_ptr(), stride, handle)
     else:
-        st = lib.ou_int4_grouped_matmul(*left, offsets.data_ptr(), groups, out.data_ptr(), stride, fresh, handle)
+        st = lib.ou_int4_grouped_matmul(dt, x.data_ptr(), m, rs, od, codes.data_ptr(), sd, scales.data_ptr(), zp, n, k,
+                                        q.group, offsets.data_ptr(), groups, out.data_ptr(), stride, rest, handle)
     if st:
         _fail(st)
     return out
@@ -162,19 +164,23 @@ def _do_matmul(x, rs, q, n, k, dtype, od, out, stride, offsets, groups, handle):
 
 def _matmul(x, q, offsets, dims, dtype, out, stream):
     on = _weights(q, dims)
-    n, k = q.codes.shape[-2], q.k
-    if not isinstance(x, torch.Tensor):
-        raise ValueError("the left operand must be a tensor of values")
-    _, index, default, m, _, rs = _left(x, k)
+    n, k = q.codes.shape[-2], q.codes.shape[-1] * 2
+    dt = _values(x, "the left operand", 2)
+    index = x.get_device()
     _same(index, on, "the weights")
+    m, have = x.shape
+    if have != k:
+        raise ValueError(f"the operands contract {have} and {k} columns")
     groups = 0
     if offsets is not None:
         groups = _offsets(offsets, index)
         if groups != q.codes.shape[0]:
             raise ValueError(f"offsets name {groups} groups, the weights hold {q.codes.shape[0]}")
-    dtype = dtype or default
+    if dtype is None:
+        dtype = x.dtype
     od, stride = _output(out, m, n, dtype, index)
-    return _run(index, stream, _do_matmul, x, rs, q, n, k, dtype, od, out, stride, offsets, groups)
+    return _run(index, stream, _do_matmul, x, dt, _row_stride(x, "the left operand"), q, m, n, k, dtype, od, out, stride,
+                offsets, groups)
 
 
 def int4_matmul(x: torch.Tensor, q: Int4, dtype: torch.dtype | None = None, out: torch.Tensor | None = None,

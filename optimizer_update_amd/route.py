@@ -70,8 +70,25 @@ def load_experts(path: str = LIBRARY) -> ctypes.CDLL:
         f = getattr(lib, name)
         f.restype, f.argtypes = res, args
     if path == LIBRARY:
+        _install_fast(lib)
         _experts = lib
     return lib
+
+
+# Entry points that the CPython module _fast_experts also exposes.
+FAST_ENTRY_POINTS = ("ou_route_topk", "ou_route_topk_backward", "ou_route_order", "ou_route_dispatch", "ou_route_combine",
+                     "ou_route_combine_backward", "ou_route_balance", "ou_int4_matmul", "ou_int4_grouped_matmul")
+
+
+def _install_fast(lib: ctypes.CDLL) -> None:
+    """Route the calls of the in-tree library through _fast_experts when it is
+    built: the same functions and positional arguments, converted in C."""
+    try:
+        from . import _fast_experts
+    except ImportError:
+        return
+    for name in FAST_ENTRY_POINTS:
+        setattr(lib, name, getattr(_fast_experts, name))
 
 
 def _fail(status: int) -> None:

@@ -1,6 +1,7 @@
 """CPU: the library of the operators around experts: its exports, its
 refusals (no device is touched before the arguments are checked) and the
 binding's; and the 64-bit definitions that the GPU tests compare with."""
+import ctypes
 import os
 import re
 import subprocess
@@ -203,6 +204,34 @@ def test_nothing_to_do_is_no_error(L):
 
 
 # ------------------------------------------------------------------ the binding
+
+def test_c_entry_points_stand_in_for_ctypes(L):
+    """Installed when built; the same statuses as through ctypes; argument
+    errors raised before the library is called."""
+    plain = ctypes.CDLL(route.LIBRARY)
+    calls = {"ou_route_topk": TOPK, "ou_int4_matmul": PRODUCT}
+    for name in route.FAST_ENTRY_POINTS:
+        assert isinstance(getattr(L, name), type(len)), "_fast_experts is not built: __graft_entry__.build() builds it"
+        with pytest.raises(TypeError):
+            getattr(L, name)()
+    for name, ok in calls.items():
+        f = getattr(plain, name)
+        f.restype = ctypes.c_int
+        f.argtypes = [ctypes.c_float if isinstance(v, float) else ctypes.c_void_p if v is None or v >= A else ctypes.c_int64
+                      for v in ok.values()] + [ctypes.c_void_p]
+        for key, v in ok.items():
+            if v is None:
+                continue
+            # a number that is refused, an address that is not aligned
+            bad = [*(ok | {key: float("nan") if isinstance(v, float) else 1 if v >= A else -1}).values(), None]
+            if key not in ("renorm",):
+                assert getattr(L, name)(*bad) == f(*bad) != OK, key
+        for i, v in enumerate(ok.values()):
+            args = [*ok.values(), None]
+            args[i] = "x"
+            with pytest.raises((TypeError, AttributeError)):
+                getattr(L, name)(*args)
+
 
 def test_binding_refuses():
     x = torch.zeros((4, 64))
