@@ -49,15 +49,19 @@ HIPCC_FLAGS = [
 
 def build(out_path: str = LIBRARY, extra_flags: list[str] | None = None, quiet: bool = True) -> str:
     """Compile the library (always; atomically replaces ``out_path``) and the
-    CPython module, and with the in-tree library those of the 4-bit operators
-    and of the operators around experts."""
+    CPython module, and with the in-tree library that of the 4-bit operators."""
     _compile(SOURCES, out_path, extra_flags, quiet)
     if out_path == LIBRARY:
         _compile(MX4_SOURCES, MX4_LIBRARY, extra_flags, quiet)
-        _compile(EXPERTS_SOURCES, EXPERTS_LIBRARY, extra_flags, quiet)
-        build_fast(FAST_EXPERTS, "pyexperts.c", "optimizer_experts")
     build_fast()
     return out_path
+
+
+def build_experts(extra_flags: list[str] | None = None, quiet: bool = True) -> str:
+    """Compile the library of the operators around experts and its CPython module."""
+    _compile(EXPERTS_SOURCES, EXPERTS_LIBRARY, extra_flags, quiet)
+    build_fast(FAST_EXPERTS, "pyexperts.c", "optimizer_experts")
+    return EXPERTS_LIBRARY
 
 
 def _compile(sources: list[str], out_path: str, extra_flags: list[str] | None, quiet: bool) -> None:
@@ -99,3 +103,4 @@ def build_fast(out_path: str = FAST, source: str = "pyfast.c", library: str = "o
 
 if __name__ == "__main__":
     print(build(quiet=False))
+    print(build_experts(quiet=False))
