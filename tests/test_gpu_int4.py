@@ -265,13 +265,16 @@ def test_captured_and_streams():
         assert torch.equal(y, want)
 
 
-def test_many_experts_past_32_bits():
+# codes in one kernel's steps and in the other's runs of tiles
+@pytest.mark.parametrize("e,n,k", [(136, 8192, 8192), (540, 8192, 2048)])
+def test_many_experts_past_32_bits(e, n, k):
     """Weights whose last matrices lie past 2^32 bytes."""
-    e, n, k = 136, 8192, 8192
     q = ou.Int4(torch.randint(0, 256, (e, n, k // 2), dtype=torch.uint8, device="cuda"),
                 torch.full((e, n, k // 128), 2.0 ** -6, dtype=BF16, device="cuda"), None, 128)
-    x = torch.randn((2, k), device="cuda").to(BF16)
+    x = torch.randn((4, k), device="cuda").to(BF16)
     off = torch.zeros(e + 1, dtype=torch.int32, device="cuda")
-    off[e] = 2
+    off[e] = 4
     y = ou.int4_grouped_matmul(x, q, off)
-    assert torch.equal(y, ou.int4_matmul(x, q[e - 1]))
+    last = ou.Int4(q.codes[e - 1].clone(), q.scales[e - 1].clone(), None, 128)
+    want, size = R.int4_product(R.host(x), last)
+    _check(y, want, size, k, BF16)
