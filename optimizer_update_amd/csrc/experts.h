@@ -73,8 +73,7 @@ struct Int4Args {
     const int32_t* offsets;
     int64_t m, n, k, x_stride, out_stride;
     int32_t group, experts, zero_rest, out_dtype, scale_dtype;
-    int32_t x_wide;         // 16-byte loads of x are allowed
-    int32_t out_wide;       // dequantisation: 16-byte stores are
+    int32_t out_wide;       // dequantisation: 16-byte stores are allowed
     int32_t tiles;          // of rows of weights a block, where x is held
 };
 
@@ -105,15 +104,16 @@ const void* balance_kernel();
 const void* int4_quantize_kernel(int dtype);
 const void* int4_dequantize_kernel(int dtype);
 
-// scales: groups of columns in 128 (1, 2 or 4); steps: of 128 columns in k.
-// may_hold: scales have 16 bits, and tiles are many.  held: a block takes
-// `tiles` tiles of 16 `held` columns of results; 0: 16 columns.
+// scales: groups of columns in 128 (1, 2 or 4); steps: of 128 columns in k; tiles:
+// of 16 rows of weights and 16 of x, about; half: scales have 16 bits.  A block
+// takes 16 `width` columns of results, `tiles` times with x held.
 struct Int4Kernel {
     const void* fn;
     int waves;
-    int held;
+    int width;
+    bool held;
 };
-Int4Kernel int4_matmul_kernel(int dtype, int scales, bool grouped, int64_t steps, bool may_hold);
+Int4Kernel int4_matmul_kernel(int dtype, int scales, bool grouped, int64_t steps, int64_t tiles, bool half);
 
 constexpr int kTopkWaves = 4;          // of a block
 constexpr int kOrderThreads = 512;

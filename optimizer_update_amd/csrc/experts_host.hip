@@ -340,11 +340,9 @@ int check_weights(int64_t n, int64_t k, int32_t group, int scale_dtype)
 double code_bytes(double n, int64_t k) { return n * static_cast<double>(k) / 2; }
 double scale_bytes(double n, int64_t k, int32_t group, int bytes) { return n * static_cast<double>(k / group) * bytes; }
 
-// From so many tiles of 16 rows of weights on x is held over runs of them, in
-// about so many blocks and up to 16 a run.  2001 tiles, k = 1024: 10.5 us by runs
-// of 4, 11.9 by 6, 16.6 by 2, 16.5 to 21 with x not held; 256 tiles, k = 4096: 7.4
-// us against 5.5; 512 rows, 64 experts, k = 2048: 80 by 8 or 16, 88 by 4.
-constexpr int64_t kInt4Held = 1024;
+// Where x is held: in about so many blocks, up to 16 tiles of 16 rows of weights a
+// block.  2001 tiles, k = 1024: 10.5 us by runs of 4, 11.9 by 6, 16.6 by 2; 512
+// rows, 64 experts, k = 2048: 80 by 8 or 16, 88 by 4.
 constexpr int64_t kInt4Blocks = 640;
 
 int int4_product(int dtype, Int4Args& p, void* stream)
@@ -366,16 +364,15 @@ int int4_product(int dtype, Int4Args& p, void* stream)
                            {"out", p.out, extent(p.m, p.n, p.out_stride, eo), static_cast<unsigned>(eo), true}};
     if (int st = check_buffers(bufs, 6)) return st;
     const int scales = p.group % 128 == 0 ? 1 : p.group % 64 == 0 ? 2 : 4;
-    p.x_wide = wide_rows(p.x, p.x_stride, 0, ex, 16);
+    const int64_t few = grouped ? (p.m < p.experts ? p.m : p.experts) : cut(p.m, 16);   // units with rows, about
+    const int64_t tiles = cut(p.n, 16) * few;
+    const Int4Kernel f = int4_matmul_kernel(dtype, scales, grouped, cut(p.k, 128), tiles, es == 2);
     // by groups: two more, the rows in front of the first and behind the last
     const int64_t units = grouped ? cut(p.m + 15 * static_cast<int64_t>(p.experts + 2), 16) : cut(p.m, 16);
-    const int64_t few = grouped ? (p.m < p.experts ? p.m : p.experts) : units;   // units with rows, about
-    const int64_t tiles = cut(p.n, 16) * few;
-    const Int4Kernel f = int4_matmul_kernel(dtype, scales, grouped, cut(p.k, 128), es == 2 && tiles >= kInt4Held);
-    const int64_t run = cut(tiles, kInt4Blocks), held = f.held ? f.held : 1;
-    p.tiles = static_cast<int32_t>(!f.held ? 1 : cut(run > 16 ? 16 : run, held));
+    const int64_t run = cut(tiles, kInt4Blocks);
+    p.tiles = static_cast<int32_t>(f.held ? cut(run > 16 ? 16 : run, f.width) : 1);
     void* args[] = {&p};
-    return launch({f.fn, units * cut(cut(p.n, 16 * held), p.tiles), 1, kWave * f.waves, "k_int4_matmul", 0}, args, stream);
+    return launch({f.fn, units * cut(cut(p.n, 16 * f.width), p.tiles), 1, kWave * f.waves, "k_int4_matmul", 0}, args, stream);
 }
 
 }  // namespace
@@ -438,7 +435,7 @@ OU_EXPORT int ou_int4_matmul(int dtype, const void* x, int64_t m, int64_t x_stri
                              int scale_dtype, const void* scales, const void* zeros, int64_t n, int64_t k, int32_t group,
                              void* out, int64_t out_stride, void* stream)
 {
-    Int4Args p{x, codes, scales, zeros, out, nullptr, m, n, k, x_stride, out_stride, group, 0, 0, out_dtype, scale_dtype, 0, 0, 1};
+    Int4Args p{x, codes, scales, zeros, out, nullptr, m, n, k, x_stride, out_stride, group, 0, 0, out_dtype, scale_dtype, 0, 1};
     return int4_product(dtype, p, stream);
 }
 
@@ -449,7 +446,7 @@ OU_EXPORT int ou_int4_grouped_matmul(int dtype, const void* x, int64_t m, int64_
 {
     if (int st = check_groups(offsets, experts, m)) return st;
     Int4Args p{x, codes, scales, zeros, out, offsets, m, n, k, x_stride, out_stride, group, experts, zero_rest != 0, out_dtype,
-               scale_dtype, 0, 0, 1};
+               scale_dtype, 0, 1};
     return int4_product(dtype, p, stream);
 }
 

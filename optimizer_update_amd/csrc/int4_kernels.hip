@@ -3,6 +3,8 @@
 //
 // codes [n][k / 2], the even column in the low four bits; value = (code -
 // zero) * scale, scales and zeros [n][k / group].
+#include <type_traits>
+
 #include "groups.hpp"
 #include "values.hpp"
 
@@ -168,20 +170,15 @@ struct Rows8 {
 #pragma unroll
         for (int i = 0; i < kWords / 4; ++i) w[i] = u32x4{0, 0, 0, 0};
     }
-    __device__ __forceinline__ void load(const typename Value<DT>::Elem* p, bool wide)
+    // of any alignment that the elements have: the device's loads need no more
+    __device__ __forceinline__ void load(const typename Value<DT>::Elem* p)
     {
-        if (wide) {
+        struct __attribute__((packed, aligned(sizeof(*p)))) Any {
+            u32x4 w[kWords / 4];
+        };
+        const Any v = *reinterpret_cast<const Any*>(p);
 #pragma unroll
-            for (int i = 0; i < kWords / 4; ++i) w[i] = reinterpret_cast<const u32x4*>(p)[i];
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) {
-            if constexpr (DT == kF32)
-                w[i / 4][i % 4] = __builtin_bit_cast(uint32_t, p[i]);
-            else
-                w[0][i] = static_cast<uint32_t>(p[2 * i]) | static_cast<uint32_t>(p[2 * i + 1]) << 16;
-        }
+        for (int i = 0; i < kWords / 4; ++i) w[i] = v.w[i];
     }
     // in the order of code_values()
     static __device__ __forceinline__ u32x4 ordered(u32x4 w)
@@ -244,25 +241,32 @@ __device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b)
     b = r[1];
 }
 
-// 16 rows of weights and 16 rows of x a block, the steps of 128 columns dealt to
-// its W waves in runs; U steps of a wave are in flight.  Lane group g (of 16
+// 16 NT rows of weights and 16 rows of x a block, the steps of 128 columns dealt
+// to its W waves in runs; U steps of a wave are in flight.  Lane group g (of 16
 // lanes) loads columns 32 g .. of a step, one request of 64 bytes a row; the
 // groups then exchange registers so that register i of group g holds columns
 // 32 i + 8 g .., for two reasons: an instruction's 32 columns are of one group of
 // columns, and x is asked for by 64 bytes a row (by 16 where the codes were
 // loaded).  S groups of columns are in a step: a lane group loads the scale of
-// one of four in a row, and a lane gets its row's from there.  For few tiles,
-// long rows, and scales in binary32.  One token, 4096 x 4096 bf16: 5.5 us, with
-// four steps in flight 5.9, with x held 7.4.
-template <int DT, int S, int W, int U, bool GROUPED>
+// one of four in a row, and a lane gets its row's from there.  HALF: scales have
+// 16 bits.  No load of the steady loop stands behind a condition: the compiler
+// could not tell how many are younger than the one that it waits for, and would
+// wait for all; what is not there is loaded from elsewhere and does not count.
+// One token, 4096 x 4096 bf16: 5.6 us, 9 MB at 1.6 TB/s, bound by the latency of
+// launch and first loads; 32000 x 4096 21 us, 70 MB at 3.3 TB/s, 16 rows 25.8 us,
+// 64 rows x 14336 x 4096 44 us, where codes become operands for every 16 rows.
+// 32 or 64 rows a block instead were slower up to 64 rows (32 rows x 14336 x 4096:
+// 42 and 52 us by one tile of weights, 27 and 31 by two, 24 as it is).
+template <int DT, int S, int W, int U, int NT, bool HALF, bool GROUPED>
 __global__ __launch_bounds__(kWave * W) void k_int4_matmul(Int4Args p)
 {
-    constexpr int P = Rows8<DT>::kParts;
+    constexpr int P = Rows8<DT>::kParts, T = U > 4 / S ? U : 4 / S;   // T: steps of a turn of the loop
     using Elem = typename Value<DT>::Elem;
-    __shared__ f32x4 sums[W][kWave];
+    using Bits = std::conditional_t<HALF, uint16_t, uint32_t>;
+    __shared__ f32x4 sums[W][NT][kWave];
     const int t = static_cast<int>(threadIdx.x), lane = t & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-    const uint32_t n_tiles = static_cast<uint32_t>((p.n + 15) / 16);
+    const uint32_t n_tiles = static_cast<uint32_t>((p.n + 16 * NT - 1) / (16 * NT));
     const uint32_t unit = blockIdx.x / n_tiles, ntile = blockIdx.x - unit * n_tiles;
     int64_t row0 = static_cast<int64_t>(unit) * 16, mrows = p.m - row0, matrix = 0;
     if constexpr (GROUPED) {
@@ -274,99 +278,136 @@ __global__ __launch_bounds__(kWave * W) void k_int4_matmul(Int4Args p)
         if (matrix < 0 && !p.zero_rest) return;
     }
     const int rows = mrows < 16 ? static_cast<int>(mrows) : 16;
-    const int64_t n0 = static_cast<int64_t>(ntile) * 16, columns = p.k / p.group;
-    const int chunks = GROUPED && matrix < 0 ? 0 : static_cast<int>((p.k + kChunk - 1) / kChunk);
+    const int64_t n0 = static_cast<int64_t>(ntile) * (16 * NT);
+    const uint32_t columns = static_cast<uint32_t>(p.k / p.group), k = static_cast<uint32_t>(p.k);
+    const int chunks = GROUPED && matrix < 0 ? 0 : static_cast<int>((k + kChunk - 1) / kChunk);
     const int run = (chunks + W - 1) / W, first = wave * run, last = first + run < chunks ? first + run : chunks;
-    // rows behind the edge read the last one
-    const int64_t n = (n0 + r < p.n ? n0 + r : p.n - 1) + (GROUPED && matrix > 0 ? matrix * p.n : 0);
-    const uint8_t* const codes = p.codes + n * (p.k / 2) + g * 16;
-    const int64_t scale_row = n * columns;
-    const bool live = r < rows;   // rows behind the last one are 0 and not loaded
-    const Elem* const x = static_cast<const Elem*>(p.x) + (row0 + (live ? r : 0)) * p.x_stride + g * 8;
+    // rows behind the edge read the last one (of weights) or the first (of x), columns the last 32
+    const uint8_t* codes[NT];
+    const Bits *scales[NT], *zeros[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const int64_t n = (n0 + 16 * j + r < p.n ? n0 + 16 * j + r : p.n - 1) + (GROUPED && matrix > 0 ? matrix * p.n : 0);
+        codes[j] = p.codes + n * (p.k / 2);
+        scales[j] = static_cast<const Bits*>(p.scales) + n * columns;
+        zeros[j] = p.zeros ? static_cast<const Bits*>(p.zeros) + n * columns : scales[j];
+    }
+    const Elem* const x = static_cast<const Elem*>(p.x) + (row0 + (r < rows ? r : 0)) * p.x_stride + g * 8;
     struct Step {
-        u32x4 c;
+        u32x4 c[NT];
         Rows8<DT> x[4];
     } step[U];
     auto load = [&](Step& s, int at) {
-        const int64_t k0 = static_cast<int64_t>(at) * kChunk;
-        const bool whole = k0 + kChunk <= p.k;
-        s.c = whole || k0 + g * 32 < p.k ? __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(codes + k0 / 2)) : u32x4{0, 0, 0, 0};
+        const uint32_t k0 = static_cast<uint32_t>(at) * kChunk, mine = k0 + static_cast<uint32_t>(g) * 32;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            s.x[q].zero();
-            if (live && (whole || k0 + q * 32 < p.k)) s.x[q].load(x + k0 + q * 32, p.x_wide);
-        }
+        for (int j = 0; j < NT; ++j)
+            s.c[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(codes[j] + (mine < k ? mine : k - 32) / 2));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) s.x[q].load(x + (k0 + q * 32 < k ? k0 + q * 32 : k - 32));
     };
     // scale and zero of the group of columns `4 at + g` of the wave's run
-    float scale = 0.0f, zero = 8.0f;
-    uint32_t next_scale = 0, next_zero = 0;   // their bits
+    float scale[NT], zero[NT];
+    Bits next_scale[NT], next_zero[NT];
     auto load_scales = [&](int at) {
-        const uint32_t k = static_cast<uint32_t>(first) * kChunk + static_cast<uint32_t>(4 * at + g) * (kChunk / S);
-        const uint32_t of = k / static_cast<uint32_t>(p.group), most = static_cast<uint32_t>(columns) - 1;
-        const uint32_t column = of < most ? of : most;
-        next_scale = load_bits(p.scales, scale_row + column, p.scale_dtype);
-        if (p.zeros) next_zero = load_bits(p.zeros, scale_row + column, p.scale_dtype);
+        const uint32_t from = static_cast<uint32_t>(first) * kChunk + static_cast<uint32_t>(4 * at + g) * (kChunk / S);
+        const uint32_t of = from / static_cast<uint32_t>(p.group), column = of < columns ? of : columns - 1;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            next_scale[j] = scales[j][column];
+            next_zero[j] = zeros[j][column];
+        }
     };
-    f32x4 y{0, 0, 0, 0};
+    f32x4 y[NT] = {};
     constexpr uint32_t kOne = DT == kF16 ? 0x3c003c00u : 0x3f803f80u;
     const u32x4 ones{kOne, kOne, kOne, kOne};
-    auto compute = [&](Step& s, int at) {
+    auto compute = [&](const Step& s, int at) {
         const int of = (at - first) * S;   // the step's first group of columns in the run
-        if (of % 4 == 0) {
-            scale = bits_value(next_scale, p.scale_dtype);
-            zero = p.zeros ? bits_value(next_zero, p.scale_dtype) : 8.0f;
-            if (at + 4 / S < last) load_scales(of / 4 + 1);
+        f32x4 sum[NT][S] = {}, plain[S] = {};
+        uint32_t word[NT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            uint32_t c0 = s.c[j][0], c1 = s.c[j][1], c2 = s.c[j][2], c3 = s.c[j][3];
+            swap32(c0, c2);
+            swap32(c1, c3);
+            swap16(c0, c1);
+            swap16(c2, c3);
+            word[j][0] = c0;
+            word[j][1] = c1;
+            word[j][2] = c2;
+            word[j][3] = c3;
         }
-        f32x4 sum[S] = {}, plain[S] = {};
-        uint32_t c0 = s.c[0], c1 = s.c[1], c2 = s.c[2], c3 = s.c[3];
-        swap32(c0, c2);
-        swap32(c1, c3);
-        swap16(c0, c1);
-        swap16(c2, c3);
-        const uint32_t word[4] = {c0, c1, c2, c3};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             constexpr int kPer = 4 / S;
+            u32x4 b[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) b[j] = code_values<DT>(word[j][q]);
             u32x4 a[P];
             s.x[q].operands(a);
-            const u32x4 b = code_values<DT>(word[q]);
 #pragma unroll
             for (int h = 0; h < P; ++h) {
                 plain[q / kPer] = multiply<DT>(a[h], ones, plain[q / kPer]);
-                sum[q / kPer] = multiply<DT>(a[h], b, sum[q / kPer]);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) sum[j][q / kPer] = multiply<DT>(a[h], b[j], sum[j][q / kPer]);
             }
         }
 #pragma unroll
         for (int q = 0; q < S; ++q) {
+            if (S > 1 && static_cast<uint32_t>(at) * kChunk + q * (kChunk / S) >= k) continue;   // k is a whole number of them
             const int from = ((of + q) & 3) * 64 + r * 4;   // the lane that has them
-            const float sc = __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(from, __builtin_bit_cast(int, scale)));
-            const float ze = __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(from, __builtin_bit_cast(int, zero)));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(sc, __builtin_fmaf(-ze, plain[q][e], sum[q][e]), y[e]);
+            for (int j = 0; j < NT; ++j) {
+                const float sc = __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(from, __builtin_bit_cast(int, scale[j])));
+                const float ze = __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(from, __builtin_bit_cast(int, zero[j])));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[j][e] = __builtin_fmaf(sc, __builtin_fmaf(-ze, plain[q][e], sum[j][q][e]), y[j][e]);
+            }
         }
     };
-    if (first < last) load_scales(0);
+    int at = first;
+    auto turn = [&](auto steady) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (first + u < last) load(step[u], first + u);
-    for (int at = first; at < last; at += U) {
+        for (int u = 0; u < T; ++u) {
+            if (!steady.value && at + u >= last) break;
+            if (u * S % 4 == 0) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (at + u >= last) break;
-            compute(step[u], at + u);
-            if (at + u + U < last) load(step[u], at + u + U);
+                for (int j = 0; j < NT; ++j) {
+                    scale[j] = bits_value(next_scale[j], p.scale_dtype);
+                    zero[j] = p.zeros ? bits_value(next_zero[j], p.scale_dtype) : 8.0f;
+                }
+                if (steady.value || at + u + 4 / S < last) load_scales((at + u - first) * S / 4 + 1);
+            }
+            compute(step[u % U], at + u);
+            if (steady.value || at + u + U < last) load(step[u % U], at + u + U);
         }
-    }
-    sums[wave][lane] = y;
-    __syncthreads();
-    if (wave) return;
+        at += T;
+    };
+    if (first + U + T <= last) {
+        load_scales(0);
 #pragma unroll
-    for (int w = 1; w < W; ++w) y += sums[w][lane];
-    if (n0 + r >= p.n) return;
+        for (int u = 0; u < U; ++u) load(step[u], first + u);
+        do turn(std::true_type{});
+        while (at + U + T <= last);
+    } else if (first < last) {
+        load_scales(0);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (first + u < last) load(step[u], first + u);
+    }
+    while (at < last) turn(std::false_type{});
+#pragma unroll
+    for (int j = 0; j < NT; ++j) sums[wave][j][lane] = y[j];
+    __syncthreads();
+    static_assert(NT <= W, "a wave adds up 16 by 16 results");
+    const int64_t column = n0 + 16 * wave + r;
+    if (wave >= NT || column >= p.n) return;
+    f32x4 out = sums[0][wave][lane];
+#pragma unroll
+    for (int w = 1; w < W; ++w) out += sums[w][wave][lane];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const int row = g * 4 + e;
-        if (row < rows) store_value(p.out, (row0 + row) * p.out_stride + n0 + r, y[e], p.out_dtype);
+        if (row < rows) store_value(p.out, (row0 + row) * p.out_stride + column, out[e], p.out_dtype);
     }
 }
 
@@ -374,12 +415,10 @@ __global__ __launch_bounds__(kWave * W) void k_int4_matmul(Int4Args p)
 // rows of weights one after the other, its W waves RC steps each of the
 // columns, whose x they keep in registers; codes of the next two tiles are on
 // their way.  The waves' sums meet in LDS, and the waves take turns at adding
-// them up.  No load of the steady loop stands behind a condition (the type of
-// the scales has 16 bits, what is not there is loaded from elsewhere): the
-// compiler could not tell how many are younger than the one that it waits for,
-// and would wait for all.  The waves load the scales of 16 NT / W rows each, whole
-// rows of them, and share them through LDS: when each loaded what it multiplies,
-// they were 16 requests like the codes' own (21 us of 75 without any
+// them up.  Here too no load of the steady loop stands behind a condition (the
+// type of the scales has 16 bits).  The waves load the scales of 16 NT / W rows
+// each, whole rows of them, and share them through LDS: when each loaded what it
+// multiplies, they were 16 requests like the codes' own (21 us of 75 without any
 // arithmetic); they are asked for a tile ahead of the codes.
 // 512 rows over 64 experts, k = 2048, n = 4096 bf16: 80 us, 302 MB of codes and
 // scales (experts of more than 16 rows read twice), 3.8 TB/s.  Loads alone take 58
@@ -488,7 +527,7 @@ __global__ __launch_bounds__(kWave * W) void k_int4_tiles(Int4Args p)
         for (int q = 0; q < 4; ++q) {
             Rows8<DT> v;
             v.zero();
-            if (r < rows && c < count && static_cast<int64_t>(first + c) * kChunk + q * 32 < p.k) v.load(x + c * kChunk + q * 32, p.x_wide);
+            if (r < rows && c < count && static_cast<int64_t>(first + c) * kChunk + q * 32 < p.k) v.load(x + c * kChunk + q * 32);
             v.operands(a[c][q]);
         }
     }
@@ -610,39 +649,68 @@ const void* int4_dequantize_kernel(int dtype)
 
 namespace {
 
-template <int DT, int S, bool GROUPED>
-Int4Kernel choose_waves(int64_t steps, bool held)
+// x streams past 4 tiles of rows of weights from 1024 tiles on, past 2 from 512:
+// one row, k = 4096: 256 tiles 5.6 us by one, 7.3 by two; 896 tiles 13.8, 11.5,
+// 11.7 by four; 16 rows 23.0, 16.7, 13.8; 2000 tiles 43, 30, 25.8.  Four waves
+// do by four what eight take 10 % longer for.  Binary32 with small groups by two
+// at most: the sums of four leave one wave a SIMD.
+template <int DT, int S, bool HALF, bool GROUPED>
+Int4Kernel choose_width(int64_t tiles)
 {
-    constexpr int RC = DT == kF32 ? 2 : 4;   // steps whose x is held, 64 or 48 registers of it
-    // 2001 tiles of 8 steps: eight waves of one 10.5 us by pairs of tiles, 11.2 by
-    // single ones, four waves of two 11.6 and 12.8.  16 steps, 64 experts: four
-    // waves of four 80 us, by pairs 95, eight of two 96, by pairs 82.
-    if (held && steps <= 8) return {reinterpret_cast<const void*>(k_int4_tiles<DT, S, 2, 8, 1, GROUPED>), 8, 2};
-    if constexpr (RC == 4)
-        if (held && steps <= 16) return {reinterpret_cast<const void*>(k_int4_tiles<DT, S, 1, 4, 4, GROUPED>), 4, 1};
-    if (held && steps <= 8 * RC) return {reinterpret_cast<const void*>(k_int4_tiles<DT, S, 1, 8, RC, GROUPED>), 8, 1};
-    return {reinterpret_cast<const void*>(k_int4_matmul<DT, S, 8, 2, GROUPED>), 8, 0};
+    if constexpr (DT != kF32 || S == 1)
+        if (tiles >= 1024) return {reinterpret_cast<const void*>(k_int4_matmul<DT, S, 4, 2, 4, HALF, GROUPED>), 4, 4, false};
+    if (tiles >= 512) return {reinterpret_cast<const void*>(k_int4_matmul<DT, S, 8, 2, 2, HALF, GROUPED>), 8, 2, false};
+    return {reinterpret_cast<const void*>(k_int4_matmul<DT, S, 8, 2, 1, HALF, GROUPED>), 8, 1, false};
 }
+
+// x is held where tiles are many and the waves' registers of it are filled.  8
+// steps: 2001 tiles 11.8 us, streamed 13.6, but 1024 tiles 8.2 and 6.2, and 6 steps,
+// 6144 tiles 25.9 and 23.9.  16 steps: 16384 tiles 77 and 88, 8000 tiles 45 and 50,
+// 4096 tiles 20.2 and 19.1, 2000 tiles 16.5 and 15.6, 12 steps 78 and 73.  Streamed binary32 is taken
+// apart for every tile, which small groups of columns leave no time for: 16 steps,
+// groups of 64, 16384 tiles 125 and 183 us, of 128 149 and 126.
 template <int DT, int S>
-Int4Kernel choose_grouped(bool grouped, int64_t steps, bool held)
+constexpr bool holds(int64_t steps, int64_t tiles)
 {
-    return grouped ? choose_waves<DT, S, true>(steps, held) : choose_waves<DT, S, false>(steps, held);
+    if (DT == kF32 && S > 1) return steps <= 16 && tiles >= 1536;
+    return steps > 6 && steps <= 8 ? tiles >= 1536 : DT != kF32 && steps > 12 && steps <= 16 && tiles >= 6144;
+}
+
+template <int DT, int S, bool GROUPED>
+Int4Kernel choose(int64_t steps, int64_t tiles, bool half)
+{
+    if (!half) return choose_width<DT, S, false, GROUPED>(tiles);
+    if (holds<DT, S>(steps, tiles)) {
+        // 2001 tiles of 8 steps: eight waves of one 10.5 us by pairs of tiles, 11.2 by
+        // single ones, four waves of two 11.6 and 12.8.  16 steps, 64 experts: four
+        // waves of four 80 us, by pairs 95, eight of two 96, by pairs 82.
+        if (steps <= 8) return {reinterpret_cast<const void*>(k_int4_tiles<DT, S, 2, 8, 1, GROUPED>), 8, 2, true};
+        if constexpr (DT != kF32)
+            return {reinterpret_cast<const void*>(k_int4_tiles<DT, S, 1, 4, 4, GROUPED>), 4, 1, true};
+        else if constexpr (S > 1)
+            return {reinterpret_cast<const void*>(k_int4_tiles<DT, S, 1, 8, 2, GROUPED>), 8, 1, true};
+    }
+    return choose_width<DT, S, true, GROUPED>(tiles);
 }
 template <int DT>
-Int4Kernel choose_scales(int scales, bool grouped, int64_t steps, bool held)
+Int4Kernel choose(int scales, bool grouped, int64_t steps, int64_t tiles, bool half)
 {
-    return scales == 1   ? choose_grouped<DT, 1>(grouped, steps, held)
-           : scales == 2 ? choose_grouped<DT, 2>(grouped, steps, held)
-                         : choose_grouped<DT, 4>(grouped, steps, held);
+    if (grouped)
+        return scales == 1   ? choose<DT, 1, true>(steps, tiles, half)
+               : scales == 2 ? choose<DT, 2, true>(steps, tiles, half)
+                             : choose<DT, 4, true>(steps, tiles, half);
+    return scales == 1   ? choose<DT, 1, false>(steps, tiles, half)
+           : scales == 2 ? choose<DT, 2, false>(steps, tiles, half)
+                         : choose<DT, 4, false>(steps, tiles, half);
 }
 
 }  // namespace
 
-Int4Kernel int4_matmul_kernel(int dtype, int scales, bool grouped, int64_t steps, bool held)
+Int4Kernel int4_matmul_kernel(int dtype, int scales, bool grouped, int64_t steps, int64_t tiles, bool half)
 {
-    return dtype == kF32   ? choose_scales<kF32>(scales, grouped, steps, held)
-           : dtype == kF16 ? choose_scales<kF16>(scales, grouped, steps, held)
-                           : choose_scales<kBF16>(scales, grouped, steps, held);
+    return dtype == kF32   ? choose<kF32>(scales, grouped, steps, tiles, half)
+           : dtype == kF16 ? choose<kF16>(scales, grouped, steps, tiles, half)
+                           : choose<kBF16>(scales, grouped, steps, tiles, half);
 }
 
 }  // namespace experts

@@ -121,6 +121,108 @@ def test_matmul_of_many_tiles(dtype):
     _check(ou.int4_matmul(x.cuda(), q), want, size, 512, dtype)
 
 
+def _some_rows(q, rows):
+    return ou.Int4(q.codes[rows].clone(), q.scales[rows].clone(), None if q.zeros is None else q.zeros[rows].clone(), q.group)
+
+
+# two and four tiles of weights a block, runs of columns that end inside a turn or a step, edges inside a block
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("scales", [F32, BF16])
+@pytest.mark.parametrize("zeros", [True, False])
+@pytest.mark.parametrize("m,n,k,group", [(1, 8200, 6304, 32), (17, 4117, 6400, 64), (20, 8200, 6528, 128), (3, 16400, 4192, 32),
+                                         (5, 16390, 1600, 64), (40, 6007, 1344, 96)])
+def test_matmul_of_wide_blocks(m, n, k, group, zeros, scales, dtype):
+    print("int4 wide blocks", m, n, k, group, zeros, scales, dtype, flush=True)
+    q = _weights((n,), k, group, scales, zeros)
+    x = (torch.randn((m, k), generator=_gen(1)) * torch.exp2(torch.randn(k, generator=_gen(2)))).to(dtype)
+    xd = x.cuda()
+    y = ou.int4_matmul(xd, q)
+    at = [*range(0, 70), *range(90, n - 80, 271), *range(n - 80, n)]
+    want, size = R.int4_product(R.host(x), _some_rows(q, at))
+    _check(y[:, at], want, size, k, dtype)
+    odd = torch.zeros((m, k + 3), dtype=dtype, device="cuda")
+    odd[:, 1:1 + k] = xd
+    room = torch.full((m, n + 3), 9.0, dtype=dtype, device="cuda")
+    ou.int4_matmul(odd[:, 1:1 + k], q, out=room[:, 1:1 + n])
+    assert torch.equal(room[:, 1:1 + n], y) and (room[:, 0] == 9).all() and (room[:, 1 + n:] == 9).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("scales", [F32, F16])
+@pytest.mark.parametrize("zeros", [True, False])
+@pytest.mark.parametrize("counts,n,k,group", [([3, 0, 17, 1] * 8, 520, 4224, 128), ([2] * 16, 515, 4160, 64), ([2, 18] * 9, 907, 3232, 32),
+                                              ([1, 0, 30] * 6, 1000, 2112, 64)])
+def test_grouped_matmul_of_wide_blocks(counts, n, k, group, zeros, scales, dtype):
+    print("int4 grouped wide blocks", len(counts), n, k, group, zeros, scales, dtype, flush=True)
+    e, front, behind = len(counts), 2, 19
+    m = front + sum(counts) + behind
+    q = _weights((e, n), k, group, scales, zeros)
+    x = torch.randn((m, k), generator=_gen(1)).to(dtype)
+    at = front + np.concatenate([[0], np.cumsum(counts)])
+    offsets = torch.tensor(at, dtype=torch.int32).cuda()
+    y = ou.int4_grouped_matmul(x.cuda(), q, offsets)
+    room = torch.full((m, n + 1), 3.0, dtype=dtype, device="cuda")
+    ou.int4_grouped_matmul(x.cuda(), q, offsets, out=room[:, :n])
+    assert (y[:front] == 0).all() and (y[at[-1]:] == 0).all()
+    assert (room[:front] == 3).all() and (room[at[-1]:] == 3).all() and (room[:, n] == 3).all()
+    assert torch.equal(room[front:at[-1], :n], y[front:at[-1]])
+    for i in (0, 2, e - 1):
+        want, size = R.int4_product(R.host(x[at[i]:at[i + 1]]), q[i])
+        _check(y[at[i]:at[i + 1]], want, size, k, dtype)
+
+
+# 16-bit scales, tiles enough for x to be held: 7 to 8 and 13 to 16 steps, all or some of the waves' registers filled
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("scales", [F16, BF16])
+@pytest.mark.parametrize("zeros", [True, False])
+@pytest.mark.parametrize("m,n,k,group", [(3, 24593, 1024, 32), (17, 12300, 928, 32), (2, 25000, 896, 128), (1, 24600, 960, 64),
+                                         (16, 98320, 2048, 128), (40, 32790, 1632, 96)])
+def test_matmul_with_rows_held(m, n, k, group, zeros, scales, dtype):
+    print("int4 held", m, n, k, group, zeros, scales, dtype, flush=True)
+    q = _weights((n,), k, group, scales, zeros)
+    x = (torch.randn((m, k), generator=_gen(1)) * torch.exp2(torch.randn(k, generator=_gen(2)))).to(dtype)
+    xd = x.cuda()
+    y = ou.int4_matmul(xd, q)
+    at = [*range(0, 70), *range(90, n - 300, 271), *range(n - 300, n)]
+    want, size = R.int4_product(R.host(x), _some_rows(q, at))
+    _check(y[:, at], want, size, k, dtype)
+    odd = torch.zeros((m, k + 3), dtype=dtype, device="cuda")
+    odd[:, 1:1 + k] = xd
+    assert torch.equal(ou.int4_matmul(odd[:, 1:1 + k], q), y)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("scales", [F16, BF16])
+@pytest.mark.parametrize("zeros", [True, False])
+@pytest.mark.parametrize("counts,n,k,group", [([3, 0, 17, 1] * 12, 2100, 2048, 128), ([2] * 48, 2063, 1632, 32), ([18, 1] * 24, 2085, 1984, 64),
+                                              ([1, 0, 30] * 8, 1100, 1024, 64)])
+def test_grouped_matmul_with_rows_held(counts, n, k, group, zeros, scales, dtype):
+    print("int4 grouped held", len(counts), n, k, group, zeros, scales, dtype, flush=True)
+    e, front, behind = len(counts), 2, 19
+    m = front + sum(counts) + behind
+    q = _weights((e, n), k, group, scales, zeros)
+    x = torch.randn((m, k), generator=_gen(1)).to(dtype)
+    at = front + np.concatenate([[0], np.cumsum(counts)])
+    y = ou.int4_grouped_matmul(x.cuda(), q, torch.tensor(at, dtype=torch.int32).cuda())
+    assert (y[:front] == 0).all() and (y[at[-1]:] == 0).all()
+    for i in (0, 2, e - 1):
+        want, size = R.int4_product(R.host(x[at[i]:at[i + 1]]), q[i])
+        _check(y[at[i]:at[i + 1]], want, size, k, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("scales", [F32, BF16])
+@pytest.mark.parametrize("n", [8192, 16384])
+def test_rows_do_not_mix_in_wide_blocks(n, scales, dtype):
+    q = _weights((n,), 1056, 32, scales, True)
+    x = torch.randn((5, 1056), generator=_gen(3)).to(dtype).cuda()
+    y = ou.int4_matmul(x, q)
+    # the first row stands in for those that are not there, the last columns for those behind them
+    x[0, 3], x[3, 1055] = float("nan"), float("inf")
+    z = ou.int4_matmul(x, q)
+    assert not torch.isfinite(z[[0, 3]]).any() and torch.equal(y[[1, 2, 4]], z[[1, 2, 4]])
+
+
 def test_grouped_matmul_with_offsets_that_fall_or_leave():
     q = _weights((4, 24), 64, 64, F32, True)
     x = torch.randn((40, 64), generator=_gen(1)).cuda()
@@ -274,6 +376,20 @@ def test_many_experts_past_32_bits(e, n, k):
     x = torch.randn((4, k), device="cuda").to(BF16)
     off = torch.zeros(e + 1, dtype=torch.int32, device="cuda")
     off[e] = 4
+    y = ou.int4_grouped_matmul(x, q, off)
+    last = ou.Int4(q.codes[e - 1].clone(), q.scales[e - 1].clone(), None, 128)
+    want, size = R.int4_product(R.host(x), last)
+    _check(y, want, size, k, BF16)
+
+
+def test_held_rows_past_32_bits():
+    """As above, by the kernel that holds x over many tiles."""
+    e, n, k = 540, 8192, 2048
+    q = ou.Int4(torch.randint(0, 256, (e, n, k // 2), dtype=torch.uint8, device="cuda"),
+                torch.full((e, n, k // 128), 2.0 ** -6, dtype=BF16, device="cuda"), None, 128)
+    x = torch.randn((16, k), device="cuda").to(BF16)
+    off = torch.zeros(e + 1, dtype=torch.int32, device="cuda")
+    off[e] = 16
     y = ou.int4_grouped_matmul(x, q, off)
     last = ou.Int4(q.codes[e - 1].clone(), q.scales[e - 1].clone(), None, 128)
     want, size = R.int4_product(R.host(x), last)
