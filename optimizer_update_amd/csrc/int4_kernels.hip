@@ -649,17 +649,21 @@ const void* int4_dequantize_kernel(int dtype)
 
 namespace {
 
-// x streams past 4 tiles of rows of weights from 1024 tiles on, past 2 from 512:
-// one row, k = 4096: 256 tiles 5.6 us by one, 7.3 by two; 896 tiles 13.8, 11.5,
-// 11.7 by four; 16 rows 23.0, 16.7, 13.8; 2000 tiles 43, 30, 25.8.  Four waves
-// do by four what eight take 10 % longer for.  Binary32 with small groups by two
-// at most: the sums of four leave one wave a SIMD.
+// x streams past 4 tiles of rows of weights from 896 tiles on, past 2 from 512.  One
+// row, k = 4096, groups of 128: 256 tiles 5.6 us by one, 7.3 by two; 896 tiles 13.8,
+// 11.5, 11.7 by four; 16 rows 23.0, 16.7, 13.8; 512 tiles, k = 8192, 23.1, 17.2,
+// 23.5; 2000 tiles 43, 30, 25.8.  Groups of 32, 2000 tiles of 16 rows: 43.7 by two,
+// 40.1 by four, one row 34.1 and 37.8.  Four waves do by four what eight take 10 %
+// longer for, and by two where smaller groups take the registers for a second block
+// of eight: 768 tiles, k = 2560, groups of 64, 10.3 and 12.5.  Binary32 with small
+// groups by two at most: the sums of four leave one wave a SIMD.
 template <int DT, int S, bool HALF, bool GROUPED>
 Int4Kernel choose_width(int64_t tiles)
 {
     if constexpr (DT != kF32 || S == 1)
-        if (tiles >= 1024) return {reinterpret_cast<const void*>(k_int4_matmul<DT, S, 4, 2, 4, HALF, GROUPED>), 4, 4, false};
-    if (tiles >= 512) return {reinterpret_cast<const void*>(k_int4_matmul<DT, S, 8, 2, 2, HALF, GROUPED>), 8, 2, false};
+        if (tiles >= 896) return {reinterpret_cast<const void*>(k_int4_matmul<DT, S, 4, 2, 4, HALF, GROUPED>), 4, 4, false};
+    constexpr int W = S == 1 ? 8 : 4;
+    if (tiles >= 512) return {reinterpret_cast<const void*>(k_int4_matmul<DT, S, W, 2, 2, HALF, GROUPED>), W, 2, false};
     return {reinterpret_cast<const void*>(k_int4_matmul<DT, S, 8, 2, 1, HALF, GROUPED>), 8, 1, false};
 }
 
