@@ -89,6 +89,7 @@ def _ptrs(q: Int4) -> tuple:
 
 def _do_quantize(x, lead, rows, k, group, dtype, zeros, handle):
     device = x.device
+    x = _rows_apart(x.reshape(rows, k))   # a copy, where it takes one, is made on the call's stream
     codes = torch.empty((*lead, k // 2), dtype=torch.uint8, device=device)
     scales = torch.empty((*lead, k // group), dtype=dtype, device=device)
     z = torch.empty_like(scales) if zeros else None
@@ -114,9 +115,7 @@ def int4_quantize(x: torch.Tensor, group: int = 128, zeros: bool = True, dtype: 
     group = int(group)
     if group < 32 or group % 32 or k % group:
         raise ValueError(f"group must be a multiple of 32 that divides K = {k}: got {group}")
-    rows = math.prod(lead)
-    flat = _rows_apart(x.detach().reshape(rows, k) if x.dim() == 3 else x.detach())
-    return _run(x.get_device(), stream, _do_quantize, flat, lead, rows, k, group, dtype, bool(zeros))
+    return _run(x.get_device(), stream, _do_quantize, x.detach(), lead, math.prod(lead), k, group, dtype, bool(zeros))
 
 
 def _do_dequantize(q, dtype, out, handle):
