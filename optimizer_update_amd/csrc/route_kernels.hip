@@ -301,7 +301,9 @@ __global__ __launch_bounds__(kTopkWaves * kWave) void k_topk(TopkArgs p)
             for (int h = 0; h < 4; ++h) c[i + h] += b[h];
         }
     }
+    const uint64_t rows = L == 64 ? ~uint64_t(0) : ((uint64_t(1) << (L & 63)) - 1) << (row * L);
     float hi = -kInf, lo = kInf, odd = 0.0f;
+    bool none = false;   // no expert is there: by the logits, since the extremes pass over a NaN, which counts as one
     if (full) {
 #pragma unroll
         for (int i = 0; i < V; i += 2) {
@@ -316,12 +318,15 @@ __global__ __launch_bounds__(kTopkWaves * kWave) void k_topk(TopkArgs p)
             lo = min3(lo, v[i] == -kInf ? kInf : c[i], v[i + 1] == -kInf ? kInf : c[i + 1]);
             odd += c[i] + c[i + 1];
         }
+        bool some = false;
+#pragma unroll
+        for (int i = 0; i < V; ++i) some |= v[i] != -kInf;
+        none = !(__ballot(some) & rows);
     }
     hi = lanes_max<L>(hi);
     lo = -lanes_max<L>(-lo);
     odd = lanes_sum<L>(odd);
     if (!by_logit) error += fmaxf(fabsf(hi), fabsf(lo)) * 0x1p-23f;
-    const bool none = hi == -kInf;
     bool sure = fabsf(odd) < kInf || none;
     // steps of c from `base` on; a base that is far from 0 is rounded for all
     // alike, by 64 steps at most
@@ -420,7 +425,6 @@ __global__ __launch_bounds__(kTopkWaves * kWave) void k_topk(TopkArgs p)
     }
     // Candidates: choice `sub` and, behind the choices, those left out.
     auto index_of = [](uint32_t key) { return static_cast<int>(kExperts - 1 - (key & (kExperts - 1))); };
-    const uint64_t rows = L == 64 ? ~uint64_t(0) : ((uint64_t(1) << (L & 63)) - 1) << (row * L);
     bool has = own >> kIndex;
     int chosen = has && sub < k ? index_of(own) : -1;
     float cx = Value<DT>::load(x, has ? index_of(own) : 0);
