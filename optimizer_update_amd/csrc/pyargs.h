@@ -16,7 +16,7 @@ static int to_i64(PyObject* o, long long* out)
     return !(*out == -1 && PyErr_Occurred());
 }
 
-static int to_i32(PyObject* o, int* out)
+static inline int to_i32(PyObject* o, int* out)
 {
     long long v;
     if (!to_i64(o, &v)) return 0;

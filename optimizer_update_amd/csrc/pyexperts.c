@@ -1,6 +1,6 @@
 /* pyexperts.c -- CPython entry points of liboptimizer_experts.so: the same C
  * functions that the ctypes binding calls, with the same positional arguments,
- * converted here.  A call's arguments are 9 to 18 numbers, whose conversion by
+ * converted here.  A call's arguments are 6 to 18 numbers, whose conversion by
  * ctypes is a good part of the host cost of a small call.  Every check stays in
  * the library; the calls run with the GIL released, as ctypes' do.
  */
@@ -15,6 +15,19 @@ typedef union {
     void* p;
 } arg;
 
+/* An int that is none would be another number (2^32 + 1 experts: one). */
+static int to_int(const char* name, Py_ssize_t at, PyObject* o, int* out)
+{
+    long long v;
+    if (!to_i64(o, &v)) return 0;
+    if (v < INT32_MIN || v > INT32_MAX) {
+        PyErr_Format(PyExc_OverflowError, "%s: argument %zd does not fit 32 bits", name, at + 1);
+        return 0;
+    }
+    *out = (int)v;
+    return 1;
+}
+
 /* kinds: a letter an argument, i int, l int64, f binary32, p pointer */
 static int convert(const char* name, const char* kinds, PyObject* const* a, Py_ssize_t na, arg* out)
 {
@@ -22,7 +35,7 @@ static int convert(const char* name, const char* kinds, PyObject* const* a, Py_s
     for (Py_ssize_t k = 0; k < na; ++k) {
         int ok = 0;
         switch (kinds[k]) {
-        case 'i': ok = to_i32(a[k], &out[k].i); break;
+        case 'i': ok = to_int(name, k, a[k], &out[k].i); break;
         case 'l': ok = to_i64(a[k], &out[k].l); break;
         case 'f': ok = to_f32(a[k], &out[k].f); break;
         case 'p': ok = to_ptr(a[k], &out[k].p); break;

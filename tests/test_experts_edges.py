@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import optimizer_update_amd as ou
-from optimizer_update_amd import int4
+from optimizer_update_amd import int4, route
 
 
 @pytest.mark.parametrize("make", [lambda: torch.randn(64, 40).t(), lambda: torch.randn(64, 4, 64).transpose(0, 1),
@@ -18,3 +18,34 @@ def test_quantize_copies_on_the_calls_stream(make, monkeypatch):
     ou.int4_quantize(x, 32, stream=7)
     got = seen["operand"]
     assert seen["stream"] == 7 and got.data_ptr() == x.data_ptr() and got.shape == x.shape and got.stride() == x.stride()
+
+
+# ------------------------------------------------------------------ numbers
+
+A, B, C, D, E, F, G = (0x100000000 * i for i in range(1, 8))
+CALLS = {
+    # name: arguments (a stream behind them), and which of them are 32-bit numbers
+    "ou_route_topk": ([0, A, 10, 64, 64, 0, None, 8, 2, 1, 1, 1.0, None, 4, B, C], (0, 3, 5, 7, 8, 9, 10, 13)),
+    "ou_route_topk_backward": ([2, A, 10, 64, 64, 1, 0, 1.0, B, C, 4, D], (0, 3, 5, 6, 10)),
+    "ou_route_order": ([A, 100, 16, B, C, D, None, 0], (2,)),
+    "ou_route_dispatch": ([1, A, 10, 64, 64, 2, B, C, D, 64, 1], (0, 5, 10)),
+    "ou_route_combine": ([1, A, 10, 64, 64, 2, B, C, E, 64, F, 64], (0, 5)),
+    "ou_route_combine_backward": ([1, A, 10, 64, 64, 2, B, 64, C, D, E, F, G], (0, 5)),
+    "ou_route_balance": ([A, B, 8, 0.1, C], (2,)),
+    "ou_int4_matmul": ([2, A, 3, 256, 2, B, 2, C, D, 40, 256, 64, E, 40], (0, 4, 6, 11)),
+    "ou_int4_grouped_matmul": ([2, A, 3, 256, 2, B, 2, C, D, 40, 256, 64, F, 4, E, 40, 1], (0, 4, 6, 11, 13, 16)),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_numbers_that_pass_32_bits_are_refused(name):
+    """2^32 more than a number that is allowed is not that number."""
+    f = getattr(ou.load_experts(), name)
+    args, small = CALLS[name]
+    assert set(CALLS) == set(route.FAST_ENTRY_POINTS)
+    for i in small:
+        for more in (1 << 32, -(1 << 32), 1 << 40):
+            bad = list(args)
+            bad[i] += more
+            with pytest.raises(OverflowError):
+                f(*bad, None)
