@@ -8,8 +8,9 @@ and products, plain and by expert (binding of ``liboptimizer_experts.so``,
     y = int4_matmul(x, q)                     x q^T
     y = int4_grouped_matmul(x, qe, offsets)   rows offsets[e]:offsets[e + 1] of x against expert e
 
-Made for the few rows of serving.  No gradients are recorded.  Streams,
-checks and ownership are those of the other 4-bit operators (``mx4``).
+Made for the few rows of serving.  No gradients are recorded; the products
+refuse operands that ask for them.  Streams, checks and ownership are those of
+the other 4-bit operators (``mx4``).
 """
 from __future__ import annotations
 
@@ -167,6 +168,8 @@ def _matmul(x, q, offsets, dims, dtype, out, stream):
     dt = _values(x, "the left operand", 2)
     index = x.get_device()
     _same(index, on, "the weights")
+    if (x.requires_grad or out is not None and out.requires_grad) and torch.is_grad_enabled():
+        raise ValueError("gradients are not recorded through 4-bit whole numbers: detach x, or call under no_grad()")
     m, have = x.shape
     if have != k:
         raise ValueError(f"the operands contract {have} and {k} columns")

@@ -49,3 +49,25 @@ def test_numbers_that_pass_32_bits_are_refused(name):
             bad[i] += more
             with pytest.raises(OverflowError):
                 f(*bad, None)
+
+
+# ------------------------------------------------------------------ gradients
+
+@pytest.mark.parametrize("grouped", [False, True])
+def test_products_refuse_to_drop_gradients(grouped, monkeypatch):
+    for name, to in (("_weights", lambda *a: -1), ("_values", lambda *a: 0), ("_output", lambda *a: (0, 3)), ("_run", lambda *a: "called")):
+        monkeypatch.setattr(int4, name, to)
+    lead = (2,) if grouped else ()
+    q = ou.Int4(torch.zeros((*lead, 3, 32), dtype=torch.uint8), torch.zeros((*lead, 3, 2)), None, 32)
+    offsets = (torch.tensor([0, 1, 2], dtype=torch.int32),) if grouped else ()
+    f = ou.int4_grouped_matmul if grouped else ou.int4_matmul
+    x, leaf = torch.zeros((2, 64)), torch.zeros((2, 64), requires_grad=True)
+    assert f(x, q, *offsets) == "called"
+    for operand in (leaf, leaf * 2):
+        with pytest.raises(ValueError, match="gradients"):
+            f(operand, q, *offsets)
+        with torch.no_grad():
+            assert f(operand, q, *offsets) == "called"
+        assert f(operand.detach(), q, *offsets) == "called"
+    with pytest.raises(ValueError, match="gradients"):
+        f(x, q, *offsets, out=torch.zeros((2, 3), requires_grad=True))
