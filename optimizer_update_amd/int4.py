@@ -20,7 +20,7 @@ import torch
 
 from . import DTYPES
 from .mx4 import _offsets, _output, _result_type, _row_stride, _rows_apart, _run, _same, _values
-from .route import _fail, load_experts
+from .route import _fail, _written, load_experts
 
 
 class Int4:
@@ -120,13 +120,14 @@ def int4_quantize(x: torch.Tensor, group: int = 128, zeros: bool = True, dtype: 
 
 
 def _do_dequantize(q, dtype, out, handle):
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty(q.shape, dtype=dtype, device=q.device)
     st = load_experts().ou_int4_dequantize(DTYPES[out.dtype], *_ptrs(q), math.prod(q.codes.shape[:-1]), q.k, q.group,
                                            out.data_ptr(), q.k, handle)
     if st:
         _fail(st)
-    return out
+    return _written(out) if given else out
 
 
 def int4_dequantize(q: Int4, dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None,
@@ -145,9 +146,9 @@ def int4_dequantize(q: Int4, dtype: torch.dtype = torch.float32, out: torch.Tens
 
 
 def _do_matmul(x, dt, rs, q, m, n, k, dtype, od, out, stride, offsets, groups, handle):
-    rest = 0
-    if out is None:
-        out, rest = x.new_empty((m, n), dtype=dtype), 1
+    rest = 0 if out is not None else 1
+    if rest:
+        out = x.new_empty((m, n), dtype=dtype)
     codes, scales, zeros = q.codes, q.scales, q.zeros
     sd, zp = DTYPES[scales.dtype], None if zeros is None else zeros.data_ptr()
     lib = load_experts()
@@ -159,7 +160,7 @@ def _do_matmul(x, dt, rs, q, m, n, k, dtype, od, out, stride, offsets, groups, h
                                         q.group, offsets.data_ptr(), groups, out.data_ptr(), stride, rest, handle)
     if st:
         _fail(st)
-    return out
+    return out if rest else _written(out)
 
 
 def _matmul(x, q, offsets, dims, dtype, out, stream):

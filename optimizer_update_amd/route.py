@@ -95,6 +95,12 @@ def _fail(status: int) -> None:
     raise _lib.OptimizerUpdateError(status, load_experts().ou_experts_last_error().decode(errors="replace"))
 
 
+def _written(out: torch.Tensor) -> torch.Tensor:
+    """``out``, for torch's check of saved tensors a written one."""
+    torch.autograd.graph.increment_version(out)
+    return out
+
+
 def _whole(x, name: str, dims: int) -> None:
     if not isinstance(x, torch.Tensor) or x.dtype != torch.int32 or x.dim() != dims or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of {dims} axes")
@@ -269,13 +275,12 @@ def _ordered(order, index: int) -> None:
 
 
 def _do_balance(bias, order, rate, out, handle):
-    if out is None:
-        out = torch.empty_like(bias)
-    st = load_experts().ou_route_balance(bias.data_ptr(), order.offsets.data_ptr(), order.experts, rate, out.data_ptr(),
+    made = torch.empty_like(bias) if out is None else out
+    st = load_experts().ou_route_balance(bias.data_ptr(), order.offsets.data_ptr(), order.experts, rate, made.data_ptr(),
                                          handle)
     if st:
         _fail(st)
-    return out
+    return made if out is None else _written(out)
 
 
 def route_balance(bias: torch.Tensor, order: RouteOrder, rate: float, out: torch.Tensor | None = None,
@@ -300,31 +305,33 @@ def route_balance(bias: torch.Tensor, order: RouteOrder, rate: float, out: torch
 
 def _do_dispatch(x, order, out, handle):
     (t, h), k = x.shape, order.places.shape[1]
-    if out is None:
-        out, stride, rest = x.new_empty((t * k, h)), h, 1
-    else:
+    given = out is not None
+    if given:
         stride, rest = _row_stride(out, "out"), 0
+    else:
+        out, stride, rest = x.new_empty((t * k, h)), h, 1
     st = load_experts().ou_route_dispatch(DTYPES[x.dtype], x.data_ptr(), t, h, _row_stride(x, "x"), k,
                                           order.slots.data_ptr(), order.places.data_ptr(), out.data_ptr(), stride, rest,
                                           handle)
     if st:
         _fail(st)
-    return out
+    return _written(out) if given else out
 
 
 def _do_combine(y, w, order, add, out, handle):
     (t, k), h = order.places.shape, y.shape[1]
-    if out is None:
-        out, stride = y.new_empty((t, h)), h
-    else:
+    given = out is not None
+    if given:
         stride = _row_stride(out, "out")
+    else:
+        out, stride = y.new_empty((t, h)), h
     st = load_experts().ou_route_combine(
         DTYPES[y.dtype], y.data_ptr(), t, h, _row_stride(y, "y"), k, None if w is None else w.data_ptr(),
         order.places.data_ptr(), None if add is None else add.data_ptr(), 0 if add is None else _row_stride(add, "add"),
         out.data_ptr(), stride, handle)
     if st:
         _fail(st)
-    return out
+    return _written(out) if given else out
 
 
 def _do_combine_backward(dout, y, w, order, need_y, need_w, handle):

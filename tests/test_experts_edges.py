@@ -71,3 +71,34 @@ def test_products_refuse_to_drop_gradients(grouped, monkeypatch):
         assert f(operand.detach(), q, *offsets) == "called"
     with pytest.raises(ValueError, match="gradients"):
         f(x, q, *offsets, out=torch.zeros((2, 3), requires_grad=True))
+
+
+class _Library:
+    """Answers every call with OK."""
+
+    def __getattr__(self, name):
+        return lambda *args: 0
+
+
+def test_results_that_are_given_count_as_written(monkeypatch):
+    """A graph that saved `out` earlier must not go on with what is written into it now."""
+    for m in (route, int4):
+        monkeypatch.setattr(m, "load_experts", _Library)
+    order = ou.RouteOrder(torch.zeros(3, dtype=torch.int32), torch.zeros(4, dtype=torch.int32), torch.zeros((2, 2), dtype=torch.int32))
+    q = ou.Int4(torch.zeros((3, 32), dtype=torch.uint8), torch.zeros((3, 2)), None, 32)
+    x, y, w = torch.zeros((2, 64)), torch.zeros((4, 64)), torch.zeros((2, 2))
+    offsets = torch.zeros(2, dtype=torch.int32)
+    for shape, call in (((4, 64), lambda out: route._do_dispatch(x, order, out, None)),
+                        ((2, 64), lambda out: route._do_combine(y, w, order, None, out, None)),
+                        ((2,), lambda out: route._do_balance(torch.zeros(2), order, 0.1, out, None)),
+                        ((3, 64), lambda out: int4._do_dequantize(q, torch.float32, out, None)),
+                        ((2, 3), lambda out: int4._do_matmul(x, 0, 64, q, 2, 3, 64, torch.float32, 0, out, 3, None, 0, None)),
+                        ((2, 3), lambda out: int4._do_matmul(x, 0, 64, q, 2, 3, 64, torch.float32, 0, out, 3, offsets, 1, None))):
+        assert call(None).shape == shape and call(None)._version == 0
+        out = torch.zeros(shape)
+        saved = (torch.ones(shape, requires_grad=True) * out).sum()
+        assert call(out) is out and out._version == 1
+        with pytest.raises(RuntimeError, match="modified by an inplace"):
+            saved.backward()
+        with torch.inference_mode():
+            call(torch.zeros(shape))
