@@ -139,13 +139,16 @@ int ou_int4_dequantize(int dtype, const uint8_t* codes, int scale_dtype, const v
                        int64_t out_stride, void* stream);
 
 /* out[i][j] = sum_k x[i][k] * value[j][k]: x m x k of `dtype`, out m x n of
- * out_dtype.  The products of codes and x are exact (of a binary32 x what lies
- * below 2^-133 is cut off); sums in binary32, of x code and of x apart, so that
- * a result may be infinite or NaN where 15 times the terms' magnitudes pass
- * what it holds; rounded once.  A row of x that holds an infinity or a NaN gives
- * NaN or infinities, and no other row does by it.  Made for few rows (tokens in
- * serving): from some hundred on, dequantised weights and a library product
- * are faster. */
+ * out_dtype.  A group's columns are summed in binary32, x (code - c) and x apart,
+ * and (zero - c) times the second is subtracted, with c = 7.5 for a binary32 x and
+ * 0 for 16 bits.  The products are exact; of a binary32 x what lies below 2^-133
+ * is cut off, which shows where all of a row is below 1e-33 or so.  The sums pass
+ * through |x| (|code - c| + |zero - c|) |scale|: a result's error goes by that,
+ * which its own terms may be smaller than, and it may be infinite or NaN where
+ * the sums pass what binary32 holds; rounded once.  A row of x that holds an
+ * infinity or a NaN gives NaN or infinities, and no other row does by it.  Made
+ * for few rows (tokens in serving): from some hundred on, dequantised weights and
+ * a library product are faster. */
 int ou_int4_matmul(int dtype, const void* x, int64_t m, int64_t x_stride, int out_dtype,
                    const uint8_t* codes, int scale_dtype, const void* scales, const void* zeros,
                    int64_t n, int64_t k, int32_t group, void* out, int64_t out_stride,

@@ -122,14 +122,24 @@ __global__ __launch_bounds__(kInt4Threads) void k_int4_dequantize(Int4Args p)
 
 // ---- products --------------------------------------------------------------------
 //
-// out[i][j] = sum over the groups g of scale[j][g] * (sum_k x[i][k] code[j][k]
-// - zero[j][g] * sum_k x[i][k]), both inner sums over the group's columns by
-// the 16x16x32 matrix instruction: codes are whole numbers up to 15, which
-// bfloat16 and binary16 hold exactly, and x goes in as it is (binary32 in three
-// bfloat16 parts that add up to it), so that every product is exact.  The sum
-// of x is a product with ones.  Weights are the instruction's second operand:
-// lane l holds columns of row l mod 16, and its four results are of that row,
-// so that a lane needs one scale a group.
+// out[i][j] = sum over the groups g of scale[j][g] * (sum_k x[i][k] (code[j][k]
+// - c) - (zero[j][g] - c) * sum_k x[i][k]), both inner sums over the group's
+// columns by the 16x16x32 matrix instruction: code - c is a whole or half number
+// of four bits and a sign, which bfloat16 and binary16 hold exactly, and x goes
+// in as it is (binary32 in three bfloat16 parts that add up to it, down to
+// 2^-133), so that every product is exact.  The sum of x is a product with ones.
+// Weights are the instruction's second operand: lane l holds columns of row l
+// mod 16, and its four results are of that row, so that a lane needs one scale a
+// group.
+//
+// c is 7.5 for binary32 x and 0 for 16 bits.  With 0 the inner sums pass through
+// twice the magnitude that (code - zero) has, and their error is 1.4 to 1.6 times
+// that of binary32 weights and a library product at 256 and 512 columns (less
+// from 1024 on); with 7.5 it is half of that, below the library's from 512
+// columns on and 1.05 times it at 256 (1.4e-7 to 0.9e-7 of the result).  It costs
+// 1 to 12 %: 16 x 1024 x 4096, 16 experts, 14.2 to 15.8 us, 16 rows x 14336 x
+// 4096 20.2 to 22.4.  Results of 16 bits, whose last rounding is 2^-9 or 2^-12,
+// would be the same, and 16-bit x pays 5 to 17 %: not there.
 
 using bf16x8 = __bf16 __attribute__((ext_vector_type(8)));
 using f16x8 = _Float16 __attribute__((ext_vector_type(8)));
@@ -138,24 +148,39 @@ using f32x4 = float __attribute__((ext_vector_type(4)));
 
 constexpr int kChunk = 128;   // columns of a step: 16 bytes of codes a lane
 
-// Eight codes as values of the matrix instruction's type, in the order 0, 2, 4,
-// 6, 1, 3, 5, 7.  A byte of 0 .. 15 is an 8-bit float (e4m3) of so many times
-// 2^-9, subnormal numbers and the first binade being in line, and the converter
-// multiplies by 2^9: seven instructions, fifteen by way of binary32.
+template <int DT>
+constexpr float kCentre = DT == kF32 ? 7.5f : 0.0f;
+
+// Eight codes less kCentre as values of the matrix instruction's type, in the
+// order 0, 2, 4, 6, 1, 3, 5, 7.  A byte of 0 .. 15 is an 8-bit float (e4m3) of so
+// many times 2^-9, subnormal numbers and the first binade being in line, and the
+// converter multiplies by 2^9: seven instructions, fifteen by way of binary32.
+// Less 7.5: twice the value is an odd number up to 15, its sign the code's top
+// bit, the rest the three bits below, inverted where it is negative.
+
 template <int DT>
 __device__ __forceinline__ u32x4 code_values(uint32_t c)
 {
-    const int lo = static_cast<int>(c & 0x0f0f0f0fu), hi = static_cast<int>(c >> 4 & 0x0f0f0f0fu);
+    constexpr float kUnit = kCentre<DT> != 0.0f ? 256.0f : 512.0f;
+    int lo, hi;
+    if constexpr (kCentre<DT> != 0.0f) {
+        const uint32_t above = c & 0x88888888u, n = ~(c ^ (above - (above >> 3)));
+        lo = static_cast<int>((n << 1 & 0x0e0e0e0eu) | (n << 4 & 0x80808080u) | 0x01010101u);
+        hi = static_cast<int>((n >> 3 & 0x0e0e0e0eu) | (n & 0x80808080u) | 0x01010101u);
+    } else {
+        lo = static_cast<int>(c & 0x0f0f0f0fu);
+        hi = static_cast<int>(c >> 4 & 0x0f0f0f0fu);
+    }
     if constexpr (DT == kF16)
-        return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 512.0f, false)),
-                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 512.0f, true)),
-                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.0f, false)),
-                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.0f, true))};
+        return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, kUnit, false)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, kUnit, true)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, kUnit, false)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, kUnit, true))};
     else
-        return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, false)),
-                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, true)),
-                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, false)),
-                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, true))};
+        return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, kUnit, false)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, kUnit, true)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, kUnit, false)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, kUnit, true))};
 }
 
 // x's eight neighbouring values as operands: one, or three parts of binary32.
@@ -305,7 +330,7 @@ __global__ __launch_bounds__(kWave * W) void k_int4_matmul(Int4Args p)
 #pragma unroll
         for (int q = 0; q < 4; ++q) s.x[q].load(x + (k0 + q * 32 < k ? k0 + q * 32 : k - 32));
     };
-    // scale and zero of the group of columns `4 at + g` of the wave's run
+    // scale and zero (less kCentre) of the group of columns `4 at + g` of the wave's run
     float scale[NT], zero[NT];
     Bits next_scale[NT], next_zero[NT];
     auto load_scales = [&](int at) {
@@ -373,7 +398,7 @@ __global__ __launch_bounds__(kWave * W) void k_int4_matmul(Int4Args p)
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
                     scale[j] = bits_value(next_scale[j], p.scale_dtype);
-                    zero[j] = p.zeros ? bits_value(next_zero[j], p.scale_dtype) : 8.0f;
+                    zero[j] = (p.zeros ? bits_value(next_zero[j], p.scale_dtype) : 8.0f) - kCentre<DT>;
                 }
                 if (steady.value || at + u + 4 / S < last) load_scales((at + u - first) * S / 4 + 1);
             }
@@ -432,7 +457,7 @@ __global__ __launch_bounds__(kWave * W) void k_int4_tiles(Int4Args p)
     using Elem = typename Value<DT>::Elem;
     __shared__ f32x4 sums[2][W][NT][kWave];
     __shared__ f32x4 plain[W][RC * S][4];   // x's sums over a group of columns, four rows
-    __shared__ float2 scaling[2][kRows][kUnits + 1];   // scale and zero
+    __shared__ float2 scaling[2][kRows][kUnits + 1];   // scale and zero less kCentre
     const int t = static_cast<int>(threadIdx.x), lane = t & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const uint32_t all_tiles = static_cast<uint32_t>((p.n + kRows - 1) / kRows);
@@ -507,7 +532,7 @@ __global__ __launch_bounds__(kWave * W) void k_int4_tiles(Int4Args p)
 #pragma unroll
         for (int i = 0; i < Q; ++i)
             scaling[at & 1][scale_row[i]][scale_unit[i]] =
-                float2{bits_value(s.scale[i], p.scale_dtype), p.zeros ? bits_value(s.zero[i], p.scale_dtype) : 8.0f};
+                float2{bits_value(s.scale[i], p.scale_dtype), (p.zeros ? bits_value(s.zero[i], p.scale_dtype) : 8.0f) - kCentre<DT>};
     };
     const bool some = chunks > 0;
     const int most = tiles - 1;
@@ -672,7 +697,8 @@ Int4Kernel choose_width(int64_t tiles)
 // 6144 tiles 25.9 and 23.9.  16 steps: 16384 tiles 77 and 88, 8000 tiles 45 and 50,
 // 4096 tiles 20.2 and 19.1, 2000 tiles 16.5 and 15.6, 12 steps 78 and 73.  Streamed binary32 is taken
 // apart for every tile, which small groups of columns leave no time for: 16 steps,
-// groups of 64, 16384 tiles 125 and 183 us, of 128 149 and 126.
+// groups of 64, 16384 tiles 125 and 183 us, of 128 149 and 126 (with codes that
+// were not centred; 129 held and 125 streamed with them).
 template <int DT, int S>
 constexpr bool holds(int64_t steps, int64_t tiles)
 {

@@ -189,9 +189,13 @@ def _matmul(x, q, offsets, dims, dtype, out, stream):
 def int4_matmul(x: torch.Tensor, q: Int4, dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
                 stream=None) -> torch.Tensor:
     """x q^T for x [M, K] (any row stride) and an Int4 [N, K]: [M, N] of
-    ``dtype`` (x's by default), or ``out`` (any row stride).  Codes times x are
-    exact, sums in binary32, rounded once.  For many rows (a prompt),
-    ``int4_dequantize`` and a library product are faster."""
+    ``dtype`` (x's by default), or ``out`` (any row stride).  Products are exact
+    but for what lies below 2^-133 of a float32 x; a group's columns are summed
+    in binary32, the codes (less 7.5 with a float32 x) and x apart, so that a
+    result's error goes by |x| (code + |zero|) |scale| (less 7.5 each with
+    float32) rather than by its own terms, and may be infinite or NaN where
+    these sums are; rounded once.  For many rows (a prompt), ``int4_dequantize``
+    and a library product are faster."""
     return _matmul(x, q, None, 2, dtype, out, stream)
 
 
