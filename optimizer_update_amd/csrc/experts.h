@@ -48,7 +48,8 @@ struct OrderArgs {
     int32_t bins;           // experts and those of none, rounded up to 4
 };
 
-// Rows of x or y: `units` pieces of a vector load (wide) or single elements.
+// Rows of x or y.  `cols` and the strides count elements; for the dispatch, which
+// copies, 16-byte pieces where rows allow them.
 struct RowsArgs {
     const void* x;          // dispatch: x; combine: y; its gradient: dout
     const void* y;          // gradient: y

@@ -91,12 +91,7 @@ struct Value<kBF16> {
     }
 };
 
-// The bits at `i` of an array whose type is known at run time, and their value:
-// apart, so that a load may be on its way while others are used.
-__device__ __forceinline__ uint32_t load_bits(const void* p, int64_t i, int dtype)
-{
-    return dtype == kF32 ? static_cast<const uint32_t*>(p)[i] : static_cast<const uint16_t*>(p)[i];
-}
+// The value of bits that were loaded earlier, of a type that is known at run time.
 __device__ __forceinline__ float bits_value(uint32_t b, int dtype)
 {
     return dtype == kF32   ? __builtin_bit_cast(float, b)
