@@ -6,6 +6,7 @@
 #include "../../include/optimizer_experts.h"
 #include "call.hpp"
 #include "experts.h"
+#include "int4_choice.hpp"
 
 using namespace experts;
 
@@ -363,10 +364,8 @@ int int4_product(int dtype, Int4Args& p, void* stream)
                            {"offsets", p.offsets, grouped ? 4.0 * (p.experts + 1.0) : 0, 4, false},
                            {"out", p.out, extent(p.m, p.n, p.out_stride, eo), static_cast<unsigned>(eo), true}};
     if (int st = check_buffers(bufs, 6)) return st;
-    const int scales = p.group % 128 == 0 ? 1 : p.group % 64 == 0 ? 2 : 4;
-    const int64_t few = grouped ? (p.m < p.experts ? p.m : p.experts) : cut(p.m, 16);   // units with rows, about
-    const int64_t tiles = cut(p.n, 16) * few;
-    const Int4Kernel f = int4_matmul_kernel(dtype, scales, grouped, cut(p.k, 128), tiles, es == 2);
+    const int64_t tiles = int4_tiles(p.m, p.n, grouped, p.experts);
+    const Int4Kernel f = int4_matmul_kernel(dtype, int4_scales(p.group), grouped, cut(p.k, 128), tiles, es == 2);
     // by groups: two more, the rows in front of the first and behind the last
     const int64_t units = grouped ? cut(p.m + 15 * static_cast<int64_t>(p.experts + 2), 16) : cut(p.m, 16);
     const int64_t run = cut(tiles, kInt4Blocks);

@@ -6,6 +6,7 @@
 #include <type_traits>
 
 #include "groups.hpp"
+#include "int4_choice.hpp"
 #include "values.hpp"
 
 #pragma clang fp contract(off)
@@ -674,53 +675,32 @@ const void* int4_dequantize_kernel(int dtype)
 
 namespace {
 
-// x streams past 4 tiles of rows of weights from 896 tiles on, past 2 from 512.  One
-// row, k = 4096, groups of 128: 256 tiles 5.6 us by one, 7.3 by two; 896 tiles 13.8,
-// 11.5, 11.7 by four; 16 rows 23.0, 16.7, 13.8; 512 tiles, k = 8192, 23.1, 17.2,
-// 23.5; 2000 tiles 43, 30, 25.8.  Groups of 32, 2000 tiles of 16 rows: 43.7 by two,
-// 40.1 by four, one row 34.1 and 37.8.  Four waves do by four what eight take 10 %
-// longer for, and by two where smaller groups take the registers for a second block
-// of eight: 768 tiles, k = 2560, groups of 64, 10.3 and 12.5.  Binary32 with small
-// groups by two at most: the sums of four leave one wave a SIMD.
 template <int DT, int S, bool HALF, bool GROUPED>
-Int4Kernel choose_width(int64_t tiles)
+const void* streamed(const Int4Choice& c)
 {
     if constexpr (DT != kF32 || S == 1)
-        if (tiles >= 896) return {reinterpret_cast<const void*>(k_int4_matmul<DT, S, 4, 2, 4, HALF, GROUPED>), 4, 4, false};
-    constexpr int W = S == 1 ? 8 : 4;
-    if (tiles >= 512) return {reinterpret_cast<const void*>(k_int4_matmul<DT, S, W, 2, 2, HALF, GROUPED>), W, 2, false};
-    return {reinterpret_cast<const void*>(k_int4_matmul<DT, S, 8, 2, 1, HALF, GROUPED>), 8, 1, false};
+        if (c.tiles == 4) return reinterpret_cast<const void*>(k_int4_matmul<DT, S, 4, 2, 4, HALF, GROUPED>);
+    if (c.tiles == 2) return reinterpret_cast<const void*>(k_int4_matmul<DT, S, S == 1 ? 8 : 4, 2, 2, HALF, GROUPED>);
+    return reinterpret_cast<const void*>(k_int4_matmul<DT, S, 8, 2, 1, HALF, GROUPED>);
 }
 
-// x is held where tiles are many and the waves' registers of it are filled.  8
-// steps: 2001 tiles 11.8 us, streamed 13.6, but 1024 tiles 8.2 and 6.2, and 6 steps,
-// 6144 tiles 25.9 and 23.9.  16 steps: 16384 tiles 77 and 88, 8000 tiles 45 and 50,
-// 4096 tiles 20.2 and 19.1, 2000 tiles 16.5 and 15.6, 12 steps 78 and 73.  Streamed binary32 is taken
-// apart for every tile, which small groups of columns leave no time for: 16 steps,
-// groups of 64, 16384 tiles 125 and 183 us, of 128 149 and 126 (with codes that
-// were not centred; 129 held and 125 streamed with them).
-template <int DT, int S>
-constexpr bool holds(int64_t steps, int64_t tiles)
+template <int DT, int S, bool GROUPED>
+const void* held(const Int4Choice& c)
 {
-    if (DT == kF32 && S > 1) return steps <= 16 && tiles >= 1536;
-    return steps > 6 && steps <= 8 ? tiles >= 1536 : DT != kF32 && steps > 12 && steps <= 16 && tiles >= 6144;
+    if (c.steps == 1) return reinterpret_cast<const void*>(k_int4_tiles<DT, S, 2, 8, 1, GROUPED>);
+    if constexpr (DT != kF32)
+        return reinterpret_cast<const void*>(k_int4_tiles<DT, S, 1, 4, 4, GROUPED>);
+    else if constexpr (S > 1)
+        return reinterpret_cast<const void*>(k_int4_tiles<DT, S, 1, 8, 2, GROUPED>);
+    return nullptr;   // not reached: int4_holds() leaves binary32 with one group a step at 8 steps
 }
 
 template <int DT, int S, bool GROUPED>
 Int4Kernel choose(int64_t steps, int64_t tiles, bool half)
 {
-    if (!half) return choose_width<DT, S, false, GROUPED>(tiles);
-    if (holds<DT, S>(steps, tiles)) {
-        // 2001 tiles of 8 steps: eight waves of one 10.5 us by pairs of tiles, 11.2 by
-        // single ones, four waves of two 11.6 and 12.8.  16 steps, 64 experts: four
-        // waves of four 80 us, by pairs 95, eight of two 96, by pairs 82.
-        if (steps <= 8) return {reinterpret_cast<const void*>(k_int4_tiles<DT, S, 2, 8, 1, GROUPED>), 8, 2, true};
-        if constexpr (DT != kF32)
-            return {reinterpret_cast<const void*>(k_int4_tiles<DT, S, 1, 4, 4, GROUPED>), 4, 1, true};
-        else if constexpr (S > 1)
-            return {reinterpret_cast<const void*>(k_int4_tiles<DT, S, 1, 8, 2, GROUPED>), 8, 1, true};
-    }
-    return choose_width<DT, S, true, GROUPED>(tiles);
+    const Int4Choice c = int4_choice(DT == kF32, S, half, steps, tiles);
+    const void* const fn = c.held ? held<DT, S, GROUPED>(c) : half ? streamed<DT, S, true, GROUPED>(c) : streamed<DT, S, false, GROUPED>(c);
+    return {fn, c.waves, c.tiles, c.held};
 }
 template <int DT>
 Int4Kernel choose(int scales, bool grouped, int64_t steps, int64_t tiles, bool half)

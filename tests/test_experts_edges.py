@@ -1,5 +1,8 @@
 """CPU: calls of the operators around experts that their documentation allows
 and the other tests do not make, as far as they can be seen without a device."""
+import os
+import subprocess
+
 import pytest
 import torch
 
@@ -102,3 +105,58 @@ def test_results_that_are_given_count_as_written(monkeypatch):
             saved.backward()
         with torch.inference_mode():
             call(torch.zeros(shape))
+
+
+# ------------------------------------------------------------------ which kernel
+
+MAIN = """
+#include <cstdio>
+#include "int4_choice.hpp"
+int main()
+{
+    long long m, n, k, group, f32, half, experts;
+    while (std::scanf("%lld %lld %lld %lld %lld %lld %lld", &m, &n, &k, &group, &f32, &half, &experts) == 7) {
+        const experts::Int4Choice c = experts::int4_choice(f32, experts::int4_scales(static_cast<int32_t>(group)), half, (k + 127) / 128,
+                                                           experts::int4_tiles(m, n, experts >= 0, experts));
+        std::printf("%d %d %d %d\\n", c.held, c.tiles, c.waves, c.steps);
+    }
+}
+"""
+# m, n, k, group (of products by group: rows, and matrices behind them), and what is chosen for x of 16 bits, of
+# binary32 with 16-bit scales, and with binary32 scales: the sizes that the tests on the device take for these kernels
+ONE, TWO, FOUR, TWO_SMALL, HELD8, HELD16, HELD32 = ((0, 1, 8, 0), (0, 2, 8, 0), (0, 4, 4, 0), (0, 2, 4, 0), (1, 2, 8, 1), (1, 1, 4, 4),
+                                                    (1, 1, 8, 2))
+CHOICES = [
+    ((1, 4096, 4096, 128, -1), ONE, ONE, ONE), ((64, 100, 2048, 128, -1), ONE, ONE, ONE), ((16, 40, 4096, 96, 16), ONE, ONE, ONE),
+    # blocks of two and four tiles
+    ((1, 8200, 6304, 32, -1), TWO_SMALL, TWO_SMALL, TWO_SMALL), ((17, 4117, 6400, 64, -1), TWO_SMALL, TWO_SMALL, TWO_SMALL),
+    ((20, 8200, 6528, 128, -1), FOUR, FOUR, FOUR), ((3, 16400, 4192, 32, -1), FOUR, TWO_SMALL, TWO_SMALL),
+    ((5, 16390, 1600, 64, -1), FOUR, TWO_SMALL, TWO_SMALL), ((40, 6007, 1344, 96, -1), FOUR, TWO_SMALL, TWO_SMALL),
+    ((9, 8300, 4096, 128, -1), TWO, TWO, TWO), ((189, 520, 4224, 128, 32), FOUR, FOUR, FOUR), ((53, 515, 4160, 64, 16), TWO_SMALL, TWO_SMALL, TWO_SMALL),
+    ((201, 907, 3232, 32, 18), FOUR, TWO_SMALL, TWO_SMALL), ((207, 1000, 2112, 64, 18), FOUR, TWO_SMALL, TWO_SMALL),
+    # x held: 7 to 8 and 13 to 16 steps, up to 16 for binary32 with small groups
+    ((3, 24593, 1024, 32, -1), HELD8, HELD8, TWO_SMALL), ((17, 12300, 928, 32, -1), HELD8, HELD8, TWO_SMALL),
+    ((2, 25000, 896, 128, -1), HELD8, HELD8, FOUR), ((1, 24600, 960, 64, -1), HELD8, HELD8, TWO_SMALL),
+    ((16, 98320, 2048, 128, -1), HELD16, FOUR, FOUR), ((40, 32790, 1632, 96, -1), HELD16, HELD32, TWO_SMALL),
+    ((273, 2100, 2048, 128, 48), HELD16, FOUR, FOUR), ((117, 2063, 1632, 32, 48), HELD16, HELD32, TWO_SMALL),
+    ((477, 2085, 1984, 64, 48), HELD16, HELD32, TWO_SMALL), ((269, 1100, 1024, 64, 24), HELD8, HELD8, TWO_SMALL),
+    # past 32 bits of codes: 4 rows stream, 16 rows are held
+    ((4, 8192, 8192, 128, 136), FOUR, FOUR, FOUR), ((4, 8192, 2048, 128, 540), FOUR, FOUR, FOUR), ((16, 8192, 2048, 128, 540), HELD16, FOUR, FOUR),
+    ((0, 64, 1024, 128, 0), ONE, ONE, ONE),
+]
+
+
+def test_sizes_choose_the_kernels_they_are_tested_for(tmp_path):
+    src = tmp_path / "t.cpp"
+    src.write_text(MAIN)
+    csrc = os.path.join(os.path.dirname(int4.__file__), "csrc")
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-I", csrc, str(src), "-o", str(tmp_path / "t")], check=True)
+    lines = [f"{m} {n} {k} {group} {f32} {half} {e}" for (m, n, k, group, e), *_ in CHOICES for f32, half in ((0, 1), (1, 1), (1, 0))]
+    out = subprocess.run([str(tmp_path / "t")], input="\n".join(lines), capture_output=True, text=True, check=True).stdout.split("\n")
+    got = [tuple(map(int, line.split())) for line in out if line]
+    for i, (sizes, *want) in enumerate(CHOICES):
+        assert got[3 * i:3 * i + 3] == want, sizes
+    # binary32 scales are never held, whatever x is
+    lines = [line.rsplit(" ", 2)[0] + " 0 " + line.split()[-1] for line in lines]
+    out = subprocess.run([str(tmp_path / "t")], input="\n".join(lines), capture_output=True, text=True, check=True).stdout.split("\n")
+    assert not any(int(line.split()[0]) for line in out if line)
