@@ -303,7 +303,6 @@ __global__ __launch_bounds__(kTopkWaves * kWave) void k_topk(TopkArgs p)
     }
     const uint64_t rows = L == 64 ? ~uint64_t(0) : ((uint64_t(1) << (L & 63)) - 1) << (row * L);
     float hi = -kInf, lo = kInf, odd = 0.0f;
-    bool none = false;   // no expert is there: by the logits, since the extremes pass over a NaN, which counts as one
     if (full) {
 #pragma unroll
         for (int i = 0; i < V; i += 2) {
@@ -318,15 +317,18 @@ __global__ __launch_bounds__(kTopkWaves * kWave) void k_topk(TopkArgs p)
             lo = min3(lo, v[i] == -kInf ? kInf : c[i], v[i + 1] == -kInf ? kInf : c[i + 1]);
             odd += c[i] + c[i + 1];
         }
-        bool some = false;
-#pragma unroll
-        for (int i = 0; i < V; ++i) some |= v[i] != -kInf;
-        none = !(__ballot(some) & rows);
     }
     hi = lanes_max<L>(hi);
     lo = -lanes_max<L>(-lo);
     odd = lanes_sum<L>(odd);
     if (!by_logit) error += fmaxf(fabsf(hi), fabsf(lo)) * 0x1p-23f;
+    bool none = hi == -kInf;   // no expert is there, unless there are NaN alone, which the extremes pass over
+    if (__any(none)) {
+        bool some = false;
+#pragma unroll
+        for (int i = 0; i < V; ++i) some |= v[i] != -kInf;
+        none = !(__ballot(some) & rows);
+    }
     bool sure = fabsf(odd) < kInf || none;
     // steps of c from `base` on; a base that is far from 0 is rounded for all
     // alike, by 64 steps at most
