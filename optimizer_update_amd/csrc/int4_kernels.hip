@@ -134,13 +134,14 @@ __global__ __launch_bounds__(kInt4Threads) void k_int4_dequantize(Int4Args p)
 // group.
 //
 // c is 7.5 for binary32 x and 0 for 16 bits.  With 0 the inner sums pass through
-// twice the magnitude that (code - zero) has, and their error is 1.4 to 1.6 times
-// that of binary32 weights and a library product at 256 and 512 columns (less
-// from 1024 on); with 7.5 it is half of that, below the library's from 512
-// columns on and 1.05 times it at 256 (1.4e-7 to 0.9e-7 of the result).  It costs
-// 1 to 12 %: 16 x 1024 x 4096, 16 experts, 14.2 to 15.8 us, 16 rows x 14336 x
-// 4096 20.2 to 22.4.  Results of 16 bits, whose last rounding is 2^-9 or 2^-12,
-// would be the same, and 16-bit x pays 5 to 17 %: not there.
+// twice the magnitude that (code - zero) has.  For binary32 x their error is then
+// 1.4 to 1.6 times that of binary32 weights and a library product at 256 and 512
+// columns (less from 1024 on); with 7.5 it is half of that, below the library's
+// from 512 columns on and 1.05 times it at 256 (1.4e-7 to 0.9e-7 of the result).
+// It costs 1 to 15 %: 16 x 1024 x 4096, 16 experts, 14.2 to 15.8 us, 16 rows x
+// 14336 x 4096 20.2 to 22.4.  16-bit x, whose products are shorter, is at 0.2 to
+// 0.7 times the library's error with 0 (binary32 results; others are rounded far
+// above that) and would pay 5 to 17 %.
 
 using bf16x8 = __bf16 __attribute__((ext_vector_type(8)));
 using f16x8 = _Float16 __attribute__((ext_vector_type(8)));

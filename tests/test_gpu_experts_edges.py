@@ -169,3 +169,43 @@ def test_products_with_any_zeros(dtype, zero):
     x = torch.randn((9, 512), generator=_gen(7)).to(dtype)
     want, size = _product(x, q)
     _near(ou.int4_matmul(x.cuda(), q, dtype=F32), want, _bound(x, size, want, F32))
+
+
+# ------------------------------------------------------------------ again
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_calls_repeat_themselves(dtype):
+    """Bit for bit, with other work between, on one stream or two: no result
+    depends on the order in which blocks run."""
+    g = _gen(1)
+    t, e, k, h = 1003, 64, 6, 520
+    logits = torch.randn((t, e), generator=g).to(dtype).cuda().requires_grad_(True)
+    x = torch.randn((t, h), generator=g).to(dtype).cuda().requires_grad_(True)
+    dout = torch.randn((t, h), generator=g).to(dtype).cuda()
+    bias = (torch.randn(e, generator=g) * 0.1).cuda()
+    products = [(_int4(n, kk, group, BF16, True, n), torch.randn((m, kk), generator=g).to(dtype).cuda())
+                for m, n, kk, group in ((1, 4096, 4096, 128), (13, 8200, 1024, 32), (5, 14336, 512, 128), (9, 8300, 4096, 64), (16, 24600, 1024, 64))]
+
+    def run():
+        w, ids = ou.route_topk(logits, k, scores="sigmoid", bias=bias, groups=8, top_groups=3)
+        o = ou.route_order(ids, e)
+        rows = ou.route_dispatch(x, o)
+        out = ou.route_combine(rows, w, o, add=x)
+        grads = torch.autograd.grad(out, (logits, x), dout)
+        return [w, ids, o.offsets, o.slots, o.places, rows, out, *grads, ou.route_balance(bias, o, 0.1),
+                *(ou.int4_matmul(x4, q) for q, x4 in products)]
+
+    first = run()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for i in range(12):
+        if i % 3 == 1:
+            (x.detach().float() @ x.detach().float().t()).sum()
+        if i % 3 == 2:
+            with torch.cuda.stream(side):
+                again = run()
+            side.synchronize()
+        else:
+            again = run()
+            torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
