@@ -10,7 +10,8 @@ and products, plain and by expert (binding of ``liboptimizer_experts.so``,
 
 Made for the few rows of serving.  No gradients are recorded; the products
 refuse operands that ask for them.  Streams, checks and ownership are those of
-the other 4-bit operators (``mx4``).
+the other 4-bit operators (``mx4``); copies that views take are made on the
+call's stream, and a result that is given counts as written for autograd.
 """
 from __future__ import annotations
 

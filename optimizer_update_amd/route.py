@@ -19,7 +19,9 @@ arguments; all arithmetic runs in the HIP kernels.  Every call goes to the
 current stream of the operands' device, or to ``stream`` where there is one (a
 stream of that device or its handle, 0 being the default stream); results and
 workspaces are allocated on that stream.  An operand of another stream must
-stay until the call's work is done (``record_stream``).
+stay until the call's work is done (``record_stream``).  A result that is given
+(``out``) counts as written for autograd, as one of torch's own in-place
+operations does.
 """
 from __future__ import annotations
 
